@@ -333,6 +333,93 @@ int egopq_w8a8_gemm_ex(const int8_t* a_q, const void* a_tc, const float* a_s, co
 int egopq_bf16_gemm_twin(const uint16_t* x_bf16, const uint16_t* w_bf16, int64_t M, int64_t N,
                          int64_t K, uint16_t* y_bf16, egopq_stream_t stream);
 
+/* ---- rows that pick their own weights -------------------------------------------
+ * A mixture of experts and the low-rank adapters of many requests beside the
+ * packed linear: each row of a batch names the weights it is multiplied with.
+ * Row picks (expert and adapter ids) are int32; a pick outside [0, count) is
+ * no error but a row without that product (an expert of another machine, a
+ * request without an adapter), so the calls need no host synchronization.
+ * Workspaces are caller-owned device memory, 16-byte aligned, of at least the
+ * bytes the matching query returns (0 for a refused shape and for an empty
+ * batch); calls sharing one must be ordered on one stream. Results do not
+ * depend on timing (no floating-point atomics). */
+typedef enum { EGOPQ_SCORE_SOFTMAX = 0, EGOPQ_SCORE_SIGMOID = 1 } egopq_score;
+typedef enum { EGOPQ_GROUP_MAX = 0, EGOPQ_GROUP_TOP2 = 1 } egopq_group_score;
+
+/* The router: the k experts of each of T tokens and their weights, fp32
+ * arithmetic throughout. logits: fp32, or bf16 with logits_bf16, [T][E].
+ *   s_e = softmax(logits)_e or 1 / (1 + exp(-logits_e))     (score)
+ *   c_e = s_e + bias_e      bias fp32 [E] or NULL: it moves the choice only
+ *   the E experts are n_group groups of neighbours (E % n_group == 0); a
+ *   group's score is its largest c (EGOPQ_GROUP_MAX) or the sum of its two
+ *   largest (EGOPQ_GROUP_TOP2), and only experts of the topk_group best groups
+ *   are candidates
+ *   ids[t][0..k) = the candidates of the k largest c, largest first; ties, of
+ *   groups too, go to the lowest index
+ *   weights[t][j] = s[ids] (/ (sum_j s[ids] + 1e-20) with renorm) * scale
+ * k <= topk_group * (E / n_group); at most 512 experts, 32 picks, 32 groups
+ * (more: EGOPQ_ERR_UNSUPPORTED_SHAPE). A logit of -inf masks an expert off
+ * (score 0; it is chosen only where no other candidate is left); NaN reads as
+ * -inf, +inf as the largest finite number. A softmax without a bias chooses by
+ * the logits themselves, whose order it keeps (groups by two best scores:
+ * by the scores). */
+int egopq_moe_route(const void* logits, int logits_bf16, const float* bias, int64_t T, int E, int k,
+                    int score, int n_group, int topk_group, int group_score, int renorm,
+                    float scale, float* weights, int32_t* ids, egopq_stream_t stream);
+
+/* Pack the gate and up weights of E experts for egopq_moe_experts: w_q uint8
+ * [E][2I][K] with the I gate rows and then the I up rows of each expert, scale
+ * fp16 and zero uint8 [E][2I][G]. The packed form (egopq_packed_w4_bytes(E*2I,
+ * K, group) bytes) is egopq_pack_w4's of the same rows with each expert's gate
+ * and up rows interleaved sixteen at a time: packed row 32b + i is gate row
+ * 16b + i, row 32b + 16 + i up row 16b + i (i < 16). I % 128 == 0. The down
+ * weights [E][H][I] are packed by egopq_pack_w4 as one [E*H][I] weight. */
+int egopq_moe_pack_gate_up(const uint8_t* w_q, const uint16_t* scale_f16, const uint8_t* zero,
+                           int64_t E, int64_t I, int64_t K, int group, void* packed,
+                           egopq_stream_t stream);
+
+/* The gated linears of the experts each token picked, summed:
+ *   out[t] = bf16( sum_j weights[t][j] * D_e( silu(G_e x_t) * (U_e x_t) ) ),
+ *   e = ids[t][j], silu(v) = v / (1 + exp(-v))
+ * x bf16 [T][H], ids int32 and weights fp32 [T][k], out bf16 [T][H] (a token
+ * whose picks are all outside [0, E) gives 0). variant EGOPQ_VARIANT_W4A16:
+ * bf16 activations; EGOPQ_VARIANT_W4A8: int8 codes of x and of the bf16 gated
+ * values, per row as in egopq_quant_act_i8. Accumulation in fp32; the gated
+ * values and each pick's output are rounded to bf16 once on the way. H and I
+ * multiples of 128 below 2^20, E <= 1024. path: EGOPQ_PATH_GEMV streams the weights for
+ * few rows an expert, EGOPQ_PATH_TC runs the tcgen05 products, AUTO picks by
+ * the rows an expert has on average. */
+size_t egopq_moe_experts_workspace_bytes(int64_t T, int k, int E, int64_t H, int64_t I, int group,
+                                         int variant, int path);
+int egopq_moe_experts(const uint16_t* x_bf16, const int32_t* ids, const float* weights,
+                      const void* packed_gate_up, const void* packed_down, int64_t T, int k, int E,
+                      int64_t H, int64_t I, int group, int variant, uint16_t* out_bf16,
+                      void* workspace, size_t workspace_bytes, int path, egopq_stream_t stream);
+
+/* Low-rank adapters beside a shared projection:
+ *   y_out[m] = bf16( y_in[m] + scale[a] * B_a (A_a x[m]) ),  a = ids[m]
+ * y_in, y_out bf16 [M][N] (may be the same buffer), x bf16 [M][K]; A bf16
+ * [L][r][K], B bf16 [L][N][r], scale fp32 [L]; ranks int32 [L] or NULL:
+ * adapter a uses its first ranks[a] (at most r) rows of A and columns of B,
+ * whatever the rest holds. A row whose id is outside [0, L) keeps y_in.
+ * r a multiple of 8, at most 128; K and N multiples of 128, N < 2^24,
+ * L <= 1024. A x is summed in fp32 and, scaled, rounded to bf16 once. */
+size_t egopq_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int L, int r);
+int egopq_lora_add(const uint16_t* y_in, const uint16_t* x_bf16, const uint16_t* A_bf16,
+                   const uint16_t* B_bf16, const float* scale, const int32_t* ranks,
+                   const int32_t* ids, int64_t M, int64_t N, int64_t K, int L, int r,
+                   uint16_t* y_out, void* workspace, size_t workspace_bytes,
+                   egopq_stream_t stream);
+
+/* egopq_w4a8_linear and egopq_lora_add on its output, in one call. */
+size_t egopq_w4a8_linear_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int group, int L,
+                                              int r, int path);
+int egopq_w4a8_linear_lora(const uint16_t* x_bf16, const void* packed, const uint16_t* A_bf16,
+                           const uint16_t* B_bf16, const float* scale, const int32_t* ranks,
+                           const int32_t* ids, int64_t M, int64_t N, int64_t K, int group, int L,
+                           int r, uint16_t* y_bf16, void* workspace, size_t workspace_bytes,
+                           int path, egopq_stream_t stream);
+
 /* ---- support, status --------------------------------------------------------------
  * 1 if (M, N, K, group, variant) is accepted by the parity-tested kernels on
  * the current device, 0 if not. It claims nothing the kernels do not run (a

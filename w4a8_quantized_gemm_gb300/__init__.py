@@ -84,6 +84,18 @@ def load() -> ctypes.CDLL:
             "egopq_w4a8_linear_grouped": (i32, [vp, i32, vp, vp, i64, i64, i32, vp, vp, sz, i32,
                                                 vp]),
             "egopq_bf16_gemm_twin": (i32, [vp, vp, i64, i64, i64, vp, vp]),
+            "egopq_moe_route": (i32, [vp, i32, vp, i64, i32, i32, i32, i32, i32, i32, i32,
+                                      ctypes.c_float, vp, vp, vp]),
+            "egopq_moe_pack_gate_up": (i32, [vp, vp, vp, i64, i64, i64, i32, vp, vp]),
+            "egopq_moe_experts_workspace_bytes": (sz, [i64, i32, i32, i64, i64, i32, i32, i32]),
+            "egopq_moe_experts": (i32, [vp, vp, vp, vp, vp, i64, i32, i32, i64, i64, i32, i32, vp,
+                                        vp, sz, i32, vp]),
+            "egopq_lora_workspace_bytes": (sz, [i64, i64, i64, i32, i32]),
+            "egopq_lora_add": (i32, [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, vp, vp,
+                                     sz, vp]),
+            "egopq_w4a8_linear_lora_workspace_bytes": (sz, [i64, i64, i64, i32, i32, i32, i32]),
+            "egopq_w4a8_linear_lora": (i32, [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32,
+                                             i32, vp, vp, sz, i32, vp]),
             "egopq_supported": (i32, [i64, i64, i64, i32, i32]),
             "egopq_auto_path": (i32, [i64, i32]),
             "egopq_tc_operand_bytes": (sz, [i64, i64, i32]),
@@ -422,6 +434,205 @@ def bf16_gemm_twin(x: torch.Tensor, w: torch.Tensor, out: Optional[torch.Tensor]
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
     _check(load().egopq_bf16_gemm_twin(_ptr(x), _ptr(w), M, N, K, _ptr(out), _stream(stream)))
+    return out
+
+
+# ------------------------------------------ rows that pick their own weights ---
+
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+GROUP_MAX, GROUP_TOP2 = 0, 1
+
+
+def _shape(t: torch.Tensor, *shape):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"tensor of shape {tuple(t.shape)}, expected {shape}")
+
+
+def moe_route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None,
+              score: int = SCORE_SOFTMAX, n_group: int = 1, topk_group: int = 1,
+              group_score: int = GROUP_MAX, renorm: bool = True, scale: float = 1.0,
+              out: Optional[tuple] = None, stream=None) -> tuple:
+    """The k experts of each token and their weights from router logits [T, E]
+    (fp32 or bf16): returns (weights fp32 [T, k], ids int32 [T, k]), the best
+    expert first (include/egopq.h has the formulas)."""
+    _dtype(logits, torch.float32, torch.bfloat16)
+    T, E = logits.shape
+    if bias is not None:
+        _dtype(bias, torch.float32)
+        _shape(bias, E)
+    if out is None:
+        out = (torch.empty((T, k), dtype=torch.float32, device=logits.device),
+               torch.empty((T, k), dtype=torch.int32, device=logits.device))
+    weights, ids = out
+    _dtype(weights, torch.float32)
+    _dtype(ids, torch.int32)
+    _shape(weights, T, k)
+    _shape(ids, T, k)
+    _check(load().egopq_moe_route(_ptr(logits), logits.dtype == torch.bfloat16, _ptr(bias), T, E, k,
+                                  score, n_group, topk_group, group_score, renorm, scale,
+                                  _ptr(weights), _ptr(ids), _stream(stream)))
+    return weights, ids
+
+
+class MoeLayer(NamedTuple):
+    """Packed weights of a layer's experts (moe_pack)."""
+    gate_up: torch.Tensor  # uint8, gate and up rows interleaved
+    down: torch.Tensor     # uint8
+    E: int
+    H: int
+    I: int
+
+
+def moe_pack(gate_up_q: torch.Tensor, gate_up_scale: torch.Tensor, gate_up_zero: torch.Tensor,
+             down_q: torch.Tensor, down_scale: torch.Tensor, down_zero: torch.Tensor,
+             stream=None) -> MoeLayer:
+    """Pack the experts of a layer: gate_up uint8 codes [E, 2I, H] (I gate rows,
+    then I up rows) with fp16 scales and uint8 zero points [E, 2I, H/128], and
+    down codes [E, H, I] with theirs [E, H, I/128]."""
+    _dtype(gate_up_q, torch.uint8)
+    _dtype(gate_up_scale, torch.float16)
+    _dtype(gate_up_zero, torch.uint8)
+    E, I2, H = gate_up_q.shape
+    I = I2 // 2
+    if I2 % 2:
+        raise ValueError(f"{I2} gate and up rows: an odd number")
+    _shape(gate_up_scale, E, I2, H // GROUP)
+    _shape(gate_up_zero, E, I2, H // GROUP)
+    _shape(down_q, E, H, I)
+    _shape(down_scale, E, H, I // GROUP)
+    _shape(down_zero, E, H, I // GROUP)
+    nbytes = packed_w4_bytes(E * I2, H)
+    if nbytes == 0 or I % GROUP:
+        raise EgopqError(-2, f"experts with H={H} I={I} are not packable (multiples of 128)")
+    packed = torch.empty(nbytes, dtype=torch.uint8, device=gate_up_q.device)
+    _check(load().egopq_moe_pack_gate_up(_ptr(gate_up_q), _ptr(gate_up_scale), _ptr(gate_up_zero),
+                                         E, I, H, GROUP, _ptr(packed), _stream(stream)))
+    down = pack_w4(down_q.view(E * H, I), down_scale.view(E * H, I // GROUP),
+                   down_zero.view(E * H, I // GROUP), stream=stream)
+    return MoeLayer(packed, down, E, H, I)
+
+
+def moe_workspace_bytes(T: int, k: int, E: int, H: int, I: int, variant: int = VARIANT_W4A8,
+                        path: int = PATH_AUTO) -> int:
+    return int(load().egopq_moe_experts_workspace_bytes(T, k, E, H, I, GROUP, variant, path))
+
+
+def moe_workspace(T: int, k: int, E: int, H: int, I: int, variant: int, device,
+                  path: int = PATH_AUTO) -> torch.Tensor:
+    """A workspace for moe_experts of T tokens (and of any fewer)."""
+    return torch.empty(moe_workspace_bytes(T, k, E, H, I, variant, path), dtype=torch.uint8,
+                       device=device)
+
+
+def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, layer: MoeLayer,
+                variant: int = VARIANT_W4A8, path: int = PATH_AUTO,
+                out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """The gated linears of the experts each token picked, summed with its
+    weights: x bf16 [T, H], ids int32 and weights fp32 [T, k] -> bf16 [T, H].
+    An id outside [0, E) adds nothing."""
+    _dtype(x, torch.bfloat16)
+    _dtype(ids, torch.int32)
+    _dtype(weights, torch.float32)
+    T, H = x.shape
+    k = ids.shape[1]
+    _shape(x, T, layer.H)
+    _shape(ids, T, k)
+    _shape(weights, T, k)
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    _dtype(out, torch.bfloat16)
+    _shape(out, T, H)
+    if workspace is None:
+        workspace = moe_workspace(T, k, layer.E, H, layer.I, variant, x.device, path)
+    _check(load().egopq_moe_experts(_ptr(x), _ptr(ids), _ptr(weights), _ptr(layer.gate_up),
+                                    _ptr(layer.down), T, k, layer.E, H, layer.I, GROUP, variant,
+                                    _ptr(out), _ptr(workspace), workspace.nbytes, path,
+                                    _stream(stream)))
+    return out
+
+
+class LoraAdapters:
+    """The low-rank adapters of one projection: A bf16 [L, r, K], B bf16
+    [L, N, r], scale fp32 [L], ranks int32 [L] (adapter a uses its first
+    ranks[a]; None: r everywhere)."""
+
+    def __init__(self, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor,
+                 ranks: Optional[torch.Tensor] = None):
+        _dtype(A, torch.bfloat16)
+        _dtype(B, torch.bfloat16)
+        _dtype(scale, torch.float32)
+        self.L, self.r, self.K = A.shape
+        self.N = B.shape[1]
+        _shape(B, self.L, self.N, self.r)
+        _shape(scale, self.L)
+        if ranks is not None:
+            _dtype(ranks, torch.int32)
+            _shape(ranks, self.L)
+        self.A, self.B, self.scale, self.ranks = A, B, scale, ranks
+
+
+def lora_workspace(M: int, N: int, K: int, adapters: LoraAdapters, device) -> torch.Tensor:
+    return torch.empty(int(load().egopq_lora_workspace_bytes(M, N, K, adapters.L, adapters.r)),
+                       dtype=torch.uint8, device=device)
+
+
+def lora_add(y: torch.Tensor, x: torch.Tensor, adapters: LoraAdapters, ids: torch.Tensor,
+             workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+             stream=None) -> torch.Tensor:
+    """y [M, N] + scale * B_a (A_a x) for each row's adapter a = ids[m] (rows
+    with an id outside [0, L) keep y); bf16. `out` may be y itself."""
+    _dtype(x, torch.bfloat16)
+    _dtype(y, torch.bfloat16)
+    _dtype(ids, torch.int32)
+    a = adapters
+    M = x.shape[0]
+    _shape(x, M, a.K)
+    _shape(y, M, a.N)
+    _shape(ids, M)
+    if out is None:
+        out = torch.empty_like(y)
+    _dtype(out, torch.bfloat16)
+    _shape(out, M, a.N)
+    if workspace is None:
+        workspace = lora_workspace(M, a.N, a.K, a, x.device)
+    _check(load().egopq_lora_add(_ptr(y), _ptr(x), _ptr(a.A), _ptr(a.B), _ptr(a.scale),
+                                 _ptr(a.ranks), _ptr(ids), M, a.N, a.K, a.L, a.r, _ptr(out),
+                                 _ptr(workspace), workspace.nbytes, _stream(stream)))
+    return out
+
+
+def w4a8_linear_lora_workspace(M: int, N: int, K: int, adapters: LoraAdapters, device,
+                               path: int = PATH_AUTO) -> torch.Tensor:
+    n = int(load().egopq_w4a8_linear_lora_workspace_bytes(M, N, K, GROUP, adapters.L, adapters.r,
+                                                          path))
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def w4a8_linear_lora(x: torch.Tensor, packed: torch.Tensor, N: int, adapters: LoraAdapters,
+                     ids: torch.Tensor, path: int = PATH_AUTO,
+                     workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """w4a8_linear of x [M, K] and the adapters' update of its output, in one
+    call."""
+    _dtype(x, torch.bfloat16)
+    _dtype(ids, torch.int32)
+    a = adapters
+    M, K = x.shape
+    _shape(x, M, a.K)
+    _shape(ids, M)
+    if N != a.N:
+        raise ValueError(f"adapters of {a.N} outputs beside a projection of {N}")
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    _dtype(out, torch.bfloat16)
+    _shape(out, M, N)
+    if workspace is None:
+        workspace = w4a8_linear_lora_workspace(M, N, K, a, x.device, path)
+    _check(load().egopq_w4a8_linear_lora(_ptr(x), _ptr(packed), _ptr(a.A), _ptr(a.B),
+                                         _ptr(a.scale), _ptr(a.ranks), _ptr(ids), M, N, K, GROUP,
+                                         a.L, a.r, _ptr(out), _ptr(workspace), workspace.nbytes,
+                                         path, _stream(stream)))
     return out
 
 

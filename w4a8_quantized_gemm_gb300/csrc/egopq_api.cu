@@ -32,9 +32,9 @@ int device_sm_count() {
 
 using namespace egopq;
 
-namespace {
+static thread_local char g_msg[512] = "";
 
-thread_local char g_msg[512] = "";
+namespace egopq {
 
 int fail(int code, const char* fmt, ...) {
   va_list ap;
@@ -47,6 +47,10 @@ int fail(int code, const char* fmt, ...) {
 int cuda_fail(cudaError_t e, const char* what) {
   return fail(EGOPQ_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
+
+}  // namespace egopq
+
+namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -95,10 +99,6 @@ int check_w4_shape(int64_t M, int64_t N, int64_t K, int group) {
   return EGOPQ_OK;
 }
 
-}  // namespace egopq
-
-namespace {
-
 int check_ptrs(int n, ...) {
   va_list ap;
   va_start(ap, n);
@@ -117,6 +117,10 @@ int check_ptrs(int n, ...) {
   va_end(ap);
   return EGOPQ_OK;
 }
+
+}  // namespace egopq
+
+namespace {
 
 int run_gemm(const GemmArgs& a, int path, cudaStream_t st) {
   if (path != EGOPQ_PATH_AUTO && path != EGOPQ_PATH_GEMV && path != EGOPQ_PATH_TC)

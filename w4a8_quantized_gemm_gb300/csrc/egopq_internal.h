@@ -58,6 +58,49 @@ class SmemOptIn {
   std::atomic<size_t> done_[kMaxDevices] = {};
 };
 
+// 32 packed int4 codes of one weight row (one 16-byte unit of the record:
+// K offsets 0..31 of a 32-wide slice, nibble order as packed) -> 16 words of
+// a matrix instruction's A operand, zero point folded in: fp16 (w - z) pairs for
+// W4A8, bf16 pairs for W4A16; both exact.
+template <int VARIANT>
+__device__ __forceinline__ void cvt_w4_unit(const uint4& v, uint32_t z, uint32_t (&o)[16]) {
+  const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (VARIANT == kW4A8) {
+    // fp16: 0x6400|e = 1024+e, 0x6400|(e<<4) = 1024+16e (exact)
+    const __half2 zlo = __half2half2(__ushort_as_half((uint16_t)(0x6400u | z)));
+    const __half2 nzhi = __half2half2(__float2half_rn(-64.0f - (float)z));
+    const __half2 sixteenth = __float2half2_rn(0.0625f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t w = wv[j], w2 = wv[j] >> 8;
+      uint32_t h0 = lop3_and_or(w, 0x000F000Fu, 0x64006400u);
+      uint32_t h1 = lop3_and_or(w, 0x00F000F0u, 0x64006400u);
+      uint32_t h2 = lop3_and_or(w2, 0x000F000Fu, 0x64006400u);
+      uint32_t h3 = lop3_and_or(w2, 0x00F000F0u, 0x64006400u);
+      __half2 r0 = __hsub2(*reinterpret_cast<__half2*>(&h0), zlo);
+      __half2 r1 = __hfma2(*reinterpret_cast<__half2*>(&h1), sixteenth, nzhi);
+      __half2 r2 = __hsub2(*reinterpret_cast<__half2*>(&h2), zlo);
+      __half2 r3 = __hfma2(*reinterpret_cast<__half2*>(&h3), sixteenth, nzhi);
+      o[j * 4 + 0] = *reinterpret_cast<uint32_t*>(&r0);
+      o[j * 4 + 1] = *reinterpret_cast<uint32_t*>(&r1);
+      o[j * 4 + 2] = *reinterpret_cast<uint32_t*>(&r2);
+      o[j * 4 + 3] = *reinterpret_cast<uint32_t*>(&r3);
+    }
+  } else {
+    // bf16: 0x4300|e = 128+e (exact for e < 128)
+    const __nv_bfloat162 zz = __bfloat162bfloat162(__ushort_as_bfloat16((uint16_t)(0x4300u | z)));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t h = lop3_and_or(wv[j] >> (4 * q), 0x000F000Fu, 0x43004300u);
+        __nv_bfloat162 rr = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&h), zz);
+        o[j * 4 + q] = *reinterpret_cast<uint32_t*>(&rr);
+      }
+    }
+  }
+}
+
 // Sibling linears that read the same activations, run as one launch: the
 // output tiles (128 weight rows each) of linear j are the global tiles
 // [tile0[j], tile0[j + 1]); a single linear is the table with count 1.
@@ -151,6 +194,130 @@ cudaError_t launch_pack_w4_gptq(const int32_t* qweight, const int32_t* qzeros,
                                void* packed, cudaStream_t st);
 cudaError_t launch_dequant_w4(const void* packed, int64_t N, int64_t K, uint16_t* w,
                               cudaStream_t st);
+
+// ---- rows that pick their own weights (experts, adapters) -------------------------
+// Host-side failure reporting of the entry points: records the calling thread's
+// last error and returns `code` (an egopq_status).
+int fail(int code, const char* fmt, ...);
+int cuda_fail(cudaError_t e, const char* what);
+// (name, pointer) pairs that must be non-null and 16-byte aligned.
+int check_ptrs(int n, ...);
+
+// A launch configuration whose grid may start while the preceding one drains
+// (its kernel waits with griddepcontrol.wait before it touches memory).
+struct PdlConfig {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  PdlConfig(dim3 grid, unsigned threads, size_t smem, cudaStream_t st) {
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+};
+
+constexpr int kMaxSets = 1024;  // weight sets (experts, adapters) of one call
+
+// Where a plan of n slots over S sets lies in a workspace (device memory):
+//   head   [0] slots that picked a set, [1] entries of the tile table
+//   order  [n] slots sorted by set (slot order inside a set); those without a
+//          set come last
+//   pos    [n] sorted position of each slot, -1 without a set (may be null)
+//   tiles  {set, first sorted position, rows} of each tile of at most bt rows
+//          of one set; some entries are empty (rows = 0)
+struct RowPlan {
+  int* head;
+  int32_t* order;
+  int32_t* pos;
+  int4* tiles;
+};
+// Entries the tile table can have (its allocation, and the grid over it).
+inline int64_t plan_max_tiles(int64_t n, int S, int bt) { return n / bt + (S < n ? S : n); }
+
+struct RouteArgs {
+  const void* logits;
+  const float* bias;
+  float* weights;
+  int32_t* ids;
+  int64_t T;
+  int E, k, n_group, topk_group, bf16, sigmoid, top2, renorm;
+  float scale;
+};
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t st);
+cudaError_t launch_plan(const int32_t* ids, int64_t n, int S, int bt, const RowPlan& plan,
+                        cudaStream_t st);
+
+// Experts: one call's operands and workspace parts, validated by the ABI layer.
+struct ExpertsArgs {
+  int variant;  // kW4A8 or kW4A16
+  int64_t T, H, I;
+  int E, k;
+  bool tensor;  // the tcgen05 products; else the streaming ones
+  const uint16_t* x;
+  const int32_t* ids;
+  const float* weights;
+  const uint8_t* gate_up;
+  const uint8_t* down;
+  uint16_t* out;
+  RowPlan plan;
+  // W4A8: codes of x [T][H] and of h [T*k][I], their scales and group sums
+  int8_t* x_q;
+  float* x_s;
+  int32_t* x_gsum;
+  int8_t* h_q;
+  float* h_s;
+  int32_t* h_gsum;
+  void* h_tc;          // fp16 codes of h [T*k][I] (W4A8, tensor)
+  uint16_t* rows;      // activations in sorted order [T*k][H] (tensor)
+  float* rows_s;       // their scales (W4A8, tensor)
+  uint16_t* h;         // bf16 [T*k][I]
+  uint16_t* y;         // bf16 [T*k][H]
+  uint64_t timeout_ns;
+};
+cudaError_t launch_experts(const ExpertsArgs& a, cudaStream_t st);
+// One tcgen05 product over sorted rows: kGateUp (h = silu(g) * u) or the down
+// projection.
+struct RaggedArgs {
+  int variant;
+  bool gate_up;
+  int64_t rows_max;     // rows of `act` (T * k)
+  int64_t N, K;         // weight rows and columns of one set
+  int E;
+  const void* act;      // fp16 codes or bf16 [rows_max][K], sorted rows
+  const float* a_s;     // scales of the sorted rows (W4A8)
+  const uint8_t* packed;
+  uint16_t* y;
+  RowPlan plan;
+  uint64_t timeout_ns;
+};
+
+struct LoraArgs {
+  const uint16_t* y_in;
+  const uint16_t* x;
+  const uint16_t* A;
+  const uint16_t* B;
+  const float* scale;
+  const int32_t* ranks;  // may be null: r everywhere
+  const int32_t* ids;
+  int64_t M, N, K;
+  int L, r;
+  uint16_t* y_out;
+  RowPlan plan;
+  float* h;  // [lora_splits][M][r] partial sums of A x, sorted rows
+};
+// Rows of one tile of the adapters' products, and the CTAs K is split over.
+int lora_tile(int64_t M);
+int lora_splits(int64_t M, int64_t K);
+cudaError_t launch_lora(const LoraArgs& a, cudaStream_t st);
+
+// Weights [E][2I][K] with I gate rows and then I up rows a set, packed with
+// the two interleaved sixteen rows at a time.
+cudaError_t launch_pack_gate_up(const uint8_t* w_q, const uint16_t* s, const uint8_t* z, int64_t E,
+                                int64_t I, int64_t K, void* packed, cudaStream_t st);
 
 // Each kernel unit's device error word, read and cleared (see egopq_common.cuh).
 cudaError_t take_error_word_quant_pack(unsigned* out);

@@ -336,8 +336,19 @@ __device__ __constant__ int kNibbleK[8] = {0, 2, 4, 6, 1, 3, 5, 7};
 // [8448, 8512) -- so one bulk copy stages everything a group of 128 rows needs.
 constexpr int64_t kRecBytes = 8512;
 
+// Source row of packed row n: n itself, or with gate_up = I > 0 (experts' gate
+// and up weights, I rows of each a set) the row that interleaves the two
+// sixteen at a time: packed rows 32b .. 32b + 15 of a set are its gate rows
+// 16b .., rows 32b + 16 .. its up rows 16b .. . A warp that owns 32 packed rows
+// then holds both factors of 16 outputs.
+__device__ __forceinline__ int64_t pack_source_row(int64_t n, int64_t gate_up) {
+  if (gate_up == 0) return n;
+  const int64_t set = n / (2 * gate_up), in = n - set * 2 * gate_up;
+  return set * 2 * gate_up + ((in >> 4) & 1) * gate_up + (in >> 5) * 16 + (in & 15);
+}
+
 __global__ void pack_codes_kernel(const uint8_t* __restrict__ w_q, int64_t N, int64_t K,
-                                  uint8_t* __restrict__ out) {
+                                  int64_t gate_up, uint8_t* __restrict__ out) {
   const int64_t G = K / 128;
   const int64_t nwords = N * K / 8;
   for (int64_t w = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; w < nwords;
@@ -347,7 +358,8 @@ __global__ void pack_codes_kernel(const uint8_t* __restrict__ w_q, int64_t N, in
     const int64_t unit = u / 4, j = u % 4;
     const int64_t c = unit / 128, r = unit % 128;
     const int64_t n = t * 128 + r, k0 = g * 128 + c * 32 + j * 8;
-    const uint2 src = *reinterpret_cast<const uint2*>(w_q + n * K + k0);
+    const uint2 src =
+        *reinterpret_cast<const uint2*>(w_q + pack_source_row(n, gate_up) * K + k0);
     const uint8_t* b = reinterpret_cast<const uint8_t*>(&src);
     uint32_t word = 0;
 #pragma unroll
@@ -378,15 +390,17 @@ __global__ void unpack_codes_kernel(const uint8_t* __restrict__ in, int64_t N, i
 
 // scales [N][G] and zeros [N][G] into (and out of) the records
 __global__ void pack_meta_kernel(const uint16_t* __restrict__ s, const uint8_t* __restrict__ z,
-                                 int64_t N, int64_t G, uint8_t* __restrict__ out) {
+                                 int64_t N, int64_t G, int64_t gate_up,
+                                 uint8_t* __restrict__ out) {
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < G * N;
        i += (int64_t)gridDim.x * blockDim.x) {
     const int64_t g = i / N, n = i % N;
     uint8_t* rec = out + ((n / 128) * G + g) * kRecBytes;
     const int64_t r = n % 128;
-    *reinterpret_cast<uint16_t*>(rec + 8192 + 2 * r) = s[n * G + g];
+    const int64_t sn = pack_source_row(n, gate_up);  // (an even row's neighbour is sn + 1)
+    *reinterpret_cast<uint16_t*>(rec + 8192 + 2 * r) = s[sn * G + g];
     if ((r & 1) == 0)
-      rec[8448 + r / 2] = (uint8_t)((z[n * G + g] & 0xF) | ((z[(n + 1) * G + g] & 0xF) << 4));
+      rec[8448 + r / 2] = (uint8_t)((z[sn * G + g] & 0xF) | ((z[(sn + 1) * G + g] & 0xF) << 4));
   }
 }
 
@@ -553,15 +567,25 @@ cudaError_t launch_quant_act(const uint16_t* x, int64_t M, int64_t K, int8_t* a_
   return cudaLaunchKernelEx(&cfg, quant_act_kernel, x, K, a_q, a_s, a_gsum, a_tc, tc_fp8);
 }
 
-cudaError_t launch_pack_w4(const uint8_t* w_q, const uint16_t* s, const uint8_t* z, int64_t N,
-                           int64_t K, void* packed, cudaStream_t st) {
+static cudaError_t pack_w4(const uint8_t* w_q, const uint16_t* s, const uint8_t* z, int64_t N,
+                           int64_t K, int64_t gate_up, void* packed, cudaStream_t st) {
   const int64_t G = K / 128;
   uint8_t* base = static_cast<uint8_t*>(packed);
-  pack_codes_kernel<<<grid_for(N * K / 8, 256), 256, 0, st>>>(w_q, N, K, base);
+  pack_codes_kernel<<<grid_for(N * K / 8, 256), 256, 0, st>>>(w_q, N, K, gate_up, base);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  pack_meta_kernel<<<grid_for(G * N, 256), 256, 0, st>>>(s, z, N, G, base);
+  pack_meta_kernel<<<grid_for(G * N, 256), 256, 0, st>>>(s, z, N, G, gate_up, base);
   return cudaGetLastError();
+}
+
+cudaError_t launch_pack_w4(const uint8_t* w_q, const uint16_t* s, const uint8_t* z, int64_t N,
+                           int64_t K, void* packed, cudaStream_t st) {
+  return pack_w4(w_q, s, z, N, K, 0, packed, st);
+}
+
+cudaError_t launch_pack_gate_up(const uint8_t* w_q, const uint16_t* s, const uint8_t* z, int64_t E,
+                                int64_t I, int64_t K, void* packed, cudaStream_t st) {
+  return pack_w4(w_q, s, z, E * 2 * I, K, I, packed, st);
 }
 
 cudaError_t launch_unpack_w4(const void* packed, int64_t N, int64_t K, uint8_t* w_q, uint16_t* s,

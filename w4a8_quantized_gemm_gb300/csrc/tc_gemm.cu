@@ -309,49 +309,6 @@ struct TcCfg {
   static_assert(kStageBytes % 1024 == 0, "stage alignment");
 };
 
-// 32 packed int4 codes of one weight row (one 16-byte unit of the record:
-// K offsets 0..31 of a 32-wide slice, nibble order as packed) -> 16 words of
-// the tensor-core A operand, zero point folded in: fp16 (w - z) pairs for
-// W4A8, bf16 pairs for W4A16; both exact.
-template <int VARIANT>
-__device__ __forceinline__ void cvt_w4_unit(const uint4& v, uint32_t z, uint32_t (&o)[16]) {
-  const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
-  if constexpr (VARIANT == kW4A8) {
-    // fp16: 0x6400|e = 1024+e, 0x6400|(e<<4) = 1024+16e (exact)
-    const __half2 zlo = __half2half2(__ushort_as_half((uint16_t)(0x6400u | z)));
-    const __half2 nzhi = __half2half2(__float2half_rn(-64.0f - (float)z));
-    const __half2 sixteenth = __float2half2_rn(0.0625f);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t w = wv[j], w2 = wv[j] >> 8;
-      uint32_t h0 = lop3_and_or(w, 0x000F000Fu, 0x64006400u);
-      uint32_t h1 = lop3_and_or(w, 0x00F000F0u, 0x64006400u);
-      uint32_t h2 = lop3_and_or(w2, 0x000F000Fu, 0x64006400u);
-      uint32_t h3 = lop3_and_or(w2, 0x00F000F0u, 0x64006400u);
-      __half2 r0 = __hsub2(*reinterpret_cast<__half2*>(&h0), zlo);
-      __half2 r1 = __hfma2(*reinterpret_cast<__half2*>(&h1), sixteenth, nzhi);
-      __half2 r2 = __hsub2(*reinterpret_cast<__half2*>(&h2), zlo);
-      __half2 r3 = __hfma2(*reinterpret_cast<__half2*>(&h3), sixteenth, nzhi);
-      o[j * 4 + 0] = *reinterpret_cast<uint32_t*>(&r0);
-      o[j * 4 + 1] = *reinterpret_cast<uint32_t*>(&r1);
-      o[j * 4 + 2] = *reinterpret_cast<uint32_t*>(&r2);
-      o[j * 4 + 3] = *reinterpret_cast<uint32_t*>(&r3);
-    }
-  } else {
-    // bf16: 0x4300|e = 128+e (exact for e < 128)
-    const __nv_bfloat162 zz = __bfloat162bfloat162(__ushort_as_bfloat16((uint16_t)(0x4300u | z)));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t h = lop3_and_or(wv[j] >> (4 * q), 0x000F000Fu, 0x43004300u);
-        __nv_bfloat162 rr = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&h), zz);
-        o[j * 4 + q] = *reinterpret_cast<uint32_t*>(&rr);
-      }
-    }
-  }
-}
-
 // y[m0+t][n] = bf16(a_s[m0+t] * R[t]) (W4A8) or bf16(R[t]), t < HB, rows < M,
 // into the output `o` of this tile's linear. Eight rows at a time, with a
 // compiler barrier between chunks so the a_s loads are not all hoisted (they
