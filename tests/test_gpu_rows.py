@@ -230,7 +230,16 @@ def test_experts_stream(variant, T, E, k, H, I):
 
 
 @pytest.mark.parametrize("variant", VARIANTS)
-@pytest.mark.parametrize("path", [eg.PATH_GEMV])
+@pytest.mark.parametrize("T,E,k,H,I", [
+    (1, 1, 1, 128, 128), (3, 4, 2, 256, 128), (40, 3, 2, 384, 256), (191, 1, 1, 256, 128),
+    (192, 2, 2, 128, 256), (193, 2, 1, 256, 256), (500, 6, 3, 640, 384), (333, 40, 4, 256, 128),
+    (1500, 5, 2, 256, 1152), (700, 200, 8, 128, 128)])
+def test_experts_tensor_cores(variant, T, E, k, H, I):
+    check_experts(experts_case(T + E, T, E, k, H, I), variant, eg.PATH_TC)
+
+
+@pytest.mark.parametrize("variant", VARIANTS)
+@pytest.mark.parametrize("path", [eg.PATH_GEMV, eg.PATH_TC])
 def test_experts_dropped_repeated_and_skewed_picks(variant, path):
     x, ids, w, gu, dn = experts_case(5, 70, 6, 3, 256, 128)
     ids[::3] = -1                              # tokens without any expert
@@ -246,7 +255,7 @@ def test_experts_dropped_repeated_and_skewed_picks(variant, path):
 
 
 @pytest.mark.parametrize("variant", VARIANTS)
-@pytest.mark.parametrize("path", [eg.PATH_GEMV])
+@pytest.mark.parametrize("path", [eg.PATH_GEMV, eg.PATH_TC])
 def test_experts_zero_rows_weights_and_empty_batch(variant, path):
     x, ids, w, gu, dn = experts_case(6, 20, 4, 2, 256, 128)
     x[3] = 0
@@ -258,7 +267,7 @@ def test_experts_zero_rows_weights_and_empty_batch(variant, path):
     assert eg.moe_experts(x[:0], ids[:0], w[:0], layer, variant=variant).shape == (0, 256)
 
 
-@pytest.mark.parametrize("path", [eg.PATH_GEMV])
+@pytest.mark.parametrize("path", [eg.PATH_GEMV, eg.PATH_TC])
 def test_experts_on_another_stream_and_again_in_one_workspace(path):
     case = experts_case(7, 40, 8, 4, 384, 256)
     x, ids, w, gu, dn = case

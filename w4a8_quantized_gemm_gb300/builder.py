@@ -22,8 +22,8 @@ LIB = os.path.join(BUILD, "libegopq.so")
 DEBUG_BUILD = os.path.join(BUILD, "debug")
 DEBUG_LIB = os.path.join(BUILD, "libegopq_debug.so")
 SOURCES = ["egopq_api.cu", "quant_pack.cu", "gemv.cu", "tc_gemm.cu", "no_alloc.cu",
-           "rows_api.cu", "route.cu", "experts.cu", "lora.cu"]
-HEADERS = ["egopq_common.cuh", "egopq_internal.h"]
+           "rows_api.cu", "route.cu", "experts.cu", "tc_experts.cu", "lora.cu"]
+HEADERS = ["egopq_common.cuh", "egopq_internal.h", "tc_kernel.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                 "-Xcompiler", "-Wall", "-Xcompiler", "-Wno-unknown-pragmas"]

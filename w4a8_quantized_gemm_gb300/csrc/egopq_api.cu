@@ -610,7 +610,7 @@ int egopq_device_status(egopq_stream_t stream) {
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
   unsigned int word = 0;
   cudaError_t (*const take[])(unsigned*) = {take_error_word_quant_pack, take_error_word_gemv,
-                                            take_error_word_tc_gemm};
+                                            take_error_word_tc_gemm, take_error_word_tc_experts};
   for (auto fn : take) {
     unsigned int w = 0;
     e = fn(&w);
@@ -639,6 +639,7 @@ int egopq_debug_set_record_limit(uint64_t bytes) {
   if (rc) return rc;
   cudaError_t e = set_record_limit_gemv(bytes);
   if (e == cudaSuccess) e = set_record_limit_tc_gemm(bytes);
+  if (e == cudaSuccess) e = set_record_limit_tc_experts(bytes);
   return e == cudaSuccess ? EGOPQ_OK : cuda_fail(e, "set the record limit");
 #else
   (void)bytes;

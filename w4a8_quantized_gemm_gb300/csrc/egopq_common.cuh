@@ -394,6 +394,11 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
   return r;
 }
+// silu(g) * u (fast exponential and quotient: a few 2^-22, far below the bf16
+// rounding that follows)
+__device__ __forceinline__ float gated(float g, float u) {
+  return __fdividef(g, 1.f + __expf(-g)) * u;
+}
 __device__ __forceinline__ float bf16_bits_to_f32(uint16_t b) {
   return __uint_as_float(static_cast<uint32_t>(b) << 16);
 }

@@ -227,12 +227,15 @@ constexpr int kMaxSets = 1024;  // weight sets (experts, adapters) of one call
 //   order  [n] slots sorted by set (slot order inside a set); those without a
 //          set come last
 //   pos    [n] sorted position of each slot, -1 without a set (may be null)
+//   offset [S + 1] first sorted position of each set (set s has the slots
+//          [offset[s], offset[s + 1]) of order)
 //   tiles  {set, first sorted position, rows} of each tile of at most bt rows
 //          of one set; some entries are empty (rows = 0)
 struct RowPlan {
   int* head;
   int32_t* order;
   int32_t* pos;
+  int32_t* offset;
   int4* tiles;
 };
 // Entries the tile table can have (its allocation, and the grid over it).
@@ -279,6 +282,11 @@ struct ExpertsArgs {
   uint64_t timeout_ns;
 };
 cudaError_t launch_experts(const ExpertsArgs& a, cudaStream_t st);
+// Rows the tensor-core products' buffers hold (at least one more than
+// kTcFp8MaxM, so that the quantizer writes fp16 codes).
+inline int64_t experts_rows(int64_t n) { return n > 64 ? n : 65; }
+// AUTO's choice for n picks over E experts.
+inline bool experts_on_tensor_cores(int64_t n, int E) { return n > (int64_t)48 * E; }
 // One tcgen05 product over sorted rows: kGateUp (h = silu(g) * u) or the down
 // projection.
 struct RaggedArgs {
@@ -294,6 +302,7 @@ struct RaggedArgs {
   RowPlan plan;
   uint64_t timeout_ns;
 };
+cudaError_t launch_ragged(const RaggedArgs& a, cudaStream_t st);
 
 struct LoraArgs {
   const uint16_t* y_in;
@@ -323,10 +332,12 @@ cudaError_t launch_pack_gate_up(const uint8_t* w_q, const uint16_t* s, const uin
 cudaError_t take_error_word_quant_pack(unsigned* out);
 cudaError_t take_error_word_gemv(unsigned* out);
 cudaError_t take_error_word_tc_gemm(unsigned* out);
+cudaError_t take_error_word_tc_experts(unsigned* out);
 // Debug builds: the packed-record read limit of each unit that reads records
 // (cudaErrorNotSupported in release builds).
 cudaError_t set_record_limit_gemv(unsigned long long bytes);
 cudaError_t set_record_limit_tc_gemm(unsigned long long bytes);
+cudaError_t set_record_limit_tc_experts(unsigned long long bytes);
 
 // Byte size of the packed records of one linear with N rows and G groups.
 __host__ __device__ inline uint64_t packed_record_bytes(int64_t N, int G) {

@@ -57,6 +57,22 @@ struct StreamParams {
   int N, G;
 };
 
+// 16 int8 codes as fp16 pairs, in order: code + 128 as a byte under 0x64 is the
+// fp16 number 1024 + code + 128 (every step exact).
+__device__ __forceinline__ void codes_to_f16(const uint4& v, uint32_t* o) {
+  const __half2 bias = __float2half2_rn(1152.f);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t u = w[q] ^ 0x80808080u;
+    const uint32_t lo = prmt(u, 0x64646464u, 0x4140), hi = prmt(u, 0x64646464u, 0x4342);
+    const __half2 l2 = __hsub2(*reinterpret_cast<const __half2*>(&lo), bias);
+    const __half2 h2 = __hsub2(*reinterpret_cast<const __half2*>(&hi), bias);
+    o[q * 2] = *reinterpret_cast<const uint32_t*>(&l2);
+    o[q * 2 + 1] = *reinterpret_cast<const uint32_t*>(&h2);
+  }
+}
+
 // 32 activations of one row at K offset 32 * (lane % 4) of a group, as the
 // B-operand words of the group's eight K steps (words 2s and 2s + 1 of step s).
 template <int VARIANT>
@@ -68,21 +84,8 @@ __device__ __forceinline__ void load_act(const void* act, int64_t at, bool live,
       v[0] = __ldg(src);
       v[1] = __ldg(src + 1);
     }
-    // code + 128 as a byte under 0x64 is the fp16 number 1024 + code + 128
-    const __half2 bias = __float2half2_rn(1152.f);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t u = w[q] ^ 0x80808080u;
-        const uint32_t lo = prmt(u, 0x64646464u, 0x4140), hi = prmt(u, 0x64646464u, 0x4342);
-        const __half2 l2 = __hsub2(*reinterpret_cast<const __half2*>(&lo), bias);
-        const __half2 h2 = __hsub2(*reinterpret_cast<const __half2*>(&hi), bias);
-        b[i * 8 + q * 2] = *reinterpret_cast<const uint32_t*>(&l2);
-        b[i * 8 + q * 2 + 1] = *reinterpret_cast<const uint32_t*>(&h2);
-      }
-    }
+    codes_to_f16(v[0], b);
+    codes_to_f16(v[1], b + 8);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -95,11 +98,6 @@ __device__ __forceinline__ void load_act(const void* act, int64_t at, bool live,
       b[i * 4 + 3] = v.w;
     }
   }
-}
-
-// silu(g) * u
-__device__ __forceinline__ float gated(float g, float u) {
-  return __fdividef(g, 1.f + __expf(-g)) * u;
 }
 
 template <int VARIANT, bool GATE_UP, int NT>
@@ -261,6 +259,38 @@ combine_kernel(const uint16_t* __restrict__ y, const float* __restrict__ weights
   reinterpret_cast<uint4*>(out + t * H)[v] = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// ---- rows in sorted order -----------------------------------------------------------
+// rows[p] = x[order[p] / k] for the p that have an expert: bf16 as they are, or
+// int8 codes as fp16 (and their scales). One CTA a row.
+constexpr int kGatherThreads = 128;
+
+template <bool CODES>
+__global__ void __launch_bounds__(kGatherThreads)
+gather_rows_kernel(const void* __restrict__ x, const float* __restrict__ x_s,
+                   const int32_t* __restrict__ order, const int* __restrict__ head, int k,
+                   int64_t H, uint16_t* __restrict__ rows, float* __restrict__ rows_s) {
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  const int64_t p = blockIdx.x;
+  if (p >= head[0]) return;
+  const int64_t t = __ldg(order + p) / k;
+  uint4* dst = reinterpret_cast<uint4*>(rows + p * H);
+  if constexpr (CODES) {
+    if (threadIdx.x == 0) rows_s[p] = __ldg(x_s + t);
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const int8_t*>(x) + t * H);
+    for (int64_t v = threadIdx.x; v < H / 16; v += kGatherThreads) {
+      const uint4 c = __ldg(src + v);
+      uint32_t o[8];
+      codes_to_f16(c, o);
+      dst[2 * v] = make_uint4(o[0], o[1], o[2], o[3]);
+      dst[2 * v + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+  } else {
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + t * H);
+    for (int64_t v = threadIdx.x; v < H / 8; v += kGatherThreads) dst[v] = __ldg(src + v);
+  }
+}
+
 // ---- launches -----------------------------------------------------------------------
 template <int VARIANT, bool GATE_UP>
 static cudaError_t launch_stream(const StreamParams& p, int64_t tiles, int bt, cudaStream_t st) {
@@ -272,8 +302,64 @@ static cudaError_t launch_stream(const StreamParams& p, int64_t tiles, int bt, c
   }
 }
 
+static cudaError_t launch_combine(const ExpertsArgs& a, cudaStream_t st) {
+  PdlConfig c(dim3((unsigned)a.T, (unsigned)((a.H / 8 + kCombineThreads - 1) / kCombineThreads), 1),
+              kCombineThreads, 0, st);
+  return cudaLaunchKernelEx(&c.cfg, combine_kernel, (const uint16_t*)a.y, a.weights,
+                            (const int32_t*)a.plan.pos, a.k, a.H, a.out);
+}
+
+// Many rows an expert: the rows in sorted order, then the tcgen05 products.
+template <int VARIANT>
+static cudaError_t run_experts_tensor(const ExpertsArgs& a, cudaStream_t st) {
+  constexpr bool kCodes = VARIANT == kW4A8;
+  const int64_t n = a.T * a.k;
+  cudaError_t e = launch_plan(a.ids, n, a.E, 192, a.plan, st);
+  if (e != cudaSuccess) return e;
+  if (kCodes) {
+    e = launch_quant_act(a.x, a.T, a.H, a.x_q, a.x_s, a.x_gsum, nullptr, st);
+    if (e != cudaSuccess) return e;
+  }
+  PdlConfig c(dim3((unsigned)n, 1, 1), kGatherThreads, 0, st);
+  e = cudaLaunchKernelEx(&c.cfg, gather_rows_kernel<kCodes>,
+                         kCodes ? (const void*)a.x_q : (const void*)a.x, (const float*)a.x_s,
+                         (const int32_t*)a.plan.order, (const int*)a.plan.head, a.k, a.H, a.rows,
+                         a.rows_s);
+  if (e != cudaSuccess) return e;
+  RaggedArgs r{};
+  r.variant = VARIANT;
+  r.gate_up = true;
+  r.rows_max = n;
+  r.N = 2 * a.I;
+  r.K = a.H;
+  r.E = a.E;
+  r.act = a.rows;
+  r.a_s = a.rows_s;
+  r.packed = a.gate_up;
+  r.y = a.h;
+  r.plan = a.plan;
+  r.timeout_ns = a.timeout_ns;
+  if ((e = launch_ragged(r, st)) != cudaSuccess) return e;
+  if (kCodes) {
+    // (rows past the last one that has an expert are quantized too: nothing
+    // reads them)
+    e = launch_quant_act(a.h, experts_rows(n), a.I, nullptr, a.h_s, a.h_gsum, a.h_tc, st);
+    if (e != cudaSuccess) return e;
+  }
+  r.gate_up = false;
+  r.N = a.H;
+  r.K = a.I;
+  r.act = kCodes ? a.h_tc : (const void*)a.h;
+  r.a_s = a.h_s;
+  r.packed = a.down;
+  r.y = a.y;
+  if ((e = launch_ragged(r, st)) != cudaSuccess) return e;
+  return launch_combine(a, st);
+}
+
 template <int VARIANT>
 static cudaError_t run_experts(const ExpertsArgs& a, cudaStream_t st) {
+  if (a.tensor) return run_experts_tensor<VARIANT>(a, st);
   constexpr bool kCodes = VARIANT == kW4A8;
   const int64_t n = a.T * a.k;
   // rows of a tile: a token picks an expert once as a rule, so hardly an expert
@@ -312,10 +398,7 @@ static cudaError_t run_experts(const ExpertsArgs& a, cudaStream_t st) {
   p.N = (int)a.H;
   p.G = (int)(a.I / 128);
   if ((e = launch_stream<VARIANT, false>(p, tiles, bt, st)) != cudaSuccess) return e;
-  PdlConfig c(dim3((unsigned)a.T, (unsigned)((a.H / 8 + kCombineThreads - 1) / kCombineThreads), 1),
-              kCombineThreads, 0, st);
-  return cudaLaunchKernelEx(&c.cfg, combine_kernel, (const uint16_t*)a.y, a.weights,
-                            (const int32_t*)a.plan.pos, a.k, a.H, a.out);
+  return launch_combine(a, st);
 }
 
 cudaError_t launch_experts(const ExpertsArgs& a, cudaStream_t st) {

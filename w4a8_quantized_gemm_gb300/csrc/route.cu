@@ -284,6 +284,7 @@ plan_kernel(const int32_t* __restrict__ ids, int n, int S, int bt, RowPlan plan)
   // tiles of at most bt rows: set s takes the entries from base / bt + rank up
   // to the next set's first, (base + count) / bt + rank + 1: as many as it
   // needs, or one more, which is then empty
+  if (tid == 0) plan.offset[set] = base;
   if (set < S) {
     if (count > 0) {
       const int t0 = base / bt + rank, t1 = (base + count) / bt + rank + 1;

@@ -26,8 +26,9 @@ struct Carver {
   }
 };
 
-void carve_plan(Carver& c, RowPlan& plan, int64_t n, int64_t tiles, bool pos) {
+void carve_plan(Carver& c, RowPlan& plan, int64_t n, int S, int64_t tiles, bool pos) {
   plan.head = c.take<int>(2);
+  plan.offset = c.take<int32_t>(S + 1);
   plan.order = c.take<int32_t>(n);
   plan.pos = pos ? c.take<int32_t>(n) : nullptr;
   plan.tiles = c.take<int4>(tiles);
@@ -36,23 +37,30 @@ void carve_plan(Carver& c, RowPlan& plan, int64_t n, int64_t tiles, bool pos) {
 size_t carve_experts(void* ws, ExpertsArgs& a) {
   Carver c(ws);
   const int64_t n = a.T * a.k;
-  carve_plan(c, a.plan, n, plan_max_tiles(n, a.E, 8), true);
+  carve_plan(c, a.plan, n, a.E, plan_max_tiles(n, a.E, 8), true);
+  // (the tensor-core products read fp16 codes, a form the quantizer writes for
+  // more than kTcFp8MaxM rows)
+  const int64_t rows = a.tensor ? experts_rows(n) : n;
   if (a.variant == kW4A8) {
     a.x_q = c.take<int8_t>(a.T * a.H);
     a.x_s = c.take<float>(a.T);
     a.x_gsum = c.take<int32_t>(a.T * (a.H / 128));
-    a.h_q = c.take<int8_t>(n * a.I);
-    a.h_s = c.take<float>(n);
-    a.h_gsum = c.take<int32_t>(n * (a.I / 128));
+    a.h_q = c.take<int8_t>(a.tensor ? 0 : n * a.I);
+    a.h_s = c.take<float>(rows);
+    a.h_gsum = c.take<int32_t>(rows * (a.I / 128));
+    a.h_tc = c.take<uint16_t>(a.tensor ? rows * a.I : 0);
+    a.rows_s = c.take<float>(a.tensor ? n : 0);
   }
-  a.h = c.take<uint16_t>(n * a.I);
+  a.h = c.take<uint16_t>(rows * a.I);
+  // the sorted activations are dead once the gate and up products have run
   a.y = c.take<uint16_t>(n * a.H);
+  a.rows = a.y;
   return c.used;
 }
 
 size_t carve_lora(void* ws, LoraArgs& a) {
   Carver c(ws);
-  carve_plan(c, a.plan, a.M, plan_max_tiles(a.M, a.L, lora_tile(a.M)), false);
+  carve_plan(c, a.plan, a.M, a.L, plan_max_tiles(a.M, a.L, lora_tile(a.M)), false);
   a.h = c.take<float>((int64_t)lora_splits(a.M, a.K) * a.M * a.r);
   return c.used;
 }
@@ -176,8 +184,15 @@ size_t egopq_moe_experts_workspace_bytes(int64_t T, int k, int E, int64_t H, int
   a.E = E;
   a.H = H;
   a.I = I;
-  (void)path;
-  return carve_experts(nullptr, a);
+  // enough for every smaller batch too, whichever products AUTO takes there
+  size_t most = 0;
+  for (int tensor = 0; tensor < 2; ++tensor) {
+    if ((path == EGOPQ_PATH_GEMV && tensor) || (path == EGOPQ_PATH_TC && !tensor)) continue;
+    a.tensor = tensor != 0;
+    const size_t need = carve_experts(nullptr, a);
+    if (need > most) most = need;
+  }
+  return most;
 }
 
 int egopq_moe_experts(const uint16_t* x_bf16, const int32_t* ids, const float* weights,
@@ -200,7 +215,7 @@ int egopq_moe_experts(const uint16_t* x_bf16, const int32_t* ids, const float* w
   a.I = I;
   a.E = E;
   a.k = k;
-  a.tensor = false;
+  a.tensor = path == EGOPQ_PATH_TC || (path == EGOPQ_PATH_AUTO && experts_on_tensor_cores(T * k, E));
   a.x = x_bf16;
   a.ids = ids;
   a.weights = weights;
@@ -213,6 +228,8 @@ int egopq_moe_experts(const uint16_t* x_bf16, const int32_t* ids, const float* w
     return fail(EGOPQ_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
   if ((rc = check_arch())) return rc;
   cudaError_t e = launch_experts(a, (cudaStream_t)stream);
+  if (e == cudaErrorNotSupported)
+    return fail(EGOPQ_ERR_UNSUPPORTED_SHAPE, "too many rows for the requested path");
   return e == cudaSuccess ? EGOPQ_OK : cuda_fail(e, "moe_experts launch");
 }
 
