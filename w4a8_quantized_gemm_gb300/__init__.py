@@ -50,6 +50,8 @@ def build(force: bool = False) -> str:
 def load() -> ctypes.CDLL:
     """Load libegopq.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -130,8 +132,9 @@ def _check(rc: int):
 
 
 def _stream(stream: Optional[torch.cuda.Stream] = None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is None:  # (the raw handle: a Stream object a call costs microseconds)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -145,7 +148,7 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _dtype(t: torch.Tensor, *dtypes):
-    if t.dtype not in dtypes:
+    if t.dtype not in dtypes:  # (dtypes are compared by identity)
         raise TypeError(f"expected dtype in {dtypes}, got {t.dtype}")
 
 
@@ -444,7 +447,7 @@ GROUP_MAX, GROUP_TOP2 = 0, 1
 
 
 def _shape(t: torch.Tensor, *shape):
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"tensor of shape {tuple(t.shape)}, expected {shape}")
 
 

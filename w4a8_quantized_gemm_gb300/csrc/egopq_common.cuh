@@ -394,6 +394,29 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
   return r;
 }
+// Reciprocal of the row scale s for quant_code's product form, or NaN where
+// that form is not used (s zero, below 2^-100, above 2^126 or not finite): a
+// NaN product sends every element of the row to the IEEE quotient.
+__device__ __forceinline__ float quant_recip(float s) {
+  return (s >= 0x1p-100f && s <= 0x1p+126f) ? __frcp_rn(s) : __int_as_float(0x7fc00000);
+}
+
+// clamp(round_half_even(fp32 quotient x / s), -127, 127) as an fp32 integer,
+// equal to __float2int_rn(__fdiv_rn(x, s)) clamped. With inv the correctly
+// rounded 1/s, r = fl(x * inv) is within |x / s| * 2^-23 of the exact quotient
+// q (two roundings of at most 2^-24 relative), and fl(q) within |q| * 2^-24 of
+// q; as |q| <= 127 * (1 + 2^-23), r and fl(q) lie within 2.3e-5 of each other.
+// So they round to the same integer unless r lies within that distance of a
+// half-integer; where r lies within 1e-4 of one (|r - rint(r)| >= 0.4999, or r
+// NaN) the IEEE quotient decides. On the product's side |r| < 127.5, so its
+// integer needs no clamp.
+__device__ __forceinline__ float quant_code(float x, float s, float inv) {
+  const float r = x * inv;
+  const float rf = rintf(r);
+  if (fabsf(r - rf) < 0.4999f) return rf;
+  return (float)max(-127, min(127, __float2int_rn(__fdiv_rn(x, s))));
+}
+
 // silu(g) * u (fast exponential and quotient: a few 2^-22, far below the bf16
 // rounding that follows)
 __device__ __forceinline__ float gated(float g, float u) {

@@ -230,7 +230,8 @@ constexpr int kMaxSets = 1024;  // weight sets (experts, adapters) of one call
 //   offset [S + 1] first sorted position of each set (set s has the slots
 //          [offset[s], offset[s + 1]) of order)
 //   tiles  {set, first sorted position, rows} of each tile of at most bt rows
-//          of one set; some entries are empty (rows = 0)
+//          of one set; some entries are empty (rows = 0). Not written with
+//          bt = 0.
 struct RowPlan {
   int* head;
   int32_t* order;
@@ -254,12 +255,18 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t st);
 cudaError_t launch_plan(const int32_t* ids, int64_t n, int S, int bt, const RowPlan& plan,
                         cudaStream_t st);
 
+// How a call's products run (experts.cu).
+enum ExpertsWay { kExpertsFew, kExpertsStream, kExpertsTensor };
+// (AUTO: the tcgen05 products from more than kStreamRows picks an expert)
+constexpr int64_t kStreamRows = 48;
+ExpertsWay experts_way(int64_t T, int k, int E, int path);
+
 // Experts: one call's operands and workspace parts, validated by the ABI layer.
 struct ExpertsArgs {
   int variant;  // kW4A8 or kW4A16
   int64_t T, H, I;
   int E, k;
-  bool tensor;  // the tcgen05 products; else the streaming ones
+  ExpertsWay way;
   const uint16_t* x;
   const int32_t* ids;
   const float* weights;
@@ -267,26 +274,17 @@ struct ExpertsArgs {
   const uint8_t* down;
   uint16_t* out;
   RowPlan plan;
-  // W4A8: codes of x [T][H] and of h [T*k][I], their scales and group sums
-  int8_t* x_q;
+  int8_t* x_q;     // codes of x [T][H] and their scales (W4A8, few and stream)
   float* x_s;
-  int32_t* x_gsum;
-  int8_t* h_q;
+  uint16_t* rows;  // activations in sorted order [T*k][H], bf16 or fp16 codes (tensor)
+  float* rows_s;   // their scales (W4A8, tensor)
+  uint16_t* h;     // bf16 [T*k][I]
+  void* h_q;       // its codes, int8 or fp16 (tensor), and their scales (W4A8)
   float* h_s;
-  int32_t* h_gsum;
-  void* h_tc;          // fp16 codes of h [T*k][I] (W4A8, tensor)
-  uint16_t* rows;      // activations in sorted order [T*k][H] (tensor)
-  float* rows_s;       // their scales (W4A8, tensor)
-  uint16_t* h;         // bf16 [T*k][I]
-  uint16_t* y;         // bf16 [T*k][H]
+  void* y;         // [T*k][H], fp32 (stream) or bf16 (tensor)
   uint64_t timeout_ns;
 };
 cudaError_t launch_experts(const ExpertsArgs& a, cudaStream_t st);
-// Rows the tensor-core products' buffers hold (at least one more than
-// kTcFp8MaxM, so that the quantizer writes fp16 codes).
-inline int64_t experts_rows(int64_t n) { return n > 64 ? n : 65; }
-// AUTO's choice for n picks over E experts.
-inline bool experts_on_tensor_cores(int64_t n, int E) { return n > (int64_t)48 * E; }
 // One tcgen05 product over sorted rows: kGateUp (h = silu(g) * u) or the down
 // projection.
 struct RaggedArgs {
@@ -318,9 +316,11 @@ struct LoraArgs {
   RowPlan plan;
   float* h;  // [lora_splits][M][r] partial sums of A x, sorted rows
 };
-// Rows of one tile of the adapters' products, and the CTAs K is split over.
-int lora_tile(int64_t M);
-int lora_splits(int64_t M, int64_t K);
+// Whether M rows take the one-launch form (no plan, no workspace); else the rows
+// of a tile and the parts K is split into.
+bool lora_few(int64_t M);
+int lora_tile();
+int lora_splits(int64_t M, int64_t K, int L);
 cudaError_t launch_lora(const LoraArgs& a, cudaStream_t st);
 
 // Weights [E][2I][K] with I gate rows and then I up rows a set, packed with

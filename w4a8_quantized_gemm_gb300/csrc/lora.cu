@@ -4,15 +4,18 @@
 //   y[m] = bf16( y0[m] + scale_a * B_a (A_a x[m]) ),  a = ids[m]
 //
 // A [L][r][K], B [L][N][r] bf16; adapter a uses its first ranks[a] rows of A
-// (columns of B). A row with ids outside [0, L) keeps y0. Rows are sorted by
-// adapter (RowPlan), so that the rows of one adapter share its weights.
+// (columns of B). A row with ids outside [0, L) keeps y0.
 //
-// Two kernels: A x into fp32 sums [splits][M][r] (K split over warps and, for
-// few rows, over CTAs: the sums of the parts are added in order by the second
-// kernel, so the result does not depend on timing), then the product with B
-// and the addition to y0. Both run on mma.m16n8k16 with fragments loaded
-// straight from memory: the order of K inside a fragment is free as long as
-// both operands share it, so each thread reads 16 contiguous bytes of its row.
+// Up to 128 rows (decode) take one launch: a cluster of CTAs an adapter (and
+// slab of columns) finds its rows in the ids alone, splits K for A x, adds the
+// parts through distributed shared memory and splits the columns for the
+// product with B. More rows are sorted by adapter (RowPlan) and take two
+// kernels with A x in memory between them. Every sum is added in a fixed
+// order, so results do not depend on timing.
+//
+// All products run on mma.m16n8k16 with fragments loaded straight from memory:
+// the order of K inside a fragment is free as long as both operands share it,
+// so each thread reads 16 (A, x) or 8 (B) contiguous bytes of its row.
 #include "egopq_internal.h"
 
 namespace egopq {
@@ -27,8 +30,12 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
 }
 
 constexpr int kLoraWarps = 8;
-constexpr int kLoraTile = 16;      // rows of a tile
+constexpr int kLoraThreads = 32 * kLoraWarps;
+constexpr int kLoraTile = 64;     // rows of a tile of the two kernels
 constexpr int kLoraMaxRank = 128;
+constexpr int kLoraFewRows = 128;  // rows of a one-launch batch
+constexpr int kLoraCluster = 8;
+constexpr int kHsLd = kLoraMaxRank + 8;  // padded row of the bf16 A x in shared memory
 
 struct LoraParams {
   const uint16_t* y_in;
@@ -37,13 +44,14 @@ struct LoraParams {
   const uint16_t* B;
   const float* scale;
   const int32_t* ranks;
+  const int32_t* ids;
   uint16_t* y_out;
-  float* h;
+  float* h;  // [splits][M][r]
   const int* head;
   const int4* tiles;
   const int32_t* order;
   int64_t M, N, K;
-  int r, splits;
+  int L, r, splits;
 };
 
 // ranks[a] as a number in [0, r]
@@ -51,13 +59,257 @@ __device__ __forceinline__ int adapter_rank(const LoraParams& p, int a) {
   return p.ranks ? max(0, min(p.r, __ldg(p.ranks + a))) : p.r;
 }
 
-// h[split][sorted row][0, rank) = the split's part of A_a x. One CTA a tile of
-// 16 rows and a part of K, whose warps take 32-wide steps of it in turn; NR
-// n8-tiles of ranks at a time.
+// acc[mt][t] += x rows (two a thread and row tile: xr[2 mt], xr[2 mt + 1], null
+// where there is none) times ranks [c0, c0 + 8 NR) of A over the 32-wide K
+// steps s0, s0 + step, ... below s1. Pointers include the thread's 8 * tig.
+template <int MT, int NR>
+__device__ __forceinline__ void shrink_steps(float (&acc)[MT][NR][4], const uint16_t* const* xr,
+                                             const uint16_t* Ab, int64_t K, int c0, int rank,
+                                             int s0, int s1, int step) {
+  const int gid = (threadIdx.x & 31) >> 2;
+#pragma unroll 2
+  for (int s = s0; s < s1; s += step) {
+    uint4 a[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        a[mt][q] = xr[2 * mt + q]
+                       ? __ldg(reinterpret_cast<const uint4*>(xr[2 * mt + q] + (int64_t)s * 32))
+                       : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int t = 0; t < NR; ++t) {
+      const int j = c0 + t * 8 + gid;
+      uint4 b = {};
+      if (j < rank) b = __ldg(reinterpret_cast<const uint4*>(Ab + (int64_t)j * K + s * 32));
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        mma_bf16(acc[mt][t], a[mt][0].x, a[mt][1].x, a[mt][0].y, a[mt][1].y, b.x, b.y);
+        mma_bf16(acc[mt][t], a[mt][0].z, a[mt][1].z, a[mt][0].w, a[mt][1].w, b.z, b.w);
+      }
+    }
+  }
+}
+
+// acc[mt][t] += rows of hs (16 mt + ...) times columns n0 .. n0 + 32 of B
+// (Bb: row n0 of the adapter's B). Column c of n8-tile t is column
+// (c / 2) * 8 + 2t + c % 2 of the 32, so that a thread's sums over the four
+// tiles are eight neighbouring columns of y: one 16-byte access a row.
+template <int MT>
+__device__ __forceinline__ void expand_steps(float (&acc)[MT][4][4], const uint16_t (*hs)[kHsLd],
+                                             int mts, const uint16_t* Bb, int r, int rank) {
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  for (int j0 = 0; j0 < rank; j0 += 16) {
+    // 16 ranks: thread column tig holds ranks 4 tig .. 4 tig + 3 of them
+    const int j = j0 + 4 * tig;
+    uint2 b[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int col = (gid >> 1) * 8 + 2 * t + (gid & 1);
+      b[t] = j < r ? __ldg(reinterpret_cast<const uint2*>(Bb + (int64_t)col * r + j))
+                   : make_uint2(0u, 0u);
+      // columns of B past the adapter's rank meet zeros of h, but may hold
+      // anything: leave them out
+      if (j + 3 >= rank) {
+        if (j >= rank) b[t] = make_uint2(0u, 0u);
+        else if (j + 1 >= rank) b[t] = make_uint2(b[t].x & 0xFFFFu, 0u);
+        else if (j + 2 >= rank) b[t].y = 0u;
+        else b[t].y &= 0xFFFFu;
+      }
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      if (mt >= mts) break;
+      const uint2 a0 = *reinterpret_cast<const uint2*>(&hs[mt * 16 + gid][j]);
+      const uint2 a1 = *reinterpret_cast<const uint2*>(&hs[mt * 16 + gid + 8][j]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) mma_bf16(acc[mt][t], a0.x, a1.x, a0.y, a1.y, b[t].x, b[t].y);
+    }
+  }
+}
+
+// Eight neighbouring columns of y plus their updates, rounded.
+__device__ __forceinline__ uint4 add_row(const uint4& v, const float (&acc)[4][4], int half) {
+  const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+    o[t] = (uint32_t)f32_to_bf16_bits(__uint_as_float(q[t] << 16) + acc[t][2 * half]) |
+           ((uint32_t)f32_to_bf16_bits(__uint_as_float(q[t] & 0xFFFF0000u) + acc[t][2 * half + 1])
+            << 16);
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <int MT, int NT>
+__device__ __forceinline__ void zero_acc(float (&acc)[MT][NT][4]) {
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[m][t][q] = 0.f;
+}
+
+// ---- few rows: one launch ------------------------------------------------------------
+// Cluster (slab, adapter b): 8 CTAs. CTA c sums A x over its eighth of K for
+// up to 16 rows of the b-th adapter in the batch, takes the other parts through
+// distributed shared memory in rank order, scales and rounds h once (bf16, the
+// operand of the product: relative 2^-8 of the update at most, below the
+// rounding of y itself where the update is no larger than y) and updates its
+// columns. The slab's part of B is asked into L2 before A x is summed, so that
+// its trip from HBM runs beside it. Latency-bound: one row of 3584 x 3584 at
+// rank 16 reads 0.25 MB.
 template <int NR>
-__global__ void __launch_bounds__(32 * kLoraWarps)
-lora_shrink_kernel(const LoraParams p) {
+__global__ void __launch_bounds__(kLoraThreads)
+lora_few_kernel(const LoraParams p) {
+  __shared__ uint32_t seen[kMaxSets / 32];
+  __shared__ int rows_of[kLoraFewRows];
+  __shared__ int n_rows_s;
   __shared__ float red[kLoraWarps][16][8 * NR + 1];
+  __shared__ float part[16][kLoraMaxRank];
+  __shared__ __align__(16) uint16_t hs[16][kHsLd];
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  const int M = (int)p.M, words = (p.L + 31) / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gid = lane >> 2, tig = lane & 3;
+  for (int i = threadIdx.x; i < words; i += kLoraThreads) seen[i] = 0;
+  __syncthreads();
+  if ((int)threadIdx.x < M) {
+    const int v = __ldg(p.ids + threadIdx.x);
+    if (v >= 0 && v < p.L) atomicOr(&seen[v >> 5], 1u << (v & 31));
+  }
+  __syncthreads();
+  // the b-th adapter of the batch (its bit, counted from below); one past the
+  // last: the rows without an adapter
+  int b = blockIdx.y, w = 0;
+  while (w < words && b >= __popc(seen[w])) b -= __popc(seen[w++]);
+  const bool none = w == words;
+  if (none && (b > 0 || p.y_in == p.y_out)) return;  // (the whole cluster)
+  int set = -1;
+  if (!none) {
+    uint32_t m = seen[w];
+    for (; b > 0; --b) m &= m - 1;
+    set = w * 32 + __ffs(m) - 1;
+  }
+  // its rows, in order
+  if (warp == 0) {
+    int n = 0;
+    for (int i0 = 0; i0 < M; i0 += 32) {
+      const int i = i0 + lane;
+      int v = i < M ? __ldg(p.ids + i) : -2;
+      if (i < M && (v < 0 || v >= p.L)) v = -1;
+      const uint32_t hit = __ballot_sync(0xffffffffu, i < M && v == set);
+      if ((hit >> lane) & 1) rows_of[n + __popc(hit & ((1u << lane) - 1))] = i;
+      n += __popc(hit);
+    }
+    if (lane == 0) n_rows_s = n;
+  }
+  __syncthreads();
+  const int n_rows = n_rows_s;
+  const int rank_c = (int)cluster_ctarank();
+  const int slab = blockIdx.x / kLoraCluster, slabs = gridDim.x / kLoraCluster;
+  // this CTA's columns, 32 at a time
+  const int64_t chunks = p.N / 32, parts = (int64_t)slabs * kLoraCluster;
+  const int64_t me = (int64_t)slab * kLoraCluster + rank_c;
+  const int64_t c_lo = me * chunks / parts, c_hi = (me + 1) * chunks / parts;
+  if (none) {
+    for (int i = 0; i < n_rows; ++i) {
+      const int64_t at = (int64_t)rows_of[i] * p.N;
+      for (int64_t v = c_lo * 4 + threadIdx.x; v < c_hi * 4; v += kLoraThreads)
+        reinterpret_cast<uint4*>(p.y_out + at)[v] =
+            *(reinterpret_cast<const uint4*>(p.y_in + at) + v);
+    }
+    return;
+  }
+  const int rank = adapter_rank(p, set);
+  const float sc = __ldg(p.scale + set);
+  const uint16_t* Bset = p.B + (int64_t)set * p.N * p.r;
+  {
+    const uint8_t* from = reinterpret_cast<const uint8_t*>(Bset + c_lo * 32 * p.r);
+    const int64_t bytes = (c_hi - c_lo) * 64 * p.r;
+    for (int64_t i = (int64_t)threadIdx.x * 128; i < bytes; i += (int64_t)kLoraThreads * 128)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i));
+  }
+  const int steps = (int)(p.K / 32);
+  const int s0 = rank_c * steps / kLoraCluster, s1 = (rank_c + 1) * steps / kLoraCluster;
+  const uint16_t* Ab = p.A + (int64_t)set * p.r * p.K + 8 * tig;
+  for (int t0 = 0; t0 < n_rows; t0 += 16) {
+    const int rows = min(16, n_rows - t0);
+    const uint16_t* xr[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      xr[q] = gid + 8 * q < rows ? p.x + (int64_t)rows_of[t0 + gid + 8 * q] * p.K + 8 * tig
+                                 : nullptr;
+    for (int c0 = 0; c0 < rank; c0 += 8 * NR) {
+      float acc[1][NR][4];
+      zero_acc<1, NR>(acc);
+      shrink_steps<1, NR>(acc, xr, Ab, p.K, c0, rank, s0 + warp, s1, kLoraWarps);
+#pragma unroll
+      for (int t = 0; t < NR; ++t)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          red[warp][(q >> 1) * 8 + gid][t * 8 + tig * 2 + (q & 1)] = acc[0][t][q];
+      __syncthreads();
+      for (int i = threadIdx.x; i < rows * 8 * NR; i += kLoraThreads) {
+        const int j = i % (8 * NR), row = i / (8 * NR);
+        if (c0 + j < rank) {
+          float v = 0.f;
+#pragma unroll
+          for (int k = 0; k < kLoraWarps; ++k) v += red[k][row][j];
+          part[row][c0 + j] = v;
+        }
+      }
+      __syncthreads();
+    }
+    cluster_sync_all();  // every CTA's part is in its shared memory
+    const int kr = (rank + 15) & ~15;
+    const uint32_t local = smem_u32(part);
+    for (int i = threadIdx.x; i < 16 * kr; i += kLoraThreads) {
+      const int row = i / kr, j = i - row * kr;
+      float v = 0.f;
+      if (row < rows && j < rank) {
+        const uint32_t at = local + (uint32_t)(row * kLoraMaxRank + j) * 4;
+        float q[kLoraCluster];
+#pragma unroll
+        for (int c = 0; c < kLoraCluster; ++c) q[c] = ld_dsmem_f32(map_to_rank(at, c));
+#pragma unroll
+        for (int c = 0; c < kLoraCluster; ++c) v += q[c];
+      }
+      hs[row][j] = f32_to_bf16_bits(sc * v);
+    }
+    cluster_sync_all();  // (also the block's barrier) parts may be rewritten, CTAs may leave
+    for (int64_t c = c_lo + warp; c < c_hi; c += kLoraWarps) {
+      const int64_t n0 = c * 32;
+      uint4 y[2];
+      int64_t at[2];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int row = gid + 8 * half;
+        at[half] = row < rows ? (int64_t)rows_of[t0 + row] * p.N + n0 + 8 * tig : -1;
+        if (at[half] >= 0) y[half] = *reinterpret_cast<const uint4*>(p.y_in + at[half]);
+      }
+      float acc[1][4][4];
+      zero_acc<1, 4>(acc);
+      expand_steps<1>(acc, hs, 1, Bset + n0 * p.r, p.r, rank);
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+        if (at[half] >= 0)
+          *reinterpret_cast<uint4*>(p.y_out + at[half]) = add_row(y[half], acc[0], half);
+    }
+    __syncthreads();  // hs is rewritten for the next rows
+  }
+}
+
+// ---- many rows: two kernels -----------------------------------------------------------
+// h[split][sorted row][0, rank) = the split's part of A_a x. One CTA a tile of
+// 64 rows and a part of K: warps (row half, K quarter), each 32 rows; the K
+// quarters add their sums to shared memory in turn. Reads x once; A_a comes
+// from L2 (a tile of 64 rows reads it once for its two row halves).
+template <int NR>
+__global__ void __launch_bounds__(kLoraThreads)
+lora_shrink_kernel(const LoraParams p) {
+  __shared__ float red[kLoraTile][8 * NR + 1];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   if ((int)blockIdx.x >= p.head[1]) return;
@@ -66,65 +318,54 @@ lora_shrink_kernel(const LoraParams p) {
   const int rank = adapter_rank(p, tile.x);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
-  // K in steps of 32: this CTA's are [s0, s1)
+  const int half = warp & 1, kw = warp >> 1;
+  constexpr int kParts = kLoraWarps / 2;
   const int steps = (int)(p.K / 32);
   const int s0 = (int)((int64_t)blockIdx.y * steps / p.splits);
   const int s1 = (int)((int64_t)(blockIdx.y + 1) * steps / p.splits);
-  const bool live0 = gid < tile.z, live1 = gid + 8 < tile.z;
-  const uint16_t* x0 = p.x + (live0 ? (int64_t)__ldg(p.order + tile.y + gid) * p.K : 0) + 8 * tig;
-  const uint16_t* x1 =
-      p.x + (live1 ? (int64_t)__ldg(p.order + tile.y + gid + 8) * p.K : 0) + 8 * tig;
+  const uint16_t* xr[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int row = half * 32 + (q >> 1) * 16 + (q & 1) * 8 + gid;
+    xr[q] = row < tile.z ? p.x + (int64_t)__ldg(p.order + tile.y + row) * p.K + 8 * tig : nullptr;
+  }
+  const bool work = half * 32 < tile.z;
   const uint16_t* Ab = p.A + (int64_t)tile.x * p.r * p.K + 8 * tig;
   for (int c0 = 0; c0 < rank; c0 += 8 * NR) {
-    float acc[NR][4];
+    float acc[2][NR][4];
+    zero_acc<2, NR>(acc);
+    if (work) shrink_steps<2, NR>(acc, xr, Ab, p.K, c0, rank, s0 + kw, s1, kParts);
+    for (int k = 0; k < kParts; ++k) {
+      if (kw == k && work) {
 #pragma unroll
-    for (int t = 0; t < NR; ++t)
+        for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) acc[t][q] = 0.f;
-#pragma unroll 2
-    for (int s = s0 + warp; s < s1; s += kLoraWarps) {
-      uint4 a0 = {}, a1 = {};
-      if (live0) a0 = __ldg(reinterpret_cast<const uint4*>(x0 + s * 32));
-      if (live1) a1 = __ldg(reinterpret_cast<const uint4*>(x1 + s * 32));
+          for (int t = 0; t < NR; ++t)
 #pragma unroll
-      for (int t = 0; t < NR; ++t) {
-        const int j = c0 + t * 8 + gid;
-        uint4 b = {};
-        if (j < rank) b = __ldg(reinterpret_cast<const uint4*>(Ab + (int64_t)j * p.K + s * 32));
-        mma_bf16(acc[t], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
-        mma_bf16(acc[t], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
+            for (int q = 0; q < 4; ++q) {
+              float& v =
+                  red[half * 32 + mt * 16 + (q >> 1) * 8 + gid][t * 8 + tig * 2 + (q & 1)];
+              v = k == 0 ? acc[mt][t][q] : v + acc[mt][t][q];
+            }
       }
+      __syncthreads();
     }
-#pragma unroll
-    for (int t = 0; t < NR; ++t)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        red[warp][(q >> 1) * 8 + gid][t * 8 + tig * 2 + (q & 1)] = acc[t][q];
-    __syncthreads();
-    for (int i = threadIdx.x; i < 16 * 8 * NR; i += 32 * kLoraWarps) {
+    for (int i = threadIdx.x; i < tile.z * 8 * NR; i += kLoraThreads) {
       const int j = i % (8 * NR), row = i / (8 * NR);
-      if (row < tile.z && c0 + j < rank) {
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < kLoraWarps; ++w) v += red[w][row][j];
-        p.h[((int64_t)blockIdx.y * p.M + tile.y + row) * p.r + c0 + j] = v;
-      }
+      if (c0 + j < rank)
+        p.h[((int64_t)blockIdx.y * p.M + tile.y + row) * p.r + c0 + j] = red[row][j];
     }
     __syncthreads();
   }
 }
 
-// y = bf16(y0 + scale * B_a h). One CTA a tile of 16 rows and 32 * kLoraWarps
-// columns, 32 a warp. The tile's h -- the splits added in order, scaled in
-// fp32, and rounded to bf16 once, as the product's operand: relative 2^-8 of
-// the update, below the rounding of y itself where the update is no larger
-// than y -- lies in shared memory. Column c of the warp's n8-tile t is column
-// (c / 2) * 8 + 2t + c % 2 of its 32, so that a thread's sums over the four
-// tiles are eight neighbouring columns: one 16-byte load and store a row.
-__global__ void __launch_bounds__(32 * kLoraWarps)
+// y = bf16(y0 + scale * B_a h). One CTA a tile of 64 rows and 256 columns, 32 a
+// warp; the tile's h (the splits added in order, scaled, rounded to bf16 once:
+// see lora_few_kernel) lies in shared memory. Bound by y0 and y: 2 x 29 MB at
+// 4093 x 3584.
+__global__ void __launch_bounds__(kLoraThreads)
 lora_expand_kernel(const LoraParams p) {
-  constexpr int LD = kLoraMaxRank + 8;
-  __shared__ __align__(16) uint16_t hs[16][LD];
+  __shared__ __align__(16) uint16_t hs[kLoraTile][kHsLd];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   const int n_tiles = p.head[1];
@@ -137,9 +378,28 @@ lora_expand_kernel(const LoraParams p) {
     tile = __ldg(p.tiles + blockIdx.x);
     if (tile.z == 0) return;
     rank = adapter_rank(p, tile.x);
+  } else {
+    // tiles past the table copy the rows without an adapter, which the plan
+    // lists last (nothing to do where y is updated in place)
+    const int64_t first = p.head[0] + (int64_t)((int)blockIdx.x - n_tiles) * kLoraTile;
+    if (first >= p.M || p.y_in == p.y_out) return;
+    tile = make_int4(0, (int)first, (int)min((int64_t)kLoraTile, p.M - first), 0);
+  }
+  // y0 is on its way while h is put together
+  uint4 y[8];
+  int64_t at[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = i * 8 + gid;
+    at[i] = row < tile.z && n0 < p.N
+                ? (int64_t)__ldg(p.order + tile.y + row) * p.N + n0 + 8 * tig
+                : -1;
+    if (at[i] >= 0) y[i] = *reinterpret_cast<const uint4*>(p.y_in + at[i]);
+  }
+  if (rank > 0) {
     const float sc = __ldg(p.scale + tile.x);
     const int kr = (rank + 15) & ~15;
-    for (int i = threadIdx.x; i < 16 * kr; i += 32 * kLoraWarps) {
+    for (int i = threadIdx.x; i < kLoraTile * kr; i += kLoraThreads) {
       const int row = i / kr, j = i - row * kr;
       float v = 0.f;
       if (row < tile.z && j < rank)
@@ -147,69 +407,29 @@ lora_expand_kernel(const LoraParams p) {
           v += p.h[((int64_t)s * p.M + tile.y + row) * p.r + j];
       hs[row][j] = f32_to_bf16_bits(sc * v);
     }
-  } else {
-    // tiles past the table copy the rows without an adapter, which the plan
-    // lists last (nothing to do where y is updated in place)
-    const int first = p.head[0] + ((int)blockIdx.x - n_tiles) * 16;
-    tile = make_int4(0, first, min(16, (int)p.M - first), 0);
-    if (tile.z <= 0 || p.y_in == p.y_out) return;
   }
   __syncthreads();
   if (n0 >= p.N) return;
-  float acc[4][4];
+  float acc[4][4][4];
+  zero_acc<4, 4>(acc);
+  expand_steps<4>(acc, hs, (tile.z + 15) / 16, p.B + ((int64_t)tile.x * p.N + n0) * p.r, p.r, rank);
 #pragma unroll
-  for (int t = 0; t < 4; ++t)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) acc[t][q] = 0.f;
-  const uint16_t* Bb = p.B + ((int64_t)tile.x * p.N + n0) * p.r;
-  for (int j0 = 0; j0 < rank; j0 += 16) {
-    // 16 ranks: thread column tig holds ranks 4 tig .. 4 tig + 3 of them
-    const int j = j0 + 4 * tig;
-    const uint2 a0 = *reinterpret_cast<const uint2*>(&hs[gid][j]);
-    const uint2 a1 = *reinterpret_cast<const uint2*>(&hs[gid + 8][j]);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int col = (gid >> 1) * 8 + 2 * t + (gid & 1);
-      uint2 b = {};
-      if (j < p.r) b = __ldg(reinterpret_cast<const uint2*>(Bb + (int64_t)col * p.r + j));
-      // columns of B past the adapter's rank meet zeros of h, but may hold
-      // anything: leave them out
-      if (j + 3 >= rank) {
-        if (j >= rank) b = make_uint2(0u, 0u);
-        else if (j + 1 >= rank) b = make_uint2(b.x & 0xFFFFu, 0u);
-        else if (j + 2 >= rank) b.y = 0u;
-        else b.y &= 0xFFFFu;
-      }
-      mma_bf16(acc[t], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
-    }
-  }
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int row = gid + 8 * half;
-    if (row >= tile.z) continue;
-    const int64_t at = (int64_t)__ldg(p.order + tile.y + row) * p.N + n0 + 8 * tig;
-    const uint4 v = *reinterpret_cast<const uint4*>(p.y_in + at);
-    const uint32_t q[4] = {v.x, v.y, v.z, v.w};
-    uint32_t o[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-      o[t] = (uint32_t)f32_to_bf16_bits(__uint_as_float(q[t] << 16) + acc[t][2 * half]) |
-             ((uint32_t)f32_to_bf16_bits(__uint_as_float(q[t] & 0xFFFF0000u) +
-                                         acc[t][2 * half + 1])
-              << 16);
-    *reinterpret_cast<uint4*>(p.y_out + at) = make_uint4(o[0], o[1], o[2], o[3]);
-  }
+  for (int i = 0; i < 8; ++i)
+    if (at[i] >= 0)
+      *reinterpret_cast<uint4*>(p.y_out + at[i]) = add_row(y[i], acc[i >> 1], i & 1);
 }
 
-int lora_tile(int64_t) { return kLoraTile; }
+bool lora_few(int64_t M) { return M <= kLoraFewRows; }
 
-int lora_splits(int64_t M, int64_t K) {
-  // parts of K so that about a CTA an SM runs, none of fewer steps than warps
-  const int64_t tiles = (M + kLoraTile - 1) / kLoraTile;
-  int64_t s = 128 / (tiles > 0 ? tiles : 1);
+int lora_tile() { return kLoraTile; }
+
+int lora_splits(int64_t M, int64_t K, int L) {
+  // parts of K so that about two CTAs an SM run, each of two steps a warp or more
+  const int64_t tiles = M / kLoraTile + (L < M ? L : M);
+  int64_t s = 304 / (tiles > 0 ? tiles : 1);
   const int64_t most = K / (32 * kLoraWarps);
   if (s > most) s = most;
-  if (s > 8) s = 8;
+  if (s > 4) s = 4;
   return s < 1 ? 1 : (int)s;
 }
 
@@ -221,6 +441,7 @@ cudaError_t launch_lora(const LoraArgs& a, cudaStream_t st) {
   p.B = a.B;
   p.scale = a.scale;
   p.ranks = a.ranks;
+  p.ids = a.ids;
   p.y_out = a.y_out;
   p.h = a.h;
   p.head = a.plan.head;
@@ -229,23 +450,44 @@ cudaError_t launch_lora(const LoraArgs& a, cudaStream_t st) {
   p.M = a.M;
   p.N = a.N;
   p.K = a.K;
+  p.L = a.L;
   p.r = a.r;
-  p.splits = lora_splits(a.M, a.K);
+  p.splits = 1;
+  const int64_t sets = a.L < a.M ? a.L : a.M;
+  if (lora_few(a.M)) {
+    // column slabs: enough clusters for two CTAs an SM, none under 2048 columns
+    // (each slab sums A x again)
+    int64_t slabs = (a.N + 2047) / 2048;
+    const int64_t want = (38 + sets - 1) / sets;
+    if (slabs > want) slabs = want;
+    PdlConfig c(dim3((unsigned)(slabs * kLoraCluster), (unsigned)(sets + 1), 1), kLoraThreads, 0,
+                st);
+    cudaLaunchAttribute attr[2];
+    attr[0] = c.attr[0];
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kLoraCluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    c.cfg.attrs = attr;
+    c.cfg.numAttrs = 2;
+    return a.r <= 16   ? cudaLaunchKernelEx(&c.cfg, lora_few_kernel<2>, p)
+           : a.r <= 32 ? cudaLaunchKernelEx(&c.cfg, lora_few_kernel<4>, p)
+                       : cudaLaunchKernelEx(&c.cfg, lora_few_kernel<8>, p);
+  }
+  p.splits = lora_splits(a.M, a.K, a.L);
   cudaError_t e = launch_plan(a.ids, a.M, a.L, kLoraTile, a.plan, st);
   if (e != cudaSuccess) return e;
   const int64_t tiles = plan_max_tiles(a.M, a.L, kLoraTile);
   {
-    PdlConfig c(dim3((unsigned)tiles, (unsigned)p.splits, 1), 32 * kLoraWarps, 0, st);
-    e = a.r <= 16 ? cudaLaunchKernelEx(&c.cfg, lora_shrink_kernel<2>, p)
+    PdlConfig c(dim3((unsigned)tiles, (unsigned)p.splits, 1), kLoraThreads, 0, st);
+    e = a.r <= 16   ? cudaLaunchKernelEx(&c.cfg, lora_shrink_kernel<2>, p)
         : a.r <= 32 ? cudaLaunchKernelEx(&c.cfg, lora_shrink_kernel<4>, p)
                     : cudaLaunchKernelEx(&c.cfg, lora_shrink_kernel<8>, p);
     if (e != cudaSuccess) return e;
   }
-  // (the rows without an adapter make at most ceil(M / 16) tiles more)
-  const int64_t grid = tiles + (a.M + 15) / 16;
-  PdlConfig c(dim3((unsigned)grid,
-                   (unsigned)((a.N + 32 * kLoraWarps - 1) / (32 * kLoraWarps)), 1),
-              32 * kLoraWarps, 0, st);
+  // (the rows without an adapter make at most ceil(M / 64) tiles more)
+  const int64_t grid = tiles + (a.M + kLoraTile - 1) / kLoraTile;
+  PdlConfig c(dim3((unsigned)grid, (unsigned)((a.N + 255) / 256), 1), kLoraThreads, 0, st);
   return cudaLaunchKernelEx(&c.cfg, lora_expand_kernel, p);
 }
 

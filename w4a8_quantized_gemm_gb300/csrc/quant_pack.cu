@@ -66,29 +66,6 @@ __device__ __forceinline__ void store_tc_operand(void* a_tc, bool fp8, int64_t M
   }
 }
 
-// Reciprocal of the row scale s for quant_code's product form, or NaN where
-// that form is not used (s zero, below 2^-100, above 2^126 or not finite): a
-// NaN product sends every element of the row to the IEEE quotient.
-__device__ __forceinline__ float quant_recip(float s) {
-  return (s >= 0x1p-100f && s <= 0x1p+126f) ? __frcp_rn(s) : __int_as_float(0x7fc00000);
-}
-
-// clamp(round_half_even(fp32 quotient x / s), -127, 127) as an fp32 integer,
-// equal to __float2int_rn(__fdiv_rn(x, s)) clamped. With inv the correctly
-// rounded 1/s, r = fl(x * inv) is within |x / s| * 2^-23 of the exact quotient
-// q (two roundings of at most 2^-24 relative), and fl(q) within |q| * 2^-24 of
-// q; as |q| <= 127 * (1 + 2^-23), r and fl(q) lie within 2.3e-5 of each other.
-// So they round to the same integer unless r lies within that distance of a
-// half-integer; where r lies within 1e-4 of one (|r - rint(r)| >= 0.4999, or r
-// NaN) the IEEE quotient decides. On the product's side |r| < 127.5, so its
-// integer needs no clamp.
-__device__ __forceinline__ float quant_code(float x, float s, float inv) {
-  const float r = x * inv;
-  const float rf = rintf(r);
-  if (fabsf(r - rf) < 0.4999f) return rf;
-  return (float)max(-127, min(127, __float2int_rn(__fdiv_rn(x, s))));
-}
-
 // Quantizes the 8 bf16 values of one 16-byte vector v (K = 8*idx .. 8*idx+7
 // of token m, scale s, inv = quant_recip(s)) and writes their codes: to a_q
 // when given, to the tensor-core operand form when a_tc is given, and, summed

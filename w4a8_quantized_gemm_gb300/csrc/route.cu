@@ -204,14 +204,14 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t st) {
 
 // ---- plan ----------------------------------------------------------------------
 // One CTA a weight set, and one more for the rows that pick none. Each CTA
-// reads all n picks (out of L2, once: in registers up to 32 a thread), so it
-// knows its own first sorted position -- the picks of lower sets -- and the
-// number of non-empty lower sets without hearing from another CTA, and the
-// whole plan is one launch. A thread holds consecutive picks, so a scan over
-// the threads keeps the slots of a set in order.
+// reads all n picks (out of L2), so it knows its own first sorted position --
+// the picks of lower sets -- and the number of non-empty lower sets without
+// hearing from another CTA, and the whole plan is one launch. A thread holds
+// PT consecutive picks in registers, so one scan over the threads keeps the
+// slots of a set in order; more than PT * 1024 picks go in rounds.
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanPerThread = 32;  // picks a thread holds at once
 
+template <int PT>
 __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(const int32_t* __restrict__ ids, int n, int S, int bt, RowPlan plan) {
   griddep_wait();
@@ -221,70 +221,121 @@ plan_kernel(const int32_t* __restrict__ ids, int n, int S, int bt, RowPlan plan)
   const int set = blockIdx.x;  // S: the rows without a set
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nthr = blockDim.x, nwarp = nthr >> 5;
-  for (int i = tid; i < kMaxSets / 32; i += nthr) seen[i] = 0;
-  __syncthreads();
-  const int chunk = nthr * kPlanPerThread;
-  // pass 1 counts picks of this set and of lower ones
-  auto set_of = [&](int i) { const int v = __ldg(ids + i); return (v < 0 || v >= S) ? S : v; };
-  int eq = 0, lt = 0;
-  for (int c0 = 0; c0 < n; c0 += chunk) {
-    const int i0 = c0 + tid;
-#pragma unroll 8
-    for (int j = 0; j < kPlanPerThread; ++j) {
-      const int i = i0 + j * nthr;
-      if (i >= n) break;
-      const int v = set_of(i);
-      eq += v == set;
-      lt += v < set;
-      if (v < S) {
-        const uint32_t bit = 1u << (v & 31);
-        if (!(*(volatile uint32_t*)&seen[v >> 5] & bit)) atomicOr(&seen[v >> 5], bit);
+  if (bt) {
+    for (int i = tid; i < kMaxSets / 32; i += nthr) seen[i] = 0;
+    __syncthreads();
+  }
+  int v[PT];
+  // picks [i0, i0 + PT) as set numbers; past the end: S + 1
+  auto load = [&](int64_t i0) {
+#pragma unroll
+    for (int q = 0; q < PT; q += 4) {
+      int4 u = make_int4(S + 1, S + 1, S + 1, S + 1);
+      const int64_t i = i0 + q;
+      if (i + 3 < n) {
+        u = __ldg(reinterpret_cast<const int4*>(ids + i));
+      } else if (i < n) {
+        u.x = __ldg(ids + i);
+        if (i + 1 < n) u.y = __ldg(ids + i + 1);
+        if (i + 2 < n) u.z = __ldg(ids + i + 2);
+      }
+      v[q] = u.x;
+      v[q + 1] = u.y;
+      v[q + 2] = u.z;
+      v[q + 3] = u.w;
+    }
+#pragma unroll
+    for (int q = 0; q < PT; ++q) {
+      if (i0 + q >= n) v[q] = S + 1;
+      else if (v[q] < 0 || v[q] >= S) v[q] = S;
+    }
+  };
+  const int64_t round = (int64_t)nthr * PT;
+  int eq = 0, lt = 0, mine = 0;
+  for (int64_t c0 = 0; c0 < n; c0 += round) {
+    load(c0 + (int64_t)tid * PT);
+    mine = 0;
+    int last = -1;
+#pragma unroll
+    for (int q = 0; q < PT; ++q) {
+      mine += v[q] == set;
+      lt += v[q] < set;
+      if (bt && v[q] < S && v[q] != last) {
+        last = v[q];
+        const uint32_t bit = 1u << (last & 31);
+        if (!(*(volatile uint32_t*)&seen[last >> 5] & bit)) atomicOr(&seen[last >> 5], bit);
       }
     }
+    eq += mine;
   }
-  eq = __reduce_add_sync(0xffffffffu, eq);
+  const int all_eq = __reduce_add_sync(0xffffffffu, eq);
   lt = __reduce_add_sync(0xffffffffu, lt);
   if (lane == 0) {
-    warp_eq[warp] = eq;
+    warp_eq[warp] = all_eq;
     warp_lt[warp] = lt;
   }
   __syncthreads();
-  int count = 0, base = 0;
-  for (int w = 0; w < nwarp; ++w) {
-    count += warp_eq[w];
-    base += warp_lt[w];
+  // totals, and (one round) the slots of the warps before this one
+  int count = warp_eq[lane < nwarp ? lane : 0], base = warp_lt[lane < nwarp ? lane : 0];
+  if (lane >= nwarp) count = base = 0;
+  int before = lane < warp ? count : 0;
+  count = __reduce_add_sync(0xffffffffu, count);
+  base = __reduce_add_sync(0xffffffffu, base);
+  before = __reduce_add_sync(0xffffffffu, before);
+  // the slots in order: the thread's come after those of the threads before it
+  auto write = [&](int64_t i0, int at) {
+#pragma unroll
+    for (int q = 0; q < PT; ++q) {
+      if (v[q] == set) {
+        plan.order[at] = (int)(i0 + q);
+        if (plan.pos) plan.pos[i0 + q] = set < S ? at : -1;
+        ++at;
+      }
+    }
+  };
+  auto lanes_before = [&](int m) {
+    int incl = m;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    return incl - m;
+  };
+  if (n <= round) {
+    if (all_eq) write((int64_t)tid * PT, base + before + lanes_before(mine));
+  } else {
+    int done = 0;
+    for (int64_t c0 = 0; c0 < n && done < count; c0 += round) {
+      load(c0 + (int64_t)tid * PT);
+      mine = 0;
+#pragma unroll
+      for (int q = 0; q < PT; ++q) mine += v[q] == set;
+      const int in_warp = __reduce_add_sync(0xffffffffu, mine);
+      __syncthreads();
+      if (lane == 0) warp_eq[warp] = in_warp;
+      __syncthreads();
+      int sum = lane < nwarp ? warp_eq[lane] : 0;
+      const int below = __reduce_add_sync(0xffffffffu, lane < warp ? sum : 0);
+      sum = __reduce_add_sync(0xffffffffu, sum);
+      if (in_warp) write(c0 + (int64_t)tid * PT, base + done + below + lanes_before(mine));
+      done += sum;
+    }
   }
-  int rank = 0;  // non-empty sets below this one
+  if (tid == 0) {
+    plan.offset[set] = base;
+    if (set == S) plan.head[0] = base;  // rows that have a set
+  }
+  if (!bt) return;
+  // tiles of at most bt rows: set s takes the entries from base / bt + rank up
+  // to the next set's first, (base + count) / bt + rank + 1: as many as it
+  // needs, or one more, which is then empty (rank: non-empty sets below)
+  int rank = 0;
   for (int w = 0; w < (set + 31) / 32; ++w) {
     uint32_t m = seen[w];
     if (w == set / 32) m &= (1u << (set & 31)) - 1;
     rank += __popc(m);
   }
-  // pass 2 writes the slots in order, a chunk of consecutive picks a thread
-  int done = 0;
-  for (int c0 = 0; c0 < n && done < count; c0 += nthr) {
-    const int i = c0 + tid;
-    const bool mine = i < n && set_of(i) == set;
-    const uint32_t b = __ballot_sync(0xffffffffu, mine);
-    __syncthreads();
-    if (lane == 0) warp_eq[warp] = __popc(b);
-    __syncthreads();
-    int before = done, total = 0;
-    for (int w = 0; w < nwarp; ++w) {
-      if (w < warp) before += warp_eq[w];
-      total += warp_eq[w];
-    }
-    if (mine) {
-      const int at = base + before + __popc(b & ((1u << lane) - 1));
-      plan.order[at] = i;
-      if (plan.pos) plan.pos[i] = set < S ? at : -1;
-    }
-    done += total;
-  }
-  // tiles of at most bt rows: set s takes the entries from base / bt + rank up
-  // to the next set's first, (base + count) / bt + rank + 1: as many as it
-  // needs, or one more, which is then empty
-  if (tid == 0) plan.offset[set] = base;
   if (set < S) {
     if (count > 0) {
       const int t0 = base / bt + rank, t1 = (base + count) / bt + rank + 1;
@@ -295,23 +346,18 @@ plan_kernel(const int32_t* __restrict__ ids, int n, int S, int bt, RowPlan plan)
       }
     }
   } else if (tid == 0) {
-    plan.head[0] = base;              // rows that have a set
     plan.head[1] = base / bt + rank;  // entries of the tile table
   }
 }
 
 cudaError_t launch_plan(const int32_t* ids, int64_t n, int S, int bt, const RowPlan& plan,
                         cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(S + 1), 1, 1);
-  cfg.blockDim = dim3(n <= 256 ? 128 : (n <= 4096 ? 512 : kPlanThreads), 1, 1);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, plan_kernel, ids, (int)n, S, bt, plan);
+  // four picks a thread while that fits one round, else 32
+  const bool small = n <= 4 * kPlanThreads;
+  const int64_t want = small ? (n + 3) / 4 : kPlanThreads;
+  PdlConfig c(dim3((unsigned)(S + 1), 1, 1), (unsigned)((want + 31) / 32 * 32), 0, st);
+  return small ? cudaLaunchKernelEx(&c.cfg, plan_kernel<4>, ids, (int)n, S, bt, plan)
+               : cudaLaunchKernelEx(&c.cfg, plan_kernel<32>, ids, (int)n, S, bt, plan);
 }
 
 }  // namespace egopq

@@ -37,31 +37,35 @@ void carve_plan(Carver& c, RowPlan& plan, int64_t n, int S, int64_t tiles, bool 
 size_t carve_experts(void* ws, ExpertsArgs& a) {
   Carver c(ws);
   const int64_t n = a.T * a.k;
-  carve_plan(c, a.plan, n, a.E, plan_max_tiles(n, a.E, 8), true);
-  // (the tensor-core products read fp16 codes, a form the quantizer writes for
-  // more than kTcFp8MaxM rows)
-  const int64_t rows = a.tensor ? experts_rows(n) : n;
-  if (a.variant == kW4A8) {
-    a.x_q = c.take<int8_t>(a.T * a.H);
-    a.x_s = c.take<float>(a.T);
-    a.x_gsum = c.take<int32_t>(a.T * (a.H / 128));
-    a.h_q = c.take<int8_t>(a.tensor ? 0 : n * a.I);
-    a.h_s = c.take<float>(rows);
-    a.h_gsum = c.take<int32_t>(rows * (a.I / 128));
-    a.h_tc = c.take<uint16_t>(a.tensor ? rows * a.I : 0);
-    a.rows_s = c.take<float>(a.tensor ? n : 0);
+  const bool codes = a.variant == kW4A8, tensor = a.way == kExpertsTensor;
+  if (a.way != kExpertsFew)
+    carve_plan(c, a.plan, n, a.E, tensor ? 0 : plan_max_tiles(n, a.E, 8), true);
+  if (codes) {
+    a.x_q = c.take<int8_t>(tensor ? 0 : a.T * a.H);
+    a.x_s = c.take<float>(tensor ? 0 : a.T);
+    a.rows_s = c.take<float>(tensor ? n : 0);
+    a.h_q = c.take<int8_t>(n * a.I * (tensor ? 2 : 1));
+    a.h_s = c.take<float>(n);
   }
-  a.h = c.take<uint16_t>(rows * a.I);
-  // the sorted activations are dead once the gate and up products have run
-  a.y = c.take<uint16_t>(n * a.H);
-  a.rows = a.y;
+  a.h = c.take<uint16_t>(n * a.I);
+  if (tensor) {
+    // the sorted activations are dead once the gate and up products have run
+    a.rows = c.take<uint16_t>(n * a.H);
+    a.y = a.rows;
+  } else if (a.way == kExpertsStream) {
+    a.y = c.take<float>(n * a.H);
+  }
   return c.used;
 }
 
 size_t carve_lora(void* ws, LoraArgs& a) {
   Carver c(ws);
-  carve_plan(c, a.plan, a.M, a.L, plan_max_tiles(a.M, a.L, lora_tile(a.M)), false);
-  a.h = c.take<float>((int64_t)lora_splits(a.M, a.K) * a.M * a.r);
+  if (lora_few(a.M)) {
+    c.take<int>(1);  // (needs none; a size of zero would say "refused")
+    return c.used;
+  }
+  carve_plan(c, a.plan, a.M, a.L, plan_max_tiles(a.M, a.L, lora_tile()), false);
+  a.h = c.take<float>((int64_t)lora_splits(a.M, a.K, a.L) * a.M * a.r);
   return c.used;
 }
 
@@ -184,11 +188,16 @@ size_t egopq_moe_experts_workspace_bytes(int64_t T, int k, int E, int64_t H, int
   a.E = E;
   a.H = H;
   a.I = I;
-  // enough for every smaller batch too, whichever products AUTO takes there
+  // enough for every smaller batch too, whichever way it takes
   size_t most = 0;
-  for (int tensor = 0; tensor < 2; ++tensor) {
-    if ((path == EGOPQ_PATH_GEMV && tensor) || (path == EGOPQ_PATH_TC && !tensor)) continue;
-    a.tensor = tensor != 0;
+  for (ExpertsWay way : {kExpertsStream, kExpertsTensor}) {
+    if ((path == EGOPQ_PATH_GEMV && way == kExpertsTensor) ||
+        (path == EGOPQ_PATH_TC && way != kExpertsTensor))
+      continue;
+    a.T = T;
+    if (path == EGOPQ_PATH_AUTO && way == kExpertsStream && T * k > kStreamRows * E)
+      a.T = kStreamRows * E / k;  // the largest batch that still streams
+    a.way = way;
     const size_t need = carve_experts(nullptr, a);
     if (need > most) most = need;
   }
@@ -215,7 +224,7 @@ int egopq_moe_experts(const uint16_t* x_bf16, const int32_t* ids, const float* w
   a.I = I;
   a.E = E;
   a.k = k;
-  a.tensor = path == EGOPQ_PATH_TC || (path == EGOPQ_PATH_AUTO && experts_on_tensor_cores(T * k, E));
+  a.way = experts_way(T, k, E, path);
   a.x = x_bf16;
   a.ids = ids;
   a.weights = weights;
