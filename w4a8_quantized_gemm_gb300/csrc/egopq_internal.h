@@ -274,12 +274,12 @@ struct ExpertsArgs {
   const uint8_t* down;
   uint16_t* out;
   RowPlan plan;
-  int8_t* x_q;     // codes of x [T][H] and their scales (W4A8, few and stream)
+  uint16_t* x_q;   // fp16 codes of x [T][H] and their scales (W4A8, few and stream)
   float* x_s;
   uint16_t* rows;  // activations in sorted order [T*k][H], bf16 or fp16 codes (tensor)
   float* rows_s;   // their scales (W4A8, tensor)
   uint16_t* h;     // bf16 [T*k][I]
-  void* h_q;       // its codes, int8 or fp16 (tensor), and their scales (W4A8)
+  uint16_t* h_q;   // its fp16 codes, and their scales (W4A8)
   float* h_s;
   void* y;         // [T*k][H], fp32 (stream) or bf16 (tensor)
   uint64_t timeout_ns;

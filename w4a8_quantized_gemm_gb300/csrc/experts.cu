@@ -62,7 +62,7 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
 }
 
 struct StreamParams {
-  const void* act;         // bf16 or int8 codes [rows][K]
+  const uint16_t* act;     // bf16, or fp16 codes (see quant_rows_kernel) [rows][K]
   const float* a_s;        // scales of those rows (W4A8)
   const uint8_t* packed;   // [E] packed weights of N rows
   uint16_t* h;             // gate and up products: bf16 [sorted row or slot][N / 2]
@@ -90,117 +90,159 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// 16 int8 codes as fp16 pairs, in order: code + 128 as a byte under 0x64 is the
-// fp16 number 1024 + code + 128 (every step exact).
-__device__ __forceinline__ void codes_to_f16(const uint4& v, uint32_t* o) {
-  const __half2 bias = __float2half2_rn(1152.f);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// The four operand words of one word of packed codes, with as little arithmetic
+// as it takes: the zero point is not subtracted here but from the group's sum,
+// as z (or z + 128) times the sum of the activations, which one more row tile
+// of ones gives in the same fragment layout.
+//   W4A8: the masked nibbles themselves are fp16 numbers below the smallest
+//   normal one, q * 2^-24 (words 0 and 2) and q * 2^-20 (words 1 and 3, whose
+//   activations come divided by 16: see quant_rows_kernel); every product and
+//   sum is a whole multiple of 2^-24, below 2^24 of them, so the group's sum is
+//   exact.
+//   W4A16: 128 + q as bf16. The group's sum then carries 128 sum(x) besides,
+//   which costs the fp32 sum at most seven of its 24 bits: the result keeps
+//   more than the 8 of a bf16 output by a factor of 2^9.
+template <int VARIANT>
+__device__ __forceinline__ void raw_w4_word(uint32_t w, uint32_t (&o)[4]) {
+  if constexpr (VARIANT == kW4A8) {
+    const uint32_t w2 = w >> 8;
+    o[0] = w & 0x000F000Fu;
+    o[1] = w & 0x00F000F0u;
+    o[2] = w2 & 0x000F000Fu;
+    o[3] = w2 & 0x00F000F0u;
+  } else {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const uint32_t u = w[q] ^ 0x80808080u;
-    const uint32_t lo = prmt(u, 0x64646464u, 0x4140), hi = prmt(u, 0x64646464u, 0x4342);
-    const __half2 l2 = __hsub2(*reinterpret_cast<const __half2*>(&lo), bias);
-    const __half2 h2 = __hsub2(*reinterpret_cast<const __half2*>(&hi), bias);
-    o[q * 2] = *reinterpret_cast<const uint32_t*>(&l2);
-    o[q * 2 + 1] = *reinterpret_cast<const uint32_t*>(&h2);
+    for (int q = 0; q < 4; ++q) o[q] = lop3_and_or(w >> (4 * q), 0x000F000Fu, 0x43004300u);
   }
 }
 
-// 32 activations of one row as they lie in memory (two 16-byte vectors of
-// codes, four of bf16), and as the B-operand words of a group's eight K steps.
-template <int VARIANT>
-struct ActRaw {
-  static constexpr int kVec = VARIANT == kW4A8 ? 2 : 4;
-  uint4 v[kVec];
-  __device__ __forceinline__ void load(const void* act, int64_t at, bool live) {
-    const uint8_t* src = static_cast<const uint8_t*>(act) + at * (VARIANT == kW4A8 ? 1 : 2);
-#pragma unroll
-    for (int i = 0; i < kVec; ++i)
-      v[i] = live ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0, 0, 0, 0);
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int j) {
+  return j == 0 ? v.x : (j == 1 ? v.y : (j == 2 ? v.z : v.w));
+}
+
+// A warp's stream of units (one group of its 32 weight rows from rbase, times
+// the activations of up to 8 NT rows), through a ring of kStages records.
+template <int VARIANT, int NT>
+struct Stream {
+  uint32_t ring_at;
+  const uint8_t* ring;
+  int w_off, m_off;  // this lane's bytes of a record
+  int put = 0;
+
+  __device__ __forceinline__ Stream(uint8_t* r, int rbase) : ring(r) {
+    const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+    ring_at = smem_u32(r);
+    // its row's 16 bytes of chunk tig (rows 8 apart 128 bytes apart), and a
+    // word of the 32 rows' scales or zero points
+    w_off = (tig * 128 + rbase + gid) * 16;
+    m_off = lane < 16 ? 8192 + 2 * rbase + lane * 4 : 8448 + rbase / 2 + (lane - 16) * 4;
   }
-  __device__ __forceinline__ void words(uint32_t (&b)[16]) const {
-    if constexpr (VARIANT == kW4A8) {
-      codes_to_f16(v[0], b);
-      codes_to_f16(v[1], b + 8);
-    } else {
+
+  template <typename Rec>
+  __device__ __forceinline__ void issue(bool live, Rec& next_rec) {
+    if (live) {
+      const int lane = threadIdx.x & 31;
+      const uint8_t* rec = next_rec();
+      const uint32_t st = ring_at + put * kStageBytes;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        b[4 * i] = v[i].x;
-        b[4 * i + 1] = v[i].y;
-        b[4 * i + 2] = v[i].z;
-        b[4 * i + 3] = v[i].w;
+      for (int q = 0; q < 4; ++q) cp_async16(st + (q * 32 + lane) * 16, rec + w_off + 128 * q);
+      if (lane < 20) cp_async4(st + 2048 + lane * 4, rec + m_off);
+      put = put + 1 == kStages ? 0 : put + 1;
+    }
+    cp_async_commit();
+  }
+
+  // The first records on their way (weights depend on no earlier kernel).
+  template <typename Rec>
+  __device__ __forceinline__ void prime(int n_units, Rec next_rec) {
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i < n_units, next_rec);
+  }
+
+  // sum += the products of the n_units units. next_rec(): the next unit's
+  // record (after those primed); next_x(nt): this lane's 32 activations of
+  // column tile nt of the next unit, or null; each called once a unit, in
+  // order; after(): once a unit is in `sum`.
+  template <typename Rec, typename NextX, typename After>
+  __device__ __forceinline__ void run(int n_units, Rec next_rec, NextX next_x, After after,
+                                      float (&sum)[2][NT][4]) {
+    const int lane = threadIdx.x & 31, gid = lane >> 2;
+    uint4 x[NT][4];  // word j: the K steps 2j and 2j + 1
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const uint4* src = n_units > 0 ? next_x(nt) : nullptr;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[nt][j] = src ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+    }
+    int get = 0;
+    for (int i = 0; i < n_units; ++i) {
+      cp_async_wait<kStages - 2>();
+      __syncwarp();  // unit i has landed, and every lane has read unit i - 1
+      const uint8_t* st = ring + get * kStageBytes;
+      get = get + 1 == kStages ? 0 : get + 1;
+      uint4 w[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) w[q] = *reinterpret_cast<const uint4*>(st + (q * 32 + lane) * 16);
+      const uint4 zw = *reinterpret_cast<const uint4*>(st + 2112);
+      uint16_t sh[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        sh[q] = *reinterpret_cast<const uint16_t*>(st + 2048 + 2 * (gid + 8 * q));
+      issue(i + kStages - 1 < n_units, next_rec);
+      const uint4* src[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) src[nt] = i + 1 < n_units ? next_x(nt) : nullptr;
+      float acc[2][NT][4], ones[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[0][nt][q] = acc[1][nt][q] = ones[nt][q] = 0.f;
+      // (three independent chains of matrix instructions a column tile)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t a[4][4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) raw_w4_word<VARIANT>(word_of(w[q], j), a[q]);
+        constexpr uint32_t kOne = VARIANT == kW4A8 ? 0x3C003C00u : 0x3F803F80u;
+        // (words 1 and 3 times 16, to undo the division of W4A8)
+        constexpr uint32_t kOne16 = VARIANT == kW4A8 ? 0x4C004C00u : 0x3F803F80u;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint4 b = x[nt][j];
+          mma_16816<VARIANT>(acc[0][nt], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
+          mma_16816<VARIANT>(acc[1][nt], a[2][0], a[3][0], a[2][1], a[3][1], b.x, b.y);
+          mma_16816<VARIANT>(ones[nt], kOne, kOne, kOne16, kOne16, b.x, b.y);
+          mma_16816<VARIANT>(acc[0][nt], a[0][2], a[1][2], a[0][3], a[1][3], b.z, b.w);
+          mma_16816<VARIANT>(acc[1][nt], a[2][2], a[3][2], a[2][3], a[3][3], b.z, b.w);
+          mma_16816<VARIANT>(ones[nt], kOne, kOne, kOne16, kOne16, b.z, b.w);
+          // the next unit's word, a unit ahead of its use
+          if (src[nt]) x[nt][j] = __ldg(src[nt] + j);
+        }
       }
+      // zero points: rows 8q .. 8q + 7 are the nibbles of word q
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float s = f16_bits_to_f32(sh[q]);
+        const uint32_t zz = (word_of(zw, q) >> (4 * gid)) & 0xFu;
+        // -(z + 128) as a float: 2^23 + 128 + z under a sign, plus 2^23
+        const float z =
+            __uint_as_float(0xCB000000u | (zz + (VARIANT == kW4A8 ? 0u : 128u))) + 8388608.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float p = acc[q >> 1][nt][(q & 1) * 2 + c];
+            // p 2^24 - z sum(a) (exact), or p - (z + 128) sum(x)
+            const float v = VARIANT == kW4A8 ? fmaf(p, 16777216.f, z * ones[nt][c])
+                                             : fmaf(z, ones[nt][c], p);
+            float& t = sum[q >> 1][nt][(q & 1) * 2 + c];
+            t = fmaf(s, v, t);
+          }
+      }
+      after();
     }
   }
 };
-
-// sum += the products of this warp's n_units (record, activations) units with
-// the 32 weight rows from rbase. rec_of(i): unit i's record; load_x(i, nt,
-// raw): its activations for column tile nt; after(i): called once unit i is
-// in `sum`.
-template <int VARIANT, int NT, typename Rec, typename LoadX, typename After>
-__device__ __forceinline__ void stream_units(uint8_t* ring, int n_units, int rbase, Rec rec_of,
-                                             LoadX load_x, After after, float (&sum)[2][NT][4]) {
-  const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
-  const uint32_t ring_at = smem_u32(ring);
-  auto issue = [&](int i) {
-    if (i < n_units) {
-      const uint8_t* rec = rec_of(i);
-      const uint32_t st = ring_at + (uint32_t)(i % kStages) * kStageBytes;
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        cp_async16(st + (q * 32 + lane) * 16, rec + (tig * 128 + rbase + gid + 8 * q) * 16);
-      if (lane < 16) cp_async4(st + 2048 + lane * 4, rec + 8192 + 2 * rbase + lane * 4);
-      else if (lane < 20) cp_async4(st + 2048 + lane * 4, rec + 8448 + rbase / 2 + (lane - 16) * 4);
-    }
-    cp_async_commit();
-  };
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) issue(i);
-  ActRaw<VARIANT> raw[NT];
-  if (n_units > 0) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) load_x(0, nt, raw[nt]);
-  }
-  for (int i = 0; i < n_units; ++i) {
-    cp_async_wait<kStages - 2>();
-    __syncwarp();  // unit i has landed, and every lane has read unit i - 1
-    issue(i + kStages - 1);
-    const uint8_t* st = ring + (i % kStages) * kStageBytes;
-    uint32_t b[NT][16];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      raw[nt].words(b[nt]);
-      if (i + 1 < n_units) load_x(i + 1, nt, raw[nt]);
-    }
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      uint32_t a[2][16];
-      float s[2];
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int row = gid + 8 * (2 * mt + q);
-        const uint4 v = *reinterpret_cast<const uint4*>(st + ((2 * mt + q) * 32 + lane) * 16);
-        s[q] = f16_bits_to_f32(*reinterpret_cast<const uint16_t*>(st + 2048 + 2 * row));
-        const uint32_t zb = st[2112 + (row >> 1)];
-        cvt_w4_unit<VARIANT>(v, (row & 1) ? (zb >> 4) : (zb & 0xF), a[q]);
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          mma_16816<VARIANT>(acc, a[0][2 * j], a[1][2 * j], a[0][2 * j + 1], a[1][2 * j + 1],
-                             b[nt][2 * j], b[nt][2 * j + 1]);
-        sum[mt][nt][0] = fmaf(s[0], acc[0], sum[mt][nt][0]);
-        sum[mt][nt][1] = fmaf(s[0], acc[1], sum[mt][nt][1]);
-        sum[mt][nt][2] = fmaf(s[1], acc[2], sum[mt][nt][2]);
-        sum[mt][nt][3] = fmaf(s[1], acc[3], sum[mt][nt][3]);
-      }
-    }
-    after(i);
-  }
-}
 
 // The warp's 32 x 8 NT sums into its rows of `red` ([32][LD] a warp).
 template <int NT, int LD>
@@ -226,70 +268,87 @@ __device__ __forceinline__ void zero_sums(float (&sum)[2][NT][4]) {
 }
 
 // ---- few tokens: the picked experts, from the ids alone -----------------------------
-// Every CTA reads the (at most 128) ids and marks the picked experts in a bit
-// set; expert number b is the b-th set bit.
+// Every warp reads the (at most 128) ids, four a lane, and marks the picked
+// experts in a bit set of its own; expert number b is the b-th set bit.
 struct FewPicks {
-  uint32_t seen[kMaxSets / 32];
-  int ids[kFewSlots];
+  int id[4];        // ids of slots lane, lane + 32, ...; -1: none or no expert
+  uint32_t seen;    // experts 32 lane ..
+  int before;       // picked experts of the lanes below
+  int count;        // picked experts
+
+  __device__ __forceinline__ FewPicks(const StreamParams& p, uint32_t* bits) {
+    const int lane = threadIdx.x & 31, n = p.T * p.k;
+    bits[lane] = 0;
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = q * 32 + lane;
+      id[q] = i < n ? __ldcg(p.ids + i) : -1;  // (L2: see experts_few_down_kernel)
+      if (id[q] < 0 || id[q] >= p.E) id[q] = -1;
+      else atomicOr(&bits[id[q] >> 5], 1u << (id[q] & 31));
+    }
+    __syncwarp();
+    seen = bits[lane];
+    int incl = __popc(seen);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    before = incl - __popc(seen);
+    count = __shfl_sync(0xffffffffu, incl, 31);
+  }
+  // Expert number b (below the count).
+  __device__ __forceinline__ int expert(int b) const {
+    const int own = b - before;
+    const bool here = own >= 0 && own < __popc(seen);
+    uint32_t m = seen;
+    for (int i = 0; here && i < own; ++i) m &= m - 1;
+    const uint32_t who = __ballot_sync(0xffffffffu, here);
+    return __shfl_sync(0xffffffffu, (threadIdx.x & 31) * 32 + __ffs(m) - 1, __ffs(who) - 1);
+  }
+  // The slots that picked expert e, as 128 bits.
+  __device__ __forceinline__ void slots(int e, uint32_t (&m)[4]) const {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) m[q] = __ballot_sync(0xffffffffu, id[q] == e);
+  }
 };
 
-// Fills `f` (all threads; ends with a barrier); returns the number of experts.
-__device__ __forceinline__ int few_picks(FewPicks& f, const StreamParams& p) {
-  const int n = p.T * p.k, words = (p.E + 31) / 32;
-  for (int i = threadIdx.x; i < words; i += blockDim.x) f.seen[i] = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int v = __ldg(p.ids + i);
-    f.ids[i] = v;
-    if (v >= 0 && v < p.E) atomicOr(&f.seen[v >> 5], 1u << (v & 31));
+// Token t's first slot among the 128 bits m (slots t k .. t k + k - 1), or -1.
+__device__ __forceinline__ int few_slot(const uint32_t (&m)[4], int t, int T, int k) {
+  int found = -1;
+  const int lo = t * k, hi = t < T ? lo + k : lo;
+#pragma unroll
+  for (int q = 3; q >= 0; --q) {
+    const int a = max(lo - 32 * q, 0), b = min(hi - 32 * q, 32);
+    if (a < b) {
+      const uint32_t w = m[q] & (0xffffffffu >> (32 - b)) & (0xffffffffu << a);
+      if (w) found = 32 * q + __ffs(w) - 1;
+    }
   }
-  __syncthreads();
-  int count = 0;
-  for (int w = 0; w < words; ++w) count += __popc(f.seen[w]);
-  return count;
-}
-
-// The b-th picked expert (b below the count).
-__device__ __forceinline__ int few_expert(const FewPicks& f, int b) {
-  int w = 0;
-  for (int c = __popc(f.seen[0]); b >= c; c = __popc(f.seen[w])) {
-    b -= c;
-    ++w;
-  }
-  uint32_t m = f.seen[w];
-  for (; b > 0; --b) m &= m - 1;
-  return w * 32 + __ffs(m) - 1;
-}
-
-// Token t's first slot with expert e, or -1.
-__device__ __forceinline__ int few_slot(const FewPicks& f, const StreamParams& p, int t, int e) {
-  for (int j = 0; j < p.k; ++j)
-    if (f.ids[t * p.k + j] == e) return t * p.k + j;
-  return -1;
+  return found;
 }
 
 // ---- h = silu(G x) * (U x) -----------------------------------------------------------
 template <int VARIANT, int NT, bool FEW>
-__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 5 : (NT == 2 ? 3 : 2))
+__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 5 : (NT == 2 ? 4 : 2))
 experts_gate_up_kernel(const StreamParams p) {
   constexpr int LD = 8 * NT + 1;  // padded row of the partial sums
   static_assert(kWarps * kStages * kStageBytes >= kWarps * 32 * LD * 4, "sums reuse the ring");
   __shared__ __align__(128) uint8_t ring[kWarps][kStages * kStageBytes];
-  __shared__ FewPicks few;
-  __shared__ int few_slots[kFewTokens];
+  __shared__ uint32_t bits[FEW ? kWarps : 1][32];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
   const int G = p.G, K = G * 128;
   int set, rows, first = 0;  // the expert, its rows here, the first one's sorted position
+  uint32_t picked[4];        // few tokens: the expert's slots
   if constexpr (FEW) {
-    if ((int)blockIdx.x >= few_picks(few, p)) return;
-    set = few_expert(few, blockIdx.x);
-    if (threadIdx.x < kFewTokens)
-      few_slots[threadIdx.x] =
-          (int)threadIdx.x < p.T ? few_slot(few, p, threadIdx.x, set) : -1;
-    __syncthreads();
+    const FewPicks few(p, bits[warp]);
+    if ((int)blockIdx.x >= few.count) return;
+    set = few.expert(blockIdx.x);
+    few.slots(set, picked);
     rows = p.T;
   } else {
     if ((int)blockIdx.x >= p.head[1]) return;
@@ -299,27 +358,36 @@ experts_gate_up_kernel(const StreamParams p) {
     rows = tile.z;
     if (rows == 0) return;
   }
-  const uint8_t* rec =
-      p.packed + (((int64_t)set * (p.N >> 7) + (blockIdx.y >> 2)) * G) * 8512;
-  int64_t at[NT];
-  bool live[NT];
+  Stream<VARIANT, NT> stream(ring[warp], (blockIdx.y & 3) * 32);
+  const uint8_t* rec = p.packed +
+                       (((int64_t)set * (p.N >> 7) + (blockIdx.y >> 2)) * G + warp) * 8512;
+  auto next_rec = [&] {
+    const uint8_t* r = rec;
+    rec += kWarps * 8512;
+    return r;
+  };
+  const int n_units = warp < G ? (G - warp + kWarps - 1) / kWarps : 0;
+  stream.prime(n_units, next_rec);
+  const uint16_t* xp[NT];  // this lane's next activations of column gid of each tile, or null
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int j = nt * 8 + gid;
-    live[nt] = FEW ? few_slots[gid] >= 0 : j < rows;
-    const int64_t row = FEW ? gid : (live[nt] ? __ldg(p.order + first + j) / p.k : 0);
-    at[nt] = row * K + 32 * tig;
+    bool live = j < rows;
+    int64_t row = gid;
+    if constexpr (FEW) live = few_slot(picked, gid, p.T, p.k) >= 0;
+    else row = live ? __ldg(p.order + first + j) / p.k : 0;
+    xp[nt] = live ? p.act + row * K + warp * 128 + 32 * tig : nullptr;
   }
   float sum[2][NT][4];
   zero_sums<NT>(sum);
-  const int n_units = warp < G ? (G - warp + kWarps - 1) / kWarps : 0;
-  stream_units<VARIANT, NT>(
-      ring[warp], n_units, (blockIdx.y & 3) * 32,
-      [&](int i) { return rec + (int64_t)(warp + i * kWarps) * 8512; },
-      [&](int i, int nt, ActRaw<VARIANT>& raw) {
-        raw.load(p.act, at[nt] + (int64_t)(warp + i * kWarps) * 128, live[nt]);
+  stream.run(
+      n_units, next_rec,
+      [&](int nt) {
+        const uint16_t* x = xp[nt];
+        if (x) xp[nt] += kWarps * 128;
+        return reinterpret_cast<const uint4*>(x);
       },
-      [](int) {}, sum);
+      [] {}, sum);
   __syncthreads();  // every warp is done with its ring
   float* red = reinterpret_cast<float*>(ring[0]);
   put_sums<NT, LD>(red + warp * 32 * LD, sum);
@@ -328,7 +396,7 @@ experts_gate_up_kernel(const StreamParams p) {
   for (int i = threadIdx.x; i < 16 * 8 * NT; i += 32 * kWarps) {
     const int c = i & 15, j = i >> 4;
     if (j >= rows) break;
-    const int64_t to = FEW ? few_slots[j] : first + j;
+    const int64_t to = FEW ? few_slot(picked, j, p.T, p.k) : first + j;
     if (to < 0) continue;
     float gate = 0.f, up = 0.f;
 #pragma unroll
@@ -347,33 +415,55 @@ experts_gate_up_kernel(const StreamParams p) {
 
 // ---- y = D h, a sorted row at a time ----------------------------------------------------
 template <int VARIANT, int NT>
-__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 5 : (NT == 2 ? 3 : 2))
+__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 5 : (NT == 2 ? 4 : 2))
 experts_down_kernel(const StreamParams p) {
   constexpr int LD = 8 * NT + 1;
   __shared__ __align__(128) uint8_t ring[kWarps][kStages * kStageBytes];
-  griddep_wait();
-  if (threadIdx.x == 0) griddep_launch_dependents();
-  if ((int)blockIdx.x >= p.head[1]) return;
-  const int4 tile = __ldg(p.tiles + blockIdx.x);
+  // the plan is older than the kernel before this one, every block of which
+  // waited for it before it let this grid start: the weights may be on their
+  // way before the gated values are there (read past L1, which this grid's own
+  // wait has not yet made current)
+  if ((int)blockIdx.x >= __ldcg(p.head + 1)) {
+    griddep_wait();
+    return;
+  }
+  const int4 tile = __ldcg(p.tiles + blockIdx.x);
   const int rows = tile.z;
-  if (rows == 0) return;
+  if (rows == 0) {
+    griddep_wait();
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
   const int G = p.G, K = G * 128;
-  const uint8_t* rec =
-      p.packed + (((int64_t)tile.x * (p.N >> 7) + (blockIdx.y >> 2)) * G) * 8512;
+  Stream<VARIANT, NT> stream(ring[warp], (blockIdx.y & 3) * 32);
+  const uint8_t* rec = p.packed +
+                       (((int64_t)tile.x * (p.N >> 7) + (blockIdx.y >> 2)) * G + warp) * 8512;
+  auto next_rec = [&] {
+    const uint8_t* r = rec;
+    rec += kWarps * 8512;
+    return r;
+  };
+  const int n_units = warp < G ? (G - warp + kWarps - 1) / kWarps : 0;
+  stream.prime(n_units, next_rec);
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  const uint16_t* xp[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int j = nt * 8 + gid;
+    xp[nt] = j < rows ? p.act + (int64_t)(tile.y + j) * K + warp * 128 + 32 * tig : nullptr;
+  }
   float sum[2][NT][4];
   zero_sums<NT>(sum);
-  const int n_units = warp < G ? (G - warp + kWarps - 1) / kWarps : 0;
-  stream_units<VARIANT, NT>(
-      ring[warp], n_units, (blockIdx.y & 3) * 32,
-      [&](int i) { return rec + (int64_t)(warp + i * kWarps) * 8512; },
-      [&](int i, int nt, ActRaw<VARIANT>& raw) {
-        raw.load(p.act,
-                 (int64_t)(tile.y + nt * 8 + gid) * K + (warp + i * kWarps) * 128 + 32 * tig,
-                 nt * 8 + gid < rows);
+  stream.run(
+      n_units, next_rec,
+      [&](int nt) {
+        const uint16_t* x = xp[nt];
+        if (x) xp[nt] += kWarps * 128;
+        return reinterpret_cast<const uint4*>(x);
       },
-      [](int) {}, sum);
+      [] {}, sum);
   __syncthreads();
   float* red = reinterpret_cast<float*>(ring[0]);
   put_sums<NT, LD>(red + warp * 32 * LD, sum);
@@ -398,60 +488,89 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1)
 experts_few_down_kernel(const StreamParams p) {
   constexpr int LD = kFewTokens + 1;
   extern __shared__ __align__(128) uint8_t few_ring[];  // [kFewWarps][kStages * kStageBytes]
-  __shared__ FewPicks few;
-  __shared__ int expert[kFewSlots];
+  __shared__ uint32_t bits[kFewWarps][32];
   __shared__ int slot[kFewSlots][kFewTokens];      // token's row of h, -1: not picked
   __shared__ float weight[kFewSlots][kFewTokens];  // its weight (and the row's scale)
-  griddep_wait();
-  if (threadIdx.x == 0) griddep_launch_dependents();
+  // the ids and the router's weights are older than the kernel before this one,
+  // every block of which waited for them before it let this grid start: the
+  // experts can be found, and their weights be on their way, before the gated
+  // values are there (ids and weights are read past L1, which this grid's own
+  // wait has not yet made current)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
   const int G = p.G, K = G * 128;
-  const int count = few_picks(few, p);
-  for (int i = threadIdx.x; i < count * kFewTokens; i += 32 * kFewWarps) {
-    const int b = i / kFewTokens, t = i % kFewTokens;
-    const int e = few_expert(few, b);
-    if (t == 0) expert[b] = e;
-    int s = -1;
-    float w = 0.f;
-    if (t < p.T) {
-      s = few_slot(few, p, t, e);
+  const FewPicks few(p, bits[warp]);
+  const int units = few.count * G;
+  const int n_units = warp < units ? (units - warp + kFewWarps - 1) / kFewWarps : 0;
+  // three walks over this warp's units (expert b, group g), kFewWarps units a
+  // step: the records run ahead of the activations, these of the sums
+  struct Walk {
+    int b, g;
+    __device__ __forceinline__ bool step(int G) {  // whether b moved
+      g += kFewWarps;
+      if (g < G) return false;
+      do {
+        g -= G;
+        ++b;
+      } while (g >= G);
+      return true;
+    }
+  };
+  Walk rw{warp / G, warp % G}, xw = rw, sw = rw;
+  const uint8_t* blk = p.packed + (int64_t)(blockIdx.x >> 2) * G * 8512;
+  const int64_t per_set = (int64_t)(p.N >> 7) * G * 8512;
+  int rec_set = n_units > 0 ? few.expert(rw.b) : 0;
+  auto next_rec = [&] {
+    const uint8_t* r = blk + rec_set * per_set + rw.g * 8512;
+    if (rw.step(G) && rw.b < few.count) rec_set = few.expert(rw.b);
+    return r;
+  };
+  Stream<VARIANT, 1> stream(few_ring + warp * kStages * kStageBytes, (blockIdx.x & 3) * 32);
+  stream.prime(n_units, next_rec);
+  for (int b = warp; b < few.count; b += kFewWarps) {
+    uint32_t picked[4];
+    few.slots(few.expert(b), picked);
+    if (lane < kFewTokens) {
+      const int s = few_slot(picked, lane, p.T, p.k);
+      float w = 0.f;
       // (a token that lists an expert twice: h is in the first slot, the
       // weights add up)
-      for (int j = s; j >= 0 && j < (t + 1) * p.k; ++j)
-        if (few.ids[j] == e) w += __ldg(p.weights + j);
-      if (VARIANT == kW4A8 && s >= 0) w *= __ldg(p.a_s + s);
+      for (int j = s; j >= 0 && j < (lane + 1) * p.k; ++j)
+        if ((picked[j >> 5] >> (j & 31)) & 1) w += __ldcg(p.weights + j);
+      slot[b][lane] = s;
+      weight[b][lane] = w;
     }
-    slot[b][t] = s;
-    weight[b][t] = w;
   }
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
   __syncthreads();
-  const int units = count * G;
-  const int n_units = warp < units ? (units - warp + kFewWarps - 1) / kFewWarps : 0;
+  if constexpr (VARIANT == kW4A8) {
+    for (int i = threadIdx.x; i < few.count * kFewTokens; i += 32 * kFewWarps) {
+      const int s = slot[i / kFewTokens][i % kFewTokens];
+      if (s >= 0) weight[i / kFewTokens][i % kFewTokens] *= p.a_s[s];
+    }
+    __syncthreads();
+  }
   float sum[2][1][4], total[2][1][4];
   zero_sums<1>(sum);
   zero_sums<1>(total);
-  stream_units<VARIANT, 1>(
-      few_ring + warp * kStages * kStageBytes, n_units, (blockIdx.x & 3) * 32,
-      [&](int i) {
-        const int u = warp + i * kFewWarps, b = u / G;
-        return p.packed + (((int64_t)expert[b] * (p.N >> 7) + (blockIdx.x >> 2)) * G + (u - b * G)) *
-                              8512;
+  stream.run(
+      n_units, next_rec,
+      [&](int) {
+        const int s = slot[xw.b][gid];
+        const uint16_t* x =
+            s >= 0 ? p.act + (int64_t)s * K + xw.g * 128 + 32 * tig : nullptr;
+        xw.step(G);
+        return reinterpret_cast<const uint4*>(x);
       },
-      [&](int i, int, ActRaw<VARIANT>& raw) {
-        const int u = warp + i * kFewWarps, b = u / G;
-        const int s = slot[b][gid];
-        raw.load(p.act, (int64_t)s * K + (u - b * G) * 128 + 32 * tig, s >= 0);
-      },
-      [&](int i) {
-        const int u = warp + i * kFewWarps, b = u / G;
-        if (i + 1 < n_units && (u + kFewWarps) / G == b) return;
-        const float w0 = weight[b][2 * tig], w1 = weight[b][2 * tig + 1];
+      [&] {
+        // (every unit adds its weighted sum: eight multiply-adds)
+        const float w0 = weight[sw.b][2 * tig], w1 = weight[sw.b][2 * tig + 1];
+        sw.step(G);
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            // (a token without this expert adds nothing, whatever its column holds)
             total[mt][0][q] = fmaf((q & 1) ? w1 : w0, sum[mt][0][q], total[mt][0][q]);
             sum[mt][0][q] = 0.f;
           }
@@ -517,8 +636,9 @@ combine_kernel(const Y* __restrict__ y, const float* __restrict__ weights,
 
 // ---- rows quantized, and rows in sorted order -----------------------------------------
 // Codes of a bf16 row as egopq_quant_act_i8 defines them (fp32 scale
-// absmax / 127, fp32 quotient rounded half to even): int8, or the same
-// integers as fp16 for the tensor cores. R threads a row.
+// absmax / 127, fp32 quotient rounded half to even) as exact fp16 numbers: the
+// integers themselves, or (STREAM) every second pair of them divided by 16, the
+// form the streaming products' operand words ask for.
 __device__ __forceinline__ float absmax8(const uint4& v, float m) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -536,22 +656,17 @@ __device__ __forceinline__ void codes8(const uint4& v, float s, float inv, bool 
     q[2 * j + 1] = zero ? 0.f : quant_code(__uint_as_float(w[j] & 0xFFFF0000u), s, inv);
   }
 }
+template <bool STREAM>
 __device__ __forceinline__ uint4 codes_f16(const float (&q)[8]) {
   uint32_t o[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const __half2 h = __floats2half2_rn(q[2 * j], q[2 * j + 1]);
+    const float f = STREAM && (j & 1) ? 0.0625f : 1.f;
+    const __half2 h = __floats2half2_rn(q[2 * j] * f, q[2 * j + 1] * f);
     o[j] = *reinterpret_cast<const uint32_t*>(&h);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
-__device__ __forceinline__ uint2 codes_i8(const float (&q)[8]) {
-  uint32_t o[2] = {0, 0};
-#pragma unroll
-  for (int j = 0; j < 8; ++j) o[j >> 2] |= ((uint32_t)(int)q[j] & 0xFFu) << (8 * (j & 3));
-  return make_uint2(o[0], o[1]);
-}
-
 // Maximum over the R threads of a row (R = 32, or the whole block).
 template <int R>
 __device__ __forceinline__ float row_max(float m, float* part) {
@@ -571,10 +686,10 @@ constexpr int kRowThreads = 128;
 constexpr int kRowVecs = 8;  // 16-byte vectors a thread keeps of its row
 
 // Rows [0, rows) (or those below head[0], where head is given) of x [.][K].
-template <int R, bool F16>
+template <int R, bool STREAM>
 __global__ void __launch_bounds__(kRowThreads)
 quant_rows_kernel(const uint16_t* __restrict__ x, const int* __restrict__ head, int64_t rows,
-                  int64_t K, void* __restrict__ codes, float* __restrict__ scales) {
+                  int64_t K, uint16_t* __restrict__ codes, float* __restrict__ scales) {
   __shared__ float part[kRowThreads / 32];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
@@ -599,8 +714,7 @@ quant_rows_kernel(const uint16_t* __restrict__ x, const int* __restrict__ head, 
   auto put = [&](const uint4& u, int64_t i) {
     float q[8];
     codes8(u, s, inv, a == 0.f, q);
-    if constexpr (F16) reinterpret_cast<uint4*>(static_cast<uint16_t*>(codes) + m * K)[i] = codes_f16(q);
-    else reinterpret_cast<uint2*>(static_cast<int8_t*>(codes) + m * K)[i] = codes_i8(q);
+    reinterpret_cast<uint4*>(codes + m * K)[i] = codes_f16<STREAM>(q);
   };
 #pragma unroll
   for (int i = 0; i < kRowVecs; ++i)
@@ -637,7 +751,7 @@ scatter_rows_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ 
     if constexpr (CODES) {
       float q[8];
       codes8(v, s, inv, a == 0.f, q);
-      v = codes_f16(q);
+      v = codes_f16<false>(q);
     }
     for (int j = 0; j < k; ++j) {
       const int at = __ldg(pos + m * k + j);
@@ -647,17 +761,17 @@ scatter_rows_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ 
 }
 
 // ---- launches -----------------------------------------------------------------------
-template <bool F16>
+template <bool STREAM>
 static cudaError_t launch_quant_rows(const uint16_t* x, const int* head, int64_t rows, int64_t K,
-                                     void* codes, float* scales, cudaStream_t st) {
+                                     uint16_t* codes, float* scales, cudaStream_t st) {
   // a warp a row where there are rows for every warp of the GPU (32768 x 1280:
   // a block a row leaves most of its threads without work), else a block
   if (rows >= 4096 && K <= 32 * kRowVecs * 8) {
     PdlConfig c(dim3((unsigned)((rows + 3) / 4), 1, 1), kRowThreads, 0, st);
-    return cudaLaunchKernelEx(&c.cfg, quant_rows_kernel<32, F16>, x, head, rows, K, codes, scales);
+    return cudaLaunchKernelEx(&c.cfg, quant_rows_kernel<32, STREAM>, x, head, rows, K, codes, scales);
   }
   PdlConfig c(dim3((unsigned)rows, 1, 1), kRowThreads, 0, st);
-  return cudaLaunchKernelEx(&c.cfg, quant_rows_kernel<kRowThreads, F16>, x, head, rows, K, codes,
+  return cudaLaunchKernelEx(&c.cfg, quant_rows_kernel<kRowThreads, STREAM>, x, head, rows, K, codes,
                             scales);
 }
 
@@ -695,13 +809,13 @@ static cudaError_t run_tensor(const ExpertsArgs& a, cudaStream_t st) {
   r.timeout_ns = a.timeout_ns;
   if ((e = launch_ragged(r, st)) != cudaSuccess) return e;
   if (kCodes) {
-    e = launch_quant_rows<true>(a.h, a.plan.head, n, a.I, a.h_q, a.h_s, st);
+    e = launch_quant_rows<false>(a.h, a.plan.head, n, a.I, a.h_q, a.h_s, st);
     if (e != cudaSuccess) return e;
   }
   r.gate_up = false;
   r.N = a.H;
   r.K = a.I;
-  r.act = kCodes ? a.h_q : (const void*)a.h;
+  r.act = kCodes ? a.h_q : a.h;
   r.a_s = a.h_s;
   r.packed = a.down;
   r.y = static_cast<uint16_t*>(a.y);
@@ -718,10 +832,10 @@ static cudaError_t run_few(const ExpertsArgs& a, StreamParams p, cudaStream_t st
   if (e != cudaSuccess) return e;
   if (VARIANT == kW4A8) {
     // (a slot without an expert holds no row: its codes are never read)
-    e = launch_quant_rows<false>(a.h, nullptr, n, a.I, a.h_q, a.h_s, st);
+    e = launch_quant_rows<true>(a.h, nullptr, n, a.I, a.h_q, a.h_s, st);
     if (e != cudaSuccess) return e;
   }
-  p.act = VARIANT == kW4A8 ? a.h_q : (const void*)a.h;
+  p.act = VARIANT == kW4A8 ? a.h_q : a.h;
   p.a_s = a.h_s;
   p.packed = a.down;
   p.N = (int)a.H;
@@ -741,10 +855,10 @@ static cudaError_t run_stream(const ExpertsArgs& a, StreamParams p, cudaStream_t
   cudaError_t e = cudaLaunchKernelEx(&c.cfg, experts_gate_up_kernel<VARIANT, NT, false>, p);
   if (e != cudaSuccess) return e;
   if (VARIANT == kW4A8) {
-    e = launch_quant_rows<false>(a.h, a.plan.head, n, a.I, a.h_q, a.h_s, st);
+    e = launch_quant_rows<true>(a.h, a.plan.head, n, a.I, a.h_q, a.h_s, st);
     if (e != cudaSuccess) return e;
   }
-  p.act = VARIANT == kW4A8 ? a.h_q : (const void*)a.h;
+  p.act = VARIANT == kW4A8 ? a.h_q : a.h;
   p.a_s = a.h_s;
   p.packed = a.down;
   p.N = (int)a.H;
@@ -760,7 +874,7 @@ static cudaError_t run_experts(const ExpertsArgs& a, cudaStream_t st) {
   if (a.way == kExpertsTensor) return run_tensor<VARIANT>(a, st);
   const int64_t n = a.T * a.k;
   StreamParams p{};
-  p.act = VARIANT == kW4A8 ? (const void*)a.x_q : (const void*)a.x;
+  p.act = VARIANT == kW4A8 ? a.x_q : a.x;
   p.a_s = a.x_s;
   p.packed = a.gate_up;
   p.h = a.h;
@@ -782,7 +896,7 @@ static cudaError_t run_experts(const ExpertsArgs& a, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   if (a.way == kExpertsStream) e = launch_plan(a.ids, n, a.E, 8 * nt, a.plan, st);
   if (e == cudaSuccess && VARIANT == kW4A8)
-    e = launch_quant_rows<false>(a.x, nullptr, a.T, a.H, a.x_q, a.x_s, st);
+    e = launch_quant_rows<true>(a.x, nullptr, a.T, a.H, a.x_q, a.x_s, st);
   if (e != cudaSuccess) return e;
   if (a.way == kExpertsFew) return run_few<VARIANT>(a, p, st);
   return nt == 1   ? run_stream<VARIANT, 1>(a, p, st)

@@ -31,11 +31,11 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
 
 constexpr int kLoraWarps = 8;
 constexpr int kLoraThreads = 32 * kLoraWarps;
-constexpr int kLoraTile = 64;     // rows of a tile of the two kernels
+constexpr int kLoraTile = 32;     // rows of a tile of the two kernels
 constexpr int kLoraMaxRank = 128;
 constexpr int kLoraFewRows = 128;  // rows of a one-launch batch
 constexpr int kLoraCluster = 8;
-constexpr int kHsLd = kLoraMaxRank + 8;  // padded row of the bf16 A x in shared memory
+constexpr int kHsLd = kLoraMaxRank + 8;  // padded row of the bf16 A x in shared memory (16-byte rows)
 
 struct LoraParams {
   const uint16_t* y_in;
@@ -91,43 +91,6 @@ __device__ __forceinline__ void shrink_steps(float (&acc)[MT][NR][4], const uint
   }
 }
 
-// acc[mt][t] += rows of hs (16 mt + ...) times columns n0 .. n0 + 32 of B
-// (Bb: row n0 of the adapter's B). Column c of n8-tile t is column
-// (c / 2) * 8 + 2t + c % 2 of the 32, so that a thread's sums over the four
-// tiles are eight neighbouring columns of y: one 16-byte access a row.
-template <int MT>
-__device__ __forceinline__ void expand_steps(float (&acc)[MT][4][4], const uint16_t (*hs)[kHsLd],
-                                             int mts, const uint16_t* Bb, int r, int rank) {
-  const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
-  for (int j0 = 0; j0 < rank; j0 += 16) {
-    // 16 ranks: thread column tig holds ranks 4 tig .. 4 tig + 3 of them
-    const int j = j0 + 4 * tig;
-    uint2 b[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int col = (gid >> 1) * 8 + 2 * t + (gid & 1);
-      b[t] = j < r ? __ldg(reinterpret_cast<const uint2*>(Bb + (int64_t)col * r + j))
-                   : make_uint2(0u, 0u);
-      // columns of B past the adapter's rank meet zeros of h, but may hold
-      // anything: leave them out
-      if (j + 3 >= rank) {
-        if (j >= rank) b[t] = make_uint2(0u, 0u);
-        else if (j + 1 >= rank) b[t] = make_uint2(b[t].x & 0xFFFFu, 0u);
-        else if (j + 2 >= rank) b[t].y = 0u;
-        else b[t].y &= 0xFFFFu;
-      }
-    }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      if (mt >= mts) break;
-      const uint2 a0 = *reinterpret_cast<const uint2*>(&hs[mt * 16 + gid][j]);
-      const uint2 a1 = *reinterpret_cast<const uint2*>(&hs[mt * 16 + gid + 8][j]);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) mma_bf16(acc[mt][t], a0.x, a1.x, a0.y, a1.y, b[t].x, b[t].y);
-    }
-  }
-}
-
 // Eight neighbouring columns of y plus their updates, rounded.
 __device__ __forceinline__ uint4 add_row(const uint4& v, const float (&acc)[4][4], int half) {
   const uint32_t q[4] = {v.x, v.y, v.z, v.w};
@@ -138,6 +101,88 @@ __device__ __forceinline__ uint4 add_row(const uint4& v, const float (&acc)[4][4
            ((uint32_t)f32_to_bf16_bits(__uint_as_float(q[t] & 0xFFFF0000u) + acc[t][2 * half + 1])
             << 16);
   return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Eight ranks of B (a thread's: j .. j + 7) without those past the adapter's
+// rank, which meet zeros of h but may hold anything.
+__device__ __forceinline__ uint4 keep_ranks(uint4 v, int j, int rank) {
+  if (j + 8 <= rank) return v;
+  uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    q[i] = j + 2 * i + 1 < rank ? q[i] : (j + 2 * i < rank ? q[i] & 0xFFFFu : 0u);
+  return make_uint4(q[0], q[1], q[2], q[3]);
+}
+
+// y_out = bf16(y_in + hs B^T) for a tile's rows (16 MT of them; `rows` live,
+// row_of(i) names row i of y) over 32-column chunks first, first + step, ...
+// below `last`. Column c of a chunk's n8-tile t is column (c / 2) * 8 + 2t +
+// c % 2 of it, so that a thread's sums over the four tiles are eight
+// neighbouring columns of y: one 16-byte access a row. A thread holds eight
+// ranks a step of 32, as hs has them. The next chunk's y and first 32 ranks of
+// B are on their way while a chunk is computed.
+template <int MT, typename RowOf>
+__device__ __forceinline__ void expand_chunks(const uint16_t* y_in, uint16_t* y_out, int64_t N,
+                                              const uint16_t (*hs)[kHsLd], const uint16_t* Bset,
+                                              int r, int rank, int rows, RowOf row_of,
+                                              int64_t first, int64_t last, int64_t step) {
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  int64_t at[2 * MT];  // this thread's place in its rows of y, -1: no row
+#pragma unroll
+  for (int i = 0; i < 2 * MT; ++i)
+    at[i] = i * 8 + gid < rows ? (int64_t)row_of(i * 8 + gid) * N + 8 * tig : -1;
+  const uint16_t* Bt = Bset + (int64_t)((gid >> 1) * 8 + (gid & 1)) * r + 8 * tig;
+  uint4 yn[2 * MT], bn[4];
+  auto fetch_b = [&](int64_t c, int j0, uint4 (&b)[4]) {
+    const uint16_t* src = Bt + c * 32 * r + j0;
+    const bool in = j0 + 8 * tig < rank;  // (r is a multiple of 8)
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      b[t] = in ? __ldg(reinterpret_cast<const uint4*>(src + 2 * t * r)) : make_uint4(0, 0, 0, 0);
+  };
+  auto fetch = [&](int64_t c) {
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i)
+      if (at[i] >= 0) yn[i] = *reinterpret_cast<const uint4*>(y_in + at[i] + c * 32);
+    fetch_b(c, 0, bn);
+  };
+  if (first < last) fetch(first);
+  for (int64_t c = first; c < last; c += step) {
+    uint4 y[2 * MT], b[4];
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i) y[i] = yn[i];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) b[t] = bn[t];
+    if (c + step < last) fetch(c + step);
+    float acc[MT][4][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[m][t][q] = 0.f;
+    for (int j0 = 0; j0 < rank; j0 += 32) {
+      if (j0 > 0) fetch_b(c, j0, b);
+      const int j = j0 + 8 * tig;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) b[t] = keep_ranks(b[t], j, rank);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        if (m * 16 >= rows) break;
+        const uint4 a0 = *reinterpret_cast<const uint4*>(&hs[m * 16 + gid][j]);
+        const uint4 a1 = *reinterpret_cast<const uint4*>(&hs[m * 16 + gid + 8][j]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          mma_bf16(acc[m][t], a0.x, a1.x, a0.y, a1.y, b[t].x, b[t].y);
+          mma_bf16(acc[m][t], a0.z, a1.z, a0.w, a1.w, b[t].z, b[t].w);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i)
+      if (at[i] >= 0)
+        *reinterpret_cast<uint4*>(y_out + at[i] + c * 32) = add_row(y[i], acc[i >> 1], i & 1);
+  }
 }
 
 template <int MT, int NT>
@@ -263,7 +308,7 @@ lora_few_kernel(const LoraParams p) {
       __syncthreads();
     }
     cluster_sync_all();  // every CTA's part is in its shared memory
-    const int kr = (rank + 15) & ~15;
+    const int kr = (rank + 31) & ~31;
     const uint32_t local = smem_u32(part);
     for (int i = threadIdx.x; i < 16 * kr; i += kLoraThreads) {
       const int row = i / kr, j = i - row * kr;
@@ -279,36 +324,33 @@ lora_few_kernel(const LoraParams p) {
       hs[row][j] = f32_to_bf16_bits(sc * v);
     }
     cluster_sync_all();  // (also the block's barrier) parts may be rewritten, CTAs may leave
-    for (int64_t c = c_lo + warp; c < c_hi; c += kLoraWarps) {
-      const int64_t n0 = c * 32;
-      uint4 y[2];
-      int64_t at[2];
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int row = gid + 8 * half;
-        at[half] = row < rows ? (int64_t)rows_of[t0 + row] * p.N + n0 + 8 * tig : -1;
-        if (at[half] >= 0) y[half] = *reinterpret_cast<const uint4*>(p.y_in + at[half]);
-      }
-      float acc[1][4][4];
-      zero_acc<1, 4>(acc);
-      expand_steps<1>(acc, hs, 1, Bset + n0 * p.r, p.r, rank);
-#pragma unroll
-      for (int half = 0; half < 2; ++half)
-        if (at[half] >= 0)
-          *reinterpret_cast<uint4*>(p.y_out + at[half]) = add_row(y[half], acc[0], half);
-    }
+    expand_chunks<1>(p.y_in, p.y_out, p.N, hs, Bset, p.r, rank, rows,
+                     [&](int i) { return rows_of[t0 + i]; }, c_lo + warp, c_hi, kLoraWarps);
     __syncthreads();  // hs is rewritten for the next rows
   }
 }
 
 // ---- many rows: two kernels -----------------------------------------------------------
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(live ? 16 : 0)
+               : "memory");
+}
+
 // h[split][sorted row][0, rank) = the split's part of A_a x. One CTA a tile of
-// 64 rows and a part of K: warps (row half, K quarter), each 32 rows; the K
-// quarters add their sums to shared memory in turn. Reads x once; A_a comes
-// from L2 (a tile of 64 rows reads it once for its two row halves).
+// 32 rows and a part of K, which its warps share in 32-wide steps; each warp
+// keeps kShrinkStages - 1 steps of its rows and of A in flight into a ring of
+// its own (a lane reads back what it wrote: no barrier), and the warps add
+// their sums to shared memory in turn. x is read once; A_a comes from L2, once
+// a tile.
+constexpr int kShrinkWarps = 4;
+constexpr int kShrinkStages = 4;
+
 template <int NR>
-__global__ void __launch_bounds__(kLoraThreads)
+__global__ void __launch_bounds__(32 * kShrinkWarps)
 lora_shrink_kernel(const LoraParams p) {
+  constexpr int kStep = (4 + NR) * 512;  // bytes of a step: 4 row pairs' parts of x, NR of A
+  extern __shared__ __align__(128) uint8_t ring[];  // [kShrinkWarps][kShrinkStages][kStep]
   __shared__ float red[kLoraTile][8 * NR + 1];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
@@ -318,39 +360,75 @@ lora_shrink_kernel(const LoraParams p) {
   const int rank = adapter_rank(p, tile.x);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
-  const int half = warp & 1, kw = warp >> 1;
-  constexpr int kParts = kLoraWarps / 2;
   const int steps = (int)(p.K / 32);
-  const int s0 = (int)((int64_t)blockIdx.y * steps / p.splits);
+  const int s0 = (int)((int64_t)blockIdx.y * steps / p.splits) + warp;
   const int s1 = (int)((int64_t)(blockIdx.y + 1) * steps / p.splits);
   const uint16_t* xr[4];
+  bool live[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const int row = half * 32 + (q >> 1) * 16 + (q & 1) * 8 + gid;
-    xr[q] = row < tile.z ? p.x + (int64_t)__ldg(p.order + tile.y + row) * p.K + 8 * tig : nullptr;
+    const int row = q * 8 + gid;
+    live[q] = row < tile.z;
+    xr[q] = p.x + (live[q] ? (int64_t)__ldg(p.order + tile.y + row) * p.K : 0) + 8 * tig;
   }
-  const bool work = half * 32 < tile.z;
+  uint8_t* mine = ring + warp * kShrinkStages * kStep;
+  const uint32_t mine_at = smem_u32(mine) + lane * 16;
   const uint16_t* Ab = p.A + (int64_t)tile.x * p.r * p.K + 8 * tig;
   for (int c0 = 0; c0 < rank; c0 += 8 * NR) {
+    auto issue = [&](int s, int stage) {
+      if (s < s1) {
+        const uint32_t st = mine_at + stage * kStep;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) cp_async16_zfill(st + q * 512, xr[q] + (int64_t)s * 32, live[q]);
+#pragma unroll
+        for (int t = 0; t < NR; ++t) {
+          const int j = c0 + t * 8 + gid;
+          cp_async16_zfill(st + (4 + t) * 512, Ab + (int64_t)(j < rank ? j : 0) * p.K + s * 32,
+                           j < rank);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
     float acc[2][NR][4];
     zero_acc<2, NR>(acc);
-    if (work) shrink_steps<2, NR>(acc, xr, Ab, p.K, c0, rank, s0 + kw, s1, kParts);
-    for (int k = 0; k < kParts; ++k) {
-      if (kw == k && work) {
+#pragma unroll
+    for (int i = 0; i < kShrinkStages - 1; ++i) issue(s0 + i * kShrinkWarps, i);
+    int get = 0;
+    for (int s = s0; s < s1; s += kShrinkWarps) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kShrinkStages - 2) : "memory");
+      const uint8_t* st = mine + get * kStep + lane * 16;
+      uint4 a[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) a[q] = *reinterpret_cast<const uint4*>(st + q * 512);
+#pragma unroll
+      for (int t = 0; t < NR; ++t) {
+        const uint4 b = *reinterpret_cast<const uint4*>(st + (4 + t) * 512);
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          mma_bf16(acc[mt][t], a[2 * mt].x, a[2 * mt + 1].x, a[2 * mt].y, a[2 * mt + 1].y, b.x, b.y);
+          mma_bf16(acc[mt][t], a[2 * mt].z, a[2 * mt + 1].z, a[2 * mt].w, a[2 * mt + 1].w, b.z, b.w);
+        }
+      }
+      // (the lane's own copies only: what it has read it may overwrite)
+      issue(s + (kShrinkStages - 1) * kShrinkWarps, get == 0 ? kShrinkStages - 1 : get - 1);
+      get = get + 1 == kShrinkStages ? 0 : get + 1;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    for (int k = 0; k < kShrinkWarps; ++k) {
+      if (warp == k) {
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
           for (int t = 0; t < NR; ++t)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              float& v =
-                  red[half * 32 + mt * 16 + (q >> 1) * 8 + gid][t * 8 + tig * 2 + (q & 1)];
+              float& v = red[mt * 16 + (q >> 1) * 8 + gid][t * 8 + tig * 2 + (q & 1)];
               v = k == 0 ? acc[mt][t][q] : v + acc[mt][t][q];
             }
       }
       __syncthreads();
     }
-    for (int i = threadIdx.x; i < tile.z * 8 * NR; i += kLoraThreads) {
+    for (int i = threadIdx.x; i < tile.z * 8 * NR; i += 32 * kShrinkWarps) {
       const int j = i % (8 * NR), row = i / (8 * NR);
       if (c0 + j < rank)
         p.h[((int64_t)blockIdx.y * p.M + tile.y + row) * p.r + c0 + j] = red[row][j];
@@ -359,19 +437,20 @@ lora_shrink_kernel(const LoraParams p) {
   }
 }
 
-// y = bf16(y0 + scale * B_a h). One CTA a tile of 64 rows and 256 columns, 32 a
-// warp; the tile's h (the splits added in order, scaled, rounded to bf16 once:
-// see lora_few_kernel) lies in shared memory. Bound by y0 and y: 2 x 29 MB at
-// 4093 x 3584.
-__global__ void __launch_bounds__(kLoraThreads)
+// y = bf16(y0 + scale * B_a h). One CTA a tile of 32 rows and 512 columns, every
+// fourth 32 of them a warp; the tile's h (the splits added in order, scaled,
+// rounded to bf16 once: see lora_few_kernel) lies in shared memory. Bound by y0
+// and y: 2 x 29 MB at 4093 x 3584.
+constexpr int kExpandWarps = 4;
+constexpr int kExpandChunks = 16;
+
+__global__ void __launch_bounds__(32 * kExpandWarps)
 lora_expand_kernel(const LoraParams p) {
   __shared__ __align__(16) uint16_t hs[kLoraTile][kHsLd];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   const int n_tiles = p.head[1];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int gid = lane >> 2, tig = lane & 3;
-  const int64_t n0 = ((int64_t)blockIdx.y * kLoraWarps + warp) * 32;
+  const int warp = threadIdx.x >> 5;
   int4 tile;
   int rank = 0;
   if ((int)blockIdx.x < n_tiles) {
@@ -385,21 +464,10 @@ lora_expand_kernel(const LoraParams p) {
     if (first >= p.M || p.y_in == p.y_out) return;
     tile = make_int4(0, (int)first, (int)min((int64_t)kLoraTile, p.M - first), 0);
   }
-  // y0 is on its way while h is put together
-  uint4 y[8];
-  int64_t at[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = i * 8 + gid;
-    at[i] = row < tile.z && n0 < p.N
-                ? (int64_t)__ldg(p.order + tile.y + row) * p.N + n0 + 8 * tig
-                : -1;
-    if (at[i] >= 0) y[i] = *reinterpret_cast<const uint4*>(p.y_in + at[i]);
-  }
   if (rank > 0) {
     const float sc = __ldg(p.scale + tile.x);
-    const int kr = (rank + 15) & ~15;
-    for (int i = threadIdx.x; i < kLoraTile * kr; i += kLoraThreads) {
+    const int kr = (rank + 31) & ~31;
+    for (int i = threadIdx.x; i < kLoraTile * kr; i += 32 * kExpandWarps) {
       const int row = i / kr, j = i - row * kr;
       float v = 0.f;
       if (row < tile.z && j < rank)
@@ -409,14 +477,11 @@ lora_expand_kernel(const LoraParams p) {
     }
   }
   __syncthreads();
-  if (n0 >= p.N) return;
-  float acc[4][4][4];
-  zero_acc<4, 4>(acc);
-  expand_steps<4>(acc, hs, (tile.z + 15) / 16, p.B + ((int64_t)tile.x * p.N + n0) * p.r, p.r, rank);
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (at[i] >= 0)
-      *reinterpret_cast<uint4*>(p.y_out + at[i]) = add_row(y[i], acc[i >> 1], i & 1);
+  const int64_t c0 = (int64_t)blockIdx.y * kExpandChunks;
+  const int64_t c1 = min(c0 + kExpandChunks, p.N / 32);
+  expand_chunks<2>(p.y_in, p.y_out, p.N, hs, p.B + (int64_t)tile.x * p.N * p.r, p.r, rank, tile.z,
+                   [&](int i) { return __ldg(p.order + tile.y + i); }, c0 + warp, c1,
+                   kExpandWarps);
 }
 
 bool lora_few(int64_t M) { return M <= kLoraFewRows; }
@@ -427,10 +492,20 @@ int lora_splits(int64_t M, int64_t K, int L) {
   // parts of K so that about two CTAs an SM run, each of two steps a warp or more
   const int64_t tiles = M / kLoraTile + (L < M ? L : M);
   int64_t s = 304 / (tiles > 0 ? tiles : 1);
-  const int64_t most = K / (32 * kLoraWarps);
+  const int64_t most = K / (64 * kShrinkWarps);
   if (s > most) s = most;
-  if (s > 4) s = 4;
+  if (s > 8) s = 8;
   return s < 1 ? 1 : (int)s;
+}
+
+template <int NR>
+static cudaError_t launch_shrink(const LoraParams& p, int64_t tiles, cudaStream_t st) {
+  constexpr size_t kSmem = (size_t)kShrinkWarps * kShrinkStages * (4 + NR) * 512;
+  static SmemOptIn opt_in;
+  cudaError_t e = opt_in.ensure(lora_shrink_kernel<NR>, kSmem);
+  if (e != cudaSuccess) return e;
+  PdlConfig c(dim3((unsigned)tiles, (unsigned)p.splits, 1), 32 * kShrinkWarps, kSmem, st);
+  return cudaLaunchKernelEx(&c.cfg, lora_shrink_kernel<NR>, p);
 }
 
 cudaError_t launch_lora(const LoraArgs& a, cudaStream_t st) {
@@ -478,16 +553,15 @@ cudaError_t launch_lora(const LoraArgs& a, cudaStream_t st) {
   cudaError_t e = launch_plan(a.ids, a.M, a.L, kLoraTile, a.plan, st);
   if (e != cudaSuccess) return e;
   const int64_t tiles = plan_max_tiles(a.M, a.L, kLoraTile);
-  {
-    PdlConfig c(dim3((unsigned)tiles, (unsigned)p.splits, 1), kLoraThreads, 0, st);
-    e = a.r <= 16   ? cudaLaunchKernelEx(&c.cfg, lora_shrink_kernel<2>, p)
-        : a.r <= 32 ? cudaLaunchKernelEx(&c.cfg, lora_shrink_kernel<4>, p)
-                    : cudaLaunchKernelEx(&c.cfg, lora_shrink_kernel<8>, p);
-    if (e != cudaSuccess) return e;
-  }
-  // (the rows without an adapter make at most ceil(M / 64) tiles more)
+  e = a.r <= 16   ? launch_shrink<2>(p, tiles, st)
+      : a.r <= 32 ? launch_shrink<4>(p, tiles, st)
+                  : launch_shrink<8>(p, tiles, st);
+  if (e != cudaSuccess) return e;
+  // (the rows without an adapter make at most ceil(M / 32) tiles more)
   const int64_t grid = tiles + (a.M + kLoraTile - 1) / kLoraTile;
-  PdlConfig c(dim3((unsigned)grid, (unsigned)((a.N + 255) / 256), 1), kLoraThreads, 0, st);
+  PdlConfig c(dim3((unsigned)grid,
+                   (unsigned)((a.N / 32 + kExpandChunks - 1) / kExpandChunks), 1),
+              32 * kExpandWarps, 0, st);
   return cudaLaunchKernelEx(&c.cfg, lora_expand_kernel, p);
 }
 

@@ -41,10 +41,10 @@ size_t carve_experts(void* ws, ExpertsArgs& a) {
   if (a.way != kExpertsFew)
     carve_plan(c, a.plan, n, a.E, tensor ? 0 : plan_max_tiles(n, a.E, 8), true);
   if (codes) {
-    a.x_q = c.take<int8_t>(tensor ? 0 : a.T * a.H);
+    a.x_q = c.take<uint16_t>(tensor ? 0 : a.T * a.H);
     a.x_s = c.take<float>(tensor ? 0 : a.T);
     a.rows_s = c.take<float>(tensor ? n : 0);
-    a.h_q = c.take<int8_t>(n * a.I * (tensor ? 2 : 1));
+    a.h_q = c.take<uint16_t>(n * a.I);
     a.h_s = c.take<float>(n);
   }
   a.h = c.take<uint16_t>(n * a.I);
