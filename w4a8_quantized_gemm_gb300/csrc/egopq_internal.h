@@ -274,7 +274,8 @@ struct ExpertsArgs {
   const uint8_t* down;
   uint16_t* out;
   RowPlan plan;
-  uint16_t* x_q;   // fp16 codes of x [T][H] and their scales (W4A8, few and stream)
+  uint16_t* x_q;   // x [T][H] in the streaming products' form: fp16 codes and
+                   // their scales (W4A8, few and stream), bf16 (W4A16, stream)
   float* x_s;
   uint16_t* rows;  // activations in sorted order [T*k][H], bf16 or fp16 codes (tensor)
   float* rows_s;   // their scales (W4A8, tensor)

@@ -29,8 +29,11 @@ namespace egopq {
 // 16-byte unit of row r, chunk lane % 4 of a packed record: its 32 codes are
 // the thread's operand of all eight K steps of the group, once K is taken in
 // the order (step, lane % 4) -> 32 * (lane % 4) + 4 * step, which the
-// activations follow with 32 contiguous values a thread. So no shuffle and no
-// transposition stands between memory and the matrix instruction.
+// activations follow: word j (8 values) of a thread's 32 belongs to the steps 2j
+// and 2j + 1. So no shuffle and no transposition stands between memory and the
+// matrix instruction. Rows of activations are stored in that order where this
+// file writes them: values 32 t + 8 j + i of a group of 128 at 32 j + 8 t + i
+// (unit_place), so that a load reads 64 contiguous bytes of a row.
 //
 // The weights stream from HBM once: each warp keeps kStages - 1 groups of its
 // rows in flight (2.1 KB each) with cp.async into a ring of its own, which no
@@ -59,6 +62,11 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   }
+}
+
+// Where the 8 values (16 bytes) that are number u of their row go.
+__host__ __device__ __forceinline__ int64_t unit_place(int64_t u) {
+  return (u & ~(int64_t)15) | ((u & 3) << 2) | ((u >> 2) & 3);
 }
 
 struct StreamParams {
@@ -122,19 +130,26 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int j) {
 
 // A warp's stream of units (one group of its 32 weight rows from rbase, times
 // the activations of up to 8 NT rows), through a ring of kStages records.
-template <int VARIANT, int NT>
+// PLACED: rows in the order of unit_place, else as they come (a thread's 32
+// values contiguous).
+template <int VARIANT, int NT, bool PLACED>
 struct Stream {
+  static constexpr int kLane = PLACED ? 8 : 32;  // first value of thread column 1
+  static constexpr int kWord = PLACED ? 4 : 1;   // 16-byte units from word to word
   uint32_t ring_at;
   const uint8_t* ring;
   int w_off, m_off;  // this lane's bytes of a record
   int put = 0;
 
   __device__ __forceinline__ Stream(uint8_t* r, int rbase) : ring(r) {
-    const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+    const int lane = threadIdx.x & 31;
     ring_at = smem_u32(r);
-    // its row's 16 bytes of chunk tig (rows 8 apart 128 bytes apart), and a
-    // word of the 32 rows' scales or zero points
-    w_off = (tig * 128 + rbase + gid) * 16;
+    // row `lane`'s 16 bytes of each chunk (a copy is 512 contiguous bytes a
+    // warp: with the lanes in fragment order, 32 bytes of four chunks a quarter
+    // warp, the copies issued four times slower and one token's gate and up
+    // products took 14 instead of 9 us), and a word of the 32 rows' scales or
+    // zero points
+    w_off = (rbase + lane) * 16;
     m_off = lane < 16 ? 8192 + 2 * rbase + lane * 4 : 8448 + rbase / 2 + (lane - 16) * 4;
   }
 
@@ -145,7 +160,8 @@ struct Stream {
       const uint8_t* rec = next_rec();
       const uint32_t st = ring_at + put * kStageBytes;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) cp_async16(st + (q * 32 + lane) * 16, rec + w_off + 128 * q);
+      for (int c = 0; c < 4; ++c)  // (rows of chunk c exchanged: conflict-free fragments)
+        cp_async16(st + (c * 32 + (lane ^ (2 * c))) * 16, rec + w_off + 2048 * c);
       if (lane < 20) cp_async4(st + 2048 + lane * 4, rec + m_off);
       put = put + 1 == kStages ? 0 : put + 1;
     }
@@ -166,13 +182,13 @@ struct Stream {
   template <typename Rec, typename NextX, typename After>
   __device__ __forceinline__ void run(int n_units, Rec next_rec, NextX next_x, After after,
                                       float (&sum)[2][NT][4]) {
-    const int lane = threadIdx.x & 31, gid = lane >> 2;
+    const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
     uint4 x[NT][4];  // word j: the K steps 2j and 2j + 1
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const uint4* src = n_units > 0 ? next_x(nt) : nullptr;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[nt][j] = src ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < 4; ++j) x[nt][j] = src ? __ldg(src + j * kWord) : make_uint4(0, 0, 0, 0);
     }
     int get = 0;
     for (int i = 0; i < n_units; ++i) {
@@ -182,7 +198,9 @@ struct Stream {
       get = get + 1 == kStages ? 0 : get + 1;
       uint4 w[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) w[q] = *reinterpret_cast<const uint4*>(st + (q * 32 + lane) * 16);
+      for (int q = 0; q < 4; ++q)
+        w[q] = *reinterpret_cast<const uint4*>(
+            st + (tig * 32 + ((gid + 8 * q) ^ (2 * tig))) * 16);
       const uint4 zw = *reinterpret_cast<const uint4*>(st + 2112);
       uint16_t sh[4];
 #pragma unroll
@@ -216,7 +234,7 @@ struct Stream {
           mma_16816<VARIANT>(acc[1][nt], a[2][2], a[3][2], a[2][3], a[3][3], b.z, b.w);
           mma_16816<VARIANT>(ones[nt], kOne, kOne, kOne16, kOne16, b.z, b.w);
           // the next unit's word, a unit ahead of its use
-          if (src[nt]) x[nt][j] = __ldg(src[nt] + j);
+          if (src[nt]) x[nt][j] = __ldg(src[nt] + j * kWord);
         }
       }
       // zero points: rows 8q .. 8q + 7 are the nibbles of word q
@@ -224,19 +242,20 @@ struct Stream {
       for (int q = 0; q < 4; ++q) {
         const float s = f16_bits_to_f32(sh[q]);
         const uint32_t zz = (word_of(zw, q) >> (4 * gid)) & 0xFu;
-        // -(z + 128) as a float: 2^23 + 128 + z under a sign, plus 2^23
-        const float z =
+        // -(z + 128) as a float: 2^23 + 128 + z under a sign, plus 2^23; W4A8: of
+        // the scaled sums, -z 2^-24
+        const float zf =
             __uint_as_float(0xCB000000u | (zz + (VARIANT == kW4A8 ? 0u : 128u))) + 8388608.f;
+        const float z = VARIANT == kW4A8 ? zf * 0x1p-24f : zf;
+        const float sz = VARIANT == kW4A8 ? s * 0x1p24f : s;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const float p = acc[q >> 1][nt][(q & 1) * 2 + c];
-            // p 2^24 - z sum(a) (exact), or p - (z + 128) sum(x)
-            const float v = VARIANT == kW4A8 ? fmaf(p, 16777216.f, z * ones[nt][c])
-                                             : fmaf(z, ones[nt][c], p);
+            // sum(a q) - z sum(a) (exact), or sum(x (128 + q)) - (z + 128) sum(x)
+            const float v = fmaf(z, ones[nt][c], acc[q >> 1][nt][(q & 1) * 2 + c]);
             float& t = sum[q >> 1][nt][(q & 1) * 2 + c];
-            t = fmaf(s, v, t);
+            t = fmaf(sz, v, t);
           }
       }
       after();
@@ -358,7 +377,8 @@ experts_gate_up_kernel(const StreamParams p) {
     rows = tile.z;
     if (rows == 0) return;
   }
-  Stream<VARIANT, NT> stream(ring[warp], (blockIdx.y & 3) * 32);
+  using S = Stream<VARIANT, NT, !(FEW && VARIANT == kW4A16)>;
+  S stream(ring[warp], (blockIdx.y & 3) * 32);
   const uint8_t* rec = p.packed +
                        (((int64_t)set * (p.N >> 7) + (blockIdx.y >> 2)) * G + warp) * 8512;
   auto next_rec = [&] {
@@ -376,7 +396,7 @@ experts_gate_up_kernel(const StreamParams p) {
     int64_t row = gid;
     if constexpr (FEW) live = few_slot(picked, gid, p.T, p.k) >= 0;
     else row = live ? __ldg(p.order + first + j) / p.k : 0;
-    xp[nt] = live ? p.act + row * K + warp * 128 + 32 * tig : nullptr;
+    xp[nt] = live ? p.act + row * K + warp * 128 + S::kLane * tig : nullptr;
   }
   float sum[2][NT][4];
   zero_sums<NT>(sum);
@@ -409,7 +429,8 @@ experts_gate_up_kernel(const StreamParams p) {
       gate *= as;
       up *= as;
     }
-    p.h[to * I + blockIdx.y * 16 + c] = f32_to_bf16_bits(gated(gate, up));
+    const int64_t at = blockIdx.y * 16 + c;
+    p.h[to * I + unit_place(at >> 3) * 8 + (at & 7)] = f32_to_bf16_bits(gated(gate, up));
   }
 }
 
@@ -436,7 +457,7 @@ experts_down_kernel(const StreamParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
   const int G = p.G, K = G * 128;
-  Stream<VARIANT, NT> stream(ring[warp], (blockIdx.y & 3) * 32);
+  Stream<VARIANT, NT, true> stream(ring[warp], (blockIdx.y & 3) * 32);
   const uint8_t* rec = p.packed +
                        (((int64_t)tile.x * (p.N >> 7) + (blockIdx.y >> 2)) * G + warp) * 8512;
   auto next_rec = [&] {
@@ -452,7 +473,7 @@ experts_down_kernel(const StreamParams p) {
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int j = nt * 8 + gid;
-    xp[nt] = j < rows ? p.act + (int64_t)(tile.y + j) * K + warp * 128 + 32 * tig : nullptr;
+    xp[nt] = j < rows ? p.act + (int64_t)(tile.y + j) * K + warp * 128 + 8 * tig : nullptr;
   }
   float sum[2][NT][4];
   zero_sums<NT>(sum);
@@ -525,7 +546,7 @@ experts_few_down_kernel(const StreamParams p) {
     if (rw.step(G) && rw.b < few.count) rec_set = few.expert(rw.b);
     return r;
   };
-  Stream<VARIANT, 1> stream(few_ring + warp * kStages * kStageBytes, (blockIdx.x & 3) * 32);
+  Stream<VARIANT, 1, true> stream(few_ring + warp * kStages * kStageBytes, (blockIdx.x & 3) * 32);
   stream.prime(n_units, next_rec);
   for (int b = warp; b < few.count; b += kFewWarps) {
     uint32_t picked[4];
@@ -559,7 +580,7 @@ experts_few_down_kernel(const StreamParams p) {
       [&](int) {
         const int s = slot[xw.b][gid];
         const uint16_t* x =
-            s >= 0 ? p.act + (int64_t)s * K + xw.g * 128 + 32 * tig : nullptr;
+            s >= 0 ? p.act + (int64_t)s * K + xw.g * 128 + 8 * tig : nullptr;
         xw.step(G);
         return reinterpret_cast<const uint4*>(x);
       },
@@ -637,8 +658,10 @@ combine_kernel(const Y* __restrict__ y, const float* __restrict__ weights,
 // ---- rows quantized, and rows in sorted order -----------------------------------------
 // Codes of a bf16 row as egopq_quant_act_i8 defines them (fp32 scale
 // absmax / 127, fp32 quotient rounded half to even) as exact fp16 numbers: the
-// integers themselves, or (STREAM) every second pair of them divided by 16, the
-// form the streaming products' operand words ask for.
+// integers themselves (tensor), or every second pair of them divided by 16, the
+// form the streaming products' operand words ask for, in the order of
+// unit_place, which their input may have already (kStreamPlaced) or not.
+enum QuantForm { kTensorForm, kStreamForm, kStreamPlaced };
 __device__ __forceinline__ float absmax8(const uint4& v, float m) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -656,12 +679,12 @@ __device__ __forceinline__ void codes8(const uint4& v, float s, float inv, bool 
     q[2 * j + 1] = zero ? 0.f : quant_code(__uint_as_float(w[j] & 0xFFFF0000u), s, inv);
   }
 }
-template <bool STREAM>
+template <QuantForm FORM>
 __device__ __forceinline__ uint4 codes_f16(const float (&q)[8]) {
   uint32_t o[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float f = STREAM && (j & 1) ? 0.0625f : 1.f;
+    const float f = FORM != kTensorForm && (j & 1) ? 0.0625f : 1.f;
     const __half2 h = __floats2half2_rn(q[2 * j] * f, q[2 * j + 1] * f);
     o[j] = *reinterpret_cast<const uint32_t*>(&h);
   }
@@ -686,7 +709,7 @@ constexpr int kRowThreads = 128;
 constexpr int kRowVecs = 8;  // 16-byte vectors a thread keeps of its row
 
 // Rows [0, rows) (or those below head[0], where head is given) of x [.][K].
-template <int R, bool STREAM>
+template <int R, QuantForm FORM>
 __global__ void __launch_bounds__(kRowThreads)
 quant_rows_kernel(const uint16_t* __restrict__ x, const int* __restrict__ head, int64_t rows,
                   int64_t K, uint16_t* __restrict__ codes, float* __restrict__ scales) {
@@ -714,12 +737,24 @@ quant_rows_kernel(const uint16_t* __restrict__ x, const int* __restrict__ head, 
   auto put = [&](const uint4& u, int64_t i) {
     float q[8];
     codes8(u, s, inv, a == 0.f, q);
-    reinterpret_cast<uint4*>(codes + m * K)[i] = codes_f16<STREAM>(q);
+    reinterpret_cast<uint4*>(codes + m * K)[FORM == kStreamForm ? unit_place(i) : i] =
+        codes_f16<FORM>(q);
   };
 #pragma unroll
   for (int i = 0; i < kRowVecs; ++i)
     if (t + i * R < nvec) put(v[i], t + i * R);
   for (int64_t i = t + kRowVecs * R; i < nvec; i += R) put(__ldg(src + i), i);
+}
+
+// bf16 rows in the order of unit_place (W4A16, stream).
+__global__ void __launch_bounds__(kRowThreads)
+place_rows_kernel(const uint16_t* __restrict__ x, int64_t K, uint16_t* __restrict__ out) {
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  const int64_t at = (int64_t)blockIdx.x * K;
+  for (int64_t i = threadIdx.x; i < K / 8; i += kRowThreads)
+    reinterpret_cast<uint4*>(out + at)[unit_place(i)] =
+        __ldg(reinterpret_cast<const uint4*>(x + at) + i);
 }
 
 // rows[pos[t, j]] = token t's activations, for each of its picks that has an
@@ -751,7 +786,7 @@ scatter_rows_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ 
     if constexpr (CODES) {
       float q[8];
       codes8(v, s, inv, a == 0.f, q);
-      v = codes_f16<false>(q);
+      v = codes_f16<kTensorForm>(q);
     }
     for (int j = 0; j < k; ++j) {
       const int at = __ldg(pos + m * k + j);
@@ -761,17 +796,17 @@ scatter_rows_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ 
 }
 
 // ---- launches -----------------------------------------------------------------------
-template <bool STREAM>
+template <QuantForm FORM>
 static cudaError_t launch_quant_rows(const uint16_t* x, const int* head, int64_t rows, int64_t K,
                                      uint16_t* codes, float* scales, cudaStream_t st) {
   // a warp a row where there are rows for every warp of the GPU (32768 x 1280:
   // a block a row leaves most of its threads without work), else a block
   if (rows >= 4096 && K <= 32 * kRowVecs * 8) {
     PdlConfig c(dim3((unsigned)((rows + 3) / 4), 1, 1), kRowThreads, 0, st);
-    return cudaLaunchKernelEx(&c.cfg, quant_rows_kernel<32, STREAM>, x, head, rows, K, codes, scales);
+    return cudaLaunchKernelEx(&c.cfg, quant_rows_kernel<32, FORM>, x, head, rows, K, codes, scales);
   }
   PdlConfig c(dim3((unsigned)rows, 1, 1), kRowThreads, 0, st);
-  return cudaLaunchKernelEx(&c.cfg, quant_rows_kernel<kRowThreads, STREAM>, x, head, rows, K, codes,
+  return cudaLaunchKernelEx(&c.cfg, quant_rows_kernel<kRowThreads, FORM>, x, head, rows, K, codes,
                             scales);
 }
 
@@ -809,7 +844,7 @@ static cudaError_t run_tensor(const ExpertsArgs& a, cudaStream_t st) {
   r.timeout_ns = a.timeout_ns;
   if ((e = launch_ragged(r, st)) != cudaSuccess) return e;
   if (kCodes) {
-    e = launch_quant_rows<false>(a.h, a.plan.head, n, a.I, a.h_q, a.h_s, st);
+    e = launch_quant_rows<kTensorForm>(a.h, a.plan.head, n, a.I, a.h_q, a.h_s, st);
     if (e != cudaSuccess) return e;
   }
   r.gate_up = false;
@@ -832,7 +867,7 @@ static cudaError_t run_few(const ExpertsArgs& a, StreamParams p, cudaStream_t st
   if (e != cudaSuccess) return e;
   if (VARIANT == kW4A8) {
     // (a slot without an expert holds no row: its codes are never read)
-    e = launch_quant_rows<true>(a.h, nullptr, n, a.I, a.h_q, a.h_s, st);
+    e = launch_quant_rows<kStreamPlaced>(a.h, nullptr, n, a.I, a.h_q, a.h_s, st);
     if (e != cudaSuccess) return e;
   }
   p.act = VARIANT == kW4A8 ? a.h_q : a.h;
@@ -855,7 +890,7 @@ static cudaError_t run_stream(const ExpertsArgs& a, StreamParams p, cudaStream_t
   cudaError_t e = cudaLaunchKernelEx(&c.cfg, experts_gate_up_kernel<VARIANT, NT, false>, p);
   if (e != cudaSuccess) return e;
   if (VARIANT == kW4A8) {
-    e = launch_quant_rows<true>(a.h, a.plan.head, n, a.I, a.h_q, a.h_s, st);
+    e = launch_quant_rows<kStreamPlaced>(a.h, a.plan.head, n, a.I, a.h_q, a.h_s, st);
     if (e != cudaSuccess) return e;
   }
   p.act = VARIANT == kW4A8 ? a.h_q : a.h;
@@ -896,7 +931,12 @@ static cudaError_t run_experts(const ExpertsArgs& a, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   if (a.way == kExpertsStream) e = launch_plan(a.ids, n, a.E, 8 * nt, a.plan, st);
   if (e == cudaSuccess && VARIANT == kW4A8)
-    e = launch_quant_rows<true>(a.x, nullptr, a.T, a.H, a.x_q, a.x_s, st);
+    e = launch_quant_rows<kStreamForm>(a.x, nullptr, a.T, a.H, a.x_q, a.x_s, st);
+  if (e == cudaSuccess && VARIANT == kW4A16 && a.way == kExpertsStream) {
+    PdlConfig c(dim3((unsigned)a.T, 1, 1), kRowThreads, 0, st);
+    e = cudaLaunchKernelEx(&c.cfg, place_rows_kernel, a.x, a.H, a.x_q);
+    p.act = a.x_q;
+  }
   if (e != cudaSuccess) return e;
   if (a.way == kExpertsFew) return run_few<VARIANT>(a, p, st);
   return nt == 1   ? run_stream<VARIANT, 1>(a, p, st)
