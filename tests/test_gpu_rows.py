@@ -367,10 +367,9 @@ def test_lora_in_place_odd_ids_and_unused_ranks():
     A, B = ad.A.clone(), ad.B.clone()
     A[:, 5:] = math.nan
     B[:, :, 5:] = math.inf
-    ranks = torch.tensor([5, 5, 0, 5], dtype=torch.int32, device=DEV)
-    odd = eg.LoraAdapters(A, B, ad.scale, ranks)
     for n in (1, 2, 3, 4, 5):
-        odd.ranks = torch.tensor([n, 5, 0, -3], dtype=torch.int32, device=DEV)
+        odd = eg.LoraAdapters(A, B, ad.scale,
+                              torch.tensor([n, 5, 0, -3], dtype=torch.int32, device=DEV))
         got = check_lora(y, x, odd, ids)
         assert torch.isfinite(got.float()).all()
         keep = (ids == 2) | (ids == 3)

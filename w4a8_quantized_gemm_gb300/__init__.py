@@ -451,6 +451,16 @@ def _shape(t: torch.Tensor, *shape):
         raise ValueError(f"tensor of shape {tuple(t.shape)}, expected {shape}")
 
 
+def _arg(t: torch.Tensor, dtype: torch.dtype, *shape) -> int:
+    """The device address of a tensor of this type and shape, after the checks
+    every call makes (in one test: they are on the path of single tokens)."""
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    _dtype(t, dtype)
+    _shape(t, *shape)
+    return _ptr(t)
+
+
 def moe_route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None,
               score: int = SCORE_SOFTMAX, n_group: int = 1, topk_group: int = 1,
               group_score: int = GROUP_MAX, renorm: bool = True, scale: float = 1.0,
@@ -458,23 +468,20 @@ def moe_route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None,
     """The k experts of each token and their weights from router logits [T, E]
     (fp32 or bf16): returns (weights fp32 [T, k], ids int32 [T, k]), the best
     expert first (include/egopq.h has the formulas)."""
-    _dtype(logits, torch.float32, torch.bfloat16)
+    bf16 = logits.dtype is torch.bfloat16
+    if not bf16:
+        _dtype(logits, torch.float32, torch.bfloat16)
     T, E = logits.shape
-    if bias is not None:
-        _dtype(bias, torch.float32)
-        _shape(bias, E)
     if out is None:
         out = (torch.empty((T, k), dtype=torch.float32, device=logits.device),
                torch.empty((T, k), dtype=torch.int32, device=logits.device))
     weights, ids = out
-    _dtype(weights, torch.float32)
-    _dtype(ids, torch.int32)
-    _shape(weights, T, k)
-    _shape(ids, T, k)
-    _check(load().egopq_moe_route(_ptr(logits), logits.dtype == torch.bfloat16, _ptr(bias), T, E, k,
-                                  score, n_group, topk_group, group_score, renorm, scale,
-                                  _ptr(weights), _ptr(ids), _stream(stream)))
-    return weights, ids
+    _check(load().egopq_moe_route(
+        _arg(logits, logits.dtype, T, E), bf16,
+        None if bias is None else _arg(bias, torch.float32, E), T, E, k, score, n_group,
+        topk_group, group_score, renorm, scale, _arg(weights, torch.float32, T, k),
+        _arg(ids, torch.int32, T, k), _stream(stream)))
+    return out
 
 
 class MoeLayer(NamedTuple):
@@ -492,24 +499,22 @@ def moe_pack(gate_up_q: torch.Tensor, gate_up_scale: torch.Tensor, gate_up_zero:
     """Pack the experts of a layer: gate_up uint8 codes [E, 2I, H] (I gate rows,
     then I up rows) with fp16 scales and uint8 zero points [E, 2I, H/128], and
     down codes [E, H, I] with theirs [E, H, I/128]."""
-    _dtype(gate_up_q, torch.uint8)
-    _dtype(gate_up_scale, torch.float16)
-    _dtype(gate_up_zero, torch.uint8)
     E, I2, H = gate_up_q.shape
     I = I2 // 2
     if I2 % 2:
         raise ValueError(f"{I2} gate and up rows: an odd number")
-    _shape(gate_up_scale, E, I2, H // GROUP)
-    _shape(gate_up_zero, E, I2, H // GROUP)
-    _shape(down_q, E, H, I)
-    _shape(down_scale, E, H, I // GROUP)
-    _shape(down_zero, E, H, I // GROUP)
     nbytes = packed_w4_bytes(E * I2, H)
     if nbytes == 0 or I % GROUP:
         raise EgopqError(-2, f"experts with H={H} I={I} are not packable (multiples of 128)")
+    q, s, z = (_arg(gate_up_q, torch.uint8, E, I2, H),
+               _arg(gate_up_scale, torch.float16, E, I2, H // GROUP),
+               _arg(gate_up_zero, torch.uint8, E, I2, H // GROUP))
+    for t, dtype, K in ((down_q, torch.uint8, I), (down_scale, torch.float16, I // GROUP),
+                        (down_zero, torch.uint8, I // GROUP)):
+        _arg(t, dtype, E, H, K)
     packed = torch.empty(nbytes, dtype=torch.uint8, device=gate_up_q.device)
-    _check(load().egopq_moe_pack_gate_up(_ptr(gate_up_q), _ptr(gate_up_scale), _ptr(gate_up_zero),
-                                         E, I, H, GROUP, _ptr(packed), _stream(stream)))
+    _check(load().egopq_moe_pack_gate_up(q, s, z, E, I, H, GROUP, packed.data_ptr(),
+                                         _stream(stream)))
     down = pack_w4(down_q.view(E * H, I), down_scale.view(E * H, I // GROUP),
                    down_zero.view(E * H, I // GROUP), stream=stream)
     return MoeLayer(packed, down, E, H, I)
@@ -534,45 +539,43 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, layer
     """The gated linears of the experts each token picked, summed with its
     weights: x bf16 [T, H], ids int32 and weights fp32 [T, k] -> bf16 [T, H].
     An id outside [0, E) adds nothing."""
-    _dtype(x, torch.bfloat16)
-    _dtype(ids, torch.int32)
-    _dtype(weights, torch.float32)
-    T, H = x.shape
-    k = ids.shape[1]
-    _shape(x, T, layer.H)
-    _shape(ids, T, k)
-    _shape(weights, T, k)
+    gate_up, down, E, H, I = layer
+    T, k = ids.shape
     if out is None:
         out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
-    _dtype(out, torch.bfloat16)
-    _shape(out, T, H)
     if workspace is None:
-        workspace = moe_workspace(T, k, layer.E, H, layer.I, variant, x.device, path)
-    _check(load().egopq_moe_experts(_ptr(x), _ptr(ids), _ptr(weights), _ptr(layer.gate_up),
-                                    _ptr(layer.down), T, k, layer.E, H, layer.I, GROUP, variant,
-                                    _ptr(out), _ptr(workspace), workspace.nbytes, path,
-                                    _stream(stream)))
+        workspace = moe_workspace(T, k, E, H, I, variant, x.device, path)
+    _check(load().egopq_moe_experts(
+        _arg(x, torch.bfloat16, T, H), _arg(ids, torch.int32, T, k),
+        _arg(weights, torch.float32, T, k), gate_up.data_ptr(), down.data_ptr(), T, k, E, H, I,
+        GROUP, variant, _arg(out, torch.bfloat16, T, H), _ptr(workspace), workspace.nbytes, path,
+        _stream(stream)))
     return out
 
 
 class LoraAdapters:
     """The low-rank adapters of one projection: A bf16 [L, r, K], B bf16
     [L, N, r], scale fp32 [L], ranks int32 [L] (adapter a uses its first
-    ranks[a]; None: r everywhere)."""
+    ranks[a]; None: r everywhere). Checked once, here; the tensors stay as they
+    are named (their values may change)."""
+
+    __slots__ = ("A", "B", "scale", "ranks", "L", "r", "K", "N", "_ptrs")
 
     def __init__(self, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor,
                  ranks: Optional[torch.Tensor] = None):
-        _dtype(A, torch.bfloat16)
-        _dtype(B, torch.bfloat16)
-        _dtype(scale, torch.float32)
-        self.L, self.r, self.K = A.shape
-        self.N = B.shape[1]
-        _shape(B, self.L, self.N, self.r)
-        _shape(scale, self.L)
-        if ranks is not None:
-            _dtype(ranks, torch.int32)
-            _shape(ranks, self.L)
-        self.A, self.B, self.scale, self.ranks = A, B, scale, ranks
+        L, r, K = A.shape
+        N = B.shape[1]
+        for t, dtype, shape in ((A, torch.bfloat16, (L, r, K)), (B, torch.bfloat16, (L, N, r)),
+                                (scale, torch.float32, (L,)), (ranks, torch.int32, (L,))):
+            if t is not None:
+                _dtype(t, dtype)
+                _shape(t, *shape)
+        ptrs = (_ptr(A), _ptr(B), _ptr(scale), _ptr(ranks))
+        for name, v in zip(self.__slots__, (A, B, scale, ranks, L, r, K, N, ptrs)):
+            object.__setattr__(self, name, v)
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"LoraAdapters.{name} is fixed: make new adapters")
 
 
 def lora_workspace(M: int, N: int, K: int, adapters: LoraAdapters, device) -> torch.Tensor:
@@ -583,25 +586,19 @@ def lora_workspace(M: int, N: int, K: int, adapters: LoraAdapters, device) -> to
 def lora_add(y: torch.Tensor, x: torch.Tensor, adapters: LoraAdapters, ids: torch.Tensor,
              workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
              stream=None) -> torch.Tensor:
-    """y [M, N] + scale * B_a (A_a x) for each row's adapter a = ids[m] (rows
+    """y [M, N] + scale * B_a (A_a x[m]) for each row's adapter a = ids[m] (rows
     with an id outside [0, L) keep y); bf16. `out` may be y itself."""
-    _dtype(x, torch.bfloat16)
-    _dtype(y, torch.bfloat16)
-    _dtype(ids, torch.int32)
-    a = adapters
+    A, B, scale, ranks = adapters._ptrs
+    L, r, K, N = adapters.L, adapters.r, adapters.K, adapters.N
     M = x.shape[0]
-    _shape(x, M, a.K)
-    _shape(y, M, a.N)
-    _shape(ids, M)
     if out is None:
         out = torch.empty_like(y)
-    _dtype(out, torch.bfloat16)
-    _shape(out, M, a.N)
     if workspace is None:
-        workspace = lora_workspace(M, a.N, a.K, a, x.device)
-    _check(load().egopq_lora_add(_ptr(y), _ptr(x), _ptr(a.A), _ptr(a.B), _ptr(a.scale),
-                                 _ptr(a.ranks), _ptr(ids), M, a.N, a.K, a.L, a.r, _ptr(out),
-                                 _ptr(workspace), workspace.nbytes, _stream(stream)))
+        workspace = lora_workspace(M, N, K, adapters, x.device)
+    _check(load().egopq_lora_add(
+        _arg(y, torch.bfloat16, M, N), _arg(x, torch.bfloat16, M, K), A, B, scale, ranks,
+        _arg(ids, torch.int32, M), M, N, K, L, r,
+        _arg(out, torch.bfloat16, M, N), _ptr(workspace), workspace.nbytes, _stream(stream)))
     return out
 
 
@@ -618,24 +615,19 @@ def w4a8_linear_lora(x: torch.Tensor, packed: torch.Tensor, N: int, adapters: Lo
                      stream=None) -> torch.Tensor:
     """w4a8_linear of x [M, K] and the adapters' update of its output, in one
     call."""
-    _dtype(x, torch.bfloat16)
-    _dtype(ids, torch.int32)
-    a = adapters
-    M, K = x.shape
-    _shape(x, M, a.K)
-    _shape(ids, M)
-    if N != a.N:
-        raise ValueError(f"adapters of {a.N} outputs beside a projection of {N}")
+    A, B, scale, ranks = adapters._ptrs
+    L, r, K = adapters.L, adapters.r, adapters.K
+    M = x.shape[0]
+    if N != adapters.N:
+        raise ValueError(f"adapters of {adapters.N} outputs beside a projection of {N}")
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-    _dtype(out, torch.bfloat16)
-    _shape(out, M, N)
     if workspace is None:
-        workspace = w4a8_linear_lora_workspace(M, N, K, a, x.device, path)
-    _check(load().egopq_w4a8_linear_lora(_ptr(x), _ptr(packed), _ptr(a.A), _ptr(a.B),
-                                         _ptr(a.scale), _ptr(a.ranks), _ptr(ids), M, N, K, GROUP,
-                                         a.L, a.r, _ptr(out), _ptr(workspace), workspace.nbytes,
-                                         path, _stream(stream)))
+        workspace = w4a8_linear_lora_workspace(M, N, K, adapters, x.device, path)
+    _check(load().egopq_w4a8_linear_lora(
+        _arg(x, torch.bfloat16, M, K), _ptr(packed), A, B, scale, ranks,
+        _arg(ids, torch.int32, M), M, N, K, GROUP, L, r, _arg(out, torch.bfloat16, M, N),
+        _ptr(workspace), workspace.nbytes, path, _stream(stream)))
     return out
 
 

@@ -13,19 +13,22 @@
 namespace egopq {
 
 // ---- router ------------------------------------------------------------------
-// One warp a token; expert e lives in lane e % 32, register e / 32. Choices
-// are compared as unsigned keys that keep the order of the floats (0: not to
-// be chosen), so one redux.sync finds a maximum and a second one the lowest
-// index that has it.
+// One warp a token; lane l holds the V experts from V l, so that the lowest lane
+// of a tie has its lowest expert. Choices are compared as unsigned keys that
+// keep the order of the floats (0: not to be chosen). A group whose experts are
+// whole lanes, a power of two of them, is scored by exchanges inside its lanes,
+// others by one lane a group out of shared memory. The weights are formed last,
+// for the picks alone. Bound by the instructions a token takes: 16384 tokens of
+// 256 experts in 8 groups, 8 picks, read 17 MB.
 constexpr int kRouteWarps = 4;
+constexpr int kRouteMaxExperts = 512;
 
 __device__ __forceinline__ uint32_t order_key(float c) {
-  if (c != c) c = -INFINITY;                  // a NaN choice ranks last
   const uint32_t u = __float_as_uint(c + 0.f);  // (-0 + 0 = +0: they tie)
-  return (u >> 31) ? ~u : (u | 0x80000000u);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_value(uint32_t k) {
-  return __uint_as_float((k >> 31) ? (k & 0x7fffffffu) : ~k);
+  return __uint_as_float(k ^ ((uint32_t)((int32_t)~k >> 31) | 0x80000000u));
 }
 
 struct RouteParams {
@@ -35,139 +38,205 @@ struct RouteParams {
   int32_t* ids;
   int64_t T;
   int E, k, n_group, topk_group, per_group;
-  int bf16, sigmoid, top2, renorm;
+  int group_lanes;  // lanes of a group, a power of two; 0: groups are not whole lanes
+  int bf16, vec, sigmoid, top2, renorm;
   float scale;
 };
 
-template <int V>  // registers a lane: E <= 32 * V
+// A logit as a finite number or -inf (an expert masked off): NaN reads as -inf
+// and +inf as the largest finite value.
+__device__ __forceinline__ float clean_logit(float l) {
+  return l != l ? -INFINITY : fminf(l, 3.402823466e38f);
+}
+__device__ __forceinline__ float sigmoid_rn(float l) { return __frcp_rn(1.f + expf(-l)); }
+
+template <int V>
 __global__ void __launch_bounds__(32 * kRouteWarps)
 route_kernel(const RouteParams p) {
+  __shared__ uint32_t group_keys[kRouteWarps][V == 1 ? 32 : 32 * V];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
   if (t >= p.T) return;
+  const int e0 = lane * V;
+  const float* row32 = static_cast<const float*>(p.logits) + t * p.E;
+  const uint16_t* row16 = static_cast<const uint16_t*>(p.logits) + t * p.E;
   float s[V];
-  // logits as finite numbers or -inf (an expert masked off): NaN reads as
-  // -inf and +inf as the largest finite value
+  bool loaded = false;
+  if constexpr (V % 4 == 0) {
+    // whole 16-byte (fp32) or 8-byte (bf16) vectors: E a multiple of 4
+    if (p.vec) {
+      loaded = true;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = i * 32 + lane;
-    float l = -INFINITY;
-    if (e < p.E) {
-      l = p.bf16 ? bf16_bits_to_f32(__ldg(static_cast<const uint16_t*>(p.logits) + t * p.E + e))
-                 : __ldg(static_cast<const float*>(p.logits) + t * p.E + e);
-      if (l != l) l = -INFINITY;
-      l = fminf(l, 3.402823466e38f);
+      for (int i = 0; i < V; i += 4) {
+        float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        if (e0 + i < p.E) {
+          if (p.bf16) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2*>(row16 + e0 + i));
+            v = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
+                            __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
+          } else {
+            v = __ldg(reinterpret_cast<const float4*>(row32 + e0 + i));
+          }
+        }
+        s[i] = v.x;
+        s[i + 1] = v.y;
+        s[i + 2] = v.z;
+        s[i + 3] = v.w;
+      }
     }
-    s[i] = l;
   }
-  uint32_t key[V];
-  float inv_sum = 1.f, mx = 0.f;
+  if (!loaded) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      s[i] = -INFINITY;
+      if (e0 + i < p.E) s[i] = p.bf16 ? bf16_bits_to_f32(__ldg(row16 + e0 + i)) : __ldg(row32 + e0 + i);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) s[i] = clean_logit(s[i]);
+  float mx = 0.f, inv_sum = 1.f;
+  // the softmax without a bias chooses by the logits, whose order it keeps
+  // (groups by their two best: by the scores, which are added)
+  const bool by_score = p.bias || p.top2;
   if (p.sigmoid) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) s[i] = __fdiv_rn(1.f, 1.f + expf(-s[i]));
+    for (int i = 0; i < V; ++i) s[i] = sigmoid_rn(s[i]);
   } else {
-    // the softmax keeps its logits until the weights are formed: without a
-    // bias they are the choice (the softmax keeps their order)
     mx = s[0];
 #pragma unroll
     for (int i = 1; i < V; ++i) mx = fmaxf(mx, s[i]);
     mx = key_value(__reduce_max_sync(0xffffffffu, order_key(mx)));
     if (mx == -INFINITY) mx = 0.f;  // every expert masked off: scores of zero
-    float sum = 0.f;
+    float sum = 0.f, ex[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum += expf(s[i] - mx);
+    for (int i = 0; i < V; ++i) {
+      ex[i] = expf(s[i] - mx);
+      sum += ex[i];
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     inv_sum = sum > 0.f ? __fdiv_rn(1.f, sum) : 0.f;
-    if (p.bias || p.top2) {
+    if (by_score) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) s[i] = expf(s[i] - mx) * inv_sum;
+      for (int i = 0; i < V; ++i) s[i] = ex[i] * inv_sum;
     }
   }
-  const bool by_logit = !p.sigmoid && !(p.bias || p.top2);
+  uint32_t key[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int e = i * 32 + lane;
     key[i] = 0;
-    if (e < p.E) key[i] = order_key(p.bias ? s[i] + __ldg(p.bias + e) : s[i]);
+    if (e0 + i < p.E) {
+      float c = s[i];
+      if (p.bias) {
+        c += __ldg(p.bias + e0 + i);
+        if (c != c) c = -INFINITY;  // a NaN choice ranks last
+      }
+      key[i] = order_key(c);
+    }
   }
   if (p.topk_group < p.n_group) {
-    // lane g gets group g's score
-    uint32_t gkey = 0;
-    for (int g = 0; g < p.n_group; ++g) {
-      const int lo = g * p.per_group, hi = lo + p.per_group;
-      uint32_t m1 = 0, m2 = 0;
+    // a group's score from its largest key and, for the two best, the second
+    // (0: there is none)
+    auto score_of = [&](uint32_t m1, uint32_t m2) {
+      return p.top2 && m2 ? order_key(key_value(m1) + key_value(m2)) : m1;
+    };
+    uint32_t m1 = 0, m2 = 0;
+    if (p.group_lanes) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int e = i * 32 + lane;
-        const uint32_t kk = (e >= lo && e < hi) ? key[i] : 0u;
-        m2 = max(m2, min(m1, kk));
-        m1 = max(m1, kk);
+        m2 = max(m2, min(m1, key[i]));
+        m1 = max(m1, key[i]);
       }
-      const uint32_t best = __reduce_max_sync(0xffffffffu, m1);
-      uint32_t gk = best;
-      if (p.top2) {
-        // the second best: of the best's first holder its own second, of the
-        // other lanes their first
-        const int holder = __ffs(__ballot_sync(0xffffffffu, m1 == best)) - 1;
-        const uint32_t second = __reduce_max_sync(0xffffffffu, lane == holder ? m2 : m1);
-        const float sum = second ? key_value(best) + key_value(second) : key_value(best);
-        gk = order_key(sum);
+      for (int o = 1; o < p.group_lanes; o <<= 1) {
+        const uint32_t o1 = __shfl_xor_sync(0xffffffffu, m1, o);
+        const uint32_t o2 = __shfl_xor_sync(0xffffffffu, m2, o);
+        m2 = max(max(m2, o2), min(m1, o1));
+        m1 = max(m1, o1);
       }
-      if (lane == g) gkey = gk;
-    }
-    uint32_t keep = 0;
-    for (int j = 0; j < p.topk_group; ++j) {
-      const uint32_t best = __reduce_max_sync(0xffffffffu, gkey);
-      const int g = __ffs(__ballot_sync(0xffffffffu, gkey == best)) - 1;
-      keep |= 1u << g;
-      if (lane == g) gkey = 0;
-    }
+      const uint32_t mine = score_of(m1, m2);
+      // my group is kept if fewer than topk_group groups are better (or as good
+      // and lower)
+      const int g = lane / p.group_lanes;
+      int better = 0;
+      for (int q = 0; q < p.n_group; ++q) {
+        const uint32_t other = __shfl_sync(0xffffffffu, mine, q * p.group_lanes);
+        better += other > mine || (other == mine && q < g);
+      }
+      if (better >= p.topk_group) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = i * 32 + lane;
-      if (e < p.E && !((keep >> (e / p.per_group)) & 1)) key[i] = 0;
+        for (int i = 0; i < V; ++i) key[i] = 0;
+      }
+    } else {
+      uint32_t* keys = group_keys[warp];
+#pragma unroll
+      for (int i = 0; i < V; ++i) keys[e0 + i] = key[i];
+      __syncwarp();
+      uint32_t mine = 0;  // lane g: group g's score
+      if (lane < p.n_group) {
+        for (int i = 0; i < p.per_group; ++i) {
+          const uint32_t kk = keys[lane * p.per_group + i];
+          m2 = max(m2, min(m1, kk));
+          m1 = max(m1, kk);
+        }
+        mine = score_of(m1, m2);
+      }
+      int better = 0;
+      for (int q = 0; q < p.n_group; ++q) {
+        const uint32_t other = __shfl_sync(0xffffffffu, mine, q);
+        better += other > mine || (other == mine && q < lane);
+      }
+      const uint32_t keep =
+          __ballot_sync(0xffffffffu, lane < p.n_group && better < p.topk_group);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (e0 + i < p.E && !((keep >> ((e0 + i) / p.per_group)) & 1)) key[i] = 0;
     }
   }
-  float my_w = 0.f;
   int my_id = 0;
   for (int j = 0; j < p.k; ++j) {
     uint32_t best = key[0];
-    int bi = 0;
-    float bs = s[0];
 #pragma unroll
-    for (int i = 1; i < V; ++i) {
-      if (key[i] > best) {
-        best = key[i];
-        bi = i;
-        bs = s[i];
-      }
-    }
+    for (int i = 1; i < V; ++i) best = max(best, key[i]);
     const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-    const unsigned e = best == top ? (unsigned)(bi * 32 + lane) : 0xffffffffu;
-    const unsigned win = __reduce_min_sync(0xffffffffu, e);
-    const float ws = __shfl_sync(0xffffffffu, bs, win & 31);
-    if (lane == j) {
-      my_w = ws;
-      my_id = (int)win;
-    }
+    const int who = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
+    int at = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if ((unsigned)(i * 32 + lane) == win) key[i] = 0;
+    for (int i = V - 1; i >= 0; --i)
+      if (key[i] == top) at = i;
+    if (lane == who) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i == at) key[i] = 0;
+    }
+    const int id = who * V + __shfl_sync(0xffffffffu, at, who);
+    if (lane == j) my_id = id;
   }
-  if (by_logit && lane < p.k) my_w = expf(my_w - mx) * inv_sum;
+  float w = 0.f;
+  if (lane < p.k) {
+    const float l = clean_logit(p.bf16 ? bf16_bits_to_f32(__ldg(row16 + my_id)) : __ldg(row32 + my_id));
+    w = p.sigmoid ? sigmoid_rn(l) : expf(l - mx) * inv_sum;
+  }
   if (p.renorm) {
-    float sum = lane < p.k ? my_w : 0.f;
+    float sum = w;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    my_w = __fdiv_rn(my_w, sum + 1e-20f);
+    w = __fdiv_rn(w, sum + 1e-20f);
   }
   if (lane < p.k) {
-    p.weights[t * p.k + lane] = my_w * p.scale;
+    p.weights[t * p.k + lane] = w * p.scale;
     p.ids[t * p.k + lane] = my_id;
   }
+}
+
+template <int V>
+static cudaError_t launch_route_v(RouteParams p, cudaStream_t st) {
+  const int lanes = p.per_group % V ? 0 : p.per_group / V;
+  p.group_lanes = lanes && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+  PdlConfig c(dim3((unsigned)((p.T + kRouteWarps - 1) / kRouteWarps), 1, 1), 32 * kRouteWarps, 0,
+              st);
+  return cudaLaunchKernelEx(&c.cfg, route_kernel<V>, p);
 }
 
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t st) {
@@ -182,24 +251,20 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t st) {
   p.n_group = a.n_group;
   p.topk_group = a.topk_group;
   p.per_group = a.E / a.n_group;
+  p.group_lanes = 0;
   p.bf16 = a.bf16;
+  p.vec = a.E % 4 == 0;
   p.sigmoid = a.sigmoid;
   p.top2 = a.top2;
   p.renorm = a.renorm;
   p.scale = a.scale;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.T + kRouteWarps - 1) / kRouteWarps), 1, 1);
-  cfg.blockDim = dim3(32 * kRouteWarps, 1, 1);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (a.E <= 64) return cudaLaunchKernelEx(&cfg, route_kernel<2>, p);
-  if (a.E <= 128) return cudaLaunchKernelEx(&cfg, route_kernel<4>, p);
-  if (a.E <= 256) return cudaLaunchKernelEx(&cfg, route_kernel<8>, p);
-  return cudaLaunchKernelEx(&cfg, route_kernel<16>, p);
+  if (a.E <= 32) return launch_route_v<1>(p, st);
+  if (a.E <= 64) return launch_route_v<2>(p, st);
+  if (a.E <= 128) return launch_route_v<4>(p, st);
+  // (160 experts in 8 groups of 20 are four whole lanes a group at five a lane)
+  if (a.E <= 160 && p.per_group % 5 == 0) return launch_route_v<5>(p, st);
+  if (a.E <= 256) return launch_route_v<8>(p, st);
+  return launch_route_v<16>(p, st);
 }
 
 // ---- plan ----------------------------------------------------------------------
