@@ -317,11 +317,13 @@ struct LoraArgs {
   RowPlan plan;
   float* h;  // [lora_splits][M][r] partial sums of A x, sorted rows
 };
-// Whether M rows take the one-launch form (no plan, no workspace); else the rows
-// of a tile and the parts K is split into.
+// Whether M rows run without a plan (and without a workspace); else the rows of
+// a tile.
 bool lora_few(int64_t M);
 int lora_tile();
-int lora_splits(int64_t M, int64_t K, int L);
+// Parts of K whose sums of A x lie in memory between two kernels (0: one
+// kernel does both products).
+int lora_splits(int64_t M, int64_t K);
 cudaError_t launch_lora(const LoraArgs& a, cudaStream_t st);
 
 // Weights [E][2I][K] with I gate rows and then I up rows a set, packed with

@@ -6,12 +6,11 @@
 // A [L][r][K], B [L][N][r] bf16; adapter a uses its first ranks[a] rows of A
 // (columns of B). A row with ids outside [0, L) keeps y0.
 //
-// Up to 128 rows (decode) take one launch: a cluster of CTAs an adapter (and
-// slab of columns) finds its rows in the ids alone, splits K for A x, adds the
-// parts through distributed shared memory and splits the columns for the
-// product with B. More rows are sorted by adapter (RowPlan) and take two
-// kernels with A x in memory between them. Every sum is added in a fixed
-// order, so results do not depend on timing.
+// One kernel: a cluster of CTAs takes up to 32 rows of one adapter, splits K for
+// A x, adds the parts through distributed shared memory in rank order and
+// splits the columns for the product with B. Up to 128 rows (decode) the
+// cluster finds its rows in the ids alone; more rows are sorted by adapter
+// first (RowPlan). Results do not depend on timing.
 //
 // All products run on mma.m16n8k16 with fragments loaded straight from memory:
 // the order of K inside a fragment is free as long as both operands share it,
@@ -31,9 +30,10 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
 
 constexpr int kLoraWarps = 8;
 constexpr int kLoraThreads = 32 * kLoraWarps;
-constexpr int kLoraTile = 32;     // rows of a tile of the two kernels
+constexpr int kLoraTile = 32;      // rows of a tile of a planned batch
 constexpr int kLoraMaxRank = 128;
-constexpr int kLoraFewRows = 128;  // rows of a one-launch batch
+constexpr int kLoraFewRows = 128;  // rows of a batch without a plan
+constexpr int kLoraManyRows = 1024;  // a batch of more takes two kernels
 constexpr int kLoraCluster = 8;
 constexpr int kHsLd = kLoraMaxRank + 8;  // padded row of the bf16 A x in shared memory (16-byte rows)
 
@@ -46,12 +46,12 @@ struct LoraParams {
   const int32_t* ranks;
   const int32_t* ids;
   uint16_t* y_out;
-  float* h;  // [splits][M][r]
   const int* head;
   const int4* tiles;
   const int32_t* order;
+  float* h;  // [splits][M][r] partial sums of A x, sorted rows (two kernels)
   int64_t M, N, K;
-  int L, r, splits;
+  int L, r, slabs, splits;
 };
 
 // ranks[a] as a number in [0, r]
@@ -96,17 +96,18 @@ __device__ __forceinline__ uint4 add_row(const uint4& v, const float (&acc)[4][4
   const uint32_t q[4] = {v.x, v.y, v.z, v.w};
   uint32_t o[4];
 #pragma unroll
-  for (int t = 0; t < 4; ++t)
-    o[t] = (uint32_t)f32_to_bf16_bits(__uint_as_float(q[t] << 16) + acc[t][2 * half]) |
-           ((uint32_t)f32_to_bf16_bits(__uint_as_float(q[t] & 0xFFFF0000u) + acc[t][2 * half + 1])
-            << 16);
+  for (int t = 0; t < 4; ++t) {
+    const __nv_bfloat162 r =
+        __floats2bfloat162_rn(__uint_as_float(q[t] << 16) + acc[t][2 * half],
+                              __uint_as_float(q[t] & 0xFFFF0000u) + acc[t][2 * half + 1]);
+    o[t] = *reinterpret_cast<const uint32_t*>(&r);
+  }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // Eight ranks of B (a thread's: j .. j + 7) without those past the adapter's
 // rank, which meet zeros of h but may hold anything.
 __device__ __forceinline__ uint4 keep_ranks(uint4 v, int j, int rank) {
-  if (j + 8 <= rank) return v;
   uint32_t q[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -116,74 +117,95 @@ __device__ __forceinline__ uint4 keep_ranks(uint4 v, int j, int rank) {
 
 // y_out = bf16(y_in + hs B^T) for a tile's rows (16 MT of them; `rows` live,
 // row_of(i) names row i of y) over 32-column chunks first, first + step, ...
-// below `last`. Column c of a chunk's n8-tile t is column (c / 2) * 8 + 2t +
-// c % 2 of it, so that a thread's sums over the four tiles are eight
-// neighbouring columns of y: one 16-byte access a row. A thread holds eight
-// ranks a step of 32, as hs has them. The next chunk's y and first 32 ranks of
-// B are on their way while a chunk is computed.
-template <int MT, typename RowOf>
-__device__ __forceinline__ void expand_chunks(const uint16_t* y_in, uint16_t* y_out, int64_t N,
-                                              const uint16_t (*hs)[kHsLd], const uint16_t* Bset,
-                                              int r, int rank, int rows, RowOf row_of,
-                                              int64_t first, int64_t last, int64_t step) {
-  const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+// below `last`; JS = ceil(r / 32). Column c of a chunk's n8-tile t is column
+// (c / 2) * 8 + 2t + c % 2 of it, so that a thread's sums over the four tiles
+// are eight neighbouring columns of y: one 16-byte access a row. A thread holds
+// eight ranks a step of 32, as hs has them. begin() puts the first chunk's y
+// and B on their way (before hs is known), and every register of them is loaded
+// again for the next chunk as soon as this one has used it.
+template <int MT, int JS>
+struct Expand {
+  const uint16_t* y_in;
+  uint16_t* y_out;
+  const uint16_t* Bt;
   int64_t at[2 * MT];  // this thread's place in its rows of y, -1: no row
-#pragma unroll
-  for (int i = 0; i < 2 * MT; ++i)
-    at[i] = i * 8 + gid < rows ? (int64_t)row_of(i * 8 + gid) * N + 8 * tig : -1;
-  const uint16_t* Bt = Bset + (int64_t)((gid >> 1) * 8 + (gid & 1)) * r + 8 * tig;
-  uint4 yn[2 * MT], bn[4];
-  auto fetch_b = [&](int64_t c, int j0, uint4 (&b)[4]) {
-    const uint16_t* src = Bt + c * 32 * r + j0;
-    const bool in = j0 + 8 * tig < rank;  // (r is a multiple of 8)
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-      b[t] = in ? __ldg(reinterpret_cast<const uint4*>(src + 2 * t * r)) : make_uint4(0, 0, 0, 0);
-  };
-  auto fetch = [&](int64_t c) {
+  int r, rank, rows;
+  uint4 y[2 * MT], b[JS][4];
+
+  template <typename RowOf>
+  __device__ __forceinline__ Expand(const LoraParams& p, const uint16_t* Bset, int rank_, int rows_,
+                                    RowOf row_of)
+      : y_in(p.y_in), y_out(p.y_out), r(p.r), rank(rank_), rows(rows_) {
+    const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
 #pragma unroll
     for (int i = 0; i < 2 * MT; ++i)
-      if (at[i] >= 0) yn[i] = *reinterpret_cast<const uint4*>(y_in + at[i] + c * 32);
-    fetch_b(c, 0, bn);
-  };
-  if (first < last) fetch(first);
-  for (int64_t c = first; c < last; c += step) {
-    uint4 y[2 * MT], b[4];
+      at[i] = i * 8 + gid < rows ? (int64_t)row_of(i * 8 + gid) * p.N + 8 * tig : -1;
+    Bt = Bset + (int64_t)((gid >> 1) * 8 + (gid & 1)) * r + 8 * tig;
 #pragma unroll
-    for (int i = 0; i < 2 * MT; ++i) y[i] = yn[i];
+    for (int js = 0; js < JS; ++js)
 #pragma unroll
-    for (int t = 0; t < 4; ++t) b[t] = bn[t];
-    if (c + step < last) fetch(c + step);
-    float acc[MT][4][4];
+      for (int t = 0; t < 4; ++t) b[js][t] = make_uint4(0, 0, 0, 0);  // (ranks never loaded)
+  }
+  __device__ __forceinline__ void fetch_b(int64_t c, int js) {
+    const uint16_t* src = Bt + c * 32 * r + js * 32;
+    if (js * 32 + 8 * (int)(threadIdx.x & 3) < rank) {  // (r is a multiple of 8)
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+      for (int t = 0; t < 4; ++t) b[js][t] = __ldg(reinterpret_cast<const uint4*>(src + 2 * t * r));
+    }
+  }
+  __device__ __forceinline__ void fetch_y(int64_t c, int i) {
+    if (at[i] >= 0) y[i] = *reinterpret_cast<const uint4*>(y_in + at[i] + c * 32);
+  }
+  __device__ __forceinline__ void begin(int64_t first, int64_t last) {
+    if (first >= last) return;
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+    for (int i = 0; i < 2 * MT; ++i) fetch_y(first, i);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) acc[m][t][q] = 0.f;
-    for (int j0 = 0; j0 < rank; j0 += 32) {
-      if (j0 > 0) fetch_b(c, j0, b);
-      const int j = j0 + 8 * tig;
+    for (int js = 0; js < JS; ++js) fetch_b(first, js);
+  }
+  __device__ __forceinline__ void run(const uint16_t (*hs)[kHsLd], int64_t first, int64_t last,
+                                      int64_t step) {
+    const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+    for (int64_t c = first; c < last; c += step) {
+      const bool more = c + step < last;
+      float acc[MT][4][4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) b[t] = keep_ranks(b[t], j, rank);
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        if (m * 16 >= rows) break;
-        const uint4 a0 = *reinterpret_cast<const uint4*>(&hs[m * 16 + gid][j]);
-        const uint4 a1 = *reinterpret_cast<const uint4*>(&hs[m * 16 + gid + 8][j]);
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          mma_bf16(acc[m][t], a0.x, a1.x, a0.y, a1.y, b[t].x, b[t].y);
-          mma_bf16(acc[m][t], a0.z, a1.z, a0.w, a1.w, b[t].z, b[t].w);
+          for (int q = 0; q < 4; ++q) acc[m][t][q] = 0.f;
+#pragma unroll
+      for (int js = 0; js < JS; ++js) {
+        if (js * 32 >= rank) break;
+        const int j = js * 32 + 8 * tig;
+        if (rank & 7) {
+#pragma unroll
+          for (int t = 0; t < 4; ++t) b[js][t] = keep_ranks(b[js][t], j, rank);
         }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          if (m * 16 >= rows) break;
+          const uint4 a0 = *reinterpret_cast<const uint4*>(&hs[m * 16 + gid][j]);
+          const uint4 a1 = *reinterpret_cast<const uint4*>(&hs[m * 16 + gid + 8][j]);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const uint4 bb = b[js][t];
+            mma_bf16(acc[m][t], a0.x, a1.x, a0.y, a1.y, bb.x, bb.y);
+            mma_bf16(acc[m][t], a0.z, a1.z, a0.w, a1.w, bb.z, bb.w);
+          }
+        }
+        if (more) fetch_b(c + step, js);
+      }
+#pragma unroll
+      for (int i = 0; i < 2 * MT; ++i) {
+        if (at[i] >= 0)
+          *reinterpret_cast<uint4*>(y_out + at[i] + c * 32) = add_row(y[i], acc[i >> 1], i & 1);
+        if (more) fetch_y(c + step, i);
       }
     }
-#pragma unroll
-    for (int i = 0; i < 2 * MT; ++i)
-      if (at[i] >= 0)
-        *reinterpret_cast<uint4*>(y_out + at[i] + c * 32) = add_row(y[i], acc[i >> 1], i & 1);
   }
-}
+};
 
 template <int MT, int NT>
 __device__ __forceinline__ void zero_acc(float (&acc)[MT][NT][4]) {
@@ -195,70 +217,93 @@ __device__ __forceinline__ void zero_acc(float (&acc)[MT][NT][4]) {
       for (int q = 0; q < 4; ++q) acc[m][t][q] = 0.f;
 }
 
-// ---- few rows: one launch ------------------------------------------------------------
-// Cluster (slab, adapter b): 8 CTAs. CTA c sums A x over its eighth of K for
-// up to 16 rows of the b-th adapter in the batch, takes the other parts through
-// distributed shared memory in rank order, scales and rounds h once (bf16, the
-// operand of the product: relative 2^-8 of the update at most, below the
-// rounding of y itself where the update is no larger than y) and updates its
-// columns. The slab's part of B is asked into L2 before A x is summed, so that
-// its trip from HBM runs beside it. Latency-bound: one row of 3584 x 3584 at
-// rank 16 reads 0.25 MB.
-template <int NR>
-__global__ void __launch_bounds__(kLoraThreads)
-lora_few_kernel(const LoraParams p) {
-  __shared__ uint32_t seen[kMaxSets / 32];
-  __shared__ int rows_of[kLoraFewRows];
+// ---- the kernel ------------------------------------------------------------------------
+__device__ __forceinline__ void st_dsmem_u16(uint32_t addr, uint16_t v) {
+  asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
+}
+
+// Cluster (tile, slab): 8 CTAs. CTA c sums A x over its eighth of K for up to
+// 16 MT rows of one adapter, takes an eighth of the (row, rank) sums from all
+// parts through distributed shared memory, scales them, rounds them once to
+// bf16 (the operand of the product with B: relative 2^-8 of the update at most,
+// below the rounding of y itself where the update is no larger than y) and
+// gives them to all eight; then every CTA updates its columns. B's part is
+// asked into L2 before A x is summed, so that its trip from HBM runs beside
+// it. A slab is a range of columns; each slab sums A x again.
+// Few rows are bound by latency (one row of 3584 x 3584 at rank 16 reads
+// 0.25 MB), many by y0 and y.
+template <int NR, int MT, int JS, bool PLAN>
+__global__ void __launch_bounds__(kLoraThreads, MT == 1 && NR <= 4 ? 3 : 2)
+lora_kernel(const LoraParams p) {
+  constexpr int kRows = 16 * MT, kRed = 8 * NR + 1;
+  extern __shared__ float red[];  // [kLoraWarps][kRows][kRed]
+  __shared__ float part[kRows][JS * 32];
+  __shared__ __align__(16) uint16_t hs[kRows][kHsLd];
+  __shared__ uint32_t seen[PLAN ? 1 : kMaxSets / 32];
+  __shared__ int rows_of[PLAN ? kRows : kLoraFewRows];
   __shared__ int n_rows_s;
-  __shared__ float red[kLoraWarps][16][8 * NR + 1];
-  __shared__ float part[16][kLoraMaxRank];
-  __shared__ __align__(16) uint16_t hs[16][kHsLd];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
-  const int M = (int)p.M, words = (p.L + 31) / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
-  for (int i = threadIdx.x; i < words; i += kLoraThreads) seen[i] = 0;
-  __syncthreads();
-  if ((int)threadIdx.x < M) {
-    const int v = __ldg(p.ids + threadIdx.x);
-    if (v >= 0 && v < p.L) atomicOr(&seen[v >> 5], 1u << (v & 31));
-  }
-  __syncthreads();
-  // the b-th adapter of the batch (its bit, counted from below); one past the
-  // last: the rows without an adapter
-  int b = blockIdx.y, w = 0;
-  while (w < words && b >= __popc(seen[w])) b -= __popc(seen[w++]);
-  const bool none = w == words;
-  if (none && (b > 0 || p.y_in == p.y_out)) return;  // (the whole cluster)
-  int set = -1;
-  if (!none) {
-    uint32_t m = seen[w];
-    for (; b > 0; --b) m &= m - 1;
-    set = w * 32 + __ffs(m) - 1;
-  }
-  // its rows, in order
-  if (warp == 0) {
-    int n = 0;
-    for (int i0 = 0; i0 < M; i0 += 32) {
-      const int i = i0 + lane;
-      int v = i < M ? __ldg(p.ids + i) : -2;
-      if (i < M && (v < 0 || v >= p.L)) v = -1;
-      const uint32_t hit = __ballot_sync(0xffffffffu, i < M && v == set);
-      if ((hit >> lane) & 1) rows_of[n + __popc(hit & ((1u << lane) - 1))] = i;
-      n += __popc(hit);
-    }
-    if (lane == 0) n_rows_s = n;
-  }
-  __syncthreads();
-  const int n_rows = n_rows_s;
   const int rank_c = (int)cluster_ctarank();
-  const int slab = blockIdx.x / kLoraCluster, slabs = gridDim.x / kLoraCluster;
+  const int number = (int)(blockIdx.x / kLoraCluster);
+  const int slab = number % p.slabs;
+  int b = number / p.slabs;  // the tile, or the adapter's number in the batch
+  // the adapter (-1: rows without one, which are copied) and its rows, in order
+  int set = -1, n_rows = 0;
+  if constexpr (PLAN) {
+    int4 tile;
+    if (b < p.head[1]) {
+      tile = __ldg(p.tiles + b);
+      set = tile.x;
+    } else {
+      const int64_t first = p.head[0] + (int64_t)(b - p.head[1]) * kRows;
+      tile = make_int4(-1, (int)first, (int)max((int64_t)0, min((int64_t)kRows, p.M - first)), 0);
+    }
+    n_rows = tile.z;
+    if (n_rows == 0 || (set < 0 && p.y_in == p.y_out)) return;  // (the whole cluster)
+    if ((int)threadIdx.x < n_rows) rows_of[threadIdx.x] = __ldg(p.order + tile.y + threadIdx.x);
+  } else {
+    const int M = (int)p.M, words = (p.L + 31) / 32;
+    for (int i = threadIdx.x; i < words; i += kLoraThreads) seen[i] = 0;
+    __syncthreads();
+    if ((int)threadIdx.x < M) {
+      const int v = __ldg(p.ids + threadIdx.x);
+      if (v >= 0 && v < p.L) atomicOr(&seen[v >> 5], 1u << (v & 31));
+    }
+    __syncthreads();
+    // the b-th adapter of the batch (its bit, counted from below); one past the
+    // last: the rows without an adapter
+    int w = 0;
+    while (w < words && b >= __popc(seen[w])) b -= __popc(seen[w++]);
+    if (w == words) {
+      if (b > 0 || p.y_in == p.y_out) return;  // (the whole cluster)
+    } else {
+      uint32_t m = seen[w];
+      for (; b > 0; --b) m &= m - 1;
+      set = w * 32 + __ffs(m) - 1;
+    }
+    if (warp == 0) {
+      int n = 0;
+      for (int i0 = 0; i0 < M; i0 += 32) {
+        const int i = i0 + lane;
+        int v = i < M ? __ldg(p.ids + i) : -2;
+        if (i < M && (v < 0 || v >= p.L)) v = -1;
+        const uint32_t hit = __ballot_sync(0xffffffffu, i < M && v == set);
+        if ((hit >> lane) & 1) rows_of[n + __popc(hit & ((1u << lane) - 1))] = i;
+        n += __popc(hit);
+      }
+      if (lane == 0) n_rows_s = n;
+    }
+  }
+  __syncthreads();
+  if constexpr (!PLAN) n_rows = n_rows_s;
   // this CTA's columns, 32 at a time
-  const int64_t chunks = p.N / 32, parts = (int64_t)slabs * kLoraCluster;
+  const int64_t chunks = p.N / 32, parts = (int64_t)p.slabs * kLoraCluster;
   const int64_t me = (int64_t)slab * kLoraCluster + rank_c;
   const int64_t c_lo = me * chunks / parts, c_hi = (me + 1) * chunks / parts;
-  if (none) {
+  if (set < 0) {
     for (int i = 0; i < n_rows; ++i) {
       const int64_t at = (int64_t)rows_of[i] * p.N;
       for (int64_t v = c_lo * 4 + threadIdx.x; v < c_hi * 4; v += kLoraThreads)
@@ -279,61 +324,69 @@ lora_few_kernel(const LoraParams p) {
   const int steps = (int)(p.K / 32);
   const int s0 = rank_c * steps / kLoraCluster, s1 = (rank_c + 1) * steps / kLoraCluster;
   const uint16_t* Ab = p.A + (int64_t)set * p.r * p.K + 8 * tig;
-  for (int t0 = 0; t0 < n_rows; t0 += 16) {
-    const int rows = min(16, n_rows - t0);
-    const uint16_t* xr[2];
+  for (int t0 = 0; t0 < n_rows; t0 += kRows) {
+    const int rows = min(kRows, n_rows - t0);
+    {
+      const uint16_t* xr[2 * MT];
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
-      xr[q] = gid + 8 * q < rows ? p.x + (int64_t)rows_of[t0 + gid + 8 * q] * p.K + 8 * tig
-                                 : nullptr;
-    for (int c0 = 0; c0 < rank; c0 += 8 * NR) {
-      float acc[1][NR][4];
-      zero_acc<1, NR>(acc);
-      shrink_steps<1, NR>(acc, xr, Ab, p.K, c0, rank, s0 + warp, s1, kLoraWarps);
+      for (int q = 0; q < 2 * MT; ++q)
+        xr[q] = gid + 8 * q < rows ? p.x + (int64_t)rows_of[t0 + gid + 8 * q] * p.K + 8 * tig
+                                   : nullptr;
+      for (int c0 = 0; c0 < rank; c0 += 8 * NR) {
+        float acc[MT][NR][4];
+        zero_acc<MT, NR>(acc);
+        shrink_steps<MT, NR>(acc, xr, Ab, p.K, c0, rank, s0 + warp, s1, kLoraWarps);
+        float* mine = red + warp * kRows * kRed;
 #pragma unroll
-      for (int t = 0; t < NR; ++t)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          red[warp][(q >> 1) * 8 + gid][t * 8 + tig * 2 + (q & 1)] = acc[0][t][q];
-      __syncthreads();
-      for (int i = threadIdx.x; i < rows * 8 * NR; i += kLoraThreads) {
-        const int j = i % (8 * NR), row = i / (8 * NR);
-        if (c0 + j < rank) {
+          for (int t = 0; t < NR; ++t)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              mine[(m * 16 + (q >> 1) * 8 + gid) * kRed + t * 8 + tig * 2 + (q & 1)] =
+                  acc[m][t][q];
+        __syncthreads();
+        for (int i = threadIdx.x; i < rows * 8 * NR; i += kLoraThreads) {
+          const int j = i % (8 * NR), row = i / (8 * NR);
           float v = 0.f;
 #pragma unroll
-          for (int k = 0; k < kLoraWarps; ++k) v += red[k][row][j];
-          part[row][c0 + j] = v;
+          for (int k = 0; k < kLoraWarps; ++k) v += red[(k * kRows + row) * kRed + j];
+          if (c0 + j < JS * 32) part[row][c0 + j] = v;
         }
+        __syncthreads();
       }
-      __syncthreads();
     }
-    cluster_sync_all();  // every CTA's part is in its shared memory
+    cluster_sync_all();  // every CTA's part is in its shared memory, and hs is free
+    // an eighth of the rows' sums, in fours of ranks to a thread's row
     const int kr = (rank + 31) & ~31;
-    const uint32_t local = smem_u32(part);
-    for (int i = threadIdx.x; i < 16 * kr; i += kLoraThreads) {
+    const uint32_t part_at = smem_u32(part), hs_at = smem_u32(hs);
+    for (int i = rank_c * kLoraThreads + threadIdx.x; i < kRows * kr;
+         i += kLoraCluster * kLoraThreads) {
       const int row = i / kr, j = i - row * kr;
       float v = 0.f;
       if (row < rows && j < rank) {
-        const uint32_t at = local + (uint32_t)(row * kLoraMaxRank + j) * 4;
+        const uint32_t at = part_at + (uint32_t)(row * JS * 32 + j) * 4;
         float q[kLoraCluster];
 #pragma unroll
         for (int c = 0; c < kLoraCluster; ++c) q[c] = ld_dsmem_f32(map_to_rank(at, c));
 #pragma unroll
         for (int c = 0; c < kLoraCluster; ++c) v += q[c];
       }
-      hs[row][j] = f32_to_bf16_bits(sc * v);
+      const uint16_t h = f32_to_bf16_bits(sc * v);
+      const uint32_t to = hs_at + (uint32_t)(row * kHsLd + j) * 2;
+#pragma unroll
+      for (int c = 0; c < kLoraCluster; ++c) st_dsmem_u16(map_to_rank(to, c), h);
     }
-    cluster_sync_all();  // (also the block's barrier) parts may be rewritten, CTAs may leave
-    expand_chunks<1>(p.y_in, p.y_out, p.N, hs, Bset, p.r, rank, rows,
-                     [&](int i) { return rows_of[t0 + i]; }, c_lo + warp, c_hi, kLoraWarps);
-    __syncthreads();  // hs is rewritten for the next rows
+    Expand<MT, JS> ex(p, Bset, rank, rows, [&](int i) { return rows_of[t0 + i]; });
+    ex.begin(c_lo + warp, c_hi);
+    cluster_sync_all();  // (also the block's barrier) hs is whole; nothing remote follows
+    ex.run(hs, c_lo + warp, c_hi, kLoraWarps);
   }
 }
 
-// ---- many rows: two kernels -----------------------------------------------------------
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(live ? 16 : 0)
+// ---- very many rows: two kernels with A x between them in memory ------------------------
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
 
@@ -344,7 +397,7 @@ __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, 
 // their sums to shared memory in turn. x is read once; A_a comes from L2, once
 // a tile.
 constexpr int kShrinkWarps = 4;
-constexpr int kShrinkStages = 4;
+constexpr int kShrinkStages = 3;
 
 template <int NR>
 __global__ void __launch_bounds__(32 * kShrinkWarps)
@@ -364,28 +417,34 @@ lora_shrink_kernel(const LoraParams p) {
   const int s0 = (int)((int64_t)blockIdx.y * steps / p.splits) + warp;
   const int s1 = (int)((int64_t)(blockIdx.y + 1) * steps / p.splits);
   const uint16_t* xr[4];
-  bool live[4];
+  uint32_t x_bytes[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int row = q * 8 + gid;
-    live[q] = row < tile.z;
-    xr[q] = p.x + (live[q] ? (int64_t)__ldg(p.order + tile.y + row) * p.K : 0) + 8 * tig;
+    x_bytes[q] = row < tile.z ? 16u : 0u;
+    xr[q] = p.x + (row < tile.z ? (int64_t)__ldg(p.order + tile.y + row) * p.K : 0) + 8 * tig;
   }
   uint8_t* mine = ring + warp * kShrinkStages * kStep;
   const uint32_t mine_at = smem_u32(mine) + lane * 16;
+  // (a row without a rank or a token is read from row 0 and its bytes dropped)
   const uint16_t* Ab = p.A + (int64_t)tile.x * p.r * p.K + 8 * tig;
   for (int c0 = 0; c0 < rank; c0 += 8 * NR) {
+    const uint16_t* ar[NR];
+    uint32_t a_bytes[NR];
+#pragma unroll
+    for (int t = 0; t < NR; ++t) {
+      const int j = c0 + t * 8 + gid;
+      a_bytes[t] = j < rank ? 16u : 0u;
+      ar[t] = Ab + (int64_t)(j < rank ? j : 0) * p.K;
+    }
     auto issue = [&](int s, int stage) {
       if (s < s1) {
         const uint32_t st = mine_at + stage * kStep;
+        const uint32_t off = (uint32_t)s * 32;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) cp_async16_zfill(st + q * 512, xr[q] + (int64_t)s * 32, live[q]);
+        for (int q = 0; q < 4; ++q) cp_async16_zfill(st + q * 512, xr[q] + off, x_bytes[q]);
 #pragma unroll
-        for (int t = 0; t < NR; ++t) {
-          const int j = c0 + t * 8 + gid;
-          cp_async16_zfill(st + (4 + t) * 512, Ab + (int64_t)(j < rank ? j : 0) * p.K + s * 32,
-                           j < rank);
-        }
+        for (int t = 0; t < NR; ++t) cp_async16_zfill(st + (4 + t) * 512, ar[t] + off, a_bytes[t]);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -439,11 +498,12 @@ lora_shrink_kernel(const LoraParams p) {
 
 // y = bf16(y0 + scale * B_a h). One CTA a tile of 32 rows and 512 columns, every
 // fourth 32 of them a warp; the tile's h (the splits added in order, scaled,
-// rounded to bf16 once: see lora_few_kernel) lies in shared memory. Bound by y0
+// rounded to bf16 once: see lora_kernel) lies in shared memory. Bound by y0
 // and y: 2 x 29 MB at 4093 x 3584.
 constexpr int kExpandWarps = 4;
 constexpr int kExpandChunks = 16;
 
+template <int JS>
 __global__ void __launch_bounds__(32 * kExpandWarps)
 lora_expand_kernel(const LoraParams p) {
   __shared__ __align__(16) uint16_t hs[kLoraTile][kHsLd];
@@ -464,37 +524,60 @@ lora_expand_kernel(const LoraParams p) {
     if (first >= p.M || p.y_in == p.y_out) return;
     tile = make_int4(0, (int)first, (int)min((int64_t)kLoraTile, p.M - first), 0);
   }
+  const int64_t c0 = (int64_t)blockIdx.y * kExpandChunks;
+  const int64_t c1 = min(c0 + kExpandChunks, p.N / 32);
+  Expand<2, JS> ex(p, p.B + (int64_t)tile.x * p.N * p.r, rank, tile.z,
+                   [&](int i) { return __ldg(p.order + tile.y + i); });
+  ex.begin(c0 + warp, c1);
   if (rank > 0) {
+    // a thread takes four ranks of a row: every load of its parts is on its way
+    // before the first is used (r is a multiple of 8)
     const float sc = __ldg(p.scale + tile.x);
-    const int kr = (rank + 31) & ~31;
-    for (int i = threadIdx.x; i < kLoraTile * kr; i += 32 * kExpandWarps) {
-      const int row = i / kr, j = i - row * kr;
-      float v = 0.f;
-      if (row < tile.z && j < rank)
-        for (int s = 0; s < p.splits; ++s)
-          v += p.h[((int64_t)s * p.M + tile.y + row) * p.r + j];
-      hs[row][j] = f32_to_bf16_bits(sc * v);
+    constexpr int kVec = JS * 8;  // fours of ranks in a row of hs
+    constexpr int kEach = kLoraTile * kVec / (32 * kExpandWarps);
+    float4 v[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < p.splits; ++s) {
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        const int i = threadIdx.x + e * 32 * kExpandWarps, row = i / kVec, j = i % kVec * 4;
+        if (row < tile.z && j < rank) {
+          const float4 q = *reinterpret_cast<const float4*>(
+              p.h + ((int64_t)s * p.M + tile.y + row) * p.r + j);
+          v[e].x += q.x;
+          v[e].y += q.y;
+          v[e].z += q.z;
+          v[e].w += q.w;
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = threadIdx.x + e * 32 * kExpandWarps, row = i / kVec, j = i % kVec * 4;
+      // (ranks past the adapter's were never written: leave them out)
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(j < rank ? sc * v[e].x : 0.f,
+                                                      j + 1 < rank ? sc * v[e].y : 0.f);
+      const __nv_bfloat162 hi = __floats2bfloat162_rn(j + 2 < rank ? sc * v[e].z : 0.f,
+                                                      j + 3 < rank ? sc * v[e].w : 0.f);
+      *reinterpret_cast<uint2*>(&hs[row][j]) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     }
   }
   __syncthreads();
-  const int64_t c0 = (int64_t)blockIdx.y * kExpandChunks;
-  const int64_t c1 = min(c0 + kExpandChunks, p.N / 32);
-  expand_chunks<2>(p.y_in, p.y_out, p.N, hs, p.B + (int64_t)tile.x * p.N * p.r, p.r, rank, tile.z,
-                   [&](int i) { return __ldg(p.order + tile.y + i); }, c0 + warp, c1,
-                   kExpandWarps);
+  ex.run(hs, c0 + warp, c1, kExpandWarps);
 }
 
 bool lora_few(int64_t M) { return M <= kLoraFewRows; }
 
 int lora_tile() { return kLoraTile; }
 
-int lora_splits(int64_t M, int64_t K, int L) {
+int lora_splits(int64_t M, int64_t K) {
+  if (M <= kLoraManyRows) return 0;
   // parts of K so that about two CTAs an SM run, each of two steps a warp or more
-  const int64_t tiles = M / kLoraTile + (L < M ? L : M);
-  int64_t s = 304 / (tiles > 0 ? tiles : 1);
+  int64_t s = 304 / (M / kLoraTile + 1);
   const int64_t most = K / (64 * kShrinkWarps);
   if (s > most) s = most;
-  if (s > 8) s = 8;
   return s < 1 ? 1 : (int)s;
 }
 
@@ -508,6 +591,32 @@ static cudaError_t launch_shrink(const LoraParams& p, int64_t tiles, cudaStream_
   return cudaLaunchKernelEx(&c.cfg, lora_shrink_kernel<NR>, p);
 }
 
+template <int NR, int MT, int JS, bool PLAN>
+static cudaError_t launch_lora_kernel(const LoraParams& p, int64_t clusters, cudaStream_t st) {
+  constexpr size_t kSmem = (size_t)kLoraWarps * 16 * MT * (8 * NR + 1) * 4;
+  auto kern = lora_kernel<NR, MT, JS, PLAN>;
+  static SmemOptIn opt_in;
+  if (cudaError_t e = opt_in.ensure(kern, kSmem); e != cudaSuccess) return e;
+  PdlConfig c(dim3((unsigned)(clusters * kLoraCluster), 1, 1), kLoraThreads, kSmem, st);
+  cudaLaunchAttribute attr[2];
+  attr[0] = c.attr[0];
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kLoraCluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  c.cfg.attrs = attr;
+  c.cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&c.cfg, kern, p);
+}
+
+template <int MT, bool PLAN>
+static cudaError_t launch_lora_rank(const LoraParams& p, int64_t clusters, cudaStream_t st) {
+  return p.r <= 16   ? launch_lora_kernel<2, MT, 1, PLAN>(p, clusters, st)
+         : p.r <= 32 ? launch_lora_kernel<4, MT, 1, PLAN>(p, clusters, st)
+         : p.r <= 64 ? launch_lora_kernel<8, MT, 2, PLAN>(p, clusters, st)
+                     : launch_lora_kernel<8, MT, 4, PLAN>(p, clusters, st);
+}
+
 cudaError_t launch_lora(const LoraArgs& a, cudaStream_t st) {
   LoraParams p;
   p.y_in = a.y_in;
@@ -518,7 +627,6 @@ cudaError_t launch_lora(const LoraArgs& a, cudaStream_t st) {
   p.ranks = a.ranks;
   p.ids = a.ids;
   p.y_out = a.y_out;
-  p.h = a.h;
   p.head = a.plan.head;
   p.tiles = a.plan.tiles;
   p.order = a.plan.order;
@@ -527,42 +635,34 @@ cudaError_t launch_lora(const LoraArgs& a, cudaStream_t st) {
   p.K = a.K;
   p.L = a.L;
   p.r = a.r;
-  p.splits = 1;
+  const bool few = lora_few(a.M);
+  // (the rows without an adapter make at most ceil(M / 32) tiles more)
   const int64_t sets = a.L < a.M ? a.L : a.M;
-  if (lora_few(a.M)) {
-    // column slabs: enough clusters for two CTAs an SM, none under 2048 columns
-    // (each slab sums A x again)
-    int64_t slabs = (a.N + 2047) / 2048;
-    const int64_t want = (38 + sets - 1) / sets;
-    if (slabs > want) slabs = want;
-    PdlConfig c(dim3((unsigned)(slabs * kLoraCluster), (unsigned)(sets + 1), 1), kLoraThreads, 0,
-                st);
-    cudaLaunchAttribute attr[2];
-    attr[0] = c.attr[0];
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = kLoraCluster;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    c.cfg.attrs = attr;
-    c.cfg.numAttrs = 2;
-    return a.r <= 16   ? cudaLaunchKernelEx(&c.cfg, lora_few_kernel<2>, p)
-           : a.r <= 32 ? cudaLaunchKernelEx(&c.cfg, lora_few_kernel<4>, p)
-                       : cudaLaunchKernelEx(&c.cfg, lora_few_kernel<8>, p);
-  }
-  p.splits = lora_splits(a.M, a.K, a.L);
+  const int64_t work = few ? sets : a.M / kLoraTile + 1;  // clusters that multiply, about
+  const int64_t most =
+      few ? sets + 1 : plan_max_tiles(a.M, a.L, kLoraTile) + (a.M + kLoraTile - 1) / kLoraTile;
+  // column slabs: enough clusters for two CTAs an SM, none under 2048 columns
+  int64_t slabs = (a.N + 2047) / 2048;
+  const int64_t want = (38 + work - 1) / work;
+  if (slabs > want) slabs = want;
+  p.slabs = (int)slabs;
+  if (most * slabs * kLoraCluster >= (1LL << 31)) return cudaErrorNotSupported;
+  if (few) return launch_lora_rank<1, false>(p, most * slabs, st);
   cudaError_t e = launch_plan(a.ids, a.M, a.L, kLoraTile, a.plan, st);
   if (e != cudaSuccess) return e;
+  p.splits = lora_splits(a.M, a.K);
+  if (p.splits == 0) return launch_lora_rank<2, true>(p, most * slabs, st);
+  p.h = a.h;
   const int64_t tiles = plan_max_tiles(a.M, a.L, kLoraTile);
   e = a.r <= 16   ? launch_shrink<2>(p, tiles, st)
       : a.r <= 32 ? launch_shrink<4>(p, tiles, st)
                   : launch_shrink<8>(p, tiles, st);
   if (e != cudaSuccess) return e;
-  // (the rows without an adapter make at most ceil(M / 32) tiles more)
-  const int64_t grid = tiles + (a.M + kLoraTile - 1) / kLoraTile;
-  PdlConfig c(dim3((unsigned)grid,
-                   (unsigned)((a.N / 32 + kExpandChunks - 1) / kExpandChunks), 1),
+  PdlConfig c(dim3((unsigned)most, (unsigned)((a.N / 32 + kExpandChunks - 1) / kExpandChunks), 1),
               32 * kExpandWarps, 0, st);
-  return cudaLaunchKernelEx(&c.cfg, lora_expand_kernel, p);
+  return a.r <= 32   ? cudaLaunchKernelEx(&c.cfg, lora_expand_kernel<1>, p)
+         : a.r <= 64 ? cudaLaunchKernelEx(&c.cfg, lora_expand_kernel<2>, p)
+                     : cudaLaunchKernelEx(&c.cfg, lora_expand_kernel<4>, p);
 }
 
 }  // namespace egopq

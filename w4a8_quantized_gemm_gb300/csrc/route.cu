@@ -21,7 +21,6 @@ namespace egopq {
 // for the picks alone. Bound by the instructions a token takes: 16384 tokens of
 // 256 experts in 8 groups, 8 picks, read 17 MB.
 constexpr int kRouteWarps = 4;
-constexpr int kRouteMaxExperts = 512;
 
 __device__ __forceinline__ uint32_t order_key(float c) {
   const uint32_t u = __float_as_uint(c + 0.f);  // (-0 + 0 = +0: they tie)

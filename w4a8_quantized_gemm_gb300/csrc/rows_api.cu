@@ -65,7 +65,7 @@ size_t carve_lora(void* ws, LoraArgs& a) {
     return c.used;
   }
   carve_plan(c, a.plan, a.M, a.L, plan_max_tiles(a.M, a.L, lora_tile()), false);
-  a.h = c.take<float>((int64_t)lora_splits(a.M, a.K, a.L) * a.M * a.r);
+  a.h = c.take<float>(lora_splits(a.M, a.K) * a.M * a.r);
   return c.used;
 }
 
@@ -283,6 +283,8 @@ int egopq_lora_add(const uint16_t* y_in, const uint16_t* x_bf16, const uint16_t*
     return fail(EGOPQ_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
   if ((rc = check_arch())) return rc;
   cudaError_t e = launch_lora(a, (cudaStream_t)stream);
+  if (e == cudaErrorNotSupported)
+    return fail(EGOPQ_ERR_UNSUPPORTED_SHAPE, "too many rows for one call (M=%lld)", (long long)M);
   return e == cudaSuccess ? EGOPQ_OK : cuda_fail(e, "lora_add launch");
 }
 
