@@ -320,7 +320,7 @@ struct LoraArgs {
 // Whether M rows run without a plan (and without a workspace); else the rows of
 // a tile.
 bool lora_few(int64_t M);
-int lora_tile();
+int lora_tile(int64_t M);
 // Parts of K whose sums of A x lie in memory between two kernels (0: one
 // kernel does both products).
 int lora_splits(int64_t M, int64_t K);

@@ -33,7 +33,8 @@ constexpr int kLoraThreads = 32 * kLoraWarps;
 constexpr int kLoraTile = 32;      // rows of a tile of a planned batch
 constexpr int kLoraMaxRank = 128;
 constexpr int kLoraFewRows = 128;  // rows of a batch without a plan
-constexpr int kLoraManyRows = 1024;  // a batch of more takes two kernels
+constexpr int kLoraManyRows = 1024;  // a batch of more takes two kernels, of
+constexpr int kManyTile = 128;       // tiles of so many rows
 constexpr int kLoraCluster = 8;
 constexpr int kHsLd = kLoraMaxRank + 8;  // padded row of the bf16 A x in shared memory (16-byte rows)
 
@@ -407,9 +408,14 @@ lora_shrink_kernel(const LoraParams p) {
   __shared__ float red[kLoraTile][8 * NR + 1];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
-  if ((int)blockIdx.x >= p.head[1]) return;
-  const int4 tile = __ldg(p.tiles + blockIdx.x);
-  if (tile.z == 0) return;
+  constexpr int kSub = kManyTile / kLoraTile;
+  const int number = (int)(blockIdx.x / kSub);
+  if (number >= p.head[1]) return;
+  int4 tile = __ldg(p.tiles + number);
+  const int skip = (int)(blockIdx.x % kSub) * kLoraTile;
+  tile.y += skip;
+  tile.z = min(kLoraTile, tile.z - skip);
+  if (tile.z <= 0) return;
   const int rank = adapter_rank(p, tile.x);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
@@ -496,21 +502,23 @@ lora_shrink_kernel(const LoraParams p) {
   }
 }
 
-// y = bf16(y0 + scale * B_a h). One CTA a tile of 32 rows and 512 columns, every
-// fourth 32 of them a warp; the tile's h (the splits added in order, scaled,
-// rounded to bf16 once: see lora_kernel) lies in shared memory. Bound by y0
-// and y: 2 x 29 MB at 4093 x 3584.
-constexpr int kExpandWarps = 4;
-constexpr int kExpandChunks = 16;
+// y = bf16(y0 + scale * B_a h). One CTA a tile of 128 rows and 256 columns, 32 a
+// warp, whose part of B stays in registers (32 JS ranks at a time) while the
+// rows go by, sixteen at a time, three sixteens of y on their way; the tile's h
+// (the splits added in order, scaled, rounded to bf16 once: see lora_kernel)
+// lies in shared memory. Bound by y0 and y: 2 x 29 MB at 4093 x 3584.
+constexpr int kExpandAhead = 3;
 
 template <int JS>
-__global__ void __launch_bounds__(32 * kExpandWarps)
+__global__ void __launch_bounds__(kLoraThreads, 2)
 lora_expand_kernel(const LoraParams p) {
-  __shared__ __align__(16) uint16_t hs[kLoraTile][kHsLd];
+  constexpr int LD = JS * 32 + 8;  // padded row of h: 16-byte rows, no bank conflicts
+  __shared__ __align__(16) uint16_t hs[kManyTile][LD];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   const int n_tiles = p.head[1];
-  const int warp = threadIdx.x >> 5;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gid = lane >> 2, tig = lane & 3;
   int4 tile;
   int rank = 0;
   if ((int)blockIdx.x < n_tiles) {
@@ -520,57 +528,124 @@ lora_expand_kernel(const LoraParams p) {
   } else {
     // tiles past the table copy the rows without an adapter, which the plan
     // lists last (nothing to do where y is updated in place)
-    const int64_t first = p.head[0] + (int64_t)((int)blockIdx.x - n_tiles) * kLoraTile;
+    const int64_t first = p.head[0] + (int64_t)((int)blockIdx.x - n_tiles) * kManyTile;
     if (first >= p.M || p.y_in == p.y_out) return;
-    tile = make_int4(0, (int)first, (int)min((int64_t)kLoraTile, p.M - first), 0);
+    tile = make_int4(0, (int)first, (int)min((int64_t)kManyTile, p.M - first), 0);
   }
-  const int64_t c0 = (int64_t)blockIdx.y * kExpandChunks;
-  const int64_t c1 = min(c0 + kExpandChunks, p.N / 32);
-  Expand<2, JS> ex(p, p.B + (int64_t)tile.x * p.N * p.r, rank, tile.z,
-                   [&](int i) { return __ldg(p.order + tile.y + i); });
-  ex.begin(c0 + warp, c1);
-  if (rank > 0) {
-    // a thread takes four ranks of a row: every load of its parts is on its way
-    // before the first is used (r is a multiple of 8)
-    const float sc = __ldg(p.scale + tile.x);
-    constexpr int kVec = JS * 8;  // fours of ranks in a row of hs
-    constexpr int kEach = kLoraTile * kVec / (32 * kExpandWarps);
-    float4 v[kEach];
+  const int64_t c = (int64_t)blockIdx.y * kLoraWarps + warp;  // this warp's 32 columns
+  const bool in = c * 32 < p.N;
+  // B: column n of n8-tile t is column (n / 2) * 8 + 2t + n % 2 of the warp's,
+  // so that a thread's sums over the four tiles are eight neighbouring columns
+  // of y; eight ranks a thread and step of 32, as hs has them
+  uint4 b[JS][4];
+  {
+    const uint16_t* src = p.B + ((int64_t)tile.x * p.N + c * 32 + (gid >> 1) * 8 + (gid & 1)) * p.r;
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < p.splits; ++s) {
+    for (int js = 0; js < JS; ++js) {
+      const int j = js * 32 + 8 * tig;
 #pragma unroll
-      for (int e = 0; e < kEach; ++e) {
-        const int i = threadIdx.x + e * 32 * kExpandWarps, row = i / kVec, j = i % kVec * 4;
-        if (row < tile.z && j < rank) {
-          const float4 q = *reinterpret_cast<const float4*>(
-              p.h + ((int64_t)s * p.M + tile.y + row) * p.r + j);
-          v[e].x += q.x;
-          v[e].y += q.y;
-          v[e].z += q.z;
-          v[e].w += q.w;
-        }
+      for (int t = 0; t < 4; ++t) {
+        b[js][t] = make_uint4(0, 0, 0, 0);
+        if (in && j < rank) b[js][t] = __ldg(reinterpret_cast<const uint4*>(src + 2 * t * p.r + j));
       }
     }
+    if (rank & 7) {
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-      const int i = threadIdx.x + e * 32 * kExpandWarps, row = i / kVec, j = i % kVec * 4;
-      // (ranks past the adapter's were never written: leave them out)
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(j < rank ? sc * v[e].x : 0.f,
-                                                      j + 1 < rank ? sc * v[e].y : 0.f);
-      const __nv_bfloat162 hi = __floats2bfloat162_rn(j + 2 < rank ? sc * v[e].z : 0.f,
-                                                      j + 3 < rank ? sc * v[e].w : 0.f);
-      *reinterpret_cast<uint2*>(&hs[row][j]) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      for (int js = 0; js < JS; ++js)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) b[js][t] = keep_ranks(b[js][t], js * 32 + 8 * tig, rank);
+    }
+  }
+  // y of sixteen rows: this thread's two, a negative place where there is none
+  int64_t at[kExpandAhead][2];
+  uint4 y[kExpandAhead][2];
+  auto fetch = [&](int m, int slot) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int row = m * 16 + half * 8 + gid;
+      at[slot][half] = in && row < tile.z
+                           ? (int64_t)__ldg(p.order + tile.y + row) * p.N + c * 32 + 8 * tig
+                           : -1;
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+      if (at[slot][half] >= 0)
+        y[slot][half] = *reinterpret_cast<const uint4*>(p.y_in + at[slot][half]);
+  };
+#pragma unroll
+  for (int m = 0; m < kExpandAhead; ++m) fetch(m, m);
+  if (rank > 0) {
+    // a thread takes four ranks of a row (r is a multiple of 8)
+    const float sc = __ldg(p.scale + tile.x);
+    constexpr int kVec = JS * 8;  // fours of ranks in a row of hs
+    constexpr int kEach = kManyTile * kVec / kLoraThreads;
+    constexpr int kBatch = kEach < 4 ? kEach : 4;  // loads on their way at once
+    for (int e0 = 0; e0 < kEach; e0 += kBatch) {
+      float4 v[kBatch];
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int s = 0; s < p.splits; ++s) {
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          const int i = threadIdx.x + (e0 + e) * kLoraThreads, row = i / kVec, j = i % kVec * 4;
+          if (row < tile.z && j < rank) {
+            const float4 q = *reinterpret_cast<const float4*>(
+                p.h + ((int64_t)s * p.M + tile.y + row) * p.r + j);
+            v[e].x += q.x;
+            v[e].y += q.y;
+            v[e].z += q.z;
+            v[e].w += q.w;
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        const int i = threadIdx.x + (e0 + e) * kLoraThreads, row = i / kVec, j = i % kVec * 4;
+        // (ranks past the adapter's were never written: leave them out)
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(j < rank ? sc * v[e].x : 0.f,
+                                                        j + 1 < rank ? sc * v[e].y : 0.f);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(j + 2 < rank ? sc * v[e].z : 0.f,
+                                                        j + 3 < rank ? sc * v[e].w : 0.f);
+        *reinterpret_cast<uint2*>(&hs[row][j]) = make_uint2(
+            *reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      }
     }
   }
   __syncthreads();
-  ex.run(hs, c0 + warp, c1, kExpandWarps);
+  const int m_end = (tile.z + 15) / 16;
+  for (int m0 = 0; m0 < m_end; m0 += kExpandAhead) {
+#pragma unroll
+    for (int slot = 0; slot < kExpandAhead; ++slot) {
+      const int m = m0 + slot;
+      if (m >= m_end) break;
+      float acc[4][4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[t][q] = 0.f;
+#pragma unroll
+      for (int js = 0; js < JS; ++js) {
+        if (js * 32 >= rank) break;
+        const uint4 a0 = *reinterpret_cast<const uint4*>(&hs[m * 16 + gid][js * 32 + 8 * tig]);
+        const uint4 a1 = *reinterpret_cast<const uint4*>(&hs[m * 16 + gid + 8][js * 32 + 8 * tig]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          mma_bf16(acc[t], a0.x, a1.x, a0.y, a1.y, b[js][t].x, b[js][t].y);
+          mma_bf16(acc[t], a0.z, a1.z, a0.w, a1.w, b[js][t].z, b[js][t].w);
+        }
+      }
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+        if (at[slot][half] >= 0)
+          *reinterpret_cast<uint4*>(p.y_out + at[slot][half]) = add_row(y[slot][half], acc, half);
+      if (m + kExpandAhead < m_end) fetch(m + kExpandAhead, slot);
+    }
+  }
 }
 
 bool lora_few(int64_t M) { return M <= kLoraFewRows; }
 
-int lora_tile() { return kLoraTile; }
+int lora_tile(int64_t M) { return M > kLoraManyRows ? kManyTile : kLoraTile; }
 
 int lora_splits(int64_t M, int64_t K) {
   if (M <= kLoraManyRows) return 0;
@@ -636,11 +711,11 @@ cudaError_t launch_lora(const LoraArgs& a, cudaStream_t st) {
   p.L = a.L;
   p.r = a.r;
   const bool few = lora_few(a.M);
-  // (the rows without an adapter make at most ceil(M / 32) tiles more)
+  // (the rows without an adapter make at most ceil(M / tile) tiles more)
   const int64_t sets = a.L < a.M ? a.L : a.M;
   const int64_t work = few ? sets : a.M / kLoraTile + 1;  // clusters that multiply, about
-  const int64_t most =
-      few ? sets + 1 : plan_max_tiles(a.M, a.L, kLoraTile) + (a.M + kLoraTile - 1) / kLoraTile;
+  const int bt = lora_tile(a.M);
+  const int64_t most = few ? sets + 1 : plan_max_tiles(a.M, a.L, bt) + (a.M + bt - 1) / bt;
   // column slabs: enough clusters for two CTAs an SM, none under 2048 columns
   int64_t slabs = (a.N + 2047) / 2048;
   const int64_t want = (38 + work - 1) / work;
@@ -648,18 +723,17 @@ cudaError_t launch_lora(const LoraArgs& a, cudaStream_t st) {
   p.slabs = (int)slabs;
   if (most * slabs * kLoraCluster >= (1LL << 31)) return cudaErrorNotSupported;
   if (few) return launch_lora_rank<1, false>(p, most * slabs, st);
-  cudaError_t e = launch_plan(a.ids, a.M, a.L, kLoraTile, a.plan, st);
+  cudaError_t e = launch_plan(a.ids, a.M, a.L, bt, a.plan, st);
   if (e != cudaSuccess) return e;
   p.splits = lora_splits(a.M, a.K);
   if (p.splits == 0) return launch_lora_rank<2, true>(p, most * slabs, st);
   p.h = a.h;
-  const int64_t tiles = plan_max_tiles(a.M, a.L, kLoraTile);
+  const int64_t tiles = plan_max_tiles(a.M, a.L, bt) * (kManyTile / kLoraTile);
   e = a.r <= 16   ? launch_shrink<2>(p, tiles, st)
       : a.r <= 32 ? launch_shrink<4>(p, tiles, st)
                   : launch_shrink<8>(p, tiles, st);
   if (e != cudaSuccess) return e;
-  PdlConfig c(dim3((unsigned)most, (unsigned)((a.N / 32 + kExpandChunks - 1) / kExpandChunks), 1),
-              32 * kExpandWarps, 0, st);
+  PdlConfig c(dim3((unsigned)most, (unsigned)((a.N + 255) / 256), 1), kLoraThreads, 0, st);
   return a.r <= 32   ? cudaLaunchKernelEx(&c.cfg, lora_expand_kernel<1>, p)
          : a.r <= 64 ? cudaLaunchKernelEx(&c.cfg, lora_expand_kernel<2>, p)
                      : cudaLaunchKernelEx(&c.cfg, lora_expand_kernel<4>, p);
