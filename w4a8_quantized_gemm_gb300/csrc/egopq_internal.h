@@ -257,8 +257,11 @@ cudaError_t launch_plan(const int32_t* ids, int64_t n, int S, int bt, const RowP
 
 // How a call's products run (experts.cu).
 enum ExpertsWay { kExpertsFew, kExpertsStream, kExpertsTensor };
-// (AUTO: the tcgen05 products from more than kStreamRows picks an expert)
-constexpr int64_t kStreamRows = 48;
+// (AUTO: the tcgen05 products from more than kStreamRows picks an expert;
+// 64 experts, 8 picks, 3584 x 1280, W4A16: 10 picks an expert 174 us streamed
+// and 172 on the tensor cores, 12.5 picks 188 and 174; 32 experts, 4 picks,
+// 2048 x 1024: 10 picks 51 and 60, 18.8 picks 69 and 61)
+constexpr int64_t kStreamRows = 12;
 ExpertsWay experts_way(int64_t T, int k, int E, int path);
 
 // Experts: one call's operands and workspace parts, validated by the ABI layer.
@@ -277,25 +280,26 @@ struct ExpertsArgs {
   uint16_t* x_q;   // x [T][H] in the streaming products' form: fp16 codes and
                    // their scales (W4A8, few and stream), bf16 (W4A16, stream)
   float* x_s;
-  uint16_t* rows;  // activations in sorted order [T*k][H], bf16 or fp16 codes (tensor)
-  float* rows_s;   // their scales (W4A8, tensor)
+  uint16_t* rows;  // activations in sorted order [T*k][H], fp16 (tensor), and
+  float* rows_s;   // their scales
   uint16_t* h;     // bf16 [T*k][I]
-  uint16_t* h_q;   // its fp16 codes, and their scales (W4A8)
+  uint16_t* h_q;   // fp16 codes of h and their scales (W4A8, and tensor)
   float* h_s;
   void* y;         // [T*k][H], fp32 (stream) or bf16 (tensor)
   uint64_t timeout_ns;
 };
 cudaError_t launch_experts(const ExpertsArgs& a, cudaStream_t st);
-// One tcgen05 product over sorted rows: kGateUp (h = silu(g) * u) or the down
+// One tcgen05 product over sorted rows: h = silu(gate) * up, or the down
 // projection.
 struct RaggedArgs {
-  int variant;
   bool gate_up;
+  bool exact;           // gate and up: every group's sum exact (tc_experts.cu)
+  bool wide;            // tiles of 128 rows (exact: 192), else 64
   int64_t rows_max;     // rows of `act` (T * k)
   int64_t N, K;         // weight rows and columns of one set
   int E;
-  const void* act;      // fp16 codes or bf16 [rows_max][K], sorted rows
-  const float* a_s;     // scales of the sorted rows (W4A8)
+  const uint16_t* act;  // fp16 [rows_max][K], sorted rows
+  const float* a_s;     // scales of the sorted rows
   const uint8_t* packed;
   uint16_t* y;
   RowPlan plan;

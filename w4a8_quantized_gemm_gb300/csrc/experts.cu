@@ -12,7 +12,7 @@
 //           themselves, every CTA finds the picked experts in the ids alone,
 //           and the down product sums over the experts in registers: no plan,
 //           no per-pick output
-//   stream  rows sorted by expert (RowPlan), tiles of up to 32 rows of one
+//   stream  rows sorted by expert (RowPlan), tiles of up to 16 rows of one
 //   tensor  the tcgen05 products of tc_experts.cu over sorted rows
 #include "egopq_internal.h"
 
@@ -350,7 +350,7 @@ __device__ __forceinline__ int few_slot(const uint32_t (&m)[4], int t, int T, in
 
 // ---- h = silu(G x) * (U x) -----------------------------------------------------------
 template <int VARIANT, int NT, bool FEW>
-__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 5 : (NT == 2 ? 4 : 2))
+__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 5 : 4)
 experts_gate_up_kernel(const StreamParams p) {
   constexpr int LD = 8 * NT + 1;  // padded row of the partial sums
   static_assert(kWarps * kStages * kStageBytes >= kWarps * 32 * LD * 4, "sums reuse the ring");
@@ -436,7 +436,7 @@ experts_gate_up_kernel(const StreamParams p) {
 
 // ---- y = D h, a sorted row at a time ----------------------------------------------------
 template <int VARIANT, int NT>
-__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 5 : (NT == 2 ? 4 : 2))
+__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 5 : 4)
 experts_down_kernel(const StreamParams p) {
   constexpr int LD = 8 * NT + 1;
   __shared__ __align__(128) uint8_t ring[kWarps][kStages * kStageBytes];
@@ -660,8 +660,25 @@ combine_kernel(const Y* __restrict__ y, const float* __restrict__ weights,
 // absmax / 127, fp32 quotient rounded half to even) as exact fp16 numbers: the
 // integers themselves (tensor), or every second pair of them divided by 16, the
 // form the streaming products' operand words ask for, in the order of
-// unit_place, which their input may have already (kStreamPlaced) or not.
-enum QuantForm { kTensorForm, kStreamForm, kStreamPlaced };
+// unit_place, which their input may have already (kStreamPlaced) or not. The
+// tensor products take W4A16's activations as fp16 as well: kPowerForm is the
+// bf16 value over a power of two that brings the row's largest to [2^14, 2^15).
+enum QuantForm { kTensorForm, kStreamForm, kStreamPlaced, kPowerForm };
+
+// A row's scale from its largest magnitude.
+template <QuantForm FORM>
+__device__ __forceinline__ float row_scale(float a) {
+  if constexpr (FORM == kPowerForm) {
+    // 2^(exponent of a - 14), at least 2^-100 (so that its inverse is a number:
+    // smaller rows lose bits below 2^-124); 1 for a row of zeros, infinities or
+    // NaNs
+    const int e = (int)(__float_as_uint(a) >> 23);
+    if (a == 0.f || e == 255) return 1.f;
+    return __uint_as_float((uint32_t)max(e - 14, 27) << 23);
+  } else {
+    return __fdiv_rn(a, 127.0f);
+  }
+}
 __device__ __forceinline__ float absmax8(const uint4& v, float m) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -671,25 +688,33 @@ __device__ __forceinline__ float absmax8(const uint4& v, float m) {
   }
   return m;
 }
-__device__ __forceinline__ void codes8(const uint4& v, float s, float inv, bool zero, float (&q)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    q[2 * j] = zero ? 0.f : quant_code(__uint_as_float(w[j] << 16), s, inv);
-    q[2 * j + 1] = zero ? 0.f : quant_code(__uint_as_float(w[j] & 0xFFFF0000u), s, inv);
-  }
-}
+// Eight values of a row of scale s (inv: its inverse for the form, 0 in a row
+// of zeros) as eight fp16.
 template <QuantForm FORM>
-__device__ __forceinline__ uint4 codes_f16(const float (&q)[8]) {
+__device__ __forceinline__ uint4 row_f16(const uint4& v, float s, float inv, bool zero) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t o[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float f = FORM != kTensorForm && (j & 1) ? 0.0625f : 1.f;
-    const __half2 h = __floats2half2_rn(q[2 * j] * f, q[2 * j + 1] * f);
+    float q0 = __uint_as_float(w[j] << 16), q1 = __uint_as_float(w[j] & 0xFFFF0000u);
+    if constexpr (FORM == kPowerForm) {
+      q0 *= inv;
+      q1 *= inv;
+    } else {
+      const float f = FORM != kTensorForm && (j & 1) ? 0.0625f : 1.f;
+      q0 = zero ? 0.f : quant_code(q0, s, inv) * f;
+      q1 = zero ? 0.f : quant_code(q1, s, inv) * f;
+    }
+    const __half2 h = __floats2half2_rn(q0, q1);
     o[j] = *reinterpret_cast<const uint32_t*>(&h);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
+template <QuantForm FORM>
+__device__ __forceinline__ float row_inverse(float s) {
+  return FORM == kPowerForm ? __frcp_rn(s) : quant_recip(s);
+}
+
 // Maximum over the R threads of a row (R = 32, or the whole block).
 template <int R>
 __device__ __forceinline__ float row_max(float m, float* part) {
@@ -732,13 +757,11 @@ quant_rows_kernel(const uint16_t* __restrict__ x, const int* __restrict__ head, 
     if (t + i * R < nvec) a = absmax8(v[i], a);
   for (int64_t i = t + kRowVecs * R; i < nvec; i += R) a = absmax8(__ldg(src + i), a);
   a = row_max<R>(a, part);
-  const float s = __fdiv_rn(a, 127.0f), inv = quant_recip(s);
+  const float s = row_scale<FORM>(a), inv = row_inverse<FORM>(s);
   if (t == 0) scales[m] = s;
   auto put = [&](const uint4& u, int64_t i) {
-    float q[8];
-    codes8(u, s, inv, a == 0.f, q);
     reinterpret_cast<uint4*>(codes + m * K)[FORM == kStreamForm ? unit_place(i) : i] =
-        codes_f16<FORM>(q);
+        row_f16<FORM>(u, s, inv, a == 0.f);
   };
 #pragma unroll
   for (int i = 0; i < kRowVecs; ++i)
@@ -757,10 +780,10 @@ place_rows_kernel(const uint16_t* __restrict__ x, int64_t K, uint16_t* __restric
         __ldg(reinterpret_cast<const uint4*>(x + at) + i);
 }
 
-// rows[pos[t, j]] = token t's activations, for each of its picks that has an
-// expert: bf16 as they are, or (CODES) their fp16 codes, and rows_s their
-// scales. One CTA a token: x is read once, each copy written once.
-template <bool CODES>
+// rows[pos[t, j]] = token t's activations as fp16 and rows_s their scale, for
+// each of its picks that has an expert. One CTA a token: x is read from memory
+// once, each copy written once.
+template <QuantForm FORM>
 __global__ void __launch_bounds__(kRowThreads)
 scatter_rows_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ pos, int k,
                     int64_t K, uint16_t* __restrict__ rows, float* __restrict__ rows_s) {
@@ -770,24 +793,16 @@ scatter_rows_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ 
   const int64_t m = blockIdx.x;
   const uint4* src = reinterpret_cast<const uint4*>(x + m * K);
   const int64_t nvec = K / 8;
-  float s = 0.f, inv = 0.f, a = 0.f;
-  if constexpr (CODES) {
-    for (int64_t i = threadIdx.x; i < nvec; i += kRowThreads) a = absmax8(__ldg(src + i), a);
-    a = row_max<kRowThreads>(a, part);
-    s = __fdiv_rn(a, 127.0f);
-    inv = quant_recip(s);
-    for (int j = threadIdx.x; j < k; j += kRowThreads) {
-      const int at = __ldg(pos + m * k + j);
-      if (at >= 0) rows_s[at] = s;
-    }
+  float a = 0.f;
+  for (int64_t i = threadIdx.x; i < nvec; i += kRowThreads) a = absmax8(__ldg(src + i), a);
+  a = row_max<kRowThreads>(a, part);
+  const float s = row_scale<FORM>(a), inv = row_inverse<FORM>(s);
+  for (int j = threadIdx.x; j < k; j += kRowThreads) {
+    const int at = __ldg(pos + m * k + j);
+    if (at >= 0) rows_s[at] = s;
   }
   for (int64_t i = threadIdx.x; i < nvec; i += kRowThreads) {
-    uint4 v = __ldg(src + i);
-    if constexpr (CODES) {
-      float q[8];
-      codes8(v, s, inv, a == 0.f, q);
-      v = codes_f16<kTensorForm>(q);
-    }
+    const uint4 v = row_f16<FORM>(__ldg(src + i), s, inv, a == 0.f);
     for (int j = 0; j < k; ++j) {
       const int at = __ldg(pos + m * k + j);
       if (at >= 0) reinterpret_cast<uint4*>(rows + (int64_t)at * K)[i] = v;
@@ -821,17 +836,18 @@ static cudaError_t launch_combine(const ExpertsArgs& a, const Y* y, cudaStream_t
 // Many rows an expert: the rows in sorted order, then the tcgen05 products.
 template <int VARIANT>
 static cudaError_t run_tensor(const ExpertsArgs& a, cudaStream_t st) {
-  constexpr bool kCodes = VARIANT == kW4A8;
+  constexpr QuantForm kForm = VARIANT == kW4A8 ? kTensorForm : kPowerForm;
   const int64_t n = a.T * a.k;
   cudaError_t e = launch_plan(a.ids, n, a.E, 0, a.plan, st);
   if (e != cudaSuccess) return e;
   PdlConfig c(dim3((unsigned)a.T, 1, 1), kRowThreads, 0, st);
-  e = cudaLaunchKernelEx(&c.cfg, scatter_rows_kernel<kCodes>, a.x, (const int32_t*)a.plan.pos, a.k,
+  e = cudaLaunchKernelEx(&c.cfg, scatter_rows_kernel<kForm>, a.x, (const int32_t*)a.plan.pos, a.k,
                          a.H, a.rows, a.rows_s);
   if (e != cudaSuccess) return e;
   RaggedArgs r{};
-  r.variant = VARIANT;
   r.gate_up = true;
+  r.wide = n > 64 * (int64_t)a.E;  // (see tc_experts.cu)
+  r.exact = VARIANT == kW4A8;
   r.rows_max = n;
   r.N = 2 * a.I;
   r.K = a.H;
@@ -843,14 +859,12 @@ static cudaError_t run_tensor(const ExpertsArgs& a, cudaStream_t st) {
   r.plan = a.plan;
   r.timeout_ns = a.timeout_ns;
   if ((e = launch_ragged(r, st)) != cudaSuccess) return e;
-  if (kCodes) {
-    e = launch_quant_rows<kTensorForm>(a.h, a.plan.head, n, a.I, a.h_q, a.h_s, st);
-    if (e != cudaSuccess) return e;
-  }
+  e = launch_quant_rows<kForm>(a.h, a.plan.head, n, a.I, a.h_q, a.h_s, st);
+  if (e != cudaSuccess) return e;
   r.gate_up = false;
   r.N = a.H;
   r.K = a.I;
-  r.act = kCodes ? a.h_q : a.h;
+  r.act = a.h_q;
   r.a_s = a.h_s;
   r.packed = a.down;
   r.y = static_cast<uint16_t*>(a.y);
@@ -926,8 +940,10 @@ static cudaError_t run_experts(const ExpertsArgs& a, cudaStream_t st) {
   p.N = (int)(2 * a.I);
   p.G = (int)(a.H / 128);
   // rows of a tile: the average expert's in one tile as a rule (an expert with
-  // more takes several, whose weights then come from L2)
-  const int nt = n <= (int64_t)6 * a.E ? 1 : (n <= (int64_t)12 * a.E ? 2 : 4);
+  // more takes several, whose weights then come from L2; 64 experts, 8 picks,
+  // 3584 x 1280, W4A16: 6 picks an expert take 125 us in tiles of 8, 8 picks
+  // 156 us in tiles of 16)
+  const int nt = n <= (int64_t)6 * a.E ? 1 : 2;
   cudaError_t e = cudaSuccess;
   if (a.way == kExpertsStream) e = launch_plan(a.ids, n, a.E, 8 * nt, a.plan, st);
   if (e == cudaSuccess && VARIANT == kW4A8)
@@ -939,9 +955,7 @@ static cudaError_t run_experts(const ExpertsArgs& a, cudaStream_t st) {
   }
   if (e != cudaSuccess) return e;
   if (a.way == kExpertsFew) return run_few<VARIANT>(a, p, st);
-  return nt == 1   ? run_stream<VARIANT, 1>(a, p, st)
-         : nt == 2 ? run_stream<VARIANT, 2>(a, p, st)
-                   : run_stream<VARIANT, 4>(a, p, st);
+  return nt == 1 ? run_stream<VARIANT, 1>(a, p, st) : run_stream<VARIANT, 2>(a, p, st);
 }
 
 cudaError_t launch_experts(const ExpertsArgs& a, cudaStream_t st) {

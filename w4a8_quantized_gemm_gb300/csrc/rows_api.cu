@@ -40,10 +40,10 @@ size_t carve_experts(void* ws, ExpertsArgs& a) {
   const bool codes = a.variant == kW4A8, tensor = a.way == kExpertsTensor;
   if (a.way != kExpertsFew)
     carve_plan(c, a.plan, n, a.E, tensor ? 0 : plan_max_tiles(n, a.E, 8), true);
-  a.x_q = c.take<uint16_t>(tensor || (!codes && a.way == kExpertsFew) ? 0 : a.T * a.H);
-  if (codes) {
-    a.x_s = c.take<float>(tensor ? 0 : a.T);
-    a.rows_s = c.take<float>(tensor ? n : 0);
+  if (!tensor && (codes || a.way == kExpertsStream)) a.x_q = c.take<uint16_t>(a.T * a.H);
+  if (!tensor && codes) a.x_s = c.take<float>(a.T);
+  if (tensor) a.rows_s = c.take<float>(n);
+  if (tensor || codes) {
     a.h_q = c.take<uint16_t>(n * a.I);
     a.h_s = c.take<float>(n);
   }

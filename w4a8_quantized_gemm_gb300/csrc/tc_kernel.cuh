@@ -135,10 +135,9 @@ struct TcParams {
 };
 
 // What a launch multiplies: one row range with one weight (the linears), or
-// sorted rows of which each set's range has its own weights (the experts):
-// with gate and up rows interleaved sixteen at a time, written as
-// silu(gate) * up, or as they are.
-enum TcMode { kTcLinear = 0, kTcGateUp = 1, kTcDown = 2 };
+// sorted rows of which each set's range has its own weights, gate and up rows
+// interleaved sixteen at a time, written as silu(gate) * up (the experts).
+enum TcMode { kTcLinear = 0, kTcGateUp = 1 };
 constexpr int kTcMaxSets = 1024;
 
 template <int VARIANT, int BT>
@@ -476,10 +475,10 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap act_map,
   };
 
   // weight block nt of all sets' (ragged products): its records and output
-  // columns (MODE kTcGateUp writes 64 columns a block of 128 rows)
+  // columns (64 a block of 128 gate and up rows)
   auto ragged_ref = [&](int nt) {
     const int in_set = nt % p.n_tiles;
-    constexpr int kCols = MODE == kTcGateUp ? 64 : 128;
+    constexpr int kCols = 64;
     return TileRef{p.seg.packed[0] + (int64_t)nt * G * 8512, p.seg.y[0],
                    (int64_t)p.n_tiles * kCols, (int64_t)in_set * kCols, 0};
   };
@@ -1044,13 +1043,13 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap act_map,
       }
     };
     // ragged products: rows m0 + col0 .. of the tile's set, `rows` of them,
-    // staged as above (gated first: the lane pairs 16 apart hold gate and up of
+    // staged as above (gated first: the lanes 16 apart hold gate and up of
     // one output, and of two tokens each takes one) and written by the whole
     // warpgroup, 16 bytes a thread, so that a tile's last rows can end
     // anywhere and no row of the next set is touched
     auto epilogue_ragged = [&](const float (&Rv)[HB], int k, int64_t m0, int rows,
                                const TileRef& o) {
-      constexpr int kCols = MODE == kTcGateUp ? 64 : 128;
+      constexpr int kCols = 64;
       asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory");  // the staging rows are free
       const float* as_row = as_stage + (k & 1) * BT + col0;
 #pragma unroll
@@ -1062,20 +1061,14 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap act_map,
           av[0] = a0.x; av[1] = a0.y; av[2] = a0.z; av[3] = a0.w;
           av[4] = a1.x; av[5] = a1.y; av[6] = a1.z; av[7] = a1.w;
         }
-        if constexpr (MODE == kTcGateUp) {
-          const bool up = (lane & 16) != 0;
-          const int col = (warp & 3) * 16 + (lane & 15);
+        const bool up = (lane & 16) != 0;
+        const int col = (warp & 3) * 16 + (lane & 15);
 #pragma unroll
-          for (int q = 0; q < 8; q += 2) {
-            const float v0 = Rv[c + q] * av[q], v1 = Rv[c + q + 1] * av[q + 1];
-            const float other = __shfl_xor_sync(0xffffffffu, up ? v0 : v1, 16);
-            const float h = up ? gated(other, v1) : gated(v0, other);
-            ybuf[(c + q + (up ? 1 : 0)) * kCols + col] = f32_to_bf16_bits(h);
-          }
-        } else {
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            ybuf[(c + q) * kCols + r] = f32_to_bf16_bits(Rv[c + q] * av[q]);
+        for (int q = 0; q < 8; q += 2) {
+          const float v0 = Rv[c + q] * av[q], v1 = Rv[c + q + 1] * av[q + 1];
+          const float other = __shfl_xor_sync(0xffffffffu, up ? v0 : v1, 16);
+          const float h = up ? gated(other, v1) : gated(v0, other);
+          ybuf[(c + q + (up ? 1 : 0)) * kCols + col] = f32_to_bf16_bits(h);
         }
       }
       asm volatile("bar.sync %0, 128;" ::"r"(2 + wg) : "memory");
