@@ -282,7 +282,7 @@ struct ExpertsArgs {
   float* x_s;
   uint16_t* rows;  // activations in sorted order [T*k][H], fp16 (tensor), and
   float* rows_s;   // their scales
-  uint16_t* h;     // bf16 [T*k][I]
+  void* h;         // gated values [T*k][I], bf16; fp32 (W4A16, tensor)
   uint16_t* h_q;   // fp16 codes of h and their scales (W4A8, and tensor)
   float* h_s;
   void* y;         // [T*k][H], fp32 (stream) or bf16 (tensor)
@@ -301,7 +301,7 @@ struct RaggedArgs {
   const uint16_t* act;  // fp16 [rows_max][K], sorted rows
   const float* a_s;     // scales of the sorted rows
   const uint8_t* packed;
-  uint16_t* y;
+  void* y;              // bf16; of the folded gate and up products fp32
   RowPlan plan;
   uint64_t timeout_ns;
 };

@@ -21,8 +21,9 @@ namespace egopq {
 // ---- products for few rows an expert --------------------------------------------
 // A warp takes 32 packed weight rows of one expert (16 gate and the 16 up rows
 // of the same outputs, or 32 rows of the down projection) times up to 8 * NT
-// rows, over every W-th group of K; the CTA's W warps add their sums through
-// shared memory in warp order.
+// rows: the CTA's four warps four such blocks each with all of K, or, where that
+// would leave SMs without work, one block with K split between them, whose sums
+// they add through shared memory in warp order.
 //
 // The products run on mma.m16n8k16 with the weights as the 16-row operand. A
 // thread of the fragment (row r = lane / 4, columns by lane % 4) reads the
@@ -263,6 +264,20 @@ struct Stream {
   }
 };
 
+// A warp's share of the work of the gate and up or down products: a block of 32
+// weight rows (of blockIdx.y's four, or blockIdx.y itself) and groups of K
+// first, first + step, ... , `units` of them -- all of K, or a part that the
+// block's other warps complete.
+struct Share {
+  int block, first, step, units;
+  __device__ __forceinline__ Share(bool split, int warp, int G) {
+    block = split ? blockIdx.y : blockIdx.y * kWarps + warp;
+    first = split ? warp : 0;
+    step = split ? kWarps : 1;
+    units = first < G ? (G - first + step - 1) / step : 0;
+  }
+};
+
 // The warp's 32 x 8 NT sums into its rows of `red` ([32][LD] a warp).
 template <int NT, int LD>
 __device__ __forceinline__ void put_sums(float* red, const float (&sum)[2][NT][4]) {
@@ -349,7 +364,7 @@ __device__ __forceinline__ int few_slot(const uint32_t (&m)[4], int t, int T, in
 }
 
 // ---- h = silu(G x) * (U x) -----------------------------------------------------------
-template <int VARIANT, int NT, bool FEW>
+template <int VARIANT, int NT, bool FEW, bool SPLIT>
 __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 5 : 4)
 experts_gate_up_kernel(const StreamParams p) {
   constexpr int LD = 8 * NT + 1;  // padded row of the partial sums
@@ -378,16 +393,16 @@ experts_gate_up_kernel(const StreamParams p) {
     if (rows == 0) return;
   }
   using S = Stream<VARIANT, NT, !(FEW && VARIANT == kW4A16)>;
-  S stream(ring[warp], (blockIdx.y & 3) * 32);
-  const uint8_t* rec = p.packed +
-                       (((int64_t)set * (p.N >> 7) + (blockIdx.y >> 2)) * G + warp) * 8512;
+  const Share sh(SPLIT, warp, G);
+  S stream(ring[warp], (sh.block & 3) * 32);
+  const uint8_t* rec =
+      p.packed + (((int64_t)set * (p.N >> 7) + (sh.block >> 2)) * G + sh.first) * 8512;
   auto next_rec = [&] {
     const uint8_t* r = rec;
-    rec += kWarps * 8512;
+    rec += sh.step * 8512;
     return r;
   };
-  const int n_units = warp < G ? (G - warp + kWarps - 1) / kWarps : 0;
-  stream.prime(n_units, next_rec);
+  stream.prime(sh.units, next_rec);
   const uint16_t* xp[NT];  // this lane's next activations of column gid of each tile, or null
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -396,46 +411,60 @@ experts_gate_up_kernel(const StreamParams p) {
     int64_t row = gid;
     if constexpr (FEW) live = few_slot(picked, gid, p.T, p.k) >= 0;
     else row = live ? __ldg(p.order + first + j) / p.k : 0;
-    xp[nt] = live ? p.act + row * K + warp * 128 + S::kLane * tig : nullptr;
+    xp[nt] = live ? p.act + row * K + sh.first * 128 + S::kLane * tig : nullptr;
   }
   float sum[2][NT][4];
   zero_sums<NT>(sum);
   stream.run(
-      n_units, next_rec,
+      sh.units, next_rec,
       [&](int nt) {
         const uint16_t* x = xp[nt];
-        if (x) xp[nt] += kWarps * 128;
+        if (x) xp[nt] += sh.step * 128;
         return reinterpret_cast<const uint4*>(x);
       },
       [] {}, sum);
+  const int I = p.N >> 1;
+  auto put = [&](int j, int at, float gate, float up) {  // output `at` of column j
+    const int64_t to = FEW ? few_slot(picked, j, p.T, p.k) : first + j;
+    if (to < 0) return;
+    if constexpr (VARIANT == kW4A8) {
+      const float as = __ldg(p.a_s + (FEW ? j : __ldg(p.order + first + j) / p.k));
+      gate *= as;
+      up *= as;
+    }
+    p.h[to * I + unit_place(at >> 3) * 8 + (at & 7)] = f32_to_bf16_bits(gated(gate, up));
+  };
+  if constexpr (!SPLIT) {
+    // this warp's sums are whole: row q >> 1 of each pair, column q & 1
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int j = nt * 8 + tig * 2 + (q & 1);
+        if (j < rows)
+          put(j, sh.block * 16 + gid + (q >> 1) * 8, sum[0][nt][q], sum[1][nt][q]);
+      }
+    return;
+  }
   __syncthreads();  // every warp is done with its ring
   float* red = reinterpret_cast<float*>(ring[0]);
   put_sums<NT, LD>(red + warp * 32 * LD, sum);
   __syncthreads();
-  const int I = p.N >> 1;
   for (int i = threadIdx.x; i < 16 * 8 * NT; i += 32 * kWarps) {
     const int c = i & 15, j = i >> 4;
     if (j >= rows) break;
-    const int64_t to = FEW ? few_slot(picked, j, p.T, p.k) : first + j;
-    if (to < 0) continue;
     float gate = 0.f, up = 0.f;
 #pragma unroll
     for (int q = 0; q < kWarps; ++q) {
       gate += red[(q * 32 + c) * LD + j];
       up += red[(q * 32 + 16 + c) * LD + j];
     }
-    if constexpr (VARIANT == kW4A8) {
-      const float as = __ldg(p.a_s + (FEW ? j : __ldg(p.order + first + j) / p.k));
-      gate *= as;
-      up *= as;
-    }
-    const int64_t at = blockIdx.y * 16 + c;
-    p.h[to * I + unit_place(at >> 3) * 8 + (at & 7)] = f32_to_bf16_bits(gated(gate, up));
+    put(j, sh.block * 16 + c, gate, up);
   }
 }
 
 // ---- y = D h, a sorted row at a time ----------------------------------------------------
-template <int VARIANT, int NT>
+template <int VARIANT, int NT, bool SPLIT>
 __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 5 : 4)
 experts_down_kernel(const StreamParams p) {
   constexpr int LD = 8 * NT + 1;
@@ -457,34 +486,50 @@ experts_down_kernel(const StreamParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
   const int G = p.G, K = G * 128;
-  Stream<VARIANT, NT, true> stream(ring[warp], (blockIdx.y & 3) * 32);
-  const uint8_t* rec = p.packed +
-                       (((int64_t)tile.x * (p.N >> 7) + (blockIdx.y >> 2)) * G + warp) * 8512;
+  const Share sh(SPLIT, warp, G);
+  Stream<VARIANT, NT, true> stream(ring[warp], (sh.block & 3) * 32);
+  const uint8_t* rec =
+      p.packed + (((int64_t)tile.x * (p.N >> 7) + (sh.block >> 2)) * G + sh.first) * 8512;
   auto next_rec = [&] {
     const uint8_t* r = rec;
-    rec += kWarps * 8512;
+    rec += sh.step * 8512;
     return r;
   };
-  const int n_units = warp < G ? (G - warp + kWarps - 1) / kWarps : 0;
-  stream.prime(n_units, next_rec);
+  stream.prime(sh.units, next_rec);
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   const uint16_t* xp[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int j = nt * 8 + gid;
-    xp[nt] = j < rows ? p.act + (int64_t)(tile.y + j) * K + warp * 128 + 8 * tig : nullptr;
+    xp[nt] = j < rows ? p.act + (int64_t)(tile.y + j) * K + sh.first * 128 + 8 * tig : nullptr;
   }
   float sum[2][NT][4];
   zero_sums<NT>(sum);
   stream.run(
-      n_units, next_rec,
+      sh.units, next_rec,
       [&](int nt) {
         const uint16_t* x = xp[nt];
-        if (x) xp[nt] += kWarps * 128;
+        if (x) xp[nt] += sh.step * 128;
         return reinterpret_cast<const uint4*>(x);
       },
       [] {}, sum);
+  auto put = [&](int j, int at, float v) {
+    if constexpr (VARIANT == kW4A8) v *= __ldg(p.a_s + tile.y + j);
+    p.y[(int64_t)(tile.y + j) * p.N + at] = v;
+  };
+  if constexpr (!SPLIT) {
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int j = nt * 8 + tig * 2 + (q & 1);
+          if (j < rows) put(j, sh.block * 32 + mt * 16 + gid + (q >> 1) * 8, sum[mt][nt][q]);
+        }
+    return;
+  }
   __syncthreads();
   float* red = reinterpret_cast<float*>(ring[0]);
   put_sums<NT, LD>(red + warp * 32 * LD, sum);
@@ -495,8 +540,7 @@ experts_down_kernel(const StreamParams p) {
     float v = 0.f;
 #pragma unroll
     for (int q = 0; q < kWarps; ++q) v += red[(q * 32 + c) * LD + j];
-    if constexpr (VARIANT == kW4A8) v *= __ldg(p.a_s + tile.y + j);
-    p.y[(int64_t)(tile.y + j) * p.N + blockIdx.y * 32 + c] = v;
+    put(j, sh.block * 32 + c, v);
   }
 }
 
@@ -662,7 +706,7 @@ combine_kernel(const Y* __restrict__ y, const float* __restrict__ weights,
 // form the streaming products' operand words ask for, in the order of
 // unit_place, which their input may have already (kStreamPlaced) or not. The
 // tensor products take W4A16's activations as fp16 as well: kPowerForm is the
-// bf16 value over a power of two that brings the row's largest to [2^14, 2^15).
+// value over a power of two that brings the row's largest to [2^14, 2^15).
 enum QuantForm { kTensorForm, kStreamForm, kStreamPlaced, kPowerForm };
 
 // A row's scale from its largest magnitude.
@@ -679,24 +723,40 @@ __device__ __forceinline__ float row_scale(float a) {
     return __fdiv_rn(a, 127.0f);
   }
 }
-__device__ __forceinline__ float absmax8(const uint4& v, float m) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// Eight neighbouring values of a row, bf16 or fp32.
+template <typename X>
+struct Eight {
+  float q[8];
+  __device__ __forceinline__ void load(const X* row, int64_t i) {
+    if constexpr (sizeof(X) == 4) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(row) + 2 * i);
+      const float4 b = __ldg(reinterpret_cast<const float4*>(row) + 2 * i + 1);
+      q[0] = a.x; q[1] = a.y; q[2] = a.z; q[3] = a.w;
+      q[4] = b.x; q[5] = b.y; q[6] = b.z; q[7] = b.w;
+    } else {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(row) + i);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    m = fmaxf(m, fabsf(__uint_as_float(w[j] << 16)));
-    m = fmaxf(m, fabsf(__uint_as_float(w[j] & 0xFFFF0000u)));
+      for (int j = 0; j < 4; ++j) {
+        q[2 * j] = __uint_as_float(w[j] << 16);
+        q[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      }
+    }
   }
-  return m;
-}
+  __device__ __forceinline__ float absmax(float m) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(q[j]));
+    return m;
+  }
+};
 // Eight values of a row of scale s (inv: its inverse for the form, 0 in a row
 // of zeros) as eight fp16.
-template <QuantForm FORM>
-__device__ __forceinline__ uint4 row_f16(const uint4& v, float s, float inv, bool zero) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+template <QuantForm FORM, typename X>
+__device__ __forceinline__ uint4 row_f16(const Eight<X>& v, float s, float inv, bool zero) {
   uint32_t o[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    float q0 = __uint_as_float(w[j] << 16), q1 = __uint_as_float(w[j] & 0xFFFF0000u);
+    float q0 = v.q[2 * j], q1 = v.q[2 * j + 1];
     if constexpr (FORM == kPowerForm) {
       q0 *= inv;
       q1 *= inv;
@@ -731,13 +791,13 @@ __device__ __forceinline__ float row_max(float m, float* part) {
 }
 
 constexpr int kRowThreads = 128;
-constexpr int kRowVecs = 8;  // 16-byte vectors a thread keeps of its row
+constexpr int kRowVecs = 4;  // eights of its row a thread keeps
 
 // Rows [0, rows) (or those below head[0], where head is given) of x [.][K].
-template <int R, QuantForm FORM>
+template <int R, QuantForm FORM, typename X>
 __global__ void __launch_bounds__(kRowThreads)
-quant_rows_kernel(const uint16_t* __restrict__ x, const int* __restrict__ head, int64_t rows,
-                  int64_t K, uint16_t* __restrict__ codes, float* __restrict__ scales) {
+quant_rows_kernel(const X* __restrict__ x, const int* __restrict__ head, int64_t rows, int64_t K,
+                  uint16_t* __restrict__ codes, float* __restrict__ scales) {
   __shared__ float part[kRowThreads / 32];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
@@ -745,28 +805,36 @@ quant_rows_kernel(const uint16_t* __restrict__ x, const int* __restrict__ head, 
   if (head) rows = head[0];
   if (m >= rows) return;  // (a whole warp, or the whole block)
   const int t = threadIdx.x % R;
-  const uint4* src = reinterpret_cast<const uint4*>(x + m * K);
+  const X* src = x + m * K;
   const int64_t nvec = K / 8;
-  uint4 v[kRowVecs];
+  Eight<X> v[kRowVecs];
   float a = 0.f;
 #pragma unroll
   for (int i = 0; i < kRowVecs; ++i)
-    if (t + i * R < nvec) v[i] = __ldg(src + t + i * R);
+    if (t + i * R < nvec) v[i].load(src, t + i * R);
 #pragma unroll
   for (int i = 0; i < kRowVecs; ++i)
-    if (t + i * R < nvec) a = absmax8(v[i], a);
-  for (int64_t i = t + kRowVecs * R; i < nvec; i += R) a = absmax8(__ldg(src + i), a);
+    if (t + i * R < nvec) a = v[i].absmax(a);
+  for (int64_t i = t + kRowVecs * R; i < nvec; i += R) {
+    Eight<X> u;
+    u.load(src, i);
+    a = u.absmax(a);
+  }
   a = row_max<R>(a, part);
   const float s = row_scale<FORM>(a), inv = row_inverse<FORM>(s);
   if (t == 0) scales[m] = s;
-  auto put = [&](const uint4& u, int64_t i) {
+  auto put = [&](const Eight<X>& u, int64_t i) {
     reinterpret_cast<uint4*>(codes + m * K)[FORM == kStreamForm ? unit_place(i) : i] =
         row_f16<FORM>(u, s, inv, a == 0.f);
   };
 #pragma unroll
   for (int i = 0; i < kRowVecs; ++i)
     if (t + i * R < nvec) put(v[i], t + i * R);
-  for (int64_t i = t + kRowVecs * R; i < nvec; i += R) put(__ldg(src + i), i);
+  for (int64_t i = t + kRowVecs * R; i < nvec; i += R) {
+    Eight<X> u;
+    u.load(src, i);
+    put(u, i);
+  }
 }
 
 // bf16 rows in the order of unit_place (W4A16, stream).
@@ -791,10 +859,14 @@ scatter_rows_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ 
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   const int64_t m = blockIdx.x;
-  const uint4* src = reinterpret_cast<const uint4*>(x + m * K);
+  const uint16_t* src = x + m * K;
   const int64_t nvec = K / 8;
+  Eight<uint16_t> u;
   float a = 0.f;
-  for (int64_t i = threadIdx.x; i < nvec; i += kRowThreads) a = absmax8(__ldg(src + i), a);
+  for (int64_t i = threadIdx.x; i < nvec; i += kRowThreads) {
+    u.load(src, i);
+    a = u.absmax(a);
+  }
   a = row_max<kRowThreads>(a, part);
   const float s = row_scale<FORM>(a), inv = row_inverse<FORM>(s);
   for (int j = threadIdx.x; j < k; j += kRowThreads) {
@@ -802,7 +874,8 @@ scatter_rows_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ 
     if (at >= 0) rows_s[at] = s;
   }
   for (int64_t i = threadIdx.x; i < nvec; i += kRowThreads) {
-    const uint4 v = row_f16<FORM>(__ldg(src + i), s, inv, a == 0.f);
+    u.load(src, i);
+    const uint4 v = row_f16<FORM>(u, s, inv, a == 0.f);
     for (int j = 0; j < k; ++j) {
       const int at = __ldg(pos + m * k + j);
       if (at >= 0) reinterpret_cast<uint4*>(rows + (int64_t)at * K)[i] = v;
@@ -811,17 +884,17 @@ scatter_rows_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ 
 }
 
 // ---- launches -----------------------------------------------------------------------
-template <QuantForm FORM>
-static cudaError_t launch_quant_rows(const uint16_t* x, const int* head, int64_t rows, int64_t K,
+template <QuantForm FORM, typename X>
+static cudaError_t launch_quant_rows(const X* x, const int* head, int64_t rows, int64_t K,
                                      uint16_t* codes, float* scales, cudaStream_t st) {
   // a warp a row where there are rows for every warp of the GPU (32768 x 1280:
   // a block a row leaves most of its threads without work), else a block
-  if (rows >= 4096 && K <= 32 * kRowVecs * 8) {
+  if (rows >= 4096 && K <= 2048) {
     PdlConfig c(dim3((unsigned)((rows + 3) / 4), 1, 1), kRowThreads, 0, st);
-    return cudaLaunchKernelEx(&c.cfg, quant_rows_kernel<32, FORM>, x, head, rows, K, codes, scales);
+    return cudaLaunchKernelEx(&c.cfg, quant_rows_kernel<32, FORM, X>, x, head, rows, K, codes, scales);
   }
   PdlConfig c(dim3((unsigned)rows, 1, 1), kRowThreads, 0, st);
-  return cudaLaunchKernelEx(&c.cfg, quant_rows_kernel<kRowThreads, FORM>, x, head, rows, K, codes,
+  return cudaLaunchKernelEx(&c.cfg, quant_rows_kernel<kRowThreads, FORM, X>, x, head, rows, K, codes,
                             scales);
 }
 
@@ -859,7 +932,12 @@ static cudaError_t run_tensor(const ExpertsArgs& a, cudaStream_t st) {
   r.plan = a.plan;
   r.timeout_ns = a.timeout_ns;
   if ((e = launch_ragged(r, st)) != cudaSuccess) return e;
-  e = launch_quant_rows<kForm>(a.h, a.plan.head, n, a.I, a.h_q, a.h_s, st);
+  if (VARIANT == kW4A8)
+    e = launch_quant_rows<kForm>(static_cast<const uint16_t*>(a.h), a.plan.head, n, a.I, a.h_q,
+                                 a.h_s, st);
+  else
+    e = launch_quant_rows<kForm>(static_cast<const float*>(a.h), a.plan.head, n, a.I, a.h_q, a.h_s,
+                                 st);
   if (e != cudaSuccess) return e;
   r.gate_up = false;
   r.N = a.H;
@@ -867,24 +945,41 @@ static cudaError_t run_tensor(const ExpertsArgs& a, cudaStream_t st) {
   r.act = a.h_q;
   r.a_s = a.h_s;
   r.packed = a.down;
-  r.y = static_cast<uint16_t*>(a.y);
+  r.y = a.y;
   if ((e = launch_ragged(r, st)) != cudaSuccess) return e;
   return launch_combine(a, (const uint16_t*)a.y, st);
+}
+
+// Whether the products of `tiles` row tiles with N weight rows split K between
+// the warps of a CTA: with all of K a warp there have to be about seven CTAs an
+// SM (64 experts, 8 picks, 3584 x 1280, W4A16, split / whole: 1 token 19.1 /
+// 32.9 us, 4 tokens 48.6 / 55.1, 8 tokens 75.1 / 72.3, 33 tokens 104 / 99; 32
+// experts, 4 picks, 2048 x 1024: 24 tokens 30 / 37).
+static bool split_k(int64_t tiles, int64_t N) {
+  return tiles * (N / 128) < 7 * (int64_t)device_sm_count();
+}
+
+template <int VARIANT, int NT, bool FEW>
+static cudaError_t launch_gate_up(const StreamParams& p, int64_t tiles, int64_t sets,
+                                  cudaStream_t st) {
+  const bool split = split_k(sets, p.N);
+  PdlConfig c(dim3((unsigned)tiles, (unsigned)(p.N / (split ? 32 : 128)), 1), 32 * kWarps, 0, st);
+  return split ? cudaLaunchKernelEx(&c.cfg, experts_gate_up_kernel<VARIANT, NT, FEW, true>, p)
+               : cudaLaunchKernelEx(&c.cfg, experts_gate_up_kernel<VARIANT, NT, FEW, false>, p);
 }
 
 template <int VARIANT>
 static cudaError_t run_few(const ExpertsArgs& a, StreamParams p, cudaStream_t st) {
   const int64_t n = a.T * a.k;
   const int64_t most = n < a.E ? n : a.E;
-  PdlConfig c(dim3((unsigned)most, (unsigned)(a.I / 16), 1), 32 * kWarps, 0, st);
-  cudaError_t e = cudaLaunchKernelEx(&c.cfg, experts_gate_up_kernel<VARIANT, 1, true>, p);
+  cudaError_t e = launch_gate_up<VARIANT, 1, true>(p, most, most, st);
   if (e != cudaSuccess) return e;
   if (VARIANT == kW4A8) {
     // (a slot without an expert holds no row: its codes are never read)
-    e = launch_quant_rows<kStreamPlaced>(a.h, nullptr, n, a.I, a.h_q, a.h_s, st);
+    e = launch_quant_rows<kStreamPlaced>(p.h, nullptr, n, a.I, a.h_q, a.h_s, st);
     if (e != cudaSuccess) return e;
   }
-  p.act = VARIANT == kW4A8 ? a.h_q : a.h;
+  p.act = VARIANT == kW4A8 ? a.h_q : p.h;
   p.a_s = a.h_s;
   p.packed = a.down;
   p.N = (int)a.H;
@@ -900,20 +995,22 @@ template <int VARIANT, int NT>
 static cudaError_t run_stream(const ExpertsArgs& a, StreamParams p, cudaStream_t st) {
   const int64_t n = a.T * a.k;
   const int64_t tiles = plan_max_tiles(n, a.E, 8 * NT);
-  PdlConfig c(dim3((unsigned)tiles, (unsigned)(a.I / 16), 1), 32 * kWarps, 0, st);
-  cudaError_t e = cudaLaunchKernelEx(&c.cfg, experts_gate_up_kernel<VARIANT, NT, false>, p);
+  const int64_t sets = n < a.E ? n : a.E;  // tiles that multiply, at least about
+  cudaError_t e = launch_gate_up<VARIANT, NT, false>(p, tiles, sets, st);
   if (e != cudaSuccess) return e;
   if (VARIANT == kW4A8) {
-    e = launch_quant_rows<kStreamPlaced>(a.h, a.plan.head, n, a.I, a.h_q, a.h_s, st);
+    e = launch_quant_rows<kStreamPlaced>(p.h, a.plan.head, n, a.I, a.h_q, a.h_s, st);
     if (e != cudaSuccess) return e;
   }
-  p.act = VARIANT == kW4A8 ? a.h_q : a.h;
+  p.act = VARIANT == kW4A8 ? a.h_q : p.h;
   p.a_s = a.h_s;
   p.packed = a.down;
   p.N = (int)a.H;
   p.G = (int)(a.I / 128);
-  PdlConfig d(dim3((unsigned)tiles, (unsigned)(a.H / 32), 1), 32 * kWarps, 0, st);
-  e = cudaLaunchKernelEx(&d.cfg, experts_down_kernel<VARIANT, NT>, p);
+  const bool split = split_k(sets, p.N);
+  PdlConfig d(dim3((unsigned)tiles, (unsigned)(p.N / (split ? 32 : 128)), 1), 32 * kWarps, 0, st);
+  e = split ? cudaLaunchKernelEx(&d.cfg, experts_down_kernel<VARIANT, NT, true>, p)
+            : cudaLaunchKernelEx(&d.cfg, experts_down_kernel<VARIANT, NT, false>, p);
   if (e != cudaSuccess) return e;
   return launch_combine(a, (const float*)a.y, st);
 }
@@ -926,7 +1023,7 @@ static cudaError_t run_experts(const ExpertsArgs& a, cudaStream_t st) {
   p.act = VARIANT == kW4A8 ? a.x_q : a.x;
   p.a_s = a.x_s;
   p.packed = a.gate_up;
-  p.h = a.h;
+  p.h = static_cast<uint16_t*>(a.h);
   p.y = static_cast<float*>(a.y);
   p.out = a.out;
   p.head = a.plan.head;

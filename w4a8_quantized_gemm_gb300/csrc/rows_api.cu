@@ -47,7 +47,7 @@ size_t carve_experts(void* ws, ExpertsArgs& a) {
     a.h_q = c.take<uint16_t>(n * a.I);
     a.h_s = c.take<float>(n);
   }
-  a.h = c.take<uint16_t>(n * a.I);
+  a.h = c.take<uint16_t>(n * a.I * (tensor && !codes ? 2 : 1));
   if (tensor) {
     // the sorted activations are dead once the gate and up products have run
     a.rows = c.take<uint16_t>(n * a.H);

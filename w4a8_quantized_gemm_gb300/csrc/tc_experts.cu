@@ -85,7 +85,7 @@ struct RgCfg {
 struct RgParams {
   const float* a_s;
   const uint8_t* packed;
-  uint16_t* y;
+  void* y;                // bf16, or fp32 (folded gate and up) [sorted rows][columns]
   const int32_t* offset;  // first sorted row of each set, [sets + 1]
   int sets, n_tiles, G;   // weight blocks of 128 rows a set, groups of K
   uint64_t timeout_ns;
@@ -108,6 +108,9 @@ ragged_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_constant
   using C = RgCfg<BT, EXACT>;
   constexpr int XS = C::kRowStages, RS = C::kRecStages, NA = C::kNumA, HB = C::kHB;
   constexpr int kCols = GATE_UP ? 64 : 128;  // output columns of a weight block
+  // W4A16's gated values stay fp32 until their row's scale is known (rounding
+  // them to bf16 first would be the largest error of the layer but its output's)
+  using Y = std::conditional_t<GATE_UP && !EXACT, float, uint16_t>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t base = (raw_addr + 1023u) & ~1023u;
@@ -409,7 +412,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_constant
     const int wg = warp >> 2;
     const int col0 = wg * HB;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    uint16_t* out = reinterpret_cast<uint16_t*>(smem + C::kOutAt) + wg * C::kRound * 128;
+    Y* out = reinterpret_cast<Y*>(smem + C::kOutAt + wg * C::kRound * 256);
     float* as = reinterpret_cast<float*>(smem + C::kAsAt) + col0;
     const int64_t ld = (int64_t)p.n_tiles * kCols;
     bool ok = true;
@@ -429,7 +432,8 @@ ragged_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_constant
           const float v0 = v[c] * a2.x, v1 = v[c + 1] * a2.y;
           const float other = __shfl_xor_sync(0xffffffffu, up ? v0 : v1, 16);
           const float h = up ? gated(other, v1) : gated(v0, other);
-          out[(c + (up ? 1 : 0)) * kCols + col] = f32_to_bf16_bits(h);
+          if constexpr (sizeof(Y) == 4) out[(c + (up ? 1 : 0)) * kCols + col] = h;
+          else out[(c + (up ? 1 : 0)) * kCols + col] = f32_to_bf16_bits(h);
         }
       } else {
 #pragma unroll
@@ -442,12 +446,12 @@ ragged_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_constant
       }
       asm volatile("bar.sync %0, 128;" ::"r"(6 + wg) : "memory");
       const int rows = ok ? min(RD, un.rows - col0 - c0) : 0;
-      constexpr int kVec = kCols / 8;  // 16-byte vectors of a row
+      constexpr int kPer = 16 / sizeof(Y), kVec = kCols / kPer;  // 16-byte vectors of a row
       const uint4* src = reinterpret_cast<const uint4*>(out);
-      uint16_t* dst = p.y + (int64_t)(un.row0 + col0 + c0) * ld + un.n0 * kCols;
+      Y* dst = static_cast<Y*>(p.y) + (int64_t)(un.row0 + col0 + c0) * ld + un.n0 * kCols;
 #pragma unroll 4
       for (int i = r; i < rows * kVec; i += 128)
-        *reinterpret_cast<uint4*>(dst + (int64_t)(i / kVec) * ld + (i % kVec) * 8) = src[i];
+        *reinterpret_cast<uint4*>(dst + (int64_t)(i / kVec) * ld + (i % kVec) * kPer) = src[i];
       asm volatile("bar.sync %0, 128;" ::"r"(6 + wg) : "memory");  // the staging rows are free
     };
     for (int k = 0; k < n_units; ++k) {
@@ -603,7 +607,7 @@ static cudaError_t launch_exact_wide(const RaggedArgs& a, cudaStream_t st) {
   p.timeout_ns = a.timeout_ns;
   p.seg.count = 1;
   p.seg.packed[0] = a.packed;
-  p.seg.y[0] = a.y;
+  p.seg.y[0] = static_cast<uint16_t*>(a.y);
   p.seg.N[0] = a.N;
   p.set_offset = a.plan.offset;
   p.sets = a.E;
