@@ -288,6 +288,41 @@ def test_experts_on_another_stream_and_again_in_one_workspace(path):
     assert ((few.double() - ref).abs() <= bound).all()
 
 
+@pytest.mark.parametrize("variant", VARIANTS)
+@pytest.mark.parametrize("T,path", [(6, eg.PATH_GEMV), (90, eg.PATH_GEMV), (90, eg.PATH_TC),
+                                    (700, eg.PATH_TC)])
+def test_experts_non_finite_rows_stay_alone(variant, T, path):
+    x, ids, w, gu, dn = experts_case(11, T, 4, 2, 256, 128)
+    layer = eg.moe_pack(*gu, *dn)
+    clean = eg.moe_experts(x, ids, w, layer, variant=variant, path=path)
+    x[2, 5] = math.nan
+    x[4, 200] = math.inf
+    y = eg.moe_experts(x, ids, w, layer, variant=variant, path=path)
+    other = torch.ones(T, dtype=torch.bool, device=DEV)
+    other[[2, 4]] = False
+    assert torch.equal(y[other], clean[other])
+    if variant == eg.VARIANT_W4A16:
+        assert not torch.isfinite(y[2].float()).any() and not torch.isfinite(y[4].float()).all()
+    assert eg.device_status() == 0
+
+
+@pytest.mark.parametrize("variant", VARIANTS)
+@pytest.mark.parametrize("T,path", [(5, eg.PATH_GEMV), (60, eg.PATH_GEMV), (60, eg.PATH_TC),
+                                    (500, eg.PATH_TC)])
+@pytest.mark.parametrize("low,high", [(-24, -14), (-20, 2), (0, 12)])
+def test_experts_scales_of_the_whole_range(variant, T, path, low, high):
+    """fp16 scales of 2^low to 2^high, subnormal ones among them."""
+    x, ids, w, gu, dn = experts_case(12, T, 4, 2, 384, 256)
+    g = gen(13)
+
+    def spread(v):
+        e = torch.randint(low, high, v[1].shape, generator=g, device=DEV)
+        m = 1 + torch.rand(v[1].shape, generator=g, device=DEV) * 0.99
+        return v[0], torch.ldexp(m, e).half(), v[2]
+
+    check_experts((x, ids, w, spread(gu), spread(dn)), variant, path)
+
+
 def test_gate_up_packing_interleaves_rows():
     g = gen(9)
     E, I, H = 3, 256, 256
