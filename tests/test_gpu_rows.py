@@ -389,6 +389,47 @@ def test_lora_add(M, N, K, L, r, mixed):
     check_lora(*lora_case(M + L, M, N, K, L, r, mixed))
 
 
+@pytest.mark.parametrize("M,N,K,L,r", [
+    (130, 4224, 384, 3, 40), (300, 8320, 256, 60, 16), (1100, 8448, 256, 30, 24),
+    (1500, 384, 640, 50, 128), (2100, 640, 1152, 7, 48), (4093, 128, 128, 64, 8)])
+def test_lora_add_planned(M, N, K, L, r):
+    check_lora(*lora_case(M + L, M, N, K, L, r, True))
+
+
+@pytest.mark.parametrize("M", [60, 400, 2100])
+def test_lora_one_adapter_takes_most_rows_and_rows_that_are_not_finite_stay_alone(M):
+    y, x, ad, ids = lora_case(5, M, 640, 512, 60, 32, False)
+    ids[: M * 9 // 10] = 7
+    want = check_lora(y, x, ad, ids)
+    x[3, 9] = math.nan
+    x[M - 1, 100] = math.inf
+    got = eg.lora_add(y, x, ad, ids)
+    other = torch.ones(M, dtype=torch.bool, device=DEV)
+    other[[3, M - 1]] = False
+    assert torch.equal(got[other], want[other])
+    assert torch.isnan(got[3].float()).all()
+
+
+@pytest.mark.parametrize("M", [400, 2100])
+def test_lora_unused_ranks_of_a_planned_batch(M):
+    y, x, ad, ids = lora_case(6, M, 256, 256, 50, 40, False)
+    n = 37
+    A, B = ad.A.clone(), ad.B.clone()
+    A[:, n:] = math.nan
+    B[:, :, n:] = math.inf
+    ranks = torch.full((50,), n, dtype=torch.int32, device=DEV)
+    ranks[::7] = 0
+    got = check_lora(y, x, eg.LoraAdapters(A, B, ad.scale, ranks), ids)
+    assert torch.isfinite(got.float()).all()
+
+
+def test_lora_workspace_of_a_larger_batch():
+    y, x, ad, ids = lora_case(8, 2100, 256, 384, 50, 16, True)
+    ws = eg.lora_workspace(2100, 256, 384, ad, DEV)
+    for M in (2100, 1200, 600, 130, 128, 1):
+        check_lora(y[:M], x[:M], ad, ids[:M], workspace=ws)
+
+
 def test_lora_in_place_odd_ids_and_unused_ranks():
     y, x, ad, ids = lora_case(3, 50, 256, 256, 4, 16, False)
     ids[::5] = -7

@@ -319,15 +319,13 @@ struct LoraArgs {
   int L, r;
   uint16_t* y_out;
   RowPlan plan;
-  float* h;  // [lora_splits][M][r] partial sums of A x, sorted rows
+  float* h;  // [lora_h_rows][r]: [parts of K][M][r] sums of A x, sorted rows
 };
-// Whether M rows run without a plan (and without a workspace); else the rows of
-// a tile.
+// Whether M rows run without a plan (and without a workspace).
 bool lora_few(int64_t M);
-int lora_tile(int64_t M);
-// Parts of K whose sums of A x lie in memory between two kernels (0: one
-// kernel does both products).
-int lora_splits(int64_t M, int64_t K);
+constexpr int kLoraTile = 32;  // rows of the smallest tile of a planned batch
+// Rows of r fp32 sums that lie in memory between two kernels, at most.
+int64_t lora_h_rows(int64_t M);
 cudaError_t launch_lora(const LoraArgs& a, cudaStream_t st);
 
 // Weights [E][2I][K] with I gate rows and then I up rows a set, packed with

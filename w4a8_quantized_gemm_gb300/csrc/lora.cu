@@ -6,16 +6,19 @@
 // A [L][r][K], B [L][N][r] bf16; adapter a uses its first ranks[a] rows of A
 // (columns of B). A row with ids outside [0, L) keeps y0.
 //
-// One kernel: a cluster of CTAs takes up to 32 rows of one adapter, splits K for
-// A x, adds the parts through distributed shared memory in rank order and
-// splits the columns for the product with B. Up to 128 rows (decode) the
-// cluster finds its rows in the ids alone; more rows are sorted by adapter
-// first (RowPlan). Results do not depend on timing.
+// One kernel where its tiles run at once: a cluster of CTAs takes up to 32 rows
+// of one adapter, splits K for A x, adds the parts through distributed shared
+// memory in rank order and splits the columns for the product with B. Up to 128
+// rows (decode) the cluster finds its rows in the ids alone; more rows are
+// sorted by adapter first (RowPlan), and many tiles of narrow rows take two
+// kernels (lora_many). Results do not depend on timing.
 //
 // All products run on mma.m16n8k16 with fragments loaded straight from memory:
 // the order of K inside a fragment is free as long as both operands share it,
 // so each thread reads 16 (A, x) or 8 (B) contiguous bytes of its row.
 #include "egopq_internal.h"
+
+#include <algorithm>
 
 namespace egopq {
 
@@ -28,13 +31,23 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+
+// `bytes` (a multiple of 16, at a 16-byte boundary) on their way into L2.
+__device__ __forceinline__ void prefetch_l2(const void* from, int bytes) {
+  if (bytes > 0)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
+}
+
 constexpr int kLoraWarps = 8;
 constexpr int kLoraThreads = 32 * kLoraWarps;
-constexpr int kLoraTile = 32;      // rows of a tile of a planned batch
 constexpr int kLoraMaxRank = 128;
 constexpr int kLoraFewRows = 128;  // rows of a batch without a plan
-constexpr int kLoraManyRows = 1024;  // a batch of more takes two kernels, of
-constexpr int kManyTile = 128;       // tiles of so many rows
+constexpr int kManyTile = 128;  // rows of a tile of the two kernels (lora_many)
+constexpr int kManyCtas = 304;  // CTAs that their first is split for, two an SM
 constexpr int kLoraCluster = 8;
 constexpr int kHsLd = kLoraMaxRank + 8;  // padded row of the bf16 A x in shared memory (16-byte rows)
 
@@ -52,7 +65,7 @@ struct LoraParams {
   const int32_t* order;
   float* h;  // [splits][M][r] partial sums of A x, sorted rows (two kernels)
   int64_t M, N, K;
-  int L, r, slabs, splits;
+  int L, r, max_slabs, clusters, splits;
 };
 
 // ranks[a] as a number in [0, r]
@@ -62,31 +75,39 @@ __device__ __forceinline__ int adapter_rank(const LoraParams& p, int a) {
 
 // acc[mt][t] += x rows (two a thread and row tile: xr[2 mt], xr[2 mt + 1], null
 // where there is none) times ranks [c0, c0 + 8 NR) of A over the 32-wide K
-// steps s0, s0 + step, ... below s1. Pointers include the thread's 8 * tig.
+// steps s0, s0 + step, ... below s1. Pointers include the thread's 8 * tig. A
+// step's loads are all issued before its products (missing rows and ranks read
+// the first and are replaced by zeros: no branch between the loads).
 template <int MT, int NR>
 __device__ __forceinline__ void shrink_steps(float (&acc)[MT][NR][4], const uint16_t* const* xr,
                                              const uint16_t* Ab, int64_t K, int c0, int rank,
                                              int s0, int s1, int step) {
   const int gid = (threadIdx.x & 31) >> 2;
-#pragma unroll 2
+  auto keep = [](uint4 v, bool in) {
+    return make_uint4(in ? v.x : 0u, in ? v.y : 0u, in ? v.z : 0u, in ? v.w : 0u);
+  };
+  const uint16_t* Aj[NR];
+#pragma unroll
+  for (int t = 0; t < NR; ++t) {
+    const int j = c0 + t * 8 + gid;
+    Aj[t] = Ab + (int64_t)(j < rank ? j : 0) * K;
+  }
   for (int s = s0; s < s1; s += step) {
-    uint4 a[MT][2];
+    uint4 a[2 * MT], b[NR];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int q = 0; q < 2 * MT; ++q)
+      a[q] = __ldg(reinterpret_cast<const uint4*>((xr[q] ? xr[q] : Ab) + (int64_t)s * 32));
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
-        a[mt][q] = xr[2 * mt + q]
-                       ? __ldg(reinterpret_cast<const uint4*>(xr[2 * mt + q] + (int64_t)s * 32))
-                       : make_uint4(0, 0, 0, 0);
+    for (int t = 0; t < NR; ++t) b[t] = __ldg(reinterpret_cast<const uint4*>(Aj[t] + s * 32));
+#pragma unroll
+    for (int q = 0; q < 2 * MT; ++q) a[q] = keep(a[q], xr[q] != nullptr);
 #pragma unroll
     for (int t = 0; t < NR; ++t) {
-      const int j = c0 + t * 8 + gid;
-      uint4 b = {};
-      if (j < rank) b = __ldg(reinterpret_cast<const uint4*>(Ab + (int64_t)j * K + s * 32));
+      const uint4 v = keep(b[t], c0 + t * 8 + gid < rank);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        mma_bf16(acc[mt][t], a[mt][0].x, a[mt][1].x, a[mt][0].y, a[mt][1].y, b.x, b.y);
-        mma_bf16(acc[mt][t], a[mt][0].z, a[mt][1].z, a[mt][0].w, a[mt][1].w, b.z, b.w);
+        mma_bf16(acc[mt][t], a[2 * mt].x, a[2 * mt + 1].x, a[2 * mt].y, a[2 * mt + 1].y, v.x, v.y);
+        mma_bf16(acc[mt][t], a[2 * mt].z, a[2 * mt + 1].z, a[2 * mt].w, a[2 * mt + 1].w, v.z, v.w);
       }
     }
   }
@@ -121,54 +142,75 @@ __device__ __forceinline__ uint4 keep_ranks(uint4 v, int j, int rank) {
 // below `last`; JS = ceil(r / 32). Column c of a chunk's n8-tile t is column
 // (c / 2) * 8 + 2t + c % 2 of it, so that a thread's sums over the four tiles
 // are eight neighbouring columns of y: one 16-byte access a row. A thread holds
-// eight ranks a step of 32, as hs has them. begin() puts the first chunk's y
-// and B on their way (before hs is known), and every register of them is loaded
-// again for the next chunk as soon as this one has used it.
+// eight ranks a step of 32, as hs has them. y and B come through a ring in
+// shared memory, a warp's own, in which a lane reads back what it copied (no
+// barrier). begin() puts the first kSlots chunks on their way, before hs is
+// known; a slot is filled again once its chunk is done.
 template <int MT, int JS>
 struct Expand {
+  static constexpr int kSlotBytes = (4 * JS + 2 * MT) * 512;
+  // CTAs of an SM that the ring and the registers leave room for
+  static constexpr int kCtas = MT * JS == 1 ? 3 : 2;
+  static constexpr int kSlots = (kCtas == 3 ? 8192 : 12288) / kSlotBytes;
+  static_assert(kSlots >= 1, "a ring holds one chunk at least");
   const uint16_t* y_in;
   uint16_t* y_out;
   const uint16_t* Bt;
   int64_t at[2 * MT];  // this thread's place in its rows of y, -1: no row
   int r, rank, rows;
-  uint4 y[2 * MT], b[JS][4];
+  uint32_t ring;  // this lane's first 16 bytes
 
   template <typename RowOf>
   __device__ __forceinline__ Expand(const LoraParams& p, const uint16_t* Bset, int rank_, int rows_,
-                                    RowOf row_of)
+                                    uint32_t ring_, RowOf row_of)
       : y_in(p.y_in), y_out(p.y_out), r(p.r), rank(rank_), rows(rows_) {
     const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+    ring = ring_ + lane * 16;
 #pragma unroll
     for (int i = 0; i < 2 * MT; ++i)
       at[i] = i * 8 + gid < rows ? (int64_t)row_of(i * 8 + gid) * p.N + 8 * tig : -1;
     Bt = Bset + (int64_t)((gid >> 1) * 8 + (gid & 1)) * r + 8 * tig;
-#pragma unroll
-    for (int js = 0; js < JS; ++js)
-#pragma unroll
-      for (int t = 0; t < 4; ++t) b[js][t] = make_uint4(0, 0, 0, 0);  // (ranks never loaded)
   }
-  __device__ __forceinline__ void fetch_b(int64_t c, int js) {
-    const uint16_t* src = Bt + c * 32 * r + js * 32;
-    if (js * 32 + 8 * (int)(threadIdx.x & 3) < rank) {  // (r is a multiple of 8)
+  // chunk c's ranks 32 js and up of B, and with the last of them its y
+  __device__ __forceinline__ void fetch(int64_t c, int64_t last, int slot, int js) {
+    if (c < last) {
+      const uint32_t to = ring + slot * kSlotBytes;
+      if (js * 32 < rank) {
+        const uint16_t* src = Bt + c * 32 * r + js * 32;
+        // (ranks past the adapter's are dropped: zeros)
+        const bool in = js * 32 + 8 * (int)(threadIdx.x & 3) < rank;  // r is a multiple of 8
 #pragma unroll
-      for (int t = 0; t < 4; ++t) b[js][t] = __ldg(reinterpret_cast<const uint4*>(src + 2 * t * r));
+        for (int t = 0; t < 4; ++t)
+          cp_async16_zfill(to + (js * 4 + t) * 512, in ? src + 2 * t * r : Bt, in ? 16u : 0u);
+      }
+      if (js == JS - 1) {
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i)
+          if (at[i] >= 0) cp_async16_zfill(to + (4 * JS + i) * 512, y_in + at[i] + c * 32, 16u);
+      }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  __device__ __forceinline__ void fetch_y(int64_t c, int i) {
-    if (at[i] >= 0) y[i] = *reinterpret_cast<const uint4*>(y_in + at[i] + c * 32);
+  __device__ __forceinline__ static uint4 piece(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
   }
-  __device__ __forceinline__ void begin(int64_t first, int64_t last) {
-    if (first >= last) return;
+  __device__ __forceinline__ void begin(int64_t first, int64_t last, int64_t step) {
 #pragma unroll
-    for (int i = 0; i < 2 * MT; ++i) fetch_y(first, i);
+    for (int d = 0; d < kSlots; ++d)
 #pragma unroll
-    for (int js = 0; js < JS; ++js) fetch_b(first, js);
+      for (int js = 0; js < JS; ++js) fetch(first + d * step, last, d, js);
   }
   __device__ __forceinline__ void run(const uint16_t (*hs)[kHsLd], int64_t first, int64_t last,
                                       int64_t step) {
     const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+    int slot = 0;
     for (int64_t c = first; c < last; c += step) {
-      const bool more = c + step < last;
+      const uint32_t from = ring + slot * kSlotBytes;
       float acc[MT][4][4];
 #pragma unroll
       for (int m = 0; m < MT; ++m)
@@ -178,32 +220,37 @@ struct Expand {
           for (int q = 0; q < 4; ++q) acc[m][t][q] = 0.f;
 #pragma unroll
       for (int js = 0; js < JS; ++js) {
-        if (js * 32 >= rank) break;
-        const int j = js * 32 + 8 * tig;
-        if (rank & 7) {
-#pragma unroll
-          for (int t = 0; t < 4; ++t) b[js][t] = keep_ranks(b[js][t], j, rank);
-        }
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          if (m * 16 >= rows) break;
-          const uint4 a0 = *reinterpret_cast<const uint4*>(&hs[m * 16 + gid][j]);
-          const uint4 a1 = *reinterpret_cast<const uint4*>(&hs[m * 16 + gid + 8][j]);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kSlots * JS - 1) : "memory");
+        if (js * 32 < rank) {
+          const int j = js * 32 + 8 * tig;
+          uint4 b[4];
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            const uint4 bb = b[js][t];
-            mma_bf16(acc[m][t], a0.x, a1.x, a0.y, a1.y, bb.x, bb.y);
-            mma_bf16(acc[m][t], a0.z, a1.z, a0.w, a1.w, bb.z, bb.w);
+            b[t] = piece(from + (js * 4 + t) * 512);
+            if (rank & 7) b[t] = keep_ranks(b[t], j, rank);
+          }
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            if (m * 16 >= rows) break;
+            const uint4 a0 = *reinterpret_cast<const uint4*>(&hs[m * 16 + gid][j]);
+            const uint4 a1 = *reinterpret_cast<const uint4*>(&hs[m * 16 + gid + 8][j]);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              mma_bf16(acc[m][t], a0.x, a1.x, a0.y, a1.y, b[t].x, b[t].y);
+              mma_bf16(acc[m][t], a0.z, a1.z, a0.w, a1.w, b[t].z, b[t].w);
+            }
           }
         }
-        if (more) fetch_b(c + step, js);
+        // (the lane's own copies only: what it has read it may overwrite)
+        if (js < JS - 1) fetch(c + kSlots * step, last, slot, js);
       }
 #pragma unroll
-      for (int i = 0; i < 2 * MT; ++i) {
+      for (int i = 0; i < 2 * MT; ++i)
         if (at[i] >= 0)
-          *reinterpret_cast<uint4*>(y_out + at[i] + c * 32) = add_row(y[i], acc[i >> 1], i & 1);
-        if (more) fetch_y(c + step, i);
-      }
+          *reinterpret_cast<uint4*>(y_out + at[i] + c * 32) =
+              add_row(piece(from + (4 * JS + i) * 512), acc[i >> 1], i & 1);
+      fetch(c + kSlots * step, last, slot, JS - 1);
+      slot = slot + 1 == kSlots ? 0 : slot + 1;
     }
   }
 };
@@ -228,20 +275,28 @@ __device__ __forceinline__ void st_dsmem_u16(uint32_t addr, uint16_t v) {
 // parts through distributed shared memory, scales them, rounds them once to
 // bf16 (the operand of the product with B: relative 2^-8 of the update at most,
 // below the rounding of y itself where the update is no larger than y) and
-// gives them to all eight; then every CTA updates its columns. B's part is
-// asked into L2 before A x is summed, so that its trip from HBM runs beside
-// it. A slab is a range of columns; each slab sums A x again.
-// Few rows are bound by latency (one row of 3584 x 3584 at rank 16 reads
-// 0.25 MB), many by y0 and y.
+// gives them to all eight; then every CTA updates its columns, the first of
+// which are on their way since its part of A x was done. A slab is a range of
+// columns; each slab sums A x again. The slabs are as many as fill the device
+// with the tiles that the ids make, which only the device knows.
+// Bound by its chain of waits: ids, A and x, two cluster barriers, B and y (67
+// rows, 64 adapters of rank 32, 3584 x 18944: 17 us, of which about 2 for the
+// rows, 5 for A x, 2 for the exchange, 6 for 48 MB of B and y). Asking B into L2
+// ahead was slower (19 us: A queues behind it), as were B and y by way of
+// registers, 25 us.
 template <int NR, int MT, int JS, bool PLAN>
-__global__ void __launch_bounds__(kLoraThreads, MT == 1 && NR <= 4 ? 3 : 2)
+__global__ void __launch_bounds__(kLoraThreads, Expand<MT, JS>::kCtas)
 lora_kernel(const LoraParams p) {
   constexpr int kRows = 16 * MT, kRed = 8 * NR + 1;
-  extern __shared__ float red[];  // [kLoraWarps][kRows][kRed]
+  // the warps' rings; before they are filled, red [kLoraWarps][kRows][kRed]
+  extern __shared__ __align__(128) uint8_t rings[];
+  constexpr int kRing = Expand<MT, JS>::kSlots * Expand<MT, JS>::kSlotBytes;
+  float* red = reinterpret_cast<float*>(rings);
   __shared__ float part[kRows][JS * 32];
   __shared__ __align__(16) uint16_t hs[kRows][kHsLd];
   __shared__ uint32_t seen[PLAN ? 1 : kMaxSets / 32];
   __shared__ int rows_of[PLAN ? kRows : kLoraFewRows];
+  __shared__ int sets[PLAN ? 1 : kLoraFewRows];  // a row's adapter, -1: none
   __shared__ int n_rows_s;
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
@@ -249,17 +304,25 @@ lora_kernel(const LoraParams p) {
   const int gid = lane >> 2, tig = lane & 3;
   const int rank_c = (int)cluster_ctarank();
   const int number = (int)(blockIdx.x / kLoraCluster);
-  const int slab = number % p.slabs;
-  int b = number / p.slabs;  // the tile, or the adapter's number in the batch
+  // this cluster's tile (or adapter, by its number in the batch) and slab of
+  // columns: the tiles that there are share the grid's clusters
+  int slabs = 1, slab = 0, b = 0;
+  auto share = [&](int tiles) {
+    slabs = max(1, min(p.max_slabs, p.clusters / tiles));
+    slab = number % slabs;
+    b = number / slabs;
+  };
   // the adapter (-1: rows without one, which are copied) and its rows, in order
   int set = -1, n_rows = 0;
   if constexpr (PLAN) {
     int4 tile;
-    if (b < p.head[1]) {
+    const int n_tiles = p.head[1], n_sorted = p.head[0];
+    share(n_tiles + (int)((p.M - n_sorted + kRows - 1) / kRows));
+    if (b < n_tiles) {
       tile = __ldg(p.tiles + b);
       set = tile.x;
     } else {
-      const int64_t first = p.head[0] + (int64_t)(b - p.head[1]) * kRows;
+      const int64_t first = n_sorted + (int64_t)(b - n_tiles) * kRows;
       tile = make_int4(-1, (int)first, (int)max((int64_t)0, min((int64_t)kRows, p.M - first)), 0);
     }
     n_rows = tile.z;
@@ -267,16 +330,21 @@ lora_kernel(const LoraParams p) {
     if ((int)threadIdx.x < n_rows) rows_of[threadIdx.x] = __ldg(p.order + tile.y + threadIdx.x);
   } else {
     const int M = (int)p.M, words = (p.L + 31) / 32;
+    int v = -1;
+    if ((int)threadIdx.x < M) v = __ldg(p.ids + threadIdx.x);
     for (int i = threadIdx.x; i < words; i += kLoraThreads) seen[i] = 0;
     __syncthreads();
     if ((int)threadIdx.x < M) {
-      const int v = __ldg(p.ids + threadIdx.x);
       if (v >= 0 && v < p.L) atomicOr(&seen[v >> 5], 1u << (v & 31));
+      else v = -1;
+      sets[threadIdx.x] = v;
     }
     __syncthreads();
     // the b-th adapter of the batch (its bit, counted from below); one past the
     // last: the rows without an adapter
-    int w = 0;
+    int w = 0, n_sets = 0;
+    for (int i = 0; i < words; ++i) n_sets += __popc(seen[i]);
+    share(n_sets + 1);
     while (w < words && b >= __popc(seen[w])) b -= __popc(seen[w++]);
     if (w == words) {
       if (b > 0 || p.y_in == p.y_out) return;  // (the whole cluster)
@@ -289,9 +357,7 @@ lora_kernel(const LoraParams p) {
       int n = 0;
       for (int i0 = 0; i0 < M; i0 += 32) {
         const int i = i0 + lane;
-        int v = i < M ? __ldg(p.ids + i) : -2;
-        if (i < M && (v < 0 || v >= p.L)) v = -1;
-        const uint32_t hit = __ballot_sync(0xffffffffu, i < M && v == set);
+        const uint32_t hit = __ballot_sync(0xffffffffu, i < M && sets[i] == set);
         if ((hit >> lane) & 1) rows_of[n + __popc(hit & ((1u << lane) - 1))] = i;
         n += __popc(hit);
       }
@@ -301,7 +367,7 @@ lora_kernel(const LoraParams p) {
   __syncthreads();
   if constexpr (!PLAN) n_rows = n_rows_s;
   // this CTA's columns, 32 at a time
-  const int64_t chunks = p.N / 32, parts = (int64_t)p.slabs * kLoraCluster;
+  const int64_t chunks = p.N / 32, parts = (int64_t)slabs * kLoraCluster;
   const int64_t me = (int64_t)slab * kLoraCluster + rank_c;
   const int64_t c_lo = me * chunks / parts, c_hi = (me + 1) * chunks / parts;
   if (set < 0) {
@@ -316,17 +382,15 @@ lora_kernel(const LoraParams p) {
   const int rank = adapter_rank(p, set);
   const float sc = __ldg(p.scale + set);
   const uint16_t* Bset = p.B + (int64_t)set * p.N * p.r;
-  {
-    const uint8_t* from = reinterpret_cast<const uint8_t*>(Bset + c_lo * 32 * p.r);
-    const int64_t bytes = (c_hi - c_lo) * 64 * p.r;
-    for (int64_t i = (int64_t)threadIdx.x * 128; i < bytes; i += (int64_t)kLoraThreads * 128)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i));
-  }
   const int steps = (int)(p.K / 32);
   const int s0 = rank_c * steps / kLoraCluster, s1 = (rank_c + 1) * steps / kLoraCluster;
   const uint16_t* Ab = p.A + (int64_t)set * p.r * p.K + 8 * tig;
+  // All that this CTA reads of A, x and B asked into L2 at once, A first: a first
+  // touch takes 2 us, which each step of A x would wait for in turn.
   for (int t0 = 0; t0 < n_rows; t0 += kRows) {
     const int rows = min(kRows, n_rows - t0);
+    Expand<MT, JS> ex(p, Bset, rank, rows, smem_u32(rings) + warp * kRing,
+                      [&](int i) { return rows_of[t0 + i]; });
     {
       const uint16_t* xr[2 * MT];
 #pragma unroll
@@ -357,6 +421,7 @@ lora_kernel(const LoraParams p) {
         __syncthreads();
       }
     }
+    ex.begin(c_lo + warp, c_hi, kLoraWarps);  // (red has been read)
     cluster_sync_all();  // every CTA's part is in its shared memory, and hs is free
     // an eighth of the rows' sums, in fours of ranks to a thread's row
     const int kr = (rank + 31) & ~31;
@@ -378,19 +443,13 @@ lora_kernel(const LoraParams p) {
 #pragma unroll
       for (int c = 0; c < kLoraCluster; ++c) st_dsmem_u16(map_to_rank(to, c), h);
     }
-    Expand<MT, JS> ex(p, Bset, rank, rows, [&](int i) { return rows_of[t0 + i]; });
-    ex.begin(c_lo + warp, c_hi);
     cluster_sync_all();  // (also the block's barrier) hs is whole; nothing remote follows
     ex.run(hs, c_lo + warp, c_hi, kLoraWarps);
+    if (t0 + kRows < n_rows) __syncthreads();  // (the rings are red's again)
   }
 }
 
 // ---- very many rows: two kernels with A x between them in memory ------------------------
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
-}
-
 // h[split][sorted row][0, rank) = the split's part of A_a x. One CTA a tile of
 // 32 rows and a part of K, which its warps share in 32-wide steps; each warp
 // keeps kShrinkStages - 1 steps of its rows and of A in flight into a ring of
@@ -645,16 +704,28 @@ lora_expand_kernel(const LoraParams p) {
 
 bool lora_few(int64_t M) { return M <= kLoraFewRows; }
 
-int lora_tile(int64_t M) { return M > kLoraManyRows ? kManyTile : kLoraTile; }
+// Whether a batch with a plan takes the two kernels. The cluster kernel holds
+// about 40 tiles at once and repeats its chain of waits for every 40 more, but
+// goes through wide rows of y without a stop, where the two kernels start a CTA
+// a 256 columns. Two kernels / cluster kernel, us: 32 adapters of rank 16,
+// 3584 x 3584: 500 rows 17.3 / 15.8, 1000 rows 20.3 / 32.6; 16 of rank 64: 700
+// rows 27.9 / 23.6, 1000 rows 29.8 / 36.6; 64 of rank 32, 3584 x 18944: 1000
+// rows 84 / 66, 4093 rows 137 / 123; 4 of rank 32, 2048 x 8192: 1000 rows 23.9 /
+// 26.9. A batch of more rows than one that takes them takes them too.
+static bool lora_many(int64_t M, int64_t N, int L) {
+  return std::min<int64_t>(L, M) + M / kLoraTile > 44 && (N < 8192 || M > 64LL * L);
+}
 
-int lora_splits(int64_t M, int64_t K) {
-  if (M <= kLoraManyRows) return 0;
-  // parts of K so that about two CTAs an SM run, each of two steps a warp or more
-  int64_t s = 304 / (M / kLoraTile + 1);
+// Parts of K of the first kernel: about two CTAs an SM, each of two steps a warp
+// or more.
+static int lora_splits(int64_t M, int64_t K) {
+  int64_t s = kManyCtas / (M / kLoraTile + 1);
   const int64_t most = K / (64 * kShrinkWarps);
   if (s > most) s = most;
   return s < 1 ? 1 : (int)s;
 }
+
+int64_t lora_h_rows(int64_t M) { return std::max<int64_t>(M, kManyCtas * kLoraTile); }
 
 template <int NR>
 static cudaError_t launch_shrink(const LoraParams& p, int64_t tiles, cudaStream_t st) {
@@ -667,11 +738,18 @@ static cudaError_t launch_shrink(const LoraParams& p, int64_t tiles, cudaStream_
 }
 
 template <int NR, int MT, int JS, bool PLAN>
-static cudaError_t launch_lora_kernel(const LoraParams& p, int64_t clusters, cudaStream_t st) {
-  constexpr size_t kSmem = (size_t)kLoraWarps * 16 * MT * (8 * NR + 1) * 4;
+static cudaError_t launch_lora_kernel(LoraParams p, int64_t most, cudaStream_t st) {
+  using Ex = Expand<MT, JS>;
+  constexpr int kRing = Ex::kSlots * Ex::kSlotBytes, kRed = 16 * MT * (8 * NR + 1) * 4;
+  constexpr size_t kSmem = (size_t)kLoraWarps * (kRing > kRed ? kRing : kRed);
   auto kern = lora_kernel<NR, MT, JS, PLAN>;
   static SmemOptIn opt_in;
   if (cudaError_t e = opt_in.ensure(kern, kSmem); e != cudaSuccess) return e;
+  // clusters for every tile there could be, or for all SMs, which the tiles that
+  // there are share
+  p.clusters = device_sm_count() * Ex::kCtas / kLoraCluster;
+  const int64_t clusters = std::max(most, std::min<int64_t>(most * p.max_slabs, p.clusters));
+  if (clusters * kLoraCluster >= (1LL << 31)) return cudaErrorNotSupported;
   PdlConfig c(dim3((unsigned)(clusters * kLoraCluster), 1, 1), kLoraThreads, kSmem, st);
   cudaLaunchAttribute attr[2];
   attr[0] = c.attr[0];
@@ -685,11 +763,11 @@ static cudaError_t launch_lora_kernel(const LoraParams& p, int64_t clusters, cud
 }
 
 template <int MT, bool PLAN>
-static cudaError_t launch_lora_rank(const LoraParams& p, int64_t clusters, cudaStream_t st) {
-  return p.r <= 16   ? launch_lora_kernel<2, MT, 1, PLAN>(p, clusters, st)
-         : p.r <= 32 ? launch_lora_kernel<4, MT, 1, PLAN>(p, clusters, st)
-         : p.r <= 64 ? launch_lora_kernel<8, MT, 2, PLAN>(p, clusters, st)
-                     : launch_lora_kernel<8, MT, 4, PLAN>(p, clusters, st);
+static cudaError_t launch_lora_rank(const LoraParams& p, int64_t most, cudaStream_t st) {
+  return p.r <= 16   ? launch_lora_kernel<2, MT, 1, PLAN>(p, most, st)
+         : p.r <= 32 ? launch_lora_kernel<4, MT, 1, PLAN>(p, most, st)
+         : p.r <= 64 ? launch_lora_kernel<8, MT, 2, PLAN>(p, most, st)
+                     : launch_lora_kernel<8, MT, 4, PLAN>(p, most, st);
 }
 
 cudaError_t launch_lora(const LoraArgs& a, cudaStream_t st) {
@@ -713,20 +791,16 @@ cudaError_t launch_lora(const LoraArgs& a, cudaStream_t st) {
   const bool few = lora_few(a.M);
   // (the rows without an adapter make at most ceil(M / tile) tiles more)
   const int64_t sets = a.L < a.M ? a.L : a.M;
-  const int64_t work = few ? sets : a.M / kLoraTile + 1;  // clusters that multiply, about
-  const int bt = lora_tile(a.M);
+  const bool many = lora_many(a.M, a.N, a.L);
+  const int bt = many ? kManyTile : kLoraTile;
   const int64_t most = few ? sets + 1 : plan_max_tiles(a.M, a.L, bt) + (a.M + bt - 1) / bt;
-  // column slabs: enough clusters for two CTAs an SM, none under 2048 columns
-  int64_t slabs = (a.N + 2047) / 2048;
-  const int64_t want = (38 + work - 1) / work;
-  if (slabs > want) slabs = want;
-  p.slabs = (int)slabs;
-  if (most * slabs * kLoraCluster >= (1LL << 31)) return cudaErrorNotSupported;
-  if (few) return launch_lora_rank<1, false>(p, most * slabs, st);
+  // slabs of 2048 columns at least
+  p.max_slabs = (int)((a.N + 2047) / 2048);
+  if (few) return launch_lora_rank<1, false>(p, most, st);
   cudaError_t e = launch_plan(a.ids, a.M, a.L, bt, a.plan, st);
   if (e != cudaSuccess) return e;
+  if (!many) return launch_lora_rank<2, true>(p, most, st);
   p.splits = lora_splits(a.M, a.K);
-  if (p.splits == 0) return launch_lora_rank<2, true>(p, most * slabs, st);
   p.h = a.h;
   const int64_t tiles = plan_max_tiles(a.M, a.L, bt) * (kManyTile / kLoraTile);
   e = a.r <= 16   ? launch_shrink<2>(p, tiles, st)

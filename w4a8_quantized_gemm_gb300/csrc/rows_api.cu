@@ -64,8 +64,9 @@ size_t carve_lora(void* ws, LoraArgs& a) {
     c.take<int>(1);  // (needs none; a size of zero would say "refused")
     return c.used;
   }
-  carve_plan(c, a.plan, a.M, a.L, plan_max_tiles(a.M, a.L, lora_tile(a.M)), false);
-  a.h = c.take<float>(lora_splits(a.M, a.K) * a.M * a.r);
+  // (for either way of a planned batch, so that a batch of fewer rows fits too)
+  carve_plan(c, a.plan, a.M, a.L, plan_max_tiles(a.M, a.L, kLoraTile), false);
+  a.h = c.take<float>(lora_h_rows(a.M) * a.r);
   return c.used;
 }
 
