@@ -573,22 +573,23 @@ __global__ void __launch_bounds__(kLoraThreads, 2)
 lora_expand_kernel(const LoraParams p) {
   constexpr int LD = JS * 32 + 8;  // padded row of h: 16-byte rows, no bank conflicts
   __shared__ __align__(16) uint16_t hs[kManyTile][LD];
-  griddep_wait();
-  if (threadIdx.x == 0) griddep_launch_dependents();
-  const int n_tiles = p.head[1];
+  // Every block of the first kernel waited for the plan before it let this one
+  // start, so the plan, y and the weights are there and are asked for before
+  // the wait (past L1: another kernel wrote them while this SM was busy).
+  const int n_tiles = __ldcg(p.head + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
   int4 tile;
   int rank = 0;
   if ((int)blockIdx.x < n_tiles) {
-    tile = __ldg(p.tiles + blockIdx.x);
-    if (tile.z == 0) return;
+    tile = __ldcg(p.tiles + blockIdx.x);
+    if (tile.z == 0) return griddep_wait();  // (a grid's end follows that of the one before)
     rank = adapter_rank(p, tile.x);
   } else {
     // tiles past the table copy the rows without an adapter, which the plan
     // lists last (nothing to do where y is updated in place)
-    const int64_t first = p.head[0] + (int64_t)((int)blockIdx.x - n_tiles) * kManyTile;
-    if (first >= p.M || p.y_in == p.y_out) return;
+    const int64_t first = __ldcg(p.head) + (int64_t)((int)blockIdx.x - n_tiles) * kManyTile;
+    if (first >= p.M || p.y_in == p.y_out) return griddep_wait();
     tile = make_int4(0, (int)first, (int)min((int64_t)kManyTile, p.M - first), 0);
   }
   const int64_t c = (int64_t)blockIdx.y * kLoraWarps + warp;  // this warp's 32 columns
@@ -623,16 +624,18 @@ lora_expand_kernel(const LoraParams p) {
     for (int half = 0; half < 2; ++half) {
       const int row = m * 16 + half * 8 + gid;
       at[slot][half] = in && row < tile.z
-                           ? (int64_t)__ldg(p.order + tile.y + row) * p.N + c * 32 + 8 * tig
+                           ? (int64_t)__ldcg(p.order + tile.y + row) * p.N + c * 32 + 8 * tig
                            : -1;
     }
 #pragma unroll
     for (int half = 0; half < 2; ++half)
       if (at[slot][half] >= 0)
-        y[slot][half] = *reinterpret_cast<const uint4*>(p.y_in + at[slot][half]);
+        y[slot][half] = __ldcg(reinterpret_cast<const uint4*>(p.y_in + at[slot][half]));
   };
 #pragma unroll
   for (int m = 0; m < kExpandAhead; ++m) fetch(m, m);
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
   if (rank > 0) {
     // a thread takes four ranks of a row (r is a multiple of 8)
     const float sc = __ldg(p.scale + tile.x);
