@@ -78,7 +78,8 @@ struct RgCfg {
   static constexpr int kAsAt = kOutAt + kOutBytes;
   static constexpr int kBarAt = kAsAt + BT * 4;
   static constexpr int kFirstAt = kBarAt + 512;  // row tiles below each set
-  static constexpr int kSmem = kFirstAt + (kMaxSets + 4) * 4 + 1024;
+  static constexpr int kOffsetAt = kFirstAt + (kMaxSets + 4) * 4;  // rows below each set
+  static constexpr int kSmem = kOffsetAt + (kMaxSets + 4) * 4 + 1024;
   static_assert(kSmem <= kMaxSmem && kSmem > kMaxSmem / 2, "shared memory of one CTA an SM");
 };
 
@@ -136,6 +137,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_constant
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarAt + 496);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBarAt + 500);
   int* first_tile = reinterpret_cast<int*>(smem + C::kFirstAt);
+  int* offset = reinterpret_cast<int*>(smem + C::kOffsetAt);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < XS; ++s) {
@@ -161,14 +163,19 @@ ragged_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_constant
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
-  griddep_wait();  // the plan and the rows belong to the stream's order
-  if (threadIdx.x == 0) griddep_launch_dependents();
+  // The plan was there before the kernel in front of this one began (its blocks
+  // wait first thing), so the units and the weights need no wait; the rows and
+  // their scales, and what this kernel writes, do (rows producer, drains).
   if (warp == 0) {
     int below = 0;
     for (int e0 = 0; e0 < p.sets; e0 += 32) {
       const int e = e0 + lane;
       int t = 0;
-      if (e < p.sets) t = (p.offset[e + 1] - p.offset[e] + BT - 1) / BT;
+      if (e < p.sets) {
+        const int row = __ldcg(p.offset + e);
+        offset[e] = row;
+        t = (__ldcg(p.offset + e + 1) - row + BT - 1) / BT;
+      }
       int incl = t;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -178,7 +185,10 @@ ragged_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_constant
       if (e < p.sets) first_tile[e] = below + incl - t;
       below += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) first_tile[p.sets] = below;
+    if (lane == 0) {
+      first_tile[p.sets] = below;
+      offset[p.sets] = __ldcg(p.offset + p.sets);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -208,8 +218,8 @@ ragged_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_constant
     const int local = u - first * p.n_tiles;
     const int t = local / tiles;
     Unit r;
-    r.row0 = p.offset[lo] + (local - t * tiles) * BT;
-    r.rows = min(BT, p.offset[lo + 1] - r.row0);
+    r.row0 = offset[lo] + (local - t * tiles) * BT;
+    r.rows = min(BT, offset[lo + 1] - r.row0);
     r.n0 = t;
     r.rec0 = p.packed + ((int64_t)lo * p.n_tiles + t) * G * 8512;
     return r;
@@ -257,6 +267,8 @@ ragged_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_constant
   auto row_role = [&] {
     // ---------------------------------------------------------------- rows
     if (lane == 0) {
+      griddep_wait();
+      griddep_launch_dependents();
       int issued = 0, gi = 0, k = 0;
       Unit un{};
       if (n_items > 0) un = unit_at(0);
@@ -408,6 +420,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_constant
   };
   auto drain_role = [&] {
     // ---------------------------------------------------------------- drains
+    griddep_wait();
     const int r = (warp & 3) * 32 + lane;
     const int wg = warp >> 2;
     const int col0 = wg * HB;
