@@ -85,8 +85,20 @@ struct StreamParams {
   int T, k, E, N, G;
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// A copy of weights, which are read once a call: they leave L2 before what the
+// kernels hand on to each other does (layers from HBM: 33 tokens of 64 experts,
+// W4A8, 99.1 -> 96.1 us, one token 21.1 -> 20.7; a layer of 100 MB that stays in
+// L2 from call to call loses 5 % at 12 tokens).
+__device__ __forceinline__ uint64_t weights_policy() {
+  uint64_t policy;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  return policy;
+}
+__device__ __forceinline__ void cp_async16_weights(uint32_t dst, const void* src,
+                                                   uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "l"(policy)
+               : "memory");
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -141,6 +153,7 @@ struct Stream {
   const uint8_t* ring;
   int w_off, m_off;  // this lane's bytes of a record
   int put = 0;
+  uint64_t policy = weights_policy();
 
   __device__ __forceinline__ Stream(uint8_t* r, int rbase) : ring(r) {
     const int lane = threadIdx.x & 31;
@@ -162,7 +175,7 @@ struct Stream {
       const uint32_t st = ring_at + put * kStageBytes;
 #pragma unroll
       for (int c = 0; c < 4; ++c)  // (rows of chunk c exchanged: conflict-free fragments)
-        cp_async16(st + (c * 32 + (lane ^ (2 * c))) * 16, rec + w_off + 2048 * c);
+        cp_async16_weights(st + (c * 32 + (lane ^ (2 * c))) * 16, rec + w_off + 2048 * c, policy);
       if (lane < 20) cp_async4(st + 2048 + lane * 4, rec + m_off);
       put = put + 1 == kStages ? 0 : put + 1;
     }
