@@ -49,6 +49,29 @@ __device__ __forceinline__ float clean_logit(float l) {
 }
 __device__ __forceinline__ float sigmoid_rn(float l) { return __frcp_rn(1.f + expf(-l)); }
 
+// A lane's keys, largest first (Batcher's merge exchange).
+template <int V>
+__device__ __forceinline__ void sort_down(uint32_t (&v)[V]) {
+#pragma unroll
+  for (int p = 1; p < V; p *= 2) {
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2) {
+#pragma unroll
+      for (int j = k % p; j + k < V; j += 2 * k) {
+#pragma unroll
+        for (int i = 0; i < k; ++i) {
+          const int a = i + j, b = a + k;
+          if (b < V && a / (2 * p) == b / (2 * p)) {
+            const uint32_t hi = max(v[a], v[b]);
+            v[b] = min(v[a], v[b]);
+            v[a] = hi;
+          }
+        }
+      }
+    }
+  }
+}
+
 template <int V>
 __global__ void __launch_bounds__(32 * kRouteWarps)
 route_kernel(const RouteParams p) {
@@ -193,25 +216,37 @@ route_kernel(const RouteParams p) {
         if (e0 + i < p.E && !((keep >> ((e0 + i) / p.per_group)) & 1)) key[i] = 0;
     }
   }
-  int my_id = 0;
+  // k times the best of the lanes' best; lane j remembers pick j's key and lane
+  // (and, of equal keys in a row out of one lane, which of them it is)
+  uint32_t best[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) best[i] = key[i];
+  sort_down<V>(best);
+  uint32_t my_key = 0, last = 0;
+  int my_lane = 0, my_nth = 0, from = -1, nth = 0;
   for (int j = 0; j < p.k; ++j) {
-    uint32_t best = key[0];
-#pragma unroll
-    for (int i = 1; i < V; ++i) best = max(best, key[i]);
-    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-    const int who = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
-    int at = 0;
-#pragma unroll
-    for (int i = V - 1; i >= 0; --i)
-      if (key[i] == top) at = i;
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best[0]);
+    const int who = __ffs(__ballot_sync(0xffffffffu, best[0] == top)) - 1;
+    nth = top == last && who == from ? nth + 1 : 0;
+    last = top;
+    from = who;
+    if (lane == j) {
+      my_key = top;
+      my_lane = who;
+      my_nth = nth;
+    }
     if (lane == who) {
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (i == at) key[i] = 0;
+      for (int i = 0; i + 1 < V; ++i) best[i] = best[i + 1];
+      best[V - 1] = 0;
     }
-    const int id = who * V + __shfl_sync(0xffffffffu, at, who);
-    if (lane == j) my_id = id;
   }
+  uint32_t equal = 0;  // the picked lane's experts of that key
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    equal |= (__shfl_sync(0xffffffffu, key[i], my_lane) == my_key ? 1u : 0u) << i;
+  for (; my_nth > 0; --my_nth) equal &= equal - 1;
+  const int my_id = lane < p.k ? my_lane * V + __ffs(equal) - 1 : 0;
   float w = 0.f;
   if (lane < p.k) {
     const float l = clean_logit(p.bf16 ? bf16_bits_to_f32(__ldg(row16 + my_id)) : __ldg(row32 + my_id));
