@@ -736,29 +736,23 @@ __device__ __forceinline__ float row_scale(float a) {
     return __fdiv_rn(a, 127.0f);
   }
 }
-// Eight neighbouring values of a row, bf16 or fp32.
+// Eight neighbouring values of a row, bf16 or fp32, as they lie in memory.
 template <typename X>
 struct Eight {
-  float q[8];
+  uint4 v[sizeof(X) / 2];
   __device__ __forceinline__ void load(const X* row, int64_t i) {
-    if constexpr (sizeof(X) == 4) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(row) + 2 * i);
-      const float4 b = __ldg(reinterpret_cast<const float4*>(row) + 2 * i + 1);
-      q[0] = a.x; q[1] = a.y; q[2] = a.z; q[3] = a.w;
-      q[4] = b.x; q[5] = b.y; q[6] = b.z; q[7] = b.w;
-    } else {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(row) + i);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        q[2 * j] = __uint_as_float(w[j] << 16);
-        q[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-      }
-    }
+    for (int q = 0; q < (int)sizeof(X) / 2; ++q)
+      v[q] = __ldg(reinterpret_cast<const uint4*>(row) + i * (sizeof(X) / 2) + q);
+  }
+  __device__ __forceinline__ float value(int j) const {
+    if constexpr (sizeof(X) == 4) return __uint_as_float(word_of(v[j >> 2], j & 3));
+    const uint32_t w = word_of(v[0], j >> 1);
+    return __uint_as_float((j & 1) ? w & 0xFFFF0000u : w << 16);
   }
   __device__ __forceinline__ float absmax(float m) const {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(q[j]));
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(value(j)));
     return m;
   }
 };
@@ -769,7 +763,7 @@ __device__ __forceinline__ uint4 row_f16(const Eight<X>& v, float s, float inv, 
   uint32_t o[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    float q0 = v.q[2 * j], q1 = v.q[2 * j + 1];
+    float q0 = v.value(2 * j), q1 = v.value(2 * j + 1);
     if constexpr (FORM == kPowerForm) {
       q0 *= inv;
       q1 *= inv;
@@ -804,13 +798,13 @@ __device__ __forceinline__ float row_max(float m, float* part) {
 }
 
 constexpr int kRowThreads = 128;
-constexpr int kRowVecs = 4;  // eights of its row a thread keeps
 
 // Rows [0, rows) (or those below head[0], where head is given) of x [.][K].
 template <int R, QuantForm FORM, typename X>
 __global__ void __launch_bounds__(kRowThreads)
 quant_rows_kernel(const X* __restrict__ x, const int* __restrict__ head, int64_t rows, int64_t K,
                   uint16_t* __restrict__ codes, float* __restrict__ scales) {
+  constexpr int kRowVecs = sizeof(X) == 4 ? 6 : 8;  // eights of its row a thread keeps
   __shared__ float part[kRowThreads / 32];
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
