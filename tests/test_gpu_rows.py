@@ -481,3 +481,55 @@ def test_w4a8_linear_lora(M):
     got = eg.w4a8_linear_lora(x, packed, N, ad, ids)
     ref, bound = lora_ref(base, x, ad, ids)
     assert ((got.double() - ref).abs() <= bound).all()
+
+
+# ------------------------------------------------ inputs that change between calls ---
+# Kernels that begin before the one in front of them has ended must still see
+# what was written just before the call, and not what the last call left.
+
+@pytest.mark.parametrize("M", [1, 5, 100, 260, 1300])
+def test_w4a8_linear_lora_follows_inputs_rewritten_in_place(M):
+    N, K, L, r = 512, 768, 20, 24
+    cases = [lora_case(20 + i, M, N, K, L, r, True) for i in range(3)]
+    packed = eg.pack_w4(*w4(gen(1), N, K))
+    ad = cases[0][2]
+    x, ids = torch.empty_like(cases[0][1]), torch.empty_like(cases[0][3])
+    ws = eg.w4a8_linear_lora_workspace(M, N, K, ad, DEV)
+    want = []
+    for _, xi, _, idi in cases:
+        y = eg.w4a8_linear(xi, packed, N)
+        want.append(eg.lora_add(y, xi, ad, idi))
+        torch.cuda.synchronize()
+    got = []
+    for i in range(24):
+        x.copy_(cases[i % 3][1])
+        ids.copy_(cases[i % 3][3])
+        got.append(eg.w4a8_linear_lora(x, packed, N, ad, ids, workspace=ws))
+    torch.cuda.synchronize()
+    for i, y in enumerate(got):
+        assert torch.equal(y, want[i % 3]), i
+    assert eg.device_status() == 0
+
+
+@pytest.mark.parametrize("variant", VARIANTS)
+@pytest.mark.parametrize("T,path", [(1, eg.PATH_AUTO), (7, eg.PATH_AUTO), (30, eg.PATH_GEMV),
+                                    (90, eg.PATH_TC), (900, eg.PATH_TC)])
+def test_experts_follow_inputs_rewritten_in_place(variant, T, path):
+    E, k, H, I = 8, 2, 512, 256
+    cases = [experts_case(30 + i, T, E, k, H, I) for i in range(3)]
+    layer = eg.moe_pack(*cases[0][3], *cases[0][4])
+    x, ids, w = (torch.empty_like(t) for t in cases[0][:3])
+    ws = eg.moe_workspace(T, k, E, H, I, variant, DEV, path)
+    want = []
+    for c in cases:
+        want.append(eg.moe_experts(*c[:3], layer, variant=variant, path=path))
+        torch.cuda.synchronize()
+    got = []
+    for i in range(24):
+        for to, new in zip((x, ids, w), cases[i % 3][:3]):
+            to.copy_(new)
+        got.append(eg.moe_experts(x, ids, w, layer, variant=variant, path=path, workspace=ws))
+    torch.cuda.synchronize()
+    for i, y in enumerate(got):
+        assert torch.equal(y, want[i % 3]), i
+    assert eg.device_status() == 0

@@ -350,7 +350,7 @@ int set_last_error(int code, const char* msg) { return fail(code, "%s", msg); }
 // Quantize x into `ws` (layout above) and run the W4A8 GEMM of the linears in
 // `segs` (N output rows in all) on `use`.
 int run_linear_segs(const uint16_t* x_bf16, const SegTable& segs, int64_t M, int64_t N, int64_t K,
-                    uint8_t* ws, int use, cudaStream_t st) {
+                    uint8_t* ws, int use, cudaStream_t st, const LoraArgs* lora = nullptr) {
   float* a_s = reinterpret_cast<float*>(ws);
   int32_t* asum = reinterpret_cast<int32_t*>(ws + align256((size_t)(4 * M)));
   uint8_t* codes = reinterpret_cast<uint8_t*>(asum) + align256((size_t)(4 * M * (K / 128)));
@@ -358,6 +358,8 @@ int run_linear_segs(const uint16_t* x_bf16, const SegTable& segs, int64_t M, int
   void* a_tc = use == EGOPQ_PATH_TC ? codes : nullptr;
   cudaError_t e = launch_quant_act(x_bf16, M, K, a_q, a_s, asum, a_tc, st);
   if (e != cudaSuccess) return cuda_fail(e, "quant_act launch");
+  if (lora && (e = launch_lora_plan(*lora, st)) != cudaSuccess)
+    return cuda_fail(e, "adapters' plan launch");
   GemmArgs a{};
   a.variant = kW4A8;
   a.M = M;
@@ -377,9 +379,10 @@ int run_linear_segs(const uint16_t* x_bf16, const SegTable& segs, int64_t M, int
   return e == cudaSuccess ? EGOPQ_OK : cuda_fail(e, "gemm launch");
 }
 
-// The one-call linear of a single weight.
+// The one-call linear of a single weight (and, where `lora` is given, the plan
+// of the adapters beside it).
 int run_linear(const uint16_t* x_bf16, const void* packed, int64_t M, int64_t N, int64_t K,
-               uint16_t* y_bf16, uint8_t* ws, int use, cudaStream_t st) {
+               uint16_t* y_bf16, uint8_t* ws, int use, cudaStream_t st, const LoraArgs* lora) {
   SegTable segs{};
   segs.count = 1;
   segs.tile0[0] = 0;
@@ -387,7 +390,7 @@ int run_linear(const uint16_t* x_bf16, const void* packed, int64_t M, int64_t N,
   segs.packed[0] = static_cast<const uint8_t*>(packed);
   segs.y[0] = y_bf16;
   segs.N[0] = N;
-  return run_linear_segs(x_bf16, segs, M, N, K, ws, use, st);
+  return run_linear_segs(x_bf16, segs, M, N, K, ws, use, st, lora);
 }
 }  // namespace egopq
 

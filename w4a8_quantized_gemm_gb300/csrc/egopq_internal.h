@@ -252,8 +252,14 @@ struct RouteArgs {
   float scale;
 };
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t st);
+//
+// An early kernel (here, quant_rows_kernel, lora_kernel) does its work, or the
+// first part of it, before it waits for the kernel in front of it, whose results
+// it does not read. It may where every block of that kernel waits first thing:
+// then all that was in the stream before is done, and what it reads of that it
+// reads past L1.
 cudaError_t launch_plan(const int32_t* ids, int64_t n, int S, int bt, const RowPlan& plan,
-                        cudaStream_t st);
+                        cudaStream_t st, bool early = false);
 
 // How a call's products run (experts.cu).
 enum ExpertsWay { kExpertsFew, kExpertsStream, kExpertsTensor };
@@ -326,7 +332,14 @@ bool lora_few(int64_t M);
 constexpr int kLoraTile = 32;  // rows of the smallest tile of a planned batch
 // Rows of r fp32 sums that lie in memory between two kernels, at most.
 int64_t lora_h_rows(int64_t M);
-cudaError_t launch_lora(const LoraArgs& a, cudaStream_t st);
+// The plan of a batch that has one, early (see launch_plan); launch_lora then
+// gets `beside`: the adapters' product begins beside the kernels in front of it,
+// which write y_in but not the rest.
+cudaError_t launch_lora_plan(const LoraArgs& a, cudaStream_t st);
+cudaError_t launch_lora(const LoraArgs& a, cudaStream_t st, bool beside = false);
+int run_linear(const uint16_t* x_bf16, const void* packed, int64_t M, int64_t N, int64_t K,
+               uint16_t* y_bf16, uint8_t* ws, int use, cudaStream_t st,
+               const LoraArgs* lora = nullptr);
 
 // Weights [E][2I][K] with I gate rows and then I up rows a set, packed with
 // the two interleaved sixteen rows at a time.

@@ -743,7 +743,7 @@ struct Eight {
   __device__ __forceinline__ void load(const X* row, int64_t i) {
 #pragma unroll
     for (int q = 0; q < (int)sizeof(X) / 2; ++q)
-      v[q] = __ldg(reinterpret_cast<const uint4*>(row) + i * (sizeof(X) / 2) + q);
+      v[q] = __ldcg(reinterpret_cast<const uint4*>(row) + i * (sizeof(X) / 2) + q);
   }
   __device__ __forceinline__ float value(int j) const {
     if constexpr (sizeof(X) == 4) return __uint_as_float(word_of(v[j >> 2], j & 3));
@@ -800,13 +800,16 @@ __device__ __forceinline__ float row_max(float m, float* part) {
 constexpr int kRowThreads = 128;
 
 // Rows [0, rows) (or those below head[0], where head is given) of x [.][K].
+// early: see launch_plan.
 template <int R, QuantForm FORM, typename X>
 __global__ void __launch_bounds__(kRowThreads)
 quant_rows_kernel(const X* __restrict__ x, const int* __restrict__ head, int64_t rows, int64_t K,
-                  uint16_t* __restrict__ codes, float* __restrict__ scales) {
-  constexpr int kRowVecs = sizeof(X) == 4 ? 6 : 8;  // eights of its row a thread keeps
+                  uint16_t* __restrict__ codes, float* __restrict__ scales, bool early) {
+  // eights of its row a thread keeps (a block a row has few: every test of one
+  // that is not there costs a small batch: 8 instead of 4 are 0.4 us)
+  constexpr int kRowVecs = R > 32 ? 4 : sizeof(X) == 4 ? 6 : 8;
   __shared__ float part[kRowThreads / 32];
-  griddep_wait();
+  if (!early) griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   const int64_t m = (int64_t)blockIdx.x * (kRowThreads / R) + threadIdx.x / R;
   if (head) rows = head[0];
@@ -842,17 +845,18 @@ quant_rows_kernel(const X* __restrict__ x, const int* __restrict__ head, int64_t
     u.load(src, i);
     put(u, i);
   }
+  if (early) griddep_wait();  // (a grid's end follows that of the one before)
 }
 
-// bf16 rows in the order of unit_place (W4A16, stream).
+// bf16 rows in the order of unit_place (W4A16, stream); early: see launch_plan.
 __global__ void __launch_bounds__(kRowThreads)
 place_rows_kernel(const uint16_t* __restrict__ x, int64_t K, uint16_t* __restrict__ out) {
-  griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   const int64_t at = (int64_t)blockIdx.x * K;
   for (int64_t i = threadIdx.x; i < K / 8; i += kRowThreads)
     reinterpret_cast<uint4*>(out + at)[unit_place(i)] =
-        __ldg(reinterpret_cast<const uint4*>(x + at) + i);
+        __ldcg(reinterpret_cast<const uint4*>(x + at) + i);
+  griddep_wait();  // (a grid's end follows that of the one before)
 }
 
 // rows[pos[t, j]] = token t's activations as fp16 and rows_s their scale, for
@@ -893,16 +897,18 @@ scatter_rows_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ 
 // ---- launches -----------------------------------------------------------------------
 template <QuantForm FORM, typename X>
 static cudaError_t launch_quant_rows(const X* x, const int* head, int64_t rows, int64_t K,
-                                     uint16_t* codes, float* scales, cudaStream_t st) {
+                                     uint16_t* codes, float* scales, cudaStream_t st,
+                                     bool early = false) {
   // a warp a row where there are rows for every warp of the GPU (32768 x 1280:
   // a block a row leaves most of its threads without work), else a block
   if (rows >= 4096 && K <= 2048) {
     PdlConfig c(dim3((unsigned)((rows + 3) / 4), 1, 1), kRowThreads, 0, st);
-    return cudaLaunchKernelEx(&c.cfg, quant_rows_kernel<32, FORM, X>, x, head, rows, K, codes, scales);
+    return cudaLaunchKernelEx(&c.cfg, quant_rows_kernel<32, FORM, X>, x, head, rows, K, codes,
+                              scales, early);
   }
   PdlConfig c(dim3((unsigned)rows, 1, 1), kRowThreads, 0, st);
   return cudaLaunchKernelEx(&c.cfg, quant_rows_kernel<kRowThreads, FORM, X>, x, head, rows, K, codes,
-                            scales);
+                            scales, early);
 }
 
 template <typename Y>
@@ -1050,8 +1056,10 @@ static cudaError_t run_experts(const ExpertsArgs& a, cudaStream_t st) {
   const int nt = n <= (int64_t)6 * a.E ? 1 : 2;
   cudaError_t e = cudaSuccess;
   if (a.way == kExpertsStream) e = launch_plan(a.ids, n, a.E, 8 * nt, a.plan, st);
+  // (the rows do not depend on the plan: they are quantized, or placed, beside it)
   if (e == cudaSuccess && VARIANT == kW4A8)
-    e = launch_quant_rows<kStreamForm>(a.x, nullptr, a.T, a.H, a.x_q, a.x_s, st);
+    e = launch_quant_rows<kStreamForm>(a.x, nullptr, a.T, a.H, a.x_q, a.x_s, st,
+                                       a.way == kExpertsStream);
   if (e == cudaSuccess && VARIANT == kW4A16 && a.way == kExpertsStream) {
     PdlConfig c(dim3((unsigned)a.T, 1, 1), kRowThreads, 0, st);
     e = cudaLaunchKernelEx(&c.cfg, place_rows_kernel, a.x, a.H, a.x_q);

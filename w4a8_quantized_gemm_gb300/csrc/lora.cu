@@ -66,18 +66,20 @@ struct LoraParams {
   float* h;  // [splits][M][r] partial sums of A x, sorted rows (two kernels)
   int64_t M, N, K;
   int L, r, max_slabs, clusters, splits;
+  bool beside;  // early: y_in alone comes from the kernel in front (launch_plan)
 };
 
 // ranks[a] as a number in [0, r]
 __device__ __forceinline__ int adapter_rank(const LoraParams& p, int a) {
-  return p.ranks ? max(0, min(p.r, __ldg(p.ranks + a))) : p.r;
+  return p.ranks ? max(0, min(p.r, __ldcg(p.ranks + a))) : p.r;
 }
 
 // acc[mt][t] += x rows (two a thread and row tile: xr[2 mt], xr[2 mt + 1], null
 // where there is none) times ranks [c0, c0 + 8 NR) of A over the 32-wide K
 // steps s0, s0 + step, ... below s1. Pointers include the thread's 8 * tig. A
 // step's loads are all issued before its products (missing rows and ranks read
-// the first and are replaced by zeros: no branch between the loads).
+// the first and are replaced by zeros: no branch between the loads; past L1, as
+// the kernel may be early).
 template <int MT, int NR>
 __device__ __forceinline__ void shrink_steps(float (&acc)[MT][NR][4], const uint16_t* const* xr,
                                              const uint16_t* Ab, int64_t K, int c0, int rank,
@@ -96,9 +98,9 @@ __device__ __forceinline__ void shrink_steps(float (&acc)[MT][NR][4], const uint
     uint4 a[2 * MT], b[NR];
 #pragma unroll
     for (int q = 0; q < 2 * MT; ++q)
-      a[q] = __ldg(reinterpret_cast<const uint4*>((xr[q] ? xr[q] : Ab) + (int64_t)s * 32));
+      a[q] = __ldcg(reinterpret_cast<const uint4*>((xr[q] ? xr[q] : Ab) + (int64_t)s * 32));
 #pragma unroll
-    for (int t = 0; t < NR; ++t) b[t] = __ldg(reinterpret_cast<const uint4*>(Aj[t] + s * 32));
+    for (int t = 0; t < NR; ++t) b[t] = __ldcg(reinterpret_cast<const uint4*>(Aj[t] + s * 32));
 #pragma unroll
     for (int q = 0; q < 2 * MT; ++q) a[q] = keep(a[q], xr[q] != nullptr);
 #pragma unroll
@@ -298,8 +300,14 @@ lora_kernel(const LoraParams p) {
   __shared__ int rows_of[PLAN ? kRows : kLoraFewRows];
   __shared__ int sets[PLAN ? 1 : kLoraFewRows];  // a row's adapter, -1: none
   __shared__ int n_rows_s;
-  griddep_wait();
-  if (threadIdx.x == 0) griddep_launch_dependents();
+  auto wait = [] {
+    griddep_wait();
+    if (threadIdx.x == 0) griddep_launch_dependents();
+  };
+  if (!p.beside) wait();
+  auto leave = [&] {  // (a grid's end follows that of the one before)
+    if (p.beside) griddep_wait();
+  };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
   const int rank_c = (int)cluster_ctarank();
@@ -316,22 +324,22 @@ lora_kernel(const LoraParams p) {
   int set = -1, n_rows = 0;
   if constexpr (PLAN) {
     int4 tile;
-    const int n_tiles = p.head[1], n_sorted = p.head[0];
+    const int n_tiles = __ldcg(p.head + 1), n_sorted = __ldcg(p.head);
     share(n_tiles + (int)((p.M - n_sorted + kRows - 1) / kRows));
     if (b < n_tiles) {
-      tile = __ldg(p.tiles + b);
+      tile = __ldcg(p.tiles + b);
       set = tile.x;
     } else {
       const int64_t first = n_sorted + (int64_t)(b - n_tiles) * kRows;
       tile = make_int4(-1, (int)first, (int)max((int64_t)0, min((int64_t)kRows, p.M - first)), 0);
     }
     n_rows = tile.z;
-    if (n_rows == 0 || (set < 0 && p.y_in == p.y_out)) return;  // (the whole cluster)
-    if ((int)threadIdx.x < n_rows) rows_of[threadIdx.x] = __ldg(p.order + tile.y + threadIdx.x);
+    if (n_rows == 0 || (set < 0 && p.y_in == p.y_out)) return leave();  // (the whole cluster)
+    if ((int)threadIdx.x < n_rows) rows_of[threadIdx.x] = __ldcg(p.order + tile.y + threadIdx.x);
   } else {
     const int M = (int)p.M, words = (p.L + 31) / 32;
     int v = -1;
-    if ((int)threadIdx.x < M) v = __ldg(p.ids + threadIdx.x);
+    if ((int)threadIdx.x < M) v = __ldcg(p.ids + threadIdx.x);
     for (int i = threadIdx.x; i < words; i += kLoraThreads) seen[i] = 0;
     __syncthreads();
     if ((int)threadIdx.x < M) {
@@ -347,7 +355,7 @@ lora_kernel(const LoraParams p) {
     share(n_sets + 1);
     while (w < words && b >= __popc(seen[w])) b -= __popc(seen[w++]);
     if (w == words) {
-      if (b > 0 || p.y_in == p.y_out) return;  // (the whole cluster)
+      if (b > 0 || p.y_in == p.y_out) return leave();  // (the whole cluster)
     } else {
       uint32_t m = seen[w];
       for (; b > 0; --b) m &= m - 1;
@@ -371,6 +379,7 @@ lora_kernel(const LoraParams p) {
   const int64_t me = (int64_t)slab * kLoraCluster + rank_c;
   const int64_t c_lo = me * chunks / parts, c_hi = (me + 1) * chunks / parts;
   if (set < 0) {
+    if (p.beside) wait();
     for (int i = 0; i < n_rows; ++i) {
       const int64_t at = (int64_t)rows_of[i] * p.N;
       for (int64_t v = c_lo * 4 + threadIdx.x; v < c_hi * 4; v += kLoraThreads)
@@ -380,13 +389,11 @@ lora_kernel(const LoraParams p) {
     return;
   }
   const int rank = adapter_rank(p, set);
-  const float sc = __ldg(p.scale + set);
+  const float sc = __ldcg(p.scale + set);
   const uint16_t* Bset = p.B + (int64_t)set * p.N * p.r;
   const int steps = (int)(p.K / 32);
   const int s0 = rank_c * steps / kLoraCluster, s1 = (rank_c + 1) * steps / kLoraCluster;
   const uint16_t* Ab = p.A + (int64_t)set * p.r * p.K + 8 * tig;
-  // All that this CTA reads of A, x and B asked into L2 at once, A first: a first
-  // touch takes 2 us, which each step of A x would wait for in turn.
   for (int t0 = 0; t0 < n_rows; t0 += kRows) {
     const int rows = min(kRows, n_rows - t0);
     Expand<MT, JS> ex(p, Bset, rank, rows, smem_u32(rings) + warp * kRing,
@@ -421,6 +428,7 @@ lora_kernel(const LoraParams p) {
         __syncthreads();
       }
     }
+    if (p.beside && t0 == 0) wait();
     ex.begin(c_lo + warp, c_hi, kLoraWarps);  // (red has been read)
     cluster_sync_all();  // every CTA's part is in its shared memory, and hs is free
     // an eighth of the rows' sums, in fours of ranks to a thread's row
@@ -773,7 +781,13 @@ static cudaError_t launch_lora_rank(const LoraParams& p, int64_t most, cudaStrea
                      : launch_lora_kernel<8, MT, 4, PLAN>(p, most, st);
 }
 
-cudaError_t launch_lora(const LoraArgs& a, cudaStream_t st) {
+cudaError_t launch_lora_plan(const LoraArgs& a, cudaStream_t st) {
+  if (lora_few(a.M)) return cudaSuccess;
+  return launch_plan(a.ids, a.M, a.L, lora_many(a.M, a.N, a.L) ? kManyTile : kLoraTile, a.plan, st,
+                     true);
+}
+
+cudaError_t launch_lora(const LoraArgs& a, cudaStream_t st, bool beside) {
   LoraParams p;
   p.y_in = a.y_in;
   p.x = a.x;
@@ -791,6 +805,7 @@ cudaError_t launch_lora(const LoraArgs& a, cudaStream_t st) {
   p.K = a.K;
   p.L = a.L;
   p.r = a.r;
+  p.beside = beside;
   const bool few = lora_few(a.M);
   // (the rows without an adapter make at most ceil(M / tile) tiles more)
   const int64_t sets = a.L < a.M ? a.L : a.M;
@@ -800,8 +815,8 @@ cudaError_t launch_lora(const LoraArgs& a, cudaStream_t st) {
   // slabs of 2048 columns at least
   p.max_slabs = (int)((a.N + 2047) / 2048);
   if (few) return launch_lora_rank<1, false>(p, most, st);
-  cudaError_t e = launch_plan(a.ids, a.M, a.L, bt, a.plan, st);
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
+  if (!beside && (e = launch_plan(a.ids, a.M, a.L, bt, a.plan, st)) != cudaSuccess) return e;
   if (!many) return launch_lora_rank<2, true>(p, most, st);
   p.splits = lora_splits(a.M, a.K);
   p.h = a.h;

@@ -28,8 +28,7 @@
 #include "egopq_internal.h"
 
 namespace egopq {
-int run_linear(const uint16_t* x_bf16, const void* packed, int64_t M, int64_t N, int64_t K,
-               uint16_t* y_bf16, uint8_t* ws, int use, cudaStream_t st);
+
 int set_last_error(int code, const char* msg);
 }  // namespace egopq
 

@@ -312,8 +312,8 @@ constexpr int kPlanThreads = 1024;
 
 template <int PT>
 __global__ void __launch_bounds__(kPlanThreads)
-plan_kernel(const int32_t* __restrict__ ids, int n, int S, int bt, RowPlan plan) {
-  griddep_wait();
+plan_kernel(const int32_t* __restrict__ ids, int n, int S, int bt, RowPlan plan, bool early) {
+  if (!early) griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   __shared__ uint32_t seen[kMaxSets / 32];  // bit s: set s has a row
   __shared__ int warp_eq[32], warp_lt[32];
@@ -332,11 +332,11 @@ plan_kernel(const int32_t* __restrict__ ids, int n, int S, int bt, RowPlan plan)
       int4 u = make_int4(S + 1, S + 1, S + 1, S + 1);
       const int64_t i = i0 + q;
       if (i + 3 < n) {
-        u = __ldg(reinterpret_cast<const int4*>(ids + i));
+        u = __ldcg(reinterpret_cast<const int4*>(ids + i));
       } else if (i < n) {
-        u.x = __ldg(ids + i);
-        if (i + 1 < n) u.y = __ldg(ids + i + 1);
-        if (i + 2 < n) u.z = __ldg(ids + i + 2);
+        u.x = __ldcg(ids + i);
+        if (i + 1 < n) u.y = __ldcg(ids + i + 1);
+        if (i + 2 < n) u.z = __ldcg(ids + i + 2);
       }
       v[q] = u.x;
       v[q + 1] = u.y;
@@ -425,6 +425,7 @@ plan_kernel(const int32_t* __restrict__ ids, int n, int S, int bt, RowPlan plan)
     plan.offset[set] = base;
     if (set == S) plan.head[0] = base;  // rows that have a set
   }
+  if (early) griddep_wait();  // (a grid's end follows that of the one before)
   if (!bt) return;
   // tiles of at most bt rows: set s takes the entries from base / bt + rank up
   // to the next set's first, (base + count) / bt + rank + 1: as many as it
@@ -450,13 +451,13 @@ plan_kernel(const int32_t* __restrict__ ids, int n, int S, int bt, RowPlan plan)
 }
 
 cudaError_t launch_plan(const int32_t* ids, int64_t n, int S, int bt, const RowPlan& plan,
-                        cudaStream_t st) {
+                        cudaStream_t st, bool early) {
   // four picks a thread while that fits one round, else 32
   const bool small = n <= 4 * kPlanThreads;
   const int64_t want = small ? (n + 3) / 4 : kPlanThreads;
   PdlConfig c(dim3((unsigned)(S + 1), 1, 1), (unsigned)((want + 31) / 32 * 32), 0, st);
-  return small ? cudaLaunchKernelEx(&c.cfg, plan_kernel<4>, ids, (int)n, S, bt, plan)
-               : cudaLaunchKernelEx(&c.cfg, plan_kernel<32>, ids, (int)n, S, bt, plan);
+  return small ? cudaLaunchKernelEx(&c.cfg, plan_kernel<4>, ids, (int)n, S, bt, plan, early)
+               : cudaLaunchKernelEx(&c.cfg, plan_kernel<32>, ids, (int)n, S, bt, plan, early);
 }
 
 }  // namespace egopq

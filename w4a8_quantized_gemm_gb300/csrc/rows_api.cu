@@ -58,6 +58,12 @@ size_t carve_experts(void* ws, ExpertsArgs& a) {
   return c.used;
 }
 
+int lora_result(cudaError_t e, int64_t M) {
+  if (e == cudaErrorNotSupported)
+    return fail(EGOPQ_ERR_UNSUPPORTED_SHAPE, "too many rows for one call (M=%lld)", (long long)M);
+  return e == cudaSuccess ? EGOPQ_OK : cuda_fail(e, "adapters launch");
+}
+
 size_t carve_lora(void* ws, LoraArgs& a) {
   Carver c(ws);
   if (lora_few(a.M)) {
@@ -283,10 +289,7 @@ int egopq_lora_add(const uint16_t* y_in, const uint16_t* x_bf16, const uint16_t*
   if (workspace_bytes < need)
     return fail(EGOPQ_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
   if ((rc = check_arch())) return rc;
-  cudaError_t e = launch_lora(a, (cudaStream_t)stream);
-  if (e == cudaErrorNotSupported)
-    return fail(EGOPQ_ERR_UNSUPPORTED_SHAPE, "too many rows for one call (M=%lld)", (long long)M);
-  return e == cudaSuccess ? EGOPQ_OK : cuda_fail(e, "lora_add launch");
+  return lora_result(launch_lora(a, (cudaStream_t)stream), M);
 }
 
 size_t egopq_w4a8_linear_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int group, int L,
@@ -317,11 +320,26 @@ int egopq_w4a8_linear_lora(const uint16_t* x_bf16, const void* packed, const uin
   const size_t need = lin_up + egopq_lora_workspace_bytes(M, N, K, L, r);
   if (workspace_bytes < need)
     return fail(EGOPQ_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
-  rc = egopq_w4a8_linear(x_bf16, packed, M, N, K, group, y_bf16, workspace, lin, path, stream);
-  if (rc) return rc;
-  return egopq_lora_add(y_bf16, x_bf16, A_bf16, B_bf16, scale, ranks, ids, M, N, K, L, r, y_bf16,
-                        static_cast<uint8_t*>(workspace) + lin_up, workspace_bytes - lin_up,
-                        stream);
+  if ((rc = check_arch())) return rc;
+  LoraArgs a{};
+  a.y_in = y_bf16;
+  a.x = x_bf16;
+  a.A = A_bf16;
+  a.B = B_bf16;
+  a.scale = scale;
+  a.ranks = ranks;
+  a.ids = ids;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.L = L;
+  a.r = r;
+  a.y_out = y_bf16;
+  carve_lora(static_cast<uint8_t*>(workspace) + lin_up, a);
+  const cudaStream_t st = (cudaStream_t)stream;
+  rc = run_linear(x_bf16, packed, M, N, K, y_bf16, static_cast<uint8_t*>(workspace),
+                  auto_path(M, kW4A8, path), st, &a);
+  return rc ? rc : lora_result(launch_lora(a, st, true), M);
 }
 
 }  // extern "C"
