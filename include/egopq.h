@@ -384,11 +384,15 @@ int egopq_moe_pack_gate_up(const uint8_t* w_q, const uint16_t* scale_f16, const 
  * x bf16 [T][H], ids int32 and weights fp32 [T][k], out bf16 [T][H] (a token
  * whose picks are all outside [0, E) gives 0). variant EGOPQ_VARIANT_W4A16:
  * bf16 activations; EGOPQ_VARIANT_W4A8: int8 codes of x and of the bf16 gated
- * values, per row as in egopq_quant_act_i8. Accumulation in fp32; the gated
- * values and each pick's output are rounded to bf16 once on the way. H and I
- * multiples of 128 below 2^20, E <= 1024. path: EGOPQ_PATH_GEMV streams the weights for
- * few rows an expert, EGOPQ_PATH_TC runs the tcgen05 products, AUTO picks by
- * the rows an expert has on average. */
+ * values, per row as in egopq_quant_act_i8. Accumulation in fp32. On the way
+ * the gated values are rounded once (to bf16; on W4A16's tensor-core path to
+ * fp16 over a power of two of their row) and, on the tensor-core path, each
+ * pick's output once to bf16. H and I multiples of 128 below 2^20, E <= 1024.
+ * path: EGOPQ_PATH_GEMV streams the weights for few rows an expert,
+ * EGOPQ_PATH_TC runs the tcgen05 products, AUTO picks by the rows an expert has
+ * on average (12 and fewer stream). The tensor-core products hold a weight
+ * s * (q - z) as fp16 (exact integers with the scales beside them in W4A8's gate
+ * and up products): a weight of 65520 and more becomes infinite there. */
 size_t egopq_moe_experts_workspace_bytes(int64_t T, int k, int E, int64_t H, int64_t I, int group,
                                          int variant, int path);
 int egopq_moe_experts(const uint16_t* x_bf16, const int32_t* ids, const float* weights,
@@ -403,7 +407,9 @@ int egopq_moe_experts(const uint16_t* x_bf16, const int32_t* ids, const float* w
  * adapter a uses its first ranks[a] (at most r) rows of A and columns of B,
  * whatever the rest holds. A row whose id is outside [0, L) keeps y_in.
  * r a multiple of 8, at most 128; K and N multiples of 128, N < 2^24,
- * L <= 1024. A x is summed in fp32 and, scaled, rounded to bf16 once. */
+ * L <= 1024. A x is summed in fp32 and, scaled, rounded to bf16 once. A
+ * workspace serves any batch of fewer rows as well (of egopq_moe_experts too,
+ * for the same sizes, variant and path). */
 size_t egopq_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int L, int r);
 int egopq_lora_add(const uint16_t* y_in, const uint16_t* x_bf16, const uint16_t* A_bf16,
                    const uint16_t* B_bf16, const float* scale, const int32_t* ranks,

@@ -740,10 +740,13 @@ __device__ __forceinline__ float row_scale(float a) {
 template <typename X>
 struct Eight {
   uint4 v[sizeof(X) / 2];
-  __device__ __forceinline__ void load(const X* row, int64_t i) {
+  // early: past L1 (see launch_plan)
+  __device__ __forceinline__ void load(const X* row, int64_t i, bool early) {
 #pragma unroll
-    for (int q = 0; q < (int)sizeof(X) / 2; ++q)
-      v[q] = __ldcg(reinterpret_cast<const uint4*>(row) + i * (sizeof(X) / 2) + q);
+    for (int q = 0; q < (int)sizeof(X) / 2; ++q) {
+      const uint4* at = reinterpret_cast<const uint4*>(row) + i * (sizeof(X) / 2) + q;
+      v[q] = early ? __ldcg(at) : __ldg(at);
+    }
   }
   __device__ __forceinline__ float value(int j) const {
     if constexpr (sizeof(X) == 4) return __uint_as_float(word_of(v[j >> 2], j & 3));
@@ -821,13 +824,13 @@ quant_rows_kernel(const X* __restrict__ x, const int* __restrict__ head, int64_t
   float a = 0.f;
 #pragma unroll
   for (int i = 0; i < kRowVecs; ++i)
-    if (t + i * R < nvec) v[i].load(src, t + i * R);
+    if (t + i * R < nvec) v[i].load(src, t + i * R, early);
 #pragma unroll
   for (int i = 0; i < kRowVecs; ++i)
     if (t + i * R < nvec) a = v[i].absmax(a);
   for (int64_t i = t + kRowVecs * R; i < nvec; i += R) {
     Eight<X> u;
-    u.load(src, i);
+    u.load(src, i, early);
     a = u.absmax(a);
   }
   a = row_max<R>(a, part);
@@ -842,7 +845,7 @@ quant_rows_kernel(const X* __restrict__ x, const int* __restrict__ head, int64_t
     if (t + i * R < nvec) put(v[i], t + i * R);
   for (int64_t i = t + kRowVecs * R; i < nvec; i += R) {
     Eight<X> u;
-    u.load(src, i);
+    u.load(src, i, early);
     put(u, i);
   }
   if (early) griddep_wait();  // (a grid's end follows that of the one before)
@@ -861,35 +864,57 @@ place_rows_kernel(const uint16_t* __restrict__ x, int64_t K, uint16_t* __restric
 
 // rows[pos[t, j]] = token t's activations as fp16 and rows_s their scale, for
 // each of its picks that has an expert. One CTA a token: x is read from memory
-// once, each copy written once.
+// once, each copy written once. Early (see launch_plan) until the picks' places
+// are asked for; the grid behind it reads the plan before its own wait, and so
+// must not begin before this one has waited.
 template <QuantForm FORM>
 __global__ void __launch_bounds__(kRowThreads)
 scatter_rows_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ pos, int k,
                     int64_t K, uint16_t* __restrict__ rows, float* __restrict__ rows_s) {
+  constexpr int kKeep = 4;  // eights of its row a thread keeps
   __shared__ float part[kRowThreads / 32];
-  griddep_wait();
-  if (threadIdx.x == 0) griddep_launch_dependents();
   const int64_t m = blockIdx.x;
   const uint16_t* src = x + m * K;
-  const int64_t nvec = K / 8;
-  Eight<uint16_t> u;
+  const int nvec = (int)(K / 8), t = threadIdx.x, lane = t & 31;
+  uint4 kept[kKeep];
   float a = 0.f;
-  for (int64_t i = threadIdx.x; i < nvec; i += kRowThreads) {
-    u.load(src, i);
-    a = u.absmax(a);
+  {
+    Eight<uint16_t> v[kKeep];
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i)
+      if (t + i * kRowThreads < nvec) v[i].load(src, t + i * kRowThreads, true);
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i)
+      if (t + i * kRowThreads < nvec) a = v[i].absmax(a);
+    for (int i = t + kKeep * kRowThreads; i < nvec; i += kRowThreads) {
+      Eight<uint16_t> u;
+      u.load(src, i, true);
+      a = u.absmax(a);
+    }
+    a = row_max<kRowThreads>(a, part);
+    const float s = row_scale<FORM>(a), inv = row_inverse<FORM>(s);
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i)
+      if (t + i * kRowThreads < nvec) kept[i] = row_f16<FORM>(v[i], s, inv, a == 0.f);
   }
-  a = row_max<kRowThreads>(a, part);
   const float s = row_scale<FORM>(a), inv = row_inverse<FORM>(s);
-  for (int j = threadIdx.x; j < k; j += kRowThreads) {
-    const int at = __ldg(pos + m * k + j);
-    if (at >= 0) rows_s[at] = s;
-  }
-  for (int64_t i = threadIdx.x; i < nvec; i += kRowThreads) {
-    u.load(src, i);
-    const uint4 v = row_f16<FORM>(u, s, inv, a == 0.f);
-    for (int j = 0; j < k; ++j) {
-      const int at = __ldg(pos + m * k + j);
-      if (at >= 0) reinterpret_cast<uint4*>(rows + (int64_t)at * K)[i] = v;
+  griddep_wait();
+  if (t == 0) griddep_launch_dependents();
+  for (int j0 = 0; j0 < k; j0 += 32) {
+    const int mine = j0 + lane < k ? __ldcg(pos + m * k + j0 + lane) : -1;
+    for (int j = 0; j < 32 && j0 + j < k; ++j) {
+      const int at = __shfl_sync(0xffffffffu, mine, j);
+      if (at < 0) continue;
+      if (t == 0) rows_s[at] = s;
+      uint4* to = reinterpret_cast<uint4*>(rows + (int64_t)at * K);
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i)
+        if (t + i * kRowThreads < nvec) to[t + i * kRowThreads] = kept[i];
+      for (int i = t + kKeep * kRowThreads; i < nvec; i += kRowThreads) {
+        Eight<uint16_t> u;
+        u.load(src, i, false);
+        to[i] = row_f16<FORM>(u, s, inv, a == 0.f);
+      }
     }
   }
 }

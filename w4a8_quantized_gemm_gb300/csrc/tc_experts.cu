@@ -163,9 +163,10 @@ ragged_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_constant
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
-  // The plan was there before the kernel in front of this one began (its blocks
-  // wait first thing), so the units and the weights need no wait; the rows and
-  // their scales, and what this kernel writes, do (rows producer, drains).
+  // The plan was there before this kernel could begin (every block of the one in
+  // front waits before it lets it), so the units and the weights need no wait;
+  // the rows and their scales, and what this kernel writes, do (rows producer,
+  // drains).
   if (warp == 0) {
     int below = 0;
     for (int e0 = 0; e0 < p.sets; e0 += 32) {
