@@ -39,10 +39,13 @@ namespace egopq {
 // The weights stream from HBM once: each warp keeps kStages - 1 groups of its
 // rows in flight (2.1 KB each) with cp.async into a ring of its own, which no
 // other warp waits for. Bound by HBM where the rows are few; the conversion of
-// the codes (about 2.5 instructions a pair) is next.
+// the codes (about 2.5 instructions a pair) and the matrix instructions (45 % of
+// their pipe) are next. 33 tokens of 64 experts (8 picks, 3584 x 1280, W4A8) take
+// 95 us, 4.8 TB/s of the 6.8 a copy reaches; one token (W4A16) 20.5 us, of which
+// the weights' 57 MB are 8.4 and the rest the two kernels' starts and ends.
 constexpr int kStages = 4;
 constexpr int kStageBytes = 2176;  // 4 x 512 codes, 64 scales, 16 zero points, padding
-constexpr int kWarps = 4;          // K parts of a CTA
+constexpr int kWarps = 4;          // of a CTA: parts of K, or blocks of rows
 constexpr int kFewWarps = 16;      // the few-token down product's
 constexpr int kFewTokens = 8;
 constexpr int kFewSlots = 128;     // picks of a few-token batch
@@ -670,7 +673,8 @@ experts_few_down_kernel(const StreamParams p) {
 
 // ---- the picks' outputs summed -----------------------------------------------------
 // out[t] = sum_j w[t,j] * y[pos[t,j]] in fp32, j in order; a dropped pick adds
-// nothing. A thread holds eight columns.
+// nothing. A thread holds eight columns. Bound by y: 4096 tokens of 8 picks and
+// 3584 columns read 235 MB in 46 us (5.1 TB/s).
 constexpr int kCombineThreads = 128;
 
 template <typename Y>  // float or uint16_t (bf16)
@@ -866,7 +870,8 @@ place_rows_kernel(const uint16_t* __restrict__ x, int64_t K, uint16_t* __restric
 // each of its picks that has an expert. One CTA a token: x is read from memory
 // once, each copy written once. Early (see launch_plan) until the picks' places
 // are asked for; the grid behind it reads the plan before its own wait, and so
-// must not begin before this one has waited.
+// must not begin before this one has waited. Bound by its writes: 4096 tokens of 8
+// picks and 3584 values write 235 MB in about 45 us.
 template <QuantForm FORM>
 __global__ void __launch_bounds__(kRowThreads)
 scatter_rows_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ pos, int k,
