@@ -533,3 +533,30 @@ def test_experts_follow_inputs_rewritten_in_place(variant, T, path):
     for i, y in enumerate(got):
         assert torch.equal(y, want[i % 3]), i
     assert eg.device_status() == 0
+
+
+# ------------------------------------------------------- offsets past 32 bits ---
+
+def some_rows(n):
+    return torch.cat([torch.arange(8), torch.randint(0, n, (200,)),
+                      torch.arange(n - 200, n)]).to(DEV)
+
+
+def test_lora_of_more_than_2_to_the_31_outputs():
+    M, N = 120000, 18944
+    y, x, ad, ids = lora_case(1, M, N, 256, 8, 16, True)
+    got = eg.lora_add(y, x, ad, ids)
+    rows = some_rows(M)
+    ref, bound = lora_ref(y[rows], x[rows], ad, ids[rows])
+    assert ((got[rows].double() - ref).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("variant", VARIANTS)
+def test_experts_of_more_than_2_to_the_31_sorted_values(variant):
+    T, E, k, H, I = 300000, 4, 4, 2048, 128
+    x, ids, w, gu, dn = experts_case(2, T, E, k, H, I)
+    y = eg.moe_experts(x, ids, w, eg.moe_pack(*gu, *dn), variant=variant)
+    rows = some_rows(T)
+    ref, bound = experts_ref(x[rows], ids[rows], w[rows], gu, dn, variant)
+    assert ((y[rows].double() - ref).abs() <= bound).all()
+    assert eg.device_status() == 0
