@@ -531,37 +531,43 @@ ragged_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_constant
         // both issuers' accumulators (a tile of one group has one, its issuer's)
         const bool both = G >= 2;
         const uint32_t da = !both && (k & 1) ? d0 + BT : d0;
+        // all of this warp's columns first: the next tile's MMAs wait for them,
+        // but not for what is done with them
+        constexpr int kRounds = HB / C::kRound;
+        float v[kRounds][C::kRound];
 #pragma unroll
-        for (int c0 = 0; c0 < HB; c0 += C::kRound) {
-          float v[C::kRound];
+        for (int c = 0; c < kRounds; ++c) {
           if (ok) {
             uint32_t v0[C::kRound / 16][16];
 #pragma unroll
-            for (int q = 0; q < C::kRound / 16; ++q) tmem_ld16(da + c0 + q * 16, v0[q]);
+            for (int q = 0; q < C::kRound / 16; ++q)
+              tmem_ld16(da + c * C::kRound + q * 16, v0[q]);
             if (both) {
               uint32_t v1[C::kRound / 16][16];
 #pragma unroll
-              for (int q = 0; q < C::kRound / 16; ++q) tmem_ld16(d0 + BT + c0 + q * 16, v1[q]);
+              for (int q = 0; q < C::kRound / 16; ++q)
+                tmem_ld16(d0 + BT + c * C::kRound + q * 16, v1[q]);
               tmem_wait_ld();
 #pragma unroll
               for (int q = 0; q < C::kRound; ++q)
-                v[q] = __uint_as_float(v0[q / 16][q % 16]) + __uint_as_float(v1[q / 16][q % 16]);
+                v[c][q] = __uint_as_float(v0[q / 16][q % 16]) + __uint_as_float(v1[q / 16][q % 16]);
             } else {
               tmem_wait_ld();
 #pragma unroll
-              for (int q = 0; q < C::kRound; ++q) v[q] = __uint_as_float(v0[q / 16][q % 16]);
-            }
-            if (c0 + C::kRound >= HB) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(dempty(k % 4));
+              for (int q = 0; q < C::kRound; ++q) v[c][q] = __uint_as_float(v0[q / 16][q % 16]);
             }
           } else {
 #pragma unroll
-            for (int q = 0; q < C::kRound; ++q) v[q] = 0.f;
+            for (int q = 0; q < C::kRound; ++q) v[c][q] = 0.f;
           }
-          put(un, c0, v);
         }
+        if (ok) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(dempty(k % 4));
+        }
+#pragma unroll
+        for (int c = 0; c < kRounds; ++c) put(un, c * C::kRound, v[c]);
       }
     }
     __syncwarp();
