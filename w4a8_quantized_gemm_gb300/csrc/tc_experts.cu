@@ -131,14 +131,14 @@ ragged_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_constant
   auto wfull = [&](int r) { return bar0 + 8u * (2 * XS + r); };
   auto wempty = [&](int r) { return bar0 + 8u * (2 * XS + RS + r); };
   auto aempty = [&](int b) { return bar0 + 8u * (2 * XS + 2 * RS + b); };
-  // folded: slot of the unit's accumulators, and the unit (mod 4) whose
-  // accumulators were read: four, because a converter set may wait for every
-  // fourth unit only (one group a tile), and must not miss a phase of its
-  // barrier; exact: slot of the group's accumulator for both
+  // folded: 2 slot + issuer of the unit's accumulators, and 2 (unit mod 4) +
+  // issuer of those that were read: four units, because a converter set may wait
+  // for every fourth unit only (one group a tile), and must not miss a phase of
+  // its barrier; exact: slot of the group's accumulator for both
   auto dfull = [&](int s) { return bar0 + 8u * (2 * XS + 2 * RS + NA + s); };
   auto dempty = [&](int s) { return bar0 + 8u * (2 * XS + 2 * RS + NA + 4 + s); };
-  auto fin = [&](int q) { return bar0 + 8u * (2 * XS + 2 * RS + NA + 8 + q); };
-  static_assert(8 * (2 * XS + 2 * RS + NA + 10) <= 496, "barrier region");
+  auto fin = [&](int q) { return bar0 + 8u * (2 * XS + 2 * RS + NA + 12 + q); };
+  static_assert(8 * (2 * XS + 2 * RS + NA + 14) <= 496, "barrier region");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarAt + 496);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBarAt + 500);
   int* first_tile = reinterpret_cast<int*>(smem + C::kFirstAt);
@@ -154,11 +154,8 @@ ragged_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_constant
       mbar_init(wempty(r), 4);
     }
     for (int b = 0; b < NA; ++b) mbar_init(aempty(b), 1);
-    for (int s = 0; s < 4; ++s) {
-      // (folded: the issuers that have a group in a tile)
-      mbar_init(dfull(s), EXACT || G < 2 ? 1 : 2);
-      mbar_init(dempty(s), C::kDrainWarps);
-    }
+    for (int s = 0; s < 4; ++s) mbar_init(dfull(s), 1);
+    for (int s = 0; s < 8; ++s) mbar_init(dempty(s), C::kDrainWarps);
     for (int q = 0; q < 2; ++q) mbar_init(fin(q), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -327,7 +324,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_constant
           tc_commit(xempty(s));
           tc_commit(aempty(b));
           // (folded: at this issuer's last group of the tile)
-          if (EXACT || gi + kStep >= G) tc_commit(dfull(slot));
+          if (EXACT || gi + kStep >= G) tc_commit(dfull(EXACT ? slot : slot * 2 + q));
         }
         any = true;
       }
@@ -403,7 +400,7 @@ ragged_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_constant
           if (!wait(dempty(i % C::kSlots), (i / C::kSlots) ^ 1)) return false;
         } else {
           const int v_unit = k - C::kSlots;
-          if (gi < 2 && v_unit >= 0 && !wait(dempty(v_unit % 4), v_unit / 4)) return false;
+          if (gi < 2 && v_unit >= 0 && !wait(dempty(v_unit % 4 * 2 + set), v_unit / 4)) return false;
         }
       }
       tmem_wait_st();
@@ -522,49 +519,42 @@ ragged_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_constant
         }
       } else {
         const int slot = k % C::kSlots;
-        if (ok) ok = mbar_wait(dfull(slot), (k / C::kSlots) & 1, abort_flag, tmo);
-        ok = __all_sync(0xffffffffu, ok);
         if (r < HB) as[r] = my_as;
         asm volatile("bar.sync %0, 128;" ::"r"(6 + wg) : "memory");
-        tc_fence_after();
-        const uint32_t d0 = tmem + lane_base + slot * 128 + col0;
-        // both issuers' accumulators (a tile of one group has one, its issuer's)
-        const bool both = G >= 2;
-        const uint32_t da = !both && (k & 1) ? d0 + BT : d0;
-        // all of this warp's columns first: the next tile's MMAs wait for them,
-        // but not for what is done with them
+        // Both issuers' accumulators, the one whose last group comes first first:
+        // it is the one the next tile begins with, whose MMAs wait for its
+        // columns to be read but for nothing that is done with them (a tile of
+        // one group has one accumulator, its issuer's).
         constexpr int kRounds = HB / C::kRound;
+        const int last = ((k + 1) * G - 1) & 1;
         float v[kRounds][C::kRound];
 #pragma unroll
-        for (int c = 0; c < kRounds; ++c) {
-          if (ok) {
-            uint32_t v0[C::kRound / 16][16];
+        for (int c = 0; c < kRounds; ++c)
 #pragma unroll
-            for (int q = 0; q < C::kRound / 16; ++q)
-              tmem_ld16(da + c * C::kRound + q * 16, v0[q]);
-            if (both) {
-              uint32_t v1[C::kRound / 16][16];
+          for (int q = 0; q < C::kRound; ++q) v[c][q] = 0.f;
+        for (int n = G < 2 ? 1 : 0; n < 2; ++n) {
+          const int q = n ? last : last ^ 1;
+          if (ok)
+            ok = mbar_wait(dfull(slot * 2 + q), (G < 2 ? k / 2 : k / C::kSlots) & 1, abort_flag, tmo);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t d = tmem + lane_base + slot * 128 + q * BT + col0;
 #pragma unroll
-              for (int q = 0; q < C::kRound / 16; ++q)
-                tmem_ld16(d0 + BT + c * C::kRound + q * 16, v1[q]);
-              tmem_wait_ld();
+          for (int c = 0; c < kRounds; ++c) {
+            uint32_t u[C::kRound / 16][16];
 #pragma unroll
-              for (int q = 0; q < C::kRound; ++q)
-                v[c][q] = __uint_as_float(v0[q / 16][q % 16]) + __uint_as_float(v1[q / 16][q % 16]);
-            } else {
-              tmem_wait_ld();
+            for (int b = 0; b < C::kRound / 16; ++b) tmem_ld16(d + c * C::kRound + b * 16, u[b]);
+            tmem_wait_ld();
 #pragma unroll
-              for (int q = 0; q < C::kRound; ++q) v[c][q] = __uint_as_float(v0[q / 16][q % 16]);
-            }
-          } else {
-#pragma unroll
-            for (int q = 0; q < C::kRound; ++q) v[c][q] = 0.f;
+            for (int b = 0; b < C::kRound; ++b) v[c][b] += __uint_as_float(u[b / 16][b % 16]);
           }
-        }
-        if (ok) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(dempty(k % 4));
+          if (lane == 0) {
+            mbar_arrive(dempty(k % 4 * 2 + q));
+            if (G < 2) mbar_arrive(dempty(k % 4 * 2 + (q ^ 1)));
+          }
         }
 #pragma unroll
         for (int c = 0; c < kRounds; ++c) put(un, c * C::kRound, v[c]);
