@@ -31,7 +31,10 @@
 //                      barriers, since an mbarrier test queues behind the MMAs
 //                      just issued
 //   2 drain warpgroups half of the BT columns each: accumulators added, scaled,
-//                      gated, staged in shared memory, stored by rows
+//                      gated, staged in shared memory, stored by rows (keep
+//                      their work short: 20 instructions more a value for
+//                      fp16 gated values over powers of two took 430 us where
+//                      fp32 ones of twice the memory take 372, 2977 tokens)
 // Tensor Memory: 256 columns of accumulators (folded: two an issuer at BT = 64,
 // so a tile's reading runs beside the next one's MMAs, one at 128; exact: four
 // groups'), 256 of A buffers.
@@ -45,10 +48,11 @@
 // expert and 128 above. Deeper rings (14 records), four converter sets, four
 // issuers, one issuer (exact, 128 rows) changed none of this or cost time.
 // All three kernels of a layer: 4096 tokens of 64 experts (8 picks, 3584 x 1280,
-// W4A8) take 921 us, 979 TFLOP/s, half of cuBLAS's bf16 rate: gate and up (in
-// 192-row exact tiles, tc_kernel.cuh) 500, down 280, the rest the rows' ways in
-// and out. 2977 tokens of 64 experts (6 picks, 2048 x 1408, W4A16) 400 us, 773
-// TFLOP/s; 509 tokens of 32 experts (4 picks, 2048 x 1024) 70.6 us.
+// W4A8) take 891 us, 1012 TFLOP/s, half of cuBLAS's bf16 rate: gate and up (in
+// 192-row exact tiles, tc_kernel.cuh) 500, down 250, the rest the rows' ways in
+// and out. 2977 tokens of 64 experts (6 picks, 2048 x 1408, W4A16) 367 us, 842
+// TFLOP/s (reading an accumulator only when it is needed next cost 394); 509
+// tokens of 32 experts (4 picks, 2048 x 1024) 71 us.
 // Every wait on an mbarrier is bounded; after one gives up, every warp still
 // makes its remaining named-barrier meetings and skips the work.
 #include "tc_kernel.cuh"
