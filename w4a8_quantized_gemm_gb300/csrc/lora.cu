@@ -574,16 +574,18 @@ lora_shrink_kernel(const LoraParams p) {
 
 // y = bf16(y0 + scale * B_a h). One CTA a tile of 128 rows and 256 columns, 32 a
 // warp, whose part of B stays in registers (32 JS ranks at a time) while the
-// rows go by, sixteen at a time, three sixteens of y on their way; the tile's h
+// rows go by, sixteen at a time, kAhead sixteens of y on their way; the tile's h
 // (the splits added in order, scaled, rounded to bf16 once: see lora_kernel)
 // lies in shared memory. Bound by y0 and y and by a CTA's start (plan, B, h, then
-// y): 2 x 29 MB at 4093 x 3584 take about 25 us, where a copy of them alone takes
+// y): 2 x 29 MB at 4093 x 3584 take about 23 us, where a copy of them alone takes
 // 16 to 19.
-constexpr int kExpandAhead = 3;
-
 template <int JS>
 __global__ void __launch_bounds__(kLoraThreads, 2)
 lora_expand_kernel(const LoraParams p) {
+  // sixteens of rows whose y is on its way: what B leaves room for (4093 rows of
+  // 3584, four / three / two of them: rank 64 41.5 / 43.7 / 42.9 us, rank 128
+  // 72.5 / 67.9 / 63.8)
+  constexpr int kAhead = JS < 4 ? 4 : 2;
   constexpr int LD = JS * 32 + 8;  // padded row of h: 16-byte rows, no bank conflicts
   __shared__ __align__(16) uint16_t hs[kManyTile][LD];
   // Every block of the first kernel waited for the plan before it let this one
@@ -630,8 +632,8 @@ lora_expand_kernel(const LoraParams p) {
     }
   }
   // y of sixteen rows: this thread's two, a negative place where there is none
-  int64_t at[kExpandAhead][2];
-  uint4 y[kExpandAhead][2];
+  int64_t at[kAhead][2];
+  uint4 y[kAhead][2];
   auto fetch = [&](int m, int slot) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -646,7 +648,7 @@ lora_expand_kernel(const LoraParams p) {
         y[slot][half] = __ldcg(reinterpret_cast<const uint4*>(p.y_in + at[slot][half]));
   };
 #pragma unroll
-  for (int m = 0; m < kExpandAhead; ++m) fetch(m, m);
+  for (int m = 0; m < kAhead; ++m) fetch(m, m);
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
   if (rank > 0) {
@@ -688,9 +690,9 @@ lora_expand_kernel(const LoraParams p) {
   }
   __syncthreads();
   const int m_end = (tile.z + 15) / 16;
-  for (int m0 = 0; m0 < m_end; m0 += kExpandAhead) {
+  for (int m0 = 0; m0 < m_end; m0 += kAhead) {
 #pragma unroll
-    for (int slot = 0; slot < kExpandAhead; ++slot) {
+    for (int slot = 0; slot < kAhead; ++slot) {
       const int m = m0 + slot;
       if (m >= m_end) break;
       float acc[4][4];
@@ -713,23 +715,26 @@ lora_expand_kernel(const LoraParams p) {
       for (int half = 0; half < 2; ++half)
         if (at[slot][half] >= 0)
           *reinterpret_cast<uint4*>(p.y_out + at[slot][half]) = add_row(y[slot][half], acc, half);
-      if (m + kExpandAhead < m_end) fetch(m + kExpandAhead, slot);
+      if (m + kAhead < m_end) fetch(m + kAhead, slot);
     }
   }
 }
 
 bool lora_few(int64_t M) { return M <= kLoraFewRows; }
 
-// Whether a batch with a plan takes the two kernels. The cluster kernel holds
-// about 40 tiles at once and repeats its chain of waits for every 40 more, but
-// goes through wide rows of y without a stop, where the two kernels start a CTA
-// a 256 columns. Two kernels / cluster kernel, us: 32 adapters of rank 16,
-// 3584 x 3584: 500 rows 17.3 / 15.8, 1000 rows 20.3 / 32.6; 16 of rank 64: 700
-// rows 27.9 / 23.6, 1000 rows 29.8 / 36.6; 64 of rank 32, 3584 x 18944: 1000
-// rows 84 / 66, 4093 rows 137 / 123; 4 of rank 32, 2048 x 8192: 1000 rows 23.9 /
-// 26.9. A batch of more rows than one that takes them takes them too.
-static bool lora_many(int64_t M, int64_t N, int L) {
-  return std::min<int64_t>(L, M) + M / kLoraTile > 44 && (N < 8192 || M > 64LL * L);
+// Whether a batch with a plan takes the two kernels. The cluster kernel holds 38
+// tiles at once (a little more at high ranks, where its second round costs less
+// than the two kernels' way of B) and repeats its chain of waits for the next
+// ones, but goes through wide rows of y without a stop, where the two kernels
+// start a CTA a 256 columns. Two kernels / cluster kernel, us, 3584 x 3584: 8
+// adapters of rank 64, 800 rows 26.3 / 23.7, 1000 rows 28.9 / 34.1; 2 of rank
+// 16, 1200 rows 19.7 / 28.8; 32 of rank 16, 256 rows 16.5 / 14.4; 16 of rank
+// 128, 800 rows 43.0 / 32.7; 3584 x 18944, 64 of rank 32: 1000 rows 84 / 66,
+// 4093 rows 137 / 123. A batch of more rows than one that takes them takes them
+// too.
+static bool lora_many(int64_t M, int64_t N, int L, int r) {
+  return std::min<int64_t>(L, M) + M / kLoraTile > (r > 64 ? 44 : 38) &&
+         (N < 8192 || M > 64LL * L);
 }
 
 // Parts of K of the first kernel: about two CTAs an SM, each of two steps a warp
@@ -788,7 +793,7 @@ static cudaError_t launch_lora_rank(const LoraParams& p, int64_t most, cudaStrea
 
 cudaError_t launch_lora_plan(const LoraArgs& a, cudaStream_t st) {
   if (lora_few(a.M)) return cudaSuccess;
-  return launch_plan(a.ids, a.M, a.L, lora_many(a.M, a.N, a.L) ? kManyTile : kLoraTile, a.plan, st,
+  return launch_plan(a.ids, a.M, a.L, lora_many(a.M, a.N, a.L, a.r) ? kManyTile : kLoraTile, a.plan, st,
                      true);
 }
 
@@ -814,7 +819,7 @@ cudaError_t launch_lora(const LoraArgs& a, cudaStream_t st, bool beside) {
   const bool few = lora_few(a.M);
   // (the rows without an adapter make at most ceil(M / tile) tiles more)
   const int64_t sets = a.L < a.M ? a.L : a.M;
-  const bool many = lora_many(a.M, a.N, a.L);
+  const bool many = lora_many(a.M, a.N, a.L, a.r);
   const int bt = many ? kManyTile : kLoraTile;
   const int64_t most = few ? sets + 1 : plan_max_tiles(a.M, a.L, bt) + (a.M + bt - 1) / bt;
   // slabs of 2048 columns at least
