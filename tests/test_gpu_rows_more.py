@@ -1,0 +1,83 @@
+"""More GPU tests of the operators whose weights each row picks, with the
+references, bounds and tolerances of test_gpu_rows."""
+import math
+
+import pytest
+import torch
+
+import w4a8_quantized_gemm_gb300 as eg
+from test_gpu_rows import (DEV, VARIANTS, check_experts, check_lora, check_route, experts_case,
+                           experts_ref, gen, lora_case, lora_ref, w4)
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------- memory of calls on other streams ---
+
+def late(stream):
+    """Work of some 20 ms in front of what comes next on the stream."""
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(40_000_000)
+
+
+def check_on_a_late_stream(call, nbytes):
+    """call(stream) allocates its workspace and output itself and is queued on two
+    streams behind other work, while the caller's stream gets memory of the same
+    sizes and writes to it: the results are those of the call alone."""
+    want = call(None)
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(2):
+        got = []
+        for side in sides:
+            late(side)
+            got.append(call(side))
+        junk = [torch.full((n,), 0x7F, dtype=torch.uint8, device=DEV)
+                for n in (nbytes, nbytes, want.nbytes, want.nbytes)]
+        torch.cuda.synchronize()
+        for y in got:
+            assert torch.equal(y, want)
+        del junk, got
+    assert eg.device_status() == 0
+
+
+@pytest.mark.parametrize("variant", VARIANTS)
+@pytest.mark.parametrize("T", [3, 40, 500])
+def test_experts_without_a_workspace_on_another_stream(variant, T):
+    x, ids, w, gu, dn = experts_case(T, T, 8, 4, 384, 256)
+    layer = eg.moe_pack(*gu, *dn)
+    check_on_a_late_stream(
+        lambda s: eg.moe_experts(x, ids, w, layer, variant=variant, stream=s),
+        eg.moe_workspace_bytes(T, 4, 8, 384, 256, variant))
+
+
+@pytest.mark.parametrize("M", [5, 300, 2100])
+def test_adapters_without_a_workspace_on_another_stream(M):
+    y, x, ad, ids = lora_case(M, M, 640, 512, 60, 32, True)
+    check_on_a_late_stream(lambda s: eg.lora_add(y, x, ad, ids, stream=s),
+                           eg.lora_workspace(M, 640, 512, ad, DEV).nbytes)
+    packed = eg.pack_w4(*w4(gen(M), 640, 512))
+    check_on_a_late_stream(lambda s: eg.w4a8_linear_lora(x, packed, 640, ad, ids, stream=s),
+                           eg.w4a8_linear_lora_workspace(M, 640, 512, ad, DEV).nbytes)
+    check_on_a_late_stream(lambda s: eg.w4a8_linear(x, packed, 640, stream=s),
+                           eg.w4a8_linear_workspace_bytes(M, 512))
+
+
+def test_an_output_made_on_another_stream_outlives_its_reader():
+    """The caller's stream reads an output and lets go of it while it still
+    reads: the next call on the other stream must not get that memory yet."""
+    x = torch.randn(512, 64, device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    here = torch.cuda.current_stream()
+    weights, ids = eg.moe_route(x, 4, stream=side)
+    torch.cuda.synchronize()
+    want = weights.clone()
+    torch.cuda.synchronize()
+    late(here)
+    copy = weights.clone()
+    del weights, ids
+    other = [eg.moe_route(-x, 4, stream=side) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want)
+    del other

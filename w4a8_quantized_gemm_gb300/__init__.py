@@ -10,6 +10,11 @@ Typical use (one linear, W4A8):
     packed = pack_w4(w_q, scale_f16, zero)            # once per weight
     a = quant_act(x)                                  # per token batch
     y = w4a8_gemm(a, packed, N, K)                    # bf16 [M, N]
+
+A call runs on the current stream, or on `stream`; the tensors it is given have
+to be ready there. What it allocates itself is `stream`'s memory (as under
+torch.cuda.stream(stream)), and the caller's stream may read its results once it
+has waited for `stream`.
 """
 from __future__ import annotations
 
@@ -147,6 +152,28 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return t.data_ptr()
 
 
+def _scratch(shape, dtype: torch.dtype, device, stream=None) -> torch.Tensor:
+    """Memory for a call's kernels. Where a stream is given it is that stream's,
+    as under torch.cuda.stream(stream): what had the memory before, and what gets
+    it next, is then in order with those kernels without any event."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _output(shape, dtype: torch.dtype, device, stream=None) -> torch.Tensor:
+    """A result a call allocates: as _scratch, and not given out again before
+    the caller's own stream, which may read it, has come as far as where the
+    caller lets go of it."""
+    t = _scratch(shape, dtype, device, stream)
+    if stream is not None:
+        here = torch.cuda.current_stream(device)
+        if here != stream:
+            t.record_stream(here)
+    return t
+
+
 def _dtype(t: torch.Tensor, *dtypes):
     if t.dtype not in dtypes:  # (dtypes are compared by identity)
         raise TypeError(f"expected dtype in {dtypes}, got {t.dtype}")
@@ -169,7 +196,7 @@ def pack_w4(w_q: torch.Tensor, scale_f16: torch.Tensor, zero: torch.Tensor,
     if nbytes == 0:
         raise EgopqError(-2, f"shape N={N} K={K} is not packable (K, N multiples of 128)")
     if out is None:
-        out = torch.empty(nbytes, dtype=torch.uint8, device=w_q.device)
+        out = _output(nbytes, torch.uint8, w_q.device, stream)
     _check(load().egopq_pack_w4(_ptr(w_q), _ptr(scale_f16), _ptr(zero), N, K, GROUP,
                                 _ptr(out), _stream(stream)))
     return out
@@ -178,9 +205,9 @@ def pack_w4(w_q: torch.Tensor, scale_f16: torch.Tensor, zero: torch.Tensor,
 def unpack_w4(packed: torch.Tensor, N: int, K: int, stream=None):
     G = K // GROUP
     dev = packed.device
-    w = torch.empty((N, K), dtype=torch.uint8, device=dev)
-    s = torch.empty((N, G), dtype=torch.float16, device=dev)
-    z = torch.empty((N, G), dtype=torch.uint8, device=dev)
+    w = _output((N, K), torch.uint8, dev, stream)
+    s = _output((N, G), torch.float16, dev, stream)
+    z = _output((N, G), torch.uint8, dev, stream)
     _check(load().egopq_unpack_w4(_ptr(packed), N, K, GROUP, _ptr(w), _ptr(s), _ptr(z),
                                   _stream(stream)))
     return w, s, z
@@ -193,7 +220,7 @@ def pack_w4_gptq(qweight: torch.Tensor, qzeros: torch.Tensor, scales: torch.Tens
     _dtype(qweight, torch.int32)
     _dtype(qzeros, torch.int32)
     K, N = qweight.shape[0] * 8, qweight.shape[1]
-    packed = torch.empty(packed_w4_bytes(N, K), dtype=torch.uint8, device=qweight.device)
+    packed = _output(packed_w4_bytes(N, K), torch.uint8, qweight.device, stream)
     _check(load().egopq_pack_w4_gptq(_ptr(qweight), _ptr(qzeros), _ptr(scales), N, K, GROUP,
                                      zero_offset, _ptr(packed), _stream(stream)))
     return packed
@@ -203,7 +230,7 @@ def dequant_w4(packed: torch.Tensor, N: int, K: int, out: Optional[torch.Tensor]
                stream=None) -> torch.Tensor:
     """The packed weight dequantized once to dense bf16 [N, K]."""
     if out is None:
-        out = torch.empty((N, K), dtype=torch.bfloat16, device=packed.device)
+        out = _output((N, K), torch.bfloat16, packed.device, stream)
     _check(load().egopq_dequant_w4(_ptr(packed), N, K, GROUP, _ptr(out), _stream(stream)))
     return out
 
@@ -258,15 +285,15 @@ def tc_operand_form(M: int) -> int:
     return rc
 
 
-def tc_operand(M: int, K: int, device) -> torch.Tensor:
+def tc_operand(M: int, K: int, device, stream=None) -> torch.Tensor:
     """A buffer for the tensor-core operand form of M x K codes (empty for an
     empty batch)."""
     if M == 0:
-        return torch.empty((0,), dtype=torch.uint8, device=device)
+        return _output((0,), torch.uint8, device, stream)
     nbytes = int(load().egopq_tc_operand_bytes(M, K, GROUP))
     if nbytes == 0:
         raise EgopqError(-2, f"no tensor-core operand for M={M} K={K}")
-    return torch.empty((nbytes,), dtype=torch.uint8, device=device)
+    return _output((nbytes,), torch.uint8, device, stream)
 
 
 def quant_act(x: torch.Tensor, with_tc: bool = True, out: Optional[QuantAct] = None,
@@ -278,10 +305,10 @@ def quant_act(x: torch.Tensor, with_tc: bool = True, out: Optional[QuantAct] = N
     M, K = x.shape
     if out is None:
         dev = x.device
-        out = QuantAct(torch.empty((M, K), dtype=torch.int8, device=dev) if with_codes else None,
-                       torch.empty((M,), dtype=torch.float32, device=dev),
-                       torch.empty((M, max(K // GROUP, 1)), dtype=torch.int32, device=dev),
-                       tc_operand(M, K, dev) if with_tc else None)
+        out = QuantAct(_output((M, K), torch.int8, dev, stream) if with_codes else None,
+                       _output((M,), torch.float32, dev, stream),
+                       _output((M, max(K // GROUP, 1)), torch.int32, dev, stream),
+                       tc_operand(M, K, dev, stream) if with_tc else None)
     _check(load().egopq_quant_act_i8(_ptr(x), M, K, GROUP, _ptr(out.a_q), _ptr(out.a_s),
                                      _ptr(out.a_gsum), _ptr(out.a_tc), _stream(stream)))
     return out
@@ -291,7 +318,7 @@ def w4a8_gemm(a: QuantAct, packed: torch.Tensor, N: int, K: int, path: int = PAT
               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     M = a.a_s.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=a.a_s.device)
+        out = _output((M, N), torch.bfloat16, a.a_s.device, stream)
     _check(load().egopq_w4a8_gemm_ex(_ptr(a.a_q), _ptr(a.a_tc), _ptr(a.a_s), _ptr(a.a_gsum),
                                      _ptr(packed), M, N, K, GROUP, _ptr(out), path,
                                      _stream(stream)))
@@ -310,10 +337,10 @@ def w4a8_linear(x: torch.Tensor, packed: torch.Tensor, N: int, path: int = PATH_
     _dtype(x, torch.bfloat16)
     M, K = x.shape
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        out = _output((M, N), torch.bfloat16, x.device, stream)
     need = w4a8_linear_workspace_bytes(M, K, path)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _scratch(need, torch.uint8, x.device, stream)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(load().egopq_w4a8_linear(_ptr(x), _ptr(packed), M, N, K, GROUP, _ptr(out),
                                     _ptr(workspace), ws_bytes, path, _stream(stream)))
@@ -334,9 +361,9 @@ class _Group:
         self.y = (ctypes.c_void_p * n)(*[_ptr(o) for o in outs])
 
 
-def _grouped_outputs(M, N, device, out):
+def _grouped_outputs(M, N, device, out, stream):
     if out is None:
-        out = [torch.empty((M, n), dtype=torch.bfloat16, device=device) for n in N]
+        out = [_output((M, n), torch.bfloat16, device, stream) for n in N]
     for o, n in zip(out, N):
         _dtype(o, torch.bfloat16)
         if tuple(o.shape) != (M, n):
@@ -349,7 +376,7 @@ def w4a8_gemm_grouped(a: QuantAct, packed: list, N: list, K: int, path: int = PA
     """Sibling linears sharing the activations `a` (q|k|v, gate|up) in one
     launch: returns [y_j bf16 [M, N_j]]."""
     M = a.a_s.shape[0]
-    out = _grouped_outputs(M, N, a.a_s.device, out)
+    out = _grouped_outputs(M, N, a.a_s.device, out, stream)
     g = _Group(packed, N, out)
     _check(load().egopq_w4a8_gemm_grouped(_ptr(a.a_q), _ptr(a.a_tc), _ptr(a.a_s), _ptr(a.a_gsum),
                                           g.count, g.packed, g.N, M, K, GROUP, g.y, path,
@@ -364,10 +391,10 @@ def w4a8_linear_grouped(x: torch.Tensor, packed: list, N: list, path: int = PATH
     weights: returns [y_j bf16 [M, N_j]]."""
     _dtype(x, torch.bfloat16)
     M, K = x.shape
-    out = _grouped_outputs(M, N, x.device, out)
+    out = _grouped_outputs(M, N, x.device, out, stream)
     need = w4a8_linear_workspace_bytes(M, K, path)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _scratch(need, torch.uint8, x.device, stream)
     g = _Group(packed, N, out)
     _check(load().egopq_w4a8_linear_grouped(_ptr(x), g.count, g.packed, g.N, M, K, GROUP, g.y,
                                             _ptr(workspace), workspace.numel(), path,
@@ -378,7 +405,7 @@ def w4a8_linear_grouped(x: torch.Tensor, packed: list, N: list, path: int = PATH
 def w4a8_group_partials(a: QuantAct, packed: torch.Tensor, N: int, K: int,
                         path: int = PATH_TC, stream=None) -> torch.Tensor:
     M = a.a_s.shape[0]
-    Q = torch.empty((M, N, K // GROUP), dtype=torch.int32, device=a.a_s.device)
+    Q = _output((M, N, K // GROUP), torch.int32, a.a_s.device, stream)
     _check(load().egopq_w4a8_group_partials(_ptr(a.a_q), _ptr(a.a_tc), _ptr(a.a_gsum),
                                             _ptr(packed), M, N, K, GROUP, _ptr(Q), path,
                                             _stream(stream)))
@@ -390,7 +417,7 @@ def w4a16_gemm(x: torch.Tensor, packed: torch.Tensor, N: int, K: int, path: int 
     _dtype(x, torch.bfloat16)
     M = x.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        out = _output((M, N), torch.bfloat16, x.device, stream)
     _check(load().egopq_w4a16_gemm_ex(_ptr(x), _ptr(packed), M, N, K, GROUP, _ptr(out), path,
                                       _stream(stream)))
     return out
@@ -404,7 +431,7 @@ def w8a16_gemm(x: torch.Tensor, w_q: torch.Tensor, scale_f16: torch.Tensor,
     M, K = x.shape
     N = w_q.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        out = _output((M, N), torch.bfloat16, x.device, stream)
     _check(load().egopq_w8a16_gemm_ex(_ptr(x), _ptr(w_q), _ptr(scale_f16), M, N, K, _ptr(out),
                                       path, _stream(stream)))
     return out
@@ -419,7 +446,7 @@ def w8a8_gemm(a: QuantAct, w_q: torch.Tensor, scale_f16: torch.Tensor, path: int
     M = a.a_s.shape[0]
     N, K = w_q.shape
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=a.a_s.device)
+        out = _output((M, N), torch.bfloat16, a.a_s.device, stream)
     _check(load().egopq_w8a8_gemm_ex(_ptr(a.a_q), _ptr(a.a_tc), _ptr(a.a_s), _ptr(w_q),
                                      _ptr(scale_f16), M, N, K, _ptr(out), path,
                                      _stream(stream)))
@@ -435,7 +462,7 @@ def bf16_gemm_twin(x: torch.Tensor, w: torch.Tensor, out: Optional[torch.Tensor]
     M, K = x.shape
     N = w.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        out = _output((M, N), torch.bfloat16, x.device, stream)
     _check(load().egopq_bf16_gemm_twin(_ptr(x), _ptr(w), M, N, K, _ptr(out), _stream(stream)))
     return out
 
@@ -473,8 +500,8 @@ def moe_route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None,
         _dtype(logits, torch.float32, torch.bfloat16)
     T, E = logits.shape
     if out is None:
-        out = (torch.empty((T, k), dtype=torch.float32, device=logits.device),
-               torch.empty((T, k), dtype=torch.int32, device=logits.device))
+        out = (_output((T, k), torch.float32, logits.device, stream),
+               _output((T, k), torch.int32, logits.device, stream))
     weights, ids = out
     _check(load().egopq_moe_route(
         _arg(logits, logits.dtype, T, E), bf16,
@@ -512,7 +539,7 @@ def moe_pack(gate_up_q: torch.Tensor, gate_up_scale: torch.Tensor, gate_up_zero:
     for t, dtype, K in ((down_q, torch.uint8, I), (down_scale, torch.float16, I // GROUP),
                         (down_zero, torch.uint8, I // GROUP)):
         _arg(t, dtype, E, H, K)
-    packed = torch.empty(nbytes, dtype=torch.uint8, device=gate_up_q.device)
+    packed = _output(nbytes, torch.uint8, gate_up_q.device, stream)
     _check(load().egopq_moe_pack_gate_up(q, s, z, E, I, H, GROUP, packed.data_ptr(),
                                          _stream(stream)))
     down = pack_w4(down_q.view(E * H, I), down_scale.view(E * H, I // GROUP),
@@ -526,10 +553,10 @@ def moe_workspace_bytes(T: int, k: int, E: int, H: int, I: int, variant: int = V
 
 
 def moe_workspace(T: int, k: int, E: int, H: int, I: int, variant: int, device,
-                  path: int = PATH_AUTO) -> torch.Tensor:
-    """A workspace for moe_experts of T tokens (and of any fewer)."""
-    return torch.empty(moe_workspace_bytes(T, k, E, H, I, variant, path), dtype=torch.uint8,
-                       device=device)
+                  path: int = PATH_AUTO, stream=None) -> torch.Tensor:
+    """A workspace for moe_experts of T tokens (and of any fewer), of the stream
+    it is to be used on."""
+    return _scratch(moe_workspace_bytes(T, k, E, H, I, variant, path), torch.uint8, device, stream)
 
 
 def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, layer: MoeLayer,
@@ -542,9 +569,9 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, layer
     gate_up, down, E, H, I = layer
     T, k = ids.shape
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        out = _output((T, H), torch.bfloat16, x.device, stream)
     if workspace is None:
-        workspace = moe_workspace(T, k, E, H, I, variant, x.device, path)
+        workspace = moe_workspace(T, k, E, H, I, variant, x.device, path, stream)
     _check(load().egopq_moe_experts(
         _arg(x, torch.bfloat16, T, H), _arg(ids, torch.int32, T, k),
         _arg(weights, torch.float32, T, k), gate_up.data_ptr(), down.data_ptr(), T, k, E, H, I,
@@ -578,9 +605,12 @@ class LoraAdapters:
         raise AttributeError(f"LoraAdapters.{name} is fixed: make new adapters")
 
 
-def lora_workspace(M: int, N: int, K: int, adapters: LoraAdapters, device) -> torch.Tensor:
-    return torch.empty(int(load().egopq_lora_workspace_bytes(M, N, K, adapters.L, adapters.r)),
-                       dtype=torch.uint8, device=device)
+def lora_workspace(M: int, N: int, K: int, adapters: LoraAdapters, device,
+                   stream=None) -> torch.Tensor:
+    """A workspace for lora_add of M rows (and of any fewer), of the stream it is
+    to be used on."""
+    return _scratch(int(load().egopq_lora_workspace_bytes(M, N, K, adapters.L, adapters.r)),
+                    torch.uint8, device, stream)
 
 
 def lora_add(y: torch.Tensor, x: torch.Tensor, adapters: LoraAdapters, ids: torch.Tensor,
@@ -592,9 +622,9 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, adapters: LoraAdapters, ids: torc
     L, r, K, N = adapters.L, adapters.r, adapters.K, adapters.N
     M = x.shape[0]
     if out is None:
-        out = torch.empty_like(y)
+        out = _output((M, N), torch.bfloat16, x.device, stream)
     if workspace is None:
-        workspace = lora_workspace(M, N, K, adapters, x.device)
+        workspace = lora_workspace(M, N, K, adapters, x.device, stream)
     _check(load().egopq_lora_add(
         _arg(y, torch.bfloat16, M, N), _arg(x, torch.bfloat16, M, K), A, B, scale, ranks,
         _arg(ids, torch.int32, M), M, N, K, L, r,
@@ -603,10 +633,12 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, adapters: LoraAdapters, ids: torc
 
 
 def w4a8_linear_lora_workspace(M: int, N: int, K: int, adapters: LoraAdapters, device,
-                               path: int = PATH_AUTO) -> torch.Tensor:
+                               path: int = PATH_AUTO, stream=None) -> torch.Tensor:
+    """A workspace for w4a8_linear_lora of M rows (and of any fewer), of the
+    stream it is to be used on."""
     n = int(load().egopq_w4a8_linear_lora_workspace_bytes(M, N, K, GROUP, adapters.L, adapters.r,
                                                           path))
-    return torch.empty(n, dtype=torch.uint8, device=device)
+    return _scratch(n, torch.uint8, device, stream)
 
 
 def w4a8_linear_lora(x: torch.Tensor, packed: torch.Tensor, N: int, adapters: LoraAdapters,
@@ -621,9 +653,9 @@ def w4a8_linear_lora(x: torch.Tensor, packed: torch.Tensor, N: int, adapters: Lo
     if N != adapters.N:
         raise ValueError(f"adapters of {adapters.N} outputs beside a projection of {N}")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        out = _output((M, N), torch.bfloat16, x.device, stream)
     if workspace is None:
-        workspace = w4a8_linear_lora_workspace(M, N, K, adapters, x.device, path)
+        workspace = w4a8_linear_lora_workspace(M, N, K, adapters, x.device, path, stream)
     _check(load().egopq_w4a8_linear_lora(
         _arg(x, torch.bfloat16, M, K), _ptr(packed), A, B, scale, ranks,
         _arg(ids, torch.int32, M), M, N, K, GROUP, L, r, _arg(out, torch.bfloat16, M, N),
