@@ -167,3 +167,55 @@ def test_workspaces_can_be_made_for_another_stream(lib, streams):
     eg.lora_workspace(3, 128, 128, adapters(), "cpu", stream=side)
     eg.w4a8_linear_lora_workspace(3, 128, 128, adapters(), "cpu", stream=side)
     assert [s for _, s in streams.made] == [side] * 3
+
+
+# ------------------------------------------------- adapters whose memory is replaced ---
+
+def lora_calls(ad):
+    """(name, the four addresses it passes on) for each call that takes adapters."""
+    M = 3
+    x, y, ids = (zeros(M, ad.K, dtype=BF16), zeros(M, ad.N, dtype=BF16), zeros(M, dtype=I32))
+    return [("egopq_lora_add", slice(2, 6), lambda: eg.lora_add(y, x, ad, ids)),
+            ("egopq_w4a8_linear_lora", slice(2, 6),
+             lambda: eg.w4a8_linear_lora(x, zeros(4096, dtype=U8), ad.N, ad, ids))]
+
+
+@pytest.mark.parametrize("which", ["A", "B", "scale", "ranks"])
+@pytest.mark.parametrize("call", [0, 1])
+def test_adapters_follow_memory_that_was_replaced(lib, which, call):
+    ad = adapters()
+    name, at, run = lora_calls(ad)[call]
+    run()
+    tensors = [ad.A, ad.B, ad.scale, ad.ranks]
+    assert list(lib.args(name)[at]) == [t.data_ptr() for t in tensors]
+    t = getattr(ad, which)
+    before = t.data_ptr()
+    t.data = t.data.clone()
+    assert t.data_ptr() != before
+    run()
+    assert list(lib.args(name)[at]) == [t.data_ptr() for t in tensors]
+
+
+@pytest.mark.parametrize("which", ["A", "B", "scale", "ranks"])
+@pytest.mark.parametrize("call", [0, 1])
+def test_adapters_whose_memory_no_longer_fits_are_refused(lib, which, call):
+    for broken in (lambda t: t[:1].clone(), lambda t: t.double().to(torch.int16)):
+        ad = adapters()
+        name, _, run = lora_calls(ad)[call]
+        t = getattr(ad, which)
+        t.data = broken(t)
+        with pytest.raises((ValueError, TypeError)):
+            run()
+        assert name not in [n for n, _ in lib.calls]
+
+
+def test_adapters_keep_the_memory_they_were_checked_with(lib):
+    """Else new memory at the address of the old could pass for it."""
+    ad = adapters()
+    assert {s.data_ptr() for s in ad._kept} == {t.data_ptr() for t in
+                                                (ad.A, ad.B, ad.scale, ad.ranks)}
+    old = ad.A.data_ptr()
+    ad.A.data = ad.A.data.clone()
+    assert old in {s.data_ptr() for s in ad._kept}
+    lora_calls(ad)[0][2]()
+    assert old not in {s.data_ptr() for s in ad._kept}

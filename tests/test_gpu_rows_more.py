@@ -81,3 +81,17 @@ def test_an_output_made_on_another_stream_outlives_its_reader():
     torch.cuda.synchronize()
     assert torch.equal(copy, want)
     del other
+
+
+@pytest.mark.parametrize("M", [5, 300, 2100])
+def test_adapters_whose_memory_is_replaced_between_calls(M):
+    y, x, ad, ids = lora_case(M, M, 256, 384, 50, 16, True)
+    other = lora_case(M + 1, M, 256, 384, 50, 16, True)[2]
+    check_lora(y, x, ad, ids)
+    want = check_lora(y, x, other, ids)
+    for t, u in ((ad.A, other.A), (ad.B, other.B), (ad.scale, other.scale),
+                 (ad.ranks, other.ranks)):
+        t.data = u.data.clone()
+    filler = [torch.full_like(t, 3) for t in (ad.A, ad.B) for _ in range(2)]
+    assert torch.equal(check_lora(y, x, ad, ids), want)
+    del filler

@@ -583,26 +583,46 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, layer
 class LoraAdapters:
     """The low-rank adapters of one projection: A bf16 [L, r, K], B bf16
     [L, N, r], scale fp32 [L], ranks int32 [L] (adapter a uses its first
-    ranks[a]; None: r everywhere). Checked once, here; the tensors stay as they
-    are named (their values may change)."""
+    ranks[a]; None: r everywhere). The tensors stay as they are named; their
+    values may change, and so may the memory behind them (t.data = ..., resize_):
+    each call reads their addresses, and one that moved is checked again. Until
+    then the memory that was checked is kept."""
 
-    __slots__ = ("A", "B", "scale", "ranks", "L", "r", "K", "N", "_ptrs")
+    __slots__ = ("A", "B", "scale", "ranks", "L", "r", "K", "N", "_ptrs", "_kept")
 
     def __init__(self, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor,
                  ranks: Optional[torch.Tensor] = None):
         L, r, K = A.shape
         N = B.shape[1]
-        for t, dtype, shape in ((A, torch.bfloat16, (L, r, K)), (B, torch.bfloat16, (L, N, r)),
-                                (scale, torch.float32, (L,)), (ranks, torch.int32, (L,))):
-            if t is not None:
-                _dtype(t, dtype)
-                _shape(t, *shape)
-        ptrs = (_ptr(A), _ptr(B), _ptr(scale), _ptr(ranks))
-        for name, v in zip(self.__slots__, (A, B, scale, ranks, L, r, K, N, ptrs)):
+        for name, v in zip(self.__slots__, (A, B, scale, ranks, L, r, K, N)):
             object.__setattr__(self, name, v)
+        self._check()
 
     def __setattr__(self, name, value):
         raise AttributeError(f"LoraAdapters.{name} is fixed: make new adapters")
+
+    def _check(self):
+        L, r, K, N = self.L, self.r, self.K, self.N
+        tensors = (self.A, self.B, self.scale, self.ranks)
+        for t, dtype, shape in zip(tensors, (torch.bfloat16, torch.bfloat16, torch.float32,
+                                             torch.int32),
+                                   ((L, r, K), (L, N, r), (L,), (L,))):
+            if t is not None:
+                _dtype(t, dtype)
+                _shape(t, *shape)
+        object.__setattr__(self, "_ptrs", tuple(_ptr(t) for t in tensors))
+        # an address that is still the same is then still this memory
+        object.__setattr__(self, "_kept", tuple(t.untyped_storage() for t in tensors
+                                                if t is not None))
+
+    def _addresses(self) -> tuple:
+        """Where A, B, scale and ranks lie now."""
+        ranks = self.ranks
+        ptrs = (self.A.data_ptr(), self.B.data_ptr(), self.scale.data_ptr(),
+                None if ranks is None else ranks.data_ptr())
+        if ptrs != self._ptrs:
+            self._check()
+        return ptrs
 
 
 def lora_workspace(M: int, N: int, K: int, adapters: LoraAdapters, device,
@@ -618,7 +638,7 @@ def lora_add(y: torch.Tensor, x: torch.Tensor, adapters: LoraAdapters, ids: torc
              stream=None) -> torch.Tensor:
     """y [M, N] + scale * B_a (A_a x[m]) for each row's adapter a = ids[m] (rows
     with an id outside [0, L) keep y); bf16. `out` may be y itself."""
-    A, B, scale, ranks = adapters._ptrs
+    A, B, scale, ranks = adapters._addresses()
     L, r, K, N = adapters.L, adapters.r, adapters.K, adapters.N
     M = x.shape[0]
     if out is None:
@@ -647,7 +667,7 @@ def w4a8_linear_lora(x: torch.Tensor, packed: torch.Tensor, N: int, adapters: Lo
                      stream=None) -> torch.Tensor:
     """w4a8_linear of x [M, K] and the adapters' update of its output, in one
     call."""
-    A, B, scale, ranks = adapters._ptrs
+    A, B, scale, ranks = adapters._addresses()
     L, r, K = adapters.L, adapters.r, adapters.K
     M = x.shape[0]
     if N != adapters.N:
