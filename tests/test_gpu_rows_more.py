@@ -95,3 +95,22 @@ def test_adapters_whose_memory_is_replaced_between_calls(M):
     filler = [torch.full_like(t, 3) for t in (ad.A, ad.B) for _ in range(2)]
     assert torch.equal(check_lora(y, x, ad, ids), want)
     del filler
+
+
+def test_adapters_of_the_widest_rows():
+    """2^24 - 128 columns are 65536 blocks of 256, more than a grid has in y."""
+    M, N, K, r = 1300, 2 ** 24 - 128, 128, 8
+    g = gen(1)
+    x = torch.randn(M, K, generator=g, device=DEV).bfloat16()
+    ad = eg.LoraAdapters((torch.randn(1, r, K, generator=g, device=DEV) / 11).bfloat16(),
+                         torch.randn(1, N, r, generator=g, device=DEV).bfloat16(),
+                         torch.ones(1, device=DEV))
+    ids = torch.zeros(M, dtype=torch.int32, device=DEV)
+    ids[5::7] = -1
+    y = torch.ones(M, N, dtype=torch.bfloat16, device=DEV)
+    eg.lora_add(y, x, ad, ids, out=y)
+    for rows in ([0, 5], [642, M - 1]):
+        ref, bound = lora_ref(torch.ones(2, N, dtype=torch.bfloat16, device=DEV), x[rows], ad,
+                              ids[rows])
+        assert ((y[rows].double() - ref).abs() <= bound).all()
+    assert (y[5::7] == 1).all()

@@ -731,10 +731,12 @@ bool lora_few(int64_t M) { return M <= kLoraFewRows; }
 // 16, 1200 rows 19.7 / 28.8; 32 of rank 16, 256 rows 16.5 / 14.4; 16 of rank
 // 128, 800 rows 43.0 / 32.7; 3584 x 18944, 64 of rank 32: 1000 rows 84 / 66,
 // 4093 rows 137 / 123. A batch of more rows than one that takes them takes them
-// too.
+// too, unless its rows are wider than 65535 blocks of kManyCols columns, the
+// most that a grid has in y: those stay with the cluster kernel.
+constexpr int kManyCols = 32 * kLoraWarps;  // columns of a CTA of the second kernel
 static bool lora_many(int64_t M, int64_t N, int L, int r) {
   return std::min<int64_t>(L, M) + M / kLoraTile > (r > 64 ? 44 : 38) &&
-         (N < 8192 || M > 64LL * L);
+         (N < 8192 || M > 64LL * L) && N <= (int64_t)65535 * kManyCols;
 }
 
 // Parts of K of the first kernel: about two CTAs an SM, each of two steps a warp
@@ -835,7 +837,8 @@ cudaError_t launch_lora(const LoraArgs& a, cudaStream_t st, bool beside) {
       : a.r <= 32 ? launch_shrink<4>(p, tiles, st)
                   : launch_shrink<8>(p, tiles, st);
   if (e != cudaSuccess) return e;
-  PdlConfig c(dim3((unsigned)most, (unsigned)((a.N + 255) / 256), 1), kLoraThreads, 0, st);
+  PdlConfig c(dim3((unsigned)most, (unsigned)((a.N + kManyCols - 1) / kManyCols), 1),
+              kLoraThreads, 0, st);
   return a.r <= 32   ? cudaLaunchKernelEx(&c.cfg, lora_expand_kernel<1>, p)
          : a.r <= 64 ? cudaLaunchKernelEx(&c.cfg, lora_expand_kernel<2>, p)
                      : cudaLaunchKernelEx(&c.cfg, lora_expand_kernel<4>, p);
