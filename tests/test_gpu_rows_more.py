@@ -114,3 +114,17 @@ def test_adapters_of_the_widest_rows():
                               ids[rows])
         assert ((y[rows].double() - ref).abs() <= bound).all()
     assert (y[5::7] == 1).all()
+
+
+@pytest.mark.parametrize("M,L", [(60, 50), (300, 5), (2100, 50)])
+def test_adapters_of_an_infinite_scale_keep_what_is_past_their_rank_out(M, L):
+    """Without a plan, planned in the cluster kernel, and in two kernels."""
+    y, x, ad, ids = lora_case(5, M, 256, 256, L, 16, False)
+    ad.scale[::3] = math.inf
+    ad = eg.LoraAdapters(ad.A, ad.B, ad.scale, torch.ones(L, dtype=torch.int32, device=DEV))
+    got = eg.lora_add(y, x, ad, ids).double()
+    ref, bound = lora_ref(y, x, ad, ids)
+    assert torch.isinf(ref).any() and not torch.isnan(ref).any()
+    f = torch.isfinite(ref)
+    assert torch.equal(got[~f], ref[~f])
+    assert ((got - ref).abs() <= bound)[f].all()

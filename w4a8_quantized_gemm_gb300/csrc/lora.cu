@@ -440,7 +440,8 @@ lora_kernel(const LoraParams p) {
          i += kLoraCluster * kLoraThreads) {
       const int row = i / kr, j = i - row * kr;
       float v = 0.f;
-      if (row < rows && j < rank) {
+      const bool in = row < rows && j < rank;
+      if (in) {
         const uint32_t at = part_at + (uint32_t)(row * JS * 32 + j) * 4;
         float q[kLoraCluster];
 #pragma unroll
@@ -448,7 +449,8 @@ lora_kernel(const LoraParams p) {
 #pragma unroll
         for (int c = 0; c < kLoraCluster; ++c) v += q[c];
       }
-      const uint16_t h = f32_to_bf16_bits(sc * v);
+      // (ranks past the adapter's are zeros, whatever its scale is)
+      const uint16_t h = in ? f32_to_bf16_bits(sc * v) : 0;
       const uint32_t to = hs_at + (uint32_t)(row * kHsLd + j) * 2;
 #pragma unroll
       for (int c = 0; c < kLoraCluster; ++c) st_dsmem_u16(map_to_rank(to, c), h);
