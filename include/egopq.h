@@ -358,9 +358,10 @@ typedef enum { EGOPQ_GROUP_MAX = 0, EGOPQ_GROUP_TOP2 = 1 } egopq_group_score;
  *   groups too, go to the lowest index
  *   weights[t][j] = s[ids] (/ (sum_j s[ids] + 1e-20) with renorm) * scale
  * k <= topk_group * (E / n_group); at most 512 experts, 32 picks, 32 groups
- * (more: EGOPQ_ERR_UNSUPPORTED_SHAPE). A logit of -inf masks an expert off
- * (score 0; it is chosen only where no other candidate is left); NaN reads as
- * -inf, +inf as the largest finite number. A softmax without a bias chooses by
+ * (more: EGOPQ_ERR_UNSUPPORTED_SHAPE). A logit of -inf masks an expert off:
+ * score 0, no part in its group's score, and chosen, whatever its bias, only
+ * where no other candidate is left; NaN reads as -inf, +inf as the largest
+ * finite number. A softmax without a bias chooses by
  * the logits themselves, whose order it keeps (groups by two best scores:
  * by the scores). */
 int egopq_moe_route(const void* logits, int logits_bf16, const float* bias, int64_t T, int E, int k,

@@ -128,3 +128,55 @@ def test_adapters_of_an_infinite_scale_keep_what_is_past_their_rank_out(M, L):
     f = torch.isfinite(ref)
     assert torch.equal(got[~f], ref[~f])
     assert ((got - ref).abs() <= bound)[f].all()
+
+
+# ---------------------------------------------------------- experts that are masked off ---
+
+@pytest.mark.parametrize("E,groups,keep,k", [(64, 1, 1, 6), (64, 8, 3, 6), (160, 8, 4, 6),
+                                             (48, 3, 2, 4), (33, 1, 1, 5), (512, 4, 1, 7)])
+@pytest.mark.parametrize("score", [0, 1])
+@pytest.mark.parametrize("top2", [0, 1])
+def test_masked_experts_are_not_chosen_for_their_bias(E, groups, keep, k, score, top2):
+    g = gen(E + k)
+    x = torch.randn(211, E, generator=g, device=DEV)
+    off = torch.rand(211, E, generator=g, device=DEV) < 0.4
+    x[off] = -math.inf
+    x[off & (torch.rand(211, E, generator=g, device=DEV) < 0.2)] = math.nan
+    b = 2 * torch.randn(E, generator=g, device=DEV)
+    kw = dict(bias=b, score=score, n_group=groups, topk_group=keep, group_score=top2)
+    w, ids = eg.moe_route(x, k, **kw)
+    # the definition in 64 bits: a masked expert is no number to choose by
+    s = torch.sigmoid(x.double()) if score else torch.softmax(
+        torch.where(off, -math.inf, x).double(), dim=1)
+    s = torch.where(off, 0.0, s)
+    c = torch.where(off, -math.inf, s + b.double())
+    part = c.view(211, groups, E // groups)
+    if keep < groups:
+        v = part.topk(2, dim=2).values
+        v = torch.where(torch.isinf(v[..., 1]) | (top2 == 0), v[..., 0], v.sum(2))
+        kept = torch.zeros_like(v, dtype=torch.bool).scatter_(
+            1, v.sort(dim=1, descending=True, stable=True).indices[:, :keep], True)
+        c = part.masked_fill(~kept[..., None], -math.inf).reshape(211, E)
+    ref, best = c.sort(dim=1, descending=True, stable=True)
+    enough = torch.isfinite(ref[:, k - 1])
+    assert enough.float().mean() > 0.9
+    assert torch.equal(ids[enough].long(), best[enough, :k])
+    assert not torch.gather(off, 1, ids.long())[enough].any()
+    p = torch.gather(s, 1, ids.long())
+    p = p / (p.sum(dim=1, keepdim=True) + 1e-20)
+    assert torch.allclose(w.double(), p, rtol=1e-5, atol=1e-30)
+
+
+def test_masked_experts_rank_behind_a_score_of_zero():
+    """1 / (1 + e^200) is 0 in 32 bits: still before an expert that is not there,
+    and so is one whose bias is -inf; masked ones go last, by index."""
+    x = torch.full((3, 40), -math.inf, device=DEV)
+    x[:, 30], x[:, 35] = -200.0, 0.0
+    w, ids = eg.moe_route(x, 4, score=eg.SCORE_SIGMOID)
+    assert ids.tolist() == [[35, 30, 0, 1]] * 3
+    assert w.tolist() == [[1.0, 0.0, 0.0, 0.0]] * 3
+    b = torch.zeros(40, device=DEV)
+    b[30] = -math.inf
+    w, ids = eg.moe_route(x, 4, score=eg.SCORE_SIGMOID, bias=b, renorm=False)
+    assert ids.tolist() == [[35, 30, 0, 1]] * 3
+    assert w.tolist() == [[0.5, 0.0, 0.0, 0.0]] * 3

@@ -15,7 +15,8 @@ namespace egopq {
 // ---- router ------------------------------------------------------------------
 // One warp a token; lane l holds the V experts from V l, so that the lowest lane
 // of a tie has its lowest expert. Choices are compared as unsigned keys that
-// keep the order of the floats (0: not to be chosen). A group whose experts are
+// keep the order of the floats (0: not to be chosen; 1: masked off by its logit,
+// behind every number, whatever the bias). A group whose experts are
 // whole lanes, a power of two of them, is scored by exchanges inside its lanes,
 // others by one lane a group out of shared memory. A lane sorts its keys once,
 // so that a pick is a maximum over the lanes and a shift (without the sort, a
@@ -24,6 +25,7 @@ namespace egopq {
 // token takes, about a thousand: 16384 tokens of 256 experts in 8 groups, 8
 // picks, move 18 MB in 17.1 us (1.0 TB/s); one token takes 2 us.
 constexpr int kRouteWarps = 4;
+constexpr uint32_t kMaskedKey = 1;  // (the lowest number's, -inf's, is 0x007FFFFF)
 
 __device__ __forceinline__ uint32_t order_key(float c) {
   const uint32_t u = __float_as_uint(c + 0.f);  // (-0 + 0 = +0: they tie)
@@ -121,6 +123,9 @@ route_kernel(const RouteParams p) {
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) s[i] = clean_logit(s[i]);
+  uint32_t live = 0;  // bit i: expert e0 + i is there and not masked off
+#pragma unroll
+  for (int i = 0; i < V; ++i) live |= (s[i] > -INFINITY ? 1u : 0u) << i;
   float mx = 0.f, inv_sum = 1.f;
   // the softmax without a bias chooses by the logits, whose order it keeps
   // (groups by their two best: by the scores, which are added)
@@ -158,14 +163,14 @@ route_kernel(const RouteParams p) {
         c += __ldg(p.bias + e0 + i);
         if (c != c) c = -INFINITY;  // a NaN choice ranks last
       }
-      key[i] = order_key(c);
+      key[i] = (live >> i) & 1 ? order_key(c) : kMaskedKey;
     }
   }
   if (p.topk_group < p.n_group) {
     // a group's score from its largest key and, for the two best, the second
-    // (0: there is none)
+    // (where there is one that is not masked off)
     auto score_of = [&](uint32_t m1, uint32_t m2) {
-      return p.top2 && m2 ? order_key(key_value(m1) + key_value(m2)) : m1;
+      return p.top2 && m2 > kMaskedKey ? order_key(key_value(m1) + key_value(m2)) : m1;
     };
     uint32_t m1 = 0, m2 = 0;
     if (p.group_lanes) {
