@@ -180,3 +180,25 @@ def test_masked_experts_rank_behind_a_score_of_zero():
     w, ids = eg.moe_route(x, 4, score=eg.SCORE_SIGMOID, bias=b, renorm=False)
     assert ids.tolist() == [[35, 30, 0, 1]] * 3
     assert w.tolist() == [[0.5, 0.0, 0.0, 0.0]] * 3
+
+
+# --------------------------------------------------- large values that meet weights of zero ---
+
+@pytest.mark.parametrize("T,path", [(1, eg.PATH_GEMV), (5, eg.PATH_GEMV), (20, eg.PATH_GEMV),
+                                    (60, eg.PATH_GEMV), (60, eg.PATH_TC), (400, eg.PATH_TC)])
+@pytest.mark.parametrize("big", [1e3, 1e4, 1e5, 1e30])
+def test_large_activations_that_meet_weights_of_zero_cost_the_others_nothing(T, path, big):
+    """Channels of x, and gated values, far larger than the rest, whose codes equal
+    their zero points: no part of the sums, and no part of their error."""
+    E, k, H, I = 4, 2, 512, 384
+    _, ids, w, gu, dn = experts_case(3, T, E, k, H, I)
+    x = torch.randn(T, H, generator=gen(2), device=DEV)
+    ch = torch.arange(5, H, 97, device=DEV)
+    if path == eg.PATH_TC:
+        big = min(big, 1e5)         # (fp16 beside it keeps what is above 2^-29 of the row's largest)
+    x[:, ch] *= big
+    gu[0][:, :, ch] = gu[2].repeat_interleave(128, -1)[:, :, ch]
+    hc = torch.arange(3, I, 50, device=DEV)
+    gu[1][:, I + hc] *= min(big, 1e4)
+    dn[0][:, :, hc] = dn[2].repeat_interleave(128, -1)[:, :, hc]
+    check_experts((x.bfloat16(), ids, w, gu, dn), eg.VARIANT_W4A16, path)

@@ -114,20 +114,21 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The four operand words of one word of packed codes, with as little arithmetic
-// as it takes: the zero point is not subtracted here but from the group's sum,
-// as z (or z + 128) times the sum of the activations, which one more row tile
-// of ones gives in the same fragment layout.
+// The four operand words of one word of packed codes.
 //   W4A8: the masked nibbles themselves are fp16 numbers below the smallest
 //   normal one, q * 2^-24 (words 0 and 2) and q * 2^-20 (words 1 and 3, whose
 //   activations come divided by 16: see quant_rows_kernel); every product and
 //   sum is a whole multiple of 2^-24, below 2^24 of them, so the group's sum is
-//   exact.
-//   W4A16: 128 + q as bf16. The group's sum then carries 128 sum(x) besides,
-//   which costs the fp32 sum at most seven of its 24 bits: the result keeps
-//   more than the 8 of a bf16 output by a factor of 2^9.
+//   exact, and the zero point is subtracted from it, as z times the sum of the
+//   activations, which one more row tile of ones gives in the same fragment
+//   layout.
+//   W4A16: q - z, exact, from 128 + q and 128 + z (zz: a pair) as bf16. The products are
+//   summed in 32 bits, where a sum is as good as its largest terms: with the
+//   zero point taken from the sum, an activation of 1e4 that meets weights of
+//   zero (q = z) cost its neighbours of size 1 more than the bf16 result's
+//   rounding.
 template <int VARIANT>
-__device__ __forceinline__ void raw_w4_word(uint32_t w, uint32_t (&o)[4]) {
+__device__ __forceinline__ void raw_w4_word(uint32_t w, __nv_bfloat162 zz, uint32_t (&o)[4]) {
   if constexpr (VARIANT == kW4A8) {
     const uint32_t w2 = w >> 8;
     o[0] = w & 0x000F000Fu;
@@ -136,7 +137,11 @@ __device__ __forceinline__ void raw_w4_word(uint32_t w, uint32_t (&o)[4]) {
     o[3] = w2 & 0x00F000F0u;
   } else {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) o[q] = lop3_and_or(w >> (4 * q), 0x000F000Fu, 0x43004300u);
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t h = lop3_and_or(w >> (4 * q), 0x000F000Fu, 0x43004300u);
+      const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&h), zz);
+      o[q] = *reinterpret_cast<const uint32_t*>(&r);
+    }
   }
 }
 
@@ -227,50 +232,56 @@ struct Stream {
       const uint4* src[NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) src[nt] = i + 1 < n_units ? next_x(nt) : nullptr;
+      // zero points: rows 8q .. 8q + 7 are the nibbles of word q
+      uint32_t z4[4];
+      __nv_bfloat162 zz[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        z4[q] = (word_of(zw, q) >> (4 * gid)) & 0xFu;
+        zz[q] = __bfloat162bfloat162(__ushort_as_bfloat16((uint16_t)(0x4300u | z4[q])));
+      }
       float acc[2][NT][4], ones[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int q = 0; q < 4; ++q) acc[0][nt][q] = acc[1][nt][q] = ones[nt][q] = 0.f;
-      // (three independent chains of matrix instructions a column tile)
+      // (independent chains of matrix instructions a column tile: two, and W4A8's
+      // ones)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         uint32_t a[4][4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) raw_w4_word<VARIANT>(word_of(w[q], j), a[q]);
-        constexpr uint32_t kOne = VARIANT == kW4A8 ? 0x3C003C00u : 0x3F803F80u;
-        // (words 1 and 3 times 16, to undo the division of W4A8)
-        constexpr uint32_t kOne16 = VARIANT == kW4A8 ? 0x4C004C00u : 0x3F803F80u;
+        for (int q = 0; q < 4; ++q) raw_w4_word<VARIANT>(word_of(w[q], j), zz[q], a[q]);
+        // ones (words 1 and 3: 16, to undo the activations' division)
+        constexpr uint32_t kOne = 0x3C003C00u, kOne16 = 0x4C004C00u;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const uint4 b = x[nt][j];
           mma_16816<VARIANT>(acc[0][nt], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
           mma_16816<VARIANT>(acc[1][nt], a[2][0], a[3][0], a[2][1], a[3][1], b.x, b.y);
-          mma_16816<VARIANT>(ones[nt], kOne, kOne, kOne16, kOne16, b.x, b.y);
+          if constexpr (VARIANT == kW4A8)
+            mma_16816<VARIANT>(ones[nt], kOne, kOne, kOne16, kOne16, b.x, b.y);
           mma_16816<VARIANT>(acc[0][nt], a[0][2], a[1][2], a[0][3], a[1][3], b.z, b.w);
           mma_16816<VARIANT>(acc[1][nt], a[2][2], a[3][2], a[2][3], a[3][3], b.z, b.w);
-          mma_16816<VARIANT>(ones[nt], kOne, kOne, kOne16, kOne16, b.z, b.w);
+          if constexpr (VARIANT == kW4A8)
+            mma_16816<VARIANT>(ones[nt], kOne, kOne, kOne16, kOne16, b.z, b.w);
           // the next unit's word, a unit ahead of its use
           if (src[nt]) x[nt][j] = __ldg(src[nt] + j * kWord);
         }
       }
-      // zero points: rows 8q .. 8q + 7 are the nibbles of word q
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const float s = f16_bits_to_f32(sh[q]);
-        const uint32_t zz = (word_of(zw, q) >> (4 * gid)) & 0xFu;
-        // -(z + 128) as a float: 2^23 + 128 + z under a sign, plus 2^23; W4A8: of
-        // the scaled sums, -z 2^-24
-        const float zf =
-            __uint_as_float(0xCB000000u | (zz + (VARIANT == kW4A8 ? 0u : 128u))) + 8388608.f;
-        const float z = VARIANT == kW4A8 ? zf * 0x1p-24f : zf;
+        // W4A8: the sums are scaled by 2^-24, and -z 2^-24 as a float is 2^23 + z
+        // under a sign, plus 2^23, times that
+        const float z = (__uint_as_float(0xCB000000u | z4[q]) + 8388608.f) * 0x1p-24f;
         const float sz = VARIANT == kW4A8 ? s * 0x1p24f : s;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            // sum(a q) - z sum(a) (exact), or sum(x (128 + q)) - (z + 128) sum(x)
-            const float v = fmaf(z, ones[nt][c], acc[q >> 1][nt][(q & 1) * 2 + c]);
+            float v = acc[q >> 1][nt][(q & 1) * 2 + c];
+            if constexpr (VARIANT == kW4A8) v = fmaf(z, ones[nt][c], v);  // (exact)
             float& t = sum[q >> 1][nt][(q & 1) * 2 + c];
             t = fmaf(sz, v, t);
           }
