@@ -202,3 +202,63 @@ def test_large_activations_that_meet_weights_of_zero_cost_the_others_nothing(T, 
     gu[1][:, I + hc] *= min(big, 1e4)
     dn[0][:, :, hc] = dn[2].repeat_interleave(128, -1)[:, :, hc]
     check_experts((x.bfloat16(), ids, w, gu, dn), eg.VARIANT_W4A16, path)
+
+
+# ------------------------------------------------ weights that change between calls ---
+
+@pytest.mark.parametrize("variant", VARIANTS)
+@pytest.mark.parametrize("T,path", [(1, eg.PATH_AUTO), (7, eg.PATH_AUTO), (30, eg.PATH_GEMV),
+                                    (90, eg.PATH_TC), (900, eg.PATH_TC)])
+def test_experts_follow_weights_rewritten_in_place(variant, T, path):
+    E, k, H, I = 8, 2, 512, 256
+    x, ids, w, _, _ = experts_case(50, T, E, k, H, I)
+    layers = []
+    for i in range(3):
+        gu, dn = experts_case(51 + i, 1, E, k, H, I)[3:]
+        gu, dn = ((q, s * (i + 1), z) for q, s, z in (gu, dn))
+        layers.append(eg.moe_pack(*gu, *dn))
+    ws = eg.moe_workspace(T, k, E, H, I, variant, DEV, path)
+    want = [eg.moe_experts(x, ids, w, layer, variant=variant, path=path) for layer in layers]
+    layer = eg.MoeLayer(layers[0].gate_up.clone(), layers[0].down.clone(), E, H, I)
+    torch.cuda.synchronize()
+    got = []
+    for i in range(24):
+        layer.gate_up.copy_(layers[i % 3].gate_up)
+        layer.down.copy_(layers[i % 3].down)
+        got.append(eg.moe_experts(x, ids, w, layer, variant=variant, path=path, workspace=ws))
+    torch.cuda.synchronize()
+    for i, y in enumerate(got):
+        assert torch.equal(y, want[i % 3]), i
+    assert eg.device_status() == 0
+
+
+@pytest.mark.parametrize("M,N", [(1, 512), (100, 512), (260, 512), (300, 8320), (2100, 512)])
+@pytest.mark.parametrize("fused", [False, True])
+def test_adapters_follow_weights_rewritten_in_place(M, N, fused):
+    K, L, r = 768, 20, 24
+    cases = [lora_case(60 + i, M, N, K, L, r, True) for i in range(3)]
+    y, x, first, ids = cases[0]
+    packed = [eg.pack_w4(*w4(gen(i), N, K)) for i in range(3)]
+    ad = eg.LoraAdapters(*(t.clone() for t in (first.A, first.B, first.scale, first.ranks)))
+    weight = packed[0].clone()
+    if fused:
+        ws = eg.w4a8_linear_lora_workspace(M, N, K, ad, DEV)
+        def call(a, p, **kw):
+            return eg.w4a8_linear_lora(x, p, N, a, ids, **kw)
+    else:
+        ws = eg.lora_workspace(M, N, K, ad, DEV)
+        def call(a, p, **kw):
+            return eg.lora_add(y, x, a, ids, **kw)
+    want = [call(c[2], p) for c, p in zip(cases, packed)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(24):
+        new = cases[i % 3][2]
+        for t, u in ((ad.A, new.A), (ad.B, new.B), (ad.scale, new.scale), (ad.ranks, new.ranks),
+                     (weight, packed[i % 3])):
+            t.copy_(u)
+        got.append(call(ad, weight, workspace=ws))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert torch.equal(g, want[i % 3]), i
+    assert eg.device_status() == 0

@@ -103,8 +103,8 @@ __device__ __forceinline__ void cp_async16_weights(uint32_t dst, const void* src
                "l"(policy)
                : "memory");
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -169,10 +169,11 @@ struct Stream {
     // row `lane`'s 16 bytes of each chunk (a copy is 512 contiguous bytes a
     // warp: with the lanes in fragment order, 32 bytes of four chunks a quarter
     // warp, the copies issued four times slower and one token's gate and up
-    // products took 14 instead of 9 us), and a word of the 32 rows' scales or
-    // zero points
+    // products took 14 instead of 9 us), and of five lanes 16 of the 32 rows'
+    // scales and zero points (all past L1: the products that begin early prime
+    // their rings before their wait)
     w_off = (rbase + lane) * 16;
-    m_off = lane < 16 ? 8192 + 2 * rbase + lane * 4 : 8448 + rbase / 2 + (lane - 16) * 4;
+    m_off = lane < 4 ? 8192 + 2 * rbase + lane * 16 : 8448 + rbase / 2;
   }
 
   template <typename Rec>
@@ -184,7 +185,7 @@ struct Stream {
 #pragma unroll
       for (int c = 0; c < 4; ++c)  // (rows of chunk c exchanged: conflict-free fragments)
         cp_async16_weights(st + (c * 32 + (lane ^ (2 * c))) * 16, rec + w_off + 2048 * c, policy);
-      if (lane < 20) cp_async4(st + 2048 + lane * 4, rec + m_off);
+      if (lane < 5) cp_async16(st + 2048 + lane * 16, rec + m_off);
       put = put + 1 == kStages ? 0 : put + 1;
     }
     cp_async_commit();

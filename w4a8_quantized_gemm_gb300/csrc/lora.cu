@@ -623,7 +623,7 @@ lora_expand_kernel(const LoraParams p) {
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         b[js][t] = make_uint4(0, 0, 0, 0);
-        if (in && j < rank) b[js][t] = __ldg(reinterpret_cast<const uint4*>(src + 2 * t * p.r + j));
+        if (in && j < rank) b[js][t] = __ldcg(reinterpret_cast<const uint4*>(src + 2 * t * p.r + j));
       }
     }
     if (rank & 7) {
