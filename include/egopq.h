@@ -338,7 +338,9 @@ int egopq_bf16_gemm_twin(const uint16_t* x_bf16, const uint16_t* w_bf16, int64_t
  * packed linear: each row of a batch names the weights it is multiplied with.
  * Row picks (expert and adapter ids) are int32; a pick outside [0, count) is
  * no error but a row without that product (an expert of another machine, a
- * request without an adapter), so the calls need no host synchronization.
+ * request without an adapter), so the calls need no host synchronization. Ids
+ * and the router's weights need the alignment of their own 4 bytes only, so that
+ * a batch can be a slice of a larger one at any row.
  * Workspaces are caller-owned device memory, 16-byte aligned, of at least the
  * bytes the matching query returns (0 for a refused shape and for an empty
  * batch); calls sharing one must be ordered on one stream. Results do not

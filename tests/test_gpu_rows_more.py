@@ -262,3 +262,49 @@ def test_adapters_follow_weights_rewritten_in_place(M, N, fused):
     for i, g in enumerate(got):
         assert torch.equal(g, want[i % 3]), i
     assert eg.device_status() == 0
+
+
+# ------------------------------------------------------- batches that are slices of others ---
+
+def at_any_row(t, first):
+    """A copy of `t` whose first element lies `first` elements behind a 16-byte
+    boundary."""
+    buf = torch.zeros(first + t.numel() + 4, dtype=t.dtype, device=DEV)
+    v = buf[first:first + t.numel()].view(t.shape)
+    v.copy_(t)
+    assert v.data_ptr() % 16 == 4 * first % 16
+    return v
+
+
+@pytest.mark.parametrize("variant", VARIANTS)
+@pytest.mark.parametrize("T,path", [(1, eg.PATH_GEMV), (7, eg.PATH_GEMV), (30, eg.PATH_GEMV),
+                                    (401, eg.PATH_TC), (1701, eg.PATH_TC)])
+@pytest.mark.parametrize("first", [1, 2, 3])
+def test_experts_of_sliced_picks(variant, T, path, first):
+    x, ids, w, gu, dn = experts_case(T, T, 8, 3, 256, 128)
+    ids[::3, 1] = -1
+    layer = eg.moe_pack(*gu, *dn)
+    want = eg.moe_experts(x, ids, w, layer, variant=variant, path=path)
+    got = eg.moe_experts(x, at_any_row(ids, first), at_any_row(w, first), layer, variant=variant,
+                         path=path)
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("M", [5, 300, 2101, 5003])
+@pytest.mark.parametrize("first", [1, 2, 3])
+def test_adapters_of_sliced_ids(M, first):
+    y, x, ad, ids = lora_case(M, M, 256, 256, 50, 16, True)
+    want = eg.lora_add(y, x, ad, ids)
+    assert torch.equal(eg.lora_add(y, x, ad, at_any_row(ids, first)), want)
+    packed = eg.pack_w4(*w4(gen(M), 256, 256))
+    want = eg.w4a8_linear_lora(x, packed, 256, ad, ids)
+    assert torch.equal(eg.w4a8_linear_lora(x, packed, 256, ad, at_any_row(ids, first)), want)
+
+
+@pytest.mark.parametrize("first", [1, 2, 3])
+def test_router_writes_into_slices(first):
+    x = torch.randn(77, 64, generator=gen(1), device=DEV)
+    w, ids = eg.moe_route(x, 6)
+    out = (at_any_row(torch.zeros_like(w), first), at_any_row(torch.zeros_like(ids), first))
+    eg.moe_route(x, 6, out=out)
+    assert torch.equal(out[0], w) and torch.equal(out[1], ids)

@@ -335,18 +335,20 @@ plan_kernel(const int32_t* __restrict__ ids, int n, int S, int bt, RowPlan plan,
     __syncthreads();
   }
   int v[PT];
+  const bool vec = (reinterpret_cast<uintptr_t>(ids) & 15) == 0;  // (a slice's need not be)
   // picks [i0, i0 + PT) as set numbers; past the end: S + 1
   auto load = [&](int64_t i0) {
 #pragma unroll
     for (int q = 0; q < PT; q += 4) {
       int4 u = make_int4(S + 1, S + 1, S + 1, S + 1);
       const int64_t i = i0 + q;
-      if (i + 3 < n) {
+      if (vec && i + 3 < n) {
         u = __ldcg(reinterpret_cast<const int4*>(ids + i));
       } else if (i < n) {
         u.x = __ldcg(ids + i);
         if (i + 1 < n) u.y = __ldcg(ids + i + 1);
         if (i + 2 < n) u.z = __ldcg(ids + i + 2);
+        if (i + 3 < n) u.w = __ldcg(ids + i + 3);
       }
       v[q] = u.x;
       v[q + 1] = u.y;

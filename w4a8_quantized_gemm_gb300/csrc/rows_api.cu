@@ -118,6 +118,12 @@ int check_aligned(const void* p, uintptr_t to, const char* name) {
   return EGOPQ_OK;
 }
 
+// A row's own picks and weights, which are read (or written) one by one: a batch
+// may be a slice of a larger one, at any row.
+int check_picks(const void* p, const char* name) {
+  return p ? check_aligned(p, 4, name) : fail(EGOPQ_ERR_INVALID_ARG, "%s is NULL", name);
+}
+
 }  // namespace
 
 extern "C" {
@@ -144,8 +150,9 @@ int egopq_moe_route(const void* logits, int logits_bf16, const float* bias, int6
                 "at most 512 experts, 32 picks and 32 groups (got E=%d k=%d n_group=%d T=%lld)", E,
                 k, n_group, (long long)T);
   if (T == 0) return EGOPQ_OK;
-  int rc = check_ptrs(3, "logits", logits, "weights", weights, "ids", ids);
+  int rc = check_ptrs(1, "logits", logits);
   if (rc) return rc;
+  if ((rc = check_picks(weights, "weights")) || (rc = check_picks(ids, "ids"))) return rc;
   if ((rc = check_aligned(bias, 16, "bias"))) return rc;
   if ((rc = check_arch())) return rc;
   RouteArgs a;
@@ -220,10 +227,10 @@ int egopq_moe_experts(const uint16_t* x_bf16, const int32_t* ids, const float* w
   if (path != EGOPQ_PATH_AUTO && path != EGOPQ_PATH_GEMV && path != EGOPQ_PATH_TC)
     return fail(EGOPQ_ERR_INVALID_ARG, "unknown path %d", path);
   if (T == 0) return EGOPQ_OK;
-  rc = check_ptrs(7, "x_bf16", x_bf16, "ids", ids, "weights", weights, "packed_gate_up",
-                  packed_gate_up, "packed_down", packed_down, "out_bf16", out_bf16, "workspace",
-                  workspace);
+  rc = check_ptrs(5, "x_bf16", x_bf16, "packed_gate_up", packed_gate_up, "packed_down",
+                  packed_down, "out_bf16", out_bf16, "workspace", workspace);
   if (rc) return rc;
+  if ((rc = check_picks(ids, "ids")) || (rc = check_picks(weights, "weights"))) return rc;
   ExpertsArgs a{};
   a.variant = variant;
   a.T = T;
@@ -267,9 +274,10 @@ int egopq_lora_add(const uint16_t* y_in, const uint16_t* x_bf16, const uint16_t*
   int rc = check_lora_shape(M, N, K, L, r);
   if (rc) return rc;
   if (M == 0) return EGOPQ_OK;
-  rc = check_ptrs(8, "y_in", y_in, "x_bf16", x_bf16, "A_bf16", A_bf16, "B_bf16", B_bf16, "scale",
-                  scale, "ids", ids, "y_out", y_out, "workspace", workspace);
+  rc = check_ptrs(7, "y_in", y_in, "x_bf16", x_bf16, "A_bf16", A_bf16, "B_bf16", B_bf16, "scale",
+                  scale, "y_out", y_out, "workspace", workspace);
   if (rc) return rc;
+  if ((rc = check_picks(ids, "ids"))) return rc;
   if ((rc = check_aligned(ranks, 16, "ranks"))) return rc;
   LoraArgs a{};
   a.y_in = y_in;
@@ -311,9 +319,10 @@ int egopq_w4a8_linear_lora(const uint16_t* x_bf16, const void* packed, const uin
     return fail(EGOPQ_ERR_INVALID_ARG, "unknown path %d", path);
   if (M == 0) return EGOPQ_OK;
   // every argument of both halves is checked before the first launch
-  rc = check_ptrs(8, "x_bf16", x_bf16, "packed", packed, "A_bf16", A_bf16, "B_bf16", B_bf16,
-                  "scale", scale, "ids", ids, "y_bf16", y_bf16, "workspace", workspace);
+  rc = check_ptrs(7, "x_bf16", x_bf16, "packed", packed, "A_bf16", A_bf16, "B_bf16", B_bf16,
+                  "scale", scale, "y_bf16", y_bf16, "workspace", workspace);
   if (rc) return rc;
+  if ((rc = check_picks(ids, "ids"))) return rc;
   if ((rc = check_aligned(ranks, 16, "ranks"))) return rc;
   const size_t lin = egopq_w4a8_linear_workspace_bytes(M, K, group, path);
   const size_t lin_up = (lin + 255) / 256 * 256;
