@@ -405,7 +405,8 @@ int egopq_moe_experts(const uint16_t* x_bf16, const int32_t* ids, const float* w
 
 /* Low-rank adapters beside a shared projection:
  *   y_out[m] = bf16( y_in[m] + scale[a] * B_a (A_a x[m]) ),  a = ids[m]
- * y_in, y_out bf16 [M][N] (may be the same buffer), x bf16 [M][K]; A bf16
+ * y_in, y_out bf16 [M][N] (the same buffer, or apart), x bf16 [M][K] apart from
+ * y_out (an overlap is refused: rows are written while others are formed); A bf16
  * [L][r][K], B bf16 [L][N][r], scale fp32 [L]; ranks int32 [L] or NULL:
  * adapter a uses its first ranks[a] (at most r) rows of A and columns of B,
  * whatever the rest holds. A row whose id is outside [0, L) keeps y_in.
@@ -420,7 +421,8 @@ int egopq_lora_add(const uint16_t* y_in, const uint16_t* x_bf16, const uint16_t*
                    uint16_t* y_out, void* workspace, size_t workspace_bytes,
                    egopq_stream_t stream);
 
-/* egopq_w4a8_linear and egopq_lora_add on its output, in one call. */
+/* egopq_w4a8_linear and egopq_lora_add on its output, in one call (y apart from
+ * x). */
 size_t egopq_w4a8_linear_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int group, int L,
                                               int r, int path);
 int egopq_w4a8_linear_lora(const uint16_t* x_bf16, const void* packed, const uint16_t* A_bf16,

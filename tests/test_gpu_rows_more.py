@@ -308,3 +308,34 @@ def test_router_writes_into_slices(first):
     out = (at_any_row(torch.zeros_like(w), first), at_any_row(torch.zeros_like(ids), first))
     eg.moe_route(x, 6, out=out)
     assert torch.equal(out[0], w) and torch.equal(out[1], ids)
+
+
+# --------------------------------------------------------------- outputs over inputs ---
+
+@pytest.mark.parametrize("M", [5, 300, 2100])
+def test_adapters_refuse_an_output_over_x(M):
+    y, x, ad, ids = lora_case(M, M, 256, 256, 50, 16, True)
+    packed = eg.pack_w4(*w4(gen(M), 256, 256))
+    for call in (lambda out: eg.lora_add(y, x, ad, ids, out=out),
+                 lambda out: eg.w4a8_linear_lora(x, packed, 256, ad, ids, out=out)):
+        keep = x.clone()
+        with pytest.raises(eg.EgopqError, match="overlap"):
+            call(x)
+        assert torch.equal(x, keep)
+    both = torch.zeros(M + 1, 256, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(eg.EgopqError, match="overlap"):
+        eg.lora_add(both[:M], x, ad, ids, out=both[1:])
+
+
+@pytest.mark.parametrize("variant", VARIANTS)
+@pytest.mark.parametrize("T,path", [(1, eg.PATH_GEMV), (7, eg.PATH_GEMV), (30, eg.PATH_GEMV),
+                                    (90, eg.PATH_TC), (900, eg.PATH_TC)])
+def test_experts_may_write_over_x(variant, T, path):
+    """Every row of x has been read before the first output is written."""
+    x, ids, w, gu, dn = experts_case(T, T, 8, 3, 512, 256)
+    layer = eg.moe_pack(*gu, *dn)
+    want = eg.moe_experts(x, ids, w, layer, variant=variant, path=path)
+    for _ in range(5):
+        y = x.clone()
+        assert eg.moe_experts(y, ids, w, layer, variant=variant, path=path, out=y) is y
+        assert torch.equal(y, want)

@@ -29,3 +29,29 @@ def test_picks_between_their_elements_are_refused(lib, at):
     assert route(lib, ids=A + at) == -3 and route(lib, weights=A + at) == -3
     assert experts(lib, ids=A + at) == -3 and experts(lib, w=A + at) == -3
     assert lora(lib, ids=A + at) == -3 and linear_lora(lib, ids=A + at) == -3
+
+
+# x [4][256], y [4][N]: bytes 2 * 4 * 256 and 2 * 4 * N from their addresses
+@pytest.mark.parametrize("x,y_in,out,N", [
+    (A, 4 * A, A, 256), (A, 4 * A, A + 2032, 256), (A + 2032, 4 * A, A, 256),
+    (A + 4096 - 16, 4 * A, A, 512), (4 * A, A, A + 16, 256), (4 * A, A + 2032, A, 256),
+    (A, A, A, 256)])
+def test_adapters_refuse_an_output_that_lies_on_what_is_read(lib, x, y_in, out, N):
+    assert lora(lib, x=x, y=y_in, out=out, N=N) == -1
+    assert b"overlap" in lib.egopq_last_error_string()
+
+
+@pytest.mark.parametrize("x,y,N", [(A, A, 256), (A, A + 2032, 256), (A + 4080, A, 512)])
+def test_linear_with_adapters_refuses_an_output_that_lies_on_x(lib, x, y, N):
+    assert linear_lora(lib, x=x, y=y, N=N) == -1
+    assert b"overlap" in lib.egopq_last_error_string()
+
+
+def test_adapters_accept_an_output_in_place_or_apart(lib):
+    """Neighbours that touch are apart: such a call gets to the device check (or,
+    on a machine that has one, would run: only shapes of no rows here)."""
+    assert lora(lib, M=0, x=A, y=A, out=A) == 0
+    for x, y_in, out in [(A, A + 2048, A + 2048), (A + 2048, A, A), (A, A + 2048, A + 4096)]:
+        if lib.egopq_supported(4, 256, 256, 128, 0):
+            pytest.skip("a device is there: the addresses here are not")
+        assert lora(lib, x=x, y=y_in, out=out) != -1

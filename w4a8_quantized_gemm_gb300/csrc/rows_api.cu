@@ -118,6 +118,22 @@ int check_aligned(const void* p, uintptr_t to, const char* name) {
   return EGOPQ_OK;
 }
 
+bool overlap(const uint16_t* a, int64_t na, const uint16_t* b, int64_t nb) {
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+  return pa < pb + 2 * (uintptr_t)nb && pb < pa + 2 * (uintptr_t)na;
+}
+
+// The adapters' update writes rows of y while other rows (and other columns of
+// the same rows) are still formed from x: y may be updated in place, row for
+// row, but not lie on x.
+int check_lora_overlap(const LoraArgs& a) {
+  if (overlap(a.x, a.M * a.K, a.y_out, a.M * a.N))
+    return fail(EGOPQ_ERR_INVALID_ARG, "the output overlaps x");
+  if (a.y_in != a.y_out && overlap(a.y_in, a.M * a.N, a.y_out, a.M * a.N))
+    return fail(EGOPQ_ERR_INVALID_ARG, "y_out overlaps y_in and is not y_in");
+  return EGOPQ_OK;
+}
+
 // A row's own picks and weights, which are read (or written) one by one: a batch
 // may be a slice of a larger one, at any row.
 int check_picks(const void* p, const char* name) {
@@ -296,6 +312,7 @@ int egopq_lora_add(const uint16_t* y_in, const uint16_t* x_bf16, const uint16_t*
   const size_t need = carve_lora(workspace, a);
   if (workspace_bytes < need)
     return fail(EGOPQ_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  if ((rc = check_lora_overlap(a))) return rc;
   if ((rc = check_arch())) return rc;
   return lora_result(launch_lora(a, (cudaStream_t)stream), M);
 }
@@ -329,7 +346,6 @@ int egopq_w4a8_linear_lora(const uint16_t* x_bf16, const void* packed, const uin
   const size_t need = lin_up + egopq_lora_workspace_bytes(M, N, K, L, r);
   if (workspace_bytes < need)
     return fail(EGOPQ_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
-  if ((rc = check_arch())) return rc;
   LoraArgs a{};
   a.y_in = y_bf16;
   a.x = x_bf16;
@@ -345,6 +361,8 @@ int egopq_w4a8_linear_lora(const uint16_t* x_bf16, const void* packed, const uin
   a.r = r;
   a.y_out = y_bf16;
   carve_lora(static_cast<uint8_t*>(workspace) + lin_up, a);
+  if ((rc = check_lora_overlap(a))) return rc;
+  if ((rc = check_arch())) return rc;
   const cudaStream_t st = (cudaStream_t)stream;
   rc = run_linear(x_bf16, packed, M, N, K, y_bf16, static_cast<uint8_t*>(workspace),
                   auto_path(M, kW4A8, path), st, &a);
