@@ -382,11 +382,14 @@ lora_kernel(const LoraParams p) {
   const int64_t c_lo = me * chunks / parts, c_hi = (me + 1) * chunks / parts;
   if (set < 0) {
     if (p.beside) wait();
-    for (int i = 0; i < n_rows; ++i) {
-      const int64_t at = (int64_t)rows_of[i] * p.N;
-      for (int64_t v = c_lo * 4 + threadIdx.x; v < c_hi * 4; v += kLoraThreads)
-        reinterpret_cast<uint4*>(p.y_out + at)[v] =
-            *(reinterpret_cast<const uint4*>(p.y_in + at) + v);
+    // (all rows' vectors at once: row by row a tile of 32 took 10 us)
+    const int nv = (int)(c_hi - c_lo) * 4;  // 16-byte vectors of a row
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n_rows * nv; i += kLoraThreads) {
+      const int row = i / nv;
+      const int64_t at = (int64_t)rows_of[row] * p.N + (c_lo * 4 + i - row * nv) * 8;
+      *reinterpret_cast<uint4*>(p.y_out + at) =
+          __ldcg(reinterpret_cast<const uint4*>(p.y_in + at));
     }
     return;
   }
