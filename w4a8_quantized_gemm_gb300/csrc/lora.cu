@@ -728,20 +728,35 @@ lora_expand_kernel(const LoraParams p) {
 bool lora_few(int64_t M) { return M <= kLoraFewRows; }
 
 // Whether a batch with a plan takes the two kernels. The cluster kernel holds 38
-// tiles at once (a little more at high ranks, where its second round costs less
-// than the two kernels' way of B) and repeats its chain of waits for the next
-// ones, but goes through wide rows of y without a stop, where the two kernels
-// start a CTA a 256 columns. Two kernels / cluster kernel, us, 3584 x 3584: 8
-// adapters of rank 64, 800 rows 26.3 / 23.7, 1000 rows 28.9 / 34.1; 2 of rank
-// 16, 1200 rows 19.7 / 28.8; 32 of rank 16, 256 rows 16.5 / 14.4; 16 of rank
-// 128, 800 rows 43.0 / 32.7; 3584 x 18944, 64 of rank 32: 1000 rows 84 / 66,
-// 4093 rows 137 / 123. A batch of more rows than one that takes them takes them
-// too, unless its rows are wider than 65535 blocks of kManyCols columns, the
-// most that a grid has in y: those stay with the cluster kernel.
-constexpr int kManyCols = 32 * kLoraWarps;  // columns of a CTA of the second kernel
+// tiles of 32 rows at once (a little more at high ranks, where its second round
+// costs less than the two kernels' way of B) and repeats its chain of waits for
+// the next ones; rows end a tile in the middle once an adapter, 3 / 8 of a tile
+// on the measured mean. The two kernels read B once for every 128 rows of an
+// adapter, which with few rows each and wide y costs more than those rounds, and
+// start a CTA a 256 columns, where the cluster kernel goes through wide rows
+// without a stop. Two kernels / cluster kernel, us, K = 3584, every row with an
+// adapter:
+//   N = 3584   2 adapters of rank 16, 1100 rows 18.4 / 16.0, 1200 rows 18.9 /
+//              21.9; 8 of rank 64, 1000 rows 31.5 / 23.4, 1200 rows 33.5 / 34.7;
+//              8 of rank 128, 1300 rows 55.1 / 52.8, 1400 rows 44.8 / 53.5; 32 of
+//              rank 16, 800 rows 18.4 / 17.6, 900 rows 18.4 / 21.6; 128 of rank
+//              16, 1000 rows 39.9 / 39.2
+//   N = 7168   64 of rank 32, 1000 rows 43.4 / 33.7, 2100 rows 48.8 / 50.0; 128
+//              of rank 16, 2100 rows 56.3 / 53.6; 8 of rank 64, 2500 rows 47.2 /
+//              61.2
+//   N = 9472   8 of rank 64, 1000 rows 45.8 / 30.8, 2500 rows 55.6 / 67.4
+//   N = 12288  32 of rank 16, 1200 rows 37.3 / 36.2, 1400 rows 36.9 / 38.0, of
+//              rank 64, 1700 rows 64.5 / 57.2, 2100 rows 71.4 / 73.5; 64 of rank
+//              32, 2100 rows 72.3 / 59.2
+//   N = 18944  8 of rank 16, 1000 rows 40.0 / 27.5, 4093 rows 101 / 92; 32 of
+//              rank 32, 4093 rows 133 / 106, 16384 rows 444 / 358; 2 of rank 64,
+//              2500 rows 84 / 91, 16384 rows 444 / 447
+// A batch of more rows than one that takes them takes them too. (N below 16384
+// also keeps the second kernel's column blocks within what a grid has in y.)
 static bool lora_many(int64_t M, int64_t N, int L, int r) {
-  return std::min<int64_t>(L, M) + M / kLoraTile > (r > 64 ? 44 : 38) &&
-         (N < 8192 || M > 64LL * L) && N <= (int64_t)65535 * kManyCols;
+  const int64_t sets = std::min<int64_t>(L, M);
+  return N < 16384 && 8 * M + 3 * kLoraTile * sets > 8 * kLoraTile * (r > 64 ? 44 : 38) &&
+         160 * M >= sets * (N - 2048);
 }
 
 // Parts of K of the first kernel: about two CTAs an SM, each of two steps a warp
@@ -842,8 +857,7 @@ cudaError_t launch_lora(const LoraArgs& a, cudaStream_t st, bool beside) {
       : a.r <= 32 ? launch_shrink<4>(p, tiles, st)
                   : launch_shrink<8>(p, tiles, st);
   if (e != cudaSuccess) return e;
-  PdlConfig c(dim3((unsigned)most, (unsigned)((a.N + kManyCols - 1) / kManyCols), 1),
-              kLoraThreads, 0, st);
+  PdlConfig c(dim3((unsigned)most, (unsigned)((a.N + 255) / 256), 1), kLoraThreads, 0, st);
   return a.r <= 32   ? cudaLaunchKernelEx(&c.cfg, lora_expand_kernel<1>, p)
          : a.r <= 64 ? cudaLaunchKernelEx(&c.cfg, lora_expand_kernel<2>, p)
                      : cudaLaunchKernelEx(&c.cfg, lora_expand_kernel<4>, p);
