@@ -393,7 +393,7 @@ int egopq_moe_pack_gate_up(const uint8_t* w_q, const uint16_t* scale_f16, const 
  * pick's output once to bf16. H and I multiples of 128 below 2^20, E <= 1024.
  * path: EGOPQ_PATH_GEMV streams the weights for few rows an expert,
  * EGOPQ_PATH_TC runs the tcgen05 products, AUTO picks by the rows an expert has
- * on average (12 and fewer stream). The tensor-core products hold a weight
+ * on average (15 and fewer stream). The tensor-core products hold a weight
  * s * (q - z) as fp16 (exact integers with the scales beside them in W4A8's gate
  * and up products): a weight of 65520 and more becomes infinite there. */
 size_t egopq_moe_experts_workspace_bytes(int64_t T, int k, int E, int64_t H, int64_t I, int group,

@@ -264,10 +264,11 @@ cudaError_t launch_plan(const int32_t* ids, int64_t n, int S, int bt, const RowP
 // How a call's products run (experts.cu).
 enum ExpertsWay { kExpertsFew, kExpertsStream, kExpertsTensor };
 // (AUTO: the tcgen05 products from more than kStreamRows picks an expert;
-// 64 experts, 8 picks, 3584 x 1280, W4A16: 10 picks an expert 174 us streamed
-// and 172 on the tensor cores, 12.5 picks 188 and 174; 32 experts, 4 picks,
-// 2048 x 1024: 10 picks 51 and 60, 18.8 picks 69 and 61)
-constexpr int64_t kStreamRows = 12;
+// streamed / on the tensor cores, us, 14 and 16 picks an expert: 64 experts, 8
+// picks, 3584 x 1280, W4A16 156 / 170 and 169 / 169, W4A8 175 / 186 and 192 /
+// 186; 32 experts, 4 picks, 2048 x 1024, W4A16 54.7 / 57.2 and 58.0 / 57.6, W4A8
+// 59.3 / 62.5 and 64.8 / 62.6)
+constexpr int64_t kStreamRows = 15;
 ExpertsWay experts_way(int64_t T, int k, int E, int path);
 
 // Experts: one call's operands and workspace parts, validated by the ABI layer.

@@ -1091,11 +1091,14 @@ static cudaError_t run_experts(const ExpertsArgs& a, cudaStream_t st) {
   p.E = a.E;
   p.N = (int)(2 * a.I);
   p.G = (int)(a.H / 128);
-  // rows of a tile: the average expert's in one tile as a rule (an expert with
-  // more takes several, whose weights then come from L2; 64 experts, 8 picks,
-  // 3584 x 1280, W4A16: 6 picks an expert take 125 us in tiles of 8, 8 picks
-  // 156 us in tiles of 16)
-  const int nt = n <= (int64_t)6 * a.E ? 1 : 2;
+  // rows of a tile, 8 or 16: an expert with more rows takes several tiles, whose
+  // weights then come from L2, but a tile of 16 multiplies twice as much per
+  // record, and W4A8 half as much again for its zero points. Tiles of 8 / of 16,
+  // us, by picks an expert: 64 experts, 8 picks, 3584 x 1280, W4A16 6: 115 / 118,
+  // 7: 125 / 120, W4A8 14: 175 / 178, 16: 192 / 192; 32 experts, 4 picks, 2048 x
+  // 1024, W4A16 6: 38.7 / 41.8, 10: 47.3 / 47.3, W4A8 14: 59.3 / 59.9, 16: 64.8 /
+  // 64.1
+  const int nt = n <= (int64_t)(VARIANT == kW4A8 ? 15 : 6) * a.E ? 1 : 2;
   cudaError_t e = cudaSuccess;
   if (a.way == kExpertsStream) e = launch_plan(a.ids, n, a.E, 8 * nt, a.plan, st);
   // (the rows do not depend on the plan: they are quantized, or placed, beside it)
