@@ -36,12 +36,6 @@ __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, 
                : "memory");
 }
 
-// `bytes` (a multiple of 16, at a 16-byte boundary) on their way into L2.
-__device__ __forceinline__ void prefetch_l2(const void* from, int bytes) {
-  if (bytes > 0)
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
-}
-
 constexpr int kLoraWarps = 8;
 constexpr int kLoraThreads = 32 * kLoraWarps;
 constexpr int kLoraMaxRank = 128;
