@@ -417,8 +417,11 @@ __device__ __forceinline__ float quant_code(float x, float s, float inv) {
   return (float)max(-127, min(127, __float2int_rn(__fdiv_rn(x, s))));
 }
 
-// silu(g) * u (fast exponential and quotient: a few 2^-22, far below the bf16
-// rounding that follows)
+// silu(g) * u. The fast exponential's error grows with |g|, by some 1.2 of its
+// last places for each 1 of it beside the 2 it begins with, and the quotient adds
+// two: 2^-21 of the result near 0, 2^-18 at |g| = 20, 2^-16 at the -87 below which
+// the quotient is 0 (where silu(g) is 1e-36) -- all below the 2^-8 of the bf16
+// that the products' results end as.
 __device__ __forceinline__ float gated(float g, float u) {
   return __fdividef(g, 1.f + __expf(-g)) * u;
 }

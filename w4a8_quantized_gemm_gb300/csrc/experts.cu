@@ -39,10 +39,11 @@ namespace egopq {
 // The weights stream from HBM once: each warp keeps kStages - 1 groups of its
 // rows in flight (2.1 KB each) with cp.async into a ring of its own, which no
 // other warp waits for. Bound by HBM where the rows are few; the conversion of
-// the codes (about 2.5 instructions a pair) and the matrix instructions (45 % of
-// their pipe) are next. 33 tokens of 64 experts (8 picks, 3584 x 1280, W4A8) take
-// 95 us, 4.8 TB/s of the 6.8 a copy reaches; one token (W4A16) 20.5 us, of which
-// the weights' 57 MB are 8.4 and the rest the two kernels' starts and ends.
+// the codes (2.5 instructions a pair in W4A8, 3.5 in W4A16) and the matrix
+// instructions (W4A8: 45 % of their pipe) are next. 33 tokens of 64 experts (8
+// picks, 3584 x 1280) touch 56 experts on average, 404 MB: W4A8 95 us, 4.2 TB/s of
+// the 6.8 a copy reaches, W4A16 100; one token 20.4 us (W4A8 24.0), of which the
+// weights' 57 MB are 8.4 and the rest the kernels' starts and ends.
 constexpr int kStages = 4;
 constexpr int kStageBytes = 2176;  // 4 x 512 codes, 64 scales, 16 zero points, padding
 constexpr int kWarps = 4;          // of a CTA: parts of K, or blocks of rows

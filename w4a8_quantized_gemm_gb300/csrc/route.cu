@@ -20,10 +20,10 @@ namespace egopq {
 // whole lanes, a power of two of them, is scored by exchanges inside its lanes,
 // others by one lane a group out of shared memory. A lane sorts its keys once,
 // so that a pick is a maximum over the lanes and a shift (without the sort, a
-// search of every lane's V keys a pick: 19.3 us where this takes 17.1). The
+// search of every lane's V keys a pick: 19.3 us where this took 17.1). The
 // weights are formed last, for the picks alone. Bound by the instructions a
 // token takes, about a thousand: 16384 tokens of 256 experts in 8 groups, 8
-// picks, move 18 MB in 17.1 us (1.0 TB/s); one token takes 2 us.
+// picks, move 18 MB in 17.5 us (1.0 TB/s); one token takes 2 us.
 constexpr int kRouteWarps = 4;
 constexpr uint32_t kMaskedKey = 1;  // (the lowest number's, -inf's, is 0x007FFFFF)
 
@@ -303,7 +303,10 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t st) {
   if (a.E <= 32) return launch_route_v<1>(p, st);
   if (a.E <= 64) return launch_route_v<2>(p, st);
   if (a.E <= 128) return launch_route_v<4>(p, st);
-  // (160 experts in 8 groups of 20 are four whole lanes a group at five a lane)
+  // (five experts a lane: 160 in 8 groups of 20 are then four whole lanes a group.
+  // Five / eight a lane, 16384 tokens: 160 experts in 8 groups 12.1 / 20.4 us, in
+  // 4 11.8 / 21.3, in one 9.9 / 12.6, 140 in 4 17.0 / 21.3; one token of 160 in 8
+  // groups 2.6 / 4.0)
   if (a.E <= 160 && p.per_group % 5 == 0) return launch_route_v<5>(p, st);
   if (a.E <= 256) return launch_route_v<8>(p, st);
   return launch_route_v<16>(p, st);

@@ -8,9 +8,10 @@
 // W4A8, or for W4A16 the bf16 values over a power of two (fp16 holds their
 // eight bits exactly from 2^-29 of the row's largest up). The weights enter in
 // one of two ways:
-//   folded  s * (q - z) as fp16, rounded once (2^-12 of it at most, far below
-//           the bf16 result's 2^-9): a whole row of K accumulates in Tensor
-//           Memory and is read once a tile
+//   folded  s * (q - z) as fp16, rounded once (2^-11 of it at most, and
+//           independently a weight, where the bf16 result's rounding is 2^-8): a
+//           whole row of K accumulates in Tensor Memory and is read once a tile.
+//           A product of 65520 and more becomes infinite
 //   exact   q - z: every group's sum is the exact integer, read a group at a
 //           time and scaled and added in fp32. For the gate and up products of
 //           W4A8, whose bf16 results are quantized again: the folded weights'
