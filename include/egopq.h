@@ -395,7 +395,8 @@ int egopq_moe_pack_gate_up(const uint8_t* w_q, const uint16_t* scale_f16, const 
  * EGOPQ_PATH_TC runs the tcgen05 products, AUTO picks by the rows an expert has
  * on average (15 and fewer stream). The tensor-core products hold a weight
  * s * (q - z) as fp16 (exact integers with the scales beside them in W4A8's gate
- * and up products): a weight of 65520 and more becomes infinite there. */
+ * and up products): a weight of 65520 and more becomes infinite there, and W4A16
+ * activations below 2^-29 of their row's largest lose bits. */
 size_t egopq_moe_experts_workspace_bytes(int64_t T, int k, int E, int64_t H, int64_t I, int group,
                                          int variant, int path);
 int egopq_moe_experts(const uint16_t* x_bf16, const int32_t* ids, const float* weights,

@@ -393,6 +393,8 @@ __device__ __forceinline__ int few_slot(const uint32_t (&m)[4], int t, int T, in
 }
 
 // ---- h = silu(G x) * (U x) -----------------------------------------------------------
+// h is rounded to bf16 once: W4A8's codes are those of bf16 values by definition,
+// and W4A16's down product takes bf16 operands.
 template <int VARIANT, int NT, bool FEW, bool SPLIT>
 __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 5 : 4)
 experts_gate_up_kernel(const StreamParams p) {

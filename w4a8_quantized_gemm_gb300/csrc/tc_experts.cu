@@ -457,6 +457,9 @@ ragged_kernel(const __grid_constant__ CUtensorMap row_map, const __grid_constant
           else out[(c + (up ? 1 : 0)) * kCols + col] = f32_to_bf16_bits(h);
         }
       } else {
+        // (a pick's output is rounded to bf16 once before the picks are summed in
+        // fp32: written and read again once a pick, it is half of fp32's memory,
+        // 235 MB at 4096 tokens of 8 picks and 3584 columns)
 #pragma unroll
         for (int c = 0; c < RD; c += 2) {
           const float2 a2 = *reinterpret_cast<const float2*>(as_c + c);
