@@ -308,12 +308,17 @@ def _plain_ragged(s, c):
 
 # -------------------------------------------------- the definition in 64 bits ---
 
+def _pow64(e):
+    """2^e in 64 bits, exactly (a power function is off by a last place)."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
 def _round64(v, bits, lowest):
     """v >= 0 to numbers of `bits` bits whose smallest power of two is 2^lowest,
     ties to even, in 64 bits."""
     e = torch.floor(torch.log2(torch.clamp(v, min=2.0 ** lowest)))
-    e = torch.where(torch.pow(2.0, e) > v, e - 1, e).clamp(min=lowest)
-    unit = torch.pow(2.0, e - (bits - 1))
+    e = torch.where(_pow64(e) > v, e - 1, e).clamp(min=lowest)
+    unit = _pow64(e - (bits - 1))
     return torch.round(v / unit) * unit
 
 
@@ -330,9 +335,9 @@ def _values64(x, fmt, ts):
     top = b.abs().max(dim=-1, keepdim=True).values
     if fmt == "e8m0":
         e = torch.floor(torch.log2(torch.clamp(top, min=2.0 ** -149)))
-        e = torch.where(torch.pow(2.0, e) > top, e - 1, torch.where(
-            torch.pow(2.0, e + 1) <= top, e + 1, e))
-        scale = torch.pow(2.0, torch.clamp(e - 2, -127, 127))
+        e = torch.where(_pow64(e) > top, e - 1, torch.where(
+            _pow64(e + 1) <= top, e + 1, e))
+        scale = _pow64(torch.clamp(e - 2, -127, 127))
     else:
         scale = torch.clamp(_round64(top / torch.full_like(top, 6.0), 4, -6), max=448.0)
     q = torch.clamp(_round64(b.abs() / torch.where(scale == 0, 1.0, scale), 2, 0), max=6.0)
@@ -346,7 +351,7 @@ def _weight64(weight, fmt):
     v = torch.empty(*packed.shape[:-1], packed.shape[-1], 2, dtype=torch.float64, device=DEV)
     v[..., 0], v[..., 1] = table[(packed % 16).long()], table[(packed // 16).long()]
     if fmt == "e8m0":
-        sc = torch.pow(2.0, scale.double() - 127.0)
+        sc = _pow64(scale.double() - 127.0)
     else:
         sc = scale.view(torch.float8_e4m3fn).double()
     return v.reshape(*sc.shape, -1).mul_(sc[..., None]).reshape(*packed.shape[:-1], -1)
