@@ -432,6 +432,84 @@ int egopq_w4a8_linear_lora(const uint16_t* x_bf16, const void* packed, const uin
                            int r, uint16_t* y_bf16, void* workspace, size_t workspace_bytes,
                            int path, egopq_stream_t stream);
 
+/* ---- microscaled 4-bit linears ----------------------------------------------------
+ * Values of 4 bits, e2m1: 0, .5, 1, 1.5, 2, 3, 4, 6 (codes 0..7) and a sign (bit
+ * 3); blocks of neighbours along K share a scale, a byte:
+ *   EGOPQ_MX4_E8M0  blocks of 32, scale 2^(byte - 127) (255: NaN)
+ *   EGOPQ_MX4_E4M3  blocks of 16, scale a positive e4m3 number (127: NaN), and one
+ *                   fp32 scale g of the whole tensor (NULL: 1)
+ * A stored value is code * scale (* g). Codes are [rows][K/2] bytes, the value of
+ * even k in the low nibble, scales [rows][K/block]. Both sides of a product are
+ * held in 4 bits, and the tensor cores multiply them with their scales, summing
+ * in fp32. K % 32 == 0; any number of rows M (0: a no-op) and weight rows N.
+ * Pointers are 16-byte aligned (tensor scales, offsets and an index 4-byte). */
+typedef enum { EGOPQ_MX4_E8M0 = 0, EGOPQ_MX4_E4M3 = 1 } egopq_mx4_format;
+typedef enum { EGOPQ_TYPE_BF16 = 0, EGOPQ_TYPE_F16 = 1, EGOPQ_TYPE_F32 = 2 } egopq_type;
+
+/* Rows to 4 bits. u = x (E8M0) or x * r, r = 1/g rounded to fp32, the product
+ * rounded once to fp32 (E4M3); A = the largest |u| of a block:
+ *   E8M0: scale 2^e, e = floor(log2 A) - 2, at least -127 (A = 0 too)
+ *   E4M3: scale = A / 6 rounded to e4m3, at most 448; 0 leaves the block 0
+ *   codes = u / scale to the nearest, ties to the even code, at most 6
+ * Where A is infinite or NaN the block's scale is NaN and its codes 0. gated:
+ * x is [M][2K], and u = silu(x[:K]) * x[K:] (* r), silu(v) = v / (1 + exp(-v)),
+ * not rounded at all: codes and scales are those of the real number (a product
+ * beyond fp32 makes its block NaN). tensor_scale: g, fp32 [1], or NULL (must be
+ * NULL for E8M0).
+ * codes and scales may be NULL (together), and so may operand: the form that
+ * egopq_mx4_gemm reads, egopq_mx4_operand_bytes(M, K, format) bytes. */
+size_t egopq_mx4_operand_bytes(int64_t M, int64_t K, int format);
+int egopq_mx4_quant(const void* x, int x_type, int64_t M, int64_t K, int format,
+                    const float* tensor_scale, int gated, uint8_t* codes, uint8_t* scales,
+                    void* operand, egopq_stream_t stream);
+
+/* The values that codes and scales stand for: y [M][K] = code * scale (exact in
+ * fp32), times g if there is one (rounded to fp32), rounded to y_type. */
+int egopq_mx4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K, int format,
+                      const float* tensor_scale, int y_type, void* y, egopq_stream_t stream);
+
+/* Weights of `sets` linears (1; or the experts of a layer), codes [sets][N][K/2]
+ * and scales [sets][N][K/block], into the products' layout and back:
+ * egopq_mx4_packed_bytes bytes (0 for a refused shape), records of 128 rows and
+ * 256 K, their codes swizzled as the tensor cores read them and their scales
+ * behind them; rows and columns past the weight are zeros. sets <= 1024. */
+size_t egopq_mx4_packed_bytes(int64_t sets, int64_t N, int64_t K, int format);
+int egopq_mx4_pack(const uint8_t* codes, const uint8_t* scales, int64_t sets, int64_t N, int64_t K,
+                   int format, void* packed, egopq_stream_t stream);
+int egopq_mx4_unpack(const void* packed, int64_t sets, int64_t N, int64_t K, int format,
+                     uint8_t* codes, uint8_t* scales, egopq_stream_t stream);
+
+/* y [M][N] = rows times weights: sum_k a[m][k] w[n][k] over the stored values,
+ * times a_scale[0] * w_scale[0] (fp32; NULL: 1), rounded once to y_type.
+ * operand: of egopq_mx4_quant for the same M, K and format; packed: one set. */
+int egopq_mx4_gemm(const void* operand, const void* packed, const float* a_scale,
+                   const float* w_scale, int64_t M, int64_t N, int64_t K, int format, int y_type,
+                   void* y, egopq_stream_t stream);
+
+/* egopq_mx4_quant of x (tensor_scale = a_scale) into the workspace and the product
+ * with `packed`, in one call. x [M][K], or [M][2K] gated; y apart from x. A
+ * workspace (egopq_mx4_linear_workspace_bytes, 0 for a refused shape and for no
+ * rows) serves fewer rows as well; calls sharing one must be ordered on one
+ * stream. sets: 0 for egopq_mx4_linear, else those of the ragged call. */
+size_t egopq_mx4_linear_workspace_bytes(int64_t rows, int64_t sets, int64_t K, int format);
+int egopq_mx4_linear(const void* x, int x_type, int64_t M, int64_t N, int64_t K, int gated,
+                     const float* a_scale, const void* packed, const float* w_scale, int format,
+                     int y_type, void* y, void* workspace, size_t workspace_bytes,
+                     egopq_stream_t stream);
+
+/* The same with a weight for each run of rows: rows [offsets[e], offsets[e + 1])
+ * of y are x's times set e's weight (scaled by a_scale[0] * w_scale[e]). offsets
+ * int32 [sets + 1], device, rising, within [0, rows] (a value outside, or below
+ * one before it, counts as the nearest allowed); a set may be empty, and y's rows
+ * before offsets[0] and from offsets[sets] on stay as they are. index int32
+ * [rows] or NULL: row r of the batch is x's row index[r] (x has x_rows rows; an
+ * index outside reads as a row of zeros); without it x_rows == rows. */
+int egopq_mx4_linear_ragged(const void* x, int x_type, int64_t x_rows, const int32_t* index,
+                            const int32_t* offsets, int64_t rows, int64_t sets, int64_t N,
+                            int64_t K, int gated, const float* a_scale, const void* packed,
+                            const float* w_scale, int format, int y_type, void* y, void* workspace,
+                            size_t workspace_bytes, egopq_stream_t stream);
+
 /* ---- support, status --------------------------------------------------------------
  * 1 if (M, N, K, group, variant) is accepted by the parity-tested kernels on
  * the current device, 0 if not. It claims nothing the kernels do not run (a

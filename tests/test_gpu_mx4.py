@@ -1,0 +1,279 @@
+"""Microscaled 4-bit linears on the GPU against their definition in 64 bits
+(tests/mx4_helpers.py)."""
+import math
+
+import pytest
+import torch
+
+import w4a8_quantized_gemm_gb300 as eg
+from mx4_helpers import BLOCK, dequant, quant, same_codes, tolerance, values_in
+
+pytestmark = pytest.mark.gpu
+
+FORMATS = [eg.MX4_E8M0, eg.MX4_E4M3]
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def rand(g, *shape, scale=1.0, dtype=torch.bfloat16):
+    return (torch.randn(shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def tscale(x, fmt):
+    return (x.float().abs().max() / 2688.0).reshape(1) if fmt == eg.MX4_E4M3 else None
+
+
+def weight(g, fmt, *shape):
+    """A packed weight and its 64-bit values [.., N, K] (scaled)."""
+    w = rand(g, *shape, scale=0.05, dtype=torch.float32)
+    sets = shape[0] if len(shape) == 3 else 1
+    ts = None
+    if fmt == eg.MX4_E4M3:
+        ts = w.reshape(sets, -1).abs().amax(dim=1) / 2688.0
+    u = w if ts is None else w / (ts.view(sets, 1, 1) if len(shape) == 3 else ts)
+    c, s = quant(u.reshape(-1, shape[-1]).double(), fmt)
+    c, s = c.view(*shape[:-1], -1), s.view(*shape[:-1], -1)
+    v = dequant(c, s, fmt)
+    if ts is not None:
+        v = v * (ts.double().view(sets, 1, 1) if len(shape) == 3 else ts.double())
+    return eg.mx4_pack(c, s, fmt, tensor_scale=ts), v, (c, s)
+
+
+def rows64(x, K, fmt, ts, gated=False):
+    v = dequant(*quant(values_in(x, K, fmt, ts, gated), fmt), fmt)
+    return v if ts is None else v * ts.double()
+
+
+def check(y, a, w):
+    """y against a [M, K] times w [N, K]."""
+    ref = a @ w.t()
+    off = (y.double() - ref).abs()
+    bad = off > tolerance(ref, a.abs() @ w.abs().t(), a.shape[1], y.dtype)
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()}, {off.max()}"
+
+
+# --------------------------------------------------------------- quantization ---
+
+def awkward(g, M, K, dtype):
+    """Blocks of every size a type has, zeros, ties, a lone large value."""
+    x = torch.randn(M, K, generator=g, device="cuda")
+    e = torch.randint(-24 if dtype is torch.float16 else -140, 10, (M, K // 16), generator=g,
+                      device="cuda")
+    x = x * torch.ldexp(torch.ones((), device="cuda", dtype=torch.float64),
+                        e).repeat_interleave(16, dim=1)
+    x[::3, : K // 2] = (torch.randint(-24, 25, (len(x[::3]), K // 2), generator=g, device="cuda")
+                        * 0.25).double()
+    x[1::5, 16:32] = 0.0
+    x[2::7, 0] = 30000.0
+    return x.to(dtype)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,K", [(1, 32), (3, 96), (130, 288), (259, 1056), (1, 18944)])
+def test_codes_and_scales(fmt, dtype, M, K):
+    x = awkward(gen(1), M, K, dtype)
+    rows = eg.mx4_quant(x, fmt)
+    c, s = quant(x.double(), fmt)
+    assert torch.equal(rows.scales, s)
+    assert same_codes(rows.codes, c)
+    # the products' form holds the same
+    c2, s2 = eg.mx4_unpack(eg.Mx4Weight(rows.a_tc, 0, M, K, fmt, None))
+    assert torch.equal(s2, rows.scales) and torch.equal(c2, rows.codes)
+    assert eg.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("scale", [1.0, 0.0117, 3.0e-5, 1000.0])
+def test_tensor_scale(dtype, scale):
+    x = awkward(gen(2), 67, 480, dtype)
+    ts = torch.tensor([scale], device="cuda")
+    rows = eg.mx4_quant(x, eg.MX4_E4M3, tensor_scale=ts)
+    c, s = quant(values_in(x, 480, 1, ts, False), eg.MX4_E4M3)
+    assert torch.equal(rows.scales, s) and same_codes(rows.codes, c)
+    v = dequant(rows.codes, rows.scales, eg.MX4_E4M3) * ts.double()
+    for out in TYPES:
+        got = eg.mx4_dequant(rows, dtype=out)
+        assert torch.equal(got, v.float().to(out))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_values_back(fmt, dtype):
+    """Every code under every scale, exactly."""
+    top = 255 if fmt == eg.MX4_E8M0 else 128
+    n = BLOCK[fmt]
+    scales = torch.arange(top, dtype=torch.uint8, device="cuda").repeat_interleave(32 // n)
+    K = top * 32
+    codes = (torch.arange(K // 2, device="cuda") * 37 % 256).to(torch.uint8).view(1, -1)
+    rows = eg.Mx4Rows(codes, scales.view(1, -1), None, 1, K, fmt, None)
+    want = dequant(codes, scales.view(1, -1), fmt).float().to(dtype)
+    assert torch.equal(torch.nan_to_num(eg.mx4_dequant(rows, dtype=dtype), nan=7.5),
+                       torch.nan_to_num(want, nan=7.5))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_blocks_without_a_value(fmt):
+    x = rand(gen(3), 4, 128, dtype=torch.float32)
+    n = BLOCK[fmt]
+    x[0, 5], x[1, n + 1], x[2, 2 * n] = math.nan, math.inf, -math.inf
+    rows = eg.mx4_quant(x, fmt)
+    v = eg.mx4_dequant(rows, dtype=torch.float32)
+    nan = torch.zeros(4, 128, dtype=torch.bool, device="cuda")
+    nan[0, :n] = nan[1, n:2 * n] = nan[2, 2 * n:3 * n] = True
+    assert torch.equal(v.isnan(), nan)
+    assert torch.equal(rows.scales[3], quant(x[3:].double(), fmt)[1][0])
+    # a row that holds one gives NaN, its neighbours do not
+    w, w64, _ = weight(gen(4), fmt, 40, 128)
+    y = eg.mx4_linear(x, w)
+    assert y[:3].isnan().all()
+    check(y[3:], rows64(x[3:], 128, fmt, None), w64)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,K", [(1, 32), (33, 1056), (700, 1408)])
+def test_gated_codes(fmt, dtype, M, K):
+    """Codes of the real gated values: none of 64 bits' is off by rounding."""
+    g = gen(5)
+    x = rand(g, M, 2 * K, scale=2.5, dtype=dtype)
+    x[::4, :16] = 0.0
+    # large gates: the gated value is next to a product of short numbers
+    x[1::4, 32:64] = (torch.randint(8, 40, (len(x[1::4]), min(32, 2 * K - 32)), generator=g,
+                                    device="cuda").to(dtype))
+    ts = torch.tensor([0.013], device="cuda") if fmt == eg.MX4_E4M3 else None
+    rows = eg.mx4_quant(x, fmt, tensor_scale=ts, gated=True)
+    c, s = quant(values_in(x, K, fmt, ts, True), fmt)
+    assert torch.equal(rows.scales, s) and same_codes(rows.codes, c)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_gated_values_where_fp32_runs_out(fmt):
+    """Gates far below zero, tiny products, a tensor scale that makes up for them."""
+    K = 64
+    x = torch.zeros(6, 2 * K, device="cuda")
+    i = torch.arange(K, device="cuda")
+    x[0, :K], x[0, K:] = -85.0 - 0.25 * i, 1e30
+    x[1, :K], x[1, K:] = 1e-25, 1e-20 * (1 + i)
+    x[2, :K], x[2, K:] = -60.0 - i, 1.0
+    x[3, :K], x[3, K:] = 1e-30 * (1 + i), 1e-15
+    x[4, :K], x[4, K:] = 3.0e30, 1e6
+    x[4, 40], x[4, K + 40] = 3e30, 3e30          # beyond fp32
+    x[5, ::3] = 1.0
+    ts = torch.tensor([1e-30], device="cuda") if fmt == eg.MX4_E4M3 else None
+    if ts is not None:
+        x[4] = 0.0
+    rows = eg.mx4_quant(x, fmt, tensor_scale=ts, gated=True)
+    c, s = quant(values_in(x, K, fmt, ts, True), fmt)
+    assert torch.equal(rows.scales, s) and same_codes(rows.codes, c)
+
+
+# -------------------------------------------------------------------- products ---
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,K", [
+    (1, 1, 32), (1, 128, 256), (2, 130, 64), (7, 200, 96), (16, 256, 512), (17, 127, 288),
+    (64, 384, 1056), (65, 33, 320), (128, 129, 2048), (129, 257, 768), (300, 500, 1312),
+    (1, 3584, 3584), (5, 512, 18944), (517, 1031, 2080)])
+def test_linear(fmt, M, N, K):
+    g = gen(M * 7 + N)
+    x = rand(g, M, K)
+    w, w64, _ = weight(g, fmt, N, K)
+    ts = tscale(x, fmt)
+    y = eg.mx4_linear(x, w, tensor_scale=ts)
+    assert eg.device_status() == 0
+    check(y, rows64(x, K, fmt, ts), w64)
+    # in two calls, the same
+    rows = eg.mx4_quant(x, fmt, tensor_scale=ts, with_codes=False)
+    assert torch.equal(eg.mx4_gemm(rows, w), y)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("x_type", TYPES)
+@pytest.mark.parametrize("y_type", TYPES)
+def test_types(fmt, x_type, y_type):
+    g = gen(11)
+    x = rand(g, 37, 416, dtype=x_type)
+    w, w64, _ = weight(g, fmt, 201, 416)
+    y = eg.mx4_linear(x, w, dtype=y_type)
+    assert y.dtype is y_type
+    check(y, rows64(x, 416, fmt, None), w64)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(1, 384, 1408), (40, 200, 96), (259, 130, 512)])
+def test_gated_linear(fmt, M, N, K):
+    g = gen(12)
+    x = rand(g, M, 2 * K, scale=1.5)
+    ts = torch.tensor([0.004], device="cuda") if fmt == eg.MX4_E4M3 else None
+    w, w64, _ = weight(g, fmt, N, K)
+    y = eg.mx4_linear(x, w, tensor_scale=ts, gated=True)
+    check(y, rows64(x, K, fmt, ts, gated=True), w64)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_pack_and_back(fmt):
+    for shape in [(1, 32), (130, 288), (3, 129, 96)]:
+        w, _, (c, s) = weight(gen(13), fmt, *shape)
+        c2, s2 = eg.mx4_unpack(w)
+        assert torch.equal(c, c2) and torch.equal(s, s2)
+
+
+# --------------------------------------------------------------- ragged products ---
+
+def check_ragged(counts, N, K, fmt, before=0, after=0, tokens=None, gated=False, seed=20,
+                 dtype=torch.bfloat16):
+    g = gen(seed)
+    E, n = len(counts), before + sum(counts) + after
+    off = before + torch.tensor([0] + counts, device="cuda").cumsum(0)
+    x = rand(g, tokens or n, K * (2 if gated else 1), dtype=dtype)
+    index = None
+    if tokens:
+        index = torch.randint(0, tokens, (n,), generator=g, device="cuda", dtype=torch.int32)
+    w, w64, _ = weight(g, fmt, E, N, K)
+    ts = tscale(x, fmt)
+    y = torch.full((n, N), 77.0, dtype=dtype, device="cuda")
+    eg.mx4_linear_ragged(x, off.int(), w, index=index, tensor_scale=ts, gated=gated, out=y)
+    assert eg.device_status() == 0
+    a = rows64(x, K, fmt, ts, gated)
+    if tokens:
+        a = a[index.long()]
+    for e in range(E):
+        lo, hi = int(off[e]), int(off[e + 1])
+        if lo < hi:
+            check(y[lo:hi], a[lo:hi], w64[e])
+    assert (y[:before] == 77.0).all() and (y[n - after:] == 77.0).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("counts,N,K", [
+    ([1], 32, 32), ([0, 0, 3], 130, 96), ([5, 0, 1, 16, 17], 256, 512),
+    ([127, 128, 129, 1, 0, 300], 200, 288), ([0] * 40 + [2] + [0] * 40, 64, 256),
+    ([3] * 33, 100, 64), ([700, 20], 384, 1056)])
+def test_ragged(fmt, counts, N, K):
+    check_ragged(counts, N, K, fmt)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_ragged_gathered_and_gated(fmt):
+    check_ragged([9, 0, 150, 30], 257, 480, fmt, tokens=50)
+    check_ragged([9, 0, 150, 30], 257, 480, fmt, gated=True)
+    check_ragged([2, 0, 3], 64, 96, fmt, before=4, after=130)
+    check_ragged([2, 0, 3], 64, 96, fmt, before=1, after=2, tokens=3, gated=True,
+                 dtype=torch.float16)
+
+
+def test_ragged_without_rows():
+    w, _, _ = weight(gen(21), 0, 4, 64, 64)
+    x = rand(gen(22), 6, 64)
+    y = torch.full((6, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+    eg.mx4_linear_ragged(x, torch.zeros(5, dtype=torch.int32, device="cuda"), w, out=y)
+    assert (y == 5.0).all()
+    assert eg.mx4_linear_ragged(x[:0], torch.zeros(5, dtype=torch.int32, device="cuda"),
+                                w).shape == (0, 64)
+    assert eg.device_status() == 0

@@ -103,6 +103,18 @@ def load() -> ctypes.CDLL:
             "egopq_w4a8_linear_lora_workspace_bytes": (sz, [i64, i64, i64, i32, i32, i32, i32]),
             "egopq_w4a8_linear_lora": (i32, [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32,
                                              i32, vp, vp, sz, i32, vp]),
+            "egopq_mx4_operand_bytes": (sz, [i64, i64, i32]),
+            "egopq_mx4_quant": (i32, [vp, i32, i64, i64, i32, vp, i32, vp, vp, vp, vp]),
+            "egopq_mx4_dequant": (i32, [vp, vp, i64, i64, i32, vp, i32, vp, vp]),
+            "egopq_mx4_packed_bytes": (sz, [i64, i64, i64, i32]),
+            "egopq_mx4_pack": (i32, [vp, vp, i64, i64, i64, i32, vp, vp]),
+            "egopq_mx4_unpack": (i32, [vp, i64, i64, i64, i32, vp, vp, vp]),
+            "egopq_mx4_gemm": (i32, [vp, vp, vp, vp, i64, i64, i64, i32, i32, vp, vp]),
+            "egopq_mx4_linear_workspace_bytes": (sz, [i64, i64, i64, i32]),
+            "egopq_mx4_linear": (i32, [vp, i32, i64, i64, i64, i32, vp, vp, vp, i32, i32, vp, vp,
+                                       sz, vp]),
+            "egopq_mx4_linear_ragged": (i32, [vp, i32, i64, vp, vp, i64, i64, i64, i64, i32, vp,
+                                              vp, vp, i32, i32, vp, vp, sz, vp]),
             "egopq_supported": (i32, [i64, i64, i64, i32, i32]),
             "egopq_auto_path": (i32, [i64, i32]),
             "egopq_tc_operand_bytes": (sz, [i64, i64, i32]),
@@ -680,6 +692,241 @@ def w4a8_linear_lora(x: torch.Tensor, packed: torch.Tensor, N: int, adapters: Lo
         _arg(x, torch.bfloat16, M, K), _ptr(packed), A, B, scale, ranks,
         _arg(ids, torch.int32, M), M, N, K, GROUP, L, r, _arg(out, torch.bfloat16, M, N),
         _ptr(workspace), workspace.nbytes, path, _stream(stream)))
+    return out
+
+
+# --------------------------------------------------- microscaled 4-bit linears ---
+
+MX4_E8M0, MX4_E4M3 = 0, 1
+_MX4_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def mx4_block(fmt: int) -> int:
+    """Neighbours along K that share a scale: 32 (MX4_E8M0) or 16 (MX4_E4M3)."""
+    if fmt not in (MX4_E8M0, MX4_E4M3):
+        raise ValueError(f"unknown 4-bit format {fmt}")
+    return 32 if fmt == MX4_E8M0 else 16
+
+
+def _mx4_type(dtype: torch.dtype) -> int:
+    t = _MX4_TYPES.get(dtype)
+    if t is None:
+        raise TypeError(f"expected dtype in {tuple(_MX4_TYPES)}, got {dtype}")
+    return t
+
+
+def _mx4_scale(t: Optional[torch.Tensor], n: int) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dim() == 0 and n == 1:
+        t = t.reshape(1)
+    return _arg(t, torch.float32, n)
+
+
+class Mx4Rows(NamedTuple):
+    """Rows in 4 bits (mx4_quant): codes uint8 [M, K/2] and scales uint8
+    [M, K/block], or None; the form the products read, or None; the tensor's
+    scale (MX4_E4M3), or None for 1."""
+    codes: Optional[torch.Tensor]
+    scales: Optional[torch.Tensor]
+    a_tc: Optional[torch.Tensor]
+    M: int
+    K: int
+    fmt: int
+    tensor_scale: Optional[torch.Tensor]
+
+
+class Mx4Weight(NamedTuple):
+    """A packed 4-bit weight, or the weights of `sets` experts (mx4_pack)."""
+    packed: torch.Tensor
+    sets: int  # 0: one weight [N, K]; else [sets, N, K]
+    N: int
+    K: int
+    fmt: int
+    tensor_scale: Optional[torch.Tensor]
+
+
+def mx4_quant(x: torch.Tensor, fmt: int = MX4_E8M0, tensor_scale: Optional[torch.Tensor] = None,
+              gated: bool = False, with_codes: bool = True, with_tc: bool = True,
+              out: Optional[Mx4Rows] = None, stream=None) -> Mx4Rows:
+    """x [M, K] (bf16, fp16 or fp32) to 4-bit codes and block scales; gated: x is
+    [M, 2K], and silu(x[:, :K]) * x[:, K:] is quantized (include/egopq.h has the
+    formulas). tensor_scale fp32 [1]: MX4_E4M3 only. with_codes writes codes and
+    scales, with_tc the form that mx4_gemm reads. `out`: rows of an earlier call of
+    the same sizes."""
+    block, kind = mx4_block(fmt), _mx4_type(x.dtype)
+    M, K = x.shape
+    if gated:
+        if K % 2:
+            raise ValueError(f"{K} gate and up values: an odd number")
+        K //= 2
+    if out is None:
+        dev = x.device
+        codes = scales = a_tc = None
+        if K % 32:
+            raise EgopqError(-2, f"K ({K}) must be a multiple of 32")
+        if with_codes:
+            codes = _output((M, K // 2), torch.uint8, dev, stream)
+            scales = _output((M, K // block), torch.uint8, dev, stream)
+        if with_tc:
+            a_tc = _output((int(load().egopq_mx4_operand_bytes(M, K, fmt)),), torch.uint8, dev,
+                           stream)
+        out = Mx4Rows(codes, scales, a_tc, M, K, fmt, tensor_scale)
+    else:
+        if (out.M, out.K, out.fmt) != (M, K, fmt):
+            raise ValueError(f"out holds {out.M} x {out.K} of format {out.fmt}, expected "
+                             f"{M} x {K} of {fmt}")
+        _mx4_rows_check(out)
+        out = out._replace(tensor_scale=tensor_scale)
+    _check(load().egopq_mx4_quant(_ptr(x), kind, M, K, fmt, _mx4_scale(tensor_scale, 1), gated,
+                                  _ptr(out.codes), _ptr(out.scales), _ptr(out.a_tc),
+                                  _stream(stream)))
+    return out
+
+
+def _mx4_rows_check(rows: Mx4Rows):
+    """The sizes that a call relies on, of rows that may have been put together by
+    hand."""
+    M, K, block = rows.M, rows.K, mx4_block(rows.fmt)
+    if rows.codes is not None:
+        _arg(rows.codes, torch.uint8, M, K // 2)
+    if rows.scales is not None:
+        _arg(rows.scales, torch.uint8, M, K // block)
+    if rows.a_tc is not None:
+        need = int(load().egopq_mx4_operand_bytes(M, K, rows.fmt))
+        if rows.a_tc.nbytes < need:
+            raise ValueError(f"a_tc of {rows.a_tc.nbytes} bytes, {need} needed")
+
+
+def mx4_dequant(rows: Mx4Rows, dtype: torch.dtype = torch.bfloat16,
+                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The values [M, K] that rows' codes and scales stand for."""
+    if rows.codes is None or rows.scales is None:
+        raise ValueError("rows without codes and scales (with_codes=False)")
+    _mx4_rows_check(rows)
+    if out is None:
+        out = _output((rows.M, rows.K), dtype, rows.codes.device, stream)
+    _check(load().egopq_mx4_dequant(_ptr(rows.codes), _ptr(rows.scales), rows.M, rows.K, rows.fmt,
+                                    _mx4_scale(rows.tensor_scale, 1), _mx4_type(dtype),
+                                    _arg(out, dtype, rows.M, rows.K), _stream(stream)))
+    return out
+
+
+def mx4_pack(codes: torch.Tensor, scales: torch.Tensor, fmt: int = MX4_E8M0,
+             tensor_scale: Optional[torch.Tensor] = None, stream=None) -> Mx4Weight:
+    """Pack 4-bit weights for the products: codes uint8 [N, K/2] and scales uint8
+    [N, K/block] of one linear (as mx4_quant writes them), or [E, N, ..] of a
+    layer's experts; tensor_scale fp32 [1] or [E] (MX4_E4M3 only)."""
+    block = mx4_block(fmt)
+    sets = codes.shape[0] if codes.dim() == 3 else 0
+    N, K = codes.shape[-2], codes.shape[-1] * 2
+    lead = (sets,) if sets else ()
+    nbytes = int(load().egopq_mx4_packed_bytes(max(sets, 1), N, K, fmt))
+    if codes.dim() not in (2, 3) or nbytes == 0:
+        raise EgopqError(-2, f"codes of shape {tuple(codes.shape)} are not packable")
+    if fmt == MX4_E8M0 and tensor_scale is not None:
+        raise EgopqError(-1, "E8M0 blocks have no tensor scale")
+    if tensor_scale is not None:
+        _mx4_scale(tensor_scale, max(sets, 1))
+    c = _arg(codes, torch.uint8, *lead, N, K // 2)
+    s = _arg(scales, torch.uint8, *lead, N, K // block)
+    packed = _output((nbytes,), torch.uint8, codes.device, stream)
+    _check(load().egopq_mx4_pack(c, s, max(sets, 1), N, K, fmt, packed.data_ptr(),
+                                 _stream(stream)))
+    return Mx4Weight(packed, sets, N, K, fmt, tensor_scale)
+
+
+def mx4_unpack(weight: Mx4Weight, stream=None) -> tuple:
+    """(codes, scales) of a packed weight, as mx4_pack took them."""
+    packed, sets, N, K, fmt, _ = weight
+    lead, dev = ((sets,) if sets else ()), packed.device
+    codes = _output((*lead, N, K // 2), torch.uint8, dev, stream)
+    scales = _output((*lead, N, K // mx4_block(fmt)), torch.uint8, dev, stream)
+    _check(load().egopq_mx4_unpack(_ptr(packed), max(sets, 1), N, K, fmt, _ptr(codes),
+                                   _ptr(scales), _stream(stream)))
+    return codes, scales
+
+
+def mx4_gemm(rows: Mx4Rows, weight: Mx4Weight, dtype: torch.dtype = torch.bfloat16,
+             out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Rows in 4 bits times a packed 4-bit weight: y [M, N]."""
+    packed, sets, N, K, fmt, w_scale = weight
+    if sets:
+        raise ValueError("weights of several sets: mx4_linear_ragged")
+    if (rows.K, rows.fmt) != (K, fmt):
+        raise ValueError(f"rows of K={rows.K} format {rows.fmt}, a weight of K={K} format {fmt}")
+    if rows.a_tc is None:
+        raise ValueError("rows without the products' form (with_tc=False)")
+    _mx4_rows_check(rows)
+    if out is None:
+        out = _output((rows.M, N), dtype, packed.device, stream)
+    _check(load().egopq_mx4_gemm(_ptr(rows.a_tc), _ptr(packed), _mx4_scale(rows.tensor_scale, 1),
+                                 _mx4_scale(w_scale, 1), rows.M, N, K, fmt, _mx4_type(out.dtype),
+                                 _arg(out, out.dtype, rows.M, N), _stream(stream)))
+    return out
+
+
+def mx4_workspace(rows: int, weight: Mx4Weight, device, stream=None) -> torch.Tensor:
+    """A workspace for mx4_linear or (a weight of several sets) mx4_linear_ragged
+    of `rows` rows and of any fewer, of the stream it is to be used on."""
+    n = int(load().egopq_mx4_linear_workspace_bytes(rows, weight.sets, weight.K, weight.fmt))
+    return _scratch(n, torch.uint8, device, stream)
+
+
+def _mx4_width(x: torch.Tensor, K: int, gated: bool):
+    if x.dim() != 2 or x.shape[1] != (2 * K if gated else K):
+        raise ValueError(f"x of shape {tuple(x.shape)} for {'gated ' if gated else ''}K = {K}")
+
+
+def mx4_linear(x: torch.Tensor, weight: Mx4Weight, tensor_scale: Optional[torch.Tensor] = None,
+               gated: bool = False, dtype: Optional[torch.dtype] = None,
+               out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """mx4_quant of x [M, K] (gated: [M, 2K], gate and up halves) and the product
+    with a packed 4-bit weight, in one call: y [M, N], of x's type unless dtype or
+    out says otherwise. tensor_scale: the rows' (MX4_E4M3)."""
+    packed, sets, N, K, fmt, w_scale = weight
+    if sets:
+        raise ValueError("weights of several sets: mx4_linear_ragged")
+    _mx4_width(x, K, gated)
+    M = x.shape[0]
+    if out is None:
+        out = _output((M, N), dtype or x.dtype, x.device, stream)
+    if workspace is None:
+        workspace = mx4_workspace(M, weight, x.device, stream)
+    _check(load().egopq_mx4_linear(
+        _ptr(x), _mx4_type(x.dtype), M, N, K, gated, _mx4_scale(tensor_scale, 1), _ptr(packed),
+        _mx4_scale(w_scale, 1), fmt, _mx4_type(out.dtype), _arg(out, out.dtype, M, N),
+        _ptr(workspace), workspace.nbytes, _stream(stream)))
+    return out
+
+
+def mx4_linear_ragged(x: torch.Tensor, offsets: torch.Tensor, weight: Mx4Weight,
+                      index: Optional[torch.Tensor] = None,
+                      tensor_scale: Optional[torch.Tensor] = None, gated: bool = False,
+                      dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """mx4_linear of rows sorted by the weight they take: rows
+    [offsets[e], offsets[e + 1]) (int32 [E + 1], on the device) times weight e of a
+    weight of E sets. Row r is x's row r, or index[r] (int32 [rows]) of an x of any
+    number of rows. y's other rows stay as they are: those of a y that the call
+    makes are not written."""
+    packed, sets, N, K, fmt, w_scale = weight
+    if not sets:
+        raise ValueError("a weight of several sets is needed (codes [E, N, K/2])")
+    _mx4_width(x, K, gated)
+    rows = x.shape[0] if index is None else index.shape[0]
+    if out is None:
+        out = _output((rows, N), dtype or x.dtype, x.device, stream)
+    if workspace is None:
+        workspace = mx4_workspace(rows, weight, x.device, stream)
+    _check(load().egopq_mx4_linear_ragged(
+        _ptr(x), _mx4_type(x.dtype), x.shape[0],
+        None if index is None else _arg(index, torch.int32, rows),
+        _arg(offsets, torch.int32, sets + 1), rows, sets, N, K, gated,
+        _mx4_scale(tensor_scale, 1), _ptr(packed), _mx4_scale(w_scale, sets), fmt,
+        _mx4_type(out.dtype), _arg(out, out.dtype, rows, N), _ptr(workspace), workspace.nbytes,
+        _stream(stream)))
     return out
 
 
