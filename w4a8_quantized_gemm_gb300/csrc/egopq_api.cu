@@ -614,7 +614,7 @@ int egopq_device_status(egopq_stream_t stream) {
   unsigned int word = 0;
   cudaError_t (*const take[])(unsigned*) = {take_error_word_quant_pack, take_error_word_gemv,
                                             take_error_word_tc_gemm, take_error_word_tc_experts,
-                                            take_error_word_mx4_gemm};
+                                            take_error_word_mx4_gemm, take_error_word_mx4_pair};
   for (auto fn : take) {
     unsigned int w = 0;
     e = fn(&w);

@@ -353,6 +353,7 @@ cudaError_t take_error_word_gemv(unsigned* out);
 cudaError_t take_error_word_tc_gemm(unsigned* out);
 cudaError_t take_error_word_tc_experts(unsigned* out);
 cudaError_t take_error_word_mx4_gemm(unsigned* out);
+cudaError_t take_error_word_mx4_pair(unsigned* out);
 // Debug builds: the packed-record read limit of each unit that reads records
 // (cudaErrorNotSupported in release builds).
 cudaError_t set_record_limit_gemv(unsigned long long bytes);

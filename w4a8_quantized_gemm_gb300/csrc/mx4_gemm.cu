@@ -10,84 +10,36 @@
 // rounds once. Weights are the instruction's 128 rows and a tile of one set's rows
 // its columns, as many as there are (a multiple of 16): few rows, or a ragged
 // set's last ones, cost what they are.
-#include "mx4_internal.h"
+#include "mx4_tc.cuh"
 
 namespace egopq {
 
 namespace {
 
-constexpr int kBT = 128;      // rows of a tile at most
+constexpr int kBT = 64;       // rows of a tile at most
 constexpr int kEpiWarps = 4;  // one for each 32 lanes of Tensor Memory
 constexpr int kThreads = (kEpiWarps + 2) * 32;
+constexpr int kMaxSplit = 8;  // CTAs that share a unit's K, a cluster
 
+// Two CTAs share an SM, so that one's loads cover the other's ends.
 template <int FMT>
 struct Cfg {
   static constexpr int kRec = mx4_record_bytes(FMT);
   static constexpr int kScale = kRec - kMx4Codes;
   static constexpr int kAtoms = kScale / 512;  // of a K block and 128 rows
-  static constexpr int kStage = 2 * kRec;      // a weight record and a row record
-  static constexpr int kStages = 6;
+  static constexpr int kRowsAt = kRec;         // a stage: a weight record, rows' codes, scales
+  static constexpr int kRowScaleAt = kRec + kBT * 128;
+  static constexpr int kStage = kRowScaleAt + kScale;
+  static constexpr int kStages = FMT == EGOPQ_MX4_E8M0 ? 4 : 3;
   static constexpr int kMiscAt = kStages * kStage;
   static constexpr int kMisc = 256;
   // Tensor Memory: two accumulators, then each stage's scales
   static constexpr int kScaleCols = 8 * kAtoms;
-  static_assert(2 * kBT + kStages * kScaleCols <= 512, "Tensor Memory");
-  static_assert(kRec % 1024 == 0, "swizzle atoms");
+  static constexpr int kCols = 256;
+  static_assert(2 * kBT + kStages * kScaleCols <= kCols, "Tensor Memory");
+  static_assert(kRec % 1024 == 0 && kStage % 1024 == 0, "swizzle atoms");
+  static_assert(kStages * kStage >= kBT * 512, "partial sums");
 };
-
-struct GemmParams {
-  const uint8_t* operand;
-  const uint8_t* packed;
-  const float* a_scale;
-  const float* w_scale;
-  const int32_t* offsets;
-  void* y;
-  int64_t M, N, K;
-  int sets, nb, kb, type;
-  uint64_t timeout_ns;
-};
-
-__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint32_t saddr) {
-  // 32 lanes x 16 bytes, to all four lane quarters: rows of 16 bytes, eight rows
-  // of 128 bytes a core matrix (stride 128), no swizzle
-  const uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) |
-                     static_cast<uint64_t>(128 >> 4) << 32 | static_cast<uint64_t>(1) << 46;
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
-}
-template <int FMT>
-__device__ __forceinline__ void tc_mma_mx4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                           uint32_t sa, uint32_t sb, uint32_t accumulate) {
-  if constexpr (FMT == EGOPQ_MX4_E8M0)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
-        "[%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], "
-        "[%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
-        : "memory");
-}
-// e2m1 x e2m1, fp32 sums, K = 64, both K-major; id: which two of a word's four
-// scales (0 or 2; with 4X all four).
-template <int FMT>
-__device__ __forceinline__ uint32_t idesc_mx4(int rows, int cols, int id) {
-  return ((uint32_t)id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(cols >> 3) << 17) |
-         ((FMT == EGOPQ_MX4_E8M0 ? 1u : 0u) << 23) | ((uint32_t)(rows >> 4) << 24) |
-         ((uint32_t)id << 29);
-}
-
-__device__ __forceinline__ void store_y(void* y, int64_t at, int type, float v) {
-  if (type == kMx4F32) static_cast<float*>(y)[at] = v;
-  else
-    static_cast<uint16_t*>(y)[at] = type == kMx4Bf16
-                                        ? f32_to_bf16_bits(v)
-                                        : __half_as_ushort(__float2half_rn(v));
-}
 
 // A unit of work: a block of weight rows times a tile of one set's rows.
 struct Unit {
@@ -95,12 +47,13 @@ struct Unit {
   const uint8_t* rows;  // its first row record
   int64_t row0;         // first row of y
   int count;            // rows
+  int half;             // first row in its records
   int n0;               // first column of y
   int set;
 };
 
 template <int FMT>
-__global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const GemmParams p) {
+__global__ void __launch_bounds__(kThreads, 2) mx4_few_kernel(const Mx4Params p) {
   using C = Cfg<FMT>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
@@ -115,7 +68,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const GemmParams 
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 4);
   int* first = reinterpret_cast<int*>(smem + C::kMiscAt + C::kMisc);
-  int* block = first + p.sets + 1;  // (a tile is a block of 128 rows)
+  int* block = first + p.sets + 1;
+  int* tile = block + p.sets + 1;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -131,16 +85,17 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const GemmParams 
     fence_mbar_init();
   }
   if (warp == kEpiWarps + 1) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_alloc(smem_u32(tmem_slot), C::kCols);
     tmem_relinquish();
   }
   if (warp == 0) {
     // (the offsets were there before this kernel could begin: the quantization in
     // front of a ragged product waits for them itself, every block of it)
-    if (p.offsets) mx4_scan_sets(p.offsets, p.sets, p.M, first, block);
+    if (p.offsets) mx4_scan_sets(p.offsets, p.sets, p.M, kBT, first, block, tile);
     else if (lane < 2) {
       first[lane] = lane ? (int)p.M : 0;
-      block[lane] = lane ? (int)((p.M + kBT - 1) / kBT) : 0;
+      block[lane] = 0;
+      tile[lane] = lane ? (int)((p.M + kBT - 1) / kBT) : 0;
     }
   }
   tc_fence_before();
@@ -148,24 +103,28 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const GemmParams 
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint64_t tmo = p.timeout_ns;
-  const int total = block[p.sets] * p.nb;
-  const int n_units = (int)blockIdx.x < total
-                          ? (total - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x
-                          : 0;
-  // Neighbouring blocks take one weight block and a set's tiles one after the
+  // A cluster of `split` CTAs takes a unit, each an equal run of its K blocks.
+  const int split = p.split, rank = split > 1 ? (int)cluster_ctarank() : 0;
+  const int team = (int)blockIdx.x / split, teams = (int)gridDim.x / split;
+  const int total = tile[p.sets] * p.nb;
+  const int n_units = team < total ? (total - team + teams - 1) / teams : 0;
+  const int kb0 = p.kb * rank / split, kb_n = p.kb * (rank + 1) / split - kb0;
+  // Neighbouring CTAs take one weight block and a set's tiles one after the
   // other, so that a weight is read from memory once.
   auto unit_at = [&](int i) {
-    const int u = (int)blockIdx.x + i * (int)gridDim.x;
-    const int e = mx4_find_set(block, p.sets, u / p.nb);
-    const int tiles = block[e + 1] - block[e];
-    const int local = u - block[e] * p.nb;
+    const int u = team + i * teams;
+    const int e = mx4_find_set(tile, p.sets, u / p.nb);
+    const int tiles = tile[e + 1] - tile[e];
+    const int local = u - tile[e] * p.nb;
     const int n = local / tiles, t = local - n * tiles;
     Unit r;
     r.set = e;
-    r.w = p.packed + ((int64_t)e * p.nb + n) * p.kb * C::kRec;
-    r.rows = p.operand + (int64_t)(block[e] + t) * p.kb * C::kRec;
+    r.w = p.packed + (((int64_t)e * p.nb + n) * p.kb + kb0) * C::kRec;
     r.row0 = (int64_t)first[e] + (int64_t)t * kBT;
     r.count = min(kBT, first[e + 1] - (int)r.row0);
+    // (a tile begins at row 0 or 64 of a record: its scales two columns in)
+    r.rows = p.operand + ((int64_t)(block[e] + t * kBT / 128) * p.kb + kb0) * C::kRec;
+    r.half = t * kBT % 128;
     r.n0 = n * 128;
     return r;
   };
@@ -173,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const GemmParams 
   if (warp == kEpiWarps) {
     // ---------------------------------------------------------------- producer
     if (lane == 0) {
-      const int n_items = n_units * p.kb;
+      const int n_items = n_units * kb_n;
       int issued = 0;
       Unit un{};
       // the first weights are on their way before this kernel's own wait: nothing
@@ -188,27 +147,32 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const GemmParams 
       };
       auto load_rows = [&](const Unit& x, int kb, int s) {
         const uint8_t* rec = x.rows + (int64_t)kb * C::kRec;
-        const uint32_t to = base + s * C::kStage + C::kRec;
-        bulk_load(to, rec, (uint32_t)((x.count + 7) & ~7) * 128, full(s));
-        bulk_load(to + kMx4Codes, rec + kMx4Codes, C::kScale, full(s));
+        const uint32_t to = base + s * C::kStage;
+        bulk_load(to + C::kRowsAt, rec + x.half * 128, (uint32_t)((x.count + 7) & ~7) * 128,
+                  full(s));
+        bulk_load(to + C::kRowScaleAt, rec + kMx4Codes, C::kScale, full(s));
       };
       for (int i = 0; i < ahead; ++i) {
-        if (i % p.kb == 0) un = unit_at(i / p.kb);
-        load_w(un, i % p.kb, i);
+        if (i % kb_n == 0) un = unit_at(i / kb_n);
+        load_w(un, i % kb_n, i);
       }
       griddep_wait();
       griddep_launch_dependents();
       for (int i = 0; i < ahead; ++i) {
-        if (i % p.kb == 0) un = unit_at(i / p.kb);
-        load_rows(un, i % p.kb, i);
+        if (i % kb_n == 0) un = unit_at(i / kb_n);
+        load_rows(un, i % kb_n, i);
         ++issued;
       }
+      int unit = (ahead - 1) / kb_n, kb = (ahead - 1) % kb_n;
       for (int i = ahead; i < n_items; ++i) {
         const int s = i % C::kStages;
         if (!mbar_wait(empty(s), ((i / C::kStages) & 1) ^ 1, abort_flag, tmo)) break;
-        if (i % p.kb == 0) un = unit_at(i / p.kb);
-        load_w(un, i % p.kb, s);
-        load_rows(un, i % p.kb, s);
+        if (++kb == kb_n) {
+          kb = 0;
+          un = unit_at(++unit);
+        }
+        load_w(un, kb, s);
+        load_rows(un, kb, s);
         ++issued;
       }
       for (int i = (issued > C::kStages ? issued - C::kStages : 0); i < issued; ++i) {
@@ -222,31 +186,27 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const GemmParams 
       bool ok = true;
       int i = 0;
       for (int k = 0; k < n_units && ok; ++k) {
-        const int cols = (unit_at(k).count + 15) & ~15;
+        const Unit un = unit_at(k);
+        const int cols = (un.count + 15) & ~15;
         const int b = k & 1;
         if (k >= 2) ok = mbar_wait(free_acc(b), ((k >> 1) & 1) ^ 1, abort_flag, tmo);
         const uint32_t d = tmem + b * kBT;
-        for (int kb = 0; kb < p.kb && ok; ++kb, ++i) {
+        for (int kb = 0; kb < kb_n && ok; ++kb, ++i) {
           const int s = i % C::kStages;
           ok = mbar_wait(full(s), (i / C::kStages) & 1, abort_flag, tmo);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t a_at = base + s * C::kStage, b_at = a_at + C::kRec;
+          const uint32_t a_at = base + s * C::kStage, b_at = a_at + C::kRowsAt;
           // a stage's scales have columns of their own: they are free once the
           // stage is
           const uint32_t sa = tmem + 2 * kBT + s * C::kScaleCols, sb = sa + 4 * C::kAtoms;
 #pragma unroll
           for (int j = 0; j < C::kAtoms; ++j) {
-            tc_cp_scales(sa + 4 * j, a_at + kMx4Codes + j * 512);
-            tc_cp_scales(sb + 4 * j, b_at + kMx4Codes + j * 512);
+            tc_cp_scales<1>(sa + 4 * j, a_at + kMx4Codes + j * 512);
+            tc_cp_scales<1>(sb + 4 * j, a_at + C::kRowScaleAt + j * 512);
           }
-          const int steps = (int)min((int64_t)4, (p.K - (int64_t)kb * 256 + 63) / 64);
-          for (int j = 0; j < steps; ++j) {
-            const int at = C::kAtoms == 4 ? j : j >> 1, id = C::kAtoms == 4 ? 0 : (j & 1) * 2;
-            tc_mma_mx4<FMT>(d, sdesc_kmajor_sw128(a_at + 32 * j), sdesc_kmajor_sw128(b_at + 32 * j),
-                            idesc_mx4<FMT>(128, cols, id), sa + 4 * at, sb + 4 * at,
-                            (kb | j) != 0);
-          }
+          tc_block_mx4<FMT, 1>(d, a_at, b_at, sa, 4, sb + un.half / 32, 4, 128, cols,
+                               mx4_steps(p.K, kb0 + kb), kb == 0);
           tc_commit(empty(s));
         }
         if (ok) tc_commit(done(b));
@@ -273,10 +233,18 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const GemmParams 
       const uint32_t d = tmem + b * kBT + ((uint32_t)(warp * 32) << 16);
       const int64_t n = un.n0 + warp * 32 + lane;
       const bool in = n < p.N;
+      // (of a split unit: the sums as they are, [column][128], over the stages,
+      // which all instructions have read)
+      float* part = reinterpret_cast<float*>(smem) + warp * 32 + lane;
       for (int c = 0; c < un.count; c += 16) {
         uint32_t v[16];
         tmem_ld16(d + c, v);
         tmem_wait_ld();
+        if (split > 1) {
+#pragma unroll
+          for (int q = 0; q < 16; ++q) part[(c + q) * 128] = __uint_as_float(v[q]);
+          continue;
+        }
 #pragma unroll
         for (int q = 0; q < 16; ++q)
           if (in && c + q < un.count)
@@ -288,18 +256,39 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_gemm_kernel(const GemmParams 
     }
   }
   __syncwarp();
+  if (split > 1) {
+    // One unit a cluster. CTA r adds up columns r, r + split, ..: the parts in
+    // their order, whoever came first.
+    cluster_sync_all();
+    if (warp < kEpiWarps && n_units > 0) {
+      const Unit un = unit_at(0);
+      float g = p.a_scale ? __ldg(p.a_scale) : 1.f;
+      if (p.w_scale) g *= __ldg(p.w_scale + un.set);
+      const int64_t n = un.n0 + warp * 32 + lane;
+      if (n < p.N)
+        for (int c = rank; c < un.count; c += split) {
+          const uint32_t at = base + (uint32_t)(c * 128 + warp * 32 + lane) * 4;
+          float sum = 0.f;
+#pragma unroll
+          for (int r = 0; r < kMaxSplit; ++r)
+            if (r < split) sum += ld_dsmem_f32(map_to_rank(at, r));
+          store_y(p.y, (un.row0 + c) * p.N + n, p.type, sum * g);
+        }
+    }
+    cluster_sync_all();  // (no CTA leaves while another reads its parts)
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == kEpiWarps + 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, C::kCols);
   }
 }
 
 template <int FMT>
-cudaError_t launch_fmt(const Mx4GemmArgs& a, cudaStream_t st) {
+cudaError_t launch_few(const Mx4GemmArgs& a, cudaStream_t st) {
   using C = Cfg<FMT>;
-  GemmParams p;
+  Mx4Params p;
   p.operand = a.operand;
   p.packed = a.packed;
   p.a_scale = a.a_scale;
@@ -314,25 +303,40 @@ cudaError_t launch_fmt(const Mx4GemmArgs& a, cudaStream_t st) {
   p.kb = (int)mx4_kblocks(a.K);
   p.type = a.type;
   p.timeout_ns = a.timeout_ns;
-  const int64_t tiles =
-      a.offsets ? mx4_row_blocks(a.M, a.sets) : (a.M + kBT - 1) / kBT;
+  const int64_t tiles = a.offsets ? mx4_tiles(a.M, a.sets, kBT) : (a.M + kBT - 1) / kBT;
   const int64_t most = tiles * p.nb;
   const int sms = device_sm_count();
   if (sms < 1) return cudaErrorInvalidConfiguration;
   if (most >= (1LL << 31) || (most / sms + 1) * p.kb >= (1LL << 31)) return cudaErrorNotSupported;
-  const size_t smem = C::kMiscAt + C::kMisc + 2 * (size_t)(a.sets + 1) * sizeof(int);
-  auto kern = mx4_gemm_kernel<FMT>;
+  // Fewer units than the SMs hold CTAs: K is split.
+  const int64_t slots = 2 * sms;
+  p.split = (int)(slots / most);
+  if (p.split > kMaxSplit) p.split = kMaxSplit;
+  if (p.split > p.kb) p.split = p.kb;
+  if (p.split < 1) p.split = 1;
+  const size_t smem = C::kMiscAt + C::kMisc + 3 * (size_t)(a.sets + 1) * sizeof(int);
+  auto kern = mx4_few_kernel<FMT>;
   static SmemOptIn opt_in;
   if (cudaError_t e = opt_in.ensure(kern, smem); e != cudaSuccess) return e;
-  PdlConfig c(dim3((unsigned)(most < sms ? most : sms), 1, 1), kThreads, smem, st);
+  PdlConfig c(dim3((unsigned)(p.split > 1 ? most * p.split : most < slots ? most : slots), 1, 1),
+              kThreads, smem, st);
+  cudaLaunchAttribute attr[2] = {c.attr[0], {}};
+  if (p.split > 1) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    c.cfg.attrs = attr;
+    c.cfg.numAttrs = 2;
+  }
   return cudaLaunchKernelEx(&c.cfg, kern, p);
 }
 
 }  // namespace
 
 cudaError_t launch_mx4_gemm(const Mx4GemmArgs& a, cudaStream_t st) {
-  return a.format == EGOPQ_MX4_E8M0 ? launch_fmt<EGOPQ_MX4_E8M0>(a, st)
-                                    : launch_fmt<EGOPQ_MX4_E4M3>(a, st);
+  if (a.M > 64 * (int64_t)a.sets) return launch_mx4_pair(a, st);
+  return a.format == EGOPQ_MX4_E8M0 ? launch_few<EGOPQ_MX4_E8M0>(a, st)
+                                    : launch_few<EGOPQ_MX4_E4M3>(a, st);
 }
 
 cudaError_t take_error_word_mx4_gemm(unsigned* out) { return take_local_error_word(out); }

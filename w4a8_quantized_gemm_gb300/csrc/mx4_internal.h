@@ -28,11 +28,13 @@ __host__ __device__ constexpr int mx4_record_bytes(int format) {
   return kMx4Codes + 128 * 256 / mx4_block(format);
 }
 __host__ __device__ constexpr int64_t mx4_kblocks(int64_t K) { return (K + 255) / 256; }
-// Blocks of 128 rows that `rows` rows of `sets` sets can take, each set's first
-// row at the start of one.
-inline int64_t mx4_row_blocks(int64_t rows, int64_t sets) {
-  return rows / 128 + (sets < rows ? sets : rows);
+// Tiles of bt rows of one set each that `rows` rows of `sets` sets can make.
+inline int64_t mx4_tiles(int64_t rows, int64_t sets, int bt) {
+  return rows / bt + (sets < rows ? sets : rows);
 }
+// Blocks of 128 rows that they can take in the records, each set's first row at
+// the start of one.
+inline int64_t mx4_row_blocks(int64_t rows, int64_t sets) { return mx4_tiles(rows, sets, 128); }
 
 struct Mx4QuantArgs {
   const void* x;
@@ -75,16 +77,19 @@ struct Mx4GemmArgs {
 };
 // cudaErrorNotSupported: more work than one launch's counters hold.
 cudaError_t launch_mx4_gemm(const Mx4GemmArgs& a, cudaStream_t st);
+cudaError_t launch_mx4_pair(const Mx4GemmArgs& a, cudaStream_t st);  // (of many rows)
 
 // ---- ragged rows ---------------------------------------------------------------
 // One warp: where each set's rows begin (clamped to [0, M] and to the sets
 // before, so that no value of offsets leads outside a buffer), and how many
-// 128-row blocks lie before it. Each array has sets + 1 entries. Offsets are read
-// past L1 (the caller may run before the kernel in front of it has ended).
-__device__ __forceinline__ void mx4_scan_sets(const int32_t* offsets, int sets, int64_t M,
-                                              int* first, int* block) {
+// 128-row blocks and tiles of bt rows lie before it (bt at most 128 and a divisor
+// of it, or a multiple). Each array has sets + 1 entries; tile may be null.
+// Offsets are read past L1 (the caller may run before the kernel in front of it
+// has ended).
+__device__ __forceinline__ void mx4_scan_sets(const int32_t* offsets, int sets, int64_t M, int bt,
+                                              int* first, int* block, int* tile) {
   const int lane = threadIdx.x & 31;
-  int low = 0, blocks = 0;  // of the sets before this pass
+  int low = 0, blocks = 0, tiles = 0;  // of the sets before this pass
   for (int e0 = 0; e0 <= sets; e0 += 32) {
     const int e = e0 + lane;
     int v = 0;
@@ -102,19 +107,24 @@ __device__ __forceinline__ void mx4_scan_sets(const int32_t* offsets, int sets, 
       if (e < sets) next = max(v, (int)min((int64_t)max(__ldcg(offsets + e + 1), 0), M));
     }
     const int rows = e < sets ? next - v : 0;
-    const int own = (rows + 127) >> 7;
-    int b = own;
+    const int own_b = (rows + 127) >> 7, own_t = (rows + bt - 1) / bt;
+    int b = own_b, t = own_t;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, b, o);
-      if (lane >= o) b += up;
+      const int ub = __shfl_up_sync(0xffffffffu, b, o), ut = __shfl_up_sync(0xffffffffu, t, o);
+      if (lane >= o) {
+        b += ub;
+        t += ut;
+      }
     }
     if (e <= sets) {
       first[e] = v;
-      block[e] = blocks + b - own;
+      block[e] = blocks + b - own_b;
+      if (tile) tile[e] = tiles + t - own_t;
     }
     low = __shfl_sync(0xffffffffu, v, 31);
     blocks += __shfl_sync(0xffffffffu, b, 31);
+    tiles += __shfl_sync(0xffffffffu, t, 31);
   }
 }
 // The set whose entries of the rising array `at` hold q: the last with at[e] <= q.

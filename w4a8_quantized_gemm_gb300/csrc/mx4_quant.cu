@@ -43,52 +43,77 @@ __device__ __forceinline__ float e8m0_value(uint32_t byte) {
   return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7fc00000u : byte << 23);
 }
 
-// Eight values of a row at p, as fp32.
+// Eight values of a row, as they lie in memory and as fp32.
 template <int TYPE>
-__device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) {
-  if constexpr (TYPE == kMx4F32) {
-    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-    const float4 a = __ldcs(q), b = __ldcs(q + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at));
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+struct Eight {
+  uint4 w[TYPE == kMx4F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* p, int64_t at) {
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) +
+                                                    at * (TYPE == kMx4F32 ? 4 : 2));
+    w[0] = __ldcs(q);
+    if constexpr (TYPE == kMx4F32) w[1] = __ldcs(q + 1);
+  }
+  __device__ __forceinline__ void zero() {
+    w[0] = make_uint4(0, 0, 0, 0);
+    if constexpr (TYPE == kMx4F32) w[1] = w[0];
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    const uint32_t a[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+    if constexpr (TYPE == kMx4F32) {
+      const uint32_t b[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (TYPE == kMx4Bf16) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
+      for (int i = 0; i < 4; ++i) {
+        v[i] = __uint_as_float(a[i]);
+        v[4 + i] = __uint_as_float(b[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (TYPE == kMx4Bf16) {
+          v[2 * i] = __uint_as_float(a[i] << 16);
+          v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+        } else {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a[i]));
+          v[2 * i] = f.x;
+          v[2 * i + 1] = f.y;
+        }
       }
     }
   }
-}
+};
 
 // ---- gated values -----------------------------------------------------------------
-// h = silu(g) * u * r in fp32: the exponential is within 2 of its last places, the
-// sum, the quotient and the products within half of one each, 2^-21 together. The
-// codes are those of the real h: where fp32 lies within 2^-20 of a border (and
-// where h is so small that fp32 has fewer bits), 64 bits decide.
-// `weak`: a value for which that does not hold, as fp32 has run out of exponents
-// on the way (zeros are exact).
-__device__ __forceinline__ float gated32(float g, float u, float r, bool& weak) {
-  const float h = __fdiv_rn(g, 1.f + expf(-g)) * u, v = h * r;
-  weak = weak || (g != 0.f && u != 0.f &&
-                  (g < -80.f || fabsf(h) < 0x1p-100f || fabsf(v) < 0x1p-100f));
-  return v;
+// h = silu(g) * u * r in fp32, for -32 <= g: the exponent's rounding (46 at most)
+// makes the fast exponential 2^-19 off and its own two last places 2^-22, the fast
+// quotient's are two, the sum's and the products' half of one each: below 2^-18
+// together. The codes are those of the real h: where fp32 lies within 2^-18 of a
+// border, 64 bits decide, for a value in 30000 or so (which costs its warp about 2000
+// cycles, at 1/64 of the rate).
+__device__ __forceinline__ float gated32(float g, float u) {
+  return __fdividef(g, 1.f + __expf(-g)) * u;
 }
-__device__ __forceinline__ double gated64(float g, float u, float r) {
+// Whether that does not hold, as g is below -32 or fp32 has run out of exponents on
+// the way to v = h * r (zeros are exact).
+__device__ __forceinline__ bool gated_weak(float g, float u, float v, float r) {
+  return g != 0.f && u != 0.f &&
+         (g < -32.f || fabsf(v) < 0x1p-100f || fabsf(v) < 0x1p-100f * r);
+}
+__device__ __noinline__ double gated64(float g, float u, float r) {
   return (double)g / (1.0 + exp(-(double)g)) * (double)u * (double)r;
 }
-// Whether the positive number v lies within 8 of its last places of a number
-// whose lowest mantissa bit is 2^-keep: every border between codes is one.
-__device__ __forceinline__ bool near_short(float v, int keep) {
-  const uint32_t low = (1u << (23 - keep)) - 1;
-  return ((__float_as_uint(v) + 8u) & low) < 16u;
+// How far above the number below it whose lowest mantissa bit is 2^-keep v lies, in
+// last places and counted from kNear places below that number: every border
+// between codes is such a number, and v is within kNear places of one where this is
+// below 2 kNear. (The sign does not matter.)
+constexpr uint32_t kNear = 32;
+__device__ __forceinline__ uint32_t above_short(float v, int keep) {
+  return (__float_as_uint(v) + kNear) & ((1u << (23 - keep)) - 1);
+}
+// max(|a|, |b|), NaN if one is
+__device__ __forceinline__ float max_abs(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
 }
 
 struct QuantParams {
@@ -100,125 +125,118 @@ struct QuantParams {
   uint8_t* scales;
   uint8_t* operand;
   int64_t M, K, x_rows;
-  int sets, kb;
+  int sets, kb, groups;  // K blocks of a row, and runs of U of them
 };
 
-// A warp takes 256 values of a row: eight a lane, so that a block of 32 (16) is
-// four (two) neighbours and a row's 128 bytes of codes leave as one line. Bound
-// by memory: 16 bytes a lane are on their way at a time, and the units of
-// many rows keep enough warps on an SM to cover them.
+// Where a lane's results of a row go: its codes and its block's scale in their plain
+// places and in the row's first record (null: not asked for).
+struct RowOut {
+  uint8_t *codes, *scales, *rec, *rec_scale;
+};
+
+// One run of 256 values of a row, all lanes of a warp.
 template <int FMT, int TYPE, bool GATED>
-__global__ void __launch_bounds__(kQuantWarps * 32) mx4_quant_kernel(const QuantParams p) {
-  extern __shared__ int quant_smem[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  griddep_wait();
-  if (threadIdx.x == 0) griddep_launch_dependents();
-  int *first = nullptr, *block = nullptr;
-  int64_t row0 = 0, rows = p.M;
-  if (p.offsets) {
-    first = quant_smem;
-    block = first + p.sets + 1;
-    if (warp == 0) mx4_scan_sets(p.offsets, p.sets, p.M, first, block);
-    __syncthreads();
-    row0 = first[0];
-    rows = first[p.sets] - row0;
-  }
-  const float r = p.tensor_scale ? __fdiv_rn(1.f, __ldg(p.tensor_scale)) : 1.f;
+__device__ __forceinline__ void quant_unit(const RowOut& out, const Eight<TYPE>& g8,
+                                           const Eight<TYPE>& u8, int kb, bool in, bool scaled,
+                                           float r) {
   constexpr int kLanes = mx4_block(FMT) / 8;  // of one block
-  const int64_t ld = GATED ? 2 * p.K : p.K;
-  const int64_t units = rows * p.kb;
-  for (int64_t w = (int64_t)blockIdx.x * kQuantWarps + warp; w < units;
-       w += (int64_t)gridDim.x * kQuantWarps) {
-    const int64_t row = row0 + w / p.kb;
-    const int kb = (int)(w % p.kb);
-    const int64_t k = (int64_t)kb * 256 + lane * 8;
-    const bool in = k < p.K;
-    int64_t src = row;
-    if (p.index) src = __ldg(p.index + row);
-    const bool have = in && src >= 0 && src < p.x_rows;
-    float v[8], g[8], u[8];
-    bool weak = false;
+  const int lane = threadIdx.x & 31;
+  float v[8], g[8], u[8];
+  bool weak = false;
+  g8.values(g);
+  if constexpr (GATED) {
+    u8.values(u);
+    float low = 1.f, gate = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = g[i] = u[i] = 0.f;
-    if (have) {
-      if constexpr (GATED) {
-        load8<TYPE>(p.x, src * ld + k, g);
-        load8<TYPE>(p.x, src * ld + p.K + k, u);
+    for (int i = 0; i < 8; ++i) {
+      const float h = gated32(g[i], u[i]);
+      v[i] = h * r;
+      low = fminf(low, fminf(fabsf(h), fabsf(v[i])));
+      gate = fminf(gate, g[i]);
+    }
+    if (low < 0x1p-100f || gate < -32.f) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = gated32(g[i], u[i], r, weak);
-      } else {
-        load8<TYPE>(p.x, src * ld + k, v);
-        if (p.tensor_scale) {
+      for (int i = 0; i < 8; ++i) weak = weak || gated_weak(g[i], u[i], v[i], r);
+    }
+  } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] *= r;
+    for (int i = 0; i < 8; ++i) v[i] = scaled ? g[i] * r : g[i];
+  }
+  // the block's largest magnitude (a NaN is)
+  float most = max_abs(v[0], v[1]);
+#pragma unroll
+  for (int i = 2; i < 8; ++i) most = max_abs(most, v[i]);
+#pragma unroll
+  for (int o = 1; o < kLanes; o <<= 1)
+    most = max_abs(most, __shfl_xor_sync(0xffffffffu, most, o));
+  const uint32_t top = __float_as_uint(most);
+  const bool bad = top >= 0x7f800000u;
+  uint32_t byte;
+  if constexpr (FMT == kE8M0)
+    byte = bad ? 255u : (uint32_t)max((int)(top >> 23) - 2, 0);
+  else
+    byte = bad ? 0x7fu : __nv_cvt_float_to_fp8(__fdiv_rn(most, 6.f), __NV_SATFINITE, __NV_E4M3);
+  if constexpr (GATED) {
+    // next to a border between scales (a block of zeros is exact)
+    const uint32_t over = FMT == kE8M0 ? above_short(most, 0) : above_short(__fdividef(most, 6.f), 4);
+    bool close = !bad && (weak || (top != 0 && over < 2 * kNear));
+    if (__any_sync(0xffffffffu, close)) {
+      // (a block's lanes go together; which of its values may be the largest is
+      // certain from fp32 unless one is weak)
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) {
+        const int other = __shfl_xor_sync(0xffffffffu, (close ? 1 : 0) | (weak ? 2 : 0), o);
+        close = close || (other & 1);
+        weak = weak || (other & 2);
+      }
+      double d = 0.0;
+      if (close) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (weak || fabsf(v[i]) >= most * (1.f - 0x1p-16f))
+            d = fmax(d, fabs(gated64(g[i], u[i], r)));
+      }
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) d = fmax(d, __shfl_xor_sync(0xffffffffu, d, o));
+      if (close) {
+        if constexpr (FMT == kE8M0) {
+          const int e = d > 0.0 ? ilogb(d) - 2 : -127;
+          byte = (uint32_t)max(e + 127, 0);
+        } else {
+          byte = __nv_cvt_double_to_fp8(d / 6.0, __NV_SATFINITE, __NV_E4M3);
         }
       }
     }
-    // the block's largest magnitude, as bits (NaN above infinity above all)
-    uint32_t top = 0;
+  }
+  float t[8];
+  float inv, s = 0.f;
+  if constexpr (FMT == kE8M0) {
+    // 2^(127 - byte), byte at most 252: exact, as is the product where it matters
+    inv = bad ? 0.f : __uint_as_float((254u - byte) << 23);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+    for (int i = 0; i < 8; ++i) t[i] = v[i] * inv;
+  } else {
+    s = e4m3_value(byte);
+    inv = s > 0.f ? __frcp_rn(s) : 0.f;
 #pragma unroll
-    for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const bool bad = top >= 0x7f800000u;
-    // FMT's scale of a largest value, as its byte
-    uint32_t byte;
-    if constexpr (FMT == kE8M0) {
-      byte = bad ? 255u : (uint32_t)max((int)(top >> 23) - 2, 0);
-    } else {
-      const float q = __fdiv_rn(__uint_as_float(top), 6.f);
-      byte = bad ? 0x7fu : __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
+    for (int i = 0; i < 8; ++i) {
+      t[i] = v[i] * inv;
+      // Borders m are numbers of three bits and s one of four, so m s has seven: v
+      // is on it, or v / s at least .53 of m's last places away. t is off by two of
+      // its last places; with the remainder, which is exact, it is off by 2^-22 of
+      // one before it is rounded: on the border or on the right side of it.
+      if constexpr (!GATED) t[i] = fmaf(fmaf(-t[i], s, v[i]), inv, t[i]);
     }
-    if constexpr (GATED) {
-      const float a = __uint_as_float(top);
-      bool close = !bad && (weak || (FMT == kE8M0 ? near_short(a, 0)
-                                                  : near_short(__fdiv_rn(a, 6.f), 4)));
-      if (__any_sync(0xffffffffu, close)) {
-        // every lane of a block comes along where one does: the shuffles are the
-        // warp's, and what they bring to the other blocks is not used
-        double d = 0.0;
-        if (!bad && have) {
-#pragma unroll 1
-          for (int i = 0; i < 8; ++i) d = fmax(d, fabs(gated64(g[i], u[i], r)));
-        }
+  }
+  uint32_t code = e2m1x8(t);
+  if constexpr (GATED) {
+    uint32_t over = kNear * 2;
 #pragma unroll
-        for (int o = 1; o < kLanes; o <<= 1) {
-          d = fmax(d, __shfl_xor_sync(0xffffffffu, d, o));
-          // (one mask for both: no lane leaves a shuffle out)
-          const int other = __shfl_xor_sync(0xffffffffu, (close ? 1 : 0) | (weak ? 2 : 0), o);
-          close = close || (other & 1);
-          weak = weak || (other & 2);
-        }
-        if (close) {
-          if constexpr (FMT == kE8M0) {
-            const int e = d > 0.0 ? ilogb(d) - 2 : -127;
-            byte = (uint32_t)max(e + 127, 0);
-          } else {
-            byte = __nv_cvt_double_to_fp8(d / 6.0, __NV_SATFINITE, __NV_E4M3);
-          }
-        }
-      }
-    }
-    float t[8];
-    float inv = 0.f, s = 0.f;
-    if constexpr (FMT == kE8M0) {
-      // 2^(127 - byte), byte at most 252: exact, as is the product where it matters
-      inv = bad ? 0.f : __uint_as_float((254u - byte) << 23);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = v[i] * inv;
-    } else {
-      // fp32's quotient is on the same side of a border (numbers of at most six
-      // bits, times s) as the real one
-      s = e4m3_value(byte);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = s > 0.f ? __fdiv_rn(v[i], s) : 0.f;
-    }
-    uint32_t code = e2m1x8(t);
-    if constexpr (GATED) {
+    for (int i = 0; i < 8; ++i) over = min(over, above_short(t[i], 2));
+    if ((over < 2 * kNear || weak) && !bad) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float a = fabsf(t[i]);
-        if (!bad && (weak || (a > 0.125f && near_short(a, 2)))) {
+        if (weak || (fabsf(t[i]) > 0.125f && above_short(t[i], 2) < 2 * kNear)) {
           double d = gated64(g[i], u[i], r);
           if constexpr (FMT == kE8M0) d = d * (double)inv;
           else d = s > 0.f ? d / (double)s : 0.0;
@@ -226,11 +244,69 @@ __global__ void __launch_bounds__(kQuantWarps * 32) mx4_quant_kernel(const Quant
         }
       }
     }
-    if (bad) code = 0;
-    if (p.codes && in) {
-      *reinterpret_cast<uint32_t*>(p.codes + row * (p.K / 2) + k / 2) = code;
-      if (lane % kLanes == 0)
-        p.scales[row * (p.K / mx4_block(FMT)) + k / mx4_block(FMT)] = (uint8_t)byte;
+  }
+  if (bad) code = 0;
+  if (out.codes && in) {
+    *reinterpret_cast<uint32_t*>(out.codes + kb * 128) = code;
+    if (lane % kLanes == 0) out.scales[kb * (256 / mx4_block(FMT))] = (uint8_t)byte;
+  }
+  if (out.rec) {
+    const int64_t to = (int64_t)kb * mx4_record_bytes(FMT);
+    *reinterpret_cast<uint32_t*>(out.rec + to) = code;
+    if (lane % kLanes == 0) out.rec_scale[to] = (uint8_t)byte;
+  }
+}
+
+// A warp takes U runs of 256 values of a row: eight values a lane, so that a block
+// of 32 (16) is four (two) neighbours and a row's 128 bytes of codes leave as one
+// line. Bound by memory: all of a warp's loads are on their way before the first
+// is used; few rows take U = 1, so that more warps share them.
+template <int FMT, int TYPE, bool GATED, int U>
+__global__ void __launch_bounds__(kQuantWarps * 32) mx4_quant_kernel(const QuantParams p) {
+  extern __shared__ int quant_smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  int *first = nullptr, *block = nullptr;
+  int64_t row = 0, rows_end = p.M;
+  if (p.offsets) {
+    first = quant_smem;
+    block = first + p.sets + 1;
+    if (warp == 0) mx4_scan_sets(p.offsets, p.sets, p.M, 128, first, block, nullptr);
+    __syncthreads();
+    row = first[0];
+    rows_end = first[p.sets];
+  }
+  const bool scaled = p.tensor_scale != nullptr;
+  const float r = scaled ? __fdiv_rn(1.f, __ldg(p.tensor_scale)) : 1.f;
+  const int64_t ld = GATED ? 2 * p.K : p.K;
+  constexpr int kLanes = mx4_block(FMT) / 8;
+  // this warp's runs: every `stride`-th, counted along the rows
+  const int64_t at0 = (int64_t)blockIdx.x * kQuantWarps + warp;
+  const int64_t stride = (int64_t)gridDim.x * kQuantWarps;
+  const int64_t row_step = stride / p.groups;
+  const int group_step = (int)(stride - row_step * p.groups);
+  row += at0 / p.groups;
+  int group = (int)(at0 % p.groups);
+  while (row < rows_end) {
+    int64_t src = row;
+    if (p.index) src = __ldg(p.index + row);
+    const bool have = src >= 0 && src < p.x_rows;
+    Eight<TYPE> g8[U], u8[GATED ? U : 1];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int64_t k = (int64_t)(group * U + i) * 256 + lane * 8;
+      g8[i].zero();
+      if constexpr (GATED) u8[i].zero();
+      if (have && k < p.K) {
+        g8[i].load(p.x, src * ld + k);
+        if constexpr (GATED) u8[i].load(p.x, src * ld + p.K + k);
+      }
+    }
+    RowOut out{};
+    if (p.codes) {
+      out.codes = p.codes + row * (p.K / 2) + lane * 4;
+      out.scales = p.scales + row * (p.K / mx4_block(FMT)) + lane / kLanes;
     }
     if (p.operand) {
       int64_t at = row;  // among the operand's rows
@@ -238,20 +314,29 @@ __global__ void __launch_bounds__(kQuantWarps * 32) mx4_quant_kernel(const Quant
         const int e = mx4_find_set(first, p.sets, (int)row);
         at = (int64_t)block[e] * 128 + (row - first[e]);
       }
-      uint8_t* rec = p.operand + ((at >> 7) * p.kb + kb) * mx4_record_bytes(FMT);
-      const int q = (int)(at & 127);
-      *reinterpret_cast<uint32_t*>(rec + q * 128 + ((((lane >> 2) ^ q) & 7) << 4) + (lane & 3) * 4) =
-          code;
-      if (lane % kLanes == 0) {
-        const int b = lane / kLanes;
-        rec[kMx4Codes + (b >> 2) * 512 + (q & 31) * 16 + (q >> 5) * 4 + (b & 3)] = (uint8_t)byte;
-      }
+      uint8_t* rec = p.operand + (at >> 7) * p.kb * mx4_record_bytes(FMT);
+      const int q = (int)(at & 127), b = lane / kLanes;
+      out.rec = rec + q * 128 + ((((lane >> 2) ^ q) & 7) << 4) + (lane & 3) * 4;
+      out.rec_scale = rec + kMx4Codes + (b >> 2) * 512 + (q & 31) * 16 + (q >> 5) * 4 + (b & 3);
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int kb = group * U + i;
+      if (U == 1 || kb < p.kb)
+        quant_unit<FMT, TYPE, GATED>(out, g8[i], u8[GATED ? i : 0], kb,
+                                     (int64_t)kb * 256 + lane * 8 < p.K, scaled, r);
+    }
+    row += row_step;
+    group += group_step;
+    if (group >= p.groups) {
+      group -= p.groups;
+      ++row;
     }
   }
 }
 
-template <int FMT, int TYPE, bool GATED>
-cudaError_t launch_quant(const Mx4QuantArgs& a, cudaStream_t st) {
+template <int FMT, int TYPE, bool GATED, int U>
+cudaError_t launch_quant_u(const Mx4QuantArgs& a, int64_t warps, cudaStream_t st) {
   QuantParams p;
   p.x = a.x;
   p.tensor_scale = a.tensor_scale;
@@ -265,13 +350,22 @@ cudaError_t launch_quant(const Mx4QuantArgs& a, cudaStream_t st) {
   p.x_rows = a.x_rows;
   p.sets = a.sets;
   p.kb = (int)mx4_kblocks(a.K);
-  const int sms = device_sm_count();
-  if (sms < 1) return cudaErrorInvalidConfiguration;
-  const int64_t blocks = (a.M * p.kb + kQuantWarps - 1) / kQuantWarps;
-  const int64_t most = (int64_t)sms * 16;
+  p.groups = (p.kb + U - 1) / U;
+  const int64_t blocks = (a.M * p.groups + kQuantWarps - 1) / kQuantWarps;
+  const int64_t most = warps / kQuantWarps;
   const size_t smem = a.offsets ? 2 * (size_t)(a.sets + 1) * sizeof(int) : 0;
   PdlConfig c(dim3((unsigned)(blocks < most ? blocks : most), 1, 1), kQuantWarps * 32, smem, st);
-  return cudaLaunchKernelEx(&c.cfg, mx4_quant_kernel<FMT, TYPE, GATED>, p);
+  return cudaLaunchKernelEx(&c.cfg, mx4_quant_kernel<FMT, TYPE, GATED, U>, p);
+}
+
+template <int FMT, int TYPE, bool GATED>
+cudaError_t launch_quant(const Mx4QuantArgs& a, cudaStream_t st) {
+  constexpr int kMany = GATED || TYPE == kMx4F32 ? 2 : 4;
+  const int sms = device_sm_count();
+  if (sms < 1) return cudaErrorInvalidConfiguration;
+  const int64_t warps = (int64_t)sms * 48;
+  return a.M * mx4_kblocks(a.K) <= 2 * warps ? launch_quant_u<FMT, TYPE, GATED, 1>(a, warps, st)
+                                             : launch_quant_u<FMT, TYPE, GATED, kMany>(a, warps, st);
 }
 
 template <int FMT>
@@ -290,52 +384,75 @@ cudaError_t launch_quant_type(const Mx4QuantArgs& a, cudaStream_t st) {
 }
 
 // ---- values back ------------------------------------------------------------------
-// Eight values a thread; the code times its block's scale is exact in fp32.
+// Eight values a thread and step, four steps' codes on their way at a time; the
+// code times its block's scale is exact in fp32.
+template <int FMT, int TYPE>
+__device__ __forceinline__ void dequant8(uint32_t c, uint32_t byte, bool scaled, float g, void* y,
+                                         int64_t i) {
+  const float s = FMT == kE8M0 ? e8m0_value(byte) : e4m3_value(byte);
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t h;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t}"
+        : "=r"(h)
+        : "r"(c >> (8 * j)));
+    const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
+    v[2 * j] = f.x * s;
+    v[2 * j + 1] = f.y * s;
+  }
+  if (scaled) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= g;
+  }
+  if constexpr (TYPE == kMx4F32) {
+    float4* o = static_cast<float4*>(y) + 2 * i;
+    o[0] = make_float4(v[0], v[1], v[2], v[3]);
+    o[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (TYPE == kMx4Bf16) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&b);
+      } else {
+        const __half2 b = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+    }
+    static_cast<uint4*>(y)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+constexpr int kDequantSteps = 4;
+
 template <int FMT, int TYPE>
 __global__ void __launch_bounds__(256) mx4_dequant_kernel(const uint8_t* codes,
                                                           const uint8_t* scales, int64_t n,
                                                           const float* tensor_scale, void* y) {
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
-  const float g = tensor_scale ? __ldg(tensor_scale) : 1.f;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    const uint32_t c = reinterpret_cast<const uint32_t*>(codes)[i];
-    const uint32_t byte = scales[i / (mx4_block(FMT) / 8)];
-    const float s = FMT == kE8M0 ? e8m0_value(byte) : e4m3_value(byte);
-    float v[8];
+  const bool scaled = tensor_scale != nullptr;
+  const float g = scaled ? __ldg(tensor_scale) : 1.f;
+  constexpr int kPer = mx4_block(FMT) / 8;
+  for (int64_t i0 = (int64_t)blockIdx.x * 256 * kDequantSteps + threadIdx.x; i0 < n;
+       i0 += (int64_t)gridDim.x * 256 * kDequantSteps) {
+    uint32_t c[kDequantSteps], b[kDequantSteps];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t h;
-      asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\t"
-          "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t}"
-          : "=r"(h)
-          : "r"(c >> (8 * j)));
-      const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
-      v[2 * j] = f.x * s;
-      v[2 * j + 1] = f.y * s;
-    }
-    if (tensor_scale) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= g;
-    }
-    if constexpr (TYPE == kMx4F32) {
-      float4* o = static_cast<float4*>(y) + 2 * i;
-      o[0] = make_float4(v[0], v[1], v[2], v[3]);
-      o[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (TYPE == kMx4Bf16) {
-          const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-          w[j] = *reinterpret_cast<const uint32_t*>(&b);
-        } else {
-          const __half2 b = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
-          w[j] = *reinterpret_cast<const uint32_t*>(&b);
-        }
+    for (int q = 0; q < kDequantSteps; ++q) {
+      const int64_t i = i0 + q * 256;
+      c[q] = b[q] = 0;
+      if (i < n) {
+        c[q] = __ldcs(reinterpret_cast<const uint32_t*>(codes) + i);
+        b[q] = __ldg(scales + i / kPer);
       }
-      static_cast<uint4*>(y)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+#pragma unroll
+    for (int q = 0; q < kDequantSteps; ++q) {
+      const int64_t i = i0 + q * 256;
+      if (i < n) dequant8<FMT, TYPE>(c[q], b[q], scaled, g, y, i);
     }
   }
 }
@@ -345,7 +462,7 @@ cudaError_t launch_dequant_type(const uint8_t* codes, const uint8_t* scales, int
                                 const float* ts, int type, void* y, cudaStream_t st) {
   const int sms = device_sm_count();
   if (sms < 1) return cudaErrorInvalidConfiguration;
-  const int64_t blocks = (n + 255) / 256, most = (int64_t)sms * 8;
+  const int64_t per = 256 * kDequantSteps, blocks = (n + per - 1) / per, most = (int64_t)sms * 8;
   PdlConfig c(dim3((unsigned)(blocks < most ? blocks : most), 1, 1), 256, 0, st);
   switch (type) {
     case kMx4Bf16:
