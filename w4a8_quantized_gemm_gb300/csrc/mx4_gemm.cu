@@ -18,7 +18,8 @@ namespace {
 
 constexpr int kBT = 64;       // rows of a tile at most
 constexpr int kEpiWarps = 4;  // one for each 32 lanes of Tensor Memory
-constexpr int kThreads = (kEpiWarps + 2) * 32;
+constexpr int kMmaWarp = kEpiWarps, kWeightWarp = kMmaWarp + 1, kRowWarp = kMmaWarp + 2;
+constexpr int kThreads = (kRowWarp + 1) * 32;
 constexpr int kMaxSplit = 8;  // CTAs that share a unit's K, a cluster
 
 // Two CTAs share an SM, so that one's loads cover the other's ends.
@@ -57,7 +58,7 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_few_kernel(const Mx4Params p)
   using C = Cfg<FMT>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t bars = base + C::kMiscAt;
   auto full = [&](int s) { return bars + 8u * s; };
   auto empty = [&](int s) { return bars + 8u * (C::kStages + s); };
@@ -73,7 +74,7 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_few_kernel(const Mx4Params p)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(full(s), 1);
+      mbar_init(full(s), 2);  // (two producers)
       mbar_init(empty(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -84,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_few_kernel(const Mx4Params p)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kEpiWarps + 1) {
+  if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(tmem_slot), C::kCols);
     tmem_relinquish();
   }
@@ -129,92 +130,87 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_few_kernel(const Mx4Params p)
     return r;
   };
 
-  if (warp == kEpiWarps) {
-    // ---------------------------------------------------------------- producer
-    if (lane == 0) {
-      const int n_items = n_units * kb_n;
-      int issued = 0;
-      Unit un{};
-      // the first weights are on their way before this kernel's own wait: nothing
-      // that may still run in front of it writes weights
-      const int ahead = min(C::kStages, n_items);
-      auto bytes_of = [&](const Unit& x) {
-        return (uint32_t)(C::kRec + ((x.count + 7) & ~7) * 128 + C::kScale);
-      };
-      auto load_w = [&](const Unit& x, int kb, int s) {
-        mbar_arrive_expect_tx(full(s), bytes_of(x));
-        bulk_load(base + s * C::kStage, x.w + (int64_t)kb * C::kRec, C::kRec, full(s));
-      };
-      auto load_rows = [&](const Unit& x, int kb, int s) {
-        const uint8_t* rec = x.rows + (int64_t)kb * C::kRec;
-        const uint32_t to = base + s * C::kStage;
-        bulk_load(to + C::kRowsAt, rec + x.half * 128, (uint32_t)((x.count + 7) & ~7) * 128,
-                  full(s));
-        bulk_load(to + C::kRowScaleAt, rec + kMx4Codes, C::kScale, full(s));
-      };
-      for (int i = 0; i < ahead; ++i) {
-        if (i % kb_n == 0) un = unit_at(i / kb_n);
-        load_w(un, i % kb_n, i);
-      }
-      griddep_wait();
-      griddep_launch_dependents();
-      for (int i = 0; i < ahead; ++i) {
-        if (i % kb_n == 0) un = unit_at(i / kb_n);
-        load_rows(un, i % kb_n, i);
-        ++issued;
-      }
-      int unit = (ahead - 1) / kb_n, kb = (ahead - 1) % kb_n;
-      for (int i = ahead; i < n_items; ++i) {
-        const int s = i % C::kStages;
-        if (!mbar_wait(empty(s), ((i / C::kStages) & 1) ^ 1, abort_flag, tmo)) break;
-        if (++kb == kb_n) {
-          kb = 0;
-          un = unit_at(++unit);
+  // Producers, a thread each for weights and rows: issuing a copy takes some 60
+  // cycles, and a stage's barriers more. Each tells the stage's barrier what it
+  // brings.
+  auto produce = [&](auto&& bytes_of, auto&& load) {
+    Ring<C::kStages> r;
+    int i = 0;
+    bool ok = true;
+    for (int k = 0; k < n_units && ok; ++k) {
+      const Unit un = unit_at(k);
+      const uint32_t bytes = bytes_of(un);
+      for (int kb = 0; kb < kb_n; ++kb, ++i, r.next()) {
+        if (i >= C::kStages && !mx4_wait(empty(r.s), r.phase ^ 1, abort_flag, tmo)) {
+          ok = false;
+          break;
         }
-        load_w(un, kb, s);
-        load_rows(un, kb, s);
-        ++issued;
-      }
-      for (int i = (issued > C::kStages ? issued - C::kStages : 0); i < issued; ++i) {
-        volatile int no_abort = 0;
-        mbar_wait(full(i % C::kStages), (i / C::kStages) & 1, &no_abort, tmo);
+        mbar_arrive_expect_tx(full(r.s), bytes);
+        load(un, kb, base + r.s * C::kStage, full(r.s));
       }
     }
-  } else if (warp == kEpiWarps + 1) {
+    for (int j = max(0, i - C::kStages); j < i; ++j) {  // what is on its way lands
+      volatile int no_abort = 0;
+      mx4_wait(full(j % C::kStages), (j / C::kStages) & 1, &no_abort, tmo);
+    }
+  };
+  if (warp == kWeightWarp) {
+    // Weights need no wait: nothing that may still run in front of this kernel
+    // writes them.
+    if (lane == 0)
+      produce([&](const Unit&) { return (uint32_t)C::kRec; },
+              [&](const Unit& x, int kb, uint32_t to, uint32_t bar) {
+                bulk_load(to, x.w + (int64_t)kb * C::kRec, C::kRec, bar);
+              });
+  } else if (warp == kRowWarp) {
+    if (lane == 0) {
+      griddep_wait();
+      griddep_launch_dependents();
+      produce([&](const Unit& x) { return (uint32_t)((x.count + 7) & ~7) * 128 + C::kScale; },
+              [&](const Unit& x, int kb, uint32_t to, uint32_t bar) {
+                const uint8_t* rec = x.rows + (int64_t)kb * C::kRec;
+                bulk_load(to + C::kRowsAt, rec + x.half * 128, (uint32_t)((x.count + 7) & ~7) * 128,
+                          bar);
+                bulk_load(to + C::kRowScaleAt, rec + kMx4Codes, C::kScale, bar);
+              });
+    }
+  } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- issuer
     if (lane == 0) {
-      bool ok = true;
-      int i = 0;
+      const uint64_t operand = sdesc_kmajor_sw128(base), scales = sdesc_scales(base);
+      bool ok = true, any = false;
+      Ring<C::kStages> r;
       for (int k = 0; k < n_units && ok; ++k) {
         const Unit un = unit_at(k);
-        const int cols = (un.count + 15) & ~15;
+        const uint32_t idesc = idesc_mx4<FMT>(128, (un.count + 15) & ~15);
         const int b = k & 1;
-        if (k >= 2) ok = mbar_wait(free_acc(b), ((k >> 1) & 1) ^ 1, abort_flag, tmo);
+        if (k >= 2) ok = mx4_wait(free_acc(b), ((k >> 1) & 1) ^ 1, abort_flag, tmo);
         const uint32_t d = tmem + b * kBT;
-        for (int kb = 0; kb < kb_n && ok; ++kb, ++i) {
-          const int s = i % C::kStages;
-          ok = mbar_wait(full(s), (i / C::kStages) & 1, abort_flag, tmo);
+        for (int kb = 0; kb < kb_n && ok; ++kb, r.next()) {
+          ok = mx4_wait(full(r.s), r.phase, abort_flag, tmo);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t a_at = base + s * C::kStage, b_at = a_at + C::kRowsAt;
+          any = true;
           // a stage's scales have columns of their own: they are free once the
           // stage is
-          const uint32_t sa = tmem + 2 * kBT + s * C::kScaleCols, sb = sa + 4 * C::kAtoms;
+          const uint32_t sa = tmem + 2 * kBT + r.s * C::kScaleCols, sb = sa + 4 * C::kAtoms;
+          const uint64_t from = mx4_at(scales, r.s * C::kStage);
+          const uint64_t at = mx4_at(operand, r.s * C::kStage);
 #pragma unroll
           for (int j = 0; j < C::kAtoms; ++j) {
-            tc_cp_scales<1>(sa + 4 * j, a_at + kMx4Codes + j * 512);
-            tc_cp_scales<1>(sb + 4 * j, a_at + C::kRowScaleAt + j * 512);
+            tc_cp_scales<1>(sa + 4 * j, mx4_at(from, kMx4Codes + j * 512));
+            tc_cp_scales<1>(sb + 4 * j, mx4_at(from, C::kRowScaleAt + j * 512));
           }
-          tc_block_mx4<FMT, 1>(d, a_at, b_at, sa, 4, sb + un.half / 32, 4, 128, cols,
+          tc_block_mx4<FMT, 1>(d, at, mx4_at(at, C::kRowsAt), sa, sb + un.half / 32, 4, idesc,
                                mx4_steps(p.K, kb0 + kb), kb == 0);
-          tc_commit(empty(s));
+          tc_commit(empty(r.s));
         }
         if (ok) tc_commit(done(b));
       }
-      if (i > 0) {  // what was issued ends before the block does
+      if (any) {  // what was issued ends before the block does
         tc_commit(fin());
         volatile int no_abort = 0;
-        mbar_wait(fin(), 0, &no_abort, tmo);
+        mx4_wait(fin(), 0, &no_abort, tmo);
       }
     }
   } else {
@@ -226,8 +222,7 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_few_kernel(const Mx4Params p)
       const int b = k & 1;
       float g = p.a_scale ? __ldg(p.a_scale) : 1.f;
       if (p.w_scale) g *= __ldg(p.w_scale + un.set);
-      ok = mbar_wait(done(b), (k >> 1) & 1, abort_flag, tmo);
-      ok = __all_sync(0xffffffffu, ok);
+      ok = mx4_wait_warp(done(b), (k >> 1) & 1, abort_flag, tmo);
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + b * kBT + ((uint32_t)(warp * 32) << 16);
@@ -279,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_few_kernel(const Mx4Params p)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kEpiWarps + 1) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols);
   }

@@ -12,6 +12,7 @@
 // tile's instructions wait until the epilogue has read those of the tile before;
 // the rest is read while they run.
 #include "mx4_tc.cuh"
+#include "tc_kernel.cuh"  // (encode_fn)
 
 namespace egopq {
 
@@ -19,7 +20,11 @@ namespace {
 
 constexpr int kBT = 256;      // rows of a tile at most
 constexpr int kEpiWarps = 8;  // two for each 32 lanes of Tensor Memory
-constexpr int kThreads = (kEpiWarps + 2) * 32;
+// then: the instructions' issuer, the scales' (of the weight rows and of each 128
+// rows), and two producers
+constexpr int kMmaWarp = kEpiWarps, kCopyWarp = kMmaWarp + 1, kCopies = 3,
+              kWeightWarp = kCopyWarp + kCopies, kRowWarp = kWeightWarp + 1;
+constexpr int kThreads = (kRowWarp + 1) * 32;
 
 template <int FMT>
 struct Cfg {
@@ -33,36 +38,31 @@ struct Cfg {
   static constexpr int kStages = FMT == EGOPQ_MX4_E8M0 ? 6 : 5;
   static constexpr int kMiscAt = kStages * kStage;
   static constexpr int kMisc = 256;
-  // scales: 128 weight rows' and 256 rows' words, in two sets
+  // scales: 128 weight rows' and 256 rows' words, in sets
   static constexpr int kSetCols = 12 * kAtoms;
-  static constexpr int kScaleAt = 512 - 2 * kSetCols;
+  static constexpr int kSets = FMT == EGOPQ_MX4_E8M0 ? 4 : 3;
+  static constexpr int kScaleAt = 512 - kSets * kSetCols;
   static constexpr int kAcc1 = kScaleAt - kBT;
   static constexpr int kShared = kBT - kAcc1;  // columns of both accumulators
-  static_assert(kAcc1 >= 0 && kShared % 16 == 0 && kShared <= 96, "Tensor Memory");
+  static_assert(kAcc1 >= 0 && kShared % 16 == 0 && kShared <= 144, "Tensor Memory");
   static_assert(kRec % 1024 == 0 && kStage % 1024 == 0, "swizzle atoms");
 };
 
 // ---- barriers of a pair -----------------------------------------------------------
-__device__ __forceinline__ void arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+// Arrives on another CTA's barrier, for Tensor Memory that has been read (its fence is
+// beside the call), so it orders no memory of this thread's beyond the CTA: a
+// release to the cluster waits 0.7 us for that.
+__device__ __forceinline__ void arrive_remote(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
+// Rows of 128 bytes from row y on, to this CTA's shared memory; `bar` may be the
+// other CTA's.
+__device__ __forceinline__ void load_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int y) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(y)
       : "memory");
-  return ok != 0;
-}
-// mbar_wait for a barrier that the other CTA arrives on.
-__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                             uint64_t timeout_ns) {
-  if (try_wait_cluster(bar, parity)) return true;
-  if (!mbar_wait(bar, parity, abort_flag, timeout_ns)) return false;
-  return try_wait_cluster(bar, parity);  // (done: for its scope)
 }
 // Arrives on the barrier at this place in both CTAs when every instruction so far
 // has completed.
@@ -78,9 +78,18 @@ __device__ __forceinline__ void commit_own(uint32_t bar) {
                : "memory");
 }
 
+// The operands as tensors of 128-byte rows, a record kRec / 128 of them (a bulk copy
+// without a tensor map could not tell the other CTA's barrier of its arrival).
+struct Maps {
+  CUtensorMap weight;  // a record
+  CUtensorMap rows;    // 128 rows
+  CUtensorMap part;    // 32 rows
+  CUtensorMap scale;   // a record's scales
+};
+
 struct Unit {
-  const uint8_t* w;     // this CTA's first weight record
-  const uint8_t* rows;  // the tile's first row record
+  int w;                // this CTA's first weight record
+  int rows;             // the tile's first row record
   int64_t row0;         // first row of y
   int count, cols;      // rows; the instruction's columns
   int n0;               // this CTA's first column of y
@@ -123,20 +132,21 @@ __device__ __forceinline__ void store16(const Mx4Params& p, const Unit& un, int 
 }
 
 template <int FMT>
-__global__ void __launch_bounds__(kThreads, 1) mx4_pair_kernel(const Mx4Params p) {
+__global__ void __launch_bounds__(kThreads, 1) mx4_pair_kernel(const __grid_constant__ Maps maps,
+                                                                const Mx4Params p) {
   using C = Cfg<FMT>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();
   const uint32_t bars = base + C::kMiscAt;
   auto full = [&](int s) { return bars + 8u * s; };
-  auto peer_full = [&](int s) { return bars + 8u * (C::kStages + s); };
-  auto empty = [&](int s) { return bars + 8u * (2 * C::kStages + s); };
-  auto done = [&](int b) { return bars + 8u * (3 * C::kStages + b); };
-  auto early = [&] { return bars + 8u * (3 * C::kStages + 2); };
-  auto fin = [&] { return bars + 8u * (3 * C::kStages + 3); };
-  uint8_t* misc = smem + C::kMiscAt + 8 * (3 * C::kStages + 4);
+  auto empty = [&](int s) { return bars + 8u * (C::kStages + s); };
+  auto done = [&](int b) { return bars + 8u * (2 * C::kStages + b); };
+  auto early = [&] { return bars + 8u * (2 * C::kStages + 2); };
+  auto fin = [&] { return bars + 8u * (2 * C::kStages + 3); };
+  auto brought = [&](int q) { return bars + 8u * (2 * C::kStages + 4 + q); };
+  uint8_t* misc = smem + C::kMiscAt + 8 * (2 * C::kStages + 4 + C::kSets);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 4);
   int* first = reinterpret_cast<int*>(smem + C::kMiscAt + C::kMisc);
@@ -145,17 +155,17 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_pair_kernel(const Mx4Params p
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(peer_full(s), 1);
+      mbar_init(full(s), 2);  // (the leader's two producers; both CTAs' bytes)
       mbar_init(empty(s), 1);
     }
     for (int b = 0; b < 2; ++b) mbar_init(done(b), 1);
     mbar_init(early(), 2 * kEpiWarps);
-    mbar_init(fin(), 1);
+    mbar_init(fin(), 1 + kCopies);
+    for (int q = 0; q < C::kSets; ++q) mbar_init(brought(q), kCopies);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kEpiWarps + 1) {
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      smem_u32(tmem_slot))
                  : "memory");
@@ -180,7 +190,6 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_pair_kernel(const Mx4Params p
   const int team = (int)blockIdx.x / 2, teams = (int)gridDim.x / 2;
   const int total = tile[p.sets] * nbp;
   const int n_units = team < total ? (total - team + teams - 1) / teams : 0;
-  const int n_items = n_units * p.kb;
   auto unit_at = [&](int i) {
     const int u = team + i * teams;
     const int e = mx4_find_set(tile, p.sets, u / nbp);
@@ -191,122 +200,144 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_pair_kernel(const Mx4Params p
     r.set = e;
     // (of an odd number of blocks the last pair's second is the last again: its
     // columns of y do not exist)
-    r.w = p.packed + ((int64_t)e * p.nb + min(2 * n + rank, p.nb - 1)) * p.kb * C::kRec;
-    r.rows = p.operand + (int64_t)(block[e] + 2 * t) * p.kb * C::kRec;
+    r.w = (e * p.nb + min(2 * n + rank, p.nb - 1)) * p.kb;
+    r.rows = (block[e] + 2 * t) * p.kb;
     r.row0 = (int64_t)first[e] + (int64_t)t * kBT;
     r.count = min(kBT, first[e + 1] - (int)r.row0);
-    r.cols = (r.count + 15) & ~15;
+    // (above 128 a multiple of 64, so that neither half ends inside 32 rows of a record)
+    r.cols = r.count <= 128 ? (r.count + 15) & ~15 : (r.count + 63) & ~63;
     r.n0 = (2 * n + rank) * 128;
     return r;
   };
 
-  if (warp == kEpiWarps) {
-    // ---------------------------------------------------------------- producer
-    if (lane == 0) {
-      int issued = 0;
-      Unit un{};
-      const int ahead = min(C::kStages, n_items);
-      auto load_w = [&](const Unit& x, int kb, int s) {
-        const uint32_t bytes =
-            C::kRec + x.cols / 2 * 128 + (x.cols > 128 ? 2 : 1) * C::kScale;
-        mbar_arrive_expect_tx(full(s), bytes);
-        bulk_load(base + s * C::kStage, x.w + (int64_t)kb * C::kRec, C::kRec, full(s));
-      };
-      // this CTA's half of the rows: of the first record, the second, or both
-      auto load_rows = [&](const Unit& x, int kb, int s) {
-        const uint8_t* rec = x.rows + (int64_t)kb * C::kRec;
-        const uint8_t* next = rec + (int64_t)p.kb * C::kRec;
-        const uint32_t to = base + s * C::kStage;
-        const int half = x.cols / 2, from = rank * half;
-        const int here = max(0, min(half, 128 - from));  // rows in the first record
-        if (here) bulk_load(to + C::kRowsAt, rec + from * 128, here * 128, full(s));
-        if (here < half)
-          bulk_load(to + C::kRowsAt + here * 128, next + (from + here - 128) * 128,
-                    (half - here) * 128, full(s));
-        bulk_load(to + C::kRowScaleAt, rec + kMx4Codes, C::kScale, full(s));
-        if (x.cols > 128)
-          bulk_load(to + C::kRowScaleAt + C::kScale, next + kMx4Codes, C::kScale, full(s));
-      };
-      // (weights before this kernel's own wait: see mx4_few_kernel)
-      for (int i = 0; i < ahead; ++i) {
-        if (i % p.kb == 0) un = unit_at(i / p.kb);
-        load_w(un, i % p.kb, i);
+  // Producers, a thread for weights and one for rows and their scales, in each CTA.
+  // The leader's tell its barrier what both bring.
+  auto produce = [&](auto&& bytes_of, auto&& load) {
+    Ring<C::kStages> r;
+    int i = 0;
+    bool ok = true;
+    for (int k = 0; k < n_units && ok; ++k) {
+      const Unit un = unit_at(k);
+      const uint32_t bytes = 2 * bytes_of(un);
+      for (int kb = 0; kb < p.kb; ++kb, ++i, r.next()) {
+        if (i >= C::kStages && !mx4_wait(empty(r.s), r.phase ^ 1, abort_flag, tmo)) {
+          ok = false;
+          break;
+        }
+        if (rank == 0) mbar_arrive_expect_tx(full(r.s), bytes);
+        load(un, kb, base + r.s * C::kStage, map_to_rank(full(r.s), 0));
       }
+    }
+    // What is on its way has landed, and the leader's arrivals are there, before this
+    // CTA leaves: an item's copies have been waited for by its instructions.
+    for (int j = max(0, i - C::kStages); j < i; ++j) {
+      volatile int no_abort = 0;
+      if (rank == 0) mx4_wait(full(j % C::kStages), (j / C::kStages) & 1, &no_abort, tmo);
+      if (!mx4_wait(empty(j % C::kStages), (j / C::kStages) & 1, &no_abort, tmo)) break;
+    }
+  };
+  constexpr int kRecRows = C::kRec / 128;
+  if (warp == kWeightWarp) {
+    // Weights need no wait: nothing that may still run in front of this kernel
+    // writes them.
+    if (lane == 0)
+      produce([&](const Unit&) { return (uint32_t)C::kRec; },
+              [&](const Unit& x, int kb, uint32_t to, uint32_t bar) {
+                load_pair(to, &maps.weight, bar, (x.w + kb) * kRecRows);
+              });
+  } else if (warp == kRowWarp) {
+    if (lane == 0) {
       griddep_wait();
       griddep_launch_dependents();
-      for (int i = 0; i < ahead; ++i) {
-        if (i % p.kb == 0) un = unit_at(i / p.kb);
-        load_rows(un, i % p.kb, i);
-        ++issued;
-      }
-      int unit = (ahead - 1) / p.kb, kb = (ahead - 1) % p.kb;
-      for (int i = ahead; i < n_items; ++i) {
-        const int s = i % C::kStages;
-        if (!mbar_wait(empty(s), ((i / C::kStages) & 1) ^ 1, abort_flag, tmo)) break;
-        if (++kb == p.kb) {
-          kb = 0;
-          un = unit_at(++unit);
-        }
-        load_w(un, kb, s);
-        load_rows(un, kb, s);
-        ++issued;
-      }
-      for (int i = (issued > C::kStages ? issued - C::kStages : 0); i < issued; ++i) {
-        volatile int no_abort = 0;
-        mbar_wait(full(i % C::kStages), (i / C::kStages) & 1, &no_abort, tmo);
-      }
-      // the leader's arrivals on this CTA's barriers are there before it leaves
-      for (int i = (issued > C::kStages ? issued - C::kStages : 0); i < issued; ++i)
-        if (!mbar_wait(empty(i % C::kStages), (i / C::kStages) & 1, abort_flag, tmo)) break;
+      produce(
+          [&](const Unit& x) {
+            return (uint32_t)(x.cols + 63) / 64 * 32 * 128 + (x.cols > 128 ? 2 : 1) * C::kScale;
+          },
+          [&](const Unit& x, int kb, uint32_t to, uint32_t bar) {
+            const int rec = (x.rows + kb) * kRecRows, next = rec + p.kb * kRecRows;
+            if (x.cols == kBT) {
+              load_pair(to + C::kRowsAt, &maps.rows, bar, rank ? next : rec);
+            } else {
+              // this CTA's half, 32 rows at a time, of the first record or the second
+              const int from = rank * x.cols / 2;
+              for (int c = 0; c < x.cols / 2; c += 32) {
+                const int row = from + c;
+                load_pair(to + C::kRowsAt + c * 128, &maps.part, bar,
+                          row < 128 ? rec + row : next + row - 128);
+              }
+            }
+            load_pair(to + C::kRowScaleAt, &maps.scale, bar, rec + 128);
+            if (x.cols > 128)
+              load_pair(to + C::kRowScaleAt + C::kScale, &maps.scale, bar, next + 128);
+          });
     }
-  } else if (warp == kEpiWarps + 1) {
-    if (lane == 0 && rank == 1) {
-      // ------------------------------------------------- this CTA's part is there
-      for (int i = 0; i < n_items; ++i) {
-        const int s = i % C::kStages;
-        if (!mbar_wait(full(s), (i / C::kStages) & 1, abort_flag, tmo)) break;
-        arrive_cluster(map_to_rank(peer_full(s), 0));
-      }
-    } else if (lane == 0) {
-      // -------------------------------------------------------------- issuer
+  } else if (warp >= kCopyWarp && warp < kCopyWarp + kCopies) {
+    // ------------------------------------------------------------------- scales
+    // An instruction takes its thread 50 cycles and more to issue, those of a K block
+    // 512 to run: beside the products' issuer, the weight rows' and each 128 rows'
+    // scales have a thread of their own (E4M3's twelve copies in one took 940 cycles).
+    if (lane == 0 && rank == 0) {
+      const int part = warp - kCopyWarp;
+      const uint64_t scales = sdesc_scales(
+          base + (part == 0 ? (uint32_t)kMx4Codes : C::kRowScaleAt + (part - 1) * C::kScale));
+      const uint32_t to = tmem + C::kScaleAt + (part == 0 ? 0 : 4 * C::kAtoms + 4 * (part - 1));
+      const int step = part == 0 ? 4 : 8;
       bool ok = true;
       int i = 0;
+      Ring<C::kStages> r, before;  // item i, item i - kSets
+      Ring<C::kSets> set;
       for (int k = 0; k < n_units && ok; ++k) {
-        const int cols = unit_at(k).cols;
+        const bool have = part < 2 || unit_at(k).cols > 128;
+        for (int kb = 0; kb < p.kb; ++kb, ++i, r.next(), set.next()) {
+          // its parts are there, and the instructions that read the set last have
+          // completed
+          ok = mx4_wait(full(r.s), r.phase, abort_flag, tmo);
+          if (ok && i >= C::kSets) {
+            ok = mx4_wait(empty(before.s), before.phase, abort_flag, tmo);
+            before.next();
+          }
+          if (!ok) break;
+          tc_fence_after();
+          if (have) {
+            const uint64_t from = mx4_at(scales, r.s * C::kStage);
+#pragma unroll
+            for (int q = 0; q < C::kAtoms; ++q)
+              tc_cp_scales<2>(to + set.s * C::kSetCols + step * q, mx4_at(from, q * 512));
+          }
+          commit_own(brought(set.s));
+        }
+      }
+      commit_own(fin());  // what was issued ends before either CTA does
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------------- issuer
+    if (lane == 0 && rank == 0) {
+      const uint64_t operand = sdesc_kmajor_sw128(base);
+      bool ok = true;
+      Ring<C::kStages> r;
+      Ring<C::kSets> set;
+      for (int k = 0; k < n_units && ok; ++k) {
+        const uint32_t idesc = idesc_mx4<FMT>(256, unit_at(k).cols);
         const uint32_t d = tmem + (k & 1) * C::kAcc1;
         // the shared columns have been read of the tile before, and so all of the
         // one before that
-        if (k >= 1) ok = wait_cluster(early(), (k - 1) & 1, abort_flag, tmo);
-        for (int kb = 0; kb < p.kb && ok; ++kb, ++i) {
-          const int s = i % C::kStages;
-          ok = mbar_wait(full(s), (i / C::kStages) & 1, abort_flag, tmo) &&
-               wait_cluster(peer_full(s), (i / C::kStages) & 1, abort_flag, tmo);
-          // the scales' set is free once the instructions of two K blocks before
-          // have completed
-          if (ok && i >= 2)
-            ok = mbar_wait(empty((i - 2) % C::kStages), ((i - 2) / C::kStages) & 1, abort_flag, tmo);
+        if (k >= 1) ok = mx4_wait(early(), (k - 1) & 1, abort_flag, tmo);
+        for (int kb = 0; kb < p.kb && ok; ++kb, r.next(), set.next()) {
+          // (with the scales the operands that they came with)
+          ok = mx4_wait(brought(set.s), set.phase, abort_flag, tmo);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t at = base + s * C::kStage;
-          const uint32_t sa = tmem + C::kScaleAt + (i & 1) * C::kSetCols, sb = sa + 4 * C::kAtoms;
-#pragma unroll
-          for (int j = 0; j < C::kAtoms; ++j) {
-            tc_cp_scales<2>(sa + 4 * j, at + kMx4Codes + j * 512);
-            tc_cp_scales<2>(sb + 8 * j, at + C::kRowScaleAt + j * 512);
-            if (cols > 128)
-              tc_cp_scales<2>(sb + 8 * j + 4, at + C::kRowScaleAt + C::kScale + j * 512);
-          }
-          tc_block_mx4<FMT, 2>(d, at, at + C::kRowsAt, sa, 4, sb, 8, 256, cols,
+          const uint32_t sa = tmem + C::kScaleAt + set.s * C::kSetCols;
+          const uint64_t at = mx4_at(operand, r.s * C::kStage);
+          tc_block_mx4<FMT, 2>(d, at, mx4_at(at, C::kRowsAt), sa, sa + 4 * C::kAtoms, 8, idesc,
                                mx4_steps(p.K, kb), kb == 0);
-          commit_both(empty(s));
+          commit_both(empty(r.s));
         }
         if (ok) commit_both(done(k & 1));
       }
-      if (i > 0) {  // what was issued ends before either CTA does
-        commit_own(fin());
-        volatile int no_abort = 0;
-        mbar_wait(fin(), 0, &no_abort, tmo);
-      }
+      commit_own(fin());
+      volatile int no_abort = 0;
+      mx4_wait(fin(), 0, &no_abort, tmo);
     }
   } else {
     // ---------------------------------------------------------------- epilogue
@@ -319,8 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_pair_kernel(const Mx4Params p
       const int b = k & 1;
       float g = p.a_scale ? __ldg(p.a_scale) : 1.f;
       if (p.w_scale) g *= __ldg(p.w_scale + un.set);
-      ok = mbar_wait(done(b), (k >> 1) & 1, abort_flag, tmo);
-      ok = __all_sync(0xffffffffu, ok);
+      ok = mx4_wait_warp(done(b), (k >> 1) & 1, abort_flag, tmo);
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + b * C::kAcc1 + ((uint32_t)((warp & 3) * 32) << 16);
@@ -337,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_pair_kernel(const Mx4Params p
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_cluster(early_at);
+      if (lane == 0) arrive_remote(early_at);
 #pragma unroll
       for (int j = 0; j < kFirst; ++j) {
         const int c = (2 * j + mine) * 16;
@@ -358,10 +388,23 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_pair_kernel(const Mx4Params p
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // (neither leaves while the other's instructions or arrivals may reach it)
-  if (warp == kEpiWarps + 1) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
+}
+
+// A buffer as a tensor of 128-byte rows, read `box` rows at a time.
+bool make_map(CUtensorMap* map, const void* ptr, int64_t rows, int box) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {128, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {128};
+  cuuint32_t boxes[2] = {128, (cuuint32_t)box};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, boxes,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int FMT>
@@ -389,6 +432,18 @@ cudaError_t launch_pair(const Mx4GemmArgs& a, cudaStream_t st) {
   if (pairs < 1) return cudaErrorInvalidConfiguration;
   if (most >= (1LL << 31) || (most / pairs + 1) * p.kb >= (1LL << 31))
     return cudaErrorNotSupported;
+  // the operands' rows of 128 bytes
+  const int64_t rec_rows = C::kRec / 128;
+  const int64_t blocks = a.offsets ? mx4_row_blocks(a.M, a.sets) : (a.M + 127) / 128;
+  const int64_t w_rows = (int64_t)a.sets * p.nb * p.kb * rec_rows;
+  const int64_t x_rows = blocks * p.kb * rec_rows;
+  if (w_rows >= (1LL << 31) || x_rows >= (1LL << 31)) return cudaErrorNotSupported;
+  Maps maps;
+  if (!make_map(&maps.weight, a.packed, w_rows, (int)rec_rows) ||
+      !make_map(&maps.rows, a.operand, x_rows, 128) ||
+      !make_map(&maps.part, a.operand, x_rows, 32) ||
+      !make_map(&maps.scale, a.operand, x_rows, C::kScale / 128))
+    return cudaErrorInvalidValue;
   const size_t smem = C::kMiscAt + C::kMisc + 3 * (size_t)(a.sets + 1) * sizeof(int);
   auto kern = mx4_pair_kernel<FMT>;
   static SmemOptIn opt_in;
@@ -400,7 +455,7 @@ cudaError_t launch_pair(const Mx4GemmArgs& a, cudaStream_t st) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   c.cfg.attrs = attr;
   c.cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&c.cfg, kern, p);
+  return cudaLaunchKernelEx(&c.cfg, kern, maps, p);
 }
 
 }  // namespace
