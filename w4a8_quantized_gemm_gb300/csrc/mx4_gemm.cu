@@ -176,42 +176,47 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_few_kernel(const Mx4Params p)
     }
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- issuer
-    if (lane == 0) {
-      const uint64_t operand = sdesc_kmajor_sw128(base), scales = sdesc_scales(base);
-      bool ok = true, any = false;
-      Ring<C::kStages> r;
-      for (int k = 0; k < n_units && ok; ++k) {
-        const Unit un = unit_at(k);
-        const uint32_t idesc = idesc_mx4<FMT>(128, (un.count + 15) & ~15);
-        const int b = k & 1;
-        if (k >= 2) ok = mx4_wait(free_acc(b), ((k >> 1) & 1) ^ 1, abort_flag, tmo);
-        const uint32_t d = tmem + b * kBT;
-        for (int kb = 0; kb < kb_n && ok; ++kb, r.next()) {
-          ok = mx4_wait(full(r.s), r.phase, abort_flag, tmo);
-          if (!ok) break;
-          tc_fence_after();
-          any = true;
-          // a stage's scales have columns of their own: they are free once the
-          // stage is
-          const uint32_t sa = tmem + 2 * kBT + r.s * C::kScaleCols, sb = sa + 4 * C::kAtoms;
-          const uint64_t from = mx4_at(scales, r.s * C::kStage);
-          const uint64_t at = mx4_at(operand, r.s * C::kStage);
+    // (The warp runs whole, so that what an instruction reads is formed in uniform
+    // registers, and one lane issues.)
+    const uint64_t operand = sdesc_kmajor_sw128(base), scales = sdesc_scales(base);
+    const int last_steps = mx4_steps(p.K, p.kb - 1);
+    bool ok = true, any = false;
+    Ring<C::kStages> r;
+    for (int k = 0; k < n_units && ok; ++k) {
+      const Unit un = unit_at(k);
+      const uint32_t idesc = idesc_mx4<FMT>(128, (un.count + 15) & ~15);
+      const int b = k & 1;
+      if (k >= 2) ok = mx4_wait_warp(free_acc(b), ((k >> 1) & 1) ^ 1, abort_flag, tmo);
+      const uint32_t d = tmem + b * kBT;
+      for (int kb = 0; kb < kb_n && ok; ++kb, r.next()) {
+        ok = mx4_wait_warp(full(r.s), r.phase, abort_flag, tmo);
+        if (!ok) break;
+        tc_fence_after();
+        any = true;
+        // a stage's scales have columns of their own: they are free once the
+        // stage is
+        const uint32_t sa = tmem + 2 * kBT + r.s * C::kScaleCols, sb = sa + 4 * C::kAtoms;
+        const uint64_t from = mx4_at(scales, r.s * C::kStage);
+        const uint64_t at_w = mx4_at(operand, r.s * C::kStage), at_r = mx4_at(at_w, C::kRowsAt);
+        const int steps = kb0 + kb + 1 == p.kb ? last_steps : 4;
+        if (lane == 0) {
 #pragma unroll
           for (int j = 0; j < C::kAtoms; ++j) {
             tc_cp_scales<1>(sa + 4 * j, mx4_at(from, kMx4Codes + j * 512));
             tc_cp_scales<1>(sb + 4 * j, mx4_at(from, C::kRowScaleAt + j * 512));
           }
-          tc_block_mx4<FMT, 1>(d, at, mx4_at(at, C::kRowsAt), sa, sb + un.half / 32, 4, idesc,
-                               mx4_steps(p.K, kb0 + kb), kb == 0);
+          tc_block_mx4<FMT, 1>(d, at_w, at_r, sa, sb + un.half / 32, 4, idesc, steps, kb == 0);
           tc_commit(empty(r.s));
+          if (kb + 1 == kb_n) tc_commit(done(b));
         }
-        if (ok) tc_commit(done(b));
+        __syncwarp();
       }
-      if (any) {  // what was issued ends before the block does
-        tc_commit(fin());
-        volatile int no_abort = 0;
-        mx4_wait(fin(), 0, &no_abort, tmo);
-      }
+    }
+    if (any) {  // what was issued ends before the block does
+      if (lane == 0) tc_commit(fin());
+      __syncwarp();
+      volatile int no_abort = 0;
+      mx4_wait_warp(fin(), 0, &no_abort, tmo);
     }
   } else {
     // ---------------------------------------------------------------- epilogue

@@ -273,10 +273,13 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_pair_kernel(const __grid_cons
     }
   } else if (warp >= kCopyWarp && warp < kCopyWarp + kCopies) {
     // ------------------------------------------------------------------- scales
-    // An instruction takes its thread 50 cycles and more to issue, those of a K block
+    // An instruction takes its warp 50 cycles and more to issue, those of a K block
     // 512 to run: beside the products' issuer, the weight rows' and each 128 rows'
-    // scales have a thread of their own (E4M3's twelve copies in one took 940 cycles).
-    if (lane == 0 && rank == 0) {
+    // scales have a warp of their own (E4M3's twelve copies in one took 940 cycles).
+    // The warps run whole, so that what an instruction reads is formed in uniform
+    // registers, and one lane issues (a branch of one lane around all of it took
+    // twice the time).
+    if (rank == 0) {
       const int part = warp - kCopyWarp;
       const uint64_t scales = sdesc_scales(
           base + (part == 0 ? (uint32_t)kMx4Codes : C::kRowScaleAt + (part - 1) * C::kScale));
@@ -291,28 +294,33 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_pair_kernel(const __grid_cons
         for (int kb = 0; kb < p.kb; ++kb, ++i, r.next(), set.next()) {
           // its parts are there, and the instructions that read the set last have
           // completed
-          ok = mx4_wait(full(r.s), r.phase, abort_flag, tmo);
+          ok = mx4_wait_warp(full(r.s), r.phase, abort_flag, tmo);
           if (ok && i >= C::kSets) {
-            ok = mx4_wait(empty(before.s), before.phase, abort_flag, tmo);
+            ok = mx4_wait_warp(empty(before.s), before.phase, abort_flag, tmo);
             before.next();
           }
           if (!ok) break;
           tc_fence_after();
-          if (have) {
-            const uint64_t from = mx4_at(scales, r.s * C::kStage);
+          const uint64_t from = mx4_at(scales, r.s * C::kStage);
+          const uint32_t at = to + set.s * C::kSetCols;
+          if (lane == 0) {
+            if (have) {
 #pragma unroll
-            for (int q = 0; q < C::kAtoms; ++q)
-              tc_cp_scales<2>(to + set.s * C::kSetCols + step * q, mx4_at(from, q * 512));
+              for (int q = 0; q < C::kAtoms; ++q)
+                tc_cp_scales<2>(at + step * q, mx4_at(from, q * 512));
+            }
+            commit_own(brought(set.s));
           }
-          commit_own(brought(set.s));
+          __syncwarp();
         }
       }
-      commit_own(fin());  // what was issued ends before either CTA does
+      if (lane == 0) commit_own(fin());  // what was issued ends before either CTA does
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------- issuer
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       const uint64_t operand = sdesc_kmajor_sw128(base);
+      const int last_steps = mx4_steps(p.K, p.kb - 1);
       bool ok = true;
       Ring<C::kStages> r;
       Ring<C::kSets> set;
@@ -321,23 +329,28 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_pair_kernel(const __grid_cons
         const uint32_t d = tmem + (k & 1) * C::kAcc1;
         // the shared columns have been read of the tile before, and so all of the
         // one before that
-        if (k >= 1) ok = mx4_wait(early(), (k - 1) & 1, abort_flag, tmo);
+        if (k >= 1) ok = mx4_wait_warp(early(), (k - 1) & 1, abort_flag, tmo);
         for (int kb = 0; kb < p.kb && ok; ++kb, r.next(), set.next()) {
           // (with the scales the operands that they came with)
-          ok = mx4_wait(brought(set.s), set.phase, abort_flag, tmo);
+          ok = mx4_wait_warp(brought(set.s), set.phase, abort_flag, tmo);
           if (!ok) break;
           tc_fence_after();
           const uint32_t sa = tmem + C::kScaleAt + set.s * C::kSetCols;
-          const uint64_t at = mx4_at(operand, r.s * C::kStage);
-          tc_block_mx4<FMT, 2>(d, at, mx4_at(at, C::kRowsAt), sa, sa + 4 * C::kAtoms, 8, idesc,
-                               mx4_steps(p.K, kb), kb == 0);
-          commit_both(empty(r.s));
+          const uint64_t a = mx4_at(operand, r.s * C::kStage), b = mx4_at(a, C::kRowsAt);
+          const bool last = kb + 1 == p.kb;
+          const int steps = last ? last_steps : 4;
+          if (lane == 0) {
+            tc_block_mx4<FMT, 2>(d, a, b, sa, sa + 4 * C::kAtoms, 8, idesc, steps, kb == 0);
+            commit_both(empty(r.s));
+            if (last) commit_both(done(k & 1));
+          }
+          __syncwarp();
         }
-        if (ok) commit_both(done(k & 1));
       }
-      commit_own(fin());
+      if (lane == 0) commit_own(fin());
+      __syncwarp();
       volatile int no_abort = 0;
-      mx4_wait(fin(), 0, &no_abort, tmo);
+      mx4_wait_warp(fin(), 0, &no_abort, tmo);
     }
   } else {
     // ---------------------------------------------------------------- epilogue
