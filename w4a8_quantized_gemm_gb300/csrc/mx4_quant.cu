@@ -57,6 +57,18 @@ struct Eight {
     w[0] = make_uint4(0, 0, 0, 0);
     if constexpr (TYPE == kMx4F32) w[1] = w[0];
   }
+  // The largest magnitude's pattern, of values stored as 16 bits (NaN above infinity
+  // above all), and what it stands for.
+  __device__ __forceinline__ uint32_t top16() const {
+    constexpr uint32_t kAbs = 0x7fff7fffu;
+    const uint32_t m = __vmaxu2(__vimax3_u16x2(w[0].x & kAbs, w[0].y & kAbs, w[0].z & kAbs),
+                                w[0].w & kAbs);
+    return max(m & 0xffffu, m >> 16);
+  }
+  static __device__ __forceinline__ float of16(uint32_t pattern) {
+    return TYPE == kMx4Bf16 ? __uint_as_float(pattern << 16)
+                            : __half2float(__ushort_as_half((uint16_t)pattern));
+  }
   __device__ __forceinline__ void values(float (&v)[8]) const {
     const uint32_t a[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
     if constexpr (TYPE == kMx4F32) {
@@ -81,6 +93,21 @@ struct Eight {
     }
   }
 };
+
+// Two fp32 at a time.
+__device__ __forceinline__ void mul2(float& a0, float& a1, float b) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\t"
+      "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b));
+}
+// a = b * c + a
+__device__ __forceinline__ void fma2(float& a0, float& a1, float b0, float b1, float c) {
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+      "mov.b64 c, {%4, %4};\n\tfma.rn.f32x2 a, b, c, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1), "f"(c));
+}
 
 // ---- gated values -----------------------------------------------------------------
 // h = silu(g) * u * r in fp32, for -32 <= g: the exponent's rounding (46 at most)
@@ -116,6 +143,14 @@ __device__ __forceinline__ float max_abs(float a, float b) {
   return r;
 }
 
+// v / 6, on the same side of the borders between e4m3 numbers (five bits; times six,
+// seven) as the real quotient: a product with 1/6 and a step with its remainder, as
+// for the codes below.
+__device__ __forceinline__ float sixth(float v) {
+  const float q = v * (1.f / 6.f);
+  return fmaf(fmaf(-q, 6.f, v), 1.f / 6.f, q);
+}
+
 struct QuantParams {
   const void* x;
   const float* tensor_scale;
@@ -128,30 +163,41 @@ struct QuantParams {
   int sets, kb, groups;  // K blocks of a row, and runs of U of them
 };
 
-// Where a lane's results of a row go: its codes and its block's scale in their plain
-// places and in the row's first record (null: not asked for).
+// Where a lane's results of a row's next runs go: its codes and its block's scale in
+// their plain places and in the first run's record (null: not asked for).
 struct RowOut {
   uint8_t *codes, *scales, *rec, *rec_scale;
 };
 
-// One run of 256 values of a row, all lanes of a warp.
+// The i-th run of 256 values from where `out` points, all lanes of a warp.
 template <int FMT, int TYPE, bool GATED>
-__device__ __forceinline__ void quant_unit(const RowOut& out, const Eight<TYPE>& g8,
-                                           const Eight<TYPE>& u8, int kb, bool in, bool scaled,
-                                           float r) {
+__device__ __forceinline__ void quant_unit(const RowOut& out, int i_run, const Eight<TYPE>& g8,
+                                           const Eight<TYPE>& u8, bool in, bool scaled, float r) {
   constexpr int kLanes = mx4_block(FMT) / 8;  // of one block
   const int lane = threadIdx.x & 31;
   float v[8], g[8], u[8];
   bool weak = false;
+  float most;  // the block's largest magnitude (a NaN is)
   g8.values(g);
+  if constexpr (!GATED && TYPE != kMx4F32) {
+    // (of the stored patterns: the product with r keeps their order)
+    uint32_t top = g8.top16();
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    most = Eight<TYPE>::of16(top);
+    if (FMT == kE4M3 && scaled) most *= r;
+  }
   if constexpr (GATED) {
     u8.values(u);
     float low = 1.f, gate = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float h = gated32(g[i], u[i]);
-      v[i] = h * r;
-      low = fminf(low, fminf(fabsf(h), fabsf(v[i])));
+      v[i] = gated32(g[i], u[i]);
+      if constexpr (FMT == kE4M3) {
+        low = fminf(low, fabsf(v[i]));
+        v[i] *= r;
+      }
+      low = fminf(low, fabsf(v[i]));
       gate = fminf(gate, g[i]);
     }
     if (low < 0x1p-100f || gate < -32.f) {
@@ -160,25 +206,30 @@ __device__ __forceinline__ void quant_unit(const RowOut& out, const Eight<TYPE>&
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = scaled ? g[i] * r : g[i];
+    for (int i = 0; i < 8; ++i) v[i] = g[i];
+    if (FMT == kE4M3 && scaled) {
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) mul2(v[i], v[i + 1], r);
+    }
   }
-  // the block's largest magnitude (a NaN is)
-  float most = max_abs(v[0], v[1]);
+  if constexpr (GATED || TYPE == kMx4F32) {
+    most = max_abs(v[0], v[1]);
 #pragma unroll
-  for (int i = 2; i < 8; ++i) most = max_abs(most, v[i]);
+    for (int i = 2; i < 8; ++i) most = max_abs(most, v[i]);
 #pragma unroll
-  for (int o = 1; o < kLanes; o <<= 1)
-    most = max_abs(most, __shfl_xor_sync(0xffffffffu, most, o));
+    for (int o = 1; o < kLanes; o <<= 1)
+      most = max_abs(most, __shfl_xor_sync(0xffffffffu, most, o));
+  }
   const uint32_t top = __float_as_uint(most);
   const bool bad = top >= 0x7f800000u;
   uint32_t byte;
   if constexpr (FMT == kE8M0)
     byte = bad ? 255u : (uint32_t)max((int)(top >> 23) - 2, 0);
   else
-    byte = bad ? 0x7fu : __nv_cvt_float_to_fp8(__fdiv_rn(most, 6.f), __NV_SATFINITE, __NV_E4M3);
+    byte = bad ? 0x7fu : __nv_cvt_float_to_fp8(sixth(most), __NV_SATFINITE, __NV_E4M3);
   if constexpr (GATED) {
     // next to a border between scales (a block of zeros is exact)
-    const uint32_t over = FMT == kE8M0 ? above_short(most, 0) : above_short(__fdividef(most, 6.f), 4);
+    const uint32_t over = FMT == kE8M0 ? above_short(most, 0) : above_short(sixth(most), 4);
     bool close = !bad && (weak || (top != 0 && over < 2 * kNear));
     if (__any_sync(0xffffffffu, close)) {
       // (a block's lanes go together; which of its values may be the largest is
@@ -214,18 +265,26 @@ __device__ __forceinline__ void quant_unit(const RowOut& out, const Eight<TYPE>&
     // 2^(127 - byte), byte at most 252: exact, as is the product where it matters
     inv = bad ? 0.f : __uint_as_float((254u - byte) << 23);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = v[i] * inv;
+    for (int i = 0; i < 8; ++i) t[i] = v[i];
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) mul2(t[i], t[i + 1], inv);
   } else {
     s = e4m3_value(byte);
-    inv = s > 0.f ? __frcp_rn(s) : 0.f;
+    inv = s > 0.f ? __fdividef(1.f, s) : 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      t[i] = v[i] * inv;
+    for (int i = 0; i < 8; i += 2) {
+      t[i] = v[i], t[i + 1] = v[i + 1];
+      mul2(t[i], t[i + 1], inv);
       // Borders m are numbers of three bits and s one of four, so m s has seven: v
-      // is on it, or v / s at least .53 of m's last places away. t is off by two of
-      // its last places; with the remainder, which is exact, it is off by 2^-22 of
-      // one before it is rounded: on the border or on the right side of it.
-      if constexpr (!GATED) t[i] = fmaf(fmaf(-t[i], s, v[i]), inv, t[i]);
+      // is on it, or v / s at least .53 of m's last places away. t is off by four of
+      // its last places; with the remainder, which is exact, it is off by 2^-20 of
+      // one before it is rounded: on the border or on the right side of it. (An IEEE
+      // quotient is too, but branches.)
+      if constexpr (!GATED) {
+        float r0 = v[i], r1 = v[i + 1];
+        fma2(r0, r1, t[i], t[i + 1], -s);
+        fma2(t[i], t[i + 1], r0, r1, inv);
+      }
     }
   }
   uint32_t code = e2m1x8(t);
@@ -247,13 +306,12 @@ __device__ __forceinline__ void quant_unit(const RowOut& out, const Eight<TYPE>&
   }
   if (bad) code = 0;
   if (out.codes && in) {
-    *reinterpret_cast<uint32_t*>(out.codes + kb * 128) = code;
-    if (lane % kLanes == 0) out.scales[kb * (256 / mx4_block(FMT))] = (uint8_t)byte;
+    *reinterpret_cast<uint32_t*>(out.codes + i_run * 128) = code;
+    if (lane % kLanes == 0) out.scales[i_run * (256 / mx4_block(FMT))] = (uint8_t)byte;
   }
   if (out.rec) {
-    const int64_t to = (int64_t)kb * mx4_record_bytes(FMT);
-    *reinterpret_cast<uint32_t*>(out.rec + to) = code;
-    if (lane % kLanes == 0) out.rec_scale[to] = (uint8_t)byte;
+    *reinterpret_cast<uint32_t*>(out.rec + i_run * mx4_record_bytes(FMT)) = code;
+    if (lane % kLanes == 0) out.rec_scale[i_run * mx4_record_bytes(FMT)] = (uint8_t)byte;
   }
 }
 
@@ -262,7 +320,7 @@ __device__ __forceinline__ void quant_unit(const RowOut& out, const Eight<TYPE>&
 // line. Bound by memory: all of a warp's loads are on their way before the first
 // is used; few rows take U = 1, so that more warps share them.
 template <int FMT, int TYPE, bool GATED, int U>
-__global__ void __launch_bounds__(kQuantWarps * 32) mx4_quant_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(kQuantWarps * 32, GATED ? 7 : 1) mx4_quant_kernel(const QuantParams p) {
   extern __shared__ int quant_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_wait();
@@ -305,8 +363,9 @@ __global__ void __launch_bounds__(kQuantWarps * 32) mx4_quant_kernel(const Quant
     }
     RowOut out{};
     if (p.codes) {
-      out.codes = p.codes + row * (p.K / 2) + lane * 4;
-      out.scales = p.scales + row * (p.K / mx4_block(FMT)) + lane / kLanes;
+      out.codes = p.codes + row * (p.K / 2) + group * U * 128 + lane * 4;
+      out.scales = p.scales + row * (p.K / mx4_block(FMT)) +
+                   group * U * (256 / mx4_block(FMT)) + lane / kLanes;
     }
     if (p.operand) {
       int64_t at = row;  // among the operand's rows
@@ -314,18 +373,16 @@ __global__ void __launch_bounds__(kQuantWarps * 32) mx4_quant_kernel(const Quant
         const int e = mx4_find_set(first, p.sets, (int)row);
         at = (int64_t)block[e] * 128 + (row - first[e]);
       }
-      uint8_t* rec = p.operand + (at >> 7) * p.kb * mx4_record_bytes(FMT);
+      uint8_t* rec = p.operand + ((at >> 7) * p.kb + group * U) * mx4_record_bytes(FMT);
       const int q = (int)(at & 127), b = lane / kLanes;
       out.rec = rec + q * 128 + ((((lane >> 2) ^ q) & 7) << 4) + (lane & 3) * 4;
       out.rec_scale = rec + kMx4Codes + (b >> 2) * 512 + (q & 31) * 16 + (q >> 5) * 4 + (b & 3);
     }
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int kb = group * U + i;
-      if (U == 1 || kb < p.kb)
-        quant_unit<FMT, TYPE, GATED>(out, g8[i], u8[GATED ? i : 0], kb,
-                                     (int64_t)kb * 256 + lane * 8 < p.K, scaled, r);
-    }
+    for (int i = 0; i < U; ++i)
+      if (U == 1 || group * U + i < p.kb)
+        quant_unit<FMT, TYPE, GATED>(out, i, g8[i], u8[GATED ? i : 0],
+                                     (int64_t)(group * U + i) * 256 + lane * 8 < p.K, scaled, r);
     row += row_step;
     group += group_step;
     if (group >= p.groups) {
@@ -336,7 +393,7 @@ __global__ void __launch_bounds__(kQuantWarps * 32) mx4_quant_kernel(const Quant
 }
 
 template <int FMT, int TYPE, bool GATED, int U>
-cudaError_t launch_quant_u(const Mx4QuantArgs& a, int64_t warps, cudaStream_t st) {
+cudaError_t launch_quant_u(const Mx4QuantArgs& a, int sms, cudaStream_t st) {
   QuantParams p;
   p.x = a.x;
   p.tensor_scale = a.tensor_scale;
@@ -352,7 +409,19 @@ cudaError_t launch_quant_u(const Mx4QuantArgs& a, int64_t warps, cudaStream_t st
   p.kb = (int)mx4_kblocks(a.K);
   p.groups = (p.kb + U - 1) / U;
   const int64_t blocks = (a.M * p.groups + kQuantWarps - 1) / kQuantWarps;
-  const int64_t most = warps / kQuantWarps;
+  // as many as are on the SMs at a time: a second round of blocks that takes as long
+  // as the first would leave them half empty
+  static std::atomic<int> held{0};
+  int per_sm = held.load(std::memory_order_relaxed);
+  if (per_sm < 1) {
+    if (cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+            &per_sm, mx4_quant_kernel<FMT, TYPE, GATED, U>, kQuantWarps * 32, 0);
+        e != cudaSuccess)
+      return e;
+    held.store(per_sm < 1 ? 1 : per_sm, std::memory_order_relaxed);
+    if (per_sm < 1) per_sm = 1;
+  }
+  const int64_t most = (int64_t)sms * per_sm;
   const size_t smem = a.offsets ? 2 * (size_t)(a.sets + 1) * sizeof(int) : 0;
   PdlConfig c(dim3((unsigned)(blocks < most ? blocks : most), 1, 1), kQuantWarps * 32, smem, st);
   return cudaLaunchKernelEx(&c.cfg, mx4_quant_kernel<FMT, TYPE, GATED, U>, p);
@@ -363,9 +432,9 @@ cudaError_t launch_quant(const Mx4QuantArgs& a, cudaStream_t st) {
   constexpr int kMany = GATED || TYPE == kMx4F32 ? 2 : 4;
   const int sms = device_sm_count();
   if (sms < 1) return cudaErrorInvalidConfiguration;
-  const int64_t warps = (int64_t)sms * 48;
-  return a.M * mx4_kblocks(a.K) <= 2 * warps ? launch_quant_u<FMT, TYPE, GATED, 1>(a, warps, st)
-                                             : launch_quant_u<FMT, TYPE, GATED, kMany>(a, warps, st);
+  return a.M * mx4_kblocks(a.K) <= (int64_t)sms * 96
+             ? launch_quant_u<FMT, TYPE, GATED, 1>(a, sms, st)
+             : launch_quant_u<FMT, TYPE, GATED, kMany>(a, sms, st);
 }
 
 template <int FMT>
