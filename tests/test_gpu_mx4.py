@@ -262,10 +262,48 @@ def test_ragged(fmt, counts, N, K):
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_ragged_gathered_and_gated(fmt):
     check_ragged([9, 0, 150, 30], 257, 480, fmt, tokens=50)
+    check_ragged([9, 0, 150, 30], 257, 480, fmt, tokens=300)
+    # many from few: quantized once, gathered in 4 bits
+    check_ragged([9, 0, 8000, 300, 33], 130, 1056, fmt, tokens=1900, before=2, after=1)
+    check_ragged([4, 9000, 0, 30], 33, 960, fmt, tokens=11, gated=True, before=2, after=1)
     check_ragged([9, 0, 150, 30], 257, 480, fmt, gated=True)
     check_ragged([2, 0, 3], 64, 96, fmt, before=4, after=130)
     check_ragged([2, 0, 3], 64, 96, fmt, before=1, after=2, tokens=3, gated=True,
                  dtype=torch.float16)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("tokens,n,K", [(6, 20, 96), (20, 20, 96), (30, 8192, 1056)])
+def test_index_outside_reads_zeros(fmt, tokens, n, K):
+    g = gen(23)
+    x = rand(g, tokens, K)
+    index = torch.arange(n, device="cuda", dtype=torch.int32) % tokens
+    index[3], index[11], index[n - 1] = -1, tokens, 2 ** 31 - 1
+    w, w64, _ = weight(g, fmt, 2, 40, K)
+    off = torch.tensor([0, 7, n], dtype=torch.int32, device="cuda")
+    y = eg.mx4_linear_ragged(x, off, w, index=index)
+    ok = (index >= 0) & (index < tokens)
+    assert (y[~ok] == 0).all()
+    a = rows64(x, K, fmt, None)[torch.where(ok, index, 0).long()] * ok[:, None]
+    for e, (lo, hi) in enumerate(((0, 7), (7, n))):
+        check(y[lo:hi], a[lo:hi], w64[e])
+
+
+@pytest.mark.parametrize("bad", [
+    [0, 5, 3, 10, 10], [-4, 2, 2, 9, 12], [0, 99, 99, 99, 99], [20, 1, 2, 3, 4], [5, 5, 5, 5, 5]])
+def test_offsets_out_of_order_or_range_count_as_the_nearest(bad):
+    """What the header says of them: rising, within [0, rows]."""
+    g = gen(24)
+    x = rand(g, 12, 64)
+    w, w64, _ = weight(g, 0, 4, 40, 64)
+    y = torch.full((12, 40), 9.0, dtype=torch.bfloat16, device="cuda")
+    eg.mx4_linear_ragged(x, torch.tensor(bad, dtype=torch.int32, device="cuda"), w, out=y)
+    off = torch.tensor(bad).clamp(0, 12).cummax(0).values.tolist()
+    a = rows64(x, 64, 0, None)
+    for e in range(4):
+        if off[e] < off[e + 1]:
+            check(y[off[e]:off[e + 1]], a[off[e]:off[e + 1]], w64[e])
+    assert (y[:off[0]] == 9.0).all() and (y[off[4]:] == 9.0).all()
 
 
 def test_ragged_without_rows():

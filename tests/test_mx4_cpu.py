@@ -38,9 +38,10 @@ def test_sizes(lib):
     assert lib.egopq_mx4_operand_bytes(129, 288, 1) == 4 * 18432
     assert lib.egopq_mx4_packed_bytes(3, 130, 256, 0) == 6 * 17408
     assert lib.egopq_mx4_linear_workspace_bytes(128, 0, 256, 0) == 17408
-    # each set with rows may begin a block of its own
-    assert lib.egopq_mx4_linear_workspace_bytes(300, 8, 256, 0) == 10 * 17408
-    assert lib.egopq_mx4_linear_workspace_bytes(3, 8, 256, 0) == 3 * 17408
+    # each set with rows may begin a block of its own; and codes and scales of a
+    # quarter as many rows, if the rows are gathered from so few
+    assert lib.egopq_mx4_linear_workspace_bytes(300, 8, 256, 0) == 10 * 17408 + 75 * 136 + 16
+    assert lib.egopq_mx4_linear_workspace_bytes(3, 8, 256, 0) == 3 * 17408 + 16
     for bad in ((0, 32, 0), (4, 48, 0), (4, 0, 0), (4, 32, 2), (-1, 32, 0), (1 << 31, 32, 0)):
         assert lib.egopq_mx4_operand_bytes(*bad) == 0, bad
     for bad in ((0, 8, 32, 0), (1025, 8, 32, 0), (1, 0, 32, 0), (1, 8, 31, 0), (1, 8, 32, -1)):
@@ -96,6 +97,9 @@ def test_products_refuse(lib):
     assert code(lib, linear(lib, nbytes=17407), "17408 needed") == -1
     assert code(lib, linear(lib, work=A + 64), "overlaps") == -1
     assert code(lib, linear(lib, work=2 * A - 17408 + 16), "overlaps") == -1
+    # y [4][8] of two bytes on x [4][64]
+    for y in (A, A + 496, A - 48):
+        assert code(lib, linear(lib, y=y), "y overlaps x") == -1
     assert code(lib, linear(lib, a=A), "no tensor scale") == -1
     assert code(lib, linear(lib, fmt=1, a=A + 1), "4-byte") == -3
 
@@ -109,7 +113,7 @@ def test_ragged_products_refuse(lib):
     assert code(lib, ragged(lib, x_rows=-1, index=A), "rows of x") == -1
     assert code(lib, ragged(lib, sets=0), "sizes") == -1
     assert code(lib, ragged(lib, sets=1025), "at most 1024") == -2
-    assert code(lib, ragged(lib, nbytes=3 * 17408 - 1), "needed") == -1
+    assert code(lib, ragged(lib, nbytes=3 * 17408 + 15), "needed") == -1
     assert code(lib, ragged(lib, x=None), "x is NULL") == -1
     # slices of an index and of offsets, at any of their elements
     assert code(lib, ragged(lib, off=A + 4, index=A + 12, nbytes=0), "needed") == -1

@@ -701,11 +701,22 @@ MX4_E8M0, MX4_E4M3 = 0, 1
 _MX4_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
+_MX4_BLOCK = {MX4_E8M0: 32, MX4_E4M3: 16}
+
+
 def mx4_block(fmt: int) -> int:
     """Neighbours along K that share a scale: 32 (MX4_E8M0) or 16 (MX4_E4M3)."""
-    if fmt not in (MX4_E8M0, MX4_E4M3):
+    block = _MX4_BLOCK.get(fmt)
+    if block is None:
         raise ValueError(f"unknown 4-bit format {fmt}")
-    return 32 if fmt == MX4_E8M0 else 16
+    return block
+
+
+def _mx4_here(t: torch.Tensor):
+    """Kernels run on the current device: a tensor of another is refused."""
+    if t.is_cuda and t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"tensor on {t.device}, the current device is "
+                         f"{torch._C._cuda_getDevice()}")
 
 
 def _mx4_type(dtype: torch.dtype) -> int:
@@ -755,11 +766,13 @@ def mx4_quant(x: torch.Tensor, fmt: int = MX4_E8M0, tensor_scale: Optional[torch
     scales, with_tc the form that mx4_gemm reads. `out`: rows of an earlier call of
     the same sizes."""
     block, kind = mx4_block(fmt), _mx4_type(x.dtype)
+    _mx4_here(x)
     M, K = x.shape
     if gated:
         if K % 2:
             raise ValueError(f"{K} gate and up values: an odd number")
         K //= 2
+    lib = load()
     if out is None:
         dev = x.device
         codes = scales = a_tc = None
@@ -769,7 +782,7 @@ def mx4_quant(x: torch.Tensor, fmt: int = MX4_E8M0, tensor_scale: Optional[torch
             codes = _output((M, K // 2), torch.uint8, dev, stream)
             scales = _output((M, K // block), torch.uint8, dev, stream)
         if with_tc:
-            a_tc = _output((int(load().egopq_mx4_operand_bytes(M, K, fmt)),), torch.uint8, dev,
+            a_tc = _output((int(lib.egopq_mx4_operand_bytes(M, K, fmt)),), torch.uint8, dev,
                            stream)
         out = Mx4Rows(codes, scales, a_tc, M, K, fmt, tensor_scale)
     else:
@@ -777,10 +790,14 @@ def mx4_quant(x: torch.Tensor, fmt: int = MX4_E8M0, tensor_scale: Optional[torch
             raise ValueError(f"out holds {out.M} x {out.K} of format {out.fmt}, expected "
                              f"{M} x {K} of {fmt}")
         _mx4_rows_check(out)
+        codes, scales, a_tc = out.codes, out.scales, out.a_tc
         out = out._replace(tensor_scale=tensor_scale)
-    _check(load().egopq_mx4_quant(_ptr(x), kind, M, K, fmt, _mx4_scale(tensor_scale, 1), gated,
-                                  _ptr(out.codes), _ptr(out.scales), _ptr(out.a_tc),
-                                  _stream(stream)))
+    # (what the call made itself needs no look)
+    _check(lib.egopq_mx4_quant(
+        _ptr(x), kind, M, K, fmt, None if tensor_scale is None else _mx4_scale(tensor_scale, 1),
+        gated, None if codes is None else codes.data_ptr(),
+        None if scales is None else scales.data_ptr(),
+        None if a_tc is None else a_tc.data_ptr(), _stream(stream)))
     return out
 
 
@@ -794,6 +811,7 @@ def _mx4_rows_check(rows: Mx4Rows):
         _arg(rows.scales, torch.uint8, M, K // block)
     if rows.a_tc is not None:
         need = int(load().egopq_mx4_operand_bytes(M, K, rows.fmt))
+        _ptr(rows.a_tc)
         if rows.a_tc.nbytes < need:
             raise ValueError(f"a_tc of {rows.a_tc.nbytes} bytes, {need} needed")
 
@@ -801,14 +819,17 @@ def _mx4_rows_check(rows: Mx4Rows):
 def mx4_dequant(rows: Mx4Rows, dtype: torch.dtype = torch.bfloat16,
                 out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values [M, K] that rows' codes and scales stand for."""
-    if rows.codes is None or rows.scales is None:
+    codes, scales, _, M, K, fmt, tensor_scale = rows
+    if codes is None or scales is None:
         raise ValueError("rows without codes and scales (with_codes=False)")
-    _mx4_rows_check(rows)
+    _mx4_here(codes)
+    c = _arg(codes, torch.uint8, M, K // 2)
+    s = _arg(scales, torch.uint8, M, K // mx4_block(fmt))
     if out is None:
-        out = _output((rows.M, rows.K), dtype, rows.codes.device, stream)
-    _check(load().egopq_mx4_dequant(_ptr(rows.codes), _ptr(rows.scales), rows.M, rows.K, rows.fmt,
-                                    _mx4_scale(rows.tensor_scale, 1), _mx4_type(dtype),
-                                    _arg(out, dtype, rows.M, rows.K), _stream(stream)))
+        out = _output((M, K), dtype, codes.device, stream)
+    _check(load().egopq_mx4_dequant(
+        c, s, M, K, fmt, None if tensor_scale is None else _mx4_scale(tensor_scale, 1),
+        _mx4_type(dtype), _arg(out, dtype, M, K), _stream(stream)))
     return out
 
 
@@ -828,6 +849,7 @@ def mx4_pack(codes: torch.Tensor, scales: torch.Tensor, fmt: int = MX4_E8M0,
         raise EgopqError(-1, "E8M0 blocks have no tensor scale")
     if tensor_scale is not None:
         _mx4_scale(tensor_scale, max(sets, 1))
+    _mx4_here(codes)
     c = _arg(codes, torch.uint8, *lead, N, K // 2)
     s = _arg(scales, torch.uint8, *lead, N, K // block)
     packed = _output((nbytes,), torch.uint8, codes.device, stream)
@@ -839,6 +861,7 @@ def mx4_pack(codes: torch.Tensor, scales: torch.Tensor, fmt: int = MX4_E8M0,
 def mx4_unpack(weight: Mx4Weight, stream=None) -> tuple:
     """(codes, scales) of a packed weight, as mx4_pack took them."""
     packed, sets, N, K, fmt, _ = weight
+    _mx4_here(packed)
     lead, dev = ((sets,) if sets else ()), packed.device
     codes = _output((*lead, N, K // 2), torch.uint8, dev, stream)
     scales = _output((*lead, N, K // mx4_block(fmt)), torch.uint8, dev, stream)
@@ -857,6 +880,7 @@ def mx4_gemm(rows: Mx4Rows, weight: Mx4Weight, dtype: torch.dtype = torch.bfloat
         raise ValueError(f"rows of K={rows.K} format {rows.fmt}, a weight of K={K} format {fmt}")
     if rows.a_tc is None:
         raise ValueError("rows without the products' form (with_tc=False)")
+    _mx4_here(packed)
     _mx4_rows_check(rows)
     if out is None:
         out = _output((rows.M, N), dtype, packed.device, stream)
@@ -873,9 +897,13 @@ def mx4_workspace(rows: int, weight: Mx4Weight, device, stream=None) -> torch.Te
     return _scratch(n, torch.uint8, device, stream)
 
 
-def _mx4_width(x: torch.Tensor, K: int, gated: bool):
-    if x.dim() != 2 or x.shape[1] != (2 * K if gated else K):
-        raise ValueError(f"x of shape {tuple(x.shape)} for {'gated ' if gated else ''}K = {K}")
+def _mx4_input(x: torch.Tensor, K: int, gated: bool) -> tuple:
+    """Rows and type of a linear's input."""
+    shape = x.shape
+    if len(shape) != 2 or shape[1] != (2 * K if gated else K):
+        raise ValueError(f"x of shape {tuple(shape)} for {'gated ' if gated else ''}K = {K}")
+    _mx4_here(x)
+    return shape[0], _mx4_type(x.dtype)
 
 
 def mx4_linear(x: torch.Tensor, weight: Mx4Weight, tensor_scale: Optional[torch.Tensor] = None,
@@ -888,16 +916,17 @@ def mx4_linear(x: torch.Tensor, weight: Mx4Weight, tensor_scale: Optional[torch.
     packed, sets, N, K, fmt, w_scale = weight
     if sets:
         raise ValueError("weights of several sets: mx4_linear_ragged")
-    _mx4_width(x, K, gated)
-    M = x.shape[0]
+    M, x_type = _mx4_input(x, K, gated)
     if out is None:
         out = _output((M, N), dtype or x.dtype, x.device, stream)
     if workspace is None:
         workspace = mx4_workspace(M, weight, x.device, stream)
+    y_type = out.dtype
     _check(load().egopq_mx4_linear(
-        _ptr(x), _mx4_type(x.dtype), M, N, K, gated, _mx4_scale(tensor_scale, 1), _ptr(packed),
-        _mx4_scale(w_scale, 1), fmt, _mx4_type(out.dtype), _arg(out, out.dtype, M, N),
-        _ptr(workspace), workspace.nbytes, _stream(stream)))
+        _ptr(x), x_type, M, N, K, gated,
+        None if tensor_scale is None else _mx4_scale(tensor_scale, 1), packed.data_ptr(),
+        None if w_scale is None else _mx4_scale(w_scale, 1), fmt, _mx4_type(y_type),
+        _arg(out, y_type, M, N), _ptr(workspace), workspace.nbytes, _stream(stream)))
     return out
 
 
@@ -914,19 +943,19 @@ def mx4_linear_ragged(x: torch.Tensor, offsets: torch.Tensor, weight: Mx4Weight,
     packed, sets, N, K, fmt, w_scale = weight
     if not sets:
         raise ValueError("a weight of several sets is needed (codes [E, N, K/2])")
-    _mx4_width(x, K, gated)
-    rows = x.shape[0] if index is None else index.shape[0]
+    x_rows, x_type = _mx4_input(x, K, gated)
+    rows = x_rows if index is None else index.shape[0]
     if out is None:
         out = _output((rows, N), dtype or x.dtype, x.device, stream)
     if workspace is None:
         workspace = mx4_workspace(rows, weight, x.device, stream)
+    y_type = out.dtype
     _check(load().egopq_mx4_linear_ragged(
-        _ptr(x), _mx4_type(x.dtype), x.shape[0],
-        None if index is None else _arg(index, torch.int32, rows),
+        _ptr(x), x_type, x_rows, None if index is None else _arg(index, torch.int32, rows),
         _arg(offsets, torch.int32, sets + 1), rows, sets, N, K, gated,
-        _mx4_scale(tensor_scale, 1), _ptr(packed), _mx4_scale(w_scale, sets), fmt,
-        _mx4_type(out.dtype), _arg(out, out.dtype, rows, N), _ptr(workspace), workspace.nbytes,
-        _stream(stream)))
+        None if tensor_scale is None else _mx4_scale(tensor_scale, 1), packed.data_ptr(),
+        None if w_scale is None else _mx4_scale(w_scale, sets), fmt, _mx4_type(y_type),
+        _arg(out, y_type, rows, N), _ptr(workspace), workspace.nbytes, _stream(stream)))
     return out
 
 

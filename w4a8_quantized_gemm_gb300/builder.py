@@ -24,7 +24,7 @@ DEBUG_LIB = os.path.join(BUILD, "libegopq_debug.so")
 SOURCES = ["egopq_api.cu", "quant_pack.cu", "gemv.cu", "tc_gemm.cu", "no_alloc.cu",
            "rows_api.cu", "route.cu", "experts.cu", "tc_experts.cu", "lora.cu",
            "mx4_api.cu", "mx4_quant.cu", "mx4_gemm.cu", "mx4_pair.cu"]
-HEADERS = ["egopq_common.cuh", "egopq_internal.h", "tc_kernel.cuh", "mx4_internal.h", "mx4_tc.cuh"]
+HEADERS = ["egopq_common.cuh", "egopq_internal.h", "tc_kernel.cuh", "mx4_internal.h", "mx4_tc.cuh", "mx4_quant.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                 "-Xcompiler", "-Wall", "-Xcompiler", "-Wno-unknown-pragmas"]

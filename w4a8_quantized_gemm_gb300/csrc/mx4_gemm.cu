@@ -10,6 +10,7 @@
 // rounds once. Weights are the instruction's 128 rows and a tile of one set's rows
 // its columns, as many as there are (a multiple of 16): few rows, or a ragged
 // set's last ones, cost what they are.
+#include "mx4_quant.cuh"
 #include "mx4_tc.cuh"
 
 namespace egopq {
@@ -22,16 +23,26 @@ constexpr int kMmaWarp = kEpiWarps, kWeightWarp = kMmaWarp + 1, kRowWarp = kMmaW
 constexpr int kThreads = (kRowWarp + 1) * 32;
 constexpr int kMaxSplit = 8;  // CTAs that share a unit's K, a cluster
 
+// Rows that the kernel quantizes itself (XT their type; kNone: they come as records):
+// a handful, of one linear, once a CTA and for the K blocks that are its own. They
+// then lie in shared memory behind the ring, and a stage holds weights alone. That
+// leaves out a kernel and the wait for its results.
+constexpr int kNone = -1;
+constexpr int kOwnRows = 16;             // at most
+constexpr int kOwnRuns = 64;             // runs of 256 values a CTA, at most
+constexpr int kOwnBytes = 40960;         // codes and scales, at most
+
 // Two CTAs share an SM, so that one's loads cover the other's ends.
-template <int FMT>
+template <int FMT, int XT>
 struct Cfg {
+  static constexpr bool kOwn = XT != kNone;
   static constexpr int kRec = mx4_record_bytes(FMT);
   static constexpr int kScale = kRec - kMx4Codes;
   static constexpr int kAtoms = kScale / 512;  // of a K block and 128 rows
   static constexpr int kRowsAt = kRec;         // a stage: a weight record, rows' codes, scales
   static constexpr int kRowScaleAt = kRec + kBT * 128;
-  static constexpr int kStage = kRowScaleAt + kScale;
-  static constexpr int kStages = FMT == EGOPQ_MX4_E8M0 ? 4 : 3;
+  static constexpr int kStage = kOwn ? kRec : kRowScaleAt + kScale;
+  static constexpr int kStages = kOwn || FMT == EGOPQ_MX4_E8M0 ? 4 : 3;
   static constexpr int kMiscAt = kStages * kStage;
   static constexpr int kMisc = 256;
   // Tensor Memory: two accumulators, then each stage's scales
@@ -53,9 +64,10 @@ struct Unit {
   int set;
 };
 
-template <int FMT>
-__global__ void __launch_bounds__(kThreads, 2) mx4_few_kernel(const Mx4Params p) {
-  using C = Cfg<FMT>;
+// x: the rows, where the kernel quantizes them (GATED: [gate | up]); p.operand else.
+template <int FMT, int XT, bool GATED>
+__global__ void __launch_bounds__(kThreads, 2) mx4_few_kernel(const Mx4Params p, const void* x) {
+  using C = Cfg<FMT, XT>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -65,16 +77,21 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_few_kernel(const Mx4Params p)
   auto done = [&](int b) { return bars + 8u * (2 * C::kStages + b); };
   auto free_acc = [&](int b) { return bars + 8u * (2 * C::kStages + 2 + b); };
   auto fin = [&] { return bars + 8u * (2 * C::kStages + 4); };
-  uint8_t* misc = smem + C::kMiscAt + 8 * (2 * C::kStages + 5);
+  auto own = [&] { return bars + 8u * (2 * C::kStages + 5); };
+  uint8_t* misc = smem + C::kMiscAt + 8 * (2 * C::kStages + 6);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 4);
   int* first = reinterpret_cast<int*>(smem + C::kMiscAt + C::kMisc);
   int* block = first + p.sets + 1;
   int* tile = block + p.sets + 1;
+  // own rows: behind the sets, 1024-byte aligned: [K block][codes of 16 rows], then
+  // [K block][scales]
+  constexpr int kOwnAt = C::kMiscAt + 1024;
+  static_assert(C::kMisc + 6 * sizeof(int) <= 1024, "one set's words");
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(full(s), 2);  // (two producers)
+      mbar_init(full(s), C::kOwn ? 1 : 2);  // (producers)
       mbar_init(empty(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -82,6 +99,7 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_few_kernel(const Mx4Params p)
       mbar_init(free_acc(b), kEpiWarps);
     }
     mbar_init(fin(), 1);
+    mbar_init(own(), kEpiWarps);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -163,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_few_kernel(const Mx4Params p)
                 bulk_load(to, x.w + (int64_t)kb * C::kRec, C::kRec, bar);
               });
   } else if (warp == kRowWarp) {
-    if (lane == 0) {
+    if (!C::kOwn && lane == 0) {
       griddep_wait();
       griddep_launch_dependents();
       produce([&](const Unit& x) { return (uint32_t)((x.count + 7) & ~7) * 128 + C::kScale; },
@@ -181,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_few_kernel(const Mx4Params p)
     const uint64_t operand = sdesc_kmajor_sw128(base), scales = sdesc_scales(base);
     const int last_steps = mx4_steps(p.K, p.kb - 1);
     bool ok = true, any = false;
+    if (C::kOwn && n_units > 0) ok = mx4_wait_warp(own(), 0, abort_flag, tmo);
     Ring<C::kStages> r;
     for (int k = 0; k < n_units && ok; ++k) {
       const Unit un = unit_at(k);
@@ -197,13 +216,17 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_few_kernel(const Mx4Params p)
         // stage is
         const uint32_t sa = tmem + 2 * kBT + r.s * C::kScaleCols, sb = sa + 4 * C::kAtoms;
         const uint64_t from = mx4_at(scales, r.s * C::kStage);
-        const uint64_t at_w = mx4_at(operand, r.s * C::kStage), at_r = mx4_at(at_w, C::kRowsAt);
+        const uint64_t from_r = C::kOwn ? mx4_at(scales, kOwnAt + kb_n * 2048 + kb * C::kScale)
+                                        : mx4_at(from, C::kRowScaleAt);
+        const uint64_t at_w = mx4_at(operand, r.s * C::kStage);
+        const uint64_t at_r = C::kOwn ? mx4_at(operand, kOwnAt + kb * 2048)
+                                      : mx4_at(at_w, C::kRowsAt);
         const int steps = kb0 + kb + 1 == p.kb ? last_steps : 4;
         if (lane == 0) {
 #pragma unroll
           for (int j = 0; j < C::kAtoms; ++j) {
             tc_cp_scales<1>(sa + 4 * j, mx4_at(from, kMx4Codes + j * 512));
-            tc_cp_scales<1>(sb + 4 * j, mx4_at(from, C::kRowScaleAt + j * 512));
+            tc_cp_scales<1>(sb + 4 * j, mx4_at(from_r, j * 512));
           }
           tc_block_mx4<FMT, 1>(d, at_w, at_r, sa, sb + un.half / 32, 4, idesc, steps, kb == 0);
           tc_commit(empty(r.s));
@@ -221,6 +244,46 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_few_kernel(const Mx4Params p)
   } else {
     // ---------------------------------------------------------------- epilogue
     griddep_wait();
+    if constexpr (C::kOwn) {
+      if (threadIdx.x == 0) griddep_launch_dependents();
+      if (n_units > 0) {
+        // Runs of 256 values, four of a warp's on their way at a time.
+        constexpr int kAhead = 4, kLanes = mx4_block(FMT) / 8;
+        const bool scaled = p.a_scale != nullptr;
+        const float rg = scaled ? __fdiv_rn(1.f, __ldg(p.a_scale)) : 1.f;
+        const int64_t ld = GATED ? 2 * p.K : p.K;
+        const int runs = (int)p.M * kb_n;
+        for (int u0 = warp; u0 < runs; u0 += kEpiWarps * kAhead) {
+          Eight<XT> g8[kAhead], u8[kAhead];
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) {
+            const int u = u0 + j * kEpiWarps, row = u / kb_n, kb = u - row * kb_n;
+            const int64_t k = (int64_t)(kb0 + kb) * 256 + lane * 8;
+            g8[j].zero();
+            u8[j].zero();
+            if (u < runs && k < p.K) {
+              g8[j].load(x, row * ld + k);
+              if constexpr (GATED) u8[j].load(x, row * ld + p.K + k);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) {
+            const int u = u0 + j * kEpiWarps, row = u / kb_n, kb = u - row * kb_n;
+            if (u >= runs) break;
+            const int b = lane / kLanes;
+            RowOut out{};
+            out.rec = smem + kOwnAt + kb * 2048 + row * 128 + ((((lane >> 2) ^ row) & 7) << 4) +
+                      (lane & 3) * 4;
+            out.rec_scale = smem + kOwnAt + kb_n * 2048 + kb * C::kScale + (b >> 2) * 512 +
+                            row * 16 + (b & 3);
+            quant_unit<FMT, XT, GATED>(out, 0, g8[j], u8[j], true, scaled, rg);
+          }
+        }
+        fence_proxy_async_smem();  // (the tensor cores read what these threads wrote)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(own());
+      }
+    }
     bool ok = true;
     for (int k = 0; k < n_units && ok; ++k) {
       const Unit un = unit_at(k);
@@ -285,10 +348,8 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_few_kernel(const Mx4Params p)
   }
 }
 
-template <int FMT>
-cudaError_t launch_few(const Mx4GemmArgs& a, cudaStream_t st) {
-  using C = Cfg<FMT>;
-  Mx4Params p;
+Mx4Params params_of(const Mx4GemmArgs& a) {
+  Mx4Params p{};
   p.operand = a.operand;
   p.packed = a.packed;
   p.a_scale = a.a_scale;
@@ -302,20 +363,37 @@ cudaError_t launch_few(const Mx4GemmArgs& a, cudaStream_t st) {
   p.nb = (int)((a.N + 127) / 128);
   p.kb = (int)mx4_kblocks(a.K);
   p.type = a.type;
+  p.split = 1;
   p.timeout_ns = a.timeout_ns;
-  const int64_t tiles = a.offsets ? mx4_tiles(a.M, a.sets, kBT) : (a.M + kBT - 1) / kBT;
-  const int64_t most = tiles * p.nb;
+  return p;
+}
+
+int64_t few_units(const Mx4GemmArgs& a) {
+  return (a.offsets ? mx4_tiles(a.M, a.sets, kBT) : (a.M + kBT - 1) / kBT) * ((a.N + 127) / 128);
+}
+
+// Fewer units than the SMs hold CTAs: K is split.
+int few_split(int64_t units, int64_t kb, int sms) {
+  int64_t s = 2 * (int64_t)sms / units;
+  if (s > kMaxSplit) s = kMaxSplit;
+  if (s > kb) s = kb;
+  return s < 1 ? 1 : (int)s;
+}
+
+template <int FMT, int XT, bool GATED>
+cudaError_t launch_few(const Mx4GemmArgs& a, const void* x, cudaStream_t st) {
+  using C = Cfg<FMT, XT>;
+  Mx4Params p = params_of(a);
+  const int64_t most = few_units(a);
   const int sms = device_sm_count();
   if (sms < 1) return cudaErrorInvalidConfiguration;
   if (most >= (1LL << 31) || (most / sms + 1) * p.kb >= (1LL << 31)) return cudaErrorNotSupported;
-  // Fewer units than the SMs hold CTAs: K is split.
+  p.split = few_split(most, p.kb, sms);
   const int64_t slots = 2 * sms;
-  p.split = (int)(slots / most);
-  if (p.split > kMaxSplit) p.split = kMaxSplit;
-  if (p.split > p.kb) p.split = p.kb;
-  if (p.split < 1) p.split = 1;
-  const size_t smem = C::kMiscAt + C::kMisc + 3 * (size_t)(a.sets + 1) * sizeof(int);
-  auto kern = mx4_few_kernel<FMT>;
+  const int kb_most = (p.kb + p.split - 1) / p.split;
+  const size_t smem = C::kMiscAt + (C::kOwn ? 1024 + kb_most * (2048 + C::kScale)
+                                            : C::kMisc + 3 * (size_t)(a.sets + 1) * sizeof(int));
+  auto kern = mx4_few_kernel<FMT, XT, GATED>;
   static SmemOptIn opt_in;
   if (cudaError_t e = opt_in.ensure(kern, smem); e != cudaSuccess) return e;
   PdlConfig c(dim3((unsigned)(p.split > 1 ? most * p.split : most < slots ? most : slots), 1, 1),
@@ -328,15 +406,39 @@ cudaError_t launch_few(const Mx4GemmArgs& a, cudaStream_t st) {
     c.cfg.attrs = attr;
     c.cfg.numAttrs = 2;
   }
-  return cudaLaunchKernelEx(&c.cfg, kern, p);
+  return cudaLaunchKernelEx(&c.cfg, kern, p, x);
+}
+
+template <int FMT>
+cudaError_t launch_own(const Mx4GemmArgs& a, const Mx4QuantArgs& q, cudaStream_t st) {
+  if (q.type == kMx4Bf16)
+    return q.gated ? launch_few<FMT, kMx4Bf16, true>(a, q.x, st)
+                   : launch_few<FMT, kMx4Bf16, false>(a, q.x, st);
+  return q.gated ? launch_few<FMT, kMx4F16, true>(a, q.x, st)
+                 : launch_few<FMT, kMx4F16, false>(a, q.x, st);
 }
 
 }  // namespace
 
+bool mx4_own_rows(const Mx4GemmArgs& a, const Mx4QuantArgs& q) {
+  if (a.offsets || a.M > kOwnRows || q.type == kMx4F32) return false;
+  const int sms = device_sm_count();
+  if (sms < 1) return false;
+  const int64_t kb = mx4_kblocks(a.K), split = few_split(few_units(a), kb, sms);
+  const int64_t kb_most = (kb + split - 1) / split;
+  return a.M * kb_most <= kOwnRuns &&
+         kb_most * (2048 + mx4_record_bytes(a.format) - kMx4Codes) <= kOwnBytes;
+}
+
+cudaError_t launch_mx4_own(const Mx4GemmArgs& a, const Mx4QuantArgs& q, cudaStream_t st) {
+  return a.format == EGOPQ_MX4_E8M0 ? launch_own<EGOPQ_MX4_E8M0>(a, q, st)
+                                    : launch_own<EGOPQ_MX4_E4M3>(a, q, st);
+}
+
 cudaError_t launch_mx4_gemm(const Mx4GemmArgs& a, cudaStream_t st) {
   if (a.M > 64 * (int64_t)a.sets) return launch_mx4_pair(a, st);
-  return a.format == EGOPQ_MX4_E8M0 ? launch_few<EGOPQ_MX4_E8M0>(a, st)
-                                    : launch_few<EGOPQ_MX4_E4M3>(a, st);
+  return a.format == EGOPQ_MX4_E8M0 ? launch_few<EGOPQ_MX4_E8M0, kNone, false>(a, nullptr, st)
+                                    : launch_few<EGOPQ_MX4_E4M3, kNone, false>(a, nullptr, st);
 }
 
 cudaError_t take_error_word_mx4_gemm(unsigned* out) { return take_local_error_word(out); }

@@ -54,6 +54,8 @@ struct Mx4QuantArgs {
   uint8_t* operand;      // records, may be null
 };
 cudaError_t launch_mx4_quant(const Mx4QuantArgs& a, cudaStream_t st);
+// Rows index[r] of codes [x_rows][K / 2] and scales to the operand's records.
+cudaError_t launch_mx4_gather(const Mx4QuantArgs& a, cudaStream_t st);
 cudaError_t launch_mx4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K,
                                int format, const float* tensor_scale, int type, void* y,
                                cudaStream_t st);
@@ -78,6 +80,9 @@ struct Mx4GemmArgs {
 // cudaErrorNotSupported: more work than one launch's counters hold.
 cudaError_t launch_mx4_gemm(const Mx4GemmArgs& a, cudaStream_t st);
 cudaError_t launch_mx4_pair(const Mx4GemmArgs& a, cudaStream_t st);  // (of many rows)
+// A linear of so few rows that the product's kernel quantizes them itself, and it.
+bool mx4_own_rows(const Mx4GemmArgs& a, const Mx4QuantArgs& q);
+cudaError_t launch_mx4_own(const Mx4GemmArgs& a, const Mx4QuantArgs& q, cudaStream_t st);
 
 // ---- ragged rows ---------------------------------------------------------------
 // One warp: where each set's rows begin (clamped to [0, M] and to the sets
