@@ -75,7 +75,8 @@ def awkward(g, M, K, dtype):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("M,K", [(1, 32), (3, 96), (130, 288), (259, 1056), (1, 18944)])
+@pytest.mark.parametrize("M,K", [(1, 32), (3, 96), (130, 288), (259, 1056), (1, 18944),
+                                 (1811, 2336)])
 def test_codes_and_scales(fmt, dtype, M, K):
     x = awkward(gen(1), M, K, dtype)
     rows = eg.mx4_quant(x, fmt)
@@ -137,7 +138,7 @@ def test_blocks_without_a_value(fmt):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("M,K", [(1, 32), (33, 1056), (700, 1408)])
+@pytest.mark.parametrize("M,K", [(1, 32), (33, 1056), (2600, 1408)])
 def test_gated_codes(fmt, dtype, M, K):
     """Codes of the real gated values: none of 64 bits' is off by rounding."""
     g = gen(5)
@@ -206,14 +207,37 @@ def test_types(fmt, x_type, y_type):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("M,N,K", [(1, 384, 1408), (40, 200, 96), (259, 130, 512)])
-def test_gated_linear(fmt, M, N, K):
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,N,K", [(1, 384, 1408), (3, 1000, 4512), (16, 130, 288), (40, 200, 96),
+                                   (259, 130, 512)])
+def test_gated_linear(fmt, dtype, M, N, K):
+    """Quantized by the product's kernel (few rows) or apart: the same codes."""
     g = gen(12)
-    x = rand(g, M, 2 * K, scale=1.5)
+    x = rand(g, M, 2 * K, scale=1.5, dtype=dtype)
+    x[:, :8] = -50.0
     ts = torch.tensor([0.004], device="cuda") if fmt == eg.MX4_E4M3 else None
     w, w64, _ = weight(g, fmt, N, K)
     y = eg.mx4_linear(x, w, tensor_scale=ts, gated=True)
     check(y, rows64(x, K, fmt, ts, gated=True), w64)
+    rows = eg.mx4_quant(x, fmt, tensor_scale=ts, gated=True, with_codes=False)
+    assert torch.equal(eg.mx4_gemm(rows, w, dtype=dtype), y)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("M,N,K", [(1, 40000, 288), (9, 640, 1824), (16, 33, 2048), (17, 33, 2048)])
+def test_few_rows_are_the_same_either_way(fmt, dtype, M, N, K):
+    """mx4_linear of few rows quantizes them in the product's kernel."""
+    g = gen(14)
+    x = awkward(g, M, K, dtype)
+    x[0, 3] = math.inf
+    w, _, _ = weight(g, fmt, N, K)
+    ts = torch.tensor([0.37], device="cuda") if fmt == eg.MX4_E4M3 else None
+    rows = eg.mx4_quant(x, fmt, tensor_scale=ts)
+    y, z = eg.mx4_linear(x, w, tensor_scale=ts, dtype=torch.float32), eg.mx4_gemm(
+        rows, w, dtype=torch.float32)
+    assert torch.equal(torch.nan_to_num(y, nan=1e30), torch.nan_to_num(z, nan=1e30))
+    assert y[0].isnan().all() and not y[1:].isnan().any()
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -304,6 +328,138 @@ def test_offsets_out_of_order_or_range_count_as_the_nearest(bad):
         if off[e] < off[e + 1]:
             check(y[off[e]:off[e + 1]], a[off[e]:off[e + 1]], w64[e])
     assert (y[:off[0]] == 9.0).all() and (y[off[4]:] == 9.0).all()
+
+
+# ------------------------------------------------------ streams, graphs, sharing ---
+
+def test_another_stream_and_no_workspace():
+    g = gen(30)
+    w, w64, _ = weight(g, 1, 300, 512)
+    s = torch.cuda.Stream()
+    for M in (1, 40, 200):
+        x = rand(g, M, 512)
+        ts = tscale(x, 1)
+        s.wait_stream(torch.cuda.current_stream())
+        y = eg.mx4_linear(x, w, tensor_scale=ts, stream=s)
+        rows = eg.mx4_quant(x, 1, tensor_scale=ts, stream=s)
+        z = eg.mx4_gemm(rows, w, stream=s)
+        v = eg.mx4_dequant(rows, stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+        check(y, rows64(x, 512, 1, ts), w64)
+        assert torch.equal(y, z)
+        assert torch.equal(v.double(), rows64(x, 512, 1, ts).float().bfloat16().double())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_captured_and_replayed_with_other_rows(fmt):
+    """One graph of a dense and a ragged call; offsets, index and rows change between
+    replays, within the sizes."""
+    g = gen(31)
+    n, K, N, E, T = 600, 576, 200, 6, 90
+    w, w64, _ = weight(g, fmt, E, N, K)
+    d, d64, _ = weight(g, fmt, N, K)
+    x, ts = rand(g, T, K), (torch.tensor([0.002], device="cuda") if fmt else None)
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    index = torch.zeros(n, dtype=torch.int32, device="cuda")
+    y = torch.zeros(n, N, dtype=torch.bfloat16, device="cuda")
+    z = torch.zeros(T, N, dtype=torch.bfloat16, device="cuda")
+    ws, wd = eg.mx4_workspace(n, w, "cuda"), eg.mx4_workspace(T, d, "cuda")
+
+    def call():
+        eg.mx4_linear(x, d, tensor_scale=ts, out=z, workspace=wd)
+        eg.mx4_linear_ragged(x, off, w, index=index, tensor_scale=ts, out=y, workspace=ws)
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for counts in ([100] * 6, [0, 0, 600, 0, 0, 0], [3, 0, 1, 250, 0, 90], [0] * 6):
+        x.copy_(rand(g, T, K))
+        off.copy_(torch.tensor([0] + counts).cumsum(0))
+        index.copy_(torch.randint(0, T, (n,), generator=g, device="cuda"))
+        y.fill_(3.0)
+        graph.replay()
+        a = rows64(x, K, fmt, ts)
+        check(z, a, d64)
+        lo = 0
+        for e, c in enumerate(counts):
+            if c:
+                check(y[lo:lo + c], a[index[lo:lo + c].long()], w64[e])
+            lo += c
+        assert (y[lo:] == 3.0).all()
+    assert eg.device_status() == 0
+
+
+def test_two_calls_at_once_and_results_that_do_not_depend_on_timing():
+    g = gen(32)
+    w, _, _ = weight(g, 0, 1500, 4096)
+    xs = [rand(g, m, 4096) for m in (1, 3, 70, 400)]
+    want = [eg.mx4_linear(x, w) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for x, s in zip(xs, streams):
+            got.append(eg.mx4_linear(x, w, stream=s))
+    torch.cuda.synchronize()
+    for i, y in enumerate(got):
+        assert torch.equal(y, want[i % len(xs)])
+    assert eg.device_status() == 0
+
+
+def test_smaller_batches_share_a_workspace():
+    g = gen(33)
+    w, w64, _ = weight(g, 0, 3, 130, 320)
+    ws = eg.mx4_workspace(500, w, "cuda")
+    for counts in ([200, 100, 200], [0, 3, 0], [64, 65, 1], [1, 1, 1]):
+        n = sum(counts)
+        x = rand(g, n, 320)
+        off = torch.tensor([0] + counts, device="cuda").cumsum(0)
+        y = eg.mx4_linear_ragged(x, off.int(), w, workspace=ws)
+        a = rows64(x, 320, 0, None)
+        for e in range(3):
+            if counts[e]:
+                check(y[off[e]:off[e + 1]], a[off[e]:off[e + 1]], w64[e])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_output_past_2_31_values(fmt):
+    """65,600 rows of 33,000 columns: places past 2^31, checked in the last rows."""
+    g = gen(34)
+    M, N, K = 65600, 33000, 64
+    x = rand(g, M, K)
+    w, w64, _ = weight(g, fmt, N, K)
+    y = eg.mx4_linear(x, w)
+    for rows in (slice(0, 3), slice(M - 40, M)):
+        check(y[rows], rows64(x[rows], K, fmt, None), w64)
+
+
+def test_experts_of_a_layer():
+    """The run of a layer: route, rows sorted by expert, gate and up, gated down, sum."""
+    g = gen(35)
+    T, E, k, H, I = 75, 8, 3, 288, 160
+    x = rand(g, T, H)
+    gate_up, gu64, _ = weight(g, 0, E, 2 * I, H)
+    down, d64, _ = weight(g, 0, E, H, I)
+    weights, ids = eg.moe_route(rand(g, T, E, dtype=torch.float32), k)
+    key, order = torch.sort(ids.view(-1), stable=True)
+    off = torch.searchsorted(key, torch.arange(E + 1, device="cuda", dtype=torch.int32)).int()
+    token = (order // k).int()
+    h = eg.mx4_linear_ragged(x, off, gate_up, index=token)
+    out = eg.mx4_linear_ragged(h, off, down, gated=True)
+    y = torch.zeros(T, H, device="cuda").index_add_(
+        0, token.long(), out.float() * weights.view(-1)[order][:, None])
+    # each product against 64 bits from what it was given
+    a, b = rows64(x, H, 0, None)[token.long()], rows64(h, I, 0, None, gated=True)
+    want = torch.zeros(T, H, dtype=torch.float64, device="cuda")
+    for e in range(E):
+        lo, hi = int(off[e]), int(off[e + 1])
+        if lo < hi:
+            check(h[lo:hi], a[lo:hi], gu64[e])
+            check(out[lo:hi], b[lo:hi], d64[e])
+    want.index_add_(0, token.long(), out.double() * weights.view(-1)[order].double()[:, None])
+    assert ((y.double() - want).abs() <= 8 * 2.0 ** -24 * out.double().abs().max()).all()
 
 
 def test_ragged_without_rows():
