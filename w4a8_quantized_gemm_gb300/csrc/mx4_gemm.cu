@@ -20,7 +20,7 @@ namespace {
 constexpr int kBT = 64;       // rows of a tile at most
 constexpr int kEpiWarps = 4;  // one for each 32 lanes of Tensor Memory
 constexpr int kMmaWarp = kEpiWarps, kWeightWarp = kMmaWarp + 1, kRowWarp = kMmaWarp + 2;
-constexpr int kThreads = (kRowWarp + 1) * 32;
+constexpr int kExtraWarps = 4;  // beside the epilogue's, where rows are quantized here
 constexpr int kMaxSplit = 8;  // CTAs that share a unit's K, a cluster
 
 // Rows that the kernel quantizes itself (XT their type; kNone: they come as records):
@@ -29,13 +29,23 @@ constexpr int kMaxSplit = 8;  // CTAs that share a unit's K, a cluster
 // leaves out a kernel and the wait for its results.
 constexpr int kNone = -1;
 constexpr int kOwnRows = 16;             // at most
-constexpr int kOwnRuns = 64;             // runs of 256 values a CTA, at most
+// Runs of 256 values a CTA, at most. Calls that quantize so / apart, us, behind one
+// another in a graph (outside of one, where the host's time counts, a launch less is 2
+// us less):
+//   18944 x 3584   1 row (7 runs) 8.8 / 11.3   8 (56) 11.3 / 12.1   12 (84) 12.8 / 12.5
+//     gated        1 (7) 9.0 / 11.3   4 (28) 10.9 / 11.7   6 (42) 13.8 / 12.0
+//   3584 x 18944   1 (10) 9.5 / 11.7   6 (60) 11.7 / 11.8   8 (80) 12.1 / 11.8
+//     gated        1 (10) 10.8 / 11.7   2 (20) 11.5 / 11.7   4 (40) 12.4 / 12.2
+//   3584 x 3584    1 (2) 5.8 / 6.5   8 (16) 6.8 / 6.7   16 (32) 8.5 / 7.4
+constexpr int kOwnRuns = 64, kOwnGatedRuns = 32;
 constexpr int kOwnBytes = 40960;         // codes and scales, at most
 
 // Two CTAs share an SM, so that one's loads cover the other's ends.
 template <int FMT, int XT>
 struct Cfg {
   static constexpr bool kOwn = XT != kNone;
+  static constexpr int kQuantWarps = kEpiWarps + kExtraWarps;
+  static constexpr int kThreads = (kRowWarp + 1 + (kOwn ? kExtraWarps : 0)) * 32;
   static constexpr int kRec = mx4_record_bytes(FMT);
   static constexpr int kScale = kRec - kMx4Codes;
   static constexpr int kAtoms = kScale / 512;  // of a K block and 128 rows
@@ -66,7 +76,8 @@ struct Unit {
 
 // x: the rows, where the kernel quantizes them (GATED: [gate | up]); p.operand else.
 template <int FMT, int XT, bool GATED>
-__global__ void __launch_bounds__(kThreads, 2) mx4_few_kernel(const Mx4Params p, const void* x) {
+__global__ void __launch_bounds__(Cfg<FMT, XT>::kThreads, 2)
+    mx4_few_kernel(const Mx4Params p, const void* x) {
   using C = Cfg<FMT, XT>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
@@ -99,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_few_kernel(const Mx4Params p,
       mbar_init(free_acc(b), kEpiWarps);
     }
     mbar_init(fin(), 1);
-    mbar_init(own(), kEpiWarps);
+    mbar_init(own(), C::kQuantWarps);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -172,6 +183,51 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_few_kernel(const Mx4Params p,
       mx4_wait(full(j % C::kStages), (j / C::kStages) & 1, &no_abort, tmo);
     }
   };
+  if constexpr (C::kOwn) {
+    // (the epilogue's warps and those behind the last role)
+    const int qw = warp < kEpiWarps ? warp : warp > kRowWarp ? warp - (kRowWarp + 1) + kEpiWarps : -1;
+    if (qw >= 0) {
+      griddep_wait();
+      if (threadIdx.x == 0) griddep_launch_dependents();
+      if (n_units > 0) {
+        // Runs of 256 values, two of a warp's on their way at a time.
+        constexpr int kAhead = 2, kLanes = mx4_block(FMT) / 8, kStep = C::kQuantWarps;
+        const bool scaled = p.a_scale != nullptr;
+        const float rg = scaled ? __fdiv_rn(1.f, __ldg(p.a_scale)) : 1.f;
+        const int64_t ld = GATED ? 2 * p.K : p.K;
+        const int runs = (int)p.M * kb_n;
+        for (int u0 = qw; u0 < runs; u0 += kStep * kAhead) {
+          Eight<XT> g8[kAhead], u8[kAhead];
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) {
+            const int u = u0 + j * kStep, row = u / kb_n, kb = u - row * kb_n;
+            const int64_t k = (int64_t)(kb0 + kb) * 256 + lane * 8;
+            g8[j].zero();
+            u8[j].zero();
+            if (u < runs && k < p.K) {
+              g8[j].load(x, row * ld + k);
+              if constexpr (GATED) u8[j].load(x, row * ld + p.K + k);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) {
+            const int u = u0 + j * kStep, row = u / kb_n, kb = u - row * kb_n;
+            if (u >= runs) break;
+            const int b = lane / kLanes;
+            RowOut out{};
+            out.rec = smem + kOwnAt + kb * 2048 + row * 128 + ((((lane >> 2) ^ row) & 7) << 4) +
+                      (lane & 3) * 4;
+            out.rec_scale = smem + kOwnAt + kb_n * 2048 + kb * C::kScale + (b >> 2) * 512 +
+                            row * 16 + (b & 3);
+            quant_unit<FMT, XT, GATED>(out, 0, g8[j], u8[j], true, scaled, rg);
+          }
+        }
+        fence_proxy_async_smem();  // (the tensor cores read what these threads wrote)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(own());
+      }
+    }
+  }
   if (warp == kWeightWarp) {
     // Weights need no wait: nothing that may still run in front of this kernel
     // writes them.
@@ -241,49 +297,9 @@ __global__ void __launch_bounds__(kThreads, 2) mx4_few_kernel(const Mx4Params p,
       volatile int no_abort = 0;
       mx4_wait_warp(fin(), 0, &no_abort, tmo);
     }
-  } else {
+  } else if (warp < kEpiWarps) {
     // ---------------------------------------------------------------- epilogue
     griddep_wait();
-    if constexpr (C::kOwn) {
-      if (threadIdx.x == 0) griddep_launch_dependents();
-      if (n_units > 0) {
-        // Runs of 256 values, four of a warp's on their way at a time.
-        constexpr int kAhead = 4, kLanes = mx4_block(FMT) / 8;
-        const bool scaled = p.a_scale != nullptr;
-        const float rg = scaled ? __fdiv_rn(1.f, __ldg(p.a_scale)) : 1.f;
-        const int64_t ld = GATED ? 2 * p.K : p.K;
-        const int runs = (int)p.M * kb_n;
-        for (int u0 = warp; u0 < runs; u0 += kEpiWarps * kAhead) {
-          Eight<XT> g8[kAhead], u8[kAhead];
-#pragma unroll
-          for (int j = 0; j < kAhead; ++j) {
-            const int u = u0 + j * kEpiWarps, row = u / kb_n, kb = u - row * kb_n;
-            const int64_t k = (int64_t)(kb0 + kb) * 256 + lane * 8;
-            g8[j].zero();
-            u8[j].zero();
-            if (u < runs && k < p.K) {
-              g8[j].load(x, row * ld + k);
-              if constexpr (GATED) u8[j].load(x, row * ld + p.K + k);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < kAhead; ++j) {
-            const int u = u0 + j * kEpiWarps, row = u / kb_n, kb = u - row * kb_n;
-            if (u >= runs) break;
-            const int b = lane / kLanes;
-            RowOut out{};
-            out.rec = smem + kOwnAt + kb * 2048 + row * 128 + ((((lane >> 2) ^ row) & 7) << 4) +
-                      (lane & 3) * 4;
-            out.rec_scale = smem + kOwnAt + kb_n * 2048 + kb * C::kScale + (b >> 2) * 512 +
-                            row * 16 + (b & 3);
-            quant_unit<FMT, XT, GATED>(out, 0, g8[j], u8[j], true, scaled, rg);
-          }
-        }
-        fence_proxy_async_smem();  // (the tensor cores read what these threads wrote)
-        __syncwarp();
-        if (lane == 0) mbar_arrive(own());
-      }
-    }
     bool ok = true;
     for (int k = 0; k < n_units && ok; ++k) {
       const Unit un = unit_at(k);
@@ -397,7 +413,7 @@ cudaError_t launch_few(const Mx4GemmArgs& a, const void* x, cudaStream_t st) {
   static SmemOptIn opt_in;
   if (cudaError_t e = opt_in.ensure(kern, smem); e != cudaSuccess) return e;
   PdlConfig c(dim3((unsigned)(p.split > 1 ? most * p.split : most < slots ? most : slots), 1, 1),
-              kThreads, smem, st);
+              C::kThreads, smem, st);
   cudaLaunchAttribute attr[2] = {c.attr[0], {}};
   if (p.split > 1) {
     attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -418,6 +434,32 @@ cudaError_t launch_own(const Mx4GemmArgs& a, const Mx4QuantArgs& q, cudaStream_t
                  : launch_few<FMT, kMx4F16, false>(a, q.x, st);
 }
 
+// Which kernel a product takes. One linear: by what each would take, in us, fitted to
+// the measurements below: a start, K blocks one after the other (with the columns of
+// a tile), and a split unit's sums.
+//   N x K          rows   this kernel / pairs
+//   3584 x 3584    64: 7.0 / 7.1   128: 8.2 / 7.8   192: 10.2 / 8.8
+//   18944 x 3584   17: 10.4 / 9.1  64: 14.2 / 9.3
+//   3584 x 18944   17: 9.9 / 24.6  192: 18.5 / 31.0  256: 24.4 / 26.4  384: 35.2 / 27.3
+//   50257 x 2048   17: 11.6 / 12.1  64: 13.5 / 12.7  128: 16.8 / 14.0
+//   512 x 3584     17: 4.0 / 6.9   512: 6.9 / 8.3
+// Ragged rows, whose sets only the device knows: by their mean. 64 sets of 2560 x
+// 3584, mean 32: 62.8 / 64.6, 64: 69.8 / 71.6, 96: 86.9 / 78.3; of 2048 x 1408, mean
+// 32: 29.8 / 31.4, 64: 34.4 / 33.9, 96: 43.6 / 37.5.
+bool takes_few(const Mx4GemmArgs& a, int sms) {
+  if (a.offsets) return a.M <= 64 * (int64_t)a.sets;
+  const int64_t kb = mx4_kblocks(a.K), units = few_units(a);
+  const int split = few_split(units, kb, sms);
+  const int64_t rounds = split > 1 ? 1 : (units + 2 * sms - 1) / (2 * sms);
+  const double rows = a.M < kBT ? (double)a.M : kBT;
+  const double few = 4.0 + (double)(rounds * ((kb + split - 1) / split)) * (0.45 + 0.002 * rows) +
+                     (split > 1 ? 0.15 * rows / split : 0.0);
+  const int64_t pair_units = (a.M + 255) / 256 * (((a.N + 127) / 128 + 1) / 2);
+  const int64_t pairs = sms / 2 > 0 ? sms / 2 : 1;
+  const double pair = 4.5 + 0.28 * (double)((pair_units + pairs - 1) / pairs * kb);
+  return few <= pair;
+}
+
 }  // namespace
 
 bool mx4_own_rows(const Mx4GemmArgs& a, const Mx4QuantArgs& q) {
@@ -426,7 +468,7 @@ bool mx4_own_rows(const Mx4GemmArgs& a, const Mx4QuantArgs& q) {
   if (sms < 1) return false;
   const int64_t kb = mx4_kblocks(a.K), split = few_split(few_units(a), kb, sms);
   const int64_t kb_most = (kb + split - 1) / split;
-  return a.M * kb_most <= kOwnRuns &&
+  return a.M * kb_most <= (q.gated ? kOwnGatedRuns : kOwnRuns) &&
          kb_most * (2048 + mx4_record_bytes(a.format) - kMx4Codes) <= kOwnBytes;
 }
 
@@ -436,7 +478,9 @@ cudaError_t launch_mx4_own(const Mx4GemmArgs& a, const Mx4QuantArgs& q, cudaStre
 }
 
 cudaError_t launch_mx4_gemm(const Mx4GemmArgs& a, cudaStream_t st) {
-  if (a.M > 64 * (int64_t)a.sets) return launch_mx4_pair(a, st);
+  const int sms = device_sm_count();
+  if (sms < 1) return cudaErrorInvalidConfiguration;
+  if (!takes_few(a, sms)) return launch_mx4_pair(a, st);
   return a.format == EGOPQ_MX4_E8M0 ? launch_few<EGOPQ_MX4_E8M0, kNone, false>(a, nullptr, st)
                                     : launch_few<EGOPQ_MX4_E4M3, kNone, false>(a, nullptr, st);
 }

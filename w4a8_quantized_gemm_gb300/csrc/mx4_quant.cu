@@ -25,7 +25,7 @@ struct QuantParams {
 // line. Bound by memory: all of a warp's loads are on their way before the first
 // is used; few rows take U = 1, so that more warps share them.
 template <int FMT, int TYPE, bool GATED, int U>
-__global__ void __launch_bounds__(kQuantWarps * 32, GATED ? 7 : 1) mx4_quant_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(kQuantWarps * 32, GATED ? 8 : 9) mx4_quant_kernel(const QuantParams p) {
   extern __shared__ int quant_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_wait();
