@@ -90,7 +90,7 @@ def test_codes_and_scales(fmt, dtype, M, K):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("scale", [1.0, 0.0117, 3.0e-5, 1000.0])
+@pytest.mark.parametrize("scale", [1.0, 0.0117, 3.0e-5, 1000.0, -0.02])
 def test_tensor_scale(dtype, scale):
     x = awkward(gen(2), 67, 480, dtype)
     ts = torch.tensor([scale], device="cuda")
@@ -284,6 +284,14 @@ def test_ragged(fmt, counts, N, K):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("sets,rows", [(1024, 700), (1024, 70000), (33, 31), (65, 65 * 64 + 1)])
+def test_many_sets(fmt, sets, rows):
+    g = torch.Generator().manual_seed(sets + rows)
+    counts = torch.bincount(torch.randint(0, sets, (rows,), generator=g), minlength=sets)
+    check_ragged(counts.tolist(), 24, 64, fmt)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_ragged_gathered_and_gated(fmt):
     check_ragged([9, 0, 150, 30], 257, 480, fmt, tokens=50)
     check_ragged([9, 0, 150, 30], 257, 480, fmt, tokens=300)
@@ -460,6 +468,28 @@ def test_experts_of_a_layer():
             check(out[lo:hi], b[lo:hi], d64[e])
     want.index_add_(0, token.long(), out.double() * weights.view(-1)[order].double()[:, None])
     assert ((y.double() - want).abs() <= 8 * 2.0 ** -24 * out.double().abs().max()).all()
+
+
+def test_debug_build_checks_weight_records(monkeypatch):
+    """Clean, and with the packed weight declared shorter than its buffer (the
+    redirected reads stay inside it)."""
+    monkeypatch.setattr(eg, "LIB_PATH", eg.DEBUG_LIB_PATH)
+    monkeypatch.setattr(eg, "_lib", None)
+    lib = eg.load()
+    try:
+        assert lib.egopq_debug_build() == 1
+        g = gen(36)
+        w, w64, _ = weight(g, 0, 300, 544)
+        for M in (2, 40, 200):
+            x = rand(g, M, 544)
+            check(eg.mx4_linear(x, w), rows64(x, 544, 0, None), w64)
+            assert eg.device_status() == 0
+        lib.egopq_debug_set_record_limit(2 * 17408)
+        eg.mx4_linear(rand(g, 2, 544), w)
+        assert eg.device_status() == -7
+    finally:
+        lib.egopq_debug_set_record_limit(0)
+        eg.device_status()
 
 
 def test_ragged_without_rows():

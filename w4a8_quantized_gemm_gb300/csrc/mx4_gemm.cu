@@ -234,7 +234,11 @@ __global__ void __launch_bounds__(Cfg<FMT, XT>::kThreads, 2)
     if (lane == 0)
       produce([&](const Unit&) { return (uint32_t)C::kRec; },
               [&](const Unit& x, int kb, uint32_t to, uint32_t bar) {
-                bulk_load(to, x.w + (int64_t)kb * C::kRec, C::kRec, bar);
+                const uint8_t* rec = x.w + (int64_t)kb * C::kRec;
+                if (!dbg_record_ok((uint64_t)(rec - p.packed), C::kRec,
+                                   (uint64_t)p.sets * p.nb * p.kb * C::kRec))
+                  rec = p.packed;
+                bulk_load(to, rec, C::kRec, bar);
               });
   } else if (warp == kRowWarp) {
     if (!C::kOwn && lane == 0) {
@@ -407,8 +411,11 @@ cudaError_t launch_few(const Mx4GemmArgs& a, const void* x, cudaStream_t st) {
   p.split = few_split(most, p.kb, sms);
   const int64_t slots = 2 * sms;
   const int kb_most = (p.kb + p.split - 1) / p.split;
-  const size_t smem = C::kMiscAt + (C::kOwn ? 1024 + kb_most * (2048 + C::kScale)
-                                            : C::kMisc + 3 * (size_t)(a.sets + 1) * sizeof(int));
+  size_t smem = C::kMiscAt + (C::kOwn ? 1024 + kb_most * (2048 + C::kScale)
+                                      : C::kMisc + 3 * (size_t)(a.sets + 1) * sizeof(int));
+  // Never three CTAs an SM, which Tensor Memory holds two of: the third's wait for it
+  // and a cluster's for its other CTAs could wait for one another.
+  if (smem < 80 * 1024) smem = 80 * 1024;
   auto kern = mx4_few_kernel<FMT, XT, GATED>;
   static SmemOptIn opt_in;
   if (cudaError_t e = opt_in.ensure(kern, smem); e != cudaSuccess) return e;
@@ -486,5 +493,8 @@ cudaError_t launch_mx4_gemm(const Mx4GemmArgs& a, cudaStream_t st) {
 }
 
 cudaError_t take_error_word_mx4_gemm(unsigned* out) { return take_local_error_word(out); }
+cudaError_t set_record_limit_mx4_gemm(unsigned long long bytes) {
+  return set_local_record_limit(bytes);
+}
 
 }  // namespace egopq

@@ -123,7 +123,7 @@ __device__ __forceinline__ float gated32(float g, float u) {
 // the way to v = h * r (zeros are exact).
 __device__ __forceinline__ bool gated_weak(float g, float u, float v, float r) {
   return g != 0.f && u != 0.f &&
-         (g < -32.f || fabsf(v) < 0x1p-100f || fabsf(v) < 0x1p-100f * r);
+         (g < -32.f || fabsf(v) < 0x1p-100f || fabsf(v) < 0x1p-100f * fabsf(r));
 }
 static __device__ __noinline__ double gated64(float g, float u, float r) {
   return (double)g / (1.0 + exp(-(double)g)) * (double)u * (double)r;
@@ -168,12 +168,12 @@ __device__ __forceinline__ void quant_unit(const RowOut& out, int i_run, const E
   float most;  // the block's largest magnitude (a NaN is)
   g8.values(g);
   if constexpr (!GATED && TYPE != kMx4F32) {
-    // (of the stored patterns: the product with r keeps their order)
+    // (of the stored patterns: the product with |r| keeps their order)
     uint32_t top = g8.top16();
 #pragma unroll
     for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     most = Eight<TYPE>::of16(top);
-    if (FMT == kE4M3 && scaled) most *= r;
+    if (FMT == kE4M3 && scaled) most = fabsf(most * r);
   }
   if constexpr (GATED) {
     u8.values(u);
