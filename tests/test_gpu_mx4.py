@@ -296,16 +296,19 @@ def test_ragged_gathered_and_gated(fmt):
     check_ragged([9, 0, 150, 30], 257, 480, fmt, tokens=50)
     check_ragged([9, 0, 150, 30], 257, 480, fmt, tokens=300)
     # many from few: quantized once, gathered in 4 bits
-    check_ragged([9, 0, 8000, 300, 33], 130, 1056, fmt, tokens=1900, before=2, after=1)
-    check_ragged([4, 9000, 0, 30], 33, 960, fmt, tokens=11, gated=True, before=2, after=1)
+    check_ragged([9, 0, 11900, 300, 33], 130, 1056, fmt, tokens=1900, before=2, after=1)
+    check_ragged([4, 2900, 0, 30], 33, 4512, fmt, tokens=11, gated=True, before=2, after=1)
     check_ragged([9, 0, 150, 30], 257, 480, fmt, gated=True)
     check_ragged([2, 0, 3], 64, 96, fmt, before=4, after=130)
     check_ragged([2, 0, 3], 64, 96, fmt, before=1, after=2, tokens=3, gated=True,
                  dtype=torch.float16)
+    for counts in ([0, 1, 0, 1, 1, 0], [16], [1] * 8):
+        check_ragged(counts, 300, 1056, fmt, tokens=2)
+        check_ragged(counts, 300, 1056, fmt, gated=True, before=1, dtype=torch.float32)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("tokens,n,K", [(6, 20, 96), (20, 20, 96), (30, 8192, 1056)])
+@pytest.mark.parametrize("tokens,n,K", [(6, 20, 96), (20, 20, 96), (30, 12300, 1056)])
 def test_index_outside_reads_zeros(fmt, tokens, n, K):
     g = gen(23)
     x = rand(g, tokens, K)

@@ -78,10 +78,10 @@ int launched(cudaError_t e, const char* what) {
 
 // Many rows gathered from at most a quarter as many are quantized once and gathered
 // in 4 bits. Directly / so, us, whole calls of 32 sets: 8192 rows from 1024, K 3584,
-// 28.5 / 24.7 (E4M3 34.1 / 25.6), from 4096 29.0 / 29.8; K 1024, from 1024, 14.1 /
-// 14.3 (15.5 / 14.9); 2048 rows from 256, K 3584, 18.9 / 19.1 (20.4 / 20.0).
+// 28.5 / 21.7 (E4M3 34.1 / 24.6), 4096 from 512 19.9 / 16.8 (22.6 / 17.8); K 1024,
+// 8192 from 1024, 14.1 / 15.6 (15.5 / 16.3).
 bool gathers(int64_t rows, int64_t x_rows, int64_t K) {
-  return x_rows <= rows / 4 && rows * K >= (1 << 23);
+  return x_rows <= rows / 4 && rows * K >= (3 << 22);
 }
 // Codes and scales of that many, behind the operand (a multiple of 16 bytes each).
 size_t gather_bytes(int64_t x_rows, int64_t K, int format) {

@@ -159,8 +159,9 @@ cudaError_t launch_quant_type(const Mx4QuantArgs& a, cudaStream_t st) {
 
 // ---- rows gathered in 4 bits ---------------------------------------------------------
 // Ragged rows that are gathered from fewer: each was quantized once, and this moves
-// codes and scales to their places among the records. A warp takes four K blocks of
-// a row, 16 bytes a lane; memory (L2, as to what is read) bounds it.
+// codes and scales to their places among the records. A warp takes a row, sixteen K
+// blocks at a time, 16 bytes a lane and four of them on their way; memory (L2, as to
+// what is read) bounds it.
 template <int FMT>
 __global__ void __launch_bounds__(256) mx4_gather_kernel(const QuantParams p) {
   extern __shared__ int quant_smem[];
@@ -171,45 +172,54 @@ __global__ void __launch_bounds__(256) mx4_gather_kernel(const QuantParams p) {
   if (warp == 0) mx4_scan_sets(p.offsets, p.sets, p.M, 128, first, block, nullptr);
   __syncthreads();
   constexpr int kPer = 256 / mx4_block(FMT), kWords = kPer / 4;  // scales of a K block
-  const int64_t stride = (int64_t)gridDim.x * 8, at0 = (int64_t)blockIdx.x * 8 + warp;
-  const int64_t rows_end = first[p.sets];
-  const int64_t row_step = stride / p.groups;
-  const int group_step = (int)(stride - row_step * p.groups);
-  int64_t row = first[0] + at0 / p.groups;
-  int group = (int)(at0 % p.groups);
-  const int blocks = (int)(p.K / mx4_block(FMT));
-  while (row < rows_end) {
+  constexpr int kRec = mx4_record_bytes(FMT);
+  const int rows_end = first[p.sets], blocks = (int)(p.K / mx4_block(FMT));
+  const int chunk = lane & 7, word = lane % kWords;
+  for (int64_t row = first[0] + (int64_t)blockIdx.x * 8 + warp; row < rows_end;
+       row += (int64_t)gridDim.x * 8) {
     const int64_t src = __ldg(p.index + row);
     const bool have = src >= 0 && src < p.x_rows;
-    const int kb = group * 4 + (lane >> 3), chunk = lane & 7;
-    uint4 c = make_uint4(0, 0, 0, 0);
-    if (have && (int64_t)kb * 256 + chunk * 32 < p.K)
-      c = *reinterpret_cast<const uint4*>(p.codes + src * (p.K / 2) + kb * 128 + chunk * 16);
-    // a lane's word of four scales
-    const int kb_s = group * 4 + lane / kWords, word = lane % kWords;
-    uint32_t w = 0;
-    if (lane < 4 * kWords && have) {
-      const int b = kb_s * kPer + word * 4;
-      const uint8_t* from = p.scales + src * blocks + b;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (b + i < blocks) w |= (uint32_t)from[i] << (8 * i);
-    }
     const int e = mx4_find_set(first, p.sets, (int)row);
     const int64_t at = (int64_t)block[e] * 128 + (row - first[e]);
-    uint8_t* rec = p.operand + (at >> 7) * p.kb * mx4_record_bytes(FMT);
     const int q = (int)(at & 127);
-    if (kb < p.kb)
-      *reinterpret_cast<uint4*>(rec + (int64_t)kb * mx4_record_bytes(FMT) + q * 128 +
-                                ((chunk ^ q) & 7) * 16) = c;
-    if (lane < 4 * kWords && kb_s < p.kb)
-      *reinterpret_cast<uint32_t*>(rec + (int64_t)kb_s * mx4_record_bytes(FMT) + kMx4Codes +
-                                   word * 512 + (q & 31) * 16 + (q >> 5) * 4) = w;
-    row += row_step;
-    group += group_step;
-    if (group >= p.groups) {
-      group -= p.groups;
-      ++row;
+    uint8_t* rec = p.operand + (at >> 7) * p.kb * kRec;
+    const uint8_t* codes = p.codes + src * (p.K / 2);
+    const uint8_t* scales = p.scales + src * blocks;
+    for (int kb0 = 0; kb0 < p.kb; kb0 += 16) {
+      uint4 c[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int kb = kb0 + 4 * j + (lane >> 3);
+        c[j] = make_uint4(0, 0, 0, 0);
+        if (have && (int64_t)kb * 256 + chunk * 32 < p.K)
+          c[j] = *reinterpret_cast<const uint4*>(codes + kb * 128 + chunk * 16);
+      }
+      // a lane's words of four scales: of 32 / kWords K blocks at a time
+      uint32_t w[kWords / 2];
+#pragma unroll
+      for (int j = 0; j < kWords / 2; ++j) {
+        const int b = (kb0 + j * (32 / kWords) + lane / kWords) * kPer + word * 4;
+        w[j] = 0;
+        if (have) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (b + i < blocks) w[j] |= (uint32_t)scales[b + i] << (8 * i);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int kb = kb0 + 4 * j + (lane >> 3);
+        if (kb < p.kb)
+          *reinterpret_cast<uint4*>(rec + (int64_t)kb * kRec + q * 128 + ((chunk ^ q) & 7) * 16) =
+              c[j];
+      }
+#pragma unroll
+      for (int j = 0; j < kWords / 2; ++j) {
+        const int kb = kb0 + j * (32 / kWords) + lane / kWords;
+        if (kb < p.kb)
+          *reinterpret_cast<uint32_t*>(rec + (int64_t)kb * kRec + kMx4Codes + word * 512 +
+                                       (q & 31) * 16 + (q >> 5) * 4) = w[j];
+      }
     }
   }
 }
@@ -227,10 +237,9 @@ cudaError_t launch_gather(const Mx4QuantArgs& a, cudaStream_t st) {
   p.x_rows = a.x_rows;
   p.sets = a.sets;
   p.kb = (int)mx4_kblocks(a.K);
-  p.groups = (p.kb + 3) / 4;
   const int sms = device_sm_count();
   if (sms < 1) return cudaErrorInvalidConfiguration;
-  const int64_t blocks = (a.M * p.groups + 7) / 8, most = (int64_t)sms * 8;
+  const int64_t blocks = (a.M + 7) / 8, most = (int64_t)sms * 8;
   PdlConfig c(dim3((unsigned)(blocks < most ? blocks : most), 1, 1), 256,
               2 * (size_t)(a.sets + 1) * sizeof(int), st);
   return cudaLaunchKernelEx(&c.cfg, mx4_gather_kernel<FMT>, p);
