@@ -504,3 +504,35 @@ def test_ragged_without_rows():
     assert eg.mx4_linear_ragged(x[:0], torch.zeros(5, dtype=torch.int32, device="cuda"),
                                 w).shape == (0, 64)
     assert eg.device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_tensors_elsewhere_and_weights_too_short_are_refused(fmt):
+    # (a weight put together by hand, or moved to the host with its fields)
+    g = gen(23)
+    w, _, _ = weight(g, fmt, 40, 64)
+    many, _, _ = weight(g, fmt, 2, 40, 64)
+    x, off = rand(g, 6, 64), torch.tensor([0, 2, 6], dtype=torch.int32, device="cuda")
+    rows = eg.mx4_quant(x, fmt)
+    bad = lambda t: [t._replace(packed=t.packed.cpu()), t._replace(packed=t.packed[:-16])]  # noqa: E731
+    for v in bad(w):
+        for call in (lambda: eg.mx4_linear(x, v), lambda: eg.mx4_gemm(rows, v),
+                     lambda: eg.mx4_unpack(v)):
+            with pytest.raises(ValueError, match="tensor (on|must be on)|needed"):
+                call()
+    for v in bad(many):
+        with pytest.raises(ValueError, match="tensor on|needed"):
+            eg.mx4_linear_ragged(x, off, v)
+    y = torch.empty(6, 40, dtype=torch.bfloat16)
+    ws = eg.mx4_workspace(6, many, "cuda").cpu()
+    for call in (lambda: eg.mx4_linear(x, w, out=y), lambda: eg.mx4_linear(x, w, workspace=ws),
+                 lambda: eg.mx4_linear_ragged(x, off.cpu(), many),
+                 lambda: eg.mx4_linear_ragged(x, off, many, index=torch.zeros(6, dtype=torch.int32)),
+                 lambda: eg.mx4_linear_ragged(x, off, many, workspace=ws),
+                 lambda: eg.mx4_gemm(rows, w, out=y),
+                 lambda: eg.mx4_gemm(rows._replace(a_tc=rows.a_tc.cpu()), w),
+                 lambda: eg.mx4_dequant(rows._replace(scales=rows.scales.cpu())),
+                 lambda: eg.mx4_quant(x, fmt, out=rows._replace(codes=rows.codes.cpu()))):
+        with pytest.raises(ValueError, match="tensor (on|must be on)"):
+            call()
+    assert eg.device_status() == 0

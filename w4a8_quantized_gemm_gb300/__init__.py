@@ -19,6 +19,7 @@ has waited for `stream`.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 import threading
@@ -712,11 +713,28 @@ def mx4_block(fmt: int) -> int:
     return block
 
 
-def _mx4_here(t: torch.Tensor):
-    """Kernels run on the current device: a tensor of another is refused."""
-    if t.is_cuda and t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"tensor on {t.device}, the current device is "
-                         f"{torch._C._cuda_getDevice()}")
+def _mx4_here(first: torch.Tensor, *others) -> int:
+    """The current device, which the kernels run on: a tensor of another, or of
+    none, is refused (None is not)."""
+    if not first.is_cuda:
+        raise ValueError("tensor must be on a CUDA device")
+    device = torch._C._cuda_getDevice()
+    for t in (first, *others):
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"tensor on {t.device}, the current device is {device}")
+    return device
+
+
+def _mx4_at(t: torch.Tensor) -> int:
+    """The address of a tensor that is on the device."""
+    if not t.is_contiguous():
+        raise ValueError("tensor must be contiguous")
+    return t.data_ptr()
+
+
+def _mx4_stream(stream, device: int) -> int:
+    return (torch._C._cuda_getCurrentRawStream(device) if stream is None
+            else stream.cuda_stream)
 
 
 def _mx4_type(dtype: torch.dtype) -> int:
@@ -729,9 +747,9 @@ def _mx4_type(dtype: torch.dtype) -> int:
 def _mx4_scale(t: Optional[torch.Tensor], n: int) -> Optional[int]:
     if t is None:
         return None
-    if t.dim() == 0 and n == 1:
-        t = t.reshape(1)
-    return _arg(t, torch.float32, n)
+    if t.dtype is torch.float32 and t.shape == (n,) and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    return _arg(t.reshape(1) if n == 1 and t.dim() == 0 else t, torch.float32, n)
 
 
 class Mx4Rows(NamedTuple):
@@ -757,6 +775,20 @@ class Mx4Weight(NamedTuple):
     tensor_scale: Optional[torch.Tensor]
 
 
+@functools.lru_cache(maxsize=None)
+def _mx4_packed_bytes(sets: int, N: int, K: int, fmt: int) -> int:
+    return int(load().egopq_mx4_packed_bytes(sets or 1, N, K, fmt))
+
+
+def _mx4_packed(weight: Mx4Weight) -> int:
+    """The records' address, of a weight that may have been put together by hand."""
+    packed, sets, N, K, fmt, _ = weight
+    need = _mx4_packed_bytes(sets, N, K, fmt)
+    if packed.nbytes < need:
+        raise ValueError(f"packed of {packed.nbytes} bytes, {need} needed")
+    return _mx4_at(packed)
+
+
 def mx4_quant(x: torch.Tensor, fmt: int = MX4_E8M0, tensor_scale: Optional[torch.Tensor] = None,
               gated: bool = False, with_codes: bool = True, with_tc: bool = True,
               out: Optional[Mx4Rows] = None, stream=None) -> Mx4Rows:
@@ -766,7 +798,6 @@ def mx4_quant(x: torch.Tensor, fmt: int = MX4_E8M0, tensor_scale: Optional[torch
     scales, with_tc the form that mx4_gemm reads. `out`: rows of an earlier call of
     the same sizes."""
     block, kind = mx4_block(fmt), _mx4_type(x.dtype)
-    _mx4_here(x)
     M, K = x.shape
     if gated:
         if K % 2:
@@ -791,10 +822,11 @@ def mx4_quant(x: torch.Tensor, fmt: int = MX4_E8M0, tensor_scale: Optional[torch
                              f"{M} x {K} of {fmt}")
         _mx4_rows_check(out)
         codes, scales, a_tc = out.codes, out.scales, out.a_tc
+        _mx4_here(x, codes, scales, a_tc)
         out = out._replace(tensor_scale=tensor_scale)
-    # (what the call made itself needs no look)
+    _mx4_here(x, tensor_scale)  # (what the call made itself needs no look)
     _check(lib.egopq_mx4_quant(
-        _ptr(x), kind, M, K, fmt, None if tensor_scale is None else _mx4_scale(tensor_scale, 1),
+        _mx4_at(x), kind, M, K, fmt, None if tensor_scale is None else _mx4_scale(tensor_scale, 1),
         gated, None if codes is None else codes.data_ptr(),
         None if scales is None else scales.data_ptr(),
         None if a_tc is None else a_tc.data_ptr(), _stream(stream)))
@@ -822,7 +854,7 @@ def mx4_dequant(rows: Mx4Rows, dtype: torch.dtype = torch.bfloat16,
     codes, scales, _, M, K, fmt, tensor_scale = rows
     if codes is None or scales is None:
         raise ValueError("rows without codes and scales (with_codes=False)")
-    _mx4_here(codes)
+    _mx4_here(codes, scales, tensor_scale, out)
     c = _arg(codes, torch.uint8, M, K // 2)
     s = _arg(scales, torch.uint8, M, K // mx4_block(fmt))
     if out is None:
@@ -849,7 +881,7 @@ def mx4_pack(codes: torch.Tensor, scales: torch.Tensor, fmt: int = MX4_E8M0,
         raise EgopqError(-1, "E8M0 blocks have no tensor scale")
     if tensor_scale is not None:
         _mx4_scale(tensor_scale, max(sets, 1))
-    _mx4_here(codes)
+    _mx4_here(codes, scales, tensor_scale)
     c = _arg(codes, torch.uint8, *lead, N, K // 2)
     s = _arg(scales, torch.uint8, *lead, N, K // block)
     packed = _output((nbytes,), torch.uint8, codes.device, stream)
@@ -862,10 +894,11 @@ def mx4_unpack(weight: Mx4Weight, stream=None) -> tuple:
     """(codes, scales) of a packed weight, as mx4_pack took them."""
     packed, sets, N, K, fmt, _ = weight
     _mx4_here(packed)
+    at = _mx4_packed(weight)
     lead, dev = ((sets,) if sets else ()), packed.device
     codes = _output((*lead, N, K // 2), torch.uint8, dev, stream)
     scales = _output((*lead, N, K // mx4_block(fmt)), torch.uint8, dev, stream)
-    _check(load().egopq_mx4_unpack(_ptr(packed), max(sets, 1), N, K, fmt, _ptr(codes),
+    _check(load().egopq_mx4_unpack(at, max(sets, 1), N, K, fmt, _ptr(codes),
                                    _ptr(scales), _stream(stream)))
     return codes, scales
 
@@ -880,11 +913,12 @@ def mx4_gemm(rows: Mx4Rows, weight: Mx4Weight, dtype: torch.dtype = torch.bfloat
         raise ValueError(f"rows of K={rows.K} format {rows.fmt}, a weight of K={K} format {fmt}")
     if rows.a_tc is None:
         raise ValueError("rows without the products' form (with_tc=False)")
-    _mx4_here(packed)
+    _mx4_here(packed, rows.a_tc, rows.tensor_scale, w_scale, out)
     _mx4_rows_check(rows)
+    at = _mx4_packed(weight)
     if out is None:
         out = _output((rows.M, N), dtype, packed.device, stream)
-    _check(load().egopq_mx4_gemm(_ptr(rows.a_tc), _ptr(packed), _mx4_scale(rows.tensor_scale, 1),
+    _check(load().egopq_mx4_gemm(_ptr(rows.a_tc), at, _mx4_scale(rows.tensor_scale, 1),
                                  _mx4_scale(w_scale, 1), rows.M, N, K, fmt, _mx4_type(out.dtype),
                                  _arg(out, out.dtype, rows.M, N), _stream(stream)))
     return out
@@ -902,7 +936,6 @@ def _mx4_input(x: torch.Tensor, K: int, gated: bool) -> tuple:
     shape = x.shape
     if len(shape) != 2 or shape[1] != (2 * K if gated else K):
         raise ValueError(f"x of shape {tuple(shape)} for {'gated ' if gated else ''}K = {K}")
-    _mx4_here(x)
     return shape[0], _mx4_type(x.dtype)
 
 
@@ -921,12 +954,14 @@ def mx4_linear(x: torch.Tensor, weight: Mx4Weight, tensor_scale: Optional[torch.
         out = _output((M, N), dtype or x.dtype, x.device, stream)
     if workspace is None:
         workspace = mx4_workspace(M, weight, x.device, stream)
-    y_type = out.dtype
+    device = _mx4_here(x, packed, out, workspace, tensor_scale, w_scale)
+    at, y_type = _mx4_packed(weight), out.dtype
     _check(load().egopq_mx4_linear(
-        _ptr(x), x_type, M, N, K, gated,
-        None if tensor_scale is None else _mx4_scale(tensor_scale, 1), packed.data_ptr(),
+        _mx4_at(x), x_type, M, N, K, gated,
+        None if tensor_scale is None else _mx4_scale(tensor_scale, 1), at,
         None if w_scale is None else _mx4_scale(w_scale, 1), fmt, _mx4_type(y_type),
-        _arg(out, y_type, M, N), _ptr(workspace), workspace.nbytes, _stream(stream)))
+        _arg(out, y_type, M, N), _mx4_at(workspace), workspace.nbytes,
+        _mx4_stream(stream, device)))
     return out
 
 
@@ -949,13 +984,15 @@ def mx4_linear_ragged(x: torch.Tensor, offsets: torch.Tensor, weight: Mx4Weight,
         out = _output((rows, N), dtype or x.dtype, x.device, stream)
     if workspace is None:
         workspace = mx4_workspace(rows, weight, x.device, stream)
-    y_type = out.dtype
+    device = _mx4_here(x, packed, out, workspace, offsets, index, tensor_scale, w_scale)
+    at, y_type = _mx4_packed(weight), out.dtype
     _check(load().egopq_mx4_linear_ragged(
-        _ptr(x), x_type, x_rows, None if index is None else _arg(index, torch.int32, rows),
+        _mx4_at(x), x_type, x_rows, None if index is None else _arg(index, torch.int32, rows),
         _arg(offsets, torch.int32, sets + 1), rows, sets, N, K, gated,
-        None if tensor_scale is None else _mx4_scale(tensor_scale, 1), packed.data_ptr(),
+        None if tensor_scale is None else _mx4_scale(tensor_scale, 1), at,
         None if w_scale is None else _mx4_scale(w_scale, sets), fmt, _mx4_type(y_type),
-        _arg(out, y_type, rows, N), _ptr(workspace), workspace.nbytes, _stream(stream)))
+        _arg(out, y_type, rows, N), _mx4_at(workspace), workspace.nbytes,
+        _mx4_stream(stream, device)))
     return out
 
 
