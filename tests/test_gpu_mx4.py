@@ -195,6 +195,27 @@ def test_linear(fmt, M, N, K):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,N,K", [(250, 4112, 1376), (1150, 2192, 1056), (1000, 20480, 96),
+                                   (510, 20640, 288), (1150, 2200, 1056)])
+def test_many_rows(fmt, dtype, M, N, K):
+    """Tiles of rows by weights and of weights by rows (N no multiple of 16, or y off
+    a boundary of 32 bytes): odd blocks of rows, last tiles of 16, 144 and 160."""
+    g = gen(M + N)
+    x = rand(g, M, K, dtype=dtype)
+    w, w64, _ = weight(g, fmt, N, K)
+    ts = tscale(x, fmt)
+    a64 = rows64(x, K, fmt, ts)
+    room = torch.full((M * N + 32,), 7.0, dtype=dtype, device="cuda")
+    for at in (0, 16 // room.element_size()):
+        y = room[at: at + M * N].view(M, N)
+        eg.mx4_linear(x, w, tensor_scale=ts, out=y)
+        check(y, a64, w64)
+        assert (room[at + M * N:] == 7.0).all()
+    assert eg.device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("x_type", TYPES)
 @pytest.mark.parametrize("y_type", TYPES)
 def test_types(fmt, x_type, y_type):

@@ -106,19 +106,19 @@ __device__ __forceinline__ void store16(const Mx4Params& p, const Unit& un, int 
   if (p.type != kMx4F32 && (p.N & 1) == 0) {
     uint16_t* y = static_cast<uint16_t*>(p.y) + (un.row0 + c + (odd ? 1 : 0)) * p.N + (n & ~1);
     const bool in = n < p.N;
+    const uint32_t take = odd ? 0x3276u : 0x5410u;  // (of this lane's two values and the other's)
 #pragma unroll
     for (int q = 0; q < 16; q += 2) {
       const float v0 = __uint_as_float(v[q]) * g, v1 = __uint_as_float(v[q + 1]) * g;
-      const float other = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-      const float lo = odd ? other : v0, hi = odd ? v1 : other;
       uint32_t w;
       if (p.type == kMx4Bf16) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v0, v1);
         w = *reinterpret_cast<const uint32_t*>(&b);
       } else {
-        const __half2 b = __floats2half2_rn(lo, hi);
+        const __half2 b = __floats2half2_rn(v0, v1);
         w = *reinterpret_cast<const uint32_t*>(&b);
       }
+      w = __byte_perm(w, __shfl_xor_sync(0xffffffffu, w, 1), take);
       if (in && q + (odd ? 1 : 0) < left) *reinterpret_cast<uint32_t*>(y) = w;
       y += 2 * p.N;
     }
