@@ -101,6 +101,18 @@ __device__ __forceinline__ void mul2(float& a0, float& a1, float b) {
       : "+f"(a0), "+f"(a1)
       : "f"(b));
 }
+__device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+      "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void add2(float& a0, float& a1, float b) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\t"
+      "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b));
+}
 // a = b * c + a
 __device__ __forceinline__ void fma2(float& a0, float& a1, float b0, float b1, float c) {
   asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
@@ -109,15 +121,30 @@ __device__ __forceinline__ void fma2(float& a0, float& a1, float b0, float b1, f
       : "f"(b0), "f"(b1), "f"(c));
 }
 
+// 1 / v to a last place, for v that is no subnormal.
+__device__ __forceinline__ float rcp(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 // ---- gated values -----------------------------------------------------------------
-// h = silu(g) * u * r in fp32, for -32 <= g: the exponent's rounding (46 at most)
-// makes the fast exponential 2^-19 off and its own two last places 2^-22, the fast
-// quotient's are two, the sum's and the products' half of one each: below 2^-18
-// together. The codes are those of the real h: where fp32 lies within 2^-18 of a
+// h = silu(g) * u of two values in fp32, for -32 <= g: the exponent's rounding (46 at
+// most) makes the exponential 2^-19 off and its approximation 2^-22, the reciprocal's
+// is 2^-23, the sum's and the products' half a last place each: below 2^-18 together,
+// r's product too. The codes are those of the real h: where fp32 lies within 2^-18 of a
 // border, 64 bits decide, for a value in 30000 or so (which costs its warp about 2000
 // cycles, at 1/64 of the rate).
-__device__ __forceinline__ float gated32(float g, float u) {
-  return __fdividef(g, 1.f + __expf(-g)) * u;
+__device__ __forceinline__ void gated32(float& v0, float& v1, float g0, float g1, float u0,
+                                        float u1) {
+  v0 = g0, v1 = g1;
+  mul2(v0, v1, -1.44269504f);
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(v0));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(v1));
+  add2(v0, v1, 1.f);
+  v0 = rcp(v0), v1 = rcp(v1);
+  mul2(v0, v1, g0, g1);
+  mul2(v0, v1, u0, u1);
 }
 // Whether that does not hold, as g is below -32 or fp32 has run out of exponents on
 // the way to v = h * r (zeros are exact).
@@ -135,6 +162,22 @@ static __device__ __noinline__ double gated64(float g, float u, float r) {
 constexpr uint32_t kNear = 32;
 __device__ __forceinline__ uint32_t above_short(float v, int keep) {
   return (__float_as_uint(v) + kNear) & ((1u << (23 - keep)) - 1);
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min_abs3(float a, float b, float c) {
+  float r;
+  asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// max(|a|, |b|, |c|), NaN if one is
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 // max(|a|, |b|), NaN if one is
 __device__ __forceinline__ float max_abs(float a, float b) {
@@ -179,15 +222,13 @@ __device__ __forceinline__ void quant_unit(const RowOut& out, int i_run, const E
     u8.values(u);
     float low = 1.f, gate = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = gated32(g[i], u[i]);
-      if constexpr (FMT == kE4M3) {
-        low = fminf(low, fabsf(v[i]));
-        v[i] *= r;
-      }
-      low = fminf(low, fabsf(v[i]));
-      gate = fminf(gate, g[i]);
+    for (int i = 0; i < 8; i += 2) {
+      gated32(v[i], v[i + 1], g[i], g[i + 1], u[i], u[i + 1]);
+      low = min_abs3(low, v[i], v[i + 1]);
+      gate = min3(gate, g[i], g[i + 1]);
+      if constexpr (FMT == kE4M3) mul2(v[i], v[i + 1], r);
     }
+    if (FMT == kE4M3) low = fminf(low, low * fabsf(r));
     if (low < 0x1p-100f || gate < -32.f) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) weak = weak || gated_weak(g[i], u[i], v[i], r);
@@ -203,7 +244,7 @@ __device__ __forceinline__ void quant_unit(const RowOut& out, int i_run, const E
   if constexpr (GATED || TYPE == kMx4F32) {
     most = max_abs(v[0], v[1]);
 #pragma unroll
-    for (int i = 2; i < 8; ++i) most = max_abs(most, v[i]);
+    for (int i = 2; i < 8; i += 2) most = max_abs3(most, v[i], v[i + 1]);
 #pragma unroll
     for (int o = 1; o < kLanes; o <<= 1)
       most = max_abs(most, __shfl_xor_sync(0xffffffffu, most, o));
@@ -258,7 +299,7 @@ __device__ __forceinline__ void quant_unit(const RowOut& out, int i_run, const E
     for (int i = 0; i < 8; i += 2) mul2(t[i], t[i + 1], inv);
   } else {
     s = e4m3_value(byte);
-    inv = s > 0.f ? __fdividef(1.f, s) : 0.f;
+    inv = s > 0.f ? rcp(s) : 0.f;
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
       t[i] = v[i], t[i + 1] = v[i + 1];
@@ -279,7 +320,8 @@ __device__ __forceinline__ void quant_unit(const RowOut& out, int i_run, const E
   if constexpr (GATED) {
     uint32_t over = kNear * 2;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) over = min(over, above_short(t[i], 2));
+    for (int i = 0; i < 8; i += 2)
+      over = __vimin3_u32(over, above_short(t[i], 2), above_short(t[i + 1], 2));
     if ((over < 2 * kNear || weak) && !bad) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
