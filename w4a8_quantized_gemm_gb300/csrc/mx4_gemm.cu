@@ -32,11 +32,11 @@ constexpr int kOwnRows = 16;             // at most
 // Runs of 256 values a CTA, at most. Calls that quantize so / apart, us, behind one
 // another in a graph (outside of one, where the host's time counts, a launch less is 2
 // us less):
-//   18944 x 3584   1 row (7 runs) 8.8 / 11.3   8 (56) 11.3 / 12.1   12 (84) 12.8 / 12.5
-//     gated        1 (7) 9.0 / 11.3   4 (28) 10.9 / 11.7   6 (42) 13.8 / 12.0
-//   3584 x 18944   1 (10) 9.5 / 11.7   6 (60) 11.7 / 11.8   8 (80) 12.1 / 11.8
-//     gated        1 (10) 10.8 / 11.7   2 (20) 11.5 / 11.7   4 (40) 12.4 / 12.2
-//   3584 x 3584    1 (2) 5.8 / 6.5   8 (16) 6.8 / 6.7   16 (32) 8.5 / 7.4
+//   18944 x 3584   1 row (7 runs) 8.9 / 11.3   8 (56) 11.3 / 12.2   12 (84) 12.8 / 12.5
+//     gated        1 (7) 9.2 / 11.3   4 (28) 10.9 / 11.7   6 (42) 12.1 / 12.0
+//   3584 x 18944   1 (10) 9.6 / 11.7   6 (60) 11.7 / 11.8   8 (80) 12.2 / 11.8
+//     gated        1 (10) 10.4 / 11.7   2 (20) 11.0 / 11.7   4 (40) 12.8 / 12.3
+//   3584 x 3584    1 (2) 5.3 / 6.5   8 (16) 5.6 / 6.7   16 (32) 6.5 / 7.4
 constexpr int kOwnRuns = 64, kOwnGatedRuns = 32;
 constexpr int kOwnBytes = 40960;         // codes and scales, at most
 
