@@ -197,10 +197,11 @@ def test_linear(fmt, M, N, K):
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("M,N,K", [(250, 4112, 1376), (1150, 2192, 1056), (1000, 20480, 96),
-                                   (510, 20640, 288), (1150, 2200, 1056)])
+                                   (510, 20640, 288), (1150, 2200, 1056), (1021, 3584, 544),
+                                   (131, 20000, 160), (545, 19200, 800), (2048, 3600, 352)])
 def test_many_rows(fmt, dtype, M, N, K):
-    """Tiles of rows by weights and of weights by rows (N no multiple of 16, or y off
-    a boundary of 32 bytes): odd blocks of rows, last tiles of 16, 144 and 160."""
+    """Last tiles of every kind, odd blocks of weights and of rows, y off a boundary of
+    32 bytes."""
     g = gen(M + N)
     x = rand(g, M, K, dtype=dtype)
     w, w64, _ = weight(g, fmt, N, K)
@@ -212,6 +213,8 @@ def test_many_rows(fmt, dtype, M, N, K):
         eg.mx4_linear(x, w, tensor_scale=ts, out=y)
         check(y, a64, w64)
         assert (room[at + M * N:] == 7.0).all()
+        rows = eg.mx4_quant(x, fmt, tensor_scale=ts, with_codes=False)
+        assert torch.equal(eg.mx4_gemm(rows, w, dtype=dtype), y)
     assert eg.device_status() == 0
 
 

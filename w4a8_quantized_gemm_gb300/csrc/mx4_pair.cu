@@ -204,8 +204,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_pair_kernel(const __grid_cons
     r.rows = (block[e] + 2 * t) * p.kb;
     r.row0 = (int64_t)first[e] + (int64_t)t * kBT;
     r.count = min(kBT, first[e + 1] - (int)r.row0);
-    // (above 128 a multiple of 64, so that neither half ends inside 32 rows of a record)
-    r.cols = r.count <= 128 ? (r.count + 15) & ~15 : (r.count + 63) & ~63;
+    // (above 128 all 256, garbage among them: one copy then brings a half, where one of
+    // 32 rows at a time takes longer than the instructions: 900 x 18944 x 3584 32.2 /
+    // 29.5 us, 700 x 8192 x 8192 31.1 / 29.6)
+    r.cols = r.count <= 128 ? (r.count + 15) & ~15 : kBT;
     r.n0 = (2 * n + rank) * 128;
     return r;
   };
@@ -251,23 +253,21 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_pair_kernel(const __grid_cons
       griddep_launch_dependents();
       produce(
           [&](const Unit& x) {
-            return (uint32_t)(x.cols + 63) / 64 * 32 * 128 + (x.cols > 128 ? 2 : 1) * C::kScale;
+            return x.cols == kBT ? 16384u + 2 * C::kScale
+                                 : (uint32_t)(x.cols + 63) / 64 * 32 * 128 + C::kScale;
           },
           [&](const Unit& x, int kb, uint32_t to, uint32_t bar) {
             const int rec = (x.rows + kb) * kRecRows, next = rec + p.kb * kRecRows;
             if (x.cols == kBT) {
               load_pair(to + C::kRowsAt, &maps.rows, bar, rank ? next : rec);
             } else {
-              // this CTA's half, 32 rows at a time, of the first record or the second
-              const int from = rank * x.cols / 2;
-              for (int c = 0; c < x.cols / 2; c += 32) {
-                const int row = from + c;
+              // this CTA's half, 32 rows at a time
+              for (int c = 0; c < x.cols / 2; c += 32)
                 load_pair(to + C::kRowsAt + c * 128, &maps.part, bar,
-                          row < 128 ? rec + row : next + row - 128);
-              }
+                          rec + rank * x.cols / 2 + c);
             }
             load_pair(to + C::kRowScaleAt, &maps.scale, bar, rec + 128);
-            if (x.cols > 128)
+            if (x.cols == kBT)
               load_pair(to + C::kRowScaleAt + C::kScale, &maps.scale, bar, next + 128);
           });
     }
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_pair_kernel(const __grid_cons
       Ring<C::kStages> r, before;  // item i, item i - kSets
       Ring<C::kSets> set;
       for (int k = 0; k < n_units && ok; ++k) {
-        const bool have = part < 2 || unit_at(k).cols > 128;
+        const bool have = part < 2 || unit_at(k).cols == kBT;
         for (int kb = 0; kb < p.kb; ++kb, ++i, r.next(), set.next()) {
           // its parts are there, and the instructions that read the set last have
           // completed
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_pair_kernel(const __grid_cons
 #pragma unroll
       for (int j = 0; j < kFirst; ++j) {
         const int c = (2 * j + mine) * 16;
-        if (c < C::kShared && c0 + c < un.cols) tmem_ld16(d + c0 + c, v[j]);
+        if (c < C::kShared && c0 + c < un.count) tmem_ld16(d + c0 + c, v[j]);
       }
       tmem_wait_ld();
       tc_fence_before();
@@ -384,11 +384,11 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_pair_kernel(const __grid_cons
 #pragma unroll
       for (int j = 0; j < kFirst; ++j) {
         const int c = (2 * j + mine) * 16;
-        if (c < C::kShared && c0 + c < un.cols) store16(p, un, c0 + c, n, v[j], g);
+        if (c < C::kShared && c0 + c < un.count) store16(p, un, c0 + c, n, v[j], g);
       }
       // (read before the next tile's are, and so before the instructions that
       // wait for those)
-      const int from = b ? C::kShared : 0, to = min(un.cols, b ? kBT : C::kAcc1);
+      const int from = b ? C::kShared : 0, to = min(un.count, b ? kBT : C::kAcc1);
       for (int c = from + mine * 16; c < to; c += 32) {
         uint32_t u[16];
         tmem_ld16(d + c, u);
