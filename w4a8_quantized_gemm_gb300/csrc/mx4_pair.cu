@@ -11,6 +11,10 @@
 // need more, so the accumulators overlap: columns [kAcc1, 256) belong to both. A
 // tile's instructions wait until the epilogue has read those of the tile before;
 // the rest is read while they run.
+//
+// Measured: 4096 x 18944 x 3584 88 us (6.3 PFLOP/s; E4M3, with twice the scales to
+// copy, 96), 8192 x 8192 x 8192 149 us (7.4). A K block takes some 540 cycles, of which
+// its instructions are 512, and a change of tiles 2000.
 #include "mx4_tc.cuh"
 #include "tc_kernel.cuh"  // (encode_fn)
 

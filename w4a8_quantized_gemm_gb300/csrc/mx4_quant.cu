@@ -22,8 +22,10 @@ struct QuantParams {
 
 // A warp takes U runs of 256 values of a row: eight values a lane, so that a block
 // of 32 (16) is four (two) neighbours and a row's 128 bytes of codes leave as one
-// line. Bound by memory: all of a warp's loads are on their way before the first
-// is used; few rows take U = 1, so that more warps share them.
+// line. All of a warp's loads are on their way before the first is used; few rows take
+// U = 1, so that more warps share them. Measured: 4093 x 18944 bf16 to E8M0 36.5 us (5.4
+// TB/s), to E4M3 44.7, gated 1021 x 18944 23.4 and 26.7: issue slots, 63 to 65 % busy,
+// bind before memory does.
 template <int FMT, int TYPE, bool GATED, int U>
 __global__ void __launch_bounds__(kQuantWarps * 32, GATED ? 8 : 9) mx4_quant_kernel(const QuantParams p) {
   extern __shared__ int quant_smem[];
@@ -161,7 +163,7 @@ cudaError_t launch_quant_type(const Mx4QuantArgs& a, cudaStream_t st) {
 // Ragged rows that are gathered from fewer: each was quantized once, and this moves
 // codes and scales to their places among the records. A warp takes a row, sixteen K
 // blocks at a time, 16 bytes a lane and four of them on their way; memory (L2, as to
-// what is read) bounds it.
+// what is read) bounds it: 32768 rows of 3584 from 4096 take about 19 us.
 template <int FMT>
 __global__ void __launch_bounds__(256) mx4_gather_kernel(const QuantParams p) {
   extern __shared__ int quant_smem[];
@@ -247,7 +249,8 @@ cudaError_t launch_gather(const Mx4QuantArgs& a, cudaStream_t st) {
 
 // ---- values back ------------------------------------------------------------------
 // Eight values a thread and step, four steps' codes on their way at a time; the
-// code times its block's scale is exact in fp32.
+// code times its block's scale is exact in fp32. Bound by memory: 4093 x 18944 to fp16
+// takes 30 us, a copy's rate.
 template <int FMT, int TYPE>
 __device__ __forceinline__ void dequant8(uint32_t c, uint32_t byte, bool scaled, float g, void* y,
                                          int64_t i) {
@@ -337,7 +340,8 @@ cudaError_t launch_dequant_type(const uint8_t* codes, const uint8_t* scales, int
 }
 
 // ---- weights in and out of their records ---------------------------------------------
-// A warp moves the 128 bytes of codes and the scales of one row and K block.
+// A warp moves the 128 bytes of codes and the scales of one row and K block (once a
+// weight: 18944 x 3584 takes 68 us).
 // Rows past N and values past K are zeros (in memory that the products read). No
 // early launch here: a product may read a weight before its own wait.
 template <int FMT, bool PACK>
