@@ -14,7 +14,8 @@
 //
 // Measured: 4096 x 18944 x 3584 88 us (6.3 PFLOP/s; E4M3, with twice the scales to
 // copy, 96), 8192 x 8192 x 8192 149 us (7.4). A K block takes some 540 cycles, of which
-// its instructions are 512, and a change of tiles 2000.
+// its instructions are 512 and its 35.8 KB from L2 near as many, and a change of tiles
+// 2000.
 #include "mx4_tc.cuh"
 #include "tc_kernel.cuh"  // (encode_fn)
 
