@@ -174,6 +174,36 @@ def test_gated_values_where_fp32_runs_out(fmt):
     assert torch.equal(rows.scales, s) and same_codes(rows.codes, c)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("low,high", [(-40.0, -22.0), (-24.0, -8.0), (-8.0, 30.0)])
+def test_gated_values_next_to_borders(fmt, low, high):
+    """Values within 2^-17 of a border between two codes, or (alone in their block)
+    between two scales: fp32 may not decide what it cannot tell."""
+    g, M, K = gen(24), 2048, 512
+    border = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], device="cuda",
+                          dtype=torch.float64)
+    gate = (torch.rand(M, K, generator=g, device="cuda") * (high - low) + low)
+    near = 1.0 + (torch.rand(M, K, generator=g, device="cuda").double() * 2 - 1) * 2.0 ** -17
+    want = border[torch.randint(0, 7, (M, K), generator=g, device="cuda")] * near
+    # the first of a block: 6 (a scale of 1), or the block's only value
+    first, alone = slice(0, K, BLOCK[fmt]), torch.arange(M, device="cuda") % 2 == 0
+    want[:, first] = 6.0
+    gate[:, first] = 24.0
+    lone = torch.zeros_like(want)
+    # 4, or 6 * 1.0625, which lies between two e4m3 numbers
+    lone[:, first] = (4.0 if fmt == eg.MX4_E8M0 else 6.375) * near[:, first]
+    want = torch.where(alone[:, None], lone, want)
+    lone_gate = torch.rand(M, K, generator=g, device="cuda") * (high - low) + low
+    gate = torch.where(alone[:, None], lone_gate, gate)
+    silu = gate.double() / (1.0 + torch.exp(-gate.double()))
+    up = (want / silu).float()
+    x = torch.cat([gate, up], dim=1)
+    r = eg.mx4_quant(x, fmt, gated=True)
+    codes, scales = quant(values_in(x, K, fmt, None, True), fmt)
+    assert torch.equal(r.scales, scales)
+    assert same_codes(r.codes, codes)
+
+
 # -------------------------------------------------------------------- products ---
 
 @pytest.mark.parametrize("fmt", FORMATS)

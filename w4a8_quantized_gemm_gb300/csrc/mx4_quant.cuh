@@ -129,12 +129,14 @@ __device__ __forceinline__ float rcp(float v) {
 }
 
 // ---- gated values -----------------------------------------------------------------
-// h = silu(g) * u of two values in fp32, for -32 <= g: the exponent's rounding (46 at
-// most) makes the exponential 2^-19 off and its approximation 2^-22, the reciprocal's
-// is 2^-23, the sum's and the products' half a last place each: below 2^-18 together,
-// r's product too. The codes are those of the real h: where fp32 lies within 2^-18 of a
-// border, 64 bits decide, for a value in 30000 or so (which costs its warp about 2000
-// cycles, at 1/64 of the rate).
+// h = silu(g) * u of two values in fp32, for -22 <= g. The exponent, below 32, is off by
+// half a last place, 2^-20, and by 32 times log2(e)'s own 2^-26: the exponential by
+// 0.96e-6. Its approximation adds 0.24e-6 (2^-22), the reciprocal's 0.12e-6, the sum,
+// the products (r's, and for the codes that with 1/s, itself 0.12e-6 off) 0.06e-6 each:
+// 1.74e-6 together, less than the 32 last places (1.9e-6 or more of a value) within
+// which of a border 64 bits decide instead of fp32: the codes are those of the real h.
+// That is a value in 30000 or so (which costs its warp about 2000 cycles, at 1/64 of
+// the rate).
 __device__ __forceinline__ void gated32(float& v0, float& v1, float g0, float g1, float u0,
                                         float u1) {
   v0 = g0, v1 = g1;
@@ -146,11 +148,11 @@ __device__ __forceinline__ void gated32(float& v0, float& v1, float g0, float g1
   mul2(v0, v1, g0, g1);
   mul2(v0, v1, u0, u1);
 }
-// Whether that does not hold, as g is below -32 or fp32 has run out of exponents on
+// Whether that does not hold, as g is below -22 or fp32 has run out of exponents on
 // the way to v = h * r (zeros are exact).
 __device__ __forceinline__ bool gated_weak(float g, float u, float v, float r) {
   return g != 0.f && u != 0.f &&
-         (g < -32.f || fabsf(v) < 0x1p-100f || fabsf(v) < 0x1p-100f * fabsf(r));
+         (g < -22.f || fabsf(v) < 0x1p-100f || fabsf(v) < 0x1p-100f * fabsf(r));
 }
 static __device__ __noinline__ double gated64(float g, float u, float r) {
   return (double)g / (1.0 + exp(-(double)g)) * (double)u * (double)r;
@@ -229,7 +231,7 @@ __device__ __forceinline__ void quant_unit(const RowOut& out, int i_run, const E
       if constexpr (FMT == kE4M3) mul2(v[i], v[i + 1], r);
     }
     if (FMT == kE4M3) low = fminf(low, low * fabsf(r));
-    if (low < 0x1p-100f || gate < -32.f) {
+    if (low < 0x1p-100f || gate < -22.f) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) weak = weak || gated_weak(g[i], u[i], v[i], r);
     }
