@@ -1,0 +1,41 @@
+"""Microscaled 4-bit linears at the ends of their types and between their kernels,
+against the definition in 64 bits (tests/mx4_helpers.py)."""
+import pytest
+import torch
+
+import w4a8_quantized_gemm_gb300 as eg
+from mx4_helpers import BLOCK, quant, same_codes, values_in
+from test_gpu_mx4 import FORMATS, gen
+
+pytestmark = pytest.mark.gpu
+
+
+# --------------------------------------------------------------- quantization ---
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("bits", [3, 10, 17, 23])
+def test_gated_codes_of_subnormal_gates(fmt, bits):
+    """fp32 gates of k steps of 2^-149, below 2^bits of them, with an up half that
+    brings their product (times the tensor's scale, which e4m3 blocks need for it) back
+    to ordinary numbers: half a gate is no number of fp32's where k is odd, so the
+    codes are those of the real product only if it is not formed there."""
+    g, M, K = gen(40 + bits), 512, 512
+    k = torch.randint(1, 2 ** bits, (M, K), generator=g, device="cuda", dtype=torch.int32)
+    gate = k.view(torch.float32)  # (the pattern of k * 2^-149)
+    assert torch.equal(gate.double(), k.double() * 2.0 ** -149)
+    size = torch.randint(0, 6, (M, K // BLOCK[fmt]), generator=g, device="cuda")
+    want = (0.3 + 5.7 * torch.rand(M, K, generator=g, device="cuda").double()) * (
+        2.0 ** size.double()).repeat_interleave(BLOCK[fmt], dim=1) * 2.0 ** -60
+    # in every second row the first of a block is its only value
+    lone = torch.zeros(K, dtype=torch.bool, device="cuda")
+    lone[::BLOCK[fmt]] = True
+    want[::2, ~lone] = 0.0
+    up = (want / (0.5 * gate.double())).float()
+    assert torch.isfinite(up).all()
+    sign = torch.randint(0, 2, (M, K), generator=g, device="cuda") * 2.0 - 1.0
+    x = torch.cat([gate * sign, up], dim=1)
+    ts = torch.tensor([2.0 ** -60], device="cuda") if fmt == eg.MX4_E4M3 else None
+    rows = eg.mx4_quant(x, fmt, tensor_scale=ts, gated=True)
+    codes, scales = quant(values_in(x, K, fmt, ts, True), fmt)
+    assert torch.equal(rows.scales, scales)
+    assert same_codes(rows.codes, codes)
