@@ -26,6 +26,12 @@
  *    egopq_status without launching anything when a check fails; a failed
  *    launch returns EGOPQ_ERR_CUDA. egopq_last_error_string() describes the
  *    last failure of the calling thread.
+ *  - Packed and int8 weights may be read while the kernel in front of a call on its
+ *    stream still runs, if that one lets others begin early (programmatic
+ *    dependent launch). The calls that make weights (the packing ones, and
+ *    egopq_mx4_quant with an operand) do not; what else a call here writes is not
+ *    such a weight of the call right behind it, and a kernel of the caller's that
+ *    writes weights must not let others begin before they are written.
  *  - Matrices are row-major. bf16 and fp16 values travel as their 16-bit
  *    patterns (uint16_t).
  *  - Shape gate: group == 128, K % 128 == 0, N % 128 == 0, M >= 0 (M == 0 is a
@@ -481,7 +487,8 @@ int egopq_mx4_unpack(const void* packed, int64_t sets, int64_t N, int64_t K, int
 
 /* y [M][N] = rows times weights: sum_k a[m][k] w[n][k] over the stored values,
  * times a_scale[0] * w_scale[0] (fp32; NULL: 1), rounded once to y_type.
- * operand: of egopq_mx4_quant for the same M, K and format; packed: one set. */
+ * operand: of egopq_mx4_quant for the same M, K and format; packed: one set, or the
+ * operand of an egopq_mx4_quant of N rows (the same layout). */
 int egopq_mx4_gemm(const void* operand, const void* packed, const float* a_scale,
                    const float* w_scale, int64_t M, int64_t N, int64_t K, int format, int y_type,
                    void* y, egopq_stream_t stream);

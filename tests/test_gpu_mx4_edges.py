@@ -39,3 +39,28 @@ def test_gated_codes_of_subnormal_gates(fmt, bits):
     codes, scales = quant(values_in(x, K, fmt, ts, True), fmt)
     assert torch.equal(rows.scales, scales)
     assert same_codes(rows.codes, codes)
+
+
+# ---------------------------------------------------------- weights, right away ---
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M", [1, 16, 40, 400])
+def test_a_weight_quantized_right_in_front_of_its_product(fmt, M):
+    """An operand as the weight of the next call, which begins to read weights before
+    what is in front of it has ended: the same values as of mx4_pack."""
+    g, N, K = gen(50 + M), 2560, 3584
+    x = torch.randn(M, K, generator=g, device="cuda").bfloat16()
+    for turn in range(4):
+        w = (torch.randn(N, K, generator=g, device="cuda") * 0.05).bfloat16()
+        rows = eg.mx4_quant(w, fmt)
+        want = eg.mx4_linear(x, eg.mx4_pack(rows.codes, rows.scales, fmt))
+        xr = eg.mx4_quant(x, fmt, with_codes=False)
+        for call in (lambda: eg.mx4_linear(x, eg.Mx4Weight(rows.a_tc, 0, N, K, fmt, None)),
+                     lambda: eg.mx4_gemm(xr, eg.Mx4Weight(rows.a_tc, 0, N, K, fmt, None))):
+            call()
+            torch.cuda.synchronize()
+            rows.a_tc.fill_(255)  # (codes of -6 under NaN)
+            torch.cuda.synchronize()
+            eg.mx4_quant(w, fmt, out=rows)
+            assert torch.equal(call(), want)
+    assert eg.device_status() == 0

@@ -1,0 +1,35 @@
+"""Host checks of the microscaled 4-bit linears: which kernels let the next one begin
+early (in the sources: no run shows a race for certain)."""
+import os
+import re
+
+from w4a8_quantized_gemm_gb300 import builder
+
+
+def source(name):
+    with open(os.path.join(builder.CSRC, name), encoding="utf-8") as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def body(text, head):
+    """What stands between the braces behind `head`."""
+    at = text.index("{", text.index(head))
+    depth = 0
+    for i in range(at, len(text)):
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        if depth == 0:
+            return text[at:i]
+    raise AssertionError(head)
+
+
+def test_what_makes_weights_lets_no_kernel_begin_before_its_end():
+    """Products read weights in front of their wait."""
+    text, api = source("mx4_quant.cu"), source("mx4_api.cu")
+    assert "griddep_launch_dependents" not in body(text, "mx4_pack_kernel(uint8_t* codes")
+    quant = body(text, "mx4_quant_kernel(const QuantParams p)")
+    assert re.findall(r"if \(([^\n]*)\) griddep_launch_dependents", quant) == [
+        "p.early && threadIdx.x == 0"]
+    assert quant.count("griddep_launch_dependents") == 1
+    # an operand of the caller's is such a weight; a linear's own is read by its product
+    assert "a.early = !operand;" in body(api, "int egopq_mx4_quant(")
+    assert api.count("early = true") == 1 and "early = true" in body(api, "int run(")

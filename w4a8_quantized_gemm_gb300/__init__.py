@@ -766,7 +766,8 @@ class Mx4Rows(NamedTuple):
 
 
 class Mx4Weight(NamedTuple):
-    """A packed 4-bit weight, or the weights of `sets` experts (mx4_pack)."""
+    """A packed 4-bit weight, or the weights of `sets` experts (mx4_pack). One weight's
+    `packed` may also be the a_tc of an mx4_quant of its N rows."""
     packed: torch.Tensor
     sets: int  # 0: one weight [N, K]; else [sets, N, K]
     N: int

@@ -90,6 +90,7 @@ size_t gather_bytes(int64_t x_rows, int64_t K, int format) {
 
 // Quantization and product of a call whose arguments have been checked.
 int run(Mx4QuantArgs& q, Mx4GemmArgs& g, cudaStream_t st) {
+  q.early = true;  // (only the product behind it reads the workspace, after its wait)
   if (mx4_own_rows(g, q)) return launched(launch_mx4_own(g, q, st), "mx4 product launch");
   if (q.index && gathers(q.M, q.x_rows, q.K)) {
     Mx4QuantArgs once = q;
@@ -152,6 +153,7 @@ int egopq_mx4_quant(const void* x, int x_type, int64_t M, int64_t K, int format,
   a.codes = codes;
   a.scales = scales;
   a.operand = static_cast<uint8_t*>(operand);
+  a.early = !operand;
   return launched(launch_mx4_quant(a, (cudaStream_t)stream), "mx4_quant launch");
 }
 

@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(Cfg<FMT, XT>::kThreads, 2)
   }
   if (warp == kWeightWarp) {
     // Weights need no wait: nothing that may still run in front of this kernel
-    // writes them.
+    // writes them (what makes weights lets no kernel begin before it has ended).
     if (lane == 0)
       produce([&](const Unit&) { return (uint32_t)C::kRec; },
               [&](const Unit& x, int kb, uint32_t to, uint32_t bar) {

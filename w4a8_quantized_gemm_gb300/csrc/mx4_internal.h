@@ -52,6 +52,9 @@ struct Mx4QuantArgs {
   uint8_t* codes;        // [M][K / 2], may be null
   uint8_t* scales;       // [M][K / block], may be null
   uint8_t* operand;      // records, may be null
+  // The next kernel may begin while this one writes. Not where the operand is the
+  // caller's: it may be the weight of the next call, which is read before that waits.
+  bool early;
 };
 cudaError_t launch_mx4_quant(const Mx4QuantArgs& a, cudaStream_t st);
 // Rows index[r] of codes [x_rows][K / 2] and scales to the operand's records.

@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_pair_kernel(const __grid_cons
   constexpr int kRecRows = C::kRec / 128;
   if (warp == kWeightWarp) {
     // Weights need no wait: nothing that may still run in front of this kernel
-    // writes them.
+    // writes them (what makes weights lets no kernel begin before it has ended).
     if (lane == 0)
       produce([&](const Unit&) { return (uint32_t)C::kRec; },
               [&](const Unit& x, int kb, uint32_t to, uint32_t bar) {

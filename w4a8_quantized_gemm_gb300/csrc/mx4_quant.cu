@@ -18,6 +18,7 @@ struct QuantParams {
   uint8_t* operand;
   int64_t M, K, x_rows;
   int sets, kb, groups;  // K blocks of a row, and runs of U of them
+  bool early;
 };
 
 // A warp takes U runs of 256 values of a row: eight values a lane, so that a block
@@ -31,7 +32,7 @@ __global__ void __launch_bounds__(kQuantWarps * 32, GATED ? 8 : 9) mx4_quant_ker
   extern __shared__ int quant_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_wait();
-  if (threadIdx.x == 0) griddep_launch_dependents();
+  if (p.early && threadIdx.x == 0) griddep_launch_dependents();
   int *first = nullptr, *block = nullptr;
   int64_t row = 0, rows_end = p.M;
   if (p.offsets) {
@@ -97,6 +98,7 @@ __global__ void __launch_bounds__(kQuantWarps * 32, GATED ? 8 : 9) mx4_quant_ker
       ++row;
     }
   }
+  if (!p.early) __threadfence();  // (a block's end lets the next kernel begin)
 }
 
 template <int FMT, int TYPE, bool GATED, int U>
@@ -115,6 +117,7 @@ cudaError_t launch_quant_u(const Mx4QuantArgs& a, int sms, cudaStream_t st) {
   p.sets = a.sets;
   p.kb = (int)mx4_kblocks(a.K);
   p.groups = (p.kb + U - 1) / U;
+  p.early = a.early;
   const int64_t blocks = (a.M * p.groups + kQuantWarps - 1) / kQuantWarps;
   // as many as are on the SMs at a time: a second round of blocks that takes as long
   // as the first would leave them half empty
@@ -374,6 +377,7 @@ __global__ void __launch_bounds__(256) mx4_pack_kernel(uint8_t* codes, uint8_t* 
       else if (have) scales[row * blocks + b] = *sc;
     }
   }
+  __threadfence();  // (a block's end lets the next kernel begin)
 }
 
 template <bool PACK>
