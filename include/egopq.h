@@ -335,7 +335,8 @@ int egopq_w8a8_gemm_ex(const int8_t* a_q, const void* a_tc, const float* a_s, co
  * as it is. Timed beside the packed kernels it measures what the int4 unpack
  * costs ("OSCAR PR #20", commit message: a bf16 twin kernel of identical
  * structure as the fair speed baseline); egopq_dequant_w4 plus any dense
- * library GEMM is the other comparison. Not a quantized path. */
+ * library GEMM is the other comparison. Not a quantized path. As x, w may be what
+ * the call in front has written. */
 int egopq_bf16_gemm_twin(const uint16_t* x_bf16, const uint16_t* w_bf16, int64_t M, int64_t N,
                          int64_t K, uint16_t* y_bf16, egopq_stream_t stream);
 

@@ -64,3 +64,19 @@ def test_a_weight_quantized_right_in_front_of_its_product(fmt, M):
             eg.mx4_quant(w, fmt, out=rows)
             assert torch.equal(call(), want)
     assert eg.device_status() == 0
+
+
+def test_a_weight_dequantized_right_in_front_of_its_product():
+    g, M, N, K = gen(60), 64, 2560, 3584
+    x = torch.randn(M, K, generator=g, device="cuda").bfloat16()
+    rows = eg.mx4_quant((torch.randn(N, K, generator=g, device="cuda") * 0.05).bfloat16(),
+                        with_tc=False)
+    w = eg.mx4_dequant(rows)
+    want = eg.bf16_gemm_twin(x, w)
+    for turn in range(4):
+        torch.cuda.synchronize()
+        w.fill_(float("nan"))
+        torch.cuda.synchronize()
+        eg.mx4_dequant(rows, out=w)
+        assert torch.equal(eg.bf16_gemm_twin(x, w), want)
+    assert eg.device_status() == 0

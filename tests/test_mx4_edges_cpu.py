@@ -33,3 +33,11 @@ def test_what_makes_weights_lets_no_kernel_begin_before_its_end():
     # an operand of the caller's is such a weight; a linear's own is read by its product
     assert "a.early = !operand;" in body(api, "int egopq_mx4_quant(")
     assert api.count("early = true") == 1 and "early = true" in body(api, "int run(")
+
+
+def test_dense_weights_are_read_behind_the_wait():
+    """Any kernel may write such a matrix (mx4_dequant lets the next one begin early)."""
+    text = source("tc_kernel.cuh")
+    at = text.index("load_weights(i);")
+    before = text[text.rindex("} else {", 0, at):at]
+    assert re.search(r"if constexpr \(C::kW16\) griddep_wait\(\);\s*const int n_pre", before)

@@ -657,7 +657,9 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap act_map,
         }
       } else {
         // weights do not depend on the preceding grid: start streaming them
-        // before waiting for it; activations only after
+        // before waiting for it; activations only after. (Dense bf16 ones may:
+        // any kernel's output can be such a matrix.)
+        if constexpr (C::kW16) griddep_wait();
         const int n_pre = n_items < S ? n_items : S;
         for (int i = 0; i < n_pre; ++i) {
           mbar_arrive_expect_tx(full_bar(i), C::kTxBytes);
