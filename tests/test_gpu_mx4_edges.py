@@ -80,3 +80,30 @@ def test_a_weight_dequantized_right_in_front_of_its_product():
         eg.mx4_dequant(rows, out=w)
         assert torch.equal(eg.bf16_gemm_twin(x, w), want)
     assert eg.device_status() == 0
+
+
+# -------------------------------------------------------------------- products ---
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("M,N,K", [(16, 16384, 2048), (12, 19456, 2304), (9, 14336, 2048),
+                                   (14, 9856, 1024), (12, 39040, 1280), (4, 58368, 3328)])
+def test_one_call_and_two_add_up_alike(fmt, gated, M, N, K):
+    """mx4_linear gives the values of mx4_quant and mx4_gemm, to the last bit of fp32:
+    sizes where the kernel of many rows would add up the few rows in another order.
+    (Blocks spread over 2^20, so that sums are rounded.)"""
+    g = gen(M + N)
+
+    def spread(*shape):
+        v = torch.randn(shape, generator=g, device="cuda")
+        e = torch.randint(-10, 11, (shape[0], shape[1] // 32), generator=g, device="cuda")
+        return v * (2.0 ** e).repeat_interleave(32, dim=1)
+
+    x = spread(M, 2 * K if gated else K).bfloat16()
+    r = eg.mx4_quant((spread(N, K) * 0.05).bfloat16(), fmt, with_tc=False)
+    packed = eg.mx4_pack(r.codes, r.scales, fmt)
+    rows = eg.mx4_quant(x, fmt, gated=gated, with_codes=False)
+    y = eg.mx4_linear(x, packed, gated=gated, dtype=torch.float32)
+    assert torch.equal(eg.mx4_gemm(rows, packed, dtype=torch.float32), y)
+    z = eg.mx4_linear(x.float(), packed, gated=gated)
+    assert z.dtype is torch.float32 and torch.equal(z, y)

@@ -441,6 +441,15 @@ cudaError_t launch_own(const Mx4GemmArgs& a, const Mx4QuantArgs& q, cudaStream_t
                  : launch_few<FMT, kMx4F16, false>(a, q.x, st);
 }
 
+// Whether a linear's rows are few enough for the kernel to quantize, `runs` a CTA.
+bool own_fits(const Mx4GemmArgs& a, int sms, int runs) {
+  if (a.offsets || a.M > kOwnRows) return false;
+  const int64_t kb = mx4_kblocks(a.K), split = few_split(few_units(a), kb, sms);
+  const int64_t kb_most = (kb + split - 1) / split;
+  return a.M * kb_most <= runs &&
+         kb_most * (2048 + mx4_record_bytes(a.format) - kMx4Codes) <= kOwnBytes;
+}
+
 // Which kernel a product takes. One linear: by what each would take, in us, fitted to
 // the measurements below: a start, K blocks one after the other (with the columns of
 // a tile), and a split unit's sums.
@@ -453,10 +462,15 @@ cudaError_t launch_own(const Mx4GemmArgs& a, const Mx4QuantArgs& q, cudaStream_t
 // Ragged rows, whose sets only the device knows: by their mean. 64 sets of 2560 x
 // 3584, mean 32: 62.8 / 64.6, 64: 69.8 / 71.6, 96: 86.9 / 78.3; of 2048 x 1408, mean
 // 32: 29.8 / 31.4, 64: 34.4 / 33.9, 96: 43.6 / 37.5.
+// Rows that a linear may quantize itself, over a split K, take the same kernel behind a
+// quantization of their own, so that both add up alike (K in one piece is the same sum
+// in either kernel); where pairs would be faster it costs some 1.2 us: 16 rows of 16384 x
+// 2048 8.0 / 6.6, 12 of 19456 x 2304 8.3 / 7.4, 14 of 9856 x 1024 5.6 / 4.5.
 bool takes_few(const Mx4GemmArgs& a, int sms) {
   if (a.offsets) return a.M <= 64 * (int64_t)a.sets;
   const int64_t kb = mx4_kblocks(a.K), units = few_units(a);
   const int split = few_split(units, kb, sms);
+  if (split > 1 && own_fits(a, sms, kOwnRuns)) return true;
   const int64_t rounds = split > 1 ? 1 : (units + 2 * sms - 1) / (2 * sms);
   const double rows = a.M < kBT ? (double)a.M : kBT;
   const double few = 4.0 + (double)(rounds * ((kb + split - 1) / split)) * (0.45 + 0.002 * rows) +
@@ -470,13 +484,8 @@ bool takes_few(const Mx4GemmArgs& a, int sms) {
 }  // namespace
 
 bool mx4_own_rows(const Mx4GemmArgs& a, const Mx4QuantArgs& q) {
-  if (a.offsets || a.M > kOwnRows || q.type == kMx4F32) return false;
   const int sms = device_sm_count();
-  if (sms < 1) return false;
-  const int64_t kb = mx4_kblocks(a.K), split = few_split(few_units(a), kb, sms);
-  const int64_t kb_most = (kb + split - 1) / split;
-  return a.M * kb_most <= (q.gated ? kOwnGatedRuns : kOwnRuns) &&
-         kb_most * (2048 + mx4_record_bytes(a.format) - kMx4Codes) <= kOwnBytes;
+  return sms >= 1 && q.type != kMx4F32 && own_fits(a, sms, q.gated ? kOwnGatedRuns : kOwnRuns);
 }
 
 cudaError_t launch_mx4_own(const Mx4GemmArgs& a, const Mx4QuantArgs& q, cudaStream_t st) {
