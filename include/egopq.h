@@ -512,7 +512,8 @@ int egopq_mx4_linear(const void* x, int x_type, int64_t M, int64_t N, int64_t K,
  * one before it, counts as the nearest allowed); a set may be empty, and y's rows
  * before offsets[0] and from offsets[sets] on stay as they are. index int32
  * [rows] or NULL: row r of the batch is x's row index[r] (x has x_rows rows; an
- * index outside reads as a row of zeros); without it x_rows == rows. */
+ * index outside reads as a row of zeros, and an x without rows may be NULL); without
+ * it x_rows == rows. */
 int egopq_mx4_linear_ragged(const void* x, int x_type, int64_t x_rows, const int32_t* index,
                             const int32_t* offsets, int64_t rows, int64_t sets, int64_t N,
                             int64_t K, int gated, const float* a_scale, const void* packed,

@@ -107,3 +107,21 @@ def test_one_call_and_two_add_up_alike(fmt, gated, M, N, K):
     assert torch.equal(eg.mx4_gemm(rows, packed, dtype=torch.float32), y)
     z = eg.mx4_linear(x.float(), packed, gated=gated)
     assert z.dtype is torch.float32 and torch.equal(z, y)
+
+
+# --------------------------------------------------------------- ragged products ---
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("n,K", [(20, 96), (12300, 1056)])
+def test_an_x_without_rows_reads_as_zeros(fmt, n, K):
+    """Quantized directly, and (many rows of few) by a gather."""
+    g = gen(70)
+    r = eg.mx4_quant(torch.randn(2 * 40, K, generator=g, device="cuda"), fmt, with_tc=False)
+    w = eg.mx4_pack(r.codes.view(2, 40, -1), r.scales.view(2, 40, -1), fmt)
+    y = torch.full((n, 40), 3.0, dtype=torch.bfloat16, device="cuda")
+    off = torch.tensor([1, 7, n - 2], dtype=torch.int32, device="cuda")
+    index = torch.randint(-5, 5, (n,), generator=g, device="cuda", dtype=torch.int32)
+    x = torch.empty(0, K, dtype=torch.bfloat16, device="cuda")
+    eg.mx4_linear_ragged(x, off, w, index=index, out=y)
+    assert (y[1:n - 2] == 0).all() and (y[:1] == 3.0).all() and (y[n - 2:] == 3.0).all()
+    assert eg.device_status() == 0

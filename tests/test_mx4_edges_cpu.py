@@ -1,8 +1,11 @@
 """Host checks of the microscaled 4-bit linears: which kernels let the next one begin
-early (in the sources: no run shows a race for certain)."""
+early (in the sources: no run shows a race for certain), and what is refused
+(addresses here are never read)."""
 import os
 import re
 
+from test_mx4_cpu import A, code, ragged
+from test_rows_cpu import lib  # noqa: F401
 from w4a8_quantized_gemm_gb300 import builder
 
 
@@ -41,3 +44,12 @@ def test_dense_weights_are_read_behind_the_wait():
     at = text.index("load_weights(i);")
     before = text[text.rindex("} else {", 0, at):at]
     assert re.search(r"if constexpr \(C::kW16\) griddep_wait\(\);\s*const int n_pre", before)
+
+
+# --------------------------------------------------------------------- arguments ---
+
+def test_an_x_without_rows_needs_no_address(lib):  # noqa: F811
+    # (every index is outside it; the workspace is the next thing to be looked at)
+    assert code(lib, ragged(lib, x=None, x_rows=0, index=A, nbytes=0), "needed") == -1
+    assert code(lib, ragged(lib, x=None, x_rows=1, index=A, nbytes=0), "x is NULL") == -1
+    assert code(lib, ragged(lib, x=None, x_rows=0, nbytes=0), "no index") == -1

@@ -230,8 +230,8 @@ size_t egopq_mx4_linear_workspace_bytes(int64_t rows, int64_t sets, int64_t K, i
 // What both linears check once their own shape has been accepted.
 static int check_linear(const Mx4QuantArgs& q, const Mx4GemmArgs& g, int64_t ws_sets,
                         const void* workspace, size_t workspace_bytes) {
-  int rc = check_ptrs(4, "x", q.x, "packed", g.packed, "y", g.y, "workspace", workspace);
-  if (rc) return rc;
+  int rc = q.x_rows > 0 ? check_ptrs(1, "x", q.x) : EGOPQ_OK;  // (none: nothing to read)
+  if (rc || (rc = check_ptrs(3, "packed", g.packed, "y", g.y, "workspace", workspace))) return rc;
   if ((rc = check_scales(g.format, g.a_scale, g.w_scale))) return rc;
   const size_t need = egopq_mx4_linear_workspace_bytes(g.M, ws_sets, g.K, g.format);
   if (workspace_bytes < need)
