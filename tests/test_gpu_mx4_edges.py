@@ -125,3 +125,21 @@ def test_an_x_without_rows_reads_as_zeros(fmt, n, K):
     eg.mx4_linear_ragged(x, off, w, index=index, out=y)
     assert (y[1:n - 2] == 0).all() and (y[:1] == 3.0).all() and (y[n - 2:] == 3.0).all()
     assert eg.device_status() == 0
+
+
+# ------------------------------------------------------------------------- types ---
+
+def test_a_result_has_the_type_of_its_output():
+    g = gen(71)
+    x = torch.randn(6, 64, generator=g, device="cuda").bfloat16()
+    rows = eg.mx4_quant(x)
+    w = eg.mx4_pack(rows.codes, rows.scales)
+    for call, shape in ((lambda **k: eg.mx4_dequant(rows, **k), (6, 64)),
+                        (lambda **k: eg.mx4_gemm(rows, w, **k), (6, 6)),
+                        (lambda **k: eg.mx4_linear(x, w, **k), (6, 6))):
+        assert call().dtype is torch.bfloat16
+        for t in (torch.float16, torch.float32):
+            want, out = call(dtype=t), torch.empty(shape, dtype=t, device="cuda")
+            assert want.dtype is t
+            assert call(out=out) is out and torch.equal(out, want)
+            assert call(dtype=t, out=out) is out and torch.equal(out, want)

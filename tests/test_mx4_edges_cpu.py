@@ -4,6 +4,10 @@ early (in the sources: no run shows a race for certain), and what is refused
 import os
 import re
 
+import pytest
+import torch
+
+import w4a8_quantized_gemm_gb300 as eg
 from test_mx4_cpu import A, code, ragged
 from test_rows_cpu import lib  # noqa: F401
 from w4a8_quantized_gemm_gb300 import builder
@@ -53,3 +57,25 @@ def test_an_x_without_rows_needs_no_address(lib):  # noqa: F811
     assert code(lib, ragged(lib, x=None, x_rows=0, index=A, nbytes=0), "needed") == -1
     assert code(lib, ragged(lib, x=None, x_rows=1, index=A, nbytes=0), "x is NULL") == -1
     assert code(lib, ragged(lib, x=None, x_rows=0, nbytes=0), "no index") == -1
+
+
+def test_a_type_that_contradicts_the_output_is_refused():
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    w = eg.Mx4Weight(torch.zeros(17408, dtype=torch.uint8), 0, 8, 64, 0, None)
+    many = w._replace(sets=2, packed=torch.zeros(34816, dtype=torch.uint8))
+    byte = torch.zeros(4, 32, dtype=torch.uint8)
+    rows = eg.Mx4Rows(byte, byte[:, :2].contiguous(), torch.zeros(17408, dtype=torch.uint8), 4, 64,
+                      0, None)
+    off = torch.zeros(3, dtype=torch.int32)
+    half, wide = torch.float16, torch.zeros(4, 64, dtype=torch.float16)
+    y = wide[:, :8].contiguous()
+    for call in (lambda d: eg.mx4_dequant(rows, dtype=d, out=wide),
+                 lambda d: eg.mx4_gemm(rows, w, dtype=d, out=y),
+                 lambda d: eg.mx4_linear(x, w, dtype=d, out=y),
+                 lambda d: eg.mx4_linear_ragged(x, off, many, dtype=d, out=y)):
+        for d in (torch.float32, torch.bfloat16):
+            with pytest.raises(TypeError, match="dtype"):
+                call(d)
+        for d in (None, half):  # (as far as the device, which these tensors are not on)
+            with pytest.raises(ValueError, match="CUDA"):
+                call(d)

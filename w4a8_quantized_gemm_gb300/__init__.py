@@ -744,6 +744,16 @@ def _mx4_type(dtype: torch.dtype) -> int:
     return t
 
 
+def _mx4_result(dtype: Optional[torch.dtype], out: Optional[torch.Tensor],
+                default: torch.dtype) -> torch.dtype:
+    """The type of a result: that of `out`, which dtype may not contradict."""
+    if out is None:
+        return dtype or default
+    if dtype is not None and dtype is not out.dtype:
+        raise TypeError(f"dtype {dtype} for an out of {out.dtype}")
+    return out.dtype
+
+
 def _mx4_scale(t: Optional[torch.Tensor], n: int) -> Optional[int]:
     if t is None:
         return None
@@ -849,12 +859,14 @@ def _mx4_rows_check(rows: Mx4Rows):
             raise ValueError(f"a_tc of {rows.a_tc.nbytes} bytes, {need} needed")
 
 
-def mx4_dequant(rows: Mx4Rows, dtype: torch.dtype = torch.bfloat16,
+def mx4_dequant(rows: Mx4Rows, dtype: Optional[torch.dtype] = None,
                 out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """The values [M, K] that rows' codes and scales stand for."""
+    """The values [M, K] that rows' codes and scales stand for: bf16 unless dtype or
+    out says otherwise."""
     codes, scales, _, M, K, fmt, tensor_scale = rows
     if codes is None or scales is None:
         raise ValueError("rows without codes and scales (with_codes=False)")
+    dtype = _mx4_result(dtype, out, torch.bfloat16)
     _mx4_here(codes, scales, tensor_scale, out)
     c = _arg(codes, torch.uint8, M, K // 2)
     s = _arg(scales, torch.uint8, M, K // mx4_block(fmt))
@@ -904,9 +916,10 @@ def mx4_unpack(weight: Mx4Weight, stream=None) -> tuple:
     return codes, scales
 
 
-def mx4_gemm(rows: Mx4Rows, weight: Mx4Weight, dtype: torch.dtype = torch.bfloat16,
+def mx4_gemm(rows: Mx4Rows, weight: Mx4Weight, dtype: Optional[torch.dtype] = None,
              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """Rows in 4 bits times a packed 4-bit weight: y [M, N]."""
+    """Rows in 4 bits times a packed 4-bit weight: y [M, N], bf16 unless dtype or out
+    says otherwise."""
     packed, sets, N, K, fmt, w_scale = weight
     if sets:
         raise ValueError("weights of several sets: mx4_linear_ragged")
@@ -914,14 +927,15 @@ def mx4_gemm(rows: Mx4Rows, weight: Mx4Weight, dtype: torch.dtype = torch.bfloat
         raise ValueError(f"rows of K={rows.K} format {rows.fmt}, a weight of K={K} format {fmt}")
     if rows.a_tc is None:
         raise ValueError("rows without the products' form (with_tc=False)")
+    dtype = _mx4_result(dtype, out, torch.bfloat16)
     _mx4_here(packed, rows.a_tc, rows.tensor_scale, w_scale, out)
     _mx4_rows_check(rows)
     at = _mx4_packed(weight)
     if out is None:
         out = _output((rows.M, N), dtype, packed.device, stream)
     _check(load().egopq_mx4_gemm(_ptr(rows.a_tc), at, _mx4_scale(rows.tensor_scale, 1),
-                                 _mx4_scale(w_scale, 1), rows.M, N, K, fmt, _mx4_type(out.dtype),
-                                 _arg(out, out.dtype, rows.M, N), _stream(stream)))
+                                 _mx4_scale(w_scale, 1), rows.M, N, K, fmt, _mx4_type(dtype),
+                                 _arg(out, dtype, rows.M, N), _stream(stream)))
     return out
 
 
@@ -951,17 +965,18 @@ def mx4_linear(x: torch.Tensor, weight: Mx4Weight, tensor_scale: Optional[torch.
     if sets:
         raise ValueError("weights of several sets: mx4_linear_ragged")
     M, x_type = _mx4_input(x, K, gated)
+    dtype = _mx4_result(dtype, out, x.dtype)
     if out is None:
-        out = _output((M, N), dtype or x.dtype, x.device, stream)
+        out = _output((M, N), dtype, x.device, stream)
     if workspace is None:
         workspace = mx4_workspace(M, weight, x.device, stream)
     device = _mx4_here(x, packed, out, workspace, tensor_scale, w_scale)
-    at, y_type = _mx4_packed(weight), out.dtype
+    at = _mx4_packed(weight)
     _check(load().egopq_mx4_linear(
         _mx4_at(x), x_type, M, N, K, gated,
         None if tensor_scale is None else _mx4_scale(tensor_scale, 1), at,
-        None if w_scale is None else _mx4_scale(w_scale, 1), fmt, _mx4_type(y_type),
-        _arg(out, y_type, M, N), _mx4_at(workspace), workspace.nbytes,
+        None if w_scale is None else _mx4_scale(w_scale, 1), fmt, _mx4_type(dtype),
+        _arg(out, dtype, M, N), _mx4_at(workspace), workspace.nbytes,
         _mx4_stream(stream, device)))
     return out
 
@@ -981,18 +996,19 @@ def mx4_linear_ragged(x: torch.Tensor, offsets: torch.Tensor, weight: Mx4Weight,
         raise ValueError("a weight of several sets is needed (codes [E, N, K/2])")
     x_rows, x_type = _mx4_input(x, K, gated)
     rows = x_rows if index is None else index.shape[0]
+    dtype = _mx4_result(dtype, out, x.dtype)
     if out is None:
-        out = _output((rows, N), dtype or x.dtype, x.device, stream)
+        out = _output((rows, N), dtype, x.device, stream)
     if workspace is None:
         workspace = mx4_workspace(rows, weight, x.device, stream)
     device = _mx4_here(x, packed, out, workspace, offsets, index, tensor_scale, w_scale)
-    at, y_type = _mx4_packed(weight), out.dtype
+    at = _mx4_packed(weight)
     _check(load().egopq_mx4_linear_ragged(
         _mx4_at(x), x_type, x_rows, None if index is None else _arg(index, torch.int32, rows),
         _arg(offsets, torch.int32, sets + 1), rows, sets, N, K, gated,
         None if tensor_scale is None else _mx4_scale(tensor_scale, 1), at,
-        None if w_scale is None else _mx4_scale(w_scale, sets), fmt, _mx4_type(y_type),
-        _arg(out, y_type, rows, N), _mx4_at(workspace), workspace.nbytes,
+        None if w_scale is None else _mx4_scale(w_scale, sets), fmt, _mx4_type(dtype),
+        _arg(out, dtype, rows, N), _mx4_at(workspace), workspace.nbytes,
         _mx4_stream(stream, device)))
     return out
 
