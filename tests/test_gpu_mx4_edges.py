@@ -143,3 +143,32 @@ def test_a_result_has_the_type_of_its_output():
             assert want.dtype is t
             assert call(out=out) is out and torch.equal(out, want)
             assert call(dtype=t, out=out) is out and torch.equal(out, want)
+
+
+# ------------------------------------------------------------------- debug build ---
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_debug_build_checks_the_records_of_both_kernels(monkeypatch, fmt):
+    """Of few rows and of many: a weight declared shorter than its buffer (to which the
+    redirected reads keep) is noticed, and nothing is where it is whole."""
+    monkeypatch.setattr(eg, "LIB_PATH", eg.DEBUG_LIB_PATH)
+    monkeypatch.setattr(eg, "_lib", None)
+    lib = eg.load()
+    try:
+        assert lib.egopq_debug_build() == 1
+        g, record = gen(72), 17408 if fmt == eg.MX4_E8M0 else 18432
+        r = eg.mx4_quant(torch.randn(300, 544, generator=g, device="cuda"), fmt, with_tc=False)
+        w = eg.mx4_pack(r.codes, r.scales, fmt)
+        assert w.packed.nbytes == 9 * record
+        for M in (2, 40, 200, 700):
+            x = torch.randn(M, 544, generator=g, device="cuda").bfloat16()
+            lib.egopq_debug_set_record_limit(0)
+            eg.mx4_linear(x, w)
+            assert eg.device_status() == 0, M
+            for records in (2, 8):
+                lib.egopq_debug_set_record_limit(records * record)
+                eg.mx4_linear(x, w)
+                assert eg.device_status() == -7, (M, records)
+    finally:
+        lib.egopq_debug_set_record_limit(0)
+        eg.device_status()

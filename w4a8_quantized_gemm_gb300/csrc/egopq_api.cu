@@ -645,6 +645,7 @@ int egopq_debug_set_record_limit(uint64_t bytes) {
   if (e == cudaSuccess) e = set_record_limit_tc_gemm(bytes);
   if (e == cudaSuccess) e = set_record_limit_tc_experts(bytes);
   if (e == cudaSuccess) e = set_record_limit_mx4_gemm(bytes);
+  if (e == cudaSuccess) e = set_record_limit_mx4_pair(bytes);
   return e == cudaSuccess ? EGOPQ_OK : cuda_fail(e, "set the record limit");
 #else
   (void)bytes;

@@ -360,6 +360,7 @@ cudaError_t set_record_limit_gemv(unsigned long long bytes);
 cudaError_t set_record_limit_tc_gemm(unsigned long long bytes);
 cudaError_t set_record_limit_tc_experts(unsigned long long bytes);
 cudaError_t set_record_limit_mx4_gemm(unsigned long long bytes);
+cudaError_t set_record_limit_mx4_pair(unsigned long long bytes);
 
 // Byte size of the packed records of one linear with N rows and G groups.
 __host__ __device__ inline uint64_t packed_record_bytes(int64_t N, int G) {

@@ -250,7 +250,11 @@ __global__ void __launch_bounds__(kThreads, 1) mx4_pair_kernel(const __grid_cons
     if (lane == 0)
       produce([&](const Unit&) { return (uint32_t)C::kRec; },
               [&](const Unit& x, int kb, uint32_t to, uint32_t bar) {
-                load_pair(to, &maps.weight, bar, (x.w + kb) * kRecRows);
+                int rec = x.w + kb;
+                if (!dbg_record_ok((uint64_t)rec * C::kRec, C::kRec,
+                                   (uint64_t)p.sets * p.nb * p.kb * C::kRec))
+                  rec = 0;
+                load_pair(to, &maps.weight, bar, rec * kRecRows);
               });
   } else if (warp == kRowWarp) {
     if (lane == 0) {
@@ -484,5 +488,8 @@ cudaError_t launch_mx4_pair(const Mx4GemmArgs& a, cudaStream_t st) {
 }
 
 cudaError_t take_error_word_mx4_pair(unsigned* out) { return take_local_error_word(out); }
+cudaError_t set_record_limit_mx4_pair(unsigned long long bytes) {
+  return set_local_record_limit(bytes);
+}
 
 }  // namespace egopq
