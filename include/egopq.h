@@ -449,7 +449,9 @@ int egopq_w4a8_linear_lora(const uint16_t* x_bf16, const void* packed, const uin
  * even k in the low nibble, scales [rows][K/block]. Both sides of a product are
  * held in 4 bits, and the tensor cores multiply them with their scales, summing
  * in fp32. K % 32 == 0; any number of rows M (0: a no-op) and weight rows N.
- * Pointers are 16-byte aligned (tensor scales, offsets and an index 4-byte). */
+ * Pointers are 16-byte aligned (tensor scales, offsets and an index 4-byte), and
+ * what a call writes (a workspace too) lies apart from what it reads: an overlap is
+ * refused. */
 typedef enum { EGOPQ_MX4_E8M0 = 0, EGOPQ_MX4_E4M3 = 1 } egopq_mx4_format;
 typedef enum { EGOPQ_TYPE_BF16 = 0, EGOPQ_TYPE_F16 = 1, EGOPQ_TYPE_F32 = 2 } egopq_type;
 
@@ -462,7 +464,7 @@ typedef enum { EGOPQ_TYPE_BF16 = 0, EGOPQ_TYPE_F16 = 1, EGOPQ_TYPE_F32 = 2 } ego
  * x is [M][2K], and u = silu(x[:K]) * x[K:] (* r), silu(v) = v / (1 + exp(-v)),
  * not rounded at all: codes and scales are those of the real number (a product
  * beyond fp32 makes its block NaN). tensor_scale: g, fp32 [1], not 0, or NULL
- * (must be NULL for E8M0). What is written lies apart from x.
+ * (must be NULL for E8M0).
  * codes and scales may be NULL (together), and so may operand: the form that
  * egopq_mx4_gemm reads, egopq_mx4_operand_bytes(M, K, format) bytes. */
 size_t egopq_mx4_operand_bytes(int64_t M, int64_t K, int format);
@@ -495,11 +497,10 @@ int egopq_mx4_gemm(const void* operand, const void* packed, const float* a_scale
                    void* y, egopq_stream_t stream);
 
 /* egopq_mx4_quant of x (tensor_scale = a_scale) and the product with `packed`, in
- * one call: the same values as of the two. x [M][K], or [M][2K] gated; y apart
- * from x (an overlap is refused). A workspace (egopq_mx4_linear_workspace_bytes, 0
- * for a refused shape and for no rows) serves fewer rows as well; calls sharing one
- * must be ordered on one stream. sets: 0 for egopq_mx4_linear, else those of the
- * ragged call. */
+ * one call: the same values as of the two. x [M][K], or [M][2K] gated. A workspace
+ * (egopq_mx4_linear_workspace_bytes, 0 for a refused shape and for no rows) serves
+ * fewer rows as well; calls sharing one must be ordered on one stream. sets: 0 for
+ * egopq_mx4_linear, else those of the ragged call. */
 size_t egopq_mx4_linear_workspace_bytes(int64_t rows, int64_t sets, int64_t K, int format);
 int egopq_mx4_linear(const void* x, int x_type, int64_t M, int64_t N, int64_t K, int gated,
                      const float* a_scale, const void* packed, const float* w_scale, int format,

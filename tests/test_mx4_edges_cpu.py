@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import w4a8_quantized_gemm_gb300 as eg
-from test_mx4_cpu import A, code, ragged
+from test_mx4_cpu import A, code, linear, q, ragged
 from test_rows_cpu import lib  # noqa: F401
 from w4a8_quantized_gemm_gb300 import builder
 
@@ -79,3 +79,29 @@ def test_a_type_that_contradicts_the_output_is_refused():
         for d in (None, half):  # (as far as the device, which these tensors are not on)
             with pytest.raises(ValueError, match="CUDA"):
                 call(d)
+
+
+def test_what_is_written_lies_apart_from_what_is_read(lib):  # noqa: F811
+    # 4 rows of 64: x 512 bytes, codes 128, scales 8, an operand of 17408; a weight of
+    # 8 x 64: codes 256, scales 16, 17408 packed
+    far = [2 * A, 3 * A, 4 * A]
+    for at in range(3):
+        for to in (A, A + 496, A - (112, 0, 17392)[at]):
+            out = far[:at] + [to] + far[at + 1:]
+            assert code(lib, q(lib, c=out[0], s=out[1], op=out[2]), "overlaps x") == -1, (at, to)
+    d = lib.egopq_mx4_dequant
+    for y in (A, A + 112, A - 496, 2 * A, 2 * A - 496):
+        assert code(lib, d(A, 2 * A, 4, 64, 0, None, 0, y, None), "y overlaps") == -1
+    for y in (A, A + 17392, 2 * A - 48, 2 * A + 17392):
+        assert code(lib, lib.egopq_mx4_gemm(A, 2 * A, None, None, 4, 8, 64, 0, 0, y, None),
+                    "y overlaps") == -1
+    for p in (A - 17392, A + 240, 2 * A):
+        assert code(lib, lib.egopq_mx4_pack(A, 2 * A, 1, 8, 64, 0, p, None), "overlaps") == -1
+        assert code(lib, lib.egopq_mx4_unpack(p, 1, 8, 64, 0, A, 2 * A, None), "overlaps") == -1
+    w = 8 * A
+    assert code(lib, linear(lib, w=w, y=w + 17392), "overlaps packed") == -1
+    assert code(lib, linear(lib, w=w, work=w - 17392), "overlaps packed") == -1
+    for word in ("offsets", "index"):
+        for at, what in ((2 * A + 60, "y"), (3 * A, "workspace")):
+            k = {"off": 9 * A, "index": 10 * A, "off" if word == "offsets" else "index": at}
+            assert code(lib, ragged(lib, **k), f"{what} overlaps {word}") == -1

@@ -1,5 +1,7 @@
 // mx4_api.cu -- C ABI of the microscaled 4-bit linears: argument checks and
 // workspace layout only; nothing is allocated here.
+#include <initializer_list>
+
 #include "mx4_internal.h"
 
 using namespace egopq;
@@ -61,9 +63,21 @@ int check_scales(int format, const float* a, const float* w) {
 
 int64_t type_bytes(int type) { return type == EGOPQ_TYPE_F32 ? 4 : 2; }
 
-bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-  const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
-  return pa < pb + (uintptr_t)nb && pb < pa + (uintptr_t)na;
+// A buffer, or none.
+struct Span {
+  const char* name;
+  const void* at;
+  int64_t bytes;
+};
+// What a call writes lies apart from what it reads: other blocks may still read it.
+int check_apart(const Span& out, std::initializer_list<Span> in) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(out.at);
+  for (const Span& s : in) {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(s.at);
+    if (out.at && s.at && a < b + (uintptr_t)s.bytes && b < a + (uintptr_t)out.bytes)
+      return fail(EGOPQ_ERR_INVALID_ARG, "%s overlaps %s", out.name, s.name);
+  }
+  return EGOPQ_OK;
 }
 
 size_t operand_bytes(int64_t blocks, int64_t K, int format) {
@@ -141,6 +155,12 @@ int egopq_mx4_quant(const void* x, int x_type, int64_t M, int64_t K, int format,
       (rc = check_optional(operand, "operand")) ||
       (rc = check_scales(format, tensor_scale, nullptr)))
     return rc;
+  const Span from{"x", x, M * K * (gated ? 2 : 1) * type_bytes(x_type)};
+  if ((rc = check_apart({"codes", codes, M * (K / 2)}, {from})) ||
+      (rc = check_apart({"scales", scales, M * (K / mx4_block(format))}, {from})) ||
+      (rc = check_apart({"operand", operand, (int64_t)operand_bytes((M + 127) / 128, K, format)},
+                        {from})))
+    return rc;
   if ((rc = check_arch())) return rc;
   Mx4QuantArgs a{};
   a.x = x;
@@ -165,6 +185,10 @@ int egopq_mx4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t M, in
   if (M == 0) return EGOPQ_OK;
   if ((rc = check_ptrs(3, "codes", codes, "scales", scales, "y", y))) return rc;
   if ((rc = check_scales(format, tensor_scale, nullptr))) return rc;
+  if ((rc = check_apart({"y", y, M * K * type_bytes(y_type)},
+                        {{"codes", codes, M * (K / 2)},
+                         {"scales", scales, M * (K / mx4_block(format))}})))
+    return rc;
   if ((rc = check_arch())) return rc;
   return launched(launch_mx4_dequant(codes, scales, M, K, format, tensor_scale, y_type, y,
                                      (cudaStream_t)stream),
@@ -177,6 +201,11 @@ int egopq_mx4_pack(const uint8_t* codes, const uint8_t* scales, int64_t sets, in
   if (rc) return rc;
   if ((rc = check_format(format))) return rc;
   if ((rc = check_ptrs(3, "codes", codes, "scales", scales, "packed", packed))) return rc;
+  const int64_t rows = sets * N, bytes = (int64_t)egopq_mx4_packed_bytes(sets, N, K, format);
+  if ((rc = check_apart({"packed", packed, bytes},
+                        {{"codes", codes, rows * (K / 2)},
+                         {"scales", scales, rows * (K / mx4_block(format))}})))
+    return rc;
   if ((rc = check_arch())) return rc;
   return launched(launch_mx4_pack(codes, scales, sets, N, K, format, packed, (cudaStream_t)stream),
                   "mx4_pack launch");
@@ -188,6 +217,11 @@ int egopq_mx4_unpack(const void* packed, int64_t sets, int64_t N, int64_t K, int
   if (rc) return rc;
   if ((rc = check_format(format))) return rc;
   if ((rc = check_ptrs(3, "packed", packed, "codes", codes, "scales", scales))) return rc;
+  const int64_t rows = sets * N;
+  const Span from{"packed", packed, (int64_t)egopq_mx4_packed_bytes(sets, N, K, format)};
+  if ((rc = check_apart({"codes", codes, rows * (K / 2)}, {from})) ||
+      (rc = check_apart({"scales", scales, rows * (K / mx4_block(format))}, {from})))
+    return rc;
   if ((rc = check_arch())) return rc;
   return launched(launch_mx4_unpack(packed, sets, N, K, format, codes, scales, (cudaStream_t)stream),
                   "mx4_unpack launch");
@@ -202,6 +236,10 @@ int egopq_mx4_gemm(const void* operand, const void* packed, const float* a_scale
   if (M == 0) return EGOPQ_OK;
   if ((rc = check_ptrs(3, "operand", operand, "packed", packed, "y", y))) return rc;
   if ((rc = check_scales(format, a_scale, w_scale))) return rc;
+  if ((rc = check_apart({"y", y, M * N * type_bytes(y_type)},
+                        {{"operand", operand, (int64_t)operand_bytes((M + 127) / 128, K, format)},
+                         {"packed", packed, (int64_t)operand_bytes((N + 127) / 128, K, format)}})))
+    return rc;
   if ((rc = check_arch())) return rc;
   Mx4GemmArgs g{};
   g.format = format;
@@ -236,12 +274,15 @@ static int check_linear(const Mx4QuantArgs& q, const Mx4GemmArgs& g, int64_t ws_
   const size_t need = egopq_mx4_linear_workspace_bytes(g.M, ws_sets, g.K, g.format);
   if (workspace_bytes < need)
     return fail(EGOPQ_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
-  const int64_t in = q.x_rows * g.K * (q.gated ? 2 : 1) * type_bytes(q.type);
-  const int64_t out = g.M * g.N * type_bytes(g.type);
-  if (overlap(workspace, (int64_t)need, q.x, in) || overlap(workspace, (int64_t)need, g.y, out))
-    return fail(EGOPQ_ERR_INVALID_ARG, "the workspace overlaps x or y");
   // (few rows are quantized by the blocks that need them, others writing y meanwhile)
-  if (overlap(q.x, in, g.y, out)) return fail(EGOPQ_ERR_INVALID_ARG, "y overlaps x");
+  const Span x{"x", q.x, q.x_rows * g.K * (q.gated ? 2 : 1) * type_bytes(q.type)};
+  const Span y{"y", g.y, g.M * g.N * type_bytes(g.type)};
+  const Span w{"packed", g.packed,
+               (int64_t)operand_bytes(g.sets * ((g.N + 127) / 128), g.K, g.format)};
+  const Span offsets{"offsets", g.offsets, 4 * ((int64_t)g.sets + 1)}, index{"index", q.index, 4 * q.M};
+  if ((rc = check_apart({"the workspace", workspace, (int64_t)need}, {x, y, w, offsets, index})) ||
+      (rc = check_apart(y, {x, w, offsets, index})))
+    return rc;
   return check_arch();
 }
 
