@@ -368,26 +368,6 @@ __global__ void __launch_bounds__(Cfg<FMT, XT>::kThreads, 2)
   }
 }
 
-Mx4Params params_of(const Mx4GemmArgs& a) {
-  Mx4Params p{};
-  p.operand = a.operand;
-  p.packed = a.packed;
-  p.a_scale = a.a_scale;
-  p.w_scale = a.w_scale;
-  p.offsets = a.offsets;
-  p.y = a.y;
-  p.M = a.M;
-  p.N = a.N;
-  p.K = a.K;
-  p.sets = a.sets;
-  p.nb = (int)((a.N + 127) / 128);
-  p.kb = (int)mx4_kblocks(a.K);
-  p.type = a.type;
-  p.split = 1;
-  p.timeout_ns = a.timeout_ns;
-  return p;
-}
-
 int64_t few_units(const Mx4GemmArgs& a) {
   return (a.offsets ? mx4_tiles(a.M, a.sets, kBT) : (a.M + kBT - 1) / kBT) * ((a.N + 127) / 128);
 }

@@ -432,22 +432,7 @@ bool make_map(CUtensorMap* map, const void* ptr, int64_t rows, int box) {
 template <int FMT>
 cudaError_t launch_pair(const Mx4GemmArgs& a, cudaStream_t st) {
   using C = Cfg<FMT>;
-  Mx4Params p;
-  p.operand = a.operand;
-  p.packed = a.packed;
-  p.a_scale = a.a_scale;
-  p.w_scale = a.w_scale;
-  p.offsets = a.offsets;
-  p.y = a.y;
-  p.M = a.M;
-  p.N = a.N;
-  p.K = a.K;
-  p.sets = a.sets;
-  p.nb = (int)((a.N + 127) / 128);
-  p.kb = (int)mx4_kblocks(a.K);
-  p.type = a.type;
-  p.split = 1;
-  p.timeout_ns = a.timeout_ns;
+  const Mx4Params p = params_of(a);
   const int64_t tiles = a.offsets ? mx4_tiles(a.M, a.sets, kBT) : (a.M + kBT - 1) / kBT;
   const int64_t most = tiles * ((p.nb + 1) / 2);
   const int pairs = device_sm_count() / 2;

@@ -19,6 +19,26 @@ struct Mx4Params {
   uint64_t timeout_ns;
 };
 
+inline Mx4Params params_of(const Mx4GemmArgs& a) {
+  Mx4Params p{};
+  p.operand = a.operand;
+  p.packed = a.packed;
+  p.a_scale = a.a_scale;
+  p.w_scale = a.w_scale;
+  p.offsets = a.offsets;
+  p.y = a.y;
+  p.M = a.M;
+  p.N = a.N;
+  p.K = a.K;
+  p.sets = a.sets;
+  p.nb = (int)((a.N + 127) / 128);
+  p.kb = (int)mx4_kblocks(a.K);
+  p.type = a.type;
+  p.split = 1;
+  p.timeout_ns = a.timeout_ns;
+  return p;
+}
+
 // Descriptors hold addresses in 16-byte units in their lowest bits, and every
 // address here is below 2^18: a place further on is an addition.
 __device__ __forceinline__ uint64_t mx4_at(uint64_t desc, uint32_t bytes) {
