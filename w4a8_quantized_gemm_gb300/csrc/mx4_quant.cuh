@@ -149,11 +149,12 @@ __device__ __forceinline__ void gated32(float& v0, float& v1, float g0, float g1
   mul2(v0, v1, u0, u1);
 }
 // Whether that does not hold, as g is below -22 or fp32 has run out of exponents on
-// the way to v = h * r, before u (half a subnormal g loses a bit) or behind it (zeros
-// are exact).
+// the way to v = h * r, before u (half a subnormal g loses a bit, but for the 16-bit
+// types' g) or behind it (zeros are exact).
+template <int TYPE>
 __device__ __forceinline__ bool gated_weak(float g, float u, float v, float r) {
   return g != 0.f && u != 0.f &&
-         (g < -22.f || fabsf(g) < 0x1p-100f || fabsf(v) < 0x1p-100f ||
+         (g < -22.f || (TYPE == kMx4F32 && fabsf(g) < 0x1p-100f) || fabsf(v) < 0x1p-100f ||
           fabsf(v) < 0x1p-100f * fabsf(r));
 }
 static __device__ __noinline__ double gated64(float g, float u, float r) {
@@ -229,15 +230,14 @@ __device__ __forceinline__ void quant_unit(const RowOut& out, int i_run, const E
     for (int i = 0; i < 8; i += 2) {
       gated32(v[i], v[i + 1], g[i], g[i + 1], u[i], u[i + 1]);
       low = min_abs3(low, v[i], v[i + 1]);
-      // (a 16-bit gate's half is a number of fp32's)
       if constexpr (TYPE == kMx4F32) tiny = min_abs3(tiny, g[i], g[i + 1]);
       gate = min3(gate, g[i], g[i + 1]);
       if constexpr (FMT == kE4M3) mul2(v[i], v[i + 1], r);
     }
     if (FMT == kE4M3) low = fminf(low, low * fabsf(r));
-    if (low < 0x1p-100f || tiny < 0x1p-100f || gate < -22.f) {
+    if (low < 0x1p-100f || (TYPE == kMx4F32 && tiny < 0x1p-100f) || gate < -22.f) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) weak = weak || gated_weak(g[i], u[i], v[i], r);
+      for (int i = 0; i < 8; ++i) weak = weak || gated_weak<TYPE>(g[i], u[i], v[i], r);
     }
   } else {
 #pragma unroll
