@@ -35,8 +35,10 @@ def test_what_makes_weights_lets_no_kernel_begin_before_its_end():
     assert "griddep_launch_dependents" not in body(text, "mx4_pack_kernel(uint8_t* codes")
     quant = body(text, "mx4_quant_kernel(const QuantParams p)")
     assert re.findall(r"if \(([^\n]*)\) griddep_launch_dependents", quant) == [
-        "p.early && threadIdx.x == 0"]
+        "EARLY && threadIdx.x == 0"]
     assert quant.count("griddep_launch_dependents") == 1
+    assert len(re.findall(r"return a\.early \? launch_quant_u<[^>]*, true>\(a, sms, st\)\s*"
+                          r": launch_quant_u<[^>]*, false>\(a, sms, st\);", text)) == 2
     # an operand of the caller's is such a weight; a linear's own is read by its product
     assert "a.early = !operand;" in body(api, "int egopq_mx4_quant(")
     assert api.count("early = true") == 1 and "early = true" in body(api, "int run(")

@@ -18,21 +18,25 @@ struct QuantParams {
   uint8_t* operand;
   int64_t M, K, x_rows;
   int sets, kb, groups;  // K blocks of a row, and runs of U of them
-  bool early;
 };
 
 // A warp takes U runs of 256 values of a row: eight values a lane, so that a block
 // of 32 (16) is four (two) neighbours and a row's 128 bytes of codes leave as one
 // line. All of a warp's loads are on their way before the first is used; few rows take
 // U = 1, so that more warps share them. Measured: 4093 x 18944 bf16 to E8M0 36.5 us (5.4
-// TB/s), to E4M3 44.7, gated 1021 x 18944 23.4 and 26.7: issue slots, 63 to 65 % busy,
-// bind before memory does.
-template <int FMT, int TYPE, bool GATED, int U>
+// TB/s), to E4M3 44.7, gated 1021 x 18944 23.4 and 26.7. Nothing is full: captured on
+// 4093 x 18944 fp16 and on the gated rows (E8M0 / E4M3 each), a scheduler issues in 69 and
+// 67 % of its active cycles, memory runs at 53 / 41 and 36 / 34 % of its peak, the ALUs at
+// 62 / 55 and 54 / 50. With seven warps a scheduler an instruction waits ten cycles, 1.5 to
+// 2.7 of them for loads and two for the one before it.
+// EARLY: the next kernel may begin at once; else not before every block's stores are
+// performed (a variant of its own: the fence in the same one costs those without it 2 %).
+template <int FMT, int TYPE, bool GATED, int U, bool EARLY>
 __global__ void __launch_bounds__(kQuantWarps * 32, GATED ? 8 : 9) mx4_quant_kernel(const QuantParams p) {
   extern __shared__ int quant_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_wait();
-  if (p.early && threadIdx.x == 0) griddep_launch_dependents();
+  if (EARLY && threadIdx.x == 0) griddep_launch_dependents();
   int *first = nullptr, *block = nullptr;
   int64_t row = 0, rows_end = p.M;
   if (p.offsets) {
@@ -98,10 +102,10 @@ __global__ void __launch_bounds__(kQuantWarps * 32, GATED ? 8 : 9) mx4_quant_ker
       ++row;
     }
   }
-  if (!p.early) __threadfence();  // (a block's end lets the next kernel begin)
+  if (!EARLY) __threadfence();  // (a block's end lets the next kernel begin)
 }
 
-template <int FMT, int TYPE, bool GATED, int U>
+template <int FMT, int TYPE, bool GATED, int U, bool EARLY>
 cudaError_t launch_quant_u(const Mx4QuantArgs& a, int sms, cudaStream_t st) {
   QuantParams p;
   p.x = a.x;
@@ -117,7 +121,6 @@ cudaError_t launch_quant_u(const Mx4QuantArgs& a, int sms, cudaStream_t st) {
   p.sets = a.sets;
   p.kb = (int)mx4_kblocks(a.K);
   p.groups = (p.kb + U - 1) / U;
-  p.early = a.early;
   const int64_t blocks = (a.M * p.groups + kQuantWarps - 1) / kQuantWarps;
   // as many as are on the SMs at a time: a second round of blocks that takes as long
   // as the first would leave them half empty
@@ -125,7 +128,7 @@ cudaError_t launch_quant_u(const Mx4QuantArgs& a, int sms, cudaStream_t st) {
   int per_sm = held.load(std::memory_order_relaxed);
   if (per_sm < 1) {
     if (cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-            &per_sm, mx4_quant_kernel<FMT, TYPE, GATED, U>, kQuantWarps * 32, 0);
+            &per_sm, mx4_quant_kernel<FMT, TYPE, GATED, U, EARLY>, kQuantWarps * 32, 0);
         e != cudaSuccess)
       return e;
     held.store(per_sm < 1 ? 1 : per_sm, std::memory_order_relaxed);
@@ -134,7 +137,7 @@ cudaError_t launch_quant_u(const Mx4QuantArgs& a, int sms, cudaStream_t st) {
   const int64_t most = (int64_t)sms * per_sm;
   const size_t smem = a.offsets ? 2 * (size_t)(a.sets + 1) * sizeof(int) : 0;
   PdlConfig c(dim3((unsigned)(blocks < most ? blocks : most), 1, 1), kQuantWarps * 32, smem, st);
-  return cudaLaunchKernelEx(&c.cfg, mx4_quant_kernel<FMT, TYPE, GATED, U>, p);
+  return cudaLaunchKernelEx(&c.cfg, mx4_quant_kernel<FMT, TYPE, GATED, U, EARLY>, p);
 }
 
 template <int FMT, int TYPE, bool GATED>
@@ -142,9 +145,11 @@ cudaError_t launch_quant(const Mx4QuantArgs& a, cudaStream_t st) {
   constexpr int kMany = GATED || TYPE == kMx4F32 ? 2 : 4;
   const int sms = device_sm_count();
   if (sms < 1) return cudaErrorInvalidConfiguration;
-  return a.M * mx4_kblocks(a.K) <= (int64_t)sms * 96
-             ? launch_quant_u<FMT, TYPE, GATED, 1>(a, sms, st)
-             : launch_quant_u<FMT, TYPE, GATED, kMany>(a, sms, st);
+  if (a.M * mx4_kblocks(a.K) <= (int64_t)sms * 96)
+    return a.early ? launch_quant_u<FMT, TYPE, GATED, 1, true>(a, sms, st)
+                   : launch_quant_u<FMT, TYPE, GATED, 1, false>(a, sms, st);
+  return a.early ? launch_quant_u<FMT, TYPE, GATED, kMany, true>(a, sms, st)
+                 : launch_quant_u<FMT, TYPE, GATED, kMany, false>(a, sms, st);
 }
 
 template <int FMT>
@@ -344,7 +349,7 @@ cudaError_t launch_dequant_type(const uint8_t* codes, const uint8_t* scales, int
 
 // ---- weights in and out of their records ---------------------------------------------
 // A warp moves the 128 bytes of codes and the scales of one row and K block (once a
-// weight: 18944 x 3584 takes 68 us).
+// weight: 18944 x 3584 takes 72 us).
 // Rows past N and values past K are zeros (in memory that the products read). No
 // early launch here: a product may read a weight before its own wait.
 template <int FMT, bool PACK>
