@@ -463,8 +463,8 @@ typedef enum { EGOPQ_TYPE_BF16 = 0, EGOPQ_TYPE_F16 = 1, EGOPQ_TYPE_F32 = 2 } ego
  * Where A is infinite or NaN the block's scale is NaN and its codes 0. gated:
  * x is [M][2K], and u = silu(x[:K]) * x[K:] (* r), silu(v) = v / (1 + exp(-v)),
  * not rounded at all: codes and scales are those of the real number (a product
- * beyond fp32 makes its block NaN). tensor_scale: g, fp32 [1], not 0, or NULL
- * (must be NULL for E8M0).
+ * beyond fp32 makes its block NaN; within 2^-19 of fp32's end one may).
+ * tensor_scale: g, fp32 [1], not 0, or NULL (must be NULL for E8M0).
  * codes and scales may be NULL (together), and so may operand: the form that
  * egopq_mx4_gemm reads, egopq_mx4_operand_bytes(M, K, format) bytes. */
 size_t egopq_mx4_operand_bytes(int64_t M, int64_t K, int format);
@@ -473,7 +473,8 @@ int egopq_mx4_quant(const void* x, int x_type, int64_t M, int64_t K, int format,
                     void* operand, egopq_stream_t stream);
 
 /* The values that codes and scales stand for: y [M][K] = code * scale (exact in
- * fp32), times g if there is one (rounded to fp32), rounded to y_type. */
+ * fp32, infinite beyond it), times g if there is one (rounded to fp32), rounded to
+ * y_type. */
 int egopq_mx4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K, int format,
                       const float* tensor_scale, int y_type, void* y, egopq_stream_t stream);
 

@@ -430,18 +430,24 @@ bool own_fits(const Mx4GemmArgs& a, int sms, int runs) {
          kb_most * (2048 + mx4_record_bytes(a.format) - kMx4Codes) <= kOwnBytes;
 }
 
-// Which kernel a product takes. One linear: by what each would take, in us, fitted to
-// the measurements below: a start, K blocks one after the other (with the columns of
-// a tile), and a split unit's sums.
+// Which kernel a product takes. One linear: by a rough model of what each would take, in
+// us: a start, K blocks one after the other (with the columns of a tile), and a split
+// unit's sums. Measured, E8M0, products alone:
 //   N x K          rows   this kernel / pairs
-//   3584 x 3584    64: 7.0 / 7.1   128: 8.2 / 7.8   192: 10.2 / 8.8
-//   18944 x 3584   17: 10.4 / 9.1  64: 14.2 / 9.3
-//   3584 x 18944   17: 9.9 / 24.6  192: 18.5 / 31.0  256: 24.4 / 26.4  384: 35.2 / 27.3
-//   50257 x 2048   17: 11.6 / 12.1  64: 13.5 / 12.7  128: 16.8 / 14.0
-//   512 x 3584     17: 4.0 / 6.9   512: 6.9 / 8.3
-// Ragged rows, whose sets only the device knows: by their mean. 64 sets of 2560 x
-// 3584, mean 32: 62.8 / 64.6, 64: 69.8 / 71.6, 96: 86.9 / 78.3; of 2048 x 1408, mean
-// 32: 29.8 / 31.4, 64: 34.4 / 33.9, 96: 43.6 / 37.5.
+//   3584 x 3584    64: 7.0 / 7.0   128: 8.2 / 7.5   192: 10.1 / 8.0
+//   18944 x 3584   17: 10.6 / 9.1  64: 14.3 / 9.3
+//   3584 x 18944   17: 9.9 / 23.6  192: 18.3 / 25.7  256: 24.1 / 26.1  384: 35.0 / 25.9
+//   50257 x 2048   17: 11.5 / 12.1  64: 13.4 / 12.6  128: 16.6 / 13.9
+//   512 x 3584     17: 4.0 / 6.7   512: 6.9 / 8.0
+// The model is up to a third off (a split K's blocks cost less than it says, pairs of few
+// units start sooner) and picks the slower side in three of these places, each next to
+// where the two cross: 128 rows of 3584 x 3584 (this kernel, 0.7 us), 256 of 3584 x 18944
+// (pairs, 2.0) and 17 of 50257 x 2048 (pairs, 0.6).
+// Ragged rows, whose sets only the device knows: by their mean over all sets, 64 sets of
+// 2560 x 3584, mean 32: 64.0 / 64.4, 64: 72.1 / 70.8, 96: 86.9 / 78.3; of 2048 x 1408,
+// mean 32: 28.9 / 30.8, 64: 33.6 / 33.1, 96: 43.6 / 37.5. Empty sets count, so rows that
+// lie in few of the sets may go this way where pairs are faster: 4096 rows in 16 of the 64
+// 50.6 / 35.2 and 27.3 / 19.7, in 8 50.1 / 33.3 and 26.9 / 19.8.
 // Rows that a linear may quantize itself, over a split K, take the same kernel behind a
 // quantization of their own, so that both add up alike (K in one piece is the same sum
 // in either kernel); where pairs would be faster it costs some 1.2 us: 16 rows of 16384 x

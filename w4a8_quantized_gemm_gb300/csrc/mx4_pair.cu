@@ -10,12 +10,14 @@
 // Tensor Memory has 512 columns and two accumulators of 256 and two sets of scales
 // need more, so the accumulators overlap: columns [kAcc1, 256) belong to both. A
 // tile's instructions wait until the epilogue has read those of the tile before;
-// the rest is read while they run.
+// the rest, 0.63 of a tile's columns (E4M3, whose scales take more, 0.44), is read while
+// they run.
 //
-// Measured: 4096 x 18944 x 3584 88 us (6.3 PFLOP/s; E4M3, with twice the scales to
-// copy, 96), 8192 x 8192 x 8192 149 us (7.4). A K block takes some 540 cycles, of which
-// its instructions are 512 and its 35.8 KB from L2 near as many, and a change of tiles
-// 2000.
+// Measured: 4096 x 18944 x 3584 87 us (6.4 PFLOP/s; E4M3, with twice the scales to
+// copy, 96), 8192 x 8192 x 8192 149 us (7.4), the tensor pipe busy for 68 % of the first
+// (E4M3 63). A K block takes some 540 cycles, of which its instructions are 512, and a
+// change of tiles 2000, in which they stand still: with few K blocks (K = 1408 has six)
+// that is over a third of a tile.
 #include "mx4_tc.cuh"
 #include "tc_kernel.cuh"  // (encode_fn)
 
